@@ -26,3 +26,12 @@ from .ops import (  # noqa: F401
     twell_pack,
     twell_unpack,
 )
+from .row_ops import (  # noqa: F401
+    DistillLoss,
+    LayerNorm,
+    TokenLogprobs,
+    distill_loss,
+    layer_norm_bwd,
+    layer_norm_fwd,
+    token_logprobs,
+)

@@ -16,6 +16,7 @@ c_void_p = ctypes.c_void_p
 c_int = ctypes.c_int
 c_size_t = ctypes.c_size_t
 c_float = ctypes.c_float
+c_int64 = ctypes.c_int64
 
 (TW_OK, TW_EINVAL, TW_EALIGN, TW_EUNSUPPORTED, TW_ECAPACITY, TW_ETIMEOUT, TW_ECUDA, TW_EWORKSPACE,
  TW_EBOUNDS) = range(9)
@@ -35,6 +36,8 @@ class TwHybrid(ctypes.Structure):
                 ("backup_a", c_void_p), ("backup_u", c_void_p), ("n_backup", c_void_p),
                 ("route", ctypes.c_int32), ("dense_above", ctypes.c_float), ("route_taken", c_void_p)]
 
+
+TW_F32, TW_BF16, TW_F16 = 0, 1, 2
 
 TW_ROUTE_SPARSE, TW_ROUTE_DENSE, TW_ROUTE_AUTO = 0, 1, 2
 ROUTES = {"sparse": TW_ROUTE_SPARSE, "dense": TW_ROUTE_DENSE, "auto": TW_ROUTE_AUTO}
@@ -79,6 +82,17 @@ SIGNATURES = {
     "tw_wait_timeout_probe": (c_int, [c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p]),
     "tw_wait_timeout_probe_pair": (c_int, [c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p]),
     "tw_fma_probe": (c_int, [c_void_p, c_int, c_int, ctypes.POINTER(ctypes.c_double), c_void_p]),
+    "tw_layer_norm_fwd": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_int, c_int, c_float,
+                                  c_int, c_int, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_void_p]),
+    "tw_layer_norm_bwd_workspace_size": (c_size_t, [c_int, c_int]),
+    "tw_layer_norm_bwd": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_void_p,
+                                  c_int64, c_int, c_int, c_int, c_int, c_void_p, c_int64, c_void_p, c_void_p,
+                                  c_void_p, c_size_t, c_void_p]),
+    "tw_distill": (c_int, [c_void_p, c_int64, c_int, c_int, c_int, c_void_p, c_void_p, c_int, c_int, c_void_p, c_void_p,
+                           c_float, c_float, c_float, c_void_p, c_float, c_void_p, c_void_p, c_int64, c_void_p,
+                           c_void_p]),
+    "tw_token_logprobs": (c_int, [c_void_p, c_int64, c_int, c_int, c_int, c_void_p, c_int, c_float, c_int, c_void_p,
+                                  c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
     "tw_trace_begin": (c_int, [ctypes.POINTER(c_void_p), c_int]),
     "tw_trace_end": (c_int, []),
     "tw_trace_label": (ctypes.c_char_p, [c_int]),

@@ -101,6 +101,61 @@ tw_status check_hybrid(const tw_hybrid* h, int T, int I, bool gated) {
   return TW_OK;
 }
 
+// ------------------------------------------------------------------ row operators
+// A [T, d] matrix with a row stride: aligned to its element size, an input's stride
+// >= 0 and an output's at least the row's length.
+struct RowMatrix {
+  const void* p;
+  int64_t ld;
+  bool required, output;
+};
+
+tw_status check_dtype(int dtype) { return dtype >= TW_F32 && dtype <= TW_F16 ? TW_OK : TW_EINVAL; }
+
+tw_status check_elems(const void* p, int dtype) {
+  const uintptr_t size = dtype == TW_F32 ? 4 : 2;
+  return reinterpret_cast<uintptr_t>(p) % size == 0 ? TW_OK : TW_EALIGN;
+}
+
+tw_status check_rows(const RowMatrix* m, int n, int64_t cols, int dtype) {
+  for (int i = 0; i < n; ++i) {
+    if (m[i].p == nullptr) {
+      if (m[i].required) return TW_EINVAL;
+      continue;
+    }
+    if (m[i].ld < (m[i].output ? cols : 0)) return TW_EINVAL;
+    const tw_status st = check_elems(m[i].p, dtype);
+    if (st != TW_OK) return st;
+  }
+  return TW_OK;
+}
+
+// fp32 and int32 side arrays: each required one non-null, all aligned to 4 bytes.
+tw_status check_side(std::initializer_list<const void*> required, std::initializer_list<const void*> optional) {
+  for (const void* p : required)
+    if (p == nullptr) return TW_EINVAL;
+  for (const auto& list : {required, optional})
+    for (const void* p : list)
+      if (reinterpret_cast<uintptr_t>(p) % 4 != 0) return TW_EALIGN;
+  return TW_OK;
+}
+
+// Logits [N, V] and what their kernels hold of a row on chip.
+tw_status check_logits(const void* z, int64_t ldz, int N, int V, int dtype, float temperature) {
+  if (N < 0 || V < 1 || check_dtype(dtype) != TW_OK) return TW_EINVAL;
+  if (!(temperature > 0.f) || !std::isfinite(temperature)) return TW_EINVAL;
+  if (V > 393216 || N > (1 << 27)) return TW_EUNSUPPORTED;
+  if (N == 0) return TW_OK;
+  const RowMatrix m = {z, ldz, true, false};
+  return check_rows(&m, 1, V, dtype);
+}
+
+tw_status check_norm(int T, int d, int dtype, int wtype) {
+  if (T < 0 || d < 1) return TW_EINVAL;
+  if (check_dtype(dtype) != TW_OK || (wtype != dtype && wtype != TW_F32)) return TW_EINVAL;
+  return d <= 16384 ? TW_OK : TW_EUNSUPPORTED;
+}
+
 // ------------------------------------------------------------------ workspace layouts
 struct FwdWs {
   uint16_t* X;
@@ -736,6 +791,113 @@ tw_status tw_wait_timeout_probe_pair(const uint16_t* A, const uint16_t* B, int M
   tw_status st = check_ptrs({A, B, D, dev_status});
   if (st != TW_OK) return st;
   return from_cuda(tw::gemm_dense_test(A, B, M, N, K, 0, 0, D, dev_status, as_stream(stream), withhold_kb, true));
+}
+
+// ------------------------------------------------------------------ layer norm
+tw_status tw_layer_norm_fwd(const void* x, int64_t ldx, const void* res, int64_t ldres, const void* weight,
+                            const void* bias, int T, int d, float eps, int dtype, int wtype, void* sum,
+                            int64_t ldsum, void* y, int64_t ldy, float* mean, float* rstd, void* stream) {
+  tw_status st = check_norm(T, d, dtype, wtype);
+  if (st != TW_OK) return st;
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return TW_EINVAL;
+  if (T == 0) return TW_OK;
+  if (sum != nullptr && res == nullptr) return TW_EINVAL;
+  const RowMatrix rows[] = {{x, ldx, true, false}, {res, ldres, false, false}, {sum, ldsum, false, true}, {y, ldy, true, true}};
+  st = check_rows(rows, 4, d, dtype);
+  if (st == TW_OK) st = check_elems(weight, wtype);
+  if (st == TW_OK) st = check_elems(bias, wtype);
+  if (st == TW_OK) st = check_side({}, {mean, rstd});
+  if (st != TW_OK) return st;
+  tw::NormFwdArgs a = {};
+  a.x = x, a.res = res, a.w = weight, a.b = bias, a.sum = sum, a.y = y, a.mean = mean, a.rstd = rstd;
+  a.ldx = ldx, a.ldres = res ? ldres : 0, a.ldsum = sum ? ldsum : 0, a.ldy = ldy;
+  a.T = T, a.d = d, a.eps = eps, a.dtype = dtype, a.wtype = wtype;
+  return from_cuda(tw::launch_norm_fwd(a, as_stream(stream)));
+}
+
+size_t tw_layer_norm_bwd_workspace_size(int T, int d) {
+  if (T <= 0 || d <= 0) return 0;
+  return sizeof(float) * 2 * static_cast<size_t>(d) * static_cast<size_t>(T < tw::kNormPartials ? T : tw::kNormPartials);
+}
+
+tw_status tw_layer_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const float* mean,
+                            const float* rstd, const void* weight, const void* dres, int64_t lddres, int T, int d,
+                            int dtype, int wtype, void* dx, int64_t lddx, float* dweight, float* dbias, void* ws,
+                            size_t ws_bytes, void* stream) {
+  tw_status st = check_norm(T, d, dtype, wtype);
+  if (st != TW_OK) return st;
+  st = check_side({}, {dweight, dbias});
+  if (st != TW_OK) return st;
+  const bool sums = dweight != nullptr || dbias != nullptr;
+  if (T > 0) {
+    const RowMatrix rows[] = {{dy, lddy, true, false}, {x, ldx, true, false}, {dres, lddres, false, false}, {dx, lddx, true, true}};
+    st = check_rows(rows, 4, d, dtype);
+    if (st == TW_OK) st = check_side({mean, rstd}, {});
+    if (st == TW_OK) st = check_elems(weight, wtype);
+    if (st == TW_OK && sums) st = check_ptrs({ws});
+    if (st != TW_OK) return st;
+    if (sums && ws_bytes < tw_layer_norm_bwd_workspace_size(T, d)) return TW_EWORKSPACE;
+  }
+  tw::NormBwdArgs a = {};
+  a.dy = dy, a.x = x, a.w = weight, a.dres = dres, a.mean = mean, a.rstd = rstd, a.dx = dx, a.dw = dweight, a.db = dbias;
+  a.part = sums ? static_cast<float*>(ws) : nullptr;
+  a.lddy = lddy, a.ldx = ldx, a.lddres = dres ? lddres : 0, a.lddx = lddx;
+  a.T = T, a.d = d, a.dtype = dtype, a.wtype = wtype;
+  return from_cuda(tw::launch_norm_bwd(a, as_stream(stream)));
+}
+
+// ------------------------------------------------------------------ rows of logits
+tw_status tw_distill(const void* z, int64_t ldz, int N, int V, int dtype, const int32_t* t_idx, const void* t_val,
+                     int t_dtype, int K, const float* t_rest, const int32_t* labels, float temperature,
+                     float kd_weight, float ce_weight, const float* dloss, float scale, float* loss, void* dz,
+                     int64_t lddz, int32_t* dev_status, void* stream) {
+  tw_status st = check_logits(z, ldz, N, V, dtype, temperature);
+  if (st != TW_OK) return st;
+  if (K < 0 || !std::isfinite(kd_weight) || !std::isfinite(ce_weight) || !std::isfinite(scale)) return TW_EINVAL;
+  if (K > 1024) return TW_EUNSUPPORTED;
+  if (loss == nullptr && dz == nullptr) return TW_EINVAL;
+  if (K > 0 && check_dtype(t_dtype) != TW_OK) return TW_EINVAL;
+  if (N == 0) return TW_OK;
+  if (dz != nullptr) {
+    const RowMatrix m = {dz, lddz, true, true};
+    st = check_rows(&m, 1, V, dtype);
+    if (st != TW_OK) return st;
+  }
+  if (kd_weight == 0.f) K = 0, t_rest = nullptr;
+  if (ce_weight == 0.f) labels = nullptr;
+  if (K > 0) {
+    st = check_side({t_idx}, {});
+    if (st == TW_OK && t_val == nullptr) st = TW_EINVAL;
+    if (st == TW_OK) st = check_elems(t_val, t_dtype);
+    if (st != TW_OK) return st;
+  }
+  st = check_side({dev_status}, {t_rest, labels, dloss, loss});
+  if (st != TW_OK) return st;
+  tw::DistillArgs a = {};
+  a.z = z, a.ldz = ldz, a.N = N, a.V = V, a.dtype = dtype;
+  a.t_idx = t_idx, a.t_val = t_val, a.t_dtype = t_dtype, a.K = K, a.t_rest = t_rest, a.labels = labels;
+  a.temperature = temperature, a.kd_weight = kd_weight, a.ce_weight = ce_weight;
+  a.dloss = dloss, a.scale = scale, a.loss = loss, a.dz = dz, a.lddz = lddz, a.status = dev_status;
+  return from_cuda(tw::launch_distill(a, as_stream(stream)));
+}
+
+tw_status tw_token_logprobs(const void* z, int64_t ldz, int N, int V, int dtype, const int32_t* tokens, int n_tokens,
+                            float temperature, int top_k, float* logprob, float* entropy, int32_t* top_idx,
+                            float* top_logprob, int32_t* dev_status, void* stream) {
+  tw_status st = check_logits(z, ldz, N, V, dtype, temperature);
+  if (st != TW_OK) return st;
+  if (n_tokens < 0 || top_k < 0) return TW_EINVAL;
+  if (top_k > 128) return TW_EUNSUPPORTED;
+  if (N == 0) return TW_OK;
+  st = check_side({dev_status}, {entropy});
+  if (st == TW_OK && n_tokens > 0) st = check_side({tokens, logprob}, {});
+  if (st == TW_OK && top_k > 0) st = check_side({top_idx, top_logprob}, {});
+  if (st != TW_OK) return st;
+  tw::LogprobArgs a = {};
+  a.z = z, a.ldz = ldz, a.N = N, a.V = V, a.dtype = dtype;
+  a.tokens = tokens, a.n_tokens = n_tokens, a.K = top_k, a.temperature = temperature;
+  a.logprob = logprob, a.entropy = entropy, a.top_idx = top_idx, a.top_logprob = top_logprob, a.status = dev_status;
+  return from_cuda(tw::launch_logprobs(a, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -356,4 +356,63 @@ cudaError_t gemm_dense_weight_grads(const DenseWeightGradProblem* probs, int n_p
 cudaError_t gemm_dense_test(const uint16_t* A, const uint16_t* B, int M, int N, int K, int a_mn, int b_mn, float* D,
                             int32_t* status, cudaStream_t s, int withhold_kb = -1, bool pair = false);
 
+// ---------------------------------------------------------------- tw_norm.cu
+struct NormFwdArgs {
+  const void *x, *res, *w, *b;  // res, w, b may be null
+  void *sum, *y;                // sum (x + res) may be null
+  float *mean, *rstd;           // may be null
+  int64_t ldx, ldres, ldsum, ldy;
+  int T, d;
+  float eps;
+  int dtype, wtype;
+};
+cudaError_t launch_norm_fwd(const NormFwdArgs& a, cudaStream_t s);
+
+struct NormBwdArgs {
+  const void *dy, *x, *w, *dres;  // w, dres may be null
+  const float *mean, *rstd;
+  void* dx;
+  float *dw, *db;                 // may be null
+  float* part;                    // [kNormPartials][2][d] fp32, null when dw and db are
+  int64_t lddy, ldx, lddres, lddx;
+  int T, d;
+  int dtype, wtype;
+};
+// The most CTAs whose partial sums over rows the backward keeps in its workspace.
+constexpr int kNormPartials = 512;
+cudaError_t launch_norm_bwd(const NormBwdArgs& a, cudaStream_t s);
+
+// ---------------------------------------------------------------- tw_logits.cu
+struct DistillArgs {
+  const void* z;
+  const int32_t* t_idx;   // [N, K]; K = 0: no list
+  const void* t_val;      // [N, K] of t_dtype
+  const float* t_rest;    // [N], may be null
+  const int32_t* labels;  // [N], may be null
+  const float* dloss;     // [N], may be null
+  float* loss;            // [N], may be null
+  void* dz;               // may be null, may be z
+  int32_t* status;
+  int64_t ldz, lddz;
+  int N, V, K;
+  int dtype, t_dtype;
+  float temperature, kd_weight, ce_weight, scale;
+};
+cudaError_t launch_distill(const DistillArgs& a, cudaStream_t s);
+
+struct LogprobArgs {
+  const void* z;
+  const int32_t* tokens;  // [N, n_tokens]
+  float* logprob;         // [N, n_tokens]
+  float* entropy;         // [N], may be null
+  int32_t* top_idx;       // [N, K]
+  float* top_logprob;     // [N, K]
+  int32_t* status;
+  int64_t ldz;
+  int N, V, n_tokens, K;
+  int dtype;
+  float temperature;
+};
+cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t s);
+
 }  // namespace tw

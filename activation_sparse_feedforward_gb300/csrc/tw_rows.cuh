@@ -1,0 +1,132 @@
+// Device helpers of the row operators (tw_norm.cu, tw_logits.cu): the three element
+// types, 16-byte vectors of them, asynchronous 16-byte copies into shared memory,
+// sums over teams of warps, and reads of another CTA's shared memory in a cluster.
+#pragma once
+
+#include "tw_common.cuh"
+
+namespace tw {
+
+// ------------------------------------------------------------------ element types
+// Elem<TW_*>: storage S, E elements per 16 bytes, widening to fp32 (exact) and
+// narrowing (round to nearest even).
+template <int DT>
+struct Elem;
+
+template <>
+struct Elem<TW_F32> {
+  using S = float;
+  static constexpr int E = 4;
+  static TW_DEV float get(S v) { return v; }
+  static TW_DEV S put(float v) { return v; }
+  static TW_DEV S neg_inf() { return __int_as_float(0xFF800000); }
+  static TW_DEV void unpack(const uint4& w, float (&v)[4]) {
+    v[0] = __uint_as_float(w.x), v[1] = __uint_as_float(w.y);
+    v[2] = __uint_as_float(w.z), v[3] = __uint_as_float(w.w);
+  }
+  static TW_DEV uint4 pack(const float (&v)[4]) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  }
+  // the largest of the four (a NaN loses to a number)
+  static TW_DEV float max16(const uint4& w) {
+    return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+  }
+};
+
+template <>
+struct Elem<TW_BF16> {
+  using S = uint16_t;
+  static constexpr int E = 8;
+  static TW_DEV float get(S v) { return bf16_to_f32(v); }
+  static TW_DEV S put(float v) { return f32_to_bf16(v); }
+  static TW_DEV S neg_inf() { return 0xFF80; }
+  static TW_DEV void unpack(const uint4& w, float (&v)[8]) {
+    const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(r[i]), v[2 * i + 1] = bf16_hi(r[i]);
+  }
+  static TW_DEV uint4 pack(const float (&v)[8]) {
+    return make_uint4(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]), pack_bf16x2_rn(v[4], v[5]),
+                      pack_bf16x2_rn(v[6], v[7]));
+  }
+  static TW_DEV float max16(const uint4& w) {
+    auto h = [](uint32_t u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); };
+    const __nv_bfloat162 m = __hmax2(__hmax2(h(w.x), h(w.y)), __hmax2(h(w.z), h(w.w)));
+    const float2 f = __bfloat1622float2(m);
+    return fmaxf(f.x, f.y);
+  }
+};
+
+template <>
+struct Elem<TW_F16> {
+  using S = uint16_t;
+  static constexpr int E = 8;
+  static TW_DEV float get(S v) { return f16_to_f32(v); }
+  static TW_DEV S put(float v) { return f32_to_f16(v); }
+  static TW_DEV S neg_inf() { return 0xFC00; }
+  static TW_DEV void unpack(const uint4& w, float (&v)[8]) {
+    const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r[i]));
+      v[2 * i] = f.x, v[2 * i + 1] = f.y;
+    }
+  }
+  static TW_DEV uint4 pack(const float (&v)[8]) {
+    return make_uint4(pack_f16x2_rn(v[0], v[1]), pack_f16x2_rn(v[2], v[3]), pack_f16x2_rn(v[4], v[5]),
+                      pack_f16x2_rn(v[6], v[7]));
+  }
+  static TW_DEV float max16(const uint4& w) {
+    auto h = [](uint32_t u) { return *reinterpret_cast<const __half2*>(&u); };
+    const __half2 m = __hmax2(__hmax2(h(w.x), h(w.y)), __hmax2(h(w.z), h(w.w)));
+    const float2 f = __half22float2(m);
+    return fmaxf(f.x, f.y);
+  }
+};
+
+// ------------------------------------------------------------------ asynchronous copies
+// One 16-byte copy, global to shared, past L1; the copying thread sees its own copies
+// after cp_wait_all() (no wait loop: the hardware counts them).
+TW_DEV void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+TW_DEV void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+TW_DEV void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// ------------------------------------------------------------------ reductions
+TW_DEV float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+// Barrier `id` among `n` threads (a multiple of 32): the warps of one team of a CTA.
+TW_DEV void team_barrier(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+
+// ------------------------------------------------------------------ clusters
+TW_DEV float ld_cluster_f32(uint32_t cluster_addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+TW_DEV unsigned long long ld_cluster_u64(uint32_t cluster_addr) {
+  unsigned long long v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
+// A cluster barrier in two halves: what a thread did before arriving is done for every
+// thread that has waited.
+TW_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+TW_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// 2^x (hardware approximation, about 2 ulp; subnormal results flush to zero)
+TW_DEV float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+}  // namespace tw

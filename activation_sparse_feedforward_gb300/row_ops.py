@@ -1,0 +1,273 @@
+"""Torch-facing binding of the operators at the ends of a model around the feedforward
+layer: layer norm, the distillation loss and token log probabilities (see the last
+part of include/twell.h).
+
+As in ``ops``: objects preallocate every buffer, calls enqueue on torch's current
+stream and neither allocate nor synchronise; one-shot functions build such an object.
+Matrices are [rows, columns] views with unit column stride and any row stride; a call
+may pass fewer rows than the object was made for and gets views of that many rows back.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import _lib
+from .ops import _ptr, _stream, _workspace
+
+DTYPES = {torch.float32: _lib.TW_F32, torch.bfloat16: _lib.TW_BF16, torch.float16: _lib.TW_F16}
+
+
+def _dtype_code(dtype: torch.dtype) -> int:
+    code = DTYPES.get(dtype)
+    if code is None:
+        raise ValueError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
+    return code
+
+
+def _check_matrix(name: str, t: torch.Tensor, dtype: torch.dtype, rows: int, cols: int) -> None:
+    if t.dtype != dtype or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA {dtype} tensor")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
+    if t.stride(1) != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit stride along its rows")
+
+
+def _check_vector(name: str, t: torch.Tensor, dtype: torch.dtype, n: int) -> None:
+    if t.dtype != dtype or not t.is_cuda or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of {n} elements")
+
+
+def _check_rows(name: str, t: torch.Tensor, most: int) -> int:
+    if t.dim() != 2 or t.shape[0] > most:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected at most {most} rows")
+    return t.shape[0]
+
+
+def _ld(t: torch.Tensor | None) -> int:
+    """Row stride in elements; a single row's is its length whatever torch says."""
+    return 0 if t is None else t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+class LayerNorm:
+    """Preallocated layer norm of up to T rows of width d, forward and backward (see
+    tw_layer_norm_fwd, tw_layer_norm_bwd).
+
+    weight_dtype: the type of weight and bias, `dtype` (default) or float32. backward:
+    whether the buffers of the backward (dx, fp32 dweight and dbias, workspace) are kept.
+    """
+
+    def __init__(self, T: int, d: int, dtype: torch.dtype = torch.bfloat16, weight_dtype: torch.dtype | None = None,
+                 eps: float = 1e-5, backward: bool = True, device="cuda"):
+        self.T, self.d, self.dtype, self.eps = T, d, dtype, float(eps)
+        self.weight_dtype = weight_dtype or dtype
+        self._dt, self._wdt = _dtype_code(dtype), _dtype_code(self.weight_dtype)
+        if self._wdt not in (self._dt, _lib.TW_F32):
+            raise ValueError(f"weight_dtype must be {dtype} or float32, got {self.weight_dtype}")
+        L = _lib.load()
+        self.y = torch.empty((T, d), dtype=dtype, device=device)
+        self.sum = torch.empty((T, d), dtype=dtype, device=device)
+        self._mean = torch.empty(T, dtype=torch.float32, device=device)
+        self._rstd = torch.empty(T, dtype=torch.float32, device=device)
+        self._rows = T
+        self.dx = self.dweight = self.dbias = None
+        if backward:
+            self.dx = torch.empty((T, d), dtype=dtype, device=device)
+            self.dweight = torch.empty(d, dtype=torch.float32, device=device)
+            self.dbias = torch.empty(d, dtype=torch.float32, device=device)
+            self.ws_bytes = int(L.tw_layer_norm_bwd_workspace_size(T, d))
+            self.ws = _workspace(self.ws_bytes, device)
+
+    @property
+    def mean(self) -> torch.Tensor:
+        """fp32 row means of the last forward."""
+        return self._mean[:self._rows]
+
+    @property
+    def rstd(self) -> torch.Tensor:
+        """fp32 1 / sqrt(variance + eps) of the last forward's rows."""
+        return self._rstd[:self._rows]
+
+    def forward(self, x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                residual: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+        """(y, s): s = x + residual (x itself without one), y = norm(s) weight + bias."""
+        n, d = _check_rows("x", x, self.T), self.d
+        _check_matrix("x", x, self.dtype, n, d)
+        if residual is not None:
+            _check_matrix("residual", residual, self.dtype, n, d)
+        if weight is not None:
+            _check_vector("weight", weight, self.weight_dtype, d)
+        if bias is not None:
+            _check_vector("bias", bias, self.weight_dtype, d)
+        self._rows = n
+        y, s = (self.y, self.sum) if n == self.T else (self.y[:n], self.sum[:n])
+        code = _lib.load().tw_layer_norm_fwd(
+            _ptr(x), _ld(x), _ptr(residual), _ld(residual), _ptr(weight), _ptr(bias), n, d, self.eps,
+            self._dt, self._wdt, None if residual is None else _ptr(s), d, _ptr(y), d,
+            _ptr(self._mean), _ptr(self._rstd), _stream())
+        _lib.check(code, "tw_layer_norm_fwd")
+        return y, (x if residual is None else s)
+
+    def backward(self, dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor | None = None,
+                 dres: torch.Tensor | None = None, mean: torch.Tensor | None = None,
+                 rstd: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+        """(dx, dweight, dbias) for x the tensor that was normalised (the forward's s);
+        dres is added to dx. mean, rstd: the statistics, of the last forward by default."""
+        if self.dx is None:
+            raise ValueError("this LayerNorm was made with backward=False")
+        n, d = _check_rows("x", x, self.T), self.d
+        _check_matrix("x", x, self.dtype, n, d)
+        _check_matrix("dy", dy, self.dtype, n, d)
+        if dres is not None:
+            _check_matrix("dres", dres, self.dtype, n, d)
+        if weight is not None:
+            _check_vector("weight", weight, self.weight_dtype, d)
+        mean, rstd = self.mean if mean is None else mean, self.rstd if rstd is None else rstd
+        _check_vector("mean", mean, torch.float32, n)
+        _check_vector("rstd", rstd, torch.float32, n)
+        dx = self.dx if n == self.T else self.dx[:n]
+        code = _lib.load().tw_layer_norm_bwd(
+            _ptr(dy), _ld(dy), _ptr(x), _ld(x), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(dres), _ld(dres), n, d,
+            self._dt, self._wdt, _ptr(dx), d, _ptr(self.dweight),
+            _ptr(self.dbias), _ptr(self.ws), self.ws.numel(), _stream())
+        _lib.check(code, "tw_layer_norm_bwd")
+        return dx, self.dweight, self.dbias
+
+
+def layer_norm_fwd(x, weight=None, bias=None, eps: float = 1e-5, residual=None):
+    """One-shot forward. Returns (y, s, mean, rstd)."""
+    ln = LayerNorm(x.shape[0], x.shape[1], x.dtype, None if weight is None else weight.dtype, eps, backward=False,
+                   device=x.device)
+    y, s = ln.forward(x, weight, bias, residual)
+    return y, s, ln.mean, ln.rstd
+
+
+def layer_norm_bwd(dy, x, mean, rstd, weight=None, dres=None):
+    """One-shot backward. Returns (dx, dweight, dbias)."""
+    ln = LayerNorm(x.shape[0], x.shape[1], x.dtype, None if weight is None else weight.dtype, device=x.device)
+    return ln.backward(dy, x, weight, dres, mean, rstd)
+
+
+class DistillLoss:
+    """Preallocated distillation loss of up to N rows of V logits from a teacher's top K
+    (see tw_distill): kd_weight * KD at `temperature` + ce_weight * cross entropy of the
+    labels. K = 0 is plain cross entropy. grad: whether a gradient buffer dz is kept
+    (calls may also name theirs with `out`, the logits themselves among them).
+
+    idx [n, K] int32 (-1: no entry), val [n, K] float32, bfloat16 or float16, rest [n]
+    float32 or None, labels [n] int32 (-1: none) or None. An index outside [-1, V)
+    raises TW_EINVAL in `status`.
+    """
+
+    def __init__(self, N: int, V: int, K: int, dtype: torch.dtype = torch.bfloat16, temperature: float = 1.0,
+                 kd_weight: float = 1.0, ce_weight: float = 0.0, grad: bool = True, device="cuda"):
+        self.N, self.V, self.K, self.dtype = N, V, K, dtype
+        self.temperature, self.kd_weight, self.ce_weight = float(temperature), float(kd_weight), float(ce_weight)
+        self._dt = _dtype_code(dtype)
+        _lib.load()
+        self.loss = torch.empty(N, dtype=torch.float32, device=device)
+        self.dz = torch.empty((N, V), dtype=dtype, device=device) if grad else None
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+
+    def _run(self, z, idx, val, rest, labels, dloss, scale, want_loss, dz) -> None:
+        n, K = z.shape[0], self.K
+        tdt = self._dt
+        if K > 0:
+            if idx is None or val is None:
+                raise ValueError("idx and val must be given for K > 0")
+            _check_vector("idx", idx, torch.int32, n * K)
+            tdt = _dtype_code(val.dtype)
+            _check_vector("val", val, val.dtype, n * K)
+        for name, t, dt in (("rest", rest, torch.float32), ("labels", labels, torch.int32), ("dloss", dloss, torch.float32)):
+            if t is not None:
+                _check_vector(name, t, dt, n)
+        code = _lib.load().tw_distill(
+            _ptr(z), _ld(z), n, self.V, self._dt, _ptr(idx), _ptr(val), tdt, K, _ptr(rest), _ptr(labels),
+            self.temperature, self.kd_weight, self.ce_weight, _ptr(dloss), float(scale),
+            _ptr(self.loss) if want_loss else None, _ptr(dz), _ld(dz), _ptr(self.status),
+            _stream())
+        _lib.check(code, "tw_distill")
+
+    def _grad_buffer(self, n: int, out: torch.Tensor | None) -> torch.Tensor:
+        if out is None:
+            if self.dz is None:
+                raise ValueError("this DistillLoss was made with grad=False: give `out`")
+            return self.dz if n == self.N else self.dz[:n]
+        _check_matrix("out", out, self.dtype, n, self.V)
+        return out
+
+    def forward(self, z, idx=None, val=None, rest=None, labels=None) -> torch.Tensor:
+        """fp32 losses [n]."""
+        n = _check_rows("z", z, self.N)
+        _check_matrix("z", z, self.dtype, n, self.V)
+        self._run(z, idx, val, rest, labels, None, 1.0, True, None)
+        return self.loss[:n]
+
+    def backward(self, z, idx=None, val=None, rest=None, labels=None, dloss=None, scale: float = 1.0,
+                 out: torch.Tensor | None = None) -> torch.Tensor:
+        """dz [n, V] = scale * dloss * d loss / d z (dloss [n] float32, None for 1)."""
+        n = _check_rows("z", z, self.N)
+        _check_matrix("z", z, self.dtype, n, self.V)
+        dz = self._grad_buffer(n, out)
+        self._run(z, idx, val, rest, labels, dloss, scale, False, dz)
+        return dz
+
+    def forward_backward(self, z, idx=None, val=None, rest=None, labels=None, dloss=None, scale: float = 1.0,
+                         out: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+        """(losses, dz) in one pass over z."""
+        n = _check_rows("z", z, self.N)
+        _check_matrix("z", z, self.dtype, n, self.V)
+        dz = self._grad_buffer(n, out)
+        self._run(z, idx, val, rest, labels, dloss, scale, True, dz)
+        return self.loss[:n], dz
+
+
+def distill_loss(z, idx=None, val=None, rest=None, labels=None, temperature: float = 1.0, kd_weight: float = 1.0,
+                 ce_weight: float = 0.0, dloss=None, scale: float = 1.0):
+    """One-shot loss and gradient. Returns (losses, dz, status)."""
+    op = DistillLoss(z.shape[0], z.shape[1], 0 if idx is None else idx.shape[1], z.dtype, temperature, kd_weight,
+                     ce_weight, device=z.device)
+    loss, dz = op.forward_backward(z, idx, val, rest, labels, dloss, scale)
+    return loss, dz, op.status
+
+
+class TokenLogprobs:
+    """Preallocated log probabilities of n_tokens given tokens a row, with the entropy and
+    the top_k alternatives of up to N rows of V logits (see tw_token_logprobs). A token
+    outside [-1, V) raises TW_EINVAL in `status`."""
+
+    def __init__(self, N: int, V: int, n_tokens: int = 1, top_k: int = 0, temperature: float = 1.0,
+                 dtype: torch.dtype = torch.bfloat16, device="cuda"):
+        self.N, self.V, self.n_tokens, self.top_k, self.dtype = N, V, n_tokens, top_k, dtype
+        self.temperature = float(temperature)
+        self._dt = _dtype_code(dtype)
+        _lib.load()
+        self.logprob = torch.empty((N, n_tokens), dtype=torch.float32, device=device)
+        self.entropy = torch.empty(N, dtype=torch.float32, device=device)
+        self.top_idx = torch.empty((N, top_k), dtype=torch.int32, device=device)
+        self.top_logprob = torch.empty((N, top_k), dtype=torch.float32, device=device)
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+
+    def __call__(self, z: torch.Tensor, tokens: torch.Tensor | None = None):
+        """(logprob [n, n_tokens], entropy [n], top_idx [n, top_k], top_logprob [n, top_k])."""
+        n = _check_rows("z", z, self.N)
+        _check_matrix("z", z, self.dtype, n, self.V)
+        if self.n_tokens > 0:
+            if tokens is None:
+                raise ValueError("tokens must be given for n_tokens > 0")
+            _check_vector("tokens", tokens, torch.int32, n * self.n_tokens)
+        code = _lib.load().tw_token_logprobs(
+            _ptr(z), _ld(z), n, self.V, self._dt, _ptr(tokens) if self.n_tokens > 0 else None, self.n_tokens,
+            self.temperature, self.top_k, _ptr(self.logprob), _ptr(self.entropy), _ptr(self.top_idx),
+            _ptr(self.top_logprob), _ptr(self.status), _stream())
+        _lib.check(code, "tw_token_logprobs")
+        if n == self.N:
+            return self.logprob, self.entropy, self.top_idx, self.top_logprob
+        return self.logprob[:n], self.entropy[:n], self.top_idx[:n], self.top_logprob[:n]
+
+
+def token_logprobs(z, tokens=None, top_k: int = 0, temperature: float = 1.0):
+    """One-shot form; tokens [n] or [n, s]. Returns (logprob, entropy, top_idx, top_logprob, status)."""
+    s = 0 if tokens is None else tokens.numel() // max(z.shape[0], 1)
+    op = TokenLogprobs(z.shape[0], z.shape[1], s, top_k, temperature, z.dtype, z.device)
+    return (*op(z, tokens), op.status)

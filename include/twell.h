@@ -413,6 +413,102 @@ tw_status tw_trace_begin(void* const* events, int capacity);
 int tw_trace_end(void);
 const char* tw_trace_label(int i);
 
+/* ---------------------------------------------------------------------------------
+ * The ends of a model around the feedforward layer: the norm before it, the loss
+ * that trains it and the read-out of its answers. (The pages train with a language
+ * modelling loss and evaluate on downstream suites, explainer 4 and thelatestinai
+ * listing Tables 1 and 3, but give none of these operators.)
+ *
+ * They differ from the calls above in two ways. Element types are named by tw_dtype
+ * and passed as void*. Matrices have a row stride in elements (ld*): rows need not be
+ * adjacent nor 16-byte aligned; every matrix is aligned to its element size, and the
+ * kernels use 16-byte accesses wherever a row allows them. An input's stride may be
+ * any value >= 0 (0: one row for all); an output's is at least its row length. Weights
+ * and fp32 and int32 side arrays are dense and aligned to their element size. */
+typedef enum { TW_F32 = 0, TW_BF16 = 1, TW_F16 = 2 } tw_dtype;
+
+/* Layer norm forward over the rows of x [T, d], after an optional residual add:
+ *   s = x + res (rounded to the type; s = x when res is NULL)
+ *   mean = sum(s) / d,  rstd = (sum((s - mean)^2) / d + eps)^-1/2
+ *   y = (s - mean) rstd * weight + bias
+ * res: NULL, or [T, d]; then `sum` (NULL: not kept) receives s, the residual stream
+ * that the next block adds to and that the backward takes as its x. sum may be x or
+ * res itself (same pointer and stride). weight, bias [d]: NULL for 1 and 0; of type
+ * wtype, which is dtype or TW_F32. mean, rstd [T] fp32: NULL when no backward
+ * follows. Statistics are fp32 over the row in registers; y and s are rounded once.
+ * 1 <= d <= 16384 (TW_EUNSUPPORTED above); T >= 0, T = 0 does nothing; eps >= 0 and
+ * finite. A row with a NaN or an infinity gives NaN in y. */
+tw_status tw_layer_norm_fwd(const void* x, int64_t ldx, const void* res, int64_t ldres, const void* weight,
+                            const void* bias, int T, int d, float eps, int dtype, int wtype, void* sum,
+                            int64_t ldsum, void* y, int64_t ldy, float* mean, float* rstd, void* stream);
+
+/* Workspace bytes tw_layer_norm_bwd needs (partial sums of the weight's gradients). */
+size_t tw_layer_norm_bwd_workspace_size(int T, int d);
+
+/* Layer norm backward. x is what the forward normalised (its `sum` when it added a
+ * residual), mean and rstd its statistics. With xh = (x - mean) rstd, g = dy weight:
+ *   dx = rstd (g - sum(g) / d - xh sum(g xh) / d) + dres
+ *   dweight = sum over rows of dy xh,  dbias = sum over rows of dy
+ * dres: NULL, or [T, d], the gradient that reaches s along the residual stream; dx
+ * may be dres or dy itself (same pointer and stride). weight: NULL for 1. dx [T, d] of
+ * type dtype; dweight, dbias [d] fp32, overwritten, each NULL when not wanted; T = 0
+ * writes zeros into them. The sums over rows are taken in an order that depends on
+ * T and d only: the same inputs give the same bits. Widths as the forward. */
+tw_status tw_layer_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const float* mean,
+                            const float* rstd, const void* weight, const void* dres, int64_t lddres, int T, int d,
+                            int dtype, int wtype, void* dx, int64_t lddx, float* dweight, float* dbias, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/* Distillation of a student's logits z [N, V] from a teacher's top logits, with hard
+ * labels mixed in; loss and gradient in one pass over z. Row n has a list of up to K
+ * teacher entries: tokens t_idx[n, k] (-1: no entry) and logits t_val[n, k] (type
+ * t_dtype). With tau = temperature:
+ *   P = softmax over {t_val / tau of the entries} and t_rest[n] (when t_rest is given)
+ *   q = softmax(z / tau) over all V tokens;  q_rest = sum of q over the unlisted ones
+ *   KD = tau^2 [ sum_k P_k (log P_k - log q[t_idx_k]) + P_rest (log P_rest - log q_rest) ]
+ *   CE = -log softmax(z)[label]
+ *   loss = kd_weight KD + ce_weight CE
+ *   dz_v = scale dloss[n] ( kd_weight tau (q_v - Pt_v) + ce_weight (softmax(z)_v - [v = label]) )
+ * with Pt_v the P of the entries that name v, and P_rest q_v / q_rest on unlisted v.
+ *  - t_rest [N] fp32: the log of the sum of exp(t / tau) over the teacher's unlisted
+ *    tokens, so that P is the teacher's own distribution with its tail in one bucket.
+ *    NULL, or -inf in a row: P is renormalised over the list.
+ *  - A term with P_k = 0 is 0. A token listed twice counts as two entries of the sum.
+ *  - labels [N]: -1 = none. A row without entries (all -1 or of logit -inf, and no rest)
+ *    has KD = 0; a row with neither entries nor a label has loss 0 and dz 0 whatever its
+ *    logits hold. labels, or K = 0 and t_rest = NULL, may be absent; a part whose weight
+ *    is 0 is not looked at.
+ *  - Masked logits are -inf: q = 0, dz as the formula. A row with no other logits has
+ *    loss +inf and dz 0. A NaN or +inf in a row makes its loss and dz NaN.
+ *  - loss [N] fp32, or NULL; dz [N, V] of z's type, or NULL: the loss alone, the gradient
+ *    alone (both read z once; nothing needs to be kept between them) or both. dz may be z
+ *    itself (same pointer and stride). dloss [N] fp32, or NULL for 1.
+ *  - Statistics are fp32 over a row held on chip; dz is rounded once. The same inputs
+ *    give the same bits.
+ * 0 <= K <= 1024; 1 <= V <= 393216; temperature > 0; weights finite. Device condition:
+ * a token or label outside [-1, V) raises TW_EINVAL in *dev_status and is read as -1. */
+tw_status tw_distill(const void* z, int64_t ldz, int N, int V, int dtype, const int32_t* t_idx, const void* t_val,
+                     int t_dtype, int K, const float* t_rest, const int32_t* labels, float temperature,
+                     float kd_weight, float ce_weight, const float* dloss, float scale, float* loss, void* dz,
+                     int64_t lddz, int32_t* dev_status, void* stream);
+
+/* Log probabilities of given tokens under p = softmax(z / temperature), z [N, V], with
+ * the entropy and the top alternatives of each row, in one pass over z:
+ *   logprob[n, s] = log p[tokens[n, s]]   (0 where the token is -1)
+ *   entropy[n] = -sum p log p             (natural logarithm; a term with p = 0 is 0)
+ *   top_idx, top_logprob [n, k]: the top_k largest logits in descending order, ties to
+ *     the lower token (-0 and 0 are equal), and their log probabilities
+ * n_tokens >= 0 tokens a row (tokens, logprob NULL when 0); entropy NULL when not wanted;
+ * 0 <= top_k <= 128 (top_idx, top_logprob NULL when 0). Masked logits are -inf: their
+ * log probability is -inf, and they are no alternatives: places past the unmasked ones
+ * hold index -1 and -inf. A row with nothing but -inf has entropy 0. A NaN or +inf in a
+ * row makes its log probabilities and entropy NaN and its top indices -1.
+ * 1 <= V <= 393216; temperature > 0. Device condition: a token outside [-1, V) raises
+ * TW_EINVAL in *dev_status and is read as -1. */
+tw_status tw_token_logprobs(const void* z, int64_t ldz, int N, int V, int dtype, const int32_t* tokens, int n_tokens,
+                            float temperature, int top_k, float* logprob, float* entropy, int32_t* top_idx,
+                            float* top_logprob, int32_t* dev_status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -24,8 +24,10 @@ namespace tw {
 
 namespace {
 
-constexpr int kMaxThreads = 512;
-constexpr int kMaxWarps = kMaxThreads / 32;
+constexpr int kMaxThreads = 256;
+constexpr int kMaxWarps = kMaxThreads / 32;  // 8, the most CTAs of a cluster too: partial
+constexpr int kParts = 8;                    // statistics are joined over eight lanes
+static_assert(kMaxWarps <= kParts, "one lane per warp's partial statistics");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -34,10 +36,26 @@ TW_DEV float neg_inf_f() { return __int_as_float(0xFF800000); }
 TW_DEV float base_of(float M) { return M == neg_inf_f() ? 0.f : M; }
 TW_DEV float exp_of(float z, float base, float c) { return exp2_fast((z - base) * c); }
 
+// over groups of W lanes
+template <int W = 32>
 TW_DEV float warp_max(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  for (int o = W / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
   return v;
+}
+template <int W>
+TW_DEV float group_sum(float v) {
+#pragma unroll
+  for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+TW_DEV f32x2 exp2_pair(f32x2 t) {
+  const float2 f = unpair(t);
+  return pair(exp2_fast(f.x), exp2_fast(f.y));
+}
+TW_DEV float add_lanes(f32x2 v) {
+  const float2 f = unpair(v);
+  return f.x + f.y;
 }
 
 // ------------------------------------------------------------------ a CTA's slice of a row
@@ -58,11 +76,14 @@ struct Slice {
     const int per = (vecs + cluster - 1) / cluster;
     first = rank * per;
     n = max(0, min(per, vecs - first));
+    // the first and the last vector may reach outside the row, all others are whole
+    const S* src = row + col(0);
+#pragma unroll 4
     for (int j = threadIdx.x; j < n; j += blockDim.x) {
-      const int c = col(j);
-      if (c >= 0 && c + E <= V) {
-        cp_async16(buf + j, row + c);
+      if ((first + j > 0 || lead == 0) && (first + j + 1 < vecs || (V + lead) % E == 0)) {
+        cp_async16(buf + j, src + static_cast<ptrdiff_t>(j) * E);
       } else {
+        const int c = col(j);
         S* e = reinterpret_cast<S*>(buf + j);
 #pragma unroll
         for (int i = 0; i < E; ++i) e[i] = (c + i >= 0 && c + i < V) ? row[c + i] : Elem<DT>::neg_inf();
@@ -80,6 +101,7 @@ struct Slice {
   // the largest of the thread's own vectors
   TW_DEV float own_max() const {
     float m = neg_inf_f();
+#pragma unroll 4
     for (int j = threadIdx.x; j < n; j += blockDim.x) m = fmaxf(m, Elem<DT>::max16(buf[j]));
     return m;
   }
@@ -91,15 +113,16 @@ struct DistillStat {
   float s1;             // at temperature 1 over all (TWO only)
 };
 
-// Joins one DistillStat per lane (M = -inf, sums 0 in unused lanes); all lanes get it.
-template <bool TWO>
+// Joins one DistillStat per lane over groups of W lanes (M = -inf, sums 0 in unused
+// lanes); each lane of a group gets it.
+template <bool TWO, int W>
 TW_DEV DistillStat join(DistillStat a, float c0) {
   DistillStat r;
-  r.M = warp_max(a.M);
+  r.M = warp_max<W>(a.M);
   const float base = base_of(r.M), f0 = exp_of(a.M, base, c0);
-  r.rest = warp_sum(a.rest * f0);
-  r.list = warp_sum(a.list * f0);
-  r.s1 = TWO ? warp_sum(a.s1 * exp_of(a.M, base, kLog2e)) : 0.f;
+  r.rest = group_sum<W>(a.rest * f0);
+  r.list = group_sum<W>(a.list * f0);
+  r.s1 = TWO ? group_sum<W>(a.s1 * exp_of(a.M, base, kLog2e)) : 0.f;
   return r;
 }
 
@@ -113,7 +136,7 @@ TW_DEV float teacher_logit(const void* p, size_t i, int dtype) {
 
 // One row per cluster. TWO: the hard-label term needs sums of its own (temperature not 1).
 template <int DT, bool TWO>
-__global__ void __launch_bounds__(kMaxThreads) distill_kernel(const DistillArgs a, int cluster, int slice_bytes) {
+__global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillArgs a, int cluster, int slice_bytes) {
   using El = Elem<DT>;
   using S = typename El::S;
   constexpr int E = El::E;
@@ -217,38 +240,44 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(const DistillArgs 
     st.M = m;
     st.rest = st.list = st.s1 = 0.f;
     const float b = base_of(m);
+    const f32x2 minus = both(-b), k0 = both(c0), k1 = both(kLog2e);
+    f32x2 sum0 = both(0.f), sum1 = both(0.f);
+#pragma unroll 2
     for (int j = tid; j < sl.n; j += nt) {
-      float v[E];
-      El::unpack(sl.buf[j], v);
+      f32x2 v[E / 2];
+      El::pairs(sl.buf[j], v);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        st.rest += exp_of(v[e], b, c0);
-        if (TWO) st.s1 += exp_of(v[e], b, kLog2e);
+      for (int e = 0; e < E / 2; ++e) {
+        const f32x2 d = add2(v[e], minus);
+        sum0 = add2(sum0, exp2_pair(mul2(d, k0)));
+        if (TWO) sum1 = add2(sum1, exp2_pair(mul2(d, k1)));
       }
     }
+    st.rest = add_lanes(sum0);
+    if (TWO) st.s1 = add_lanes(sum1);
     if (some)
       for (int k = tid; k < K; k += nt)
         if (l_idx[k] >= 0) {
           st.list += exp_of(l_z[k], b, c0);
           if (TWO) st.s1 += exp_of(l_z[k], b, kLog2e);
         }
-    st = join<TWO>(st, c0);
+    st = join<TWO, 32>(st, c0);
     const DistillStat none = {neg_inf_f(), 0.f, 0.f, 0.f};
     if (lane == 0) wstat[warp] = st;
     __syncthreads();
-    st = join<TWO>(lane < warps ? wstat[lane] : none, c0);
+    st = join<TWO, kParts>(lane % kParts < warps ? wstat[lane % kParts] : none, c0);
     if (cluster > 1) {
       if (tid == 0) cstat = st;
       cluster_sync();
       DistillStat p = none;
-      if (lane < cluster) {
-        const uint32_t at = peer_smem_addr(&cstat, lane);
+      if (lane % kParts < cluster) {
+        const uint32_t at = peer_smem_addr(&cstat, lane % kParts);
         p.M = ld_cluster_f32(at);
         p.rest = ld_cluster_f32(at + 4);
         p.list = ld_cluster_f32(at + 8);
         p.s1 = ld_cluster_f32(at + 12);
       }
-      st = join<TWO>(p, c0);
+      st = join<TWO, kParts>(p, c0);
       cluster_arrive();  // waited for at the end: no CTA leaves while its cstat is read
     }
   }
@@ -290,22 +319,27 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(const DistillArgs 
     const float w = label >= 0 ? gc / s1 : 0.f;
     if (!TWO) u += w;
     const bool vec = Slice<DT>::lead_of(dz) == sl.lead;
+    const f32x2 minus = both(-b), k0 = both(c0), k1 = both(kLog2e), u2 = both(u), w2 = both(w);
+#pragma unroll 2
     for (int j = tid; j < sl.n; j += nt) {
-      float v[E];
-      El::unpack(sl.buf[j], v);
+      f32x2 v[E / 2];
+      El::pairs(sl.buf[j], v);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        float d = u * exp_of(v[e], b, c0);
-        if (TWO) d = fmaf(w, exp_of(v[e], b, kLog2e), d);
-        v[e] = zero ? 0.f : d;
+      for (int e = 0; e < E / 2; ++e) {
+        const f32x2 t = add2(v[e], minus);
+        v[e] = mul2(u2, exp2_pair(mul2(t, k0)));
+        if (TWO) fma2(v[e], w2, exp2_pair(mul2(t, k1)));
       }
+      uint4 out = El::pack_pairs(v);
+      if (zero) out = make_uint4(0, 0, 0, 0);
       const int c = sl.col(j);
       if (vec && c >= 0 && c + E <= a.V) {
-        *reinterpret_cast<uint4*>(dz + c) = El::pack(v);
+        *reinterpret_cast<uint4*>(dz + c) = out;
       } else {
+        const S* o = reinterpret_cast<const S*>(&out);
 #pragma unroll
         for (int e = 0; e < E; ++e)
-          if (c + e >= 0 && c + e < a.V) dz[c + e] = El::put(v[e]);
+          if (c + e >= 0 && c + e < a.V) dz[c + e] = o[e];
       }
     }
     __syncthreads();  // the listed tokens and the label overwrite what the sweep stored
@@ -342,12 +376,13 @@ __global__ void __launch_bounds__(kMaxThreads) distill_kernel(const DistillArgs 
 struct ProbStat {
   float M, s, w;  // s = sum 2^t, w = sum 2^t t, t = c (z - M)
 };
+template <int W>
 TW_DEV ProbStat join(ProbStat a, float c) {
   ProbStat r;
-  r.M = warp_max(a.M);
+  r.M = warp_max<W>(a.M);
   const float d = (a.M - base_of(r.M)) * c, f = exp2_fast(d);
-  r.s = warp_sum(a.s * f);
-  r.w = warp_sum(f * fmaf(a.s, fmaxf(d, -1e30f), a.w));  // the bound keeps 0 (-inf) out
+  r.s = group_sum<W>(a.s * f);
+  r.w = group_sum<W>(f * fmaf(a.s, fmaxf(d, -1e30f), a.w));  // the bound keeps 0 (-inf) out
   return r;
 }
 
@@ -374,32 +409,47 @@ TW_DEV void rank_select(const Key* cand, int n, Key* top, int K) {
   }
 }
 
-// The K largest keys of the CTA's slice, descending, into top (0 past the finite ones).
-// mine: the thread's largest element. A threshold that at least K threads reach with
-// one element leaves few candidates; a list that overflows (many ties, or the largest
-// elements all with few threads) falls back to K sweeps for the next largest key.
-template <int DT>
-TW_DEV void slice_top(const Slice<DT>& sl, float mine, int K, Key* cand, Key* top, int* count, Key* wkey) {
-  using El = Elem<DT>;
-  constexpr int E = El::E;
-  const int tid = threadIdx.x, nt = blockDim.x;
-  const uint32_t high = mine > neg_inf_f() ? order_of(mine) >> 16 : 0;  // 0: nothing to give
+// A threshold on the upper half of order_of that at least K (or all) of the CTA's n
+// values reach, and not many more: a search bit by bit, by one warp.
+TW_DEV uint32_t find_threshold(const uint16_t* high, int n, int K) {
+  const int lane = threadIdx.x & 31;
+  uint32_t h[kMaxThreads / 32];
+#pragma unroll
+  for (int i = 0; i < kMaxThreads / 32; ++i) h[i] = i * 32 + lane < n ? high[i * 32 + lane] : 0;
   uint32_t thr = 0;
   for (int b = 15; b >= 0; --b) {
     const uint32_t t = thr | (1u << b);
-    const int c = __syncthreads_count(high >= t);
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < kMaxThreads / 32; ++i) c += h[i] >= t ? 1 : 0;
+    c = __reduce_add_sync(0xFFFFFFFFu, c);
     if (c >= K) {
       thr = t;
-      if (c <= 2 * K + 16) break;
+      if (c <= K + K / 2) break;
     }
   }
-  if (tid == 0) *count = 0;
-  for (int k = tid; k < K; k += nt) top[k] = 0;
-  __syncthreads();
+  return thr;
+}
+
+// The K largest keys of the CTA's slice, descending, into top (0 past the finite ones).
+// A threshold that the largest elements of at least K threads reach leaves few
+// candidates; a list that overflows (many ties, or the largest elements all with few
+// threads) falls back to K sweeps for the next largest key. high: the upper half of the
+// order of the thread's largest element, 0 when it has none; thr, count: set by the
+// caller behind a barrier.
+template <int DT>
+TW_DEV void slice_top(const Slice<DT>& sl, uint32_t high, int K, Key* cand, Key* top, uint32_t thr, int* count,
+                      Key* wkey) {
+  using El = Elem<DT>;
+  constexpr int E = El::E;
+  const int tid = threadIdx.x, nt = blockDim.x;
   if (high != 0 && high >= thr) {
     for (int j = tid; j < sl.n; j += nt) {
+      const uint4 w = sl.buf[j];
+      const float m = El::max16(w);
+      if (!(m > neg_inf_f()) || (order_of(m) >> 16) < thr) continue;
       float v[E];
-      El::unpack(sl.buf[j], v);
+      El::unpack(w, v);
 #pragma unroll
       for (int e = 0; e < E; ++e)
         if (v[e] > neg_inf_f() && (order_of(v[e]) >> 16) >= thr) {
@@ -440,13 +490,15 @@ TW_DEV void slice_top(const Slice<DT>& sl, float mine, int K, Key* cand, Key* to
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kMaxThreads) logprobs_kernel(const LogprobArgs a, int cluster, int slice_bytes) {
+__global__ void __launch_bounds__(kMaxThreads, 3) logprobs_kernel(const LogprobArgs a, int cluster, int slice_bytes) {
   using El = Elem<DT>;
   using S = typename El::S;
   constexpr int E = El::E;
   extern __shared__ uint4 smem[];
   __shared__ ProbStat wstat[kMaxWarps], cstat;
   __shared__ Key wkey[kMaxWarps];
+  __shared__ uint16_t high_of[kMaxThreads];
+  __shared__ uint32_t thr;
   __shared__ int count;
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = nt >> 5;
   const int rank = blockIdx.x % cluster;
@@ -465,53 +517,75 @@ __global__ void __launch_bounds__(kMaxThreads) logprobs_kernel(const LogprobArgs
   const float mine = sl.own_max();
   st.M = mine;
   st.s = st.w = 0.f;
-  const float b = base_of(mine);
-  for (int j = tid; j < sl.n; j += nt) {
-    float v[E];
-    El::unpack(sl.buf[j], v);
+  {
+    const float b = base_of(mine);
+    const f32x2 minus = both(-b), k = both(c);
+    f32x2 sum = both(0.f), weighted = both(0.f);
+#pragma unroll 2
+    for (int j = tid; j < sl.n; j += nt) {
+      f32x2 v[E / 2];
+      El::pairs(sl.buf[j], v);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float t = (v[e] - b) * c, p = exp2_fast(t);
-      st.s += p;
-      st.w = fmaf(p, fmaxf(t, -1e30f), st.w);  // -inf: 0 times a finite number
+      for (int e = 0; e < E / 2; ++e) {
+        const f32x2 t = mul2(add2(v[e], minus), k), p = exp2_pair(t);
+        sum = add2(sum, p);
+        const float2 f = unpair(t);
+        fma2(weighted, p, pair(fmaxf(f.x, -1e30f), fmaxf(f.y, -1e30f)));  // -inf: 0 times a finite number
+      }
+    }
+    st.s = add_lanes(sum);
+    st.w = add_lanes(weighted);
+  }
+  st = join<32>(st, c);
+  if (lane == 0) wstat[warp] = st;
+  const uint32_t high = mine > neg_inf_f() ? order_of(mine) >> 16 : 0;
+  if (K > 0) high_of[tid] = static_cast<uint16_t>(high);
+  __syncthreads();
+  // warp 0: the slice's statistics, and the threshold of its alternatives
+  const ProbStat none = {neg_inf_f(), 0.f, 0.f};
+  if (warp == 0) {
+    st = join<kParts>(lane % kParts < warps ? wstat[lane % kParts] : none, c);
+    if (lane == 0) cstat = st;
+    if (K > 0) {
+      const uint32_t t = find_threshold(high_of, nt, K);
+      if (lane == 0) thr = t, count = 0;
+      for (int k = lane; k < K; k += 32) top[k] = 0;
     }
   }
-  st = join(st, c);
-  const ProbStat none = {neg_inf_f(), 0.f, 0.f};
-  if (lane == 0) wstat[warp] = st;
-  if (K > 0) slice_top<DT>(sl, mine, K, cand, top, &count, wkey);
-  __syncthreads();
-  st = join(lane < warps ? wstat[lane] : none, c);
+  if (K > 0) {
+    __syncthreads();
+    slice_top<DT>(sl, high, K, cand, top, thr, &count, wkey);
+  }
   if (cluster > 1) {
-    if (tid == 0) cstat = st;
     cluster_sync();
     if (rank == 0) {
-      ProbStat p = none;
-      if (lane < cluster) {
-        const uint32_t at = peer_smem_addr(&cstat, lane);
-        p.M = ld_cluster_f32(at);
-        p.s = ld_cluster_f32(at + 4);
-        p.w = ld_cluster_f32(at + 8);
+      if (warp == 0) {
+        ProbStat p = none;
+        if (lane % kParts < cluster) {
+          const uint32_t at = peer_smem_addr(&cstat, lane % kParts);
+          p.M = ld_cluster_f32(at);
+          p.s = ld_cluster_f32(at + 4);
+          p.w = ld_cluster_f32(at + 8);
+        }
+        st = join<kParts>(p, c);
       }
-      st = join(p, c);
-      if (K > 0) {
-        for (int i = tid; i < cluster * K; i += nt) cand[i] = ld_cluster_u64(peer_smem_addr(top + i % K, i / K));
-      }
+      for (int i = tid; i < cluster * K; i += nt) cand[i] = ld_cluster_u64(peer_smem_addr(top + i % K, i / K));
     }
-    cluster_sync();  // every top list has been read: the CTAs may leave, rank 0 may overwrite its own
+    cluster_sync();  // every list has been read: the CTAs may leave, rank 0 may overwrite its own
     if (rank != 0) return;
     if (K > 0) {
       for (int k = tid; k < K; k += nt) top[k] = 0;
       __syncthreads();
       rank_select(cand, cluster * K, top, K);
-      __syncthreads();
     }
   }
+  if (K > 0) __syncthreads();
+  if (warp != 0) return;
 
   const float bm = base_of(st.M), l2 = log2f(st.s);
   const bool empty = st.s == 0.f;  // every logit -inf
   auto logprob = [&](float v) { return empty ? neg_inf_f() : kLn2 * ((v - bm) * c - l2); };
-  for (int i = tid; i < a.n_tokens; i += nt) {
+  for (int i = lane; i < a.n_tokens; i += 32) {
     const int t = a.tokens[row * a.n_tokens + i];
     float lp = 0.f;
     if (t >= 0 && t < a.V)
@@ -522,7 +596,7 @@ __global__ void __launch_bounds__(kMaxThreads) logprobs_kernel(const LogprobArgs
   }
   if (tid == 0 && a.entropy != nullptr) a.entropy[row] = empty ? 0.f : kLn2 * (l2 - st.w / st.s);
   const bool bad = !(st.s < __int_as_float(0x7F800000));  // a NaN or an infinity in the row
-  for (int k = tid; k < K; k += nt) {
+  for (int k = lane; k < K; k += 32) {
     const Key key = top[k];
     a.top_idx[row * K + k] = key == 0 || bad ? -1 : static_cast<int>(~static_cast<uint32_t>(key));
     a.top_logprob[row * K + k] = bad ? __int_as_float(0x7FC00000) : key == 0 ? neg_inf_f() : logprob(value_of(key >> 32));
@@ -545,9 +619,9 @@ RowShape row_shape(int64_t N, int V, int dtype, int top_k) {
   while (r.cluster < 8 && bytes() > 64 * 1024) r.cluster *= 2;
   while (r.cluster < 8 && N * r.cluster * 2 <= device_sm_count() && bytes() > 8 * 1024) r.cluster *= 2;
   r.slice_bytes = bytes();
-  // four vectors a thread; four threads an alternative, so that a threshold which top_k
+  // eight vectors a thread; two threads an alternative, so that a threshold which top_k
   // threads reach is passed by few elements
-  r.threads = std::max({128, (r.slice_bytes / 16 / 4 + 31) / 32 * 32, 4 * ((top_k + 31) / 32 * 32)});
+  r.threads = std::max({64, (r.slice_bytes / 16 / 8 + 31) / 32 * 32, 2 * ((top_k + 31) / 32 * 32)});
   r.threads = std::min(r.threads, kMaxThreads);
   return r;
 }

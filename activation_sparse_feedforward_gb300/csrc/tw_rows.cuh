@@ -8,8 +8,8 @@
 namespace tw {
 
 // ------------------------------------------------------------------ element types
-// Elem<TW_*>: storage S, E elements per 16 bytes, widening to fp32 (exact) and
-// narrowing (round to nearest even).
+// Elem<TW_*>: storage S, E elements per 16 bytes, widening to fp32 (exact; pairs: as
+// packed pairs) and narrowing (round to nearest even).
 template <int DT>
 struct Elem;
 
@@ -20,9 +20,17 @@ struct Elem<TW_F32> {
   static TW_DEV float get(S v) { return v; }
   static TW_DEV S put(float v) { return v; }
   static TW_DEV S neg_inf() { return __int_as_float(0xFF800000); }
+  static TW_DEV void pairs(const uint4& w, f32x2 (&v)[2]) {
+    v[0] = pair(__uint_as_float(w.x), __uint_as_float(w.y));
+    v[1] = pair(__uint_as_float(w.z), __uint_as_float(w.w));
+  }
   static TW_DEV void unpack(const uint4& w, float (&v)[4]) {
     v[0] = __uint_as_float(w.x), v[1] = __uint_as_float(w.y);
     v[2] = __uint_as_float(w.z), v[3] = __uint_as_float(w.w);
+  }
+  static TW_DEV uint4 pack_pairs(const f32x2 (&v)[2]) {
+    const float2 a = unpair(v[0]), b = unpair(v[1]);
+    return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
   }
   static TW_DEV uint4 pack(const float (&v)[4]) {
     return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
@@ -40,10 +48,22 @@ struct Elem<TW_BF16> {
   static TW_DEV float get(S v) { return bf16_to_f32(v); }
   static TW_DEV S put(float v) { return f32_to_bf16(v); }
   static TW_DEV S neg_inf() { return 0xFF80; }
+  static TW_DEV void pairs(const uint4& w, f32x2 (&v)[4]) {
+    v[0] = widen(w.x), v[1] = widen(w.y), v[2] = widen(w.z), v[3] = widen(w.w);
+  }
   static TW_DEV void unpack(const uint4& w, float (&v)[8]) {
     const uint32_t r[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(r[i]), v[2 * i + 1] = bf16_hi(r[i]);
+  }
+  static TW_DEV uint4 pack_pairs(const f32x2 (&v)[4]) {
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = unpair(v[i]);
+      r[i] = pack_bf16x2_rn(f.x, f.y);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
   }
   static TW_DEV uint4 pack(const float (&v)[8]) {
     return make_uint4(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]), pack_bf16x2_rn(v[4], v[5]),
@@ -64,6 +84,14 @@ struct Elem<TW_F16> {
   static TW_DEV float get(S v) { return f16_to_f32(v); }
   static TW_DEV S put(float v) { return f32_to_f16(v); }
   static TW_DEV S neg_inf() { return 0xFC00; }
+  static TW_DEV void pairs(const uint4& w, f32x2 (&v)[4]) {
+    const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r[i]));
+      v[i] = pair(f.x, f.y);
+    }
+  }
   static TW_DEV void unpack(const uint4& w, float (&v)[8]) {
     const uint32_t r[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -71,6 +99,15 @@ struct Elem<TW_F16> {
       const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r[i]));
       v[2 * i] = f.x, v[2 * i + 1] = f.y;
     }
+  }
+  static TW_DEV uint4 pack_pairs(const f32x2 (&v)[4]) {
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = unpair(v[i]);
+      r[i] = pack_f16x2_rn(f.x, f.y);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
   }
   static TW_DEV uint4 pack(const float (&v)[8]) {
     return make_uint4(pack_f16x2_rn(v[0], v[1]), pack_f16x2_rn(v[2], v[3]), pack_f16x2_rn(v[4], v[5]),
@@ -83,6 +120,19 @@ struct Elem<TW_F16> {
     return fmaxf(f.x, f.y);
   }
 };
+
+// Packed fp32 pairs, one rounding per lane (half the instructions of two floats).
+TW_DEV f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+TW_DEV f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+TW_DEV f32x2 both(float v) { return pair(v, v); }
 
 // ------------------------------------------------------------------ asynchronous copies
 // One 16-byte copy, global to shared, past L1; the copying thread sees its own copies

@@ -49,6 +49,7 @@ TW_DEV float group_sum(float v) {
   for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
 }
+
 TW_DEV f32x2 exp2_pair(f32x2 t) {
   const float2 f = unpair(t);
   return pair(exp2_fast(f.x), exp2_fast(f.y));
@@ -57,73 +58,243 @@ TW_DEV float add_lanes(f32x2 v) {
   const float2 f = unpair(v);
   return f.x + f.y;
 }
+// v^POW, POW 2 or 4
+template <int POW>
+TW_DEV f32x2 power(f32x2 v) {
+  const f32x2 q = mul2(v, v);
+  return POW == 4 ? mul2(q, q) : q;
+}
 
-// ------------------------------------------------------------------ a CTA's slice of a row
+// ------------------------------------------------------------------ a CTA's part of a row
 // The row's address may have any element alignment: vectors are counted from the
-// 16-byte boundary at or before it, so column c sits in vector (c + lead) / E. A vector
-// that reaches outside the row is filled element by element, with -inf outside.
+// 16-byte boundary at or before it, so column c sits in vector (c + lead) / E. Only the
+// row's first and last vector may reach outside it; those are read element by element,
+// with -inf outside.
 template <int DT>
-struct Slice {
+struct Part {
   using S = typename Elem<DT>::S;
   static constexpr int E = Elem<DT>::E;
-  uint4* buf;
+  const S* row;
   int lead, V, first, n;  // n vectors from the row's vector `first`
+  int lo, hi;             // those of them that are whole: [lo, hi)
 
   static TW_DEV int lead_of(const S* row) { return static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(S)); }
 
-  TW_DEV Slice(const S* row, int V_, int rank, int cluster, uint4* b) : buf(b), lead(lead_of(row)), V(V_) {
+  TW_DEV Part(const S* row_, int V_, int rank, int cluster) : row(row_), lead(lead_of(row_)), V(V_) {
     const int vecs = (V + lead + E - 1) / E;
     const int per = (vecs + cluster - 1) / cluster;
     first = rank * per;
     n = max(0, min(per, vecs - first));
-    // the first and the last vector may reach outside the row, all others are whole
-    const S* src = row + col(0);
-#pragma unroll 4
-    for (int j = threadIdx.x; j < n; j += blockDim.x) {
-      if ((first + j > 0 || lead == 0) && (first + j + 1 < vecs || (V + lead) % E == 0)) {
-        cp_async16(buf + j, src + static_cast<ptrdiff_t>(j) * E);
-      } else {
-        const int c = col(j);
-        S* e = reinterpret_cast<S*>(buf + j);
-#pragma unroll
-        for (int i = 0; i < E; ++i) e[i] = (c + i >= 0 && c + i < V) ? row[c + i] : Elem<DT>::neg_inf();
-      }
-    }
-    cp_commit();
+    lo = first == 0 && lead > 0 ? 1 : 0;
+    hi = min(n, (V + lead) / E - first);
   }
-  // first column of the slice's vector j
+  // first column of the part's vector j
   TW_DEV int col(int j) const { return (first + j) * E - lead; }
-  // the element of column c, or null when another CTA holds it
-  TW_DEV S* at(int c) const {
-    const int e = c + lead - first * E;
-    return e >= 0 && e < n * E ? reinterpret_cast<S*>(buf) + e : nullptr;
-  }
-  // the largest of the thread's own vectors
-  TW_DEV float own_max() const {
-    float m = neg_inf_f();
-#pragma unroll 4
-    for (int j = threadIdx.x; j < n; j += blockDim.x) m = fmaxf(m, Elem<DT>::max16(buf[j]));
-    return m;
+  TW_DEV bool whole(int j) const { return j >= lo && j < hi; }
+  TW_DEV const S* at(int j) const { return row + col(j); }
+  TW_DEV uint4 edge(int j) const {
+    union {
+      S e[E];
+      uint4 w;
+    } u;
+    const int c = col(j);
+#pragma unroll
+    for (int i = 0; i < E; ++i) u.e[i] = (c + i >= 0 && c + i < V) ? row[c + i] : Elem<DT>::neg_inf();
+    return u.w;
   }
 };
 
+// The same part copied to shared memory: a thread copies, and then sweeps, the whole
+// vectors lo + threadIdx.x, lo + threadIdx.x + blockDim.x, ...; the edges are the CTA's
+// first and last thread's.
+template <int DT>
+struct Slice : Part<DT> {
+  using P = Part<DT>;
+  using typename P::S;
+  using P::E;
+  uint4* buf;
+
+  TW_DEV Slice(const S* row, int V, int rank, int cluster, uint4* b) : P(row, V, rank, cluster), buf(b) {
+    const int nt = blockDim.x;
+    uint4* dst = buf + this->lo + threadIdx.x;
+    const uint4* src = reinterpret_cast<const uint4*>(P::at(this->lo)) + threadIdx.x;
+    int j = this->lo + threadIdx.x;
+#pragma unroll 4
+    for (; j < this->hi; j += nt, dst += nt, src += nt) cp_async16(dst, src);
+    if (first_edge()) buf[0] = P::edge(0);
+    if (last_edge()) buf[this->n - 1] = P::edge(this->n - 1);
+    cp_commit();
+  }
+  // whether this thread holds the slice's first (last) vector as one that is not whole
+  TW_DEV bool first_edge() const { return threadIdx.x == 0 && this->lo > 0; }
+  TW_DEV bool last_edge() const { return threadIdx.x == blockDim.x - 1 && this->hi < this->n && this->n > this->lo; }
+  // the element of column c, or null when another CTA holds it
+  TW_DEV S* element(int c) const {
+    const int e = c + this->lead - this->first * E;
+    return e >= 0 && e < this->n * E ? reinterpret_cast<S*>(buf) + e : nullptr;
+  }
+};
+
+// ------------------------------------------------------------------ exponentials of a sweep
+// A sweep takes 2^(c (z - m)) of many z for one m. Where c m is of ordinary size that is
+// one fused multiply-add and one exponential, 2^(c z - k) with k = c m rounded, and the
+// sweep's sums are corrected once by 2^(k - c m), whose exponent the fused operation
+// gives exactly. Past 2^20 the rounding of k would leave more than a fraction of the
+// exponent (a mask of the type's lowest value ends there), and m is taken off z first.
+struct Scale {
+  float m, c, k;
+  bool fused;
+  TW_DEV Scale(float max, float c_) : m(base_of(max)), c(c_), k(m * c_) { fused = fabsf(k) < 1048576.f; }
+  TW_DEV float shift() const { return fused ? -fmaf(m, c, -k) : 0.f; }  // k - c m
+  // what the exponent c z - k grows by when `to` is used in place of this one
+  TW_DEV float move(const Scale& to) const { return fmaf(m - to.m, c, shift() - to.shift()); }
+  template <bool FUSED>
+  TW_DEV f32x2 exponent(f32x2 z) const {
+    if (FUSED) {
+      f32x2 t = both(-k);
+      fma2(t, z, both(c));
+      return t;
+    }
+    return mul2(add2(z, both(-m)), both(c));
+  }
+};
+
+constexpr int kBatch = 4;  // vectors a thread takes at a time
+
+// f(j, all) for the thread's vectors j, j + blockDim.x, ... of [lo, hi) in batches of
+// kBatch; all: a constant, whether the whole batch is below hi.
+struct Yes { static constexpr bool value = true; };
+struct No { static constexpr bool value = false; };
+template <class F>
+TW_DEV void in_batches(int lo, int hi, F f) {
+  const int nt = blockDim.x;
+  int j = lo + threadIdx.x;
+  for (; j + (kBatch - 1) * nt < hi; j += kBatch * nt) f(j, Yes());
+  if (j < hi) f(j, No());
+}
+
+// A thread's online sums over its vectors, in batches. The reference m follows the
+// running maximum, but only when that is more than kSlack above it (in nats at
+// temperature 1): sums are rescaled a few times a row, and no term exceeds e^kSlack.
+constexpr float kSlack = 8.f;
+
+template <int DT>
+struct Running {
+  typename Elem<DT>::Max top;
+  float limit = -__builtin_huge_valf();
+  // Takes a batch into the maximum; true when the reference has to
+  // move to it.
+  TW_DEV bool grow(const uint4 (&r)[kBatch], float slack) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) top.add(r[i]);
+    const float m = top.get();
+    if (!(m > limit)) return false;
+    limit = m + slack;
+    return true;
+  }
+};
+// a batch of nothing but -inf
+template <int DT>
+TW_DEV uint4 no_vector() {
+  constexpr uint32_t v = DT == TW_F32 ? 0xFF800000u : DT == TW_BF16 ? 0xFF80FF80u : 0xFC00FC00u;
+  return make_uint4(v, v, v, v);
+}
+
 // ------------------------------------------------------------------ distillation
+// The hard-label term wants sums of e^z at temperature 1. How a kernel gets them beside
+// the sums of p = e^(z / temperature): HARD = kNoSum where there are no labels or the
+// temperature is 1; 2 or 4 where the temperature is that: p^2 or p^4, products in place
+// of a second exponential an element in each sweep (4096 x 131072 bf16 at temperature 2:
+// the exponentials alone would keep their unit busy for three quarters of the floor);
+// kOwnSum at any other temperature.
+constexpr int kNoSum = 0, kOwnSum = 1;
+
 struct DistillStat {
   float M, rest, list;  // sums at the temperature over the unlisted and the listed tokens
-  float s1;             // at temperature 1 over all (TWO only)
+  float s1;             // at temperature 1 over all (not with kNoSum)
 };
+
+// The scale at temperature 1 beside `a` at the temperature. (c is log2(e) / HARD, an
+// exact division, so HARD times c, k and the shift are exact too.)
+template <int HARD>
+TW_DEV Scale hard_scale(const Scale& a) {
+  Scale b(a.m, kLog2e);
+  if (HARD == 2 || HARD == 4) b.k = HARD * a.k, b.fused = a.fused;
+  return b;
+}
+
 
 // Joins one DistillStat per lane over groups of W lanes (M = -inf, sums 0 in unused
 // lanes); each lane of a group gets it.
-template <bool TWO, int W>
+template <int HARD, int W>
 TW_DEV DistillStat join(DistillStat a, float c0) {
   DistillStat r;
   r.M = warp_max<W>(a.M);
   const float base = base_of(r.M), f0 = exp_of(a.M, base, c0);
   r.rest = group_sum<W>(a.rest * f0);
   r.list = group_sum<W>(a.list * f0);
-  r.s1 = TWO ? group_sum<W>(a.s1 * exp_of(a.M, base, kLog2e)) : 0.f;
+  r.s1 = HARD != kNoSum ? group_sum<W>(a.s1 * exp_of(a.M, base, kLog2e)) : 0.f;
   return r;
+}
+
+// The thread's own vectors of the slice in one sweep: their largest element m, and the
+// sums of their exponentials relative to it at the scales c0 and log2(e).
+template <int DT, int HARD, bool FUSED>
+TW_DEV void add_exps(const uint4 (&r)[kBatch], const Scale& a, const Scale& b, f32x2& s0, f32x2& s1) {
+  using El = Elem<DT>;
+#pragma unroll
+  for (int i = 0; i < kBatch; ++i) {
+    f32x2 v[El::E / 2];
+    El::pairs(r[i], v);
+#pragma unroll
+    for (int e = 0; e < El::E / 2; ++e) {
+      const f32x2 p = exp2_pair(a.exponent<FUSED>(v[e]));
+      s0 = add2(s0, p);
+      if (HARD == kOwnSum) s1 = add2(s1, exp2_pair(b.exponent<FUSED>(v[e])));
+      if (HARD == 2) fma2(s1, p, p);
+      if (HARD == 4) {
+        const f32x2 q = mul2(p, p);
+        fma2(s1, q, q);
+      }
+    }
+  }
+}
+template <int DT, int HARD>
+TW_DEV void own_sums(const Slice<DT>& sl, float c0, float& m, float& sum0, float& sum1) {
+  Running<DT> run;
+  const float slack = kSlack * fminf(1.f, kLog2e / c0);
+  f32x2 s0 = both(0.f), s1 = both(0.f);
+  Scale a(neg_inf_f(), c0), b(neg_inf_f(), kLog2e);
+  bool fused = true, some = false;
+  const int nt = blockDim.x;
+  auto batch = [&](const uint4 (&r)[kBatch]) {
+    if (run.grow(r, slack)) {
+      Scale a2(run.top.get(), c0), b2 = hard_scale<HARD>(a2);
+      a2.fused = b2.fused = fused = a2.fused && b2.fused;
+      s0 = some ? mul2(s0, both(exp2_fast(a.move(a2)))) : both(0.f);
+      if (HARD != kNoSum) s1 = some ? mul2(s1, both(exp2_fast(b.move(b2)))) : both(0.f);
+      a = a2, b = b2, some = true;
+    }
+    if (fused)
+      add_exps<DT, HARD, true>(r, a, b, s0, s1);
+    else
+      add_exps<DT, HARD, false>(r, a, b, s0, s1);
+  };
+  in_batches(sl.lo, sl.hi, [&](int j, auto all) {
+    uint4 r[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) r[i] = all.value || j + i * nt < sl.hi ? sl.buf[j + i * nt] : no_vector<DT>();
+    batch(r);
+  });
+  if (sl.first_edge() || sl.last_edge()) {
+    const uint4 r[kBatch] = {sl.first_edge() ? sl.buf[0] : no_vector<DT>(), sl.last_edge() ? sl.buf[sl.n - 1] : no_vector<DT>(),
+                             no_vector<DT>(), no_vector<DT>()};
+    batch(r);
+  }
+  m = run.top.get();
+  const float base = base_of(m);
+  sum0 = add_lanes(s0) * exp2_fast(fmaf(a.m - base, c0, a.shift()));
+  sum1 = HARD != kNoSum ? add_lanes(s1) * exp2_fast(fmaf(b.m - base, kLog2e, b.shift())) : 0.f;
 }
 
 template <int DT>
@@ -134,12 +305,54 @@ TW_DEV float teacher_logit(const void* p, size_t i, int dtype) {
   return dtype == TW_F16 ? list_value<TW_F16>(p, i, dtype) : list_value<TW_BF16>(p, i, dtype);
 }
 
-// One row per cluster. TWO: the hard-label term needs sums of its own (temperature not 1).
-template <int DT, bool TWO>
+// u 2^(c0 (z - M)) (+ w 2^(log2(e) (z - M))) of one vector
+template <int DT, int HARD, bool FUSED>
+TW_DEV uint4 gradient(const uint4& r, const Scale& a, const Scale& b, float u, float w) {
+  using El = Elem<DT>;
+  f32x2 v[El::E / 2];
+  El::pairs(r, v);
+#pragma unroll
+  for (int e = 0; e < El::E / 2; ++e) {
+    const f32x2 z = v[e], p = exp2_pair(a.exponent<FUSED>(z));
+    v[e] = mul2(both(u), p);
+    if (HARD == kOwnSum) fma2(v[e], both(w), exp2_pair(b.exponent<FUSED>(z)));
+    if (HARD == 2 || HARD == 4) fma2(v[e], both(w), power<HARD>(p));
+  }
+  return El::pack_pairs(v);
+}
+// f of each of the thread's vectors, stored at its columns of dz.
+template <int DT, class F>
+TW_DEV void store_slice(const Slice<DT>& sl, typename Elem<DT>::S* dz, F f) {
+  using S = typename Elem<DT>::S;
+  constexpr int E = Elem<DT>::E;
+  const int nt = blockDim.x;
+  auto singly = [&](int j) {
+    const uint4 g = f(sl.buf[j]);
+    const S* o = reinterpret_cast<const S*>(&g);
+    const int c = sl.col(j);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (c + e >= 0 && c + e < sl.V) dz[c + e] = o[e];
+  };
+  if (Part<DT>::lead_of(dz) == sl.lead) {  // the same alignment as z's row
+    uint4* out = reinterpret_cast<uint4*>(dz + sl.col(0));
+    in_batches(sl.lo, sl.hi, [&](int j, auto all) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (all.value || j + i * nt < sl.hi) out[j + i * nt] = f(sl.buf[j + i * nt]);
+    });
+  } else {
+    for (int j = sl.lo + threadIdx.x; j < sl.hi; j += nt) singly(j);
+  }
+  if (sl.first_edge()) singly(0);
+  if (sl.last_edge()) singly(sl.n - 1);
+}
+
+// One row per cluster.
+template <int DT, int HARD>
 __global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillArgs a, int cluster, int slice_bytes) {
   using El = Elem<DT>;
   using S = typename El::S;
-  constexpr int E = El::E;
   extern __shared__ uint4 smem[];
   __shared__ float red[2][kMaxWarps];
   __shared__ DistillStat wstat[kMaxWarps], cstat;
@@ -214,58 +427,50 @@ __global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillAr
   bool dup = false;
   if (some) {
     for (int k = tid; k < K; k += nt) {
-      S* s = l_idx[k] >= 0 ? sl.at(l_idx[k]) : nullptr;
+      S* s = l_idx[k] >= 0 ? sl.element(l_idx[k]) : nullptr;
       if (s != nullptr) *s = static_cast<S>(k);
     }
     __syncthreads();
     for (int k = tid; k < K; k += nt) {
-      const S* s = l_idx[k] >= 0 ? sl.at(l_idx[k]) : nullptr;
+      const S* s = l_idx[k] >= 0 ? sl.element(l_idx[k]) : nullptr;
       const bool owner = s != nullptr && *s == static_cast<S>(k);
       if (s != nullptr && !owner) dup = true;
       if (!owner) l_idx[k] = -2 - l_idx[k];  // not this CTA's, or another entry's: -2 - token (padding: -1)
     }
     dup = __syncthreads_or(dup);
     for (int k = tid; k < K; k += nt)
-      if (l_idx[k] >= 0) *sl.at(l_idx[k]) = El::neg_inf();
+      if (l_idx[k] >= 0) *sl.element(l_idx[k]) = El::neg_inf();
     __syncthreads();
   }
 
   // the row's statistics
   DistillStat st;
   {
-    float m = sl.own_max();
-    if (some)
+    float m = neg_inf_f();
+    own_sums<DT, HARD>(sl, c0, m, st.rest, st.s1);
+    if (some) {  // the list's tokens that this thread owns join its maximum
+      const float was = m;
       for (int k = tid; k < K; k += nt)
         if (l_idx[k] >= 0) m = fmaxf(m, l_z[k]);
-    st.M = m;
-    st.rest = st.list = st.s1 = 0.f;
-    const float b = base_of(m);
-    const f32x2 minus = both(-b), k0 = both(c0), k1 = both(kLog2e);
-    f32x2 sum0 = both(0.f), sum1 = both(0.f);
-#pragma unroll 2
-    for (int j = tid; j < sl.n; j += nt) {
-      f32x2 v[E / 2];
-      El::pairs(sl.buf[j], v);
-#pragma unroll
-      for (int e = 0; e < E / 2; ++e) {
-        const f32x2 d = add2(v[e], minus);
-        sum0 = add2(sum0, exp2_pair(mul2(d, k0)));
-        if (TWO) sum1 = add2(sum1, exp2_pair(mul2(d, k1)));
+      if (m != was) {
+        st.rest *= exp_of(was, base_of(m), c0);
+        if (HARD != kNoSum) st.s1 *= exp_of(was, base_of(m), kLog2e);
       }
     }
-    st.rest = add_lanes(sum0);
-    if (TWO) st.s1 = add_lanes(sum1);
+    st.M = m;
+    st.list = 0.f;
+    const float b = base_of(m);
     if (some)
       for (int k = tid; k < K; k += nt)
         if (l_idx[k] >= 0) {
           st.list += exp_of(l_z[k], b, c0);
-          if (TWO) st.s1 += exp_of(l_z[k], b, kLog2e);
+          if (HARD != kNoSum) st.s1 += exp_of(l_z[k], b, kLog2e);
         }
-    st = join<TWO, 32>(st, c0);
+    st = join<HARD, 32>(st, c0);
     const DistillStat none = {neg_inf_f(), 0.f, 0.f, 0.f};
     if (lane == 0) wstat[warp] = st;
     __syncthreads();
-    st = join<TWO, kParts>(lane % kParts < warps ? wstat[lane % kParts] : none, c0);
+    st = join<HARD, kParts>(lane % kParts < warps ? wstat[lane % kParts] : none, c0);
     if (cluster > 1) {
       if (tid == 0) cstat = st;
       cluster_sync();
@@ -277,13 +482,13 @@ __global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillAr
         p.list = ld_cluster_f32(at + 8);
         p.s1 = ld_cluster_f32(at + 12);
       }
-      st = join<TWO, kParts>(p, c0);
+      st = join<HARD, kParts>(p, c0);
       cluster_arrive();  // waited for at the end: no CTA leaves while its cstat is read
     }
   }
   const float total = st.rest + st.list;
   const float b = base_of(st.M);
-  const float s1 = TWO ? st.s1 : total;
+  const float s1 = HARD != kNoSum ? st.s1 : total;
   const bool nothing = !some && label < 0;  // no target: loss and gradient are 0 whatever the logits
 
   if (rank == 0 && a.loss != nullptr) {
@@ -317,31 +522,16 @@ __global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillAr
     float u = some ? gk / total : 0.f;  // factor of 2^(c0 (z - M)) on unlisted tokens
     if (p_rest != 0.f && st.rest != 0.f) u -= gk * p_rest / st.rest;
     const float w = label >= 0 ? gc / s1 : 0.f;
-    if (!TWO) u += w;
-    const bool vec = Slice<DT>::lead_of(dz) == sl.lead;
-    const f32x2 minus = both(-b), k0 = both(c0), k1 = both(kLog2e), u2 = both(u), w2 = both(w);
-#pragma unroll 2
-    for (int j = tid; j < sl.n; j += nt) {
-      f32x2 v[E / 2];
-      El::pairs(sl.buf[j], v);
-#pragma unroll
-      for (int e = 0; e < E / 2; ++e) {
-        const f32x2 t = add2(v[e], minus);
-        v[e] = mul2(u2, exp2_pair(mul2(t, k0)));
-        if (TWO) fma2(v[e], w2, exp2_pair(mul2(t, k1)));
-      }
-      uint4 out = El::pack_pairs(v);
-      if (zero) out = make_uint4(0, 0, 0, 0);
-      const int c = sl.col(j);
-      if (vec && c >= 0 && c + E <= a.V) {
-        *reinterpret_cast<uint4*>(dz + c) = out;
-      } else {
-        const S* o = reinterpret_cast<const S*>(&out);
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-          if (c + e >= 0 && c + e < a.V) dz[c + e] = o[e];
-      }
-    }
+    if (HARD == kNoSum) u += w;
+    Scale sa(st.M, c0), sb = hard_scale<HARD>(sa);
+    const bool fused = sa.fused && sb.fused;
+    const float uf = fused ? u * exp2_fast(sa.shift()) : u, wf = fused ? w * exp2_fast(sb.shift()) : w;
+    if (zero)
+      store_slice<DT>(sl, dz, [](const uint4&) { return make_uint4(0, 0, 0, 0); });
+    else if (fused)
+      store_slice<DT>(sl, dz, [&](const uint4& r) { return gradient<DT, HARD, true>(r, sa, sb, uf, wf); });
+    else
+      store_slice<DT>(sl, dz, [&](const uint4& r) { return gradient<DT, HARD, false>(r, sa, sb, uf, wf); });
     __syncthreads();  // the listed tokens and the label overwrite what the sweep stored
     bool label_listed = false;
     if (some && !zero) {
@@ -362,9 +552,9 @@ __global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillAr
     }
     if (a.labels != nullptr) {
       label_listed = __syncthreads_or(label_listed);
-      if (tid == 0 && label >= 0 && !label_listed && !zero && sl.at(label) != nullptr) {
+      if (tid == 0 && label >= 0 && !label_listed && !zero && sl.element(label) != nullptr) {
         float d = u * exp_of(z_label, b, c0) - gc;
-        if (TWO) d = fmaf(w, exp_of(z_label, b, kLog2e), d);
+        if (HARD != kNoSum) d = fmaf(w, exp_of(z_label, b, kLog2e), d);
         dz[label] = El::put(d);
       }
     }
@@ -431,32 +621,41 @@ TW_DEV uint32_t find_threshold(const uint16_t* high, int n, int K) {
   return thr;
 }
 
-// The K largest keys of the CTA's slice, descending, into top (0 past the finite ones).
+// f(vector, index) for each of the thread's whole vectors, and for the edges, which the
+// CTA's first and last thread take.
+template <int DT, class F>
+TW_DEV void each_vector(const Part<DT>& p, F f) {
+#pragma unroll 4
+  for (int j = p.lo + threadIdx.x; j < p.hi; j += blockDim.x) f(*reinterpret_cast<const uint4*>(p.at(j)), j);
+  if (threadIdx.x == 0 && p.lo > 0) f(p.edge(0), 0);
+  if (threadIdx.x == blockDim.x - 1 && p.hi < p.n && p.n > p.lo) f(p.edge(p.n - 1), p.n - 1);
+}
+
+// The K largest keys of the CTA's part, descending, into top (0 past the finite ones).
 // A threshold that the largest elements of at least K threads reach leaves few
-// candidates; a list that overflows (many ties, or the largest elements all with few
-// threads) falls back to K sweeps for the next largest key. high: the upper half of the
-// order of the thread's largest element, 0 when it has none; thr, count: set by the
-// caller behind a barrier.
+// candidates, all with threads that reach it: those read their vectors once more (from
+// L2). A list that overflows (many ties, or the largest elements all with few threads)
+// falls back to K sweeps for the next largest key. high: the upper half of the order of
+// the thread's largest element, 0 when it has none; thr, count, top: set by the caller
+// behind a barrier.
 template <int DT>
-TW_DEV void slice_top(const Slice<DT>& sl, uint32_t high, int K, Key* cand, Key* top, uint32_t thr, int* count,
-                      Key* wkey) {
+TW_DEV void part_top(const Part<DT>& p, uint32_t high, int K, Key* cand, Key* top, uint32_t thr, int* count, Key* wkey) {
   using El = Elem<DT>;
   constexpr int E = El::E;
   const int tid = threadIdx.x, nt = blockDim.x;
   if (high != 0 && high >= thr) {
-    for (int j = tid; j < sl.n; j += nt) {
-      const uint4 w = sl.buf[j];
+    each_vector(p, [&](const uint4& w, int j) {
       const float m = El::max16(w);
-      if (!(m > neg_inf_f()) || (order_of(m) >> 16) < thr) continue;
+      if (!(m > neg_inf_f()) || (order_of(m) >> 16) < thr) return;
       float v[E];
       El::unpack(w, v);
 #pragma unroll
       for (int e = 0; e < E; ++e)
         if (v[e] > neg_inf_f() && (order_of(v[e]) >> 16) >= thr) {
-          const int p = atomicAdd(count, 1);
-          if (p < kCandidates) cand[p] = key_of(v[e], sl.col(j) + e);
+          const int at = atomicAdd(count, 1);
+          if (at < kCandidates) cand[at] = key_of(v[e], p.col(j) + e);
         }
-    }
+    });
   }
   __syncthreads();
   const int n = *count;
@@ -467,15 +666,15 @@ TW_DEV void slice_top(const Slice<DT>& sl, uint32_t high, int K, Key* cand, Key*
   Key last = ~0ull;
   for (int r = 0; r < K; ++r) {
     Key best = 0;
-    for (int j = tid; j < sl.n; j += nt) {
+    each_vector(p, [&](const uint4& w, int j) {
       float v[E];
-      El::unpack(sl.buf[j], v);
+      El::unpack(w, v);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const Key k = v[e] > neg_inf_f() ? key_of(v[e], sl.col(j) + e) : 0;
+        const Key k = v[e] > neg_inf_f() ? key_of(v[e], p.col(j) + e) : 0;
         if (k < last && k > best) best = k;
       }
-    }
+    });
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xFFFFFFFFu, best, o));
     if ((tid & 31) == 0) wkey[tid >> 5] = best;
@@ -489,12 +688,78 @@ TW_DEV void slice_top(const Slice<DT>& sl, uint32_t high, int K, Key* cand, Key*
   }
 }
 
+// One vector's share of the sums s = sum 2^t and w = sum 2^t t.
+template <int DT, bool FUSED>
+TW_DEV void add_terms(const uint4& r, const Scale& a, f32x2& s, f32x2& w) {
+  using El = Elem<DT>;
+  f32x2 v[El::E / 2];
+  El::pairs(r, v);
+#pragma unroll
+  for (int e = 0; e < El::E / 2; ++e) {
+    const f32x2 t = a.exponent<FUSED>(v[e]), p = exp2_pair(t);
+    s = add2(s, p);
+    const float2 f = unpair(t);
+    fma2(w, p, pair(fmaxf(f.x, -1e30f), fmaxf(f.y, -1e30f)));  // -inf: 0 times a finite number
+  }
+}
+
+// The thread's share of the part in one sweep: its largest element and its sums relative
+// to that.
 template <int DT>
-__global__ void __launch_bounds__(kMaxThreads, 3) logprobs_kernel(const LogprobArgs a, int cluster, int slice_bytes) {
+TW_DEV ProbStat own_probs(const Part<DT>& p, float c) {
+  Running<DT> run;
+  const float slack = kSlack * fminf(1.f, kLog2e / c);
+  f32x2 s = both(0.f), w = both(0.f);
+  Scale a(neg_inf_f(), c);
+  bool some = false;
+  const int tid = threadIdx.x, nt = blockDim.x;
+  auto batch = [&](const uint4 (&r)[kBatch]) {
+    if (run.grow(r, slack)) {
+      const Scale to(run.top.get(), c);
+      const float d = fmaxf(a.move(to), -1e30f);  // finite: s and w become 0, not NaN
+      const f32x2 f = both(some ? exp2_fast(d) : 0.f);
+      fma2(w, s, both(some ? d : 0.f));
+      w = mul2(w, f);
+      s = mul2(s, f);
+      a = to, some = true;
+    }
+    if (a.fused) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) add_terms<DT, true>(r[i], a, s, w);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) add_terms<DT, false>(r[i], a, s, w);
+    }
+  };
+  const uint4* src = reinterpret_cast<const uint4*>(p.at(0));
+  in_batches(p.lo, p.hi, [&](int j, auto all) {
+    uint4 r[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) r[i] = all.value || j + i * nt < p.hi ? src[j + i * nt] : no_vector<DT>();
+    batch(r);
+  });
+  if (p.lo > 0 || p.hi < p.n) {  // the edges: one vector of the first thread, one of the last
+    uint4 r[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) r[i] = no_vector<DT>();
+    if (tid == 0 && p.lo > 0) r[0] = p.edge(0);
+    if (tid == nt - 1 && p.hi < p.n && p.n > p.lo) r[1] = p.edge(p.n - 1);
+    batch(r);
+  }
+  ProbStat st;
+  st.M = run.top.get();
+  const float d = fmaf(a.m - base_of(st.M), c, a.shift()), f = exp2_fast(d);
+  st.s = add_lanes(s);
+  st.w = f * fmaf(st.s, d, add_lanes(w));
+  st.s *= f;
+  return st;
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kMaxThreads, 4) logprobs_kernel(const LogprobArgs a, int cluster) {
   using El = Elem<DT>;
   using S = typename El::S;
-  constexpr int E = El::E;
-  extern __shared__ uint4 smem[];
+  extern __shared__ Key lists[];
   __shared__ ProbStat wstat[kMaxWarps], cstat;
   __shared__ Key wkey[kMaxWarps];
   __shared__ uint16_t high_of[kMaxThreads];
@@ -504,38 +769,15 @@ __global__ void __launch_bounds__(kMaxThreads, 3) logprobs_kernel(const LogprobA
   const int rank = blockIdx.x % cluster;
   const size_t row = blockIdx.x / cluster;
   const int K = a.K;
-  Key* cand = reinterpret_cast<Key*>(reinterpret_cast<uint8_t*>(smem) + slice_bytes);
+  Key* cand = lists;
   Key* top = cand + (K > 0 ? kCandidates : 0);
   pdl_enter();
 
   const S* z = static_cast<const S*>(a.z) + row * a.ldz;
-  Slice<DT> sl(z, a.V, rank, cluster, smem);
+  const Part<DT> part(z, a.V, rank, cluster);
   const float c = kLog2e / a.temperature;
-  cp_wait<0>();
-
-  ProbStat st;
-  const float mine = sl.own_max();
-  st.M = mine;
-  st.s = st.w = 0.f;
-  {
-    const float b = base_of(mine);
-    const f32x2 minus = both(-b), k = both(c);
-    f32x2 sum = both(0.f), weighted = both(0.f);
-#pragma unroll 2
-    for (int j = tid; j < sl.n; j += nt) {
-      f32x2 v[E / 2];
-      El::pairs(sl.buf[j], v);
-#pragma unroll
-      for (int e = 0; e < E / 2; ++e) {
-        const f32x2 t = mul2(add2(v[e], minus), k), p = exp2_pair(t);
-        sum = add2(sum, p);
-        const float2 f = unpair(t);
-        fma2(weighted, p, pair(fmaxf(f.x, -1e30f), fmaxf(f.y, -1e30f)));  // -inf: 0 times a finite number
-      }
-    }
-    st.s = add_lanes(sum);
-    st.w = add_lanes(weighted);
-  }
+  ProbStat st = own_probs(part, c);
+  const float mine = st.M;
   st = join<32>(st, c);
   if (lane == 0) wstat[warp] = st;
   const uint32_t high = mine > neg_inf_f() ? order_of(mine) >> 16 : 0;
@@ -554,7 +796,7 @@ __global__ void __launch_bounds__(kMaxThreads, 3) logprobs_kernel(const LogprobA
   }
   if (K > 0) {
     __syncthreads();
-    slice_top<DT>(sl, high, K, cand, top, thr, &count, wkey);
+    part_top<DT>(part, high, K, cand, top, thr, &count, wkey);
   }
   if (cluster > 1) {
     cluster_sync();
@@ -594,7 +836,10 @@ __global__ void __launch_bounds__(kMaxThreads, 3) logprobs_kernel(const LogprobA
       raise_status(a.status, TW_EINVAL);
     a.logprob[row * a.n_tokens + i] = lp;
   }
-  if (tid == 0 && a.entropy != nullptr) a.entropy[row] = empty ? 0.f : kLn2 * (l2 - st.w / st.s);
+  if (tid == 0 && a.entropy != nullptr) {
+    const float h = empty ? 0.f : kLn2 * (l2 - st.w / st.s);
+    a.entropy[row] = h < 0.f ? 0.f : h;  // rounding may go below; NaN stays
+  }
   const bool bad = !(st.s < __int_as_float(0x7F800000));  // a NaN or an infinity in the row
   for (int k = lane; k < K; k += 32) {
     const Key key = top[k];
@@ -605,51 +850,65 @@ __global__ void __launch_bounds__(kMaxThreads, 3) logprobs_kernel(const LogprobA
 
 // ------------------------------------------------------------------ launch shapes
 struct RowShape {
-  int cluster, threads, slice_bytes;
+  int cluster, threads, part_bytes;
 };
 
-// A slice of at most 64 KB keeps three CTAs on an SM, so that one's copies run under
-// the others' sweeps. Fewer rows than SMs: more CTAs a row, down to 8 KB each.
-RowShape row_shape(int64_t N, int V, int dtype, int top_k) {
+// The most 16-byte vectors a row of V elements covers, at any alignment.
+int row_vectors(int V, int dtype) {
   const int E = dtype == TW_F32 ? 4 : 8;
-  const int vecs = (V + 2 * E - 2) / E;  // at any alignment
+  return (V + 2 * E - 2) / E;
+}
+
+// CTAs a row (1 to 8): as few as keep a part at `most` bytes, and, while all rows
+// together make fewer than `fill` CTAs, as many as keep it at `least`. Eight vectors a
+// thread.
+RowShape row_shape(int64_t N, int V, int dtype, int most, int64_t fill, int least) {
+  const int64_t bytes = 16 * static_cast<int64_t>(row_vectors(V, dtype));
+  auto parts = [&](int64_t size) { return (bytes + size - 1) / size; };
+  const int64_t few = std::min<int64_t>(8, parts(most));
+  const int64_t many = std::min<int64_t>({8, parts(least), fill / N});
   RowShape r;
-  r.cluster = 1;
-  auto bytes = [&] { return 16 * ((vecs + r.cluster - 1) / r.cluster); };
-  while (r.cluster < 8 && bytes() > 64 * 1024) r.cluster *= 2;
-  while (r.cluster < 8 && N * r.cluster * 2 <= device_sm_count() && bytes() > 8 * 1024) r.cluster *= 2;
-  r.slice_bytes = bytes();
-  // eight vectors a thread; two threads an alternative, so that a threshold which top_k
-  // threads reach is passed by few elements
-  r.threads = std::max({64, (r.slice_bytes / 16 / 8 + 31) / 32 * 32, 2 * ((top_k + 31) / 32 * 32)});
-  r.threads = std::min(r.threads, kMaxThreads);
+  r.cluster = static_cast<int>(std::max(few, many));
+  r.part_bytes = 16 * ((row_vectors(V, dtype) + r.cluster - 1) / r.cluster);
+  r.threads = std::min(kMaxThreads, std::max(64, (r.part_bytes / 16 / 8 + 31) / 32 * 32));
   return r;
 }
 
-template <class Kern, class Args>
-cudaError_t launch_rows(Kern kern, const Args& a, const RowShape& r, size_t smem, const char* label, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+template <class... KArgs, class... Args>
+cudaError_t launch_rows(void (*kern)(KArgs...), int64_t N, const RowShape& r, size_t smem, const char* label,
+                        cudaStream_t s, Args... args) {
+  cudaError_t e = cudaSuccess;
+  if (smem > 40 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(a.N) * r.cluster), block(r.threads);
-  e = r.cluster == 1 ? launch(kern, grid, block, smem, s, a, r.cluster, r.slice_bytes)
-                     : launch_clustered(kern, grid, block, smem, r.cluster, s, a, r.cluster, r.slice_bytes);
+  const dim3 grid(static_cast<unsigned>(N * r.cluster)), block(r.threads);
+  e = r.cluster == 1 ? launch(kern, grid, block, smem, s, args...)
+                     : launch_clustered(kern, grid, block, smem, r.cluster, s, args...);
   trace_mark(s, label);
   return e;
 }
 
+// A slice of at most 72 KB keeps three CTAs on an SM, so that one's copies run under
+// the others' sweeps. Fewer rows than SMs: more CTAs a row, down to 8 KB each.
 template <int DT>
 cudaError_t distill(const DistillArgs& a, cudaStream_t s) {
-  const RowShape r = row_shape(a.N, a.V, DT, 0);
-  const size_t smem = r.slice_bytes + 16 * static_cast<size_t>(a.K);
-  return a.labels != nullptr && a.temperature != 1.f ? launch_rows(distill_kernel<DT, true>, a, r, smem, "distill", s)
-                                                     : launch_rows(distill_kernel<DT, false>, a, r, smem, "distill", s);
+  const RowShape r = row_shape(a.N, a.V, DT, 72 * 1024, device_sm_count(), 8 * 1024);
+  const size_t smem = r.part_bytes + 16 * static_cast<size_t>(a.K);
+  auto run = [&](auto kern) { return launch_rows(kern, a.N, r, smem, "distill", s, a, r.cluster, r.part_bytes); };
+  if (a.labels == nullptr || a.temperature == 1.f) return run(distill_kernel<DT, kNoSum>);
+  if (a.temperature == 2.f) return run(distill_kernel<DT, 2>);
+  if (a.temperature == 4.f) return run(distill_kernel<DT, 4>);
+  return run(distill_kernel<DT, kOwnSum>);
 }
 
+// A row needs no place on chip: one CTA takes it, more where there are few rows. Two
+// threads an alternative, so that a threshold which K threads reach is passed by few
+// elements.
 template <int DT>
 cudaError_t logprobs(const LogprobArgs& a, cudaStream_t s) {
-  const RowShape r = row_shape(a.N, a.V, DT, a.K);
-  const size_t smem = r.slice_bytes + (a.K > 0 ? sizeof(Key) * static_cast<size_t>(kCandidates + a.K) : 0);
-  return launch_rows(logprobs_kernel<DT>, a, r, smem, "token_logprobs", s);
+  RowShape r = row_shape(a.N, a.V, DT, 1 << 30, 4 * device_sm_count(), 8 * 1024);
+  r.threads = std::min(kMaxThreads, std::max(r.threads, 2 * ((a.K + 31) / 32 * 32)));
+  const size_t smem = a.K > 0 ? sizeof(Key) * static_cast<size_t>(kCandidates + a.K) : 0;
+  return launch_rows(logprobs_kernel<DT>, a.N, r, smem, "token_logprobs", s, a, r.cluster);
 }
 
 }  // namespace

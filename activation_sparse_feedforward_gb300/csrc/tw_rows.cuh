@@ -35,7 +35,13 @@ struct Elem<TW_F32> {
   static TW_DEV uint4 pack(const float (&v)[4]) {
     return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
   }
-  // the largest of the four (a NaN loses to a number)
+  // running maximum of vectors (a NaN loses to a number)
+  struct Max {
+    float m = -__builtin_huge_valf();
+    TW_DEV void add(const uint4& w) { m = fmaxf(m, max16(w)); }
+    TW_DEV float get() const { return m; }
+  };
+  // the largest of the four
   static TW_DEV float max16(const uint4& w) {
     return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
   }
@@ -69,11 +75,23 @@ struct Elem<TW_BF16> {
     return make_uint4(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]), pack_bf16x2_rn(v[4], v[5]),
                       pack_bf16x2_rn(v[6], v[7]));
   }
+  struct Max {
+    uint32_t m = 0xFF80FF80u;
+    TW_DEV void add(const uint4& w) {
+      const __nv_bfloat162 r = __hmax2(__hmax2(h2(w.x), h2(w.y)), __hmax2(h2(w.z), h2(w.w)));
+      const __nv_bfloat162 n = __hmax2(h2(m), r);
+      m = *reinterpret_cast<const uint32_t*>(&n);
+    }
+    TW_DEV float get() const {
+      const float2 f = __bfloat1622float2(h2(m));
+      return fmaxf(f.x, f.y);
+    }
+    static TW_DEV __nv_bfloat162 h2(uint32_t u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); }
+  };
   static TW_DEV float max16(const uint4& w) {
-    auto h = [](uint32_t u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); };
-    const __nv_bfloat162 m = __hmax2(__hmax2(h(w.x), h(w.y)), __hmax2(h(w.z), h(w.w)));
-    const float2 f = __bfloat1622float2(m);
-    return fmaxf(f.x, f.y);
+    Max m;
+    m.add(w);
+    return m.get();
   }
 };
 
@@ -113,11 +131,23 @@ struct Elem<TW_F16> {
     return make_uint4(pack_f16x2_rn(v[0], v[1]), pack_f16x2_rn(v[2], v[3]), pack_f16x2_rn(v[4], v[5]),
                       pack_f16x2_rn(v[6], v[7]));
   }
+  struct Max {
+    uint32_t m = 0xFC00FC00u;
+    TW_DEV void add(const uint4& w) {
+      const __half2 r = __hmax2(__hmax2(h2(w.x), h2(w.y)), __hmax2(h2(w.z), h2(w.w)));
+      const __half2 n = __hmax2(h2(m), r);
+      m = *reinterpret_cast<const uint32_t*>(&n);
+    }
+    TW_DEV float get() const {
+      const float2 f = __half22float2(h2(m));
+      return fmaxf(f.x, f.y);
+    }
+    static TW_DEV __half2 h2(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
+  };
   static TW_DEV float max16(const uint4& w) {
-    auto h = [](uint32_t u) { return *reinterpret_cast<const __half2*>(&u); };
-    const __half2 m = __hmax2(__hmax2(h(w.x), h(w.y)), __hmax2(h(w.z), h(w.w)));
-    const float2 f = __half22float2(m);
-    return fmaxf(f.x, f.y);
+    Max m;
+    m.add(w);
+    return m.get();
   }
 };
 

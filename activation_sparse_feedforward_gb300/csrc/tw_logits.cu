@@ -25,9 +25,11 @@ namespace tw {
 namespace {
 
 constexpr int kMaxThreads = 256;
-constexpr int kMaxWarps = kMaxThreads / 32;  // 8, the most CTAs of a cluster too: partial
-constexpr int kParts = 8;                    // statistics are joined over eight lanes
-static_assert(kMaxWarps <= kParts, "one lane per warp's partial statistics");
+constexpr int kMaxWarps = kMaxThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kParts = 8;  // per-warp or per-CTA statistics of the log probabilities, joined over eight lanes
+static_assert(kMaxWarps <= kParts && kMaxCluster <= kParts, "one lane per part");
+static_assert(kMaxWarps * kMaxCluster <= 64, "two lanes' worth of per-warp statistics in a cluster");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -224,16 +226,25 @@ TW_DEV Scale hard_scale(const Scale& a) {
 }
 
 
-// Joins one DistillStat per lane over groups of W lanes (M = -inf, sums 0 in unused
-// lanes); each lane of a group gets it.
-template <int HARD, int W>
+// Joins one DistillStat per lane (M = -inf, sums 0 in unused lanes); all lanes get it.
+template <int HARD>
 TW_DEV DistillStat join(DistillStat a, float c0) {
   DistillStat r;
-  r.M = warp_max<W>(a.M);
+  r.M = warp_max(a.M);
   const float base = base_of(r.M), f0 = exp_of(a.M, base, c0);
-  r.rest = group_sum<W>(a.rest * f0);
-  r.list = group_sum<W>(a.list * f0);
-  r.s1 = HARD != kNoSum ? group_sum<W>(a.s1 * exp_of(a.M, base, kLog2e)) : 0.f;
+  r.rest = warp_sum(a.rest * f0);
+  r.list = warp_sum(a.list * f0);
+  r.s1 = HARD != kNoSum ? warp_sum(a.s1 * exp_of(a.M, base, kLog2e)) : 0.f;
+  return r;
+}
+template <int HARD>
+TW_DEV DistillStat join_two(DistillStat a, DistillStat b, float c0) {
+  DistillStat r;
+  r.M = fmaxf(a.M, b.M);
+  const float base = base_of(r.M), fa = exp_of(a.M, base, c0), fb = exp_of(b.M, base, c0);
+  r.rest = a.rest * fa + b.rest * fb;
+  r.list = a.list * fa + b.list * fb;
+  r.s1 = HARD != kNoSum ? a.s1 * exp_of(a.M, base, kLog2e) + b.s1 * exp_of(b.M, base, kLog2e) : 0.f;
   return r;
 }
 
@@ -298,11 +309,39 @@ TW_DEV void own_sums(const Slice<DT>& sl, float c0, float& m, float& sum0, float
 }
 
 template <int DT>
-TW_DEV float list_value(const void* p, size_t i, int dtype) {
-  return dtype == TW_F32 ? static_cast<const float*>(p)[i] : Elem<DT>::get(static_cast<const typename Elem<DT>::S*>(p)[i]);
+TW_DEV float value_at(const void* p, size_t i) {
+  return Elem<DT>::get(static_cast<const typename Elem<DT>::S*>(p)[i]);
 }
-TW_DEV float teacher_logit(const void* p, size_t i, int dtype) {
-  return dtype == TW_F16 ? list_value<TW_F16>(p, i, dtype) : list_value<TW_BF16>(p, i, dtype);
+TW_DEV float teacher_logit(const DistillArgs& a, size_t e) {
+  return a.t_dtype == TW_F32 ? value_at<TW_F32>(a.t_val, e) : a.t_dtype == TW_BF16 ? value_at<TW_BF16>(a.t_val, e)
+                                                                                  : value_at<TW_F16>(a.t_val, e);
+}
+
+// The rare part of the marking, by the whole CTA: entries that found -inf at their token.
+// The lowest of those whose token no other entry took owns it (its logit is masked);
+// the others learn the logit from the owner.
+template <int DT>
+TW_DEV void owners(const Slice<DT>& sl, int K, int* l_idx, float* l_z, int label, int* label_entry) {
+  __syncthreads();
+  uint32_t owns = 0;  // a bit for each of the thread's entries: at most 1024 / 64
+  int n = 0;
+  for (int k = threadIdx.x; k < K; k += blockDim.x, ++n) {
+    const int i = -2 - l_idx[k];
+    bool own = i >= 0 && sl.element(i) != nullptr;
+    for (int q = 0; own && q < K; ++q) {
+      if (l_idx[q] == i) l_z[k] = l_z[q], own = false;
+      if (q < k && l_idx[q] == -2 - i) own = false;
+    }
+    owns |= own ? 1u << n : 0u;
+  }
+  __syncthreads();
+  n = 0;
+  for (int k = threadIdx.x; k < K; k += blockDim.x, ++n)
+    if (owns >> n & 1u) {
+      l_idx[k] = -2 - l_idx[k];
+      if (l_idx[k] == label) *label_entry = k;
+    }
+  __syncthreads();
 }
 
 // u 2^(c0 (z - M)) (+ w 2^(log2(e) (z - M))) of one vector
@@ -348,70 +387,74 @@ TW_DEV void store_slice(const Slice<DT>& sl, typename Elem<DT>::S* dz, F f) {
   if (sl.last_edge()) singly(sl.n - 1);
 }
 
-// One row per cluster.
+// One row per cluster. What the CTAs tell each other is pushed into the receiver's shared
+// memory before a cluster barrier: every warp's statistics to every CTA, every warp's
+// share of the loss to rank 0.
 template <int DT, int HARD>
 __global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillArgs a, int cluster, int slice_bytes) {
   using El = Elem<DT>;
   using S = typename El::S;
   extern __shared__ uint4 smem[];
-  __shared__ float red[2][kMaxWarps];
-  __shared__ DistillStat wstat[kMaxWarps], cstat;
+  __shared__ float4 stats[kMaxCluster * kMaxWarps];
+  __shared__ float shares[kMaxCluster * kMaxWarps];
+  __shared__ int label_entry;
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = nt >> 5;
   const int rank = blockIdx.x % cluster;
   const size_t row = blockIdx.x / cluster;
   const int K = a.K;
-  // the row's list: token, log2 P, P, z at the token, whether this thread's entry owns it
+  // the row's list, entry k filled by thread k % nt: the token (-2 - token where the entry
+  // does not own its place in this CTA's slice), log2 P, P, and z at the token (until the
+  // marking: the teacher's logit)
   int* l_idx = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(smem) + slice_bytes);
   float* l_lp = reinterpret_cast<float*>(l_idx + K);
   float* l_p = l_lp + K;
   float* l_z = l_p + K;
   pdl_enter();
+  if (cluster > 1) cluster_arrive();  // waited for before the first push: every CTA has started
 
+  // the small loads go first: behind the slice's they would wait for all of it
+  const float c0 = kLog2e / a.temperature;
+  int label = a.labels != nullptr ? a.labels[row] : -1;
+  const float t_rest = a.t_rest != nullptr ? a.t_rest[row] : neg_inf_f();
+  const float up = a.scale * (a.dloss != nullptr ? a.dloss[row] : 1.f);
+  const size_t list = row * K;
+  int i_first = -1;
+  float t_first = neg_inf_f();
+  if (tid < K) i_first = a.t_idx[list + tid], t_first = teacher_logit(a, list + tid);
   const S* z = static_cast<const S*>(a.z) + row * a.ldz;
   Slice<DT> sl(z, a.V, rank, cluster, smem);
-  const float c0 = kLog2e / a.temperature;
 
-  int label = a.labels != nullptr ? a.labels[row] : -1;
   if (label < -1 || label >= a.V) {
     if (tid == 0) raise_status(a.status, TW_EINVAL);
     label = -1;
   }
-  const float z_label = label >= 0 ? El::get(z[label]) : 0.f;
-
-  // the teacher's distribution over its list and the rest
-  float tm = neg_inf_f();
   for (int k = tid; k < K; k += nt) {
-    int i = a.t_idx[row * K + k];
-    if (i < -1 || i >= a.V) {
-      raise_status(a.status, TW_EINVAL);
+    int i = k == tid ? i_first : a.t_idx[list + k];
+    float t = k == tid ? t_first : teacher_logit(a, list + k);
+    if (i < 0 || i >= a.V) {
+      if (i != -1) raise_status(a.status, TW_EINVAL);
       i = -1;
+      t = neg_inf_f();
     }
-    float t = i >= 0 ? teacher_logit(a.t_val, row * K + k, a.t_dtype) : neg_inf_f();
-    if (t > neg_inf_f()) t = fmaxf(t / a.temperature, -FLT_MAX);  // a finite logit stays one
     l_idx[k] = i;
-    l_lp[k] = t;
-    l_z[k] = i >= 0 ? El::get(z[i]) : 0.f;
-    tm = fmaxf(tm, t);
+    l_z[k] = t > neg_inf_f() ? fmaxf(t / a.temperature, -FLT_MAX) : t;  // a finite logit stays one
   }
-  const float t_rest = a.t_rest != nullptr ? a.t_rest[row] : neg_inf_f();
+
+  // the teacher's distribution over its list and the rest, by every warp for itself
   float p_rest = 0.f, lp_rest = neg_inf_f();
   bool some = false;
   if (K > 0 || a.t_rest != nullptr) {
-    tm = warp_max(fmaxf(tm, t_rest));
-    if (lane == 0) red[0][warp] = tm;
     __syncthreads();
-    tm = base_of(warp_max(lane < warps ? red[0][lane] : neg_inf_f()));
-    float ts = 0.f;
-    for (int k = tid; k < K; k += nt) ts += exp_of(l_lp[k], tm, kLog2e);
-    ts = warp_sum(ts);
-    if (lane == 0) red[1][warp] = ts;
-    __syncthreads();
-    ts = warp_sum(lane < warps ? red[1][lane] : 0.f) + exp_of(t_rest, tm, kLog2e);
+    float tm = t_rest, ts = 0.f;
+    for (int k = lane; k < K; k += 32) tm = fmaxf(tm, l_z[k]);
+    tm = base_of(warp_max(tm));
+    for (int k = lane; k < K; k += 32) ts += exp_of(l_z[k], tm, kLog2e);
+    ts = warp_sum(ts) + exp_of(t_rest, tm, kLog2e);
     some = ts != 0.f;  // NaN counts as some
     if (some) {
       const float inv = 1.f / ts, l2 = log2f(ts);
       for (int k = tid; k < K; k += nt) {
-        const float t = (l_lp[k] - tm) * kLog2e;
+        const float t = (l_z[k] - tm) * kLog2e;
         l_p[k] = exp2_fast(t) * inv;
         l_lp[k] = t - l2;
       }
@@ -419,34 +462,33 @@ __global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillAr
       lp_rest = (t_rest - tm) * kLog2e - l2;
     }
   }
+  if (tid == 0) label_entry = -1;
 
-  // Listed tokens leave the row: the entry whose number survives in the token's slot
-  // owns it (a token listed twice has one owner), and the slot becomes -inf.
+  // Listed tokens leave the row: an entry takes the token's logit and puts -inf in its
+  // place. Whoever finds -inf there comes second (a token listed twice), or the logit was
+  // masked: owners() sorts that out.
   cp_wait<0>();
   __syncthreads();
   bool dup = false;
   if (some) {
     for (int k = tid; k < K; k += nt) {
-      S* s = l_idx[k] >= 0 ? sl.element(l_idx[k]) : nullptr;
-      if (s != nullptr) *s = static_cast<S>(k);
-    }
-    __syncthreads();
-    for (int k = tid; k < K; k += nt) {
-      const S* s = l_idx[k] >= 0 ? sl.element(l_idx[k]) : nullptr;
-      const bool owner = s != nullptr && *s == static_cast<S>(k);
+      const int i = l_idx[k];
+      S* s = i >= 0 ? sl.element(i) : nullptr;
+      const float v = s != nullptr ? El::get(El::exchange(s, El::neg_inf())) : 0.f;
+      l_z[k] = v;
+      const bool owner = s != nullptr && v != neg_inf_f();
       if (s != nullptr && !owner) dup = true;
-      if (!owner) l_idx[k] = -2 - l_idx[k];  // not this CTA's, or another entry's: -2 - token (padding: -1)
+      if (!owner) l_idx[k] = -2 - i;  // padding: -1
+      if (owner && i == label) label_entry = k;
     }
     dup = __syncthreads_or(dup);
-    for (int k = tid; k < K; k += nt)
-      if (l_idx[k] >= 0) *sl.element(l_idx[k]) = El::neg_inf();
-    __syncthreads();
+    if (dup) owners(sl, K, l_idx, l_z, label, &label_entry);
   }
 
   // the row's statistics
   DistillStat st;
   {
-    float m = neg_inf_f();
+    float m;
     own_sums<DT, HARD>(sl, c0, m, st.rest, st.s1);
     if (some) {  // the list's tokens that this thread owns join its maximum
       const float was = m;
@@ -466,59 +508,63 @@ __global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillAr
           st.list += exp_of(l_z[k], b, c0);
           if (HARD != kNoSum) st.s1 += exp_of(l_z[k], b, kLog2e);
         }
-    st = join<HARD, 32>(st, c0);
-    const DistillStat none = {neg_inf_f(), 0.f, 0.f, 0.f};
-    if (lane == 0) wstat[warp] = st;
-    __syncthreads();
-    st = join<HARD, kParts>(lane % kParts < warps ? wstat[lane % kParts] : none, c0);
+    st = join<HARD>(st, c0);
+    const float4 mine = make_float4(st.M, st.rest, st.list, st.s1);
     if (cluster > 1) {
-      if (tid == 0) cstat = st;
-      cluster_sync();
-      DistillStat p = none;
-      if (lane % kParts < cluster) {
-        const uint32_t at = peer_smem_addr(&cstat, lane % kParts);
-        p.M = ld_cluster_f32(at);
-        p.rest = ld_cluster_f32(at + 4);
-        p.list = ld_cluster_f32(at + 8);
-        p.s1 = ld_cluster_f32(at + 12);
-      }
-      st = join<HARD, kParts>(p, c0);
-      cluster_arrive();  // waited for at the end: no CTA leaves while its cstat is read
+      cluster_wait();
+      if (lane < cluster) st_cluster_v4(peer_smem_addr(&stats[rank * warps + warp], lane), mine);
+      cluster_barrier();
+    } else {
+      if (lane == 0) stats[warp] = mine;
+      __syncthreads();
     }
+    const DistillStat none = {neg_inf_f(), 0.f, 0.f, 0.f};
+    const int parts = cluster * warps;
+    auto part = [&](int i) {
+      if (i >= parts) return none;
+      const float4 s = stats[i];
+      return DistillStat{s.x, s.y, s.z, s.w};
+    };
+    st = part(lane);
+    if (parts > 32) st = join_two<HARD>(st, part(lane + 32), c0);
+    st = join<HARD>(st, c0);
   }
   const float total = st.rest + st.list;
   const float b = base_of(st.M);
   const float s1 = HARD != kNoSum ? st.s1 : total;
   const bool nothing = !some && label < 0;  // no target: loss and gradient are 0 whatever the logits
+  const bool holds_label = label >= 0 && sl.element(label) != nullptr;
+  const float z_label = !holds_label ? 0.f : label_entry >= 0 ? l_z[label_entry] : El::get(*sl.element(label));
 
-  if (rank == 0 && a.loss != nullptr) {
-    float kd = 0.f;
-    const float l2 = log2f(total);
+  // the loss, in units of log2: each entry's term by the thread that found it in its slice
+  if (a.loss != nullptr) {
+    float share = 0.f;
     if (some) {
+      const float l2 = log2f(total), f = a.kd_weight * a.temperature * a.temperature;
       for (int k = tid; k < K; k += nt) {
+        const int i = l_idx[k] >= 0 ? l_idx[k] : -2 - l_idx[k];
         const float p = l_p[k];
-        if (p != 0.f && l_idx[k] != -1) kd += p * (l_lp[k] - ((l_z[k] - b) * c0 - l2));
+        if (i >= 0 && sl.element(i) != nullptr && p != 0.f) share += p * (l_lp[k] - ((l_z[k] - b) * c0 - l2));
       }
+      if (rank == 0 && tid == 0 && p_rest != 0.f) share += p_rest * (lp_rest - (log2f(st.rest) - l2));
+      share *= f;
     }
-    kd = warp_sum(kd);
-    if (lane == 0) red[0][warp] = kd;
-    __syncthreads();
-    if (tid == 0) {
-      kd = 0.f;
-      for (int w = 0; w < warps; ++w) kd += red[0][w];
-      if (p_rest != 0.f) kd += p_rest * (lp_rest - (log2f(st.rest) - l2));
-      float loss = a.kd_weight * a.temperature * a.temperature * kLn2 * kd;
-      if (label >= 0) loss += a.ce_weight * kLn2 * (log2f(s1) - (z_label - b) * kLog2e);
-      a.loss[row] = nothing ? 0.f : total == 0.f ? __int_as_float(0x7F800000) : loss;
+    if (holds_label && tid == 0) share += a.ce_weight * (log2f(s1) - (z_label - b) * kLog2e);
+    share = warp_sum(share);
+    if (lane == 0) {
+      if (cluster > 1)
+        st_cluster_f32(peer_smem_addr(&shares[rank * warps + warp], 0), share);
+      else
+        shares[warp] = share;
     }
   }
+  if (cluster > 1) cluster_arrive();  // waited for at the end
 
   if (a.dz != nullptr) {
     S* dz = static_cast<S*>(a.dz) + row * a.lddz;
     const bool zero = nothing || total == 0.f;
-    const float g = a.scale * (a.dloss != nullptr ? a.dloss[row] : 1.f);
-    const float gk = g * a.kd_weight * a.temperature;
-    const float gc = label >= 0 ? g * a.ce_weight : 0.f;
+    const float gk = up * a.kd_weight * a.temperature;
+    const float gc = label >= 0 ? up * a.ce_weight : 0.f;
     float u = some ? gk / total : 0.f;  // factor of 2^(c0 (z - M)) on unlisted tokens
     if (p_rest != 0.f && st.rest != 0.f) u -= gk * p_rest / st.rest;
     const float w = label >= 0 ? gc / s1 : 0.f;
@@ -533,7 +579,6 @@ __global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillAr
     else
       store_slice<DT>(sl, dz, [&](const uint4& r) { return gradient<DT, HARD, false>(r, sa, sb, uf, wf); });
     __syncthreads();  // the listed tokens and the label overwrite what the sweep stored
-    bool label_listed = false;
     if (some && !zero) {
       for (int k = tid; k < K; k += nt) {
         const int i = l_idx[k];
@@ -546,20 +591,27 @@ __global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillAr
         }
         float d = gk * (exp_of(l_z[k], b, c0) / total - p);
         if (label >= 0) d += w * exp_of(l_z[k], b, kLog2e);
-        if (i == label) d -= gc, label_listed = true;
+        if (i == label) d -= gc;
         dz[i] = El::put(d);
       }
     }
-    if (a.labels != nullptr) {
-      label_listed = __syncthreads_or(label_listed);
-      if (tid == 0 && label >= 0 && !label_listed && !zero && sl.element(label) != nullptr) {
-        float d = u * exp_of(z_label, b, c0) - gc;
-        if (HARD != kNoSum) d = fmaf(w, exp_of(z_label, b, kLog2e), d);
-        dz[label] = El::put(d);
-      }
+    if (tid == 0 && holds_label && label_entry < 0 && !zero) {
+      float d = u * exp_of(z_label, b, c0) - gc;
+      if (HARD != kNoSum) d = fmaf(w, exp_of(z_label, b, kLog2e), d);
+      dz[label] = El::put(d);
     }
   }
-  if (cluster > 1) cluster_wait();
+
+  if (cluster > 1)
+    cluster_wait();
+  else if (a.dz == nullptr)
+    __syncthreads();
+  if (rank == 0 && warp == 0 && a.loss != nullptr) {
+    const int parts = cluster * warps;
+    float loss = (lane < parts ? shares[lane] : 0.f) + (lane + 32 < parts ? shares[lane + 32] : 0.f);
+    loss = kLn2 * warp_sum(loss);
+    if (lane == 0) a.loss[row] = nothing ? 0.f : total == 0.f ? __int_as_float(0x7F800000) : loss;
+  }
 }
 
 // ------------------------------------------------------------------ token log probabilities
@@ -799,7 +851,7 @@ __global__ void __launch_bounds__(kMaxThreads, 4) logprobs_kernel(const LogprobA
     part_top<DT>(part, high, K, cand, top, thr, &count, wkey);
   }
   if (cluster > 1) {
-    cluster_sync();
+    cluster_barrier();
     if (rank == 0) {
       if (warp == 0) {
         ProbStat p = none;
@@ -813,7 +865,7 @@ __global__ void __launch_bounds__(kMaxThreads, 4) logprobs_kernel(const LogprobA
       }
       for (int i = tid; i < cluster * K; i += nt) cand[i] = ld_cluster_u64(peer_smem_addr(top + i % K, i / K));
     }
-    cluster_sync();  // every list has been read: the CTAs may leave, rank 0 may overwrite its own
+    cluster_barrier();  // every list has been read: the CTAs may leave, rank 0 may overwrite its own
     if (rank != 0) return;
     if (K > 0) {
       for (int k = tid; k < K; k += nt) top[k] = 0;

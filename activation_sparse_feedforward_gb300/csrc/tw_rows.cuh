@@ -13,6 +13,13 @@ namespace tw {
 template <int DT>
 struct Elem;
 
+// *p = v, and what was there, for 16 bits of shared memory
+TW_DEV uint16_t exchange16(uint16_t* p, uint16_t v) {
+  uint16_t was = *p, seen;
+  while ((seen = atomicCAS(p, was, v)) != was) was = seen;
+  return was;
+}
+
 template <>
 struct Elem<TW_F32> {
   using S = float;
@@ -20,6 +27,7 @@ struct Elem<TW_F32> {
   static TW_DEV float get(S v) { return v; }
   static TW_DEV S put(float v) { return v; }
   static TW_DEV S neg_inf() { return __int_as_float(0xFF800000); }
+  static TW_DEV S exchange(S* p, S v) { return atomicExch(p, v); }  // shared memory
   static TW_DEV void pairs(const uint4& w, f32x2 (&v)[2]) {
     v[0] = pair(__uint_as_float(w.x), __uint_as_float(w.y));
     v[1] = pair(__uint_as_float(w.z), __uint_as_float(w.w));
@@ -54,6 +62,7 @@ struct Elem<TW_BF16> {
   static TW_DEV float get(S v) { return bf16_to_f32(v); }
   static TW_DEV S put(float v) { return f32_to_bf16(v); }
   static TW_DEV S neg_inf() { return 0xFF80; }
+  static TW_DEV S exchange(S* p, S v) { return exchange16(p, v); }
   static TW_DEV void pairs(const uint4& w, f32x2 (&v)[4]) {
     v[0] = widen(w.x), v[1] = widen(w.y), v[2] = widen(w.z), v[3] = widen(w.w);
   }
@@ -102,6 +111,7 @@ struct Elem<TW_F16> {
   static TW_DEV float get(S v) { return f16_to_f32(v); }
   static TW_DEV S put(float v) { return f32_to_f16(v); }
   static TW_DEV S neg_inf() { return 0xFC00; }
+  static TW_DEV S exchange(S* p, S v) { return exchange16(p, v); }
   static TW_DEV void pairs(const uint4& w, f32x2 (&v)[4]) {
     const uint32_t r[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -186,6 +196,14 @@ TW_DEV float warp_sum(float v) {
 TW_DEV void team_barrier(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 
 // ------------------------------------------------------------------ clusters
+TW_DEV void st_cluster_f32(uint32_t cluster_addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
+}
+TW_DEV void st_cluster_v4(uint32_t cluster_addr, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "f"(v.x), "f"(v.y), "f"(v.z),
+               "f"(v.w)
+               : "memory");
+}
 TW_DEV float ld_cluster_f32(uint32_t cluster_addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
@@ -198,9 +216,19 @@ TW_DEV unsigned long long ld_cluster_u64(uint32_t cluster_addr) {
 }
 
 // A cluster barrier in two halves: what a thread did before arriving is done for every
-// thread that has waited.
-TW_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-TW_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// thread that has waited. (The warp converges first: the halves are warp-wide.)
+TW_DEV void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+TW_DEV void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+TW_DEV void cluster_barrier() {
+  cluster_arrive();
+  cluster_wait();
+}
 
 // 2^x (hardware approximation, about 2 ulp; subnormal results flush to zero)
 TW_DEV float exp2_fast(float x) {

@@ -391,7 +391,7 @@ TW_DEV void store_slice(const Slice<DT>& sl, typename Elem<DT>::S* dz, F f) {
 // memory before a cluster barrier: every warp's statistics to every CTA, every warp's
 // share of the loss to rank 0.
 template <int DT, int HARD>
-__global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillArgs a, int cluster, int slice_bytes) {
+__global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillArgs a, int cluster, int slice_bytes, int ahead) {
   using El = Elem<DT>;
   using S = typename El::S;
   extern __shared__ uint4 smem[];
@@ -423,6 +423,10 @@ __global__ void __launch_bounds__(kMaxThreads, 3) distill_kernel(const DistillAr
   if (tid < K) i_first = a.t_idx[list + tid], t_first = teacher_logit(a, list + tid);
   const S* z = static_cast<const S*>(a.z) + row * a.ldz;
   Slice<DT> sl(z, a.V, rank, cluster, smem);
+  if (tid == 0 && row + ahead < static_cast<size_t>(a.N)) {
+    const Part<DT> next(z + ahead * a.ldz, a.V, rank, cluster);
+    if (next.hi > next.lo) prefetch_l2(next.at(next.lo), 16u * (next.hi - next.lo));
+  }
 
   if (label < -1 || label >= a.V) {
     if (tid == 0) raise_status(a.status, TW_EINVAL);
@@ -685,29 +689,38 @@ TW_DEV void each_vector(const Part<DT>& p, F f) {
 
 // The K largest keys of the CTA's part, descending, into top (0 past the finite ones).
 // A threshold that the largest elements of at least K threads reach leaves few
-// candidates, all with threads that reach it: those read their vectors once more (from
-// L2). A list that overflows (many ties, or the largest elements all with few threads)
-// falls back to K sweeps for the next largest key. high: the upper half of the order of
-// the thread's largest element, 0 when it has none; thr, count, top: set by the caller
-// behind a barrier.
+// candidates, all in those threads' vectors. The whole CTA reads these once more (from
+// L2), a vector a thread: left to their owners, one lane of a warp would walk a row's
+// worth of latencies. A list that overflows (many ties, or the largest elements all with
+// few threads) falls back to K sweeps for the next largest key. high: the upper half of
+// the order of the thread's largest element, 0 when it has none; thr, count (two zeros)
+// and top: set by the caller behind a barrier; above: room for a thread number each.
 template <int DT>
-TW_DEV void part_top(const Part<DT>& p, uint32_t high, int K, Key* cand, Key* top, uint32_t thr, int* count, Key* wkey) {
+TW_DEV void part_top(const Part<DT>& p, uint32_t high, int K, Key* cand, Key* top, uint32_t thr, int* count,
+                     uint16_t* above, Key* wkey) {
   using El = Elem<DT>;
   constexpr int E = El::E;
   const int tid = threadIdx.x, nt = blockDim.x;
-  if (high != 0 && high >= thr) {
-    each_vector(p, [&](const uint4& w, int j) {
-      const float m = El::max16(w);
-      if (!(m > neg_inf_f()) || (order_of(m) >> 16) < thr) return;
-      float v[E];
-      El::unpack(w, v);
+  auto collect = [&](const uint4& w, int j) {
+    const float m = El::max16(w);
+    if (!(m > neg_inf_f()) || (order_of(m) >> 16) < thr) return;
+    float v[E];
+    El::unpack(w, v);
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (v[e] > neg_inf_f() && (order_of(v[e]) >> 16) >= thr) {
-          const int at = atomicAdd(count, 1);
-          if (at < kCandidates) cand[at] = key_of(v[e], p.col(j) + e);
-        }
-    });
+    for (int e = 0; e < E; ++e)
+      if (v[e] > neg_inf_f() && (order_of(v[e]) >> 16) >= thr) {
+        const int at = atomicAdd(count, 1);
+        if (at < kCandidates) cand[at] = key_of(v[e], p.col(j) + e);
+      }
+  };
+  if (high != 0 && high >= thr) above[atomicAdd(count + 1, 1)] = static_cast<uint16_t>(tid);
+  if (tid == 0 && p.lo > 0) collect(p.edge(0), 0);
+  if (tid == nt - 1 && p.hi < p.n && p.n > p.lo) collect(p.edge(p.n - 1), p.n - 1);
+  __syncthreads();
+  const int rounds = (p.hi - p.lo + nt - 1) / nt, work = count[1] * rounds;
+  for (int i = tid; i < work; i += nt) {
+    const int j = p.lo + above[i / rounds] + (i % rounds) * nt;
+    if (j < p.hi) collect(*reinterpret_cast<const uint4*>(p.at(j)), j);
   }
   __syncthreads();
   const int n = *count;
@@ -784,12 +797,21 @@ TW_DEV ProbStat own_probs(const Part<DT>& p, float c) {
     }
   };
   const uint4* src = reinterpret_cast<const uint4*>(p.at(0));
-  in_batches(p.lo, p.hi, [&](int j, auto all) {
-    uint4 r[kBatch];
+  // the next batch is on its way while this one is summed
+  auto load = [&](uint4 (&r)[kBatch], int j) {
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) r[i] = all.value || j + i * nt < p.hi ? src[j + i * nt] : no_vector<DT>();
-    batch(r);
-  });
+    for (int i = 0; i < kBatch; ++i) r[i] = j + i * nt < p.hi ? src[j + i * nt] : no_vector<DT>();
+  };
+  uint4 now[kBatch], next[kBatch];
+  int j = p.lo + tid;
+  load(now, j);
+  while (j < p.hi) {
+    j += kBatch * nt;
+    load(next, j);
+    batch(now);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) now[i] = next[i];
+  }
   if (p.lo > 0 || p.hi < p.n) {  // the edges: one vector of the first thread, one of the last
     uint4 r[kBatch];
 #pragma unroll
@@ -814,9 +836,9 @@ __global__ void __launch_bounds__(kMaxThreads, 4) logprobs_kernel(const LogprobA
   extern __shared__ Key lists[];
   __shared__ ProbStat wstat[kMaxWarps], cstat;
   __shared__ Key wkey[kMaxWarps];
-  __shared__ uint16_t high_of[kMaxThreads];
+  __shared__ uint16_t high_of[kMaxThreads], above[kMaxThreads];
   __shared__ uint32_t thr;
-  __shared__ int count;
+  __shared__ int count[2];
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = nt >> 5;
   const int rank = blockIdx.x % cluster;
   const size_t row = blockIdx.x / cluster;
@@ -842,13 +864,13 @@ __global__ void __launch_bounds__(kMaxThreads, 4) logprobs_kernel(const LogprobA
     if (lane == 0) cstat = st;
     if (K > 0) {
       const uint32_t t = find_threshold(high_of, nt, K);
-      if (lane == 0) thr = t, count = 0;
+      if (lane == 0) thr = t, count[0] = count[1] = 0;
       for (int k = lane; k < K; k += 32) top[k] = 0;
     }
   }
   if (K > 0) {
     __syncthreads();
-    part_top<DT>(part, high, K, cand, top, thr, &count, wkey);
+    part_top<DT>(part, high, K, cand, top, thr, count, above, wkey);
   }
   if (cluster > 1) {
     cluster_barrier();
@@ -945,7 +967,8 @@ template <int DT>
 cudaError_t distill(const DistillArgs& a, cudaStream_t s) {
   const RowShape r = row_shape(a.N, a.V, DT, 72 * 1024, device_sm_count(), 8 * 1024);
   const size_t smem = r.part_bytes + 16 * static_cast<size_t>(a.K);
-  auto run = [&](auto kern) { return launch_rows(kern, a.N, r, smem, "distill", s, a, r.cluster, r.part_bytes); };
+  const int ahead = 3 * device_sm_count() / r.cluster;
+  auto run = [&](auto kern) { return launch_rows(kern, a.N, r, smem, "distill", s, a, r.cluster, r.part_bytes, ahead); };
   if (a.labels == nullptr || a.temperature == 1.f) return run(distill_kernel<DT, kNoSum>);
   if (a.temperature == 2.f) return run(distill_kernel<DT, 2>);
   if (a.temperature == 4.f) return run(distill_kernel<DT, 4>);

@@ -186,6 +186,11 @@ TW_DEV void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Asks for [src, src + bytes) (both multiples of 16) in L2, without waiting or a place.
+TW_DEV void prefetch_l2(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
 // ------------------------------------------------------------------ reductions
 TW_DEV float warp_sum(float v) {
 #pragma unroll

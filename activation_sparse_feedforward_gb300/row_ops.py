@@ -12,7 +12,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from .ops import _ptr, _stream, _workspace
+from .ops import _workspace
 
 DTYPES = {torch.float32: _lib.TW_F32, torch.bfloat16: _lib.TW_BF16, torch.float16: _lib.TW_F16}
 
@@ -24,29 +24,38 @@ def _dtype_code(dtype: torch.dtype) -> int:
     return code
 
 
-def _check_matrix(name: str, t: torch.Tensor, dtype: torch.dtype, rows: int, cols: int) -> None:
-    if t.dtype != dtype or not t.is_cuda:
+def _matrix(name: str, t: torch.Tensor, dtype: torch.dtype, rows: int, cols: int) -> int:
+    """Checks a [rows, cols] matrix; its row stride in elements (a single row's is its
+    length, whatever torch says)."""
+    if t.dtype is not dtype or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA {dtype} tensor")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
-    if t.stride(1) != 1 and cols > 1:
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{name} must have unit stride along its rows")
+    return ld if rows > 1 else cols
 
 
-def _check_vector(name: str, t: torch.Tensor, dtype: torch.dtype, n: int) -> None:
-    if t.dtype != dtype or not t.is_cuda or t.numel() != n or not t.is_contiguous():
+def _vector(name: str, t: torch.Tensor | None, dtype: torch.dtype, n: int) -> int | None:
+    """Checks a contiguous side array of n elements, or None; its address."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or not t.is_cuda or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of {n} elements")
+    return t.data_ptr()
 
 
-def _check_rows(name: str, t: torch.Tensor, most: int) -> int:
+def _rows(name: str, t: torch.Tensor, most: int) -> int:
     if t.dim() != 2 or t.shape[0] > most:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected at most {most} rows")
     return t.shape[0]
 
 
-def _ld(t: torch.Tensor | None) -> int:
-    """Row stride in elements; a single row's is its length whatever torch says."""
-    return 0 if t is None else t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _stream_of(t: torch.Tensor) -> int:
+    """The raw current stream of the tensor's device: torch.cuda.current_stream() builds a
+    Stream object for it, 2.9 us of a small call's host time against 0.1."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 class LayerNorm:
@@ -64,48 +73,40 @@ class LayerNorm:
         self._dt, self._wdt = _dtype_code(dtype), _dtype_code(self.weight_dtype)
         if self._wdt not in (self._dt, _lib.TW_F32):
             raise ValueError(f"weight_dtype must be {dtype} or float32, got {self.weight_dtype}")
-        L = _lib.load()
+        self._lib = _lib.load()
         self.y = torch.empty((T, d), dtype=dtype, device=device)
         self.sum = torch.empty((T, d), dtype=dtype, device=device)
         self._mean = torch.empty(T, dtype=torch.float32, device=device)
         self._rstd = torch.empty(T, dtype=torch.float32, device=device)
-        self._rows = T
+        #: fp32 row means, and 1 / sqrt(variance + eps), of the last forward's rows
+        self.mean, self.rstd = self._mean, self._rstd
         self.dx = self.dweight = self.dbias = None
         if backward:
             self.dx = torch.empty((T, d), dtype=dtype, device=device)
             self.dweight = torch.empty(d, dtype=torch.float32, device=device)
             self.dbias = torch.empty(d, dtype=torch.float32, device=device)
-            self.ws_bytes = int(L.tw_layer_norm_bwd_workspace_size(T, d))
+            self.ws_bytes = int(self._lib.tw_layer_norm_bwd_workspace_size(T, d))
             self.ws = _workspace(self.ws_bytes, device)
-
-    @property
-    def mean(self) -> torch.Tensor:
-        """fp32 row means of the last forward."""
-        return self._mean[:self._rows]
-
-    @property
-    def rstd(self) -> torch.Tensor:
-        """fp32 1 / sqrt(variance + eps) of the last forward's rows."""
-        return self._rstd[:self._rows]
 
     def forward(self, x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
                 residual: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
         """(y, s): s = x + residual (x itself without one), y = norm(s) weight + bias."""
-        n, d = _check_rows("x", x, self.T), self.d
-        _check_matrix("x", x, self.dtype, n, d)
-        if residual is not None:
-            _check_matrix("residual", residual, self.dtype, n, d)
-        if weight is not None:
-            _check_vector("weight", weight, self.weight_dtype, d)
-        if bias is not None:
-            _check_vector("bias", bias, self.weight_dtype, d)
-        self._rows = n
-        y, s = (self.y, self.sum) if n == self.T else (self.y[:n], self.sum[:n])
-        code = _lib.load().tw_layer_norm_fwd(
-            _ptr(x), _ld(x), _ptr(residual), _ld(residual), _ptr(weight), _ptr(bias), n, d, self.eps,
-            self._dt, self._wdt, None if residual is None else _ptr(s), d, _ptr(y), d,
-            _ptr(self._mean), _ptr(self._rstd), _stream())
-        _lib.check(code, "tw_layer_norm_fwd")
+        n, d, dt = _rows("x", x, self.T), self.d, self.dtype
+        ldx = _matrix("x", x, dt, n, d)
+        w, b = _vector("weight", weight, self.weight_dtype, d), _vector("bias", bias, self.weight_dtype, d)
+        y, s = self.y, self.sum
+        if n != self.T:
+            y, s = y[:n], s[:n]
+        if n != self.mean.shape[0]:
+            self.mean, self.rstd = self._mean[:n], self._rstd[:n]
+        if residual is None:
+            r, ldr, to = None, 0, None
+        else:
+            r, ldr, to = residual.data_ptr(), _matrix("residual", residual, dt, n, d), s.data_ptr()
+        code = self._lib.tw_layer_norm_fwd(x.data_ptr(), ldx, r, ldr, w, b, n, d, self.eps, self._dt, self._wdt, to, d,
+                                           y.data_ptr(), d, self.mean.data_ptr(), self.rstd.data_ptr(), _stream_of(x))
+        if code:
+            _lib.check(code, "tw_layer_norm_fwd")
         return y, (x if residual is None else s)
 
     def backward(self, dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor | None = None,
@@ -113,24 +114,22 @@ class LayerNorm:
                  rstd: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
         """(dx, dweight, dbias) for x the tensor that was normalised (the forward's s);
         dres is added to dx. mean, rstd: the statistics, of the last forward by default."""
-        if self.dx is None:
+        dx = self.dx
+        if dx is None:
             raise ValueError("this LayerNorm was made with backward=False")
-        n, d = _check_rows("x", x, self.T), self.d
-        _check_matrix("x", x, self.dtype, n, d)
-        _check_matrix("dy", dy, self.dtype, n, d)
-        if dres is not None:
-            _check_matrix("dres", dres, self.dtype, n, d)
-        if weight is not None:
-            _check_vector("weight", weight, self.weight_dtype, d)
-        mean, rstd = self.mean if mean is None else mean, self.rstd if rstd is None else rstd
-        _check_vector("mean", mean, torch.float32, n)
-        _check_vector("rstd", rstd, torch.float32, n)
-        dx = self.dx if n == self.T else self.dx[:n]
-        code = _lib.load().tw_layer_norm_bwd(
-            _ptr(dy), _ld(dy), _ptr(x), _ld(x), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(dres), _ld(dres), n, d,
-            self._dt, self._wdt, _ptr(dx), d, _ptr(self.dweight),
-            _ptr(self.dbias), _ptr(self.ws), self.ws.numel(), _stream())
-        _lib.check(code, "tw_layer_norm_bwd")
+        n, d, dt = _rows("x", x, self.T), self.d, self.dtype
+        ldx, lddy = _matrix("x", x, dt, n, d), _matrix("dy", dy, dt, n, d)
+        w = _vector("weight", weight, self.weight_dtype, d)
+        m = _vector("mean", self.mean if mean is None else mean, torch.float32, n)
+        r = _vector("rstd", self.rstd if rstd is None else rstd, torch.float32, n)
+        g, ldg = (None, 0) if dres is None else (dres.data_ptr(), _matrix("dres", dres, dt, n, d))
+        if n != self.T:
+            dx = dx[:n]
+        code = self._lib.tw_layer_norm_bwd(dy.data_ptr(), lddy, x.data_ptr(), ldx, m, r, w, g, ldg, n, d, self._dt,
+                                           self._wdt, dx.data_ptr(), d, self.dweight.data_ptr(), self.dbias.data_ptr(),
+                                           self.ws.data_ptr(), self.ws_bytes, _stream_of(x))
+        if code:
+            _lib.check(code, "tw_layer_norm_bwd")
         return dx, self.dweight, self.dbias
 
 
@@ -164,62 +163,55 @@ class DistillLoss:
         self.N, self.V, self.K, self.dtype = N, V, K, dtype
         self.temperature, self.kd_weight, self.ce_weight = float(temperature), float(kd_weight), float(ce_weight)
         self._dt = _dtype_code(dtype)
-        _lib.load()
+        self._lib = _lib.load()
         self.loss = torch.empty(N, dtype=torch.float32, device=device)
         self.dz = torch.empty((N, V), dtype=dtype, device=device) if grad else None
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
 
-    def _run(self, z, idx, val, rest, labels, dloss, scale, want_loss, dz) -> None:
-        n, K = z.shape[0], self.K
+    def _run(self, z, idx, val, rest, labels, dloss, scale, want_loss, want_grad, out):
+        n, K, V = _rows("z", z, self.N), self.K, self.V
+        ld = _matrix("z", z, self.dtype, n, V)
+        dz, to, ldd = None, None, 0
+        if want_grad:
+            dz = self.dz if out is None else out
+            if dz is None:
+                raise ValueError("this DistillLoss was made with grad=False: give `out`")
+            if out is not None:
+                ldd = _matrix("out", out, self.dtype, n, V)
+            else:
+                ldd = V
+                if n != self.N:
+                    dz = dz[:n]
+            to = dz.data_ptr()
+        i = v = None
         tdt = self._dt
         if K > 0:
             if idx is None or val is None:
                 raise ValueError("idx and val must be given for K > 0")
-            _check_vector("idx", idx, torch.int32, n * K)
             tdt = _dtype_code(val.dtype)
-            _check_vector("val", val, val.dtype, n * K)
-        for name, t, dt in (("rest", rest, torch.float32), ("labels", labels, torch.int32), ("dloss", dloss, torch.float32)):
-            if t is not None:
-                _check_vector(name, t, dt, n)
-        code = _lib.load().tw_distill(
-            _ptr(z), _ld(z), n, self.V, self._dt, _ptr(idx), _ptr(val), tdt, K, _ptr(rest), _ptr(labels),
-            self.temperature, self.kd_weight, self.ce_weight, _ptr(dloss), float(scale),
-            _ptr(self.loss) if want_loss else None, _ptr(dz), _ld(dz), _ptr(self.status),
-            _stream())
-        _lib.check(code, "tw_distill")
-
-    def _grad_buffer(self, n: int, out: torch.Tensor | None) -> torch.Tensor:
-        if out is None:
-            if self.dz is None:
-                raise ValueError("this DistillLoss was made with grad=False: give `out`")
-            return self.dz if n == self.N else self.dz[:n]
-        _check_matrix("out", out, self.dtype, n, self.V)
-        return out
+            i, v = _vector("idx", idx, torch.int32, n * K), _vector("val", val, val.dtype, n * K)
+        code = self._lib.tw_distill(
+            z.data_ptr(), ld, n, V, self._dt, i, v, tdt, K, _vector("rest", rest, torch.float32, n),
+            _vector("labels", labels, torch.int32, n), self.temperature, self.kd_weight, self.ce_weight,
+            _vector("dloss", dloss, torch.float32, n), scale, self.loss.data_ptr() if want_loss else None, to, ldd,
+            self.status.data_ptr(), _stream_of(z))
+        if code:
+            _lib.check(code, "tw_distill")
+        return (self.loss if n == self.N else self.loss[:n]), dz
 
     def forward(self, z, idx=None, val=None, rest=None, labels=None) -> torch.Tensor:
         """fp32 losses [n]."""
-        n = _check_rows("z", z, self.N)
-        _check_matrix("z", z, self.dtype, n, self.V)
-        self._run(z, idx, val, rest, labels, None, 1.0, True, None)
-        return self.loss[:n]
+        return self._run(z, idx, val, rest, labels, None, 1.0, True, False, None)[0]
 
     def backward(self, z, idx=None, val=None, rest=None, labels=None, dloss=None, scale: float = 1.0,
                  out: torch.Tensor | None = None) -> torch.Tensor:
         """dz [n, V] = scale * dloss * d loss / d z (dloss [n] float32, None for 1)."""
-        n = _check_rows("z", z, self.N)
-        _check_matrix("z", z, self.dtype, n, self.V)
-        dz = self._grad_buffer(n, out)
-        self._run(z, idx, val, rest, labels, dloss, scale, False, dz)
-        return dz
+        return self._run(z, idx, val, rest, labels, dloss, scale, False, True, out)[1]
 
     def forward_backward(self, z, idx=None, val=None, rest=None, labels=None, dloss=None, scale: float = 1.0,
                          out: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
         """(losses, dz) in one pass over z."""
-        n = _check_rows("z", z, self.N)
-        _check_matrix("z", z, self.dtype, n, self.V)
-        dz = self._grad_buffer(n, out)
-        self._run(z, idx, val, rest, labels, dloss, scale, True, dz)
-        return self.loss[:n], dz
+        return self._run(z, idx, val, rest, labels, dloss, scale, True, True, out)
 
 
 def distill_loss(z, idx=None, val=None, rest=None, labels=None, temperature: float = 1.0, kd_weight: float = 1.0,
@@ -241,7 +233,7 @@ class TokenLogprobs:
         self.N, self.V, self.n_tokens, self.top_k, self.dtype = N, V, n_tokens, top_k, dtype
         self.temperature = float(temperature)
         self._dt = _dtype_code(dtype)
-        _lib.load()
+        self._lib = _lib.load()
         self.logprob = torch.empty((N, n_tokens), dtype=torch.float32, device=device)
         self.entropy = torch.empty(N, dtype=torch.float32, device=device)
         self.top_idx = torch.empty((N, top_k), dtype=torch.int32, device=device)
@@ -250,17 +242,19 @@ class TokenLogprobs:
 
     def __call__(self, z: torch.Tensor, tokens: torch.Tensor | None = None):
         """(logprob [n, n_tokens], entropy [n], top_idx [n, top_k], top_logprob [n, top_k])."""
-        n = _check_rows("z", z, self.N)
-        _check_matrix("z", z, self.dtype, n, self.V)
-        if self.n_tokens > 0:
+        n, s = _rows("z", z, self.N), self.n_tokens
+        ld = _matrix("z", z, self.dtype, n, self.V)
+        t = None
+        if s > 0:
             if tokens is None:
                 raise ValueError("tokens must be given for n_tokens > 0")
-            _check_vector("tokens", tokens, torch.int32, n * self.n_tokens)
-        code = _lib.load().tw_token_logprobs(
-            _ptr(z), _ld(z), n, self.V, self._dt, _ptr(tokens) if self.n_tokens > 0 else None, self.n_tokens,
-            self.temperature, self.top_k, _ptr(self.logprob), _ptr(self.entropy), _ptr(self.top_idx),
-            _ptr(self.top_logprob), _ptr(self.status), _stream())
-        _lib.check(code, "tw_token_logprobs")
+            t = _vector("tokens", tokens, torch.int32, n * s)
+        code = self._lib.tw_token_logprobs(
+            z.data_ptr(), ld, n, self.V, self._dt, t, s, self.temperature, self.top_k, self.logprob.data_ptr(),
+            self.entropy.data_ptr(), self.top_idx.data_ptr(), self.top_logprob.data_ptr(), self.status.data_ptr(),
+            _stream_of(z))
+        if code:
+            _lib.check(code, "tw_token_logprobs")
         if n == self.N:
             return self.logprob, self.entropy, self.top_idx, self.top_logprob
         return self.logprob[:n], self.entropy[:n], self.top_idx[:n], self.top_logprob[:n]

@@ -645,33 +645,34 @@ TW_DEV Key key_of(float v, int token) { return (static_cast<Key>(order_of(v)) <<
 constexpr int kCandidates = 1024;
 
 // top[0..K) = the K largest of cand[0..n), descending, 0 past n. Distinct keys have
-// distinct ranks: each thread counts the keys above its own. top is zeroed before.
-TW_DEV void rank_select(const Key* cand, int n, Key* top, int K) {
+// distinct ranks: each thread counts the keys above its own. top is zeroed before; cand
+// has room for one more.
+TW_DEV void rank_select(Key* cand, int n, Key* top, int K) {
+  const ulonglong2* two = reinterpret_cast<const ulonglong2*>(cand);
   for (int i = threadIdx.x; i < n; i += blockDim.x) {
     const Key k = cand[i];
     int r = 0;
-    for (int j = 0; j < n; ++j) r += cand[j] > k ? 1 : 0;
+#pragma unroll 4
+    for (int j = 0; j < n / 2; ++j) {
+      const ulonglong2 c = two[j];
+      r += (c.x > k ? 1 : 0) + (c.y > k ? 1 : 0);
+    }
+    if (n & 1) r += cand[n - 1] > k ? 1 : 0;
     if (k != 0 && r < K) top[r] = k;
   }
 }
 
-// A threshold on the upper half of order_of that at least K (or all) of the CTA's n
-// values reach, and not many more: a search bit by bit, by one warp.
-TW_DEV uint32_t find_threshold(const uint16_t* high, int n, int K) {
-  const int lane = threadIdx.x & 31;
-  uint32_t h[kMaxThreads / 32];
-#pragma unroll
-  for (int i = 0; i < kMaxThreads / 32; ++i) h[i] = i * 32 + lane < n ? high[i * 32 + lane] : 0;
+// A threshold that at least K of the CTA's values (below 2^16; one a thread) reach, and
+// not many more: bit by bit from the highest, a barrier that counts each. 0 where fewer
+// than K are not 0.
+TW_DEV uint32_t find_threshold(uint32_t v, int K) {
   uint32_t thr = 0;
   for (int b = 15; b >= 0; --b) {
-    const uint32_t t = thr | (1u << b);
-    int c = 0;
-#pragma unroll
-    for (int i = 0; i < kMaxThreads / 32; ++i) c += h[i] >= t ? 1 : 0;
-    c = __reduce_add_sync(0xFFFFFFFFu, c);
+    const uint32_t t = thr | 1u << b;
+    const int c = __syncthreads_count(v >= t);
     if (c >= K) {
       thr = t;
-      if (c <= K + K / 2) break;
+      if (c <= K + K / 2 + 2) break;
     }
   }
   return thr;
@@ -693,8 +694,8 @@ TW_DEV void each_vector(const Part<DT>& p, F f) {
 // L2), a vector a thread: left to their owners, one lane of a warp would walk a row's
 // worth of latencies. A list that overflows (many ties, or the largest elements all with
 // few threads) falls back to K sweeps for the next largest key. high: the upper half of
-// the order of the thread's largest element, 0 when it has none; thr, count (two zeros)
-// and top: set by the caller behind a barrier; above: room for a thread number each.
+// the order of the thread's largest element, 0 when it has none; count (two zeros) and top
+// (zeros): set by the caller behind a barrier; above: room for a thread number each.
 template <int DT>
 TW_DEV void part_top(const Part<DT>& p, uint32_t high, int K, Key* cand, Key* top, uint32_t thr, int* count,
                      uint16_t* above, Key* wkey) {
@@ -833,11 +834,10 @@ template <int DT>
 __global__ void __launch_bounds__(kMaxThreads, 4) logprobs_kernel(const LogprobArgs a, int cluster) {
   using El = Elem<DT>;
   using S = typename El::S;
-  extern __shared__ Key lists[];
+  extern __shared__ __align__(16) Key lists[];
   __shared__ ProbStat wstat[kMaxWarps], cstat;
   __shared__ Key wkey[kMaxWarps];
-  __shared__ uint16_t high_of[kMaxThreads], above[kMaxThreads];
-  __shared__ uint32_t thr;
+  __shared__ uint16_t above[kMaxThreads];
   __shared__ int count[2];
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = nt >> 5;
   const int rank = blockIdx.x % cluster;
@@ -845,31 +845,35 @@ __global__ void __launch_bounds__(kMaxThreads, 4) logprobs_kernel(const LogprobA
   const int K = a.K;
   Key* cand = lists;
   Key* top = cand + (K > 0 ? kCandidates : 0);
+  if (tid < 2) count[tid] = 0;
+  for (int k = tid; k < K; k += nt) top[k] = 0;
   pdl_enter();
 
   const S* z = static_cast<const S*>(a.z) + row * a.ldz;
   const Part<DT> part(z, a.V, rank, cluster);
   const float c = kLog2e / a.temperature;
+  // the first given tokens' logits come while the row does
+  int t_first = -1;
+  float z_first = 0.f;
+  const bool answers = rank == 0 && warp == 0;
+  if (answers && lane < a.n_tokens) {
+    t_first = a.tokens[row * a.n_tokens + lane];
+    if (t_first >= 0 && t_first < a.V) z_first = El::get(z[t_first]);
+  }
   ProbStat st = own_probs(part, c);
   const float mine = st.M;
   st = join<32>(st, c);
   if (lane == 0) wstat[warp] = st;
   const uint32_t high = mine > neg_inf_f() ? order_of(mine) >> 16 : 0;
-  if (K > 0) high_of[tid] = static_cast<uint16_t>(high);
+  const uint32_t thr = K > 0 ? find_threshold(high, K) : 0;
   __syncthreads();
-  // warp 0: the slice's statistics, and the threshold of its alternatives
+  // warp 0: the part's statistics
   const ProbStat none = {neg_inf_f(), 0.f, 0.f};
   if (warp == 0) {
     st = join<kParts>(lane % kParts < warps ? wstat[lane % kParts] : none, c);
     if (lane == 0) cstat = st;
-    if (K > 0) {
-      const uint32_t t = find_threshold(high_of, nt, K);
-      if (lane == 0) thr = t, count[0] = count[1] = 0;
-      for (int k = lane; k < K; k += 32) top[k] = 0;
-    }
   }
   if (K > 0) {
-    __syncthreads();
     part_top<DT>(part, high, K, cand, top, thr, count, above, wkey);
   }
   if (cluster > 1) {
@@ -885,14 +889,23 @@ __global__ void __launch_bounds__(kMaxThreads, 4) logprobs_kernel(const LogprobA
         }
         st = join<kParts>(p, c);
       }
-      for (int i = tid; i < cluster * K; i += nt) cand[i] = ld_cluster_u64(peer_smem_addr(top + i % K, i / K));
+      if (K > 0) {  // of the lists' keys, those that the largest K-th of a list does not rule out
+        if (tid == 0) count[0] = 0;
+        Key least = 0;
+        for (int r = 0; r < cluster; ++r) least = max(least, ld_cluster_u64(peer_smem_addr(top + K - 1, r)));
+        __syncthreads();
+        for (int i = tid; i < cluster * K; i += nt) {
+          const Key k = ld_cluster_u64(peer_smem_addr(top + i % K, i / K));
+          if (k != 0 && k >= least) cand[atomicAdd(count, 1)] = k;
+        }
+      }
     }
     cluster_barrier();  // every list has been read: the CTAs may leave, rank 0 may overwrite its own
     if (rank != 0) return;
     if (K > 0) {
       for (int k = tid; k < K; k += nt) top[k] = 0;
       __syncthreads();
-      rank_select(cand, cluster * K, top, K);
+      rank_select(cand, count[0], top, K);
     }
   }
   if (K > 0) __syncthreads();
@@ -902,10 +915,10 @@ __global__ void __launch_bounds__(kMaxThreads, 4) logprobs_kernel(const LogprobA
   const bool empty = st.s == 0.f;  // every logit -inf
   auto logprob = [&](float v) { return empty ? neg_inf_f() : kLn2 * ((v - bm) * c - l2); };
   for (int i = lane; i < a.n_tokens; i += 32) {
-    const int t = a.tokens[row * a.n_tokens + i];
+    const int t = i == lane ? t_first : a.tokens[row * a.n_tokens + i];
     float lp = 0.f;
     if (t >= 0 && t < a.V)
-      lp = logprob(El::get(z[t]));
+      lp = logprob(i == lane ? z_first : El::get(z[t]));
     else if (t != -1)
       raise_status(a.status, TW_EINVAL);
     a.logprob[row * a.n_tokens + i] = lp;

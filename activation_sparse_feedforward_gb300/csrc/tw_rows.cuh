@@ -28,17 +28,16 @@ struct Elem<TW_F32> {
   static TW_DEV S put(float v) { return v; }
   static TW_DEV S neg_inf() { return __int_as_float(0xFF800000); }
   static TW_DEV S exchange(S* p, S v) { return atomicExch(p, v); }  // shared memory
-  static TW_DEV void pairs(const uint4& w, f32x2 (&v)[2]) {
-    v[0] = pair(__uint_as_float(w.x), __uint_as_float(w.y));
-    v[1] = pair(__uint_as_float(w.z), __uint_as_float(w.w));
+  static TW_DEV void pairs(const uint4& w, float2 (&v)[2]) {
+    v[0] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+    v[1] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
   }
   static TW_DEV void unpack(const uint4& w, float (&v)[4]) {
     v[0] = __uint_as_float(w.x), v[1] = __uint_as_float(w.y);
     v[2] = __uint_as_float(w.z), v[3] = __uint_as_float(w.w);
   }
-  static TW_DEV uint4 pack_pairs(const f32x2 (&v)[2]) {
-    const float2 a = unpair(v[0]), b = unpair(v[1]);
-    return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+  static TW_DEV uint4 pack_pairs(const float2 (&v)[2]) {
+    return make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
   }
   static TW_DEV uint4 pack(const float (&v)[4]) {
     return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
@@ -63,22 +62,19 @@ struct Elem<TW_BF16> {
   static TW_DEV S put(float v) { return f32_to_bf16(v); }
   static TW_DEV S neg_inf() { return 0xFF80; }
   static TW_DEV S exchange(S* p, S v) { return exchange16(p, v); }
-  static TW_DEV void pairs(const uint4& w, f32x2 (&v)[4]) {
-    v[0] = widen(w.x), v[1] = widen(w.y), v[2] = widen(w.z), v[3] = widen(w.w);
+  static TW_DEV void pairs(const uint4& w, float2 (&v)[4]) {
+    const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = make_float2(bf16_lo(r[i]), bf16_hi(r[i]));
   }
   static TW_DEV void unpack(const uint4& w, float (&v)[8]) {
     const uint32_t r[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(r[i]), v[2 * i + 1] = bf16_hi(r[i]);
   }
-  static TW_DEV uint4 pack_pairs(const f32x2 (&v)[4]) {
-    uint32_t r[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = unpair(v[i]);
-      r[i] = pack_bf16x2_rn(f.x, f.y);
-    }
-    return make_uint4(r[0], r[1], r[2], r[3]);
+  static TW_DEV uint4 pack_pairs(const float2 (&v)[4]) {
+    return make_uint4(pack_bf16x2_rn(v[0].x, v[0].y), pack_bf16x2_rn(v[1].x, v[1].y), pack_bf16x2_rn(v[2].x, v[2].y),
+                      pack_bf16x2_rn(v[3].x, v[3].y));
   }
   static TW_DEV uint4 pack(const float (&v)[8]) {
     return make_uint4(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]), pack_bf16x2_rn(v[4], v[5]),
@@ -112,13 +108,10 @@ struct Elem<TW_F16> {
   static TW_DEV S put(float v) { return f32_to_f16(v); }
   static TW_DEV S neg_inf() { return 0xFC00; }
   static TW_DEV S exchange(S* p, S v) { return exchange16(p, v); }
-  static TW_DEV void pairs(const uint4& w, f32x2 (&v)[4]) {
+  static TW_DEV void pairs(const uint4& w, float2 (&v)[4]) {
     const uint32_t r[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r[i]));
-      v[i] = pair(f.x, f.y);
-    }
+    for (int i = 0; i < 4; ++i) v[i] = __half22float2(*reinterpret_cast<const __half2*>(&r[i]));
   }
   static TW_DEV void unpack(const uint4& w, float (&v)[8]) {
     const uint32_t r[4] = {w.x, w.y, w.z, w.w};
@@ -128,14 +121,9 @@ struct Elem<TW_F16> {
       v[2 * i] = f.x, v[2 * i + 1] = f.y;
     }
   }
-  static TW_DEV uint4 pack_pairs(const f32x2 (&v)[4]) {
-    uint32_t r[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = unpair(v[i]);
-      r[i] = pack_f16x2_rn(f.x, f.y);
-    }
-    return make_uint4(r[0], r[1], r[2], r[3]);
+  static TW_DEV uint4 pack_pairs(const float2 (&v)[4]) {
+    return make_uint4(pack_f16x2_rn(v[0].x, v[0].y), pack_f16x2_rn(v[1].x, v[1].y), pack_f16x2_rn(v[2].x, v[2].y),
+                      pack_f16x2_rn(v[3].x, v[3].y));
   }
   static TW_DEV uint4 pack(const float (&v)[8]) {
     return make_uint4(pack_f16x2_rn(v[0], v[1]), pack_f16x2_rn(v[2], v[3]), pack_f16x2_rn(v[4], v[5]),
@@ -161,18 +149,12 @@ struct Elem<TW_F16> {
   }
 };
 
-// Packed fp32 pairs, one rounding per lane (half the instructions of two floats).
-TW_DEV f32x2 add2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-TW_DEV f32x2 mul2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-TW_DEV f32x2 both(float v) { return pair(v, v); }
+// Two fp32 lanes an instruction, one rounding per lane. (float2 and the intrinsics, not
+// 64-bit registers: the compiler then places the halves without moves.)
+TW_DEV float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+TW_DEV float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+TW_DEV float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+TW_DEV float2 both(float v) { return make_float2(v, v); }
 
 // ------------------------------------------------------------------ asynchronous copies
 // One 16-byte copy, global to shared, past L1; the copying thread sees its own copies

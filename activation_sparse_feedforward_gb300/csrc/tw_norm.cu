@@ -10,6 +10,12 @@
 // A row is read once and stays in the registers of its team of warps, so the variance
 // is the two-sweep one (no cancellation of large means) at no extra traffic. All
 // statistics and sums are fp32; y, dx and s are rounded once.
+//
+// Both directions are bound by HBM: CTAs stay for many rows, a team keeps the rows it
+// will take next on their way through its own places of a ring in shared memory (each
+// thread copies and reads back its own 16 bytes, so the ring needs no barrier), and
+// weights and column sums stay in registers. Rows that 16-byte accesses do not fit, or
+// that are too wide for a ring, are loaded straight into registers.
 #include <algorithm>
 
 #include "tw_internal.h"
@@ -19,203 +25,323 @@ namespace tw {
 
 namespace {
 
-// Elements of a row owned by a thread: VPT chunks of 8 (VEC: consecutive elements,
-// 16-byte accesses) or 8 VPT single elements (any d, alignment and row stride).
+// Elements of a row owned by a thread, 8 VPT of them as packed pairs: vectors of 16 bytes
+// (VEC) or single elements (any d, alignment and row stride), both in strides of the
+// team so that a warp's accesses are adjacent. What lies past the row reads 0.
 template <int DT, int VPT, bool VEC>
 struct RowMap {
   using S = typename Elem<DT>::S;
-  static constexpr int NE = 8 * VPT;
-  static TW_DEV int col(int i, int tid, int tpr) {
-    return VEC ? ((i >> 3) * tpr + tid) * 8 + (i & 7) : i * tpr + tid;
+  static constexpr int NE = 8 * VPT, NP = NE / 2;
+  static constexpr int E = VEC ? Elem<DT>::E : 1, NV = NE / E;  // elements a vector, vectors
+  int d, tid, tpr;
+  TW_DEV RowMap(int d_, int tid_, int tpr_) : d(d_), tid(tid_), tpr(tpr_) {}
+  TW_DEV int col(int i) const { return (i / E * tpr + tid) * E + i % E; }
+  TW_DEV bool has(int i) const { return col(i / E * E) < d; }  // a vector is in the row whole or not at all
+
+  static TW_DEV void widen16(const uint4& w, float2* v) {
+    float2 u[Elem<DT>::E / 2];
+    Elem<DT>::pairs(w, u);
+#pragma unroll
+    for (int e = 0; e < Elem<DT>::E / 2; ++e) v[e] = u[e];
   }
-  static TW_DEV void load(const S* p, int d, int tid, int tpr, float (&v)[NE]) {
+  TW_DEV void load(const S* p, float2 (&v)[NP]) const {
     if constexpr (VEC) {
-      constexpr int E = Elem<DT>::E;
 #pragma unroll
-      for (int k = 0; k < NE / E; ++k) {
-        const int c = col(k * E, tid, tpr);
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (c < d) w = *reinterpret_cast<const uint4*>(p + c);
-        float u[E];
-        Elem<DT>::unpack(w, u);
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[k * E + e] = u[e];
-      }
+      for (int k = 0; k < NV; ++k)
+        widen16(has(k * E) ? *reinterpret_cast<const uint4*>(p + col(k * E)) : make_uint4(0, 0, 0, 0), v + k * E / 2);
     } else {
 #pragma unroll
-      for (int i = 0; i < NE; ++i) {
-        const int c = col(i, tid, tpr);
-        v[i] = c < d ? Elem<DT>::get(p[c]) : 0.f;
+      for (int i = 0; i < NP; ++i) {
+        v[i].x = has(2 * i) ? Elem<DT>::get(p[col(2 * i)]) : 0.f;
+        v[i].y = has(2 * i + 1) ? Elem<DT>::get(p[col(2 * i + 1)]) : 0.f;
       }
     }
   }
-  static TW_DEV void store(S* p, int d, int tid, int tpr, const float (&v)[NE]) {
+  TW_DEV void store(S* p, const float2 (&v)[NP]) const {
     if constexpr (VEC) {
-      constexpr int E = Elem<DT>::E;
 #pragma unroll
-      for (int k = 0; k < NE / E; ++k) {
-        const int c = col(k * E, tid, tpr);
-        float u[E];
+      for (int k = 0; k < NV; ++k) {
+        float2 u[E / 2];
 #pragma unroll
-        for (int e = 0; e < E; ++e) u[e] = v[k * E + e];
-        if (c < d) *reinterpret_cast<uint4*>(p + c) = Elem<DT>::pack(u);
+        for (int e = 0; e < E / 2; ++e) u[e] = v[k * E / 2 + e];
+        if (has(k * E)) *reinterpret_cast<uint4*>(p + col(k * E)) = Elem<DT>::pack_pairs(u);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < NE; ++i) {
-        const int c = col(i, tid, tpr);
-        if (c < d) p[c] = Elem<DT>::put(v[i]);
+      for (int i = 0; i < NP; ++i) {
+        if (has(2 * i)) p[col(2 * i)] = Elem<DT>::put(v[i].x);
+        if (has(2 * i + 1)) p[col(2 * i + 1)] = Elem<DT>::put(v[i].y);
       }
     }
+  }
+  // a vector of d weights of the row's type or fp32 (fill where it is null)
+  TW_DEV void weight(const void* w, int wtype, float fill, float2 (&v)[NP]) const {
+    if (w == nullptr) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) v[i] = both(fill);
+    } else if (wtype == DT) {
+      load(static_cast<const S*>(w), v);
+    } else {
+      const float* p = static_cast<const float*>(w);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        if constexpr (VEC) {
+          v[i] = has(2 * i) ? *reinterpret_cast<const float2*>(p + col(2 * i)) : both(0.f);
+        } else {
+          v[i].x = has(2 * i) ? p[col(2 * i)] : 0.f;
+          v[i].y = has(2 * i + 1) ? p[col(2 * i + 1)] : 0.f;
+        }
+      }
+    }
+  }
+  // f(pair) for the pairs inside the row; where a pair may be half in it (single
+  // elements) f's result is masked by keep()
+  template <class F>
+  TW_DEV void each(F f) const {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+        if (has(k * E)) {
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) f(k * E / 2 + e);
+        }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) f(i);
+    }
+  }
+  TW_DEV float2 keep(int i, float2 v) const {
+    if constexpr (!VEC) v = make_float2(has(2 * i) ? v.x : 0.f, has(2 * i + 1) ? v.y : 0.f);
+    return v;
   }
 };
 
-// The thread's elements of a weight vector of type DT or fp32 (fill where it is null).
-template <int DT, int VPT, bool VEC>
-TW_DEV void load_weight(const void* w, int wtype, float fill, int d, int tid, int tpr, float (&v)[8 * VPT]) {
-  if (w == nullptr) {
-#pragma unroll
-    for (int i = 0; i < 8 * VPT; ++i) v[i] = fill;
-  } else if (wtype == DT) {
-    RowMap<DT, VPT, VEC>::load(static_cast<const typename Elem<DT>::S*>(w), d, tid, tpr, v);
-  } else {
-    RowMap<TW_F32, VPT, VEC>::load(static_cast<const float*>(w), d, tid, tpr, v);
-  }
-}
-
-// Sum over a team's threads, the same bits in each of them. `red` holds 32 floats; a
+// Sum over a team's threads, the same bits in each of them. `red` holds 32 values; a
 // caller alternates between two of them, so that one barrier per sum is enough.
 TW_DEV float team_sum(float v, float* red, int team, int tpr) {
   v = warp_sum(v);
   if (tpr == 32) return v;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = tpr >> 5;
   if (lane == 0) red[warp] = v;
   team_barrier(team + 1, tpr);
-  return warp_sum(lane < (tpr >> 5) ? red[lane] : 0.f);
+  if (warps > 8) return warp_sum(lane < warps ? red[lane] : 0.f);
+  v = red[0];
+  for (int w = 1; w < warps; ++w) v += red[w];
+  return v;
 }
 TW_DEV float2 team_sum2(float a, float b, float2* red, int team, int tpr) {
-  a = warp_sum(a);
-  b = warp_sum(b);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+    b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+  }
   if (tpr == 32) return make_float2(a, b);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = tpr >> 5;
   if (lane == 0) red[warp] = make_float2(a, b);
   team_barrier(team + 1, tpr);
-  const float2 p = lane < (tpr >> 5) ? red[lane] : make_float2(0.f, 0.f);
-  return make_float2(warp_sum(p.x), warp_sum(p.y));
+  if (warps > 8) {
+    const float2 p = lane < warps ? red[lane] : make_float2(0.f, 0.f);
+    return make_float2(warp_sum(p.x), warp_sum(p.y));
+  }
+  float2 v = red[0];
+  for (int w = 1; w < warps; ++w) v.x += red[w].x, v.y += red[w].y;
+  return v;
 }
 
 constexpr int kMaxTeams = 15;  // named barriers 1..15
 
-template <int DT, int VPT, bool VEC>
-__global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormFwdArgs a) {
+// A thread's places in its team's ring: DEPTH rows of up to three tensors, NV vectors of
+// 16 bytes each (the thread's chunks of 8 elements). DEPTH 0: no ring.
+template <int DT, int VPT, int DEPTH>
+struct Ring {
+  using M = RowMap<DT, VPT, true>;
+  static constexpr int E = M::E, NV = M::NV;
+  uint4* mine;
+  int tensors;
+  TW_DEV Ring(uint4* smem, int team, int tensors_, const M& m)
+      : mine(smem + team * (DEPTH * tensors_ * NV * m.tpr) + m.tid), tensors(tensors_) {}
+  TW_DEV uint4* place(const M& m, int stage, int t) const { return mine + (stage * tensors + t) * NV * m.tpr; }
+  TW_DEV void copy(const M& m, int stage, int t, const typename M::S* row) const {
+    uint4* to = place(m, stage, t);
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+      if (m.has(k * E)) cp_async16(to + k * m.tpr, row + m.col(k * E));
+  }
+  TW_DEV void read(const M& m, int stage, int t, float2 (&v)[M::NP]) const {
+    const uint4* from = place(m, stage, t);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) M::widen16(m.has(k * E) ? from[k * m.tpr] : make_uint4(0, 0, 0, 0), v + k * E / 2);
+  }
+};
+
+template <int DT, int VPT, bool VEC, int DEPTH, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 3 : 1) norm_fwd_kernel(const NormFwdArgs a) {
   using M = RowMap<DT, VPT, VEC>;
   using S = typename M::S;
+  constexpr int NP = M::NP;
+  extern __shared__ uint4 smem[];
   __shared__ float red[2][kMaxTeams][32];
   pdl_enter();
   const int tid = threadIdx.x, tpr = blockDim.x, team = threadIdx.y;
-  const int row = blockIdx.x * blockDim.y + team;
-  if (row >= a.T) return;
-  const size_t r = static_cast<size_t>(row);
-  float v[M::NE];
-  M::load(static_cast<const S*>(a.x) + r * a.ldx, a.d, tid, tpr, v);
-  if (a.res != nullptr) {
-    float u[M::NE];
-    M::load(static_cast<const S*>(a.res) + r * a.ldres, a.d, tid, tpr, u);
+  const int stride = gridDim.x * blockDim.y;
+  int row = blockIdx.x * blockDim.y + team;
+  const M m(a.d, tid, tpr);
+  auto at = [](const void* p, int64_t ld, int r) { return static_cast<const S*>(p) + static_cast<size_t>(r) * ld; };
+  const RowMap<DT, VPT, true> mv(a.d, tid, tpr);
+  const Ring<DT, VPT, DEPTH> ring(smem, team, a.res != nullptr ? 2 : 1, mv);
+  auto fetch = [&](int stage, int r) {
+    if (r < a.T) {
+      ring.copy(mv, stage, 0, at(a.x, a.ldx, r));
+      if (a.res != nullptr) ring.copy(mv, stage, 1, at(a.res, a.ldres, r));
+    }
+    cp_commit();
+  };
+  if constexpr (DEPTH > 0) {
 #pragma unroll
-    for (int i = 0; i < M::NE; ++i) v[i] = Elem<DT>::get(Elem<DT>::put(v[i] + u[i]));
-    if (a.sum != nullptr) M::store(static_cast<S*>(a.sum) + r * a.ldsum, a.d, tid, tpr, v);
+    for (int s = 0; s < DEPTH; ++s) fetch(s, row + s * stride);
   }
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < M::NE; ++i) s += v[i];
+  float2 w[NP], b[NP];
+  m.weight(a.w, a.wtype, 1.f, w);
+  m.weight(a.b, a.wtype, 0.f, b);
   const float inv_d = 1.f / static_cast<float>(a.d);
-  const float mean = team_sum(s, red[0][team], team, tpr) * inv_d;
-  float q = 0.f;
+  for (int stage = 0; row < a.T; row += stride) {
+    float2 v[NP], u[NP];
+    if constexpr (DEPTH > 0) {
+      cp_wait<DEPTH - 1>();
+      ring.read(mv, stage, 0, v);
+      if (a.res != nullptr) ring.read(mv, stage, 1, u);
+    } else {
+      m.load(at(a.x, a.ldx, row), v);
+      if (a.res != nullptr) m.load(at(a.res, a.ldres, row), u);
+    }
+    const size_t r = static_cast<size_t>(row);
+    if (a.res != nullptr) {
 #pragma unroll
-  for (int i = 0; i < M::NE; ++i) {
-    const float t = M::col(i, tid, tpr) < a.d ? v[i] - mean : 0.f;
-    q = fmaf(t, t, q);
-  }
-  const float rstd = rsqrtf(team_sum(q, red[1][team], team, tpr) * inv_d + a.eps);
-  float w[M::NE], b[M::NE];
-  load_weight<DT, VPT, VEC>(a.w, a.wtype, 1.f, a.d, tid, tpr, w);
-  load_weight<DT, VPT, VEC>(a.b, a.wtype, 0.f, a.d, tid, tpr, b);
+      for (int i = 0; i < NP; ++i) v[i] = Elem<DT>::rounded(add2(v[i], u[i]));
+      if (a.sum != nullptr) m.store(static_cast<S*>(a.sum) + r * a.ldsum, v);
+    }
+    float2 s = v[0];
 #pragma unroll
-  for (int i = 0; i < M::NE; ++i) v[i] = fmaf((v[i] - mean) * rstd, w[i], b[i]);
-  M::store(static_cast<S*>(a.y) + r * a.ldy, a.d, tid, tpr, v);
-  if (tid == 0) {
-    if (a.mean != nullptr) a.mean[row] = mean;
-    if (a.rstd != nullptr) a.rstd[row] = rstd;
+    for (int i = 1; i < NP; ++i) s = add2(s, v[i]);
+    const float mean = team_sum(s.x + s.y, red[0][team], team, tpr) * inv_d;
+    if constexpr (DEPTH > 0) {  // the row has left its places
+      fetch(stage, row + DEPTH * stride);
+      stage = stage + 1 == DEPTH ? 0 : stage + 1;
+    }
+    float2 q = both(0.f);
+    m.each([&](int i) {
+      v[i] = m.keep(i, add2(v[i], both(-mean)));
+      q = fma2(v[i], v[i], q);
+    });
+    const float rstd = rsqrtf(team_sum(q.x + q.y, red[1][team], team, tpr) * inv_d + a.eps);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) v[i] = fma2(mul2(v[i], both(rstd)), w[i], b[i]);
+    m.store(static_cast<S*>(a.y) + r * a.ldy, v);
+    if (tid == 0) {
+      if (a.mean != nullptr) a.mean[row] = mean;
+      if (a.rstd != nullptr) a.rstd[row] = rstd;
+    }
   }
 }
 
-template <int DT, int VPT, bool VEC, int MAXT>
+template <int DT, int VPT, bool VEC, int DEPTH, int MAXT>
 __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwdArgs a) {
   using M = RowMap<DT, VPT, VEC>;
   using S = typename M::S;
-  extern __shared__ float acc[];  // [2][d], teams joined in order (teams > 1 only)
+  constexpr int NP = M::NP;
+  extern __shared__ uint4 smem[];  // the ring; then [2][d] fp32, the teams' column sums joined in order
   __shared__ float2 red[2][kMaxTeams][32];
   pdl_enter();
-  const int tid = threadIdx.x, tpr = blockDim.x, team = threadIdx.y;
-  float w[M::NE], dw[M::NE], db[M::NE];
-  load_weight<DT, VPT, VEC>(a.w, a.wtype, 1.f, a.d, tid, tpr, w);
+  const int tid = threadIdx.x, tpr = blockDim.x, team = threadIdx.y, teams = blockDim.y;
+  const int stride = gridDim.x * teams;
+  int row = blockIdx.x * teams + team;
+  const M m(a.d, tid, tpr);
+  auto at = [](const void* p, int64_t ld, int r) { return static_cast<const S*>(p) + static_cast<size_t>(r) * ld; };
+  const RowMap<DT, VPT, true> mv(a.d, tid, tpr);
+  const Ring<DT, VPT, DEPTH> ring(smem, team, a.dres != nullptr ? 3 : 2, mv);
+  auto fetch = [&](int stage, int r) {
+    if (r < a.T) {
+      ring.copy(mv, stage, 0, at(a.x, a.ldx, r));
+      ring.copy(mv, stage, 1, at(a.dy, a.lddy, r));
+      if (a.dres != nullptr) ring.copy(mv, stage, 2, at(a.dres, a.lddres, r));
+    }
+    cp_commit();
+  };
+  if constexpr (DEPTH > 0) {
 #pragma unroll
-  for (int i = 0; i < M::NE; ++i) dw[i] = db[i] = 0.f;
+    for (int s = 0; s < DEPTH; ++s) fetch(s, row + s * stride);
+  }
+  float2 w[NP], dw[NP], db[NP];
+  m.weight(a.w, a.wtype, 1.f, w);
+#pragma unroll
+  for (int i = 0; i < NP; ++i) dw[i] = db[i] = both(0.f);
   const float inv_d = 1.f / static_cast<float>(a.d);
-  int flip = 0;
-  for (int row = blockIdx.x * blockDim.y + team; row < a.T; row += gridDim.x * blockDim.y, flip ^= 1) {
-    const size_t r = static_cast<size_t>(row);
-    float x[M::NE], g[M::NE];
-    M::load(static_cast<const S*>(a.x) + r * a.ldx, a.d, tid, tpr, x);
-    M::load(static_cast<const S*>(a.dy) + r * a.lddy, a.d, tid, tpr, g);
-    const float mean = a.mean[row], rstd = a.rstd[row];
-    float c1 = 0.f, c2 = 0.f;
-#pragma unroll
-    for (int i = 0; i < M::NE; ++i) {
-      x[i] = M::col(i, tid, tpr) < a.d ? (x[i] - mean) * rstd : 0.f;
-      dw[i] = fmaf(g[i], x[i], dw[i]);
-      db[i] += g[i];
-      g[i] *= w[i];
-      c1 += g[i];
-      c2 = fmaf(g[i], x[i], c2);
+  float mean = row < a.T ? a.mean[row] : 0.f, rstd = row < a.T ? a.rstd[row] : 0.f;
+  for (int flip = 0, stage = 0; row < a.T; row += stride, flip ^= 1) {
+    float2 x[NP], g[NP], more[NP];
+    if constexpr (DEPTH > 0) {
+      cp_wait<DEPTH - 1>();
+      ring.read(mv, stage, 0, x);
+      ring.read(mv, stage, 1, g);
+      if (a.dres != nullptr) ring.read(mv, stage, 2, more);
+    } else {
+      m.load(at(a.x, a.ldx, row), x);
+      m.load(at(a.dy, a.lddy, row), g);
     }
-    const float2 c = team_sum2(c1, c2, red[flip][team], team, tpr);
-    c1 = c.x * inv_d;
-    c2 = c.y * inv_d;
-#pragma unroll
-    for (int i = 0; i < M::NE; ++i) g[i] = rstd * (g[i] - fmaf(x[i], c2, c1));
-    if (a.dres != nullptr) {
-      M::load(static_cast<const S*>(a.dres) + r * a.lddres, a.d, tid, tpr, x);
-#pragma unroll
-      for (int i = 0; i < M::NE; ++i) g[i] += x[i];
+    float2 c1 = both(0.f), c2 = both(0.f);
+    m.each([&](int i) {
+      x[i] = m.keep(i, mul2(add2(x[i], both(-mean)), both(rstd)));
+      dw[i] = fma2(g[i], x[i], dw[i]);
+      db[i] = add2(db[i], g[i]);
+      g[i] = mul2(g[i], w[i]);
+      c1 = add2(c1, g[i]);
+      c2 = fma2(g[i], x[i], c2);
+    });
+    const float2 c = team_sum2(c1.x + c1.y, c2.x + c2.y, red[flip][team], team, tpr);
+    if constexpr (DEPTH > 0) {  // the row has left its places
+      fetch(stage, row + DEPTH * stride);
+      stage = stage + 1 == DEPTH ? 0 : stage + 1;
+    } else if (a.dres != nullptr) {
+      m.load(at(a.dres, a.lddres, row), more);
     }
-    M::store(static_cast<S*>(a.dx) + r * a.lddx, a.d, tid, tpr, g);
+    const int next = row + stride;
+    const float mean_next = next < a.T ? a.mean[next] : 0.f, rstd_next = next < a.T ? a.rstd[next] : 0.f;
+    const float2 k1 = both(-c.x * inv_d), k2 = both(-c.y * inv_d);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      g[i] = mul2(add2(g[i], fma2(x[i], k2, k1)), both(rstd));
+      if (a.dres != nullptr) g[i] = add2(g[i], more[i]);
+    }
+    m.store(static_cast<S*>(a.dx) + static_cast<size_t>(row) * a.lddx, g);
+    mean = mean_next, rstd = rstd_next;
   }
   if (a.part == nullptr) return;
   float* out = a.part + static_cast<size_t>(blockIdx.x) * 2 * a.d;
-  for (int t = 0; t + 1 < static_cast<int>(blockDim.y); ++t) {
-    if (team == t) {
+  float* acc = reinterpret_cast<float*>(smem);
+  auto sums = [&](auto f) {  // f(column, dw, db) of the thread's columns
 #pragma unroll
-      for (int i = 0; i < M::NE; ++i) {
-        const int c = M::col(i, tid, tpr);
-        if (c < a.d) {
-          acc[c] = t == 0 ? dw[i] : acc[c] + dw[i];
-          acc[a.d + c] = t == 0 ? db[i] : acc[a.d + c] + db[i];
-        }
-      }
+    for (int i = 0; i < NP; ++i) {
+      if (m.has(2 * i)) f(m.col(2 * i), dw[i].x, db[i].x);
+      if (m.has(2 * i + 1)) f(m.col(2 * i + 1), dw[i].y, db[i].y);
     }
+  };
+  if (DEPTH > 0) {
+    cp_wait<0>();
     __syncthreads();
   }
-  if (team == static_cast<int>(blockDim.y) - 1) {
-#pragma unroll
-    for (int i = 0; i < M::NE; ++i) {
-      const int c = M::col(i, tid, tpr);
-      if (c < a.d) {
-        out[c] = team == 0 ? dw[i] : acc[c] + dw[i];
-        out[a.d + c] = team == 0 ? db[i] : acc[a.d + c] + db[i];
-      }
-    }
+  for (int t = 0; t + 1 < teams; ++t) {
+    if (team == t)
+      sums([&](int c, float p, float q) {
+        acc[c] = t == 0 ? p : acc[c] + p;
+        acc[a.d + c] = t == 0 ? q : acc[a.d + c] + q;
+      });
+    __syncthreads();
   }
+  if (team == teams - 1)
+    sums([&](int c, float p, float q) {
+      out[c] = team == 0 ? p : acc[c] + p;
+      out[a.d + c] = team == 0 ? q : acc[a.d + c] + q;
+    });
 }
 
 // dw, db = the partial sums of `n` CTAs, added in a fixed order.
@@ -254,13 +380,33 @@ Team team_of(int d, int vpt, int threads, int T) {
   t.teams = std::max(1, std::min({threads / t.tpr, kMaxTeams, T}));
   return t;
 }
+size_t ring_bytes(const Team& t, int vpt, int dtype, int tensors, int depth) {
+  return static_cast<size_t>(t.teams) * depth * tensors * t.tpr * 8 * vpt * elem_size(dtype);
+}
+constexpr size_t kSmemMost = 216 * 1024;  // beside the kernels' static shared memory
 
-template <int DT, int VPT, bool VEC>
-cudaError_t norm_fwd(const NormFwdArgs& a, cudaStream_t s) {
-  const Team t = team_of(a.d, VPT, 256, a.T);
-  cudaError_t e = launch(norm_fwd_kernel<DT, VPT, VEC>, dim3((a.T + t.teams - 1) / t.teams), dim3(t.tpr, t.teams), 0, s, a);
-  trace_mark(s, "norm_fwd");
+template <class Kern, class Args>
+cudaError_t launch_norm(Kern kern, int grid, const Team& t, size_t smem, const char* label, const Args& a,
+                        cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  if (smem > 40 * 1024)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  e = launch(kern, dim3(grid), dim3(t.tpr, t.teams), smem, s, a);
+  trace_mark(s, label);
   return e;
+}
+
+template <int DT, int VPT, bool VEC, int DEPTH, int MAXT>
+cudaError_t norm_fwd(const NormFwdArgs& a, cudaStream_t s) {
+  const Team t = team_of(a.d, VPT, MAXT <= 256 ? 256 : 32, a.T);
+  const size_t smem = ring_bytes(t, VPT, DT, a.res != nullptr ? 2 : 1, DEPTH);
+  const int rows = (a.T + t.teams - 1) / t.teams;
+  // as many CTAs as stay resident: 3 by registers (one row of up to 512 threads: 1 or 2)
+  const int fit = static_cast<int>(kSmemMost / (smem + 6 * 1024));
+  const int per_sm = DEPTH == 0 ? 8 : std::max(1, std::min(MAXT <= 256 ? 3 : 1, fit));
+  return launch_norm(norm_fwd_kernel<DT, VPT, VEC, DEPTH, MAXT>, std::min(rows, device_sm_count() * per_sm), t, smem,
+                     "norm_fwd", a, s);
 }
 
 cudaError_t norm_bwd_finish(const NormBwdArgs& a, int partials, cudaStream_t s) {
@@ -270,31 +416,50 @@ cudaError_t norm_bwd_finish(const NormBwdArgs& a, int partials, cudaStream_t s) 
   return e;
 }
 
-template <int DT, int VPT, bool VEC, int MAXT>
+template <int DT, int VPT, bool VEC, int DEPTH, int MAXT>
 cudaError_t norm_bwd(const NormBwdArgs& a, cudaStream_t s) {
   const Team t = team_of(a.d, VPT, MAXT, a.T);
   const int grid = std::min({(a.T + t.teams - 1) / t.teams, device_sm_count(), kNormPartials});
-  const size_t smem = t.teams > 1 ? 2 * sizeof(float) * a.d : 0;
-  cudaError_t e = cudaSuccess;
-  if (smem > 40 * 1024) {
-    e = cudaFuncSetAttribute(norm_bwd_kernel<DT, VPT, VEC, MAXT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-  }
-  e = launch(norm_bwd_kernel<DT, VPT, VEC, MAXT>, dim3(grid), dim3(t.tpr, t.teams), smem, s, a);
-  trace_mark(s, "norm_bwd");
+  const size_t smem = std::max(ring_bytes(t, VPT, DT, a.dres != nullptr ? 3 : 2, DEPTH),
+                               t.teams > 1 ? 2 * sizeof(float) * a.d : size_t{0});
+  cudaError_t e = launch_norm(norm_bwd_kernel<DT, VPT, VEC, DEPTH, MAXT>, grid, t, smem, "norm_bwd", a, s);
   if (e != cudaSuccess || a.part == nullptr) return e;
   return norm_bwd_finish(a, grid, s);
 }
 
+// Two chunks of 8 elements a thread from 1025 columns up. A ring of three rows a team
+// where it fits.
 template <int DT, bool VEC>
 cudaError_t norm_fwd_width(const NormFwdArgs& a, cudaStream_t s) {
-  return a.d <= 1024 ? norm_fwd<DT, 1, VEC>(a, s) : norm_fwd<DT, 2, VEC>(a, s);
+  if constexpr (VEC) {
+    const int tensors = a.res != nullptr ? 2 : 1;
+    if (a.d <= 1024) return norm_fwd<DT, 1, true, 3, 256>(a, s);
+    if (a.d <= 4096) return norm_fwd<DT, 2, true, 3, 256>(a, s);
+    if (a.d <= 8192 && ring_bytes(team_of(a.d, 2, 32, a.T), 2, DT, tensors, 3) <= kSmemMost)
+      return norm_fwd<DT, 2, true, 3, 512>(a, s);
+    return norm_fwd<DT, 2, true, 0, 1024>(a, s);
+  } else {
+    return a.d <= 2048 ? norm_fwd<DT, 1, false, 0, 256>(a, s)
+           : a.d <= 8192 ? norm_fwd<DT, 1, false, 0, 1024>(a, s) : norm_fwd<DT, 2, false, 0, 1024>(a, s);
+  }
 }
 template <int DT, bool VEC>
 cudaError_t norm_bwd_width(const NormBwdArgs& a, cudaStream_t s) {
-  if (a.d <= 512) return norm_bwd<DT, 1, VEC, 512>(a, s);
-  return a.d <= 8192 ? norm_bwd<DT, 2, VEC, 512>(a, s) : norm_bwd<DT, 2, VEC, 1024>(a, s);
+  if constexpr (VEC) {
+    const int tensors = a.dres != nullptr ? 3 : 2;
+    auto fits = [&](int vpt, int threads, int depth) {
+      return ring_bytes(team_of(a.d, vpt, threads, a.T), vpt, DT, tensors, depth) <= kSmemMost;
+    };
+    if (a.d <= 512) return norm_bwd<DT, 1, true, 3, 512>(a, s);
+    if (a.d <= 8192) {
+      if (fits(2, 512, 3)) return norm_bwd<DT, 2, true, 3, 512>(a, s);
+      return norm_bwd<DT, 2, true, 2, 512>(a, s);
+    }
+    return norm_bwd<DT, 2, true, 0, 1024>(a, s);
+  } else {
+    return a.d <= 4096 ? norm_bwd<DT, 1, false, 0, 512>(a, s)
+           : a.d <= 8192 ? norm_bwd<DT, 1, false, 0, 1024>(a, s) : norm_bwd<DT, 2, false, 0, 1024>(a, s);
+  }
 }
 
 }  // namespace

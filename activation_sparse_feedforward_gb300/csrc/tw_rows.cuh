@@ -36,6 +36,7 @@ struct Elem<TW_F32> {
     v[0] = __uint_as_float(w.x), v[1] = __uint_as_float(w.y);
     v[2] = __uint_as_float(w.z), v[3] = __uint_as_float(w.w);
   }
+  static TW_DEV float2 rounded(float2 v) { return v; }  // to the type and back
   static TW_DEV uint4 pack_pairs(const float2 (&v)[2]) {
     return make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
   }
@@ -71,6 +72,10 @@ struct Elem<TW_BF16> {
     const uint32_t r[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(r[i]), v[2 * i + 1] = bf16_hi(r[i]);
+  }
+  static TW_DEV float2 rounded(float2 v) {
+    const uint32_t r = pack_bf16x2_rn(v.x, v.y);
+    return make_float2(bf16_lo(r), bf16_hi(r));
   }
   static TW_DEV uint4 pack_pairs(const float2 (&v)[4]) {
     return make_uint4(pack_bf16x2_rn(v[0].x, v[0].y), pack_bf16x2_rn(v[1].x, v[1].y), pack_bf16x2_rn(v[2].x, v[2].y),
@@ -121,6 +126,7 @@ struct Elem<TW_F16> {
       v[2 * i] = f.x, v[2 * i + 1] = f.y;
     }
   }
+  static TW_DEV float2 rounded(float2 v) { return __half22float2(__floats2half2_rn(v.x, v.y)); }
   static TW_DEV uint4 pack_pairs(const float2 (&v)[4]) {
     return make_uint4(pack_f16x2_rn(v[0].x, v[0].y), pack_f16x2_rn(v[1].x, v[1].y), pack_f16x2_rn(v[2].x, v[2].y),
                       pack_f16x2_rn(v[3].x, v[3].y));

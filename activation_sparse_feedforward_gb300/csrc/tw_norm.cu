@@ -27,15 +27,18 @@ namespace {
 
 // Elements of a row owned by a thread, 8 VPT of them as packed pairs: vectors of 16 bytes
 // (VEC) or single elements (any d, alignment and row stride), both in strides of the
-// team so that a warp's accesses are adjacent. What lies past the row reads 0.
-template <int DT, int VPT, bool VEC>
+// team so that a warp's accesses are adjacent. What lies past the row reads 0. TPR: the
+// team's threads where they are a constant of the kernel (offsets are then immediates),
+// else 0.
+template <int DT, int VPT, bool VEC, int TPR>
 struct RowMap {
   using S = typename Elem<DT>::S;
   static constexpr int NE = 8 * VPT, NP = NE / 2;
-  static constexpr int E = VEC ? Elem<DT>::E : 1, NV = NE / E;  // elements a vector, vectors
-  int d, tid, tpr;
-  TW_DEV RowMap(int d_, int tid_, int tpr_) : d(d_), tid(tid_), tpr(tpr_) {}
-  TW_DEV int col(int i) const { return (i / E * tpr + tid) * E + i % E; }
+  static constexpr int E = VEC ? Elem<DT>::E : 1, NV = NE / E;  // elements of a vector, vectors
+  int d, tid;
+  TW_DEV RowMap(int d_, int tid_) : d(d_), tid(tid_) {}
+  static TW_DEV int tpr() { return TPR > 0 ? TPR : blockDim.x; }
+  TW_DEV int col(int i) const { return (i / E * tpr() + tid) * E + i % E; }
   TW_DEV bool has(int i) const { return col(i / E * E) < d; }  // a vector is in the row whole or not at all
 
   static TW_DEV void widen16(const uint4& w, float2* v) {
@@ -152,43 +155,43 @@ constexpr int kMaxTeams = 15;  // named barriers 1..15
 
 // A thread's places in its team's ring: DEPTH rows of up to three tensors, NV vectors of
 // 16 bytes each (the thread's chunks of 8 elements). DEPTH 0: no ring.
-template <int DT, int VPT, int DEPTH>
+template <int DT, int VPT, int DEPTH, int TPR>
 struct Ring {
-  using M = RowMap<DT, VPT, true>;
+  using M = RowMap<DT, VPT, true, TPR>;
   static constexpr int E = M::E, NV = M::NV;
   uint4* mine;
   int tensors;
   TW_DEV Ring(uint4* smem, int team, int tensors_, const M& m)
-      : mine(smem + team * (DEPTH * tensors_ * NV * m.tpr) + m.tid), tensors(tensors_) {}
-  TW_DEV uint4* place(const M& m, int stage, int t) const { return mine + (stage * tensors + t) * NV * m.tpr; }
+      : mine(smem + team * (DEPTH * tensors_ * NV * m.tpr()) + m.tid), tensors(tensors_) {}
+  TW_DEV uint4* place(const M& m, int stage, int t) const { return mine + (stage * tensors + t) * NV * m.tpr(); }
   TW_DEV void copy(const M& m, int stage, int t, const typename M::S* row) const {
     uint4* to = place(m, stage, t);
 #pragma unroll
     for (int k = 0; k < NV; ++k)
-      if (m.has(k * E)) cp_async16(to + k * m.tpr, row + m.col(k * E));
+      if (m.has(k * E)) cp_async16(to + k * m.tpr(), row + m.col(k * E));
   }
   TW_DEV void read(const M& m, int stage, int t, float2 (&v)[M::NP]) const {
     const uint4* from = place(m, stage, t);
 #pragma unroll
-    for (int k = 0; k < NV; ++k) M::widen16(m.has(k * E) ? from[k * m.tpr] : make_uint4(0, 0, 0, 0), v + k * E / 2);
+    for (int k = 0; k < NV; ++k) M::widen16(m.has(k * E) ? from[k * m.tpr()] : make_uint4(0, 0, 0, 0), v + k * E / 2);
   }
 };
 
-template <int DT, int VPT, bool VEC, int DEPTH, int MAXT>
+template <int DT, int VPT, bool VEC, int DEPTH, int TPR, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 3 : 1) norm_fwd_kernel(const NormFwdArgs a) {
-  using M = RowMap<DT, VPT, VEC>;
+  using M = RowMap<DT, VPT, VEC, TPR>;
   using S = typename M::S;
   constexpr int NP = M::NP;
   extern __shared__ uint4 smem[];
   __shared__ float red[2][kMaxTeams][32];
   pdl_enter();
-  const int tid = threadIdx.x, tpr = blockDim.x, team = threadIdx.y;
-  const int stride = gridDim.x * blockDim.y;
-  int row = blockIdx.x * blockDim.y + team;
-  const M m(a.d, tid, tpr);
+  const int tid = threadIdx.x, tpr = M::tpr(), team = threadIdx.y, teams = TPR > 0 ? MAXT / TPR : blockDim.y;
+  const int stride = gridDim.x * teams;
+  int row = blockIdx.x * teams + team;
+  const M m(a.d, tid);
   auto at = [](const void* p, int64_t ld, int r) { return static_cast<const S*>(p) + static_cast<size_t>(r) * ld; };
-  const RowMap<DT, VPT, true> mv(a.d, tid, tpr);
-  const Ring<DT, VPT, DEPTH> ring(smem, team, a.res != nullptr ? 2 : 1, mv);
+  const RowMap<DT, VPT, true, TPR> mv(a.d, tid);
+  const Ring<DT, VPT, DEPTH, TPR> ring(smem, team, a.res != nullptr ? 2 : 1, mv);
   auto fetch = [&](int stage, int r) {
     if (r < a.T) {
       ring.copy(mv, stage, 0, at(a.x, a.ldx, r));
@@ -244,21 +247,21 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 3 : 1) norm_fwd_kernel(con
   }
 }
 
-template <int DT, int VPT, bool VEC, int DEPTH, int MAXT>
+template <int DT, int VPT, bool VEC, int DEPTH, int TPR, int MAXT>
 __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwdArgs a) {
-  using M = RowMap<DT, VPT, VEC>;
+  using M = RowMap<DT, VPT, VEC, TPR>;
   using S = typename M::S;
   constexpr int NP = M::NP;
   extern __shared__ uint4 smem[];  // the ring; then [2][d] fp32, the teams' column sums joined in order
   __shared__ float2 red[2][kMaxTeams][32];
   pdl_enter();
-  const int tid = threadIdx.x, tpr = blockDim.x, team = threadIdx.y, teams = blockDim.y;
+  const int tid = threadIdx.x, tpr = M::tpr(), team = threadIdx.y, teams = TPR > 0 ? MAXT / TPR : blockDim.y;
   const int stride = gridDim.x * teams;
   int row = blockIdx.x * teams + team;
-  const M m(a.d, tid, tpr);
+  const M m(a.d, tid);
   auto at = [](const void* p, int64_t ld, int r) { return static_cast<const S*>(p) + static_cast<size_t>(r) * ld; };
-  const RowMap<DT, VPT, true> mv(a.d, tid, tpr);
-  const Ring<DT, VPT, DEPTH> ring(smem, team, a.dres != nullptr ? 3 : 2, mv);
+  const RowMap<DT, VPT, true, TPR> mv(a.d, tid);
+  const Ring<DT, VPT, DEPTH, TPR> ring(smem, team, a.dres != nullptr ? 3 : 2, mv);
   auto fetch = [&](int stage, int r) {
     if (r < a.T) {
       ring.copy(mv, stage, 0, at(a.x, a.ldx, r));
@@ -380,9 +383,7 @@ Team team_of(int d, int vpt, int threads, int T) {
   t.teams = std::max(1, std::min({threads / t.tpr, kMaxTeams, T}));
   return t;
 }
-size_t ring_bytes(const Team& t, int vpt, int dtype, int tensors, int depth) {
-  return static_cast<size_t>(t.teams) * depth * tensors * t.tpr * 8 * vpt * elem_size(dtype);
-}
+
 constexpr size_t kSmemMost = 216 * 1024;  // beside the kernels' static shared memory
 
 template <class Kern, class Args>
@@ -397,16 +398,27 @@ cudaError_t launch_norm(Kern kern, int grid, const Team& t, size_t smem, const c
   return e;
 }
 
-template <int DT, int VPT, bool VEC, int DEPTH, int MAXT>
-cudaError_t norm_fwd(const NormFwdArgs& a, cudaStream_t s) {
-  const Team t = team_of(a.d, VPT, MAXT <= 256 ? 256 : 32, a.T);
-  const size_t smem = ring_bytes(t, VPT, DT, a.res != nullptr ? 2 : 1, DEPTH);
-  const int rows = (a.T + t.teams - 1) / t.teams;
-  // as many CTAs as stay resident: 3 by registers (one row of up to 512 threads: 1 or 2)
+// Rows through a ring of DEPTH: MAXT / TPR teams of TPR threads, 16 elements a thread.
+template <int DT, int TPR, int MAXT, int DEPTH>
+size_t ring_bytes(int tensors) {
+  return static_cast<size_t>(MAXT) * DEPTH * tensors * 16 * (DT == TW_F32 ? 4 : 2);
+}
+template <int DT, int TPR, int MAXT>
+cudaError_t norm_fwd_ring(const NormFwdArgs& a, cudaStream_t s) {
+  constexpr int kTeams = MAXT / TPR;
+  const size_t smem = ring_bytes<DT, TPR, MAXT, 3>(a.res != nullptr ? 2 : 1);
+  // as many CTAs as stay resident: three by registers (512 threads: one)
   const int fit = static_cast<int>(kSmemMost / (smem + 6 * 1024));
-  const int per_sm = DEPTH == 0 ? 8 : std::max(1, std::min(MAXT <= 256 ? 3 : 1, fit));
-  return launch_norm(norm_fwd_kernel<DT, VPT, VEC, DEPTH, MAXT>, std::min(rows, device_sm_count() * per_sm), t, smem,
+  const int per_sm = std::max(1, std::min(MAXT <= 256 ? 3 : 1, fit));
+  return launch_norm(norm_fwd_kernel<DT, 2, true, 3, TPR, MAXT>,
+                     std::min((a.T + kTeams - 1) / kTeams, device_sm_count() * per_sm), Team{TPR, kTeams}, smem,
                      "norm_fwd", a, s);
+}
+template <int DT, int VPT, bool VEC, int MAXT>
+cudaError_t norm_fwd_direct(const NormFwdArgs& a, cudaStream_t s) {
+  const Team t = team_of(a.d, VPT, MAXT <= 256 ? 256 : 32, a.T);
+  return launch_norm(norm_fwd_kernel<DT, VPT, VEC, 0, 0, MAXT>,
+                     std::min((a.T + t.teams - 1) / t.teams, device_sm_count() * 8), t, 0, "norm_fwd", a, s);
 }
 
 cudaError_t norm_bwd_finish(const NormBwdArgs& a, int partials, cudaStream_t s) {
@@ -416,49 +428,55 @@ cudaError_t norm_bwd_finish(const NormBwdArgs& a, int partials, cudaStream_t s) 
   return e;
 }
 
-template <int DT, int VPT, bool VEC, int DEPTH, int MAXT>
-cudaError_t norm_bwd(const NormBwdArgs& a, cudaStream_t s) {
+cudaError_t norm_bwd_done(cudaError_t e, const NormBwdArgs& a, int grid, cudaStream_t s) {
+  return e != cudaSuccess || a.part == nullptr ? e : norm_bwd_finish(a, grid, s);
+}
+template <int DT, int TPR, int DEPTH>
+cudaError_t norm_bwd_ring(const NormBwdArgs& a, cudaStream_t s) {
+  constexpr int kThreads = 512, kTeams = kThreads / TPR;
+  const int grid = std::min({(a.T + kTeams - 1) / kTeams, device_sm_count(), kNormPartials});
+  const size_t smem = std::max(ring_bytes<DT, TPR, kThreads, DEPTH>(a.dres != nullptr ? 3 : 2), 2 * sizeof(float) * a.d);
+  return norm_bwd_done(launch_norm(norm_bwd_kernel<DT, 2, true, DEPTH, TPR, kThreads>, grid, Team{TPR, kTeams}, smem,
+                                   "norm_bwd", a, s), a, grid, s);
+}
+template <int DT, int VPT, bool VEC, int MAXT>
+cudaError_t norm_bwd_direct(const NormBwdArgs& a, cudaStream_t s) {
   const Team t = team_of(a.d, VPT, MAXT, a.T);
   const int grid = std::min({(a.T + t.teams - 1) / t.teams, device_sm_count(), kNormPartials});
-  const size_t smem = std::max(ring_bytes(t, VPT, DT, a.dres != nullptr ? 3 : 2, DEPTH),
-                               t.teams > 1 ? 2 * sizeof(float) * a.d : size_t{0});
-  cudaError_t e = launch_norm(norm_bwd_kernel<DT, VPT, VEC, DEPTH, MAXT>, grid, t, smem, "norm_bwd", a, s);
-  if (e != cudaSuccess || a.part == nullptr) return e;
-  return norm_bwd_finish(a, grid, s);
+  const size_t smem = t.teams > 1 ? 2 * sizeof(float) * a.d : 0;
+  return norm_bwd_done(launch_norm(norm_bwd_kernel<DT, VPT, VEC, 0, 0, MAXT>, grid, t, smem, "norm_bwd", a, s), a, grid, s);
 }
 
-// Two chunks of 8 elements a thread from 1025 columns up. A ring of three rows a team
-// where it fits.
+// Teams of a power of two of threads, the least that holds the row at 16 elements a
+// thread, and three rows in the ring (the backward in fp32: two).
 template <int DT, bool VEC>
 cudaError_t norm_fwd_width(const NormFwdArgs& a, cudaStream_t s) {
   if constexpr (VEC) {
-    const int tensors = a.res != nullptr ? 2 : 1;
-    if (a.d <= 1024) return norm_fwd<DT, 1, true, 3, 256>(a, s);
-    if (a.d <= 4096) return norm_fwd<DT, 2, true, 3, 256>(a, s);
-    if (a.d <= 8192 && ring_bytes(team_of(a.d, 2, 32, a.T), 2, DT, tensors, 3) <= kSmemMost)
-      return norm_fwd<DT, 2, true, 3, 512>(a, s);
-    return norm_fwd<DT, 2, true, 0, 1024>(a, s);
+    if (a.d <= 512) return norm_fwd_ring<DT, 32, 256>(a, s);
+    if (a.d <= 1024) return norm_fwd_ring<DT, 64, 256>(a, s);
+    if (a.d <= 2048) return norm_fwd_ring<DT, 128, 256>(a, s);
+    if (a.d <= 4096) return norm_fwd_ring<DT, 256, 256>(a, s);
+    if (a.d <= 8192) return norm_fwd_ring<DT, 512, 512>(a, s);
+    return norm_fwd_direct<DT, 2, true, 1024>(a, s);
   } else {
-    return a.d <= 2048 ? norm_fwd<DT, 1, false, 0, 256>(a, s)
-           : a.d <= 8192 ? norm_fwd<DT, 1, false, 0, 1024>(a, s) : norm_fwd<DT, 2, false, 0, 1024>(a, s);
+    return a.d <= 2048   ? norm_fwd_direct<DT, 1, false, 256>(a, s)
+           : a.d <= 8192 ? norm_fwd_direct<DT, 1, false, 1024>(a, s)
+                         : norm_fwd_direct<DT, 2, false, 1024>(a, s);
   }
 }
 template <int DT, bool VEC>
 cudaError_t norm_bwd_width(const NormBwdArgs& a, cudaStream_t s) {
   if constexpr (VEC) {
-    const int tensors = a.dres != nullptr ? 3 : 2;
-    auto fits = [&](int vpt, int threads, int depth) {
-      return ring_bytes(team_of(a.d, vpt, threads, a.T), vpt, DT, tensors, depth) <= kSmemMost;
-    };
-    if (a.d <= 512) return norm_bwd<DT, 1, true, 3, 512>(a, s);
-    if (a.d <= 8192) {
-      if (fits(2, 512, 3)) return norm_bwd<DT, 2, true, 3, 512>(a, s);
-      return norm_bwd<DT, 2, true, 2, 512>(a, s);
-    }
-    return norm_bwd<DT, 2, true, 0, 1024>(a, s);
+    constexpr int kDepth = DT == TW_F32 ? 2 : 3;
+    if (a.d <= 1024) return norm_bwd_ring<DT, 64, kDepth>(a, s);
+    if (a.d <= 2048) return norm_bwd_ring<DT, 128, kDepth>(a, s);
+    if (a.d <= 4096) return norm_bwd_ring<DT, 256, kDepth>(a, s);
+    if (a.d <= 8192) return norm_bwd_ring<DT, 512, kDepth>(a, s);
+    return norm_bwd_direct<DT, 2, true, 1024>(a, s);
   } else {
-    return a.d <= 4096 ? norm_bwd<DT, 1, false, 0, 512>(a, s)
-           : a.d <= 8192 ? norm_bwd<DT, 1, false, 0, 1024>(a, s) : norm_bwd<DT, 2, false, 0, 1024>(a, s);
+    return a.d <= 4096   ? norm_bwd_direct<DT, 1, false, 512>(a, s)
+           : a.d <= 8192 ? norm_bwd_direct<DT, 1, false, 1024>(a, s)
+                         : norm_bwd_direct<DT, 2, false, 1024>(a, s);
   }
 }
 

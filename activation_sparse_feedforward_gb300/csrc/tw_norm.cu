@@ -35,9 +35,9 @@ struct RowMap {
   using S = typename Elem<DT>::S;
   static constexpr int NE = 8 * VPT, NP = NE / 2;
   static constexpr int E = VEC ? Elem<DT>::E : 1, NV = NE / E;  // elements of a vector, vectors
-  int d, tid;
-  TW_DEV RowMap(int d_, int tid_) : d(d_), tid(tid_) {}
-  static TW_DEV int tpr() { return TPR > 0 ? TPR : blockDim.x; }
+  int d, tid, tpr_;
+  TW_DEV RowMap(int d_, int tid_, int tpr) : d(d_), tid(tid_), tpr_(tpr) {}
+  TW_DEV int tpr() const { return TPR > 0 ? TPR : tpr_; }
   TW_DEV int col(int i) const { return (i / E * tpr() + tid) * E + i % E; }
   TW_DEV bool has(int i) const { return col(i / E * E) < d; }  // a vector is in the row whole or not at all
 
@@ -119,12 +119,14 @@ struct RowMap {
   }
 };
 
+constexpr int kMaxTeams = 15;  // named barriers 1..15
+
 // Sum over a team's threads, the same bits in each of them. `red` holds 32 values; a
 // caller alternates between two of them, so that one barrier per sum is enough.
-TW_DEV float team_sum(float v, float* red, int team, int tpr) {
+TW_DEV float team_sum(float v, float* red, int team, int tpr, int tid) {
   v = warp_sum(v);
   if (tpr == 32) return v;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = tpr >> 5;
+  const int lane = tid & 31, warp = tid >> 5, warps = tpr >> 5;
   if (lane == 0) red[warp] = v;
   team_barrier(team + 1, tpr);
   if (warps > 8) return warp_sum(lane < warps ? red[lane] : 0.f);
@@ -132,14 +134,14 @@ TW_DEV float team_sum(float v, float* red, int team, int tpr) {
   for (int w = 1; w < warps; ++w) v += red[w];
   return v;
 }
-TW_DEV float2 team_sum2(float a, float b, float2* red, int team, int tpr) {
+TW_DEV float2 team_sum2(float a, float b, float2* red, int team, int tpr, int tid) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
     b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
   }
   if (tpr == 32) return make_float2(a, b);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = tpr >> 5;
+  const int lane = tid & 31, warp = tid >> 5, warps = tpr >> 5;
   if (lane == 0) red[warp] = make_float2(a, b);
   team_barrier(team + 1, tpr);
   if (warps > 8) {
@@ -151,7 +153,6 @@ TW_DEV float2 team_sum2(float a, float b, float2* red, int team, int tpr) {
   return v;
 }
 
-constexpr int kMaxTeams = 15;  // named barriers 1..15
 
 // A thread's places in its team's ring: DEPTH rows of up to three tensors, NV vectors of
 // 16 bytes each (the thread's chunks of 8 elements). DEPTH 0: no ring.
@@ -185,12 +186,12 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 3 : 1) norm_fwd_kernel(con
   extern __shared__ uint4 smem[];
   __shared__ float red[2][kMaxTeams][32];
   pdl_enter();
-  const int tid = threadIdx.x, tpr = M::tpr(), team = threadIdx.y, teams = TPR > 0 ? MAXT / TPR : blockDim.y;
+  const int tid = threadIdx.x, tpr = TPR > 0 ? TPR : blockDim.x, team = threadIdx.y, teams = TPR > 0 ? MAXT / TPR : blockDim.y;
   const int stride = gridDim.x * teams;
   int row = blockIdx.x * teams + team;
-  const M m(a.d, tid);
+  const M m(a.d, tid, tpr);
   auto at = [](const void* p, int64_t ld, int r) { return static_cast<const S*>(p) + static_cast<size_t>(r) * ld; };
-  const RowMap<DT, VPT, true, TPR> mv(a.d, tid);
+  const RowMap<DT, VPT, true, TPR> mv(a.d, tid, tpr);
   const Ring<DT, VPT, DEPTH, TPR> ring(smem, team, a.res != nullptr ? 2 : 1, mv);
   auto fetch = [&](int stage, int r) {
     if (r < a.T) {
@@ -226,7 +227,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 3 : 1) norm_fwd_kernel(con
     float2 s = v[0];
 #pragma unroll
     for (int i = 1; i < NP; ++i) s = add2(s, v[i]);
-    const float mean = team_sum(s.x + s.y, red[0][team], team, tpr) * inv_d;
+    const float mean = team_sum(s.x + s.y, red[0][team], team, tpr, tid) * inv_d;
     if constexpr (DEPTH > 0) {  // the row has left its places
       fetch(stage, row + DEPTH * stride);
       stage = stage + 1 == DEPTH ? 0 : stage + 1;
@@ -236,7 +237,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 3 : 1) norm_fwd_kernel(con
       v[i] = m.keep(i, add2(v[i], both(-mean)));
       q = fma2(v[i], v[i], q);
     });
-    const float rstd = rsqrtf(team_sum(q.x + q.y, red[1][team], team, tpr) * inv_d + a.eps);
+    const float rstd = rsqrtf(team_sum(q.x + q.y, red[1][team], team, tpr, tid) * inv_d + a.eps);
 #pragma unroll
     for (int i = 0; i < NP; ++i) v[i] = fma2(mul2(v[i], both(rstd)), w[i], b[i]);
     m.store(static_cast<S*>(a.y) + r * a.ldy, v);
@@ -255,12 +256,12 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwdArgs a) {
   extern __shared__ uint4 smem[];  // the ring; then [2][d] fp32, the teams' column sums joined in order
   __shared__ float2 red[2][kMaxTeams][32];
   pdl_enter();
-  const int tid = threadIdx.x, tpr = M::tpr(), team = threadIdx.y, teams = TPR > 0 ? MAXT / TPR : blockDim.y;
+  const int tid = threadIdx.x, tpr = TPR > 0 ? TPR : blockDim.x, team = threadIdx.y, teams = TPR > 0 ? MAXT / TPR : blockDim.y;
   const int stride = gridDim.x * teams;
   int row = blockIdx.x * teams + team;
-  const M m(a.d, tid);
+  const M m(a.d, tid, tpr);
   auto at = [](const void* p, int64_t ld, int r) { return static_cast<const S*>(p) + static_cast<size_t>(r) * ld; };
-  const RowMap<DT, VPT, true, TPR> mv(a.d, tid);
+  const RowMap<DT, VPT, true, TPR> mv(a.d, tid, tpr);
   const Ring<DT, VPT, DEPTH, TPR> ring(smem, team, a.dres != nullptr ? 3 : 2, mv);
   auto fetch = [&](int stage, int r) {
     if (r < a.T) {
@@ -300,7 +301,7 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwdArgs a) {
       c1 = add2(c1, g[i]);
       c2 = fma2(g[i], x[i], c2);
     });
-    const float2 c = team_sum2(c1.x + c1.y, c2.x + c2.y, red[flip][team], team, tpr);
+    const float2 c = team_sum2(c1.x + c1.y, c2.x + c2.y, red[flip][team], team, tpr, tid);
     if constexpr (DEPTH > 0) {  // the row has left its places
       fetch(stage, row + DEPTH * stride);
       stage = stage + 1 == DEPTH ? 0 : stage + 1;
@@ -345,6 +346,81 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwdArgs a) {
       out[c] = team == 0 ? p : acc[c] + p;
       out[a.d + c] = team == 0 ? q : acc[a.d + c] + q;
     });
+}
+
+// The backward of a few rows in one launch. The sums over rows need the saved statistics
+// only, not the rows' c1 and c2, so they are not kept waiting for them: the first row_ctas
+// CTAs take dx, a row a team, and the others 256 columns each, whose rows they read once
+// more (from L2) over 16 warps, joined in order.
+constexpr int kFewThreads = 512, kFewWarps = kFewThreads / 32, kFewColumns = 256;
+
+template <int DT, int VPT, bool VEC>
+__global__ void __launch_bounds__(kFewThreads) norm_bwd_few_kernel(const NormBwdArgs a, int tpr, int row_ctas) {
+  using S = typename Elem<DT>::S;
+  __shared__ float2 red[kMaxTeams + 1][32];
+  __shared__ float sums[kFewWarps][2 * kFewColumns];
+  pdl_enter();
+  auto at = [](const void* p, int64_t ld, int r) { return static_cast<const S*>(p) + static_cast<size_t>(r) * ld; };
+  if (static_cast<int>(blockIdx.x) < row_ctas) {
+    using M = RowMap<DT, VPT, VEC, 0>;
+    const int team = threadIdx.x / tpr, teams = min(kFewThreads / tpr, kMaxTeams);
+    const int row = blockIdx.x * teams + team;
+    if (team >= teams || row >= a.T) return;
+    const M m(a.d, threadIdx.x - team * tpr, tpr);
+    float2 x[M::NP], g[M::NP], w[M::NP];
+    m.load(at(a.x, a.ldx, row), x);
+    m.load(at(a.dy, a.lddy, row), g);
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    m.weight(a.w, a.wtype, 1.f, w);
+    float2 c1 = both(0.f), c2 = both(0.f);
+    m.each([&](int i) {
+      x[i] = m.keep(i, mul2(add2(x[i], both(-mean)), both(rstd)));
+      g[i] = mul2(g[i], w[i]);
+      c1 = add2(c1, g[i]);
+      c2 = fma2(g[i], x[i], c2);
+    });
+    if (a.dres != nullptr) m.load(at(a.dres, a.lddres, row), w);
+    const float2 c = team_sum2(c1.x + c1.y, c2.x + c2.y, red[team], team, tpr, m.tid);
+    const float inv_d = 1.f / static_cast<float>(a.d);
+    const float2 k1 = both(-c.x * inv_d), k2 = both(-c.y * inv_d);
+#pragma unroll
+    for (int i = 0; i < M::NP; ++i) {
+      g[i] = mul2(add2(g[i], fma2(x[i], k2, k1)), both(rstd));
+      if (a.dres != nullptr) g[i] = add2(g[i], w[i]);
+    }
+    m.store(static_cast<S*>(a.dx) + static_cast<size_t>(row) * a.lddx, g);
+    return;
+  }
+  using M = RowMap<DT, 1, VEC, 32>;
+  const int first = (blockIdx.x - row_ctas) * kFewColumns, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const M m(a.d - first, lane, 32);
+  float2 dw[M::NP], db[M::NP];
+#pragma unroll
+  for (int i = 0; i < M::NP; ++i) dw[i] = db[i] = both(0.f);
+#pragma unroll 4
+  for (int row = warp; row < a.T; row += kFewWarps) {
+    float2 x[M::NP], g[M::NP];
+    m.load(at(a.x, a.ldx, row) + first, x);
+    m.load(at(a.dy, a.lddy, row) + first, g);
+    const float mean = a.mean[row], rstd = a.rstd[row];
+#pragma unroll
+    for (int i = 0; i < M::NP; ++i) {
+      dw[i] = fma2(g[i], mul2(add2(x[i], both(-mean)), both(rstd)), dw[i]);
+      db[i] = add2(db[i], g[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < M::NP; ++i) {
+    sums[warp][m.col(2 * i)] = dw[i].x, sums[warp][m.col(2 * i + 1)] = dw[i].y;
+    sums[warp][kFewColumns + m.col(2 * i)] = db[i].x, sums[warp][kFewColumns + m.col(2 * i + 1)] = db[i].y;
+  }
+  __syncthreads();
+  float v = 0.f;
+#pragma unroll
+  for (int k = 0; k < kFewWarps; ++k) v += sums[k][threadIdx.x];
+  const int c = first + static_cast<int>(threadIdx.x) % kFewColumns;
+  float* out = threadIdx.x < kFewColumns ? a.dw : a.db;
+  if (c < a.d && out != nullptr) out[c] = v;
 }
 
 // dw, db = the partial sums of `n` CTAs, added in a fixed order.
@@ -399,14 +475,13 @@ cudaError_t launch_norm(Kern kern, int grid, const Team& t, size_t smem, const c
 }
 
 // Rows through a ring of DEPTH: MAXT / TPR teams of TPR threads, 16 elements a thread.
-template <int DT, int TPR, int MAXT, int DEPTH>
-size_t ring_bytes(int tensors) {
-  return static_cast<size_t>(MAXT) * DEPTH * tensors * 16 * (DT == TW_F32 ? 4 : 2);
+size_t ring_bytes(int dtype, int vpt, int threads, int depth, int tensors) {
+  return static_cast<size_t>(threads) * depth * tensors * 8 * vpt * elem_size(dtype);
 }
 template <int DT, int TPR, int MAXT>
 cudaError_t norm_fwd_ring(const NormFwdArgs& a, cudaStream_t s) {
   constexpr int kTeams = MAXT / TPR;
-  const size_t smem = ring_bytes<DT, TPR, MAXT, 3>(a.res != nullptr ? 2 : 1);
+  const size_t smem = ring_bytes(DT, 2, MAXT, 3, a.res != nullptr ? 2 : 1);
   // as many CTAs as stay resident: three by registers (512 threads: one)
   const int fit = static_cast<int>(kSmemMost / (smem + 6 * 1024));
   const int per_sm = std::max(1, std::min(MAXT <= 256 ? 3 : 1, fit));
@@ -431,12 +506,12 @@ cudaError_t norm_bwd_finish(const NormBwdArgs& a, int partials, cudaStream_t s) 
 cudaError_t norm_bwd_done(cudaError_t e, const NormBwdArgs& a, int grid, cudaStream_t s) {
   return e != cudaSuccess || a.part == nullptr ? e : norm_bwd_finish(a, grid, s);
 }
-template <int DT, int TPR, int DEPTH>
+template <int DT, int VPT, int TPR, int MAXT, int DEPTH>
 cudaError_t norm_bwd_ring(const NormBwdArgs& a, cudaStream_t s) {
-  constexpr int kThreads = 512, kTeams = kThreads / TPR;
+  constexpr int kTeams = MAXT / TPR;
   const int grid = std::min({(a.T + kTeams - 1) / kTeams, device_sm_count(), kNormPartials});
-  const size_t smem = std::max(ring_bytes<DT, TPR, kThreads, DEPTH>(a.dres != nullptr ? 3 : 2), 2 * sizeof(float) * a.d);
-  return norm_bwd_done(launch_norm(norm_bwd_kernel<DT, 2, true, DEPTH, TPR, kThreads>, grid, Team{TPR, kTeams}, smem,
+  const size_t smem = std::max(ring_bytes(DT, VPT, MAXT, DEPTH, a.dres != nullptr ? 3 : 2), 2 * sizeof(float) * a.d);
+  return norm_bwd_done(launch_norm(norm_bwd_kernel<DT, VPT, true, DEPTH, TPR, MAXT>, grid, Team{TPR, kTeams}, smem,
                                    "norm_bwd", a, s), a, grid, s);
 }
 template <int DT, int VPT, bool VEC, int MAXT>
@@ -445,6 +520,22 @@ cudaError_t norm_bwd_direct(const NormBwdArgs& a, cudaStream_t s) {
   const int grid = std::min({(a.T + t.teams - 1) / t.teams, device_sm_count(), kNormPartials});
   const size_t smem = t.teams > 1 ? 2 * sizeof(float) * a.d : 0;
   return norm_bwd_done(launch_norm(norm_bwd_kernel<DT, VPT, VEC, 0, 0, MAXT>, grid, t, smem, "norm_bwd", a, s), a, grid, s);
+}
+
+// Up to so many rows: one launch (norm_bwd_few_kernel). 77 rows of 2048 bf16 take 2.7 us
+// against 8.7 in two; the two meet between 450 (512 columns) and 700 rows (8192), and at
+// 90 where single elements are loaded.
+constexpr int kFewRows = 512, kFewRowsSingly = 80;
+template <int DT, bool VEC>
+cudaError_t norm_bwd_few(const NormBwdArgs& a, cudaStream_t s) {
+  const int vpt = a.d <= 4096 ? 1 : 2;
+  const int tpr = ((a.d + 8 * vpt - 1) / (8 * vpt) + 31) / 32 * 32, teams = std::min(kFewThreads / tpr, kMaxTeams);
+  const int row_ctas = (a.T + teams - 1) / teams;
+  const int column_ctas = a.part == nullptr ? 0 : (a.d + kFewColumns - 1) / kFewColumns;
+  const cudaError_t e = launch(vpt == 1 ? norm_bwd_few_kernel<DT, 1, VEC> : norm_bwd_few_kernel<DT, 2, VEC>,
+                               dim3(row_ctas + column_ctas), dim3(kFewThreads), 0, s, a, tpr, row_ctas);
+  trace_mark(s, "norm_bwd_few");
+  return e;
 }
 
 // Teams of a power of two of threads, the least that holds the row at 16 elements a
@@ -466,12 +557,13 @@ cudaError_t norm_fwd_width(const NormFwdArgs& a, cudaStream_t s) {
 }
 template <int DT, bool VEC>
 cudaError_t norm_bwd_width(const NormBwdArgs& a, cudaStream_t s) {
+  if (a.T <= (VEC ? kFewRows : kFewRowsSingly) && a.d <= 8192) return norm_bwd_few<DT, VEC>(a, s);
   if constexpr (VEC) {
     constexpr int kDepth = DT == TW_F32 ? 2 : 3;
-    if (a.d <= 1024) return norm_bwd_ring<DT, 64, kDepth>(a, s);
-    if (a.d <= 2048) return norm_bwd_ring<DT, 128, kDepth>(a, s);
-    if (a.d <= 4096) return norm_bwd_ring<DT, 256, kDepth>(a, s);
-    if (a.d <= 8192) return norm_bwd_ring<DT, 512, kDepth>(a, s);
+    if (a.d <= 1024) return norm_bwd_ring<DT, 2, 64, 512, kDepth>(a, s);
+    if (a.d <= 2048) return norm_bwd_ring<DT, 2, 128, 512, kDepth>(a, s);
+    if (a.d <= 4096) return norm_bwd_ring<DT, 2, 256, 512, kDepth>(a, s);
+    if (a.d <= 8192) return norm_bwd_ring<DT, 2, 512, 512, kDepth>(a, s);
     return norm_bwd_direct<DT, 2, true, 1024>(a, s);
   } else {
     return a.d <= 4096   ? norm_bwd_direct<DT, 1, false, 512>(a, s)

@@ -817,7 +817,8 @@ tw_status tw_layer_norm_fwd(const void* x, int64_t ldx, const void* res, int64_t
 
 size_t tw_layer_norm_bwd_workspace_size(int T, int d) {
   if (T <= 0 || d <= 0) return 0;
-  return sizeof(float) * 2 * static_cast<size_t>(d) * static_cast<size_t>(T < tw::kNormPartials ? T : tw::kNormPartials);
+  return sizeof(float) * 2 * static_cast<size_t>(tw::norm_partial_width(d)) *
+         static_cast<size_t>(T < tw::kNormPartials ? T : tw::kNormPartials);
 }
 
 tw_status tw_layer_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const float* mean,

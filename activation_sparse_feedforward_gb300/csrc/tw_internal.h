@@ -373,13 +373,20 @@ struct NormBwdArgs {
   const float *mean, *rstd;
   void* dx;
   float *dw, *db;                 // may be null
-  float* part;                    // [kNormPartials][2][d] fp32, null when dw and db are
+  float* part;                    // [kNormPartials][2][norm_partial_width(d)] fp32, null when dw and db are
   int64_t lddy, ldx, lddres, lddx;
   int T, d;
   int dtype, wtype;
 };
 // The most CTAs whose partial sums over rows the backward keeps in its workspace.
 constexpr int kNormPartials = 512;
+// The most columns of one partial: the threads' elements for d columns, teams being powers
+// of two of threads up to 8192 columns and whole warps above.
+constexpr int norm_partial_width(int d) {
+  int w = 1024;
+  while (w < d && w < 8192) w *= 2;
+  return d <= w ? w : (d + 511) / 512 * 512;
+}
 cudaError_t launch_norm_bwd(const NormBwdArgs& a, cudaStream_t s);
 
 // ---------------------------------------------------------------- tw_logits.cu

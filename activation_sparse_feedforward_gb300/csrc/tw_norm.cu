@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwdArgs a) {
   using M = RowMap<DT, VPT, VEC, TPR>;
   using S = typename M::S;
   constexpr int NP = M::NP;
-  extern __shared__ uint4 smem[];  // the ring; then [2][d] fp32, the teams' column sums joined in order
+  extern __shared__ uint4 smem[];  // the ring; then the teams' column sums
   __shared__ float2 red[2][kMaxTeams][32];
   pdl_enter();
   const int tid = threadIdx.x, tpr = TPR > 0 ? TPR : blockDim.x, team = threadIdx.y, teams = TPR > 0 ? MAXT / TPR : blockDim.y;
@@ -320,32 +320,32 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwdArgs a) {
     mean = mean_next, rstd = rstd_next;
   }
   if (a.part == nullptr) return;
-  float* out = a.part + static_cast<size_t>(blockIdx.x) * 2 * a.d;
-  float* acc = reinterpret_cast<float*>(smem);
-  auto sums = [&](auto f) {  // f(column, dw, db) of the thread's columns
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      if (m.has(2 * i)) f(m.col(2 * i), dw[i].x, db[i].x);
-      if (m.has(2 * i + 1)) f(m.col(2 * i + 1), dw[i].y, db[i].y);
-    }
-  };
+  // The CTA's partial sums, [2][NE tpr] in the order of the threads' own elements: a
+  // column order would have every access of a warp hit 32 banks' worth of conflicts here
+  // and 32 sectors there (it made the sums cost 8 us a call). The last kernel sorts.
+  const int width = M::NE * tpr;
+  float* out = a.part + static_cast<size_t>(blockIdx.x) * 2 * width;
+  float* acc = reinterpret_cast<float*>(smem) + team * 2 * width;
+  if (teams == 1) acc = out;
   if (DEPTH > 0) {
     cp_wait<0>();
     __syncthreads();
   }
-  for (int t = 0; t + 1 < teams; ++t) {
-    if (team == t)
-      sums([&](int c, float p, float q) {
-        acc[c] = t == 0 ? p : acc[c] + p;
-        acc[a.d + c] = t == 0 ? q : acc[a.d + c] + q;
-      });
-    __syncthreads();
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    acc[2 * i * tpr + tid] = dw[i].x;
+    acc[(2 * i + 1) * tpr + tid] = dw[i].y;
+    acc[width + 2 * i * tpr + tid] = db[i].x;
+    acc[width + (2 * i + 1) * tpr + tid] = db[i].y;
   }
-  if (team == teams - 1)
-    sums([&](int c, float p, float q) {
-      out[c] = team == 0 ? p : acc[c] + p;
-      out[a.d + c] = team == 0 ? q : acc[a.d + c] + q;
-    });
+  if (teams == 1) return;
+  __syncthreads();
+  acc = reinterpret_cast<float*>(smem);
+  for (int p = team * tpr + tid; p < 2 * width; p += teams * tpr) {
+    float v = acc[p];
+    for (int t = 1; t < teams; ++t) v += acc[t * 2 * width + p];
+    out[p] = v;
+  }
 }
 
 // The backward of a few rows in one launch. The sums over rows need the saved statistics
@@ -423,25 +423,25 @@ __global__ void __launch_bounds__(kFewThreads) norm_bwd_few_kernel(const NormBwd
   if (c < a.d && out != nullptr) out[c] = v;
 }
 
-// dw, db = the partial sums of `n` CTAs, added in a fixed order.
-__global__ void __launch_bounds__(512) norm_bwd_finish_kernel(const float* part, int n, int d, float* dw, float* db) {
+// dw, db = the partial sums of `n` CTAs, added in a fixed order. width, tpr, E: the order
+// of a partial's places (RowMap::col).
+__global__ void __launch_bounds__(512) norm_bwd_finish_kernel(const float* part, int n, int d, int width, int tpr, int E,
+                                                              float* dw, float* db) {
   __shared__ float s[16][33];
   pdl_enter();
-  const int c = blockIdx.x * 32 + threadIdx.x;
+  const int p = blockIdx.x * 32 + threadIdx.x;
   float v = 0.f;
-  if (c < 2 * d)
-    for (int i = threadIdx.y; i < n; i += 16) v += part[static_cast<size_t>(i) * 2 * d + c];
+#pragma unroll 4
+  for (int i = threadIdx.y; i < n; i += 16) v += part[static_cast<size_t>(i) * 2 * width + p];
   s[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
-  if (threadIdx.y != 0 || c >= 2 * d) return;
+  if (threadIdx.y != 0) return;
   v = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) v += s[i][threadIdx.x];
-  if (c < d) {
-    if (dw != nullptr) dw[c] = v;
-  } else if (db != nullptr) {
-    db[c - d] = v;
-  }
+  const int q = p < width ? p : p - width, i = q / tpr, c = (i / E * tpr + q % tpr) * E + i % E;
+  float* out = p < width ? dw : db;
+  if (c < d && out != nullptr) out[c] = v;
 }
 
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -496,30 +496,29 @@ cudaError_t norm_fwd_direct(const NormFwdArgs& a, cudaStream_t s) {
                      std::min((a.T + t.teams - 1) / t.teams, device_sm_count() * 8), t, 0, "norm_fwd", a, s);
 }
 
-cudaError_t norm_bwd_finish(const NormBwdArgs& a, int partials, cudaStream_t s) {
-  cudaError_t e = launch(norm_bwd_finish_kernel, dim3((2 * a.d + 31) / 32), dim3(32, 16), 0, s,
-                         static_cast<const float*>(a.part), partials, a.d, a.dw, a.db);
+cudaError_t norm_bwd_finish(const NormBwdArgs& a, int partials, int width, int tpr, int E, cudaStream_t s) {
+  cudaError_t e = launch(norm_bwd_finish_kernel, dim3(2 * width / 32), dim3(32, 16), 0, s,
+                         static_cast<const float*>(a.part), partials, a.d, width, tpr, E, a.dw, a.db);
   trace_mark(s, "norm_bwd_finish");
   return e;
 }
 
-cudaError_t norm_bwd_done(cudaError_t e, const NormBwdArgs& a, int grid, cudaStream_t s) {
-  return e != cudaSuccess || a.part == nullptr ? e : norm_bwd_finish(a, grid, s);
+template <int DT, int VPT, bool VEC, int DEPTH, int TPR, int MAXT>
+cudaError_t norm_bwd(const NormBwdArgs& a, const Team& t, cudaStream_t s) {
+  using M = RowMap<DT, VPT, VEC, TPR>;
+  const int grid = std::min({(a.T + t.teams - 1) / t.teams, device_sm_count(), kNormPartials}), width = M::NE * t.tpr;
+  const size_t smem = std::max(ring_bytes(DT, VPT, t.teams * t.tpr, DEPTH, a.dres != nullptr ? 3 : 2),
+                               t.teams > 1 ? 2 * sizeof(float) * t.teams * width : size_t{0});
+  const cudaError_t e = launch_norm(norm_bwd_kernel<DT, VPT, VEC, DEPTH, TPR, MAXT>, grid, t, smem, "norm_bwd", a, s);
+  return e != cudaSuccess || a.part == nullptr ? e : norm_bwd_finish(a, grid, width, t.tpr, M::E, s);
 }
 template <int DT, int VPT, int TPR, int MAXT, int DEPTH>
 cudaError_t norm_bwd_ring(const NormBwdArgs& a, cudaStream_t s) {
-  constexpr int kTeams = MAXT / TPR;
-  const int grid = std::min({(a.T + kTeams - 1) / kTeams, device_sm_count(), kNormPartials});
-  const size_t smem = std::max(ring_bytes(DT, VPT, MAXT, DEPTH, a.dres != nullptr ? 3 : 2), 2 * sizeof(float) * a.d);
-  return norm_bwd_done(launch_norm(norm_bwd_kernel<DT, VPT, true, DEPTH, TPR, MAXT>, grid, Team{TPR, kTeams}, smem,
-                                   "norm_bwd", a, s), a, grid, s);
+  return norm_bwd<DT, VPT, true, DEPTH, TPR, MAXT>(a, Team{TPR, MAXT / TPR}, s);
 }
 template <int DT, int VPT, bool VEC, int MAXT>
 cudaError_t norm_bwd_direct(const NormBwdArgs& a, cudaStream_t s) {
-  const Team t = team_of(a.d, VPT, MAXT, a.T);
-  const int grid = std::min({(a.T + t.teams - 1) / t.teams, device_sm_count(), kNormPartials});
-  const size_t smem = t.teams > 1 ? 2 * sizeof(float) * a.d : 0;
-  return norm_bwd_done(launch_norm(norm_bwd_kernel<DT, VPT, VEC, 0, 0, MAXT>, grid, t, smem, "norm_bwd", a, s), a, grid, s);
+  return norm_bwd<DT, VPT, VEC, 0, 0, MAXT>(a, team_of(a.d, VPT, MAXT, a.T), s);
 }
 
 // Up to so many rows: one launch (norm_bwd_few_kernel). 77 rows of 2048 bf16 take 2.7 us
@@ -587,7 +586,7 @@ cudaError_t launch_norm_fwd(const NormFwdArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_norm_bwd(const NormBwdArgs& a, cudaStream_t s) {
-  if (a.T == 0) return a.dw != nullptr || a.db != nullptr ? norm_bwd_finish(a, 0, s) : cudaSuccess;  // sums over no rows
+  if (a.T == 0) return a.dw != nullptr || a.db != nullptr ? norm_bwd_finish(a, 0, (a.d + 31) / 32 * 32, (a.d + 31) / 32 * 32, 1, s) : cudaSuccess;  // sums over no rows
   const int dt = a.dtype;
   const bool vec = a.d % 8 == 0 && on16(a.x) && on16(a.dy) && on16(a.dres) && on16(a.dx) && on16(a.w) &&
                    stride16(a.ldx, dt) && stride16(a.lddy, dt) && stride16(a.lddres, dt) && stride16(a.lddx, dt);

@@ -306,6 +306,14 @@ TW_DEV float teacher_logit(const DistillArgs& a, size_t e) {
                                                                                   : value_at<TW_F16>(a.t_val, e);
 }
 
+// What a row is to learn, beside its list.
+struct Target {
+  bool some;              // the teacher has mass
+  float p_rest, lp_rest;  // P and log2 P of the rest
+  int label;
+  float up;               // the upstream gradient
+};
+
 // The rare part of the marking, by the whole CTA: entries that found -inf at their token.
 // The lowest of those whose token no other entry took owns it (its logit is masked);
 // the others learn the logit from the owner.
@@ -385,82 +393,100 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillArgs 
   extern __shared__ uint4 smem[];
   __shared__ float4 stats[kMaxCluster * kWarps];
   __shared__ float shares[kMaxCluster * kWarps];
+  __shared__ Target target;
   __shared__ int label_entry;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = blockIdx.x % cluster;
   const size_t row = blockIdx.x / cluster;
   const int K = a.K;
-  // the row's list, entry k filled by thread k % kThreads: the token (-2 - token where the entry
-  // does not own its place in this CTA's slice), log2 P, P, and z at the token (until the
-  // marking: the teacher's logit)
+  // the row's list: the token (after the marking -2 - token where the entry does not own
+  // its place in this CTA's slice), log2 P, P, and z at the token (until the marking: the
+  // teacher's logit)
   int* l_idx = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(smem) + slice_bytes);
   float* l_lp = reinterpret_cast<float*>(l_idx + K);
   float* l_p = l_lp + K;
   float* l_z = l_p + K;
   pdl_enter();
-  if (cluster > 1) cluster_arrive();  // waited for before the first push: every CTA has started
+  if (cluster > 1) cluster_arrive_relaxed();  // waited for before the first push: every CTA has started
 
-  // the small loads go first: behind the slice's they would wait for all of it
+  // Warp 0 takes the row's target while the slice is on its way: its loads go before the
+  // slice's, and the other warps keep out of its way (all of them taking it for
+  // themselves cost 1 us a row in issue slots).
   const float c0 = kLog2e / a.temperature;
-  int label = a.labels != nullptr ? a.labels[row] : -1;
-  const float t_rest = a.t_rest != nullptr ? a.t_rest[row] : neg_inf_f();
-  const float up = a.scale * (a.dloss != nullptr ? a.dloss[row] : 1.f);
   const size_t list = row * K;
-  int i_first = -1;
-  float t_first = neg_inf_f();
-  if (tid < K) i_first = a.t_idx[list + tid], t_first = teacher_logit(a, list + tid);
   const S* z = static_cast<const S*>(a.z) + row * a.ldz;
+  int label = -1, i_first = -1;
+  float t_rest = neg_inf_f(), up = 1.f, t_first = neg_inf_f();
+  if (warp == 0) {
+    if (a.labels != nullptr) label = a.labels[row];
+    if (a.t_rest != nullptr) t_rest = a.t_rest[row];
+    if (a.dloss != nullptr) up = a.dloss[row];
+    if (lane < K) i_first = a.t_idx[list + lane], t_first = teacher_logit(a, list + lane);
+  }
   Slice<DT> sl(z, a.V, rank, cluster, smem);
-  if (tid == 0 && row + ahead < static_cast<size_t>(a.N)) {
-    const Part<DT> next(z + ahead * a.ldz, a.V, rank, cluster);
-    if (next.hi > next.lo) prefetch_l2(next.at(next.lo), 16u * (next.hi - next.lo));
-  }
-
-  if (label < -1 || label >= a.V) {
-    if (tid == 0) raise_status(a.status, TW_EINVAL);
-    label = -1;
-  }
-  for (int k = tid; k < K; k += kThreads) {
-    int i = k == tid ? i_first : a.t_idx[list + k];
-    float t = k == tid ? t_first : teacher_logit(a, list + k);
-    if (i < 0 || i >= a.V) {
-      if (i != -1) raise_status(a.status, TW_EINVAL);
-      i = -1;
-      t = neg_inf_f();
+  if (warp == 0) {
+    if (label < -1 || label >= a.V) {
+      if (lane == 0) raise_status(a.status, TW_EINVAL);
+      label = -1;
     }
-    l_idx[k] = i;
-    l_z[k] = t > neg_inf_f() ? fmaxf(t / a.temperature, -FLT_MAX) : t;  // a finite logit stays one
-  }
-
-  // the teacher's distribution over its list and the rest, by every warp for itself
-  float p_rest = 0.f, lp_rest = neg_inf_f();
-  bool some = false;
-  if (K > 0 || a.t_rest != nullptr) {
-    __syncthreads();
-    float tm = t_rest, ts = 0.f;
-    for (int k = lane; k < K; k += 32) tm = fmaxf(tm, l_z[k]);
-    tm = base_of(warp_max(tm));
-    for (int k = lane; k < K; k += 32) ts += exp_of(l_z[k], tm, kLog2e);
-    ts = warp_sum(ts) + exp_of(t_rest, tm, kLog2e);
-    some = ts != 0.f;  // NaN counts as some
-    if (some) {
-      const float inv = 1.f / ts, l2 = log2f(ts);
-      for (int k = tid; k < K; k += kThreads) {
-        const float t = (l_z[k] - tm) * kLog2e;
-        l_p[k] = exp2_fast(t) * inv;
-        l_lp[k] = t - l2;
+    float tm = t_rest;
+    for (int k = lane; k < K; k += 32) {
+      int i = k == lane ? i_first : a.t_idx[list + k];
+      float t = k == lane ? t_first : teacher_logit(a, list + k);
+      if (i < 0 || i >= a.V) {
+        if (i != -1) raise_status(a.status, TW_EINVAL);
+        i = -1;
+        t = neg_inf_f();
       }
-      p_rest = exp_of(t_rest, tm, kLog2e) * inv;
-      lp_rest = (t_rest - tm) * kLog2e - l2;
+      if (t > neg_inf_f()) t = fmaxf(t / a.temperature, -FLT_MAX);  // a finite logit stays one
+      l_idx[k] = i;
+      l_z[k] = t;
+      tm = fmaxf(tm, t);
+    }
+    tm = base_of(warp_max(tm));
+    float ts = 0.f;
+    for (int k = lane; k < K; k += 32) {
+      const float e = exp_of(l_z[k], tm, kLog2e);
+      l_p[k] = e;
+      ts += e;
+    }
+    const float e_rest = exp_of(t_rest, tm, kLog2e);
+    ts = warp_sum(ts) + e_rest;
+    const float inv = 1.f / ts, l2 = log2f(ts);
+    for (int k = lane; k < K; k += 32) {
+      l_p[k] *= inv;
+      l_lp[k] = (l_z[k] - tm) * kLog2e - l2;
+    }
+    if (lane == 0) {
+      target.some = ts != 0.f;  // NaN counts as some
+      target.p_rest = target.some ? e_rest * inv : 0.f;
+      target.lp_rest = (t_rest - tm) * kLog2e - l2;
+      target.label = label;
+      target.up = up * a.scale;
+      label_entry = -1;
     }
   }
-  if (tid == 0) label_entry = -1;
+  // the lists of a row that a later CTA takes: cold, their loads were the longest step
+  // before the sums
+  if (rank == 0 && warp == kWarps - 1 && row + ahead < static_cast<size_t>(a.N)) {
+    const size_t e = (row + ahead) * K;
+    const int size = a.t_dtype == TW_F32 ? 4 : 2;
+    for (int k = lane * 32; k < K; k += 32 * 32) {
+      prefetch_line(a.t_idx + e + k);
+      prefetch_line(static_cast<const uint8_t*>(a.t_val) + (e + k) * size);
+    }
+    if (lane == 0 && a.t_rest != nullptr) prefetch_line(a.t_rest + row + ahead);
+    if (lane == 0 && a.labels != nullptr) prefetch_line(a.labels + row + ahead);
+    if (lane == 0 && a.dloss != nullptr) prefetch_line(a.dloss + row + ahead);
+  }
 
   // Listed tokens leave the row: an entry takes the token's logit and puts -inf in its
   // place. Whoever finds -inf there comes second (a token listed twice), or the logit was
   // masked: owners() sorts that out.
   cp_wait<0>();
   __syncthreads();
+  label = target.label;
+  const bool some = target.some;
   bool dup = false;
   if (some) {
     for (int k = tid; k < K; k += kThreads) {
@@ -538,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillArgs 
         const float p = l_p[k];
         if (i >= 0 && sl.element(i) != nullptr && p != 0.f) share += p * (l_lp[k] - ((l_z[k] - b) * c0 - l2));
       }
-      if (rank == 0 && tid == 0 && p_rest != 0.f) share += p_rest * (lp_rest - (log2f(st.rest) - l2));
+      if (rank == 0 && tid == 0 && target.p_rest != 0.f) share += target.p_rest * (target.lp_rest - (log2f(st.rest) - l2));
       share *= f;
     }
     if (holds_label && tid == 0) share += a.ce_weight * (log2f(s1) - (z_label - b) * kLog2e);
@@ -555,10 +581,10 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillArgs 
   if (a.dz != nullptr) {
     S* dz = static_cast<S*>(a.dz) + row * a.lddz;
     const bool zero = nothing || total == 0.f;
-    const float gk = up * a.kd_weight * a.temperature;
-    const float gc = label >= 0 ? up * a.ce_weight : 0.f;
+    const float gk = target.up * a.kd_weight * a.temperature;
+    const float gc = label >= 0 ? target.up * a.ce_weight : 0.f;
     float u = some ? gk / total : 0.f;  // factor of 2^(c0 (z - M)) on unlisted tokens
-    if (p_rest != 0.f && st.rest != 0.f) u -= gk * p_rest / st.rest;
+    if (target.p_rest != 0.f && st.rest != 0.f) u -= gk * target.p_rest / st.rest;
     const float w = label >= 0 ? gc / s1 : 0.f;
     if (HARD == kNoSum) u += w;
     Scale sa(st.M, c0), sb = hard_scale<HARD>(sa);

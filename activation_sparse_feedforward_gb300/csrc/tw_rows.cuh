@@ -179,6 +179,8 @@ TW_DEV void prefetch_l2(const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 
+TW_DEV void prefetch_line(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // ------------------------------------------------------------------ reductions
 TW_DEV float warp_sum(float v) {
 #pragma unroll
@@ -213,6 +215,11 @@ TW_DEV unsigned long long ld_cluster_u64(uint32_t cluster_addr) {
 TW_DEV void cluster_arrive() {
   __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+// Arriving with nothing to show: only that this CTA has started.
+TW_DEV void cluster_arrive_relaxed() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
 TW_DEV void cluster_wait() {
   __syncwarp();

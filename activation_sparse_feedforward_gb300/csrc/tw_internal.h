@@ -406,6 +406,9 @@ struct DistillArgs {
   float temperature, kd_weight, ce_weight, scale;
 };
 cudaError_t launch_distill(const DistillArgs& a, cudaStream_t s);
+// The same with one CTA of so many threads a row (tw_distill_rows.cuh).
+cudaError_t launch_distill_rows_64(const DistillArgs& a, cudaStream_t s);
+cudaError_t launch_distill_rows_128(const DistillArgs& a, cudaStream_t s);
 
 struct LogprobArgs {
   const void* z;

@@ -1,24 +1,22 @@
 // Operators on rows of logits [N, V]: the distillation loss with its gradient, and log
 // probabilities of given tokens with the row's entropy and top alternatives.
 //
-// A row is held on chip. A cluster of 1 to 8 CTAs takes one row, each CTA a slice of it
-// in shared memory, copied there by 16-byte asynchronous copies. Every sweep over the
-// row after that (its maximum, its sums, the marking of listed tokens, the gradient)
-// reads shared memory, so HBM is read once, and a thread reads back only the vectors it
-// copied itself, so a sweep needs no barrier. The CTAs' partial statistics are joined
-// through distributed shared memory: one launch, no workspace, no atomics on results.
+//  log probabilities  One CTA a row (a cluster of up to eight where there are few rows), the
+//                     row through a ring of asynchronous copies, read once.
+//  distillation       A cluster of up to eight CTAs a row, each with a slice of it in shared
+//                     memory, so that HBM is read once. Many short rows: one small CTA a
+//                     row, which reads it a second time from L2 (tw_distill_rows.cuh).
 //
-// Softmax statistics are a maximum M of z and sums of 2^(c (z - M)), c = log2(e) /
-// temperature; two such pairs join as M = max(M1, M2), S = S1 2^(c (M1-M)) + S2 2^(c (M2-M)).
-// M is taken off before the scaling: c z alone would overflow, or lose the whole
-// exponent to rounding, where a mask is the type's lowest value. A row, slice or thread
-// with nothing but -inf has M = -inf and S = 0.
-#include <cfloat>
-
+// Bound: HBM, one read of the logits and, with a gradient, one write. Measured on one GB300
+// against the copy rate (6681 GB/s): log probabilities 8192 x 65536 bf16 with five
+// alternatives 178 us (0.90); distillation 4096 x 131072 bf16, K = 64, temperature 2, rest
+// and labels 447 us (0.72), fp32 1023 x 50011 93 us (0.66).
+//
+// Both join partial statistics through distributed shared memory: one launch, no
+// workspace, no atomics on results.
 #include <algorithm>
 
-#include "tw_internal.h"
-#include "tw_rows.cuh"
+#include "tw_logits.cuh"
 
 namespace tw {
 
@@ -32,76 +30,8 @@ constexpr int kMaxCluster = 8;
 constexpr int kParts = 8;  // per-warp or per-CTA statistics of the log probabilities, joined over eight lanes
 static_assert(kWarps <= kParts && kMaxCluster <= kParts, "one lane per part");
 static_assert(kWarps * kMaxCluster <= 64, "two lanes' worth of per-warp statistics in a cluster");
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
-TW_DEV float neg_inf_f() { return __int_as_float(0xFF800000); }
-// what to take off z: M, or 0 where there is nothing (so that -inf stays -inf)
-TW_DEV float base_of(float M) { return M == neg_inf_f() ? 0.f : M; }
-TW_DEV float exp_of(float z, float base, float c) { return exp2_fast((z - base) * c); }
-
-// over groups of W lanes
-template <int W = 32>
-TW_DEV float warp_max(float v) {
-#pragma unroll
-  for (int o = W / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-  return v;
-}
-template <int W>
-TW_DEV float group_sum(float v) {
-#pragma unroll
-  for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  return v;
-}
-
-TW_DEV float2 exp2_pair(float2 t) { return make_float2(exp2_fast(t.x), exp2_fast(t.y)); }
-TW_DEV float add_lanes(float2 v) { return v.x + v.y; }
-// v^POW, POW 2 or 4
-template <int POW>
-TW_DEV float2 power(float2 v) {
-  const float2 q = mul2(v, v);
-  return POW == 4 ? mul2(q, q) : q;
-}
-
-// ------------------------------------------------------------------ a CTA's part of a row
-// The row's address may have any element alignment: vectors are counted from the
-// 16-byte boundary at or before it, so column c sits in vector (c + lead) / E. Only the
-// row's first and last vector may reach outside it; those are read element by element,
-// with -inf outside.
-template <int DT>
-struct Part {
-  using S = typename Elem<DT>::S;
-  static constexpr int E = Elem<DT>::E;
-  const S* row;
-  int lead, V, first, n;  // n vectors from the row's vector `first`
-  int lo, hi;             // those of them that are whole: [lo, hi)
-
-  static TW_DEV int lead_of(const S* row) { return static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(S)); }
-
-  TW_DEV Part(const S* row_, int V_, int rank, int cluster) : row(row_), lead(lead_of(row_)), V(V_) {
-    const int vecs = (V + lead + E - 1) / E;
-    const int per = (vecs + cluster - 1) / cluster;
-    first = rank * per;
-    n = max(0, min(per, vecs - first));
-    lo = first == 0 && lead > 0 ? 1 : 0;
-    hi = min(n, (V + lead) / E - first);
-  }
-  // first column of the part's vector j
-  TW_DEV int col(int j) const { return (first + j) * E - lead; }
-  TW_DEV bool whole(int j) const { return j >= lo && j < hi; }
-  TW_DEV const S* at(int j) const { return row + col(j); }
-  TW_DEV uint4 edge(int j) const {
-    union {
-      S e[E];
-      uint4 w;
-    } u;
-    const int c = col(j);
-#pragma unroll
-    for (int i = 0; i < E; ++i) u.e[i] = (c + i >= 0 && c + i < V) ? row[c + i] : Elem<DT>::neg_inf();
-    return u.w;
-  }
-};
-
+// ------------------------------------------------------------------ distillation, one row per cluster
 // The same part copied to shared memory: a thread copies, and then sweeps, the whole
 // vectors lo + threadIdx.x, lo + threadIdx.x + kThreads, ...; the edges are the CTA's
 // first and last thread's.
@@ -113,7 +43,7 @@ struct Slice : Part<DT> {
   uint4* buf;
 
   TW_DEV Slice(const S* row, int V, int rank, int cluster, uint4* b) : P(row, V, rank, cluster), buf(b) {
-      uint4* dst = buf + this->lo + threadIdx.x;
+    uint4* dst = buf + this->lo + threadIdx.x;
     const uint4* src = reinterpret_cast<const uint4*>(P::at(this->lo)) + threadIdx.x;
     int j = this->lo + threadIdx.x;
 #pragma unroll 4
@@ -122,9 +52,8 @@ struct Slice : Part<DT> {
     if (last_edge()) buf[this->n - 1] = P::edge(this->n - 1);
     cp_commit();
   }
-  // whether this thread holds the slice's first (last) vector as one that is not whole
-  TW_DEV bool first_edge() const { return threadIdx.x == 0 && this->lo > 0; }
-  TW_DEV bool last_edge() const { return threadIdx.x == kThreads - 1 && this->hi < this->n && this->n > this->lo; }
+  TW_DEV bool first_edge() const { return P::template first_edge<kThreads>(); }
+  TW_DEV bool last_edge() const { return P::template last_edge<kThreads>(); }
   // the element of column c, or null when another CTA holds it
   TW_DEV S* element(int c) const {
     const int e = c + this->lead - this->first * E;
@@ -132,187 +61,23 @@ struct Slice : Part<DT> {
   }
 };
 
-// ------------------------------------------------------------------ exponentials of a sweep
-// A sweep takes 2^(c (z - m)) of many z for one m. Where c m is of ordinary size that is
-// one fused multiply-add and one exponential, 2^(c z - k) with k = c m rounded, and the
-// sweep's sums are corrected once by 2^(k - c m), whose exponent the fused operation
-// gives exactly. Past 2^20 the rounding of k would leave more than a fraction of the
-// exponent (a mask of the type's lowest value ends there), and m is taken off z first.
-struct Scale {
-  float m, c, k;
-  bool fused;
-  TW_DEV Scale(float max, float c_) : m(base_of(max)), c(c_), k(m * c_) { fused = fabsf(k) < 1048576.f; }
-  TW_DEV float shift() const { return fused ? -fmaf(m, c, -k) : 0.f; }  // k - c m
-  // what the exponent c z - k grows by when `to` is used in place of this one
-  TW_DEV float move(const Scale& to) const { return fmaf(m - to.m, c, shift() - to.shift()); }
-  template <bool FUSED>
-  TW_DEV float2 exponent(float2 z) const {
-    if (FUSED) return fma2(z, both(c), both(-k));
-    return mul2(add2(z, both(-m)), both(c));
-  }
-};
-
-constexpr int kBatch = 4;  // vectors a thread takes at a time
-
-// f(j, all) for the thread's vectors j, j + kThreads, ... of [lo, hi) in batches of
-// kBatch; all: a constant, whether the whole batch is below hi.
-struct Yes { static constexpr bool value = true; };
-struct No { static constexpr bool value = false; };
-template <class F>
-TW_DEV void in_batches(int lo, int hi, F f) {
-  int j = lo + threadIdx.x;
-  for (; j + (kBatch - 1) * kThreads < hi; j += kBatch * kThreads) f(j, Yes());
-  if (j < hi) f(j, No());
-}
-
-// A thread's online sums over its vectors, in batches. The reference m follows the
-// running maximum, but only when that is more than kSlack above it (in nats at
-// temperature 1): sums are rescaled a few times a row, and no term exceeds e^kSlack.
-constexpr float kSlack = 8.f;
-
-template <int DT>
-struct Running {
-  typename Elem<DT>::Max top;
-  float limit = -__builtin_huge_valf();
-  // Takes a batch into the maximum; true when the reference has to
-  // move to it.
-  TW_DEV bool grow(const uint4 (&r)[kBatch], float slack) {
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) top.add(r[i]);
-    const float m = top.get();
-    if (!(m > limit)) return false;
-    limit = m + slack;
-    return true;
-  }
-};
-// a batch of nothing but -inf
-template <int DT>
-TW_DEV uint4 no_vector() {
-  constexpr uint32_t v = DT == TW_F32 ? 0xFF800000u : DT == TW_BF16 ? 0xFF80FF80u : 0xFC00FC00u;
-  return make_uint4(v, v, v, v);
-}
-
-// ------------------------------------------------------------------ distillation
-// The hard-label term wants sums of e^z at temperature 1. How a kernel gets them beside
-// the sums of p = e^(z / temperature): HARD = kNoSum where there are no labels or the
-// temperature is 1; 2 or 4 where the temperature is that: p^2 or p^4, products in place
-// of a second exponential an element in each sweep (4096 x 131072 bf16 at temperature 2:
-// the exponentials alone would keep their unit busy for three quarters of the floor);
-// kOwnSum at any other temperature.
-constexpr int kNoSum = 0, kOwnSum = 1;
-
-struct DistillStat {
-  float M, rest, list;  // sums at the temperature over the unlisted and the listed tokens
-  float s1;             // at temperature 1 over all (not with kNoSum)
-};
-
-// The scale at temperature 1 beside `a` at the temperature. (c is log2(e) / HARD, an
-// exact division, so HARD times c, k and the shift are exact too.)
-template <int HARD>
-TW_DEV Scale hard_scale(const Scale& a) {
-  Scale b(a.m, kLog2e);
-  if (HARD == 2 || HARD == 4) b.k = HARD * a.k, b.fused = a.fused;
-  return b;
-}
-
-
-// Joins one DistillStat per lane (M = -inf, sums 0 in unused lanes); all lanes get it.
-template <int HARD>
-TW_DEV DistillStat join(DistillStat a, float c0) {
-  DistillStat r;
-  r.M = warp_max(a.M);
-  const float base = base_of(r.M), f0 = exp_of(a.M, base, c0);
-  r.rest = warp_sum(a.rest * f0);
-  r.list = warp_sum(a.list * f0);
-  r.s1 = HARD != kNoSum ? warp_sum(a.s1 * exp_of(a.M, base, kLog2e)) : 0.f;
-  return r;
-}
-template <int HARD>
-TW_DEV DistillStat join_two(DistillStat a, DistillStat b, float c0) {
-  DistillStat r;
-  r.M = fmaxf(a.M, b.M);
-  const float base = base_of(r.M), fa = exp_of(a.M, base, c0), fb = exp_of(b.M, base, c0);
-  r.rest = a.rest * fa + b.rest * fb;
-  r.list = a.list * fa + b.list * fb;
-  r.s1 = HARD != kNoSum ? a.s1 * exp_of(a.M, base, kLog2e) + b.s1 * exp_of(b.M, base, kLog2e) : 0.f;
-  return r;
-}
-
-// The thread's own vectors of the slice in one sweep: their largest element m, and the
-// sums of their exponentials relative to it at the scales c0 and log2(e).
-template <int DT, int HARD, bool FUSED>
-TW_DEV void add_exps(const uint4 (&r)[kBatch], const Scale& a, const Scale& b, float2& s0, float2& s1) {
-  using El = Elem<DT>;
-#pragma unroll
-  for (int i = 0; i < kBatch; ++i) {
-    float2 v[El::E / 2];
-    El::pairs(r[i], v);
-#pragma unroll
-    for (int e = 0; e < El::E / 2; ++e) {
-      const float2 p = exp2_pair(a.exponent<FUSED>(v[e]));
-      s0 = add2(s0, p);
-      if (HARD == kOwnSum) s1 = add2(s1, exp2_pair(b.exponent<FUSED>(v[e])));
-      if (HARD == 2) s1 = fma2(p, p, s1);
-      if (HARD == 4) {
-        const float2 q = mul2(p, p);
-        s1 = fma2(q, q, s1);
-      }
-    }
-  }
-}
+// The thread's own vectors of the slice in one sweep.
 template <int DT, int HARD>
-TW_DEV void own_sums(const Slice<DT>& sl, float c0, float& m, float& sum0, float& sum1) {
-  Running<DT> run;
-  const float slack = kSlack * fminf(1.f, kLog2e / c0);
-  float2 s0 = both(0.f), s1 = both(0.f);
-  Scale a(neg_inf_f(), c0), b(neg_inf_f(), kLog2e);
-  bool fused = true, some = false;
-  auto batch = [&](const uint4 (&r)[kBatch]) {
-    if (run.grow(r, slack)) {
-      Scale a2(run.top.get(), c0), b2 = hard_scale<HARD>(a2);
-      a2.fused = b2.fused = fused = a2.fused && b2.fused;
-      s0 = some ? mul2(s0, both(exp2_fast(a.move(a2)))) : both(0.f);
-      if (HARD != kNoSum) s1 = some ? mul2(s1, both(exp2_fast(b.move(b2)))) : both(0.f);
-      a = a2, b = b2, some = true;
-    }
-    if (fused)
-      add_exps<DT, HARD, true>(r, a, b, s0, s1);
-    else
-      add_exps<DT, HARD, false>(r, a, b, s0, s1);
-  };
-  in_batches(sl.lo, sl.hi, [&](int j, auto all) {
+TW_DEV DistillStat own_sums(const Slice<DT>& sl, float c0) {
+  Sums<DT, HARD> sums(c0);
+  in_batches<kThreads>(sl.lo, sl.hi, [&](int j, auto all) {
     uint4 r[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) r[i] = all.value || j + i * kThreads < sl.hi ? sl.buf[j + i * kThreads] : no_vector<DT>();
-    batch(r);
+    sums.add(r);
   });
   if (sl.first_edge() || sl.last_edge()) {
     const uint4 r[kBatch] = {sl.first_edge() ? sl.buf[0] : no_vector<DT>(), sl.last_edge() ? sl.buf[sl.n - 1] : no_vector<DT>(),
                              no_vector<DT>(), no_vector<DT>()};
-    batch(r);
+    sums.add(r);
   }
-  m = run.top.get();
-  const float base = base_of(m);
-  sum0 = add_lanes(s0) * exp2_fast(fmaf(a.m - base, c0, a.shift()));
-  sum1 = HARD != kNoSum ? add_lanes(s1) * exp2_fast(fmaf(b.m - base, kLog2e, b.shift())) : 0.f;
+  return sums.get();
 }
-
-template <int DT>
-TW_DEV float value_at(const void* p, size_t i) {
-  return Elem<DT>::get(static_cast<const typename Elem<DT>::S*>(p)[i]);
-}
-TW_DEV float teacher_logit(const DistillArgs& a, size_t e) {
-  return a.t_dtype == TW_F32 ? value_at<TW_F32>(a.t_val, e) : a.t_dtype == TW_BF16 ? value_at<TW_BF16>(a.t_val, e)
-                                                                                  : value_at<TW_F16>(a.t_val, e);
-}
-
-// What a row is to learn, beside its list.
-struct Target {
-  bool some;              // the teacher has mass
-  float p_rest, lp_rest;  // P and log2 P of the rest
-  int label;
-  float up;               // the upstream gradient
-};
 
 // The rare part of the marking, by the whole CTA: entries that found -inf at their token.
 // The lowest of those whose token no other entry took owns it (its logit is masked);
@@ -341,21 +106,6 @@ TW_DEV void owners(const Slice<DT>& sl, int K, int* l_idx, float* l_z, int label
   __syncthreads();
 }
 
-// u 2^(c0 (z - M)) (+ w 2^(log2(e) (z - M))) of one vector
-template <int DT, int HARD, bool FUSED>
-TW_DEV uint4 gradient(const uint4& r, const Scale& a, const Scale& b, float u, float w) {
-  using El = Elem<DT>;
-  float2 v[El::E / 2];
-  El::pairs(r, v);
-#pragma unroll
-  for (int e = 0; e < El::E / 2; ++e) {
-    const float2 z = v[e], p = exp2_pair(a.exponent<FUSED>(z));
-    v[e] = mul2(both(u), p);
-    if (HARD == kOwnSum) v[e] = fma2(both(w), exp2_pair(b.exponent<FUSED>(z)), v[e]);
-    if (HARD == 2 || HARD == 4) v[e] = fma2(both(w), power<HARD>(p), v[e]);
-  }
-  return El::pack_pairs(v);
-}
 // f of each of the thread's vectors, stored at its columns of dz.
 template <int DT, class F>
 TW_DEV void store_slice(const Slice<DT>& sl, typename Elem<DT>::S* dz, F f) {
@@ -371,7 +121,7 @@ TW_DEV void store_slice(const Slice<DT>& sl, typename Elem<DT>::S* dz, F f) {
   };
   if (Part<DT>::lead_of(dz) == sl.lead) {  // the same alignment as z's row
     uint4* out = reinterpret_cast<uint4*>(dz + sl.col(0));
-    in_batches(sl.lo, sl.hi, [&](int j, auto all) {
+    in_batches<kThreads>(sl.lo, sl.hi, [&](int j, auto all) {
 #pragma unroll
       for (int i = 0; i < kBatch; ++i)
         if (all.value || j + i * kThreads < sl.hi) out[j + i * kThreads] = f(sl.buf[j + i * kThreads]);
@@ -383,9 +133,9 @@ TW_DEV void store_slice(const Slice<DT>& sl, typename Elem<DT>::S* dz, F f) {
   if (sl.last_edge()) singly(sl.n - 1);
 }
 
-// One row per cluster. What the CTAs tell each other is pushed into the receiver's shared
-// memory before a cluster barrier: every warp's statistics to every CTA, every warp's
-// share of the loss to rank 0.
+// One row per cluster, its slices in shared memory. What the CTAs tell each other is pushed
+// into the receiver's shared memory before a cluster barrier: every warp's statistics to
+// every CTA, every warp's share of the loss to rank 0.
 template <int DT, int HARD>
 __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillArgs a, int cluster, int slice_bytes, int ahead) {
   using El = Elem<DT>;
@@ -399,175 +149,73 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillArgs 
   const int rank = blockIdx.x % cluster;
   const size_t row = blockIdx.x / cluster;
   const int K = a.K;
-  // the row's list: the token (after the marking -2 - token where the entry does not own
-  // its place in this CTA's slice), log2 P, P, and z at the token (until the marking: the
-  // teacher's logit)
-  int* l_idx = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(smem) + slice_bytes);
-  float* l_lp = reinterpret_cast<float*>(l_idx + K);
-  float* l_p = l_lp + K;
-  float* l_z = l_p + K;
+  const List l(reinterpret_cast<uint8_t*>(smem) + slice_bytes, K);
   pdl_enter();
   if (cluster > 1) cluster_arrive_relaxed();  // waited for before the first push: every CTA has started
 
-  // Warp 0 takes the row's target while the slice is on its way: its loads go before the
-  // slice's, and the other warps keep out of its way (all of them taking it for
-  // themselves cost 1 us a row in issue slots).
+  // Warp 0 takes the row's target while the slice is on its way; the other warps keep out
+  // of its way (all of them taking it for themselves cost 1 us a row in issue slots).
   const float c0 = kLog2e / a.temperature;
-  const size_t list = row * K;
   const S* z = static_cast<const S*>(a.z) + row * a.ldz;
-  int label = -1, i_first = -1;
-  float t_rest = neg_inf_f(), up = 1.f, t_first = neg_inf_f();
+  TargetLoads loads;
+  if (warp == 0) loads.load(a, row);
+  const Slice<DT> sl(z, a.V, rank, cluster, smem);
   if (warp == 0) {
-    if (a.labels != nullptr) label = a.labels[row];
-    if (a.t_rest != nullptr) t_rest = a.t_rest[row];
-    if (a.dloss != nullptr) up = a.dloss[row];
-    if (lane < K) i_first = a.t_idx[list + lane], t_first = teacher_logit(a, list + lane);
+    loads.finish(a, row, l, &target);
+    if (lane == 0) label_entry = -1;
   }
-  Slice<DT> sl(z, a.V, rank, cluster, smem);
-  if (warp == 0) {
-    if (label < -1 || label >= a.V) {
-      if (lane == 0) raise_status(a.status, TW_EINVAL);
-      label = -1;
-    }
-    float tm = t_rest;
-    for (int k = lane; k < K; k += 32) {
-      int i = k == lane ? i_first : a.t_idx[list + k];
-      float t = k == lane ? t_first : teacher_logit(a, list + k);
-      if (i < 0 || i >= a.V) {
-        if (i != -1) raise_status(a.status, TW_EINVAL);
-        i = -1;
-        t = neg_inf_f();
-      }
-      if (t > neg_inf_f()) t = fmaxf(t / a.temperature, -FLT_MAX);  // a finite logit stays one
-      l_idx[k] = i;
-      l_z[k] = t;
-      tm = fmaxf(tm, t);
-    }
-    tm = base_of(warp_max(tm));
-    float ts = 0.f;
-    for (int k = lane; k < K; k += 32) {
-      const float e = exp_of(l_z[k], tm, kLog2e);
-      l_p[k] = e;
-      ts += e;
-    }
-    const float e_rest = exp_of(t_rest, tm, kLog2e);
-    ts = warp_sum(ts) + e_rest;
-    const float inv = 1.f / ts, l2 = log2f(ts);
-    for (int k = lane; k < K; k += 32) {
-      l_p[k] *= inv;
-      l_lp[k] = (l_z[k] - tm) * kLog2e - l2;
-    }
-    if (lane == 0) {
-      target.some = ts != 0.f;  // NaN counts as some
-      target.p_rest = target.some ? e_rest * inv : 0.f;
-      target.lp_rest = (t_rest - tm) * kLog2e - l2;
-      target.label = label;
-      target.up = up * a.scale;
-      label_entry = -1;
-    }
-  }
-  // the lists of a row that a later CTA takes: cold, their loads were the longest step
-  // before the sums
-  if (rank == 0 && warp == kWarps - 1 && row + ahead < static_cast<size_t>(a.N)) {
-    const size_t e = (row + ahead) * K;
-    const int size = a.t_dtype == TW_F32 ? 4 : 2;
-    for (int k = lane * 32; k < K; k += 32 * 32) {
-      prefetch_line(a.t_idx + e + k);
-      prefetch_line(static_cast<const uint8_t*>(a.t_val) + (e + k) * size);
-    }
-    if (lane == 0 && a.t_rest != nullptr) prefetch_line(a.t_rest + row + ahead);
-    if (lane == 0 && a.labels != nullptr) prefetch_line(a.labels + row + ahead);
-    if (lane == 0 && a.dloss != nullptr) prefetch_line(a.dloss + row + ahead);
-  }
+  if (rank == 0 && warp == kWarps - 1 && row + ahead < static_cast<size_t>(a.N)) prefetch_target(a, row + ahead);
 
   // Listed tokens leave the row: an entry takes the token's logit and puts -inf in its
   // place. Whoever finds -inf there comes second (a token listed twice), or the logit was
   // masked: owners() sorts that out.
   cp_wait<0>();
   __syncthreads();
-  label = target.label;
+  const int label = target.label;
   const bool some = target.some;
   bool dup = false;
   if (some) {
     for (int k = tid; k < K; k += kThreads) {
-      const int i = l_idx[k];
+      const int i = l.idx[k];
       S* s = i >= 0 ? sl.element(i) : nullptr;
       const float v = s != nullptr ? El::get(El::exchange(s, El::neg_inf())) : 0.f;
-      l_z[k] = v;
+      l.z[k] = v;
       const bool owner = s != nullptr && v != neg_inf_f();
       if (s != nullptr && !owner) dup = true;
-      if (!owner) l_idx[k] = -2 - i;  // padding: -1
+      if (!owner) l.idx[k] = -2 - i;  // padding: -1
       if (owner && i == label) label_entry = k;
     }
     dup = __syncthreads_or(dup);
-    if (dup) owners(sl, K, l_idx, l_z, label, &label_entry);
+    if (dup) owners(sl, K, l.idx, l.z, label, &label_entry);
   }
 
   // the row's statistics
-  DistillStat st;
-  {
-    float m;
-    own_sums<DT, HARD>(sl, c0, m, st.rest, st.s1);
-    if (some) {  // the list's tokens that this thread owns join its maximum
-      const float was = m;
-      for (int k = tid; k < K; k += kThreads)
-        if (l_idx[k] >= 0) m = fmaxf(m, l_z[k]);
-      if (m != was) {
-        st.rest *= exp_of(was, base_of(m), c0);
-        if (HARD != kNoSum) st.s1 *= exp_of(was, base_of(m), kLog2e);
-      }
-    }
-    st.M = m;
-    st.list = 0.f;
-    const float b = base_of(m);
-    if (some)
-      for (int k = tid; k < K; k += kThreads)
-        if (l_idx[k] >= 0) {
-          st.list += exp_of(l_z[k], b, c0);
-          if (HARD != kNoSum) st.s1 += exp_of(l_z[k], b, kLog2e);
-        }
-    st = join<HARD>(st, c0);
-    const float4 mine = make_float4(st.M, st.rest, st.list, st.s1);
-    if (cluster > 1) {
-      cluster_wait();
-      if (lane < cluster) st_cluster_v4(peer_smem_addr(&stats[rank * kWarps + warp], lane), mine);
-      cluster_barrier();
-    } else {
-      if (lane == 0) stats[warp] = mine;
-      __syncthreads();
-    }
-    const DistillStat none = {neg_inf_f(), 0.f, 0.f, 0.f};
-    const int parts = cluster * kWarps;
-    auto part = [&](int i) {
-      if (i >= parts) return none;
-      const float4 s = stats[i];
-      return DistillStat{s.x, s.y, s.z, s.w};
-    };
-    st = part(lane);
-    if (parts > 32) st = join_two<HARD>(st, part(lane + 32), c0);
-    st = join<HARD>(st, c0);
+  DistillStat st = own_sums<DT, HARD>(sl, c0);
+  if (some) add_listed<HARD>(st, c0, K, kThreads, l.idx, l.z);
+  st = join<HARD>(st, c0);
+  const float4 mine = make_float4(st.M, st.rest, st.list, st.s1);
+  if (cluster > 1) {
+    cluster_wait();
+    if (lane < cluster) st_cluster_v4(peer_smem_addr(&stats[rank * kWarps + warp], lane), mine);
+    cluster_barrier();
+  } else {
+    if (lane == 0) stats[warp] = mine;
+    __syncthreads();
   }
-  const float total = st.rest + st.list;
-  const float b = base_of(st.M);
-  const float s1 = HARD != kNoSum ? st.s1 : total;
-  const bool nothing = !some && label < 0;  // no target: loss and gradient are 0 whatever the logits
-  const bool holds_label = label >= 0 && sl.element(label) != nullptr;
-  const float z_label = !holds_label ? 0.f : label_entry >= 0 ? l_z[label_entry] : El::get(*sl.element(label));
+  const int parts = cluster * kWarps;
+  auto part = [&](int i) {
+    const float4 s = i < parts ? stats[i] : make_float4(neg_inf_f(), 0.f, 0.f, 0.f);
+    return DistillStat{s.x, s.y, s.z, s.w};
+  };
+  st = part(lane);
+  if (parts > 32) st = join_two<HARD>(st, part(lane + 32), c0);
+  st = join<HARD>(st, c0);
 
-  // the loss, in units of log2: each entry's term by the thread that found it in its slice
+  const bool holds_label = label >= 0 && sl.element(label) != nullptr;
+  const float z_label = !holds_label ? 0.f : label_entry >= 0 ? l.z[label_entry] : El::get(*sl.element(label));
   if (a.loss != nullptr) {
-    float share = 0.f;
-    if (some) {
-      const float l2 = log2f(total), f = a.kd_weight * a.temperature * a.temperature;
-      for (int k = tid; k < K; k += kThreads) {
-        const int i = l_idx[k] >= 0 ? l_idx[k] : -2 - l_idx[k];
-        const float p = l_p[k];
-        if (i >= 0 && sl.element(i) != nullptr && p != 0.f) share += p * (l_lp[k] - ((l_z[k] - b) * c0 - l2));
-      }
-      if (rank == 0 && tid == 0 && target.p_rest != 0.f) share += target.p_rest * (target.lp_rest - (log2f(st.rest) - l2));
-      share *= f;
-    }
-    if (holds_label && tid == 0) share += a.ce_weight * (log2f(s1) - (z_label - b) * kLog2e);
+    float share = loss_share<HARD>(a, st, c0, l, target, kThreads, rank == 0 && tid == 0, holds_label && tid == 0, z_label,
+                                   [&](int i) { return sl.element(i) != nullptr; });
     share = warp_sum(share);
     if (lane == 0) {
       if (cluster > 1)
@@ -580,44 +228,14 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillArgs 
 
   if (a.dz != nullptr) {
     S* dz = static_cast<S*>(a.dz) + row * a.lddz;
-    const bool zero = nothing || total == 0.f;
-    const float gk = target.up * a.kd_weight * a.temperature;
-    const float gc = label >= 0 ? target.up * a.ce_weight : 0.f;
-    float u = some ? gk / total : 0.f;  // factor of 2^(c0 (z - M)) on unlisted tokens
-    if (target.p_rest != 0.f && st.rest != 0.f) u -= gk * target.p_rest / st.rest;
-    const float w = label >= 0 ? gc / s1 : 0.f;
-    if (HARD == kNoSum) u += w;
-    Scale sa(st.M, c0), sb = hard_scale<HARD>(sa);
-    const bool fused = sa.fused && sb.fused;
-    const float uf = fused ? u * exp2_fast(sa.shift()) : u, wf = fused ? w * exp2_fast(sb.shift()) : w;
-    if (zero)
-      store_slice<DT>(sl, dz, [](const uint4&) { return make_uint4(0, 0, 0, 0); });
-    else if (fused)
-      store_slice<DT>(sl, dz, [&](const uint4& r) { return gradient<DT, HARD, true>(r, sa, sb, uf, wf); });
-    else
-      store_slice<DT>(sl, dz, [&](const uint4& r) { return gradient<DT, HARD, false>(r, sa, sb, uf, wf); });
+    const Gradient<HARD> g(a, st, c0, target);
+    g.template with<DT>([&](auto f) { store_slice<DT>(sl, dz, f); });
     __syncthreads();  // the listed tokens and the label overwrite what the sweep stored
-    if (some && !zero) {
-      for (int k = tid; k < K; k += kThreads) {
-        const int i = l_idx[k];
-        if (i < 0) continue;
-        float p = l_p[k];
-        if (dup) {  // add up, in list order, every entry that names the same token
-          p = 0.f;
-          for (int q = 0; q < K; ++q)
-            if (l_idx[q] == i || l_idx[q] == -2 - i) p += l_p[q];
-        }
-        float d = gk * (exp_of(l_z[k], b, c0) / total - p);
-        if (label >= 0) d += w * exp_of(l_z[k], b, kLog2e);
-        if (i == label) d -= gc;
-        dz[i] = El::put(d);
-      }
+    if (some && !g.zero) {
+      for (int k = tid; k < K; k += kThreads)
+        if (l.idx[k] >= 0) dz[l.idx[k]] = El::put(g.listed(l, K, k, label, dup));
     }
-    if (tid == 0 && holds_label && label_entry < 0 && !zero) {
-      float d = u * exp_of(z_label, b, c0) - gc;
-      if (HARD != kNoSum) d = fmaf(w, exp_of(z_label, b, kLog2e), d);
-      dz[label] = El::put(d);
-    }
+    if (tid == 0 && holds_label && label_entry < 0 && !g.zero) dz[label] = El::put(g.at_label(z_label));
   }
 
   if (cluster > 1)
@@ -625,10 +243,10 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillArgs 
   else if (a.dz == nullptr)
     __syncthreads();
   if (rank == 0 && warp == 0 && a.loss != nullptr) {
-    const int parts = cluster * kWarps;
     float loss = (lane < parts ? shares[lane] : 0.f) + (lane + 32 < parts ? shares[lane + 32] : 0.f);
     loss = kLn2 * warp_sum(loss);
-    if (lane == 0) a.loss[row] = nothing ? 0.f : total == 0.f ? __int_as_float(0x7F800000) : loss;
+    const float total = st.rest + st.list;
+    if (lane == 0) a.loss[row] = !some && label < 0 ? 0.f : total == 0.f ? __int_as_float(0x7F800000) : loss;
   }
 }
 
@@ -699,8 +317,8 @@ template <int DT, class F>
 TW_DEV void each_vector(const Part<DT>& p, F f) {
 #pragma unroll 4
   for (int j = p.lo + threadIdx.x; j < p.hi; j += kThreads) f(*reinterpret_cast<const uint4*>(p.at(j)), j);
-  if (threadIdx.x == 0 && p.lo > 0) f(p.edge(0), 0);
-  if (threadIdx.x == kThreads - 1 && p.hi < p.n && p.n > p.lo) f(p.edge(p.n - 1), p.n - 1);
+  if (p.template first_edge<kThreads>()) f(p.edge(0), 0);
+  if (p.template last_edge<kThreads>()) f(p.edge(p.n - 1), p.n - 1);
 }
 
 // The K largest keys of the CTA's part, descending, into top (0 past the finite ones).
@@ -730,8 +348,8 @@ TW_DEV void part_top(const Part<DT>& p, uint32_t high, int K, Key* cand, Key* to
       }
   };
   if (high != 0 && high >= thr) above[atomicAdd(count + 1, 1)] = static_cast<uint16_t>(tid);
-  if (tid == 0 && p.lo > 0) collect(p.edge(0), 0);
-  if (tid == kThreads - 1 && p.hi < p.n && p.n > p.lo) collect(p.edge(p.n - 1), p.n - 1);
+  if (p.template first_edge<kThreads>()) collect(p.edge(0), 0);
+  if (p.template last_edge<kThreads>()) collect(p.edge(p.n - 1), p.n - 1);
   __syncthreads();
   const int rounds = (p.hi - p.lo + kThreads - 1) / kThreads, work = count[1] * rounds;
   for (int i = tid; i < work; i += kThreads) {
@@ -783,22 +401,20 @@ TW_DEV void add_terms(const uint4& r, const Scale& a, float2& s, float2& w) {
   }
 }
 
-// Batches a thread has on their way, in its own places of a ring in shared memory
-// (kBatch kDepth vectors a thread: 48 KB at 256 threads, four CTAs an SM). Registers held
-// one batch ahead: 8192 x 65536 bf16 took 194 us, 333 rows of 100003 fp16 28 us.
-constexpr int kDepth = 3;
-constexpr int kRingBytes = 16 * kDepth * kBatch * kThreads;
+// Three batches a thread on their way: 48 KB, four CTAs an SM. (One batch ahead in
+// registers: 8192 x 65536 bf16 took 194 us, now 178.)
+template <int DT>
+using ProbRing = RowRing<DT, kThreads, 3>;
 
 // The thread's share of the part in one sweep: its largest element and its sums relative
 // to that.
 template <int DT>
-TW_DEV ProbStat own_probs(const Part<DT>& p, float c, uint4* ring) {
+TW_DEV ProbStat own_probs(const Part<DT>& p, float c, const ProbRing<DT>& ring) {
   Running<DT> run;
   const float slack = kSlack * fminf(1.f, kLog2e / c);
   float2 s = both(0.f), w = both(0.f);
   Scale a(neg_inf_f(), c);
   bool some = false;
-  const int tid = threadIdx.x;
   auto batch = [&](const uint4 (&r)[kBatch]) {
     if (run.grow(r, slack)) {
       const Scale to(run.top.get(), c);
@@ -816,44 +432,13 @@ TW_DEV ProbStat own_probs(const Part<DT>& p, float c, uint4* ring) {
       for (int i = 0; i < kBatch; ++i) add_terms<DT, false>(r[i], a, s, w);
     }
   };
-  const uint4* src = reinterpret_cast<const uint4*>(p.at(0));
-  constexpr int kStep = kBatch * kThreads, kStage = kStep;  // vectors from a batch, a stage to the next
-  auto load = [&](uint4* to, int j) {
-    if (j + kStep - kThreads < p.hi) {
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) cp_async16(to + i * kThreads, src + j + i * kThreads);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        if (j + i * kThreads < p.hi) cp_async16(to + i * kThreads, src + j + i * kThreads);
-    }
-    cp_commit();
-  };
-  int j = p.lo + tid;
-  uint4 *const begin = ring + tid, *at = begin;
-#pragma unroll
-  for (int d = 0; d < kDepth; ++d) load(begin + d * kStage, j + d * kStep);
-  for (; j < p.hi; j += kStep) {
-    cp_wait<kDepth - 1>();
-    uint4 r[kBatch];
-    if (j + kStep - kThreads < p.hi) {
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) r[i] = at[i * kThreads];
-    } else {
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) r[i] = j + i * kThreads < p.hi ? at[i * kThreads] : no_vector<DT>();
-    }
-    batch(r);
-    load(at, j + kDepth * kStep);
-    at = at == begin + (kDepth - 1) * kStage ? begin : at + kStage;
-  }
-  cp_wait<0>();
+  ring.sweep(p, [&](const uint4 (&r)[kBatch], int) { batch(r); });
   if (p.lo > 0 || p.hi < p.n) {  // the edges: one vector of the first thread, one of the last
     uint4 r[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) r[i] = no_vector<DT>();
-    if (tid == 0 && p.lo > 0) r[0] = p.edge(0);
-    if (tid == kThreads - 1 && p.hi < p.n && p.n > p.lo) r[1] = p.edge(p.n - 1);
+    if (p.template first_edge<kThreads>()) r[0] = p.edge(0);
+    if (p.template last_edge<kThreads>()) r[1] = p.edge(p.n - 1);
     batch(r);
   }
   ProbStat st;
@@ -895,7 +480,9 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
     t_first = a.tokens[row * a.n_tokens + lane];
     if (t_first >= 0 && t_first < a.V) z_first = El::get(z[t_first]);
   }
-  ProbStat st = own_probs(part, c, smem);
+  const ProbRing<DT> ring(smem);
+  ring.start(part);
+  ProbStat st = own_probs(part, c, ring);
   const float mine = st.M;
   st = join<32>(st, c);
   if (lane == 0) wstat[warp] = st;
@@ -975,15 +562,8 @@ struct RowShape {
   int cluster, part_bytes;
 };
 
-// The most 16-byte vectors a row of V elements covers, at any alignment.
-int row_vectors(int V, int dtype) {
-  const int E = dtype == TW_F32 ? 4 : 8;
-  return (V + 2 * E - 2) / E;
-}
-
 // CTAs a row (1 to 8): as few as keep a part at `most` bytes, and, while all rows
-// together make fewer than `fill` CTAs, as many as keep it at `least`. Eight vectors a
-// thread.
+// together make fewer than `fill` CTAs, as many as keep it at `least`.
 RowShape row_shape(int64_t N, int V, int dtype, int most, int64_t fill, int least) {
   const int64_t bytes = 16 * static_cast<int64_t>(row_vectors(V, dtype));
   auto parts = [&](int64_t size) { return (bytes + size - 1) / size; };
@@ -993,6 +573,20 @@ RowShape row_shape(int64_t N, int V, int dtype, int most, int64_t fill, int leas
   r.cluster = static_cast<int>(std::max(few, many));
   r.part_bytes = 16 * ((row_vectors(V, dtype) + r.cluster - 1) / r.cluster);
   return r;
+}
+
+// Whether, and with CTAs of how many threads, one small CTA takes a row and reads it a
+// second time from L2 for the gradient (tw_distill_rows.cuh). Short rows are bound by the
+// steps between their sweeps, so many small CTAs an SM beat a few that hold rows on chip;
+// long ones would not stay in L2. Fraction of the copy rate at K = 64, temperature 2, with
+// rest and labels, 64 threads / 128 threads / one row per cluster: rows of 8 KB (bf16)
+// 0.41 / 0.31 / 0.16, 16 KB 0.55 / 0.47 / 0.30, 32 KB 0.67 / 0.63 / 0.48, 48 KB 0.69 / 0.72 /
+// 0.60; fp32 of 48 KB 0.72 / 0.91 / 0.85, 64 KB 0.67 / 0.81 / 0.85. At 32 KB a cluster is
+// faster up to two rows an SM, and 64 threads slower up to sixteen.
+int distill_rows_threads(const DistillArgs& a) {
+  const int64_t kb = static_cast<int64_t>(row_vectors(a.V, a.dtype)) / 64, sms = device_sm_count();
+  if (kb <= 24 && a.N >= 16 * sms) return 64;
+  return kb <= 52 && a.N >= 2 * sms ? 128 : 0;
 }
 
 template <class... KArgs, class... Args>
@@ -1008,18 +602,21 @@ cudaError_t launch_rows(void (*kern)(KArgs...), int64_t N, const RowShape& r, si
   return e;
 }
 
-// A slice of at most 72 KB keeps three CTAs on an SM, so that one's copies run under
-// the others' sweeps. Fewer rows than SMs: more CTAs a row, down to 8 KB each.
+// One row per cluster: slices of at most 72 KB keep three CTAs on an SM, so that one's
+// copies run under the others' sweeps. Fewer rows than SMs: more CTAs a row, down to 8 KB
+// each.
 template <int DT>
 cudaError_t distill(const DistillArgs& a, cudaStream_t s) {
   const RowShape r = row_shape(a.N, a.V, DT, 72 * 1024, device_sm_count(), 8 * 1024);
-  const size_t smem = r.part_bytes + 16 * static_cast<size_t>(a.K);
+  const size_t smem = r.part_bytes + kListBytes * static_cast<size_t>(a.K);
   const int ahead = 3 * device_sm_count() / r.cluster;
   auto run = [&](auto kern) { return launch_rows(kern, a.N, r, smem, "distill", s, a, r.cluster, r.part_bytes, ahead); };
-  if (a.labels == nullptr || a.temperature == 1.f) return run(distill_kernel<DT, kNoSum>);
-  if (a.temperature == 2.f) return run(distill_kernel<DT, 2>);
-  if (a.temperature == 4.f) return run(distill_kernel<DT, 4>);
-  return run(distill_kernel<DT, kOwnSum>);
+  switch (hard_form(a)) {
+    case kNoSum: return run(distill_kernel<DT, kNoSum>);
+    case 2: return run(distill_kernel<DT, 2>);
+    case 4: return run(distill_kernel<DT, 4>);
+    default: return run(distill_kernel<DT, kOwnSum>);
+  }
 }
 
 // A row needs no place on chip: one CTA takes it, more where there are few rows. Two
@@ -1028,7 +625,7 @@ cudaError_t distill(const DistillArgs& a, cudaStream_t s) {
 template <int DT>
 cudaError_t logprobs(const LogprobArgs& a, cudaStream_t s) {
   const RowShape r = row_shape(a.N, a.V, DT, 1 << 30, 4 * device_sm_count(), 8 * 1024);
-  const size_t smem = std::max<size_t>(kRingBytes, a.K > 0 ? sizeof(Key) * kCandidates : 0);
+  const size_t smem = std::max<size_t>(ProbRing<DT>::kBytes, a.K > 0 ? sizeof(Key) * kCandidates : 0);
   return launch_rows(logprobs_kernel<DT>, a.N, r, smem, "token_logprobs", s, a, r.cluster);
 }
 
@@ -1036,6 +633,10 @@ cudaError_t logprobs(const LogprobArgs& a, cudaStream_t s) {
 
 cudaError_t launch_distill(const DistillArgs& a, cudaStream_t s) {
   if (a.N == 0) return cudaSuccess;
+  switch (distill_rows_threads(a)) {
+    case 64: return launch_distill_rows_64(a, s);
+    case 128: return launch_distill_rows_128(a, s);
+  }
   return a.dtype == TW_F32 ? distill<TW_F32>(a, s) : a.dtype == TW_BF16 ? distill<TW_BF16>(a, s) : distill<TW_F16>(a, s);
 }
 

@@ -108,7 +108,7 @@ def _check_distill(loss, dz, z, idx, val, rest, labels, tau, kd, ce, dloss=None,
         assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[0], got[bad][0], rd[bad][0], tol[bad][0])
 
 
-VS = [(3, 1), (3, 2), (4, 7), (5, 33), (4, 1000), (7, 4097), (3, 32000), (2, 50011), (200, 300)]
+VS = [(3, 1), (3, 2), (4, 7), (5, 33), (4, 1000), (7, 4097), (3, 32000), (2, 50011), (310, 300)]
 
 
 @pytest.mark.parametrize("N,V", VS)
@@ -140,8 +140,11 @@ def test_distill_matches_oracle(N, V, dtype, tau, kd, ce, with_rest):
 
 
 @pytest.mark.parametrize("dtype,V,N", [(F32, 131071, 2), (BF16, 262144, 2), (F32, 393216, 1), (F16, 100003, 30),
-                                       (BF16, 60000, 200)])
-def test_distill_long_rows_in_clusters(dtype, V, N):
+                                       (BF16, 60000, 200), (BF16, 100003, 170), (F32, 60011, 160), (F16, 4099, 400),
+                                       (F32, 131070, 153), (BF16, 8191, 2500), (F32, 13001, 320), (F16, 26000, 305)])
+def test_distill_long_rows_and_many(dtype, V, N):
+    """Sizes on both sides of the choice between a cluster and one CTA a row, and of the
+    latter's sizes; more rows than CTAs stay."""
     rng = np.random.default_rng(V)
     K = 64
     z = _logits(rng, N, V, dtype)
@@ -166,9 +169,10 @@ def test_distill_list_lengths_and_teacher_types(K):
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("pad,off,out_pad", [(5, 0, 5), (0, 3, 0), (3, 1, 4), (8, 8, 16)])
-def test_distill_strided_rows_write_their_own_columns_only(dtype, pad, off, out_pad):
+@pytest.mark.parametrize("N", [9, 310, 2500])
+def test_distill_strided_rows_write_their_own_columns_only(dtype, pad, off, out_pad, N):
     rng = np.random.default_rng(pad + off)
-    N, V, K = 9, 1237, 5
+    V, K = 1237, 5
     z = _logits(rng, N, V, dtype, pad, off)
     idx, val = _teacher(rng, z, K)
     buf = torch.full((N, V + out_pad + off), 9.0, dtype=dtype, device="cuda")
@@ -179,7 +183,7 @@ def test_distill_strided_rows_write_their_own_columns_only(dtype, pad, off, out_
     assert (buf[:, :off] == 9).all() and (buf[:, off + V:] == 9).all()
 
 
-@pytest.mark.parametrize("dtype,V,N", [(BF16, 777, 5), (F32, 90000, 3)])
+@pytest.mark.parametrize("dtype,V,N", [(BF16, 777, 5), (F32, 90000, 3), (BF16, 777, 500), (F32, 9001, 310), (BF16, 777, 2600), (BF16, 90001, 155)])
 def test_distill_gradient_in_place(dtype, V, N):
     rng = np.random.default_rng(1)
     z = _logits(rng, N, V, dtype, 3).contiguous()
@@ -206,23 +210,27 @@ def test_cross_entropy_alone():
         assert (loss.double() - ref).abs().max().item() <= _log_tol(z, tau)
 
 
-def test_a_token_listed_twice_counts_twice():
+@pytest.mark.parametrize("N", [3, 310, 2500])
+def test_a_token_listed_twice_counts_twice(N):
     rng = np.random.default_rng(3)
-    z = _logits(rng, 3, 400, F32)
+    z = _logits(rng, N, 400, F32).contiguous()
     idx, val = _teacher(rng, z, 6, ragged=False)
     idx[0, 3] = idx[0, 1]
     idx[1, :] = idx[1, 0]
-    rest = torch.zeros(3, device="cuda")
+    idx[2, 2:] = idx[2, 1]
+    z[2, int(idx[2, 1])] = -float("inf")   # and masked
+    rest = torch.zeros(N, device="cuda")
     loss, dz, _ = tw.distill_loss(z, idx, val, rest=rest, temperature=1.5)
     _check_distill(loss, dz, z, idx, val, rest, None, 1.5, 1.0, 0.0)
 
 
-def test_masked_tokens_empty_rows_and_special_values():
+@pytest.mark.parametrize("V,tiles", [(96, 1), (96, 26), (96, 210), (13001, 1), (13001, 26), (40001, 13)])
+def test_masked_tokens_empty_rows_and_special_values(V, tiles):
     """-inf logits on and off the list, at the label, everywhere; the whole vocabulary listed
     with a rest; rows without target whose logits are NaN; NaN and +inf rows; teacher entries
     of logit -inf."""
     rng = np.random.default_rng(4)
-    N, V, K = 12, 96, 4
+    N, K = 12, 4
     inf = float("inf")
     z = _logits(rng, N, V, F32).contiguous()
     idx, val = _teacher(rng, z, K, ragged=False)
@@ -248,9 +256,14 @@ def test_masked_tokens_empty_rows_and_special_values():
     labels = torch.from_numpy(lab).cuda()
     for rest in (None, torch.from_numpy(np.r_[np.zeros(4), -inf, np.zeros(2), -inf, np.zeros(4)].astype(np.float32)).cuda()):
         for tau, kd, ce in ((1.0, 0.5, 0.5), (2.0, 0.5, 0.5), (2.0, 1.0, 0.0)):
-            loss, dz, st = tw.distill_loss(z, idx, val, rest=rest, labels=labels, temperature=tau, kd_weight=kd, ce_weight=ce)
+            many = [None if t is None else t.repeat(tiles, *[1] * (t.dim() - 1)) for t in (z, idx, val, rest, labels)]
+            loss, dz, st = tw.distill_loss(many[0], many[1], many[2], rest=many[3], labels=many[4], temperature=tau,
+                                           kd_weight=kd, ce_weight=ce)
             tw.raise_if_device_error(st)
-            _check_distill(loss, dz, z, idx, val, rest, labels, tau, kd, ce)
+            _check_distill(loss[:N], dz[:N], z, idx, val, rest, labels, tau, kd, ce)
+            for t in range(1, tiles):
+                assert torch.equal(loss[:N].nan_to_num(7.0), loss[t * N:t * N + N].nan_to_num(7.0))
+                assert torch.equal(dz[:N].nan_to_num(7.0), dz[t * N:t * N + N].nan_to_num(7.0))
     zs = _logits(rng, 2, 4, F32)
     full = torch.tensor([[3, 1, 0, 2]] * 2, dtype=torch.int32, device="cuda")
     rest = torch.tensor([-inf, 0.0], device="cuda")  # row 1: teacher mass where the student has no token
@@ -408,7 +421,7 @@ def test_logprobs_strided_rows_fewer_rows_and_no_tokens():
     assert op(z[:0], tokens[:0])[0].shape == (0, 1)
 
 
-@pytest.mark.parametrize("N,V", [(3, 131072), (64, 5000)])
+@pytest.mark.parametrize("N,V", [(3, 131072), (64, 5000), (310, 5000), (2500, 5000), (160, 70000)])
 def test_same_bits_every_time_on_another_stream_and_in_a_graph(N, V):
     rng = np.random.default_rng(9)
     z = _logits(rng, N, V, BF16)

@@ -389,14 +389,20 @@ TW_DEV void teacher_distribution(const List& l, int K, float t_rest, Target* tar
 // One warp takes a row's target: load() before the row's own loads, which would hold these
 // up, finish() while the row is on its way.
 struct TargetLoads {
-  int label = -1, i_first = -1;
-  float t_rest = neg_inf_f(), up = 1.f, t_first = neg_inf_f();
+  static constexpr int kFirst = 4;  // entries a lane loads at once: lists of up to 128
+  int label = -1, i_first[kFirst];
+  float t_rest = neg_inf_f(), up = 1.f, t_first[kFirst];
   TW_DEV void load(const DistillArgs& a, size_t row) {
     const int lane = threadIdx.x & 31;
     if (a.labels != nullptr) label = a.labels[row];
     if (a.t_rest != nullptr) t_rest = a.t_rest[row];
     if (a.dloss != nullptr) up = a.dloss[row];
-    if (lane < a.K) i_first = a.t_idx[row * a.K + lane], t_first = teacher_logit(a, row * a.K + lane);
+#pragma unroll
+    for (int n = 0; n < kFirst; ++n) {
+      const int k = lane + 32 * n;
+      i_first[n] = k < a.K ? a.t_idx[row * a.K + k] : -1;
+      t_first[n] = k < a.K ? teacher_logit(a, row * a.K + k) : 0.f;
+    }
   }
   TW_DEV void finish(const DistillArgs& a, size_t row, const List& l, Target* target) {
     const int lane = threadIdx.x & 31, K = a.K;
@@ -404,9 +410,7 @@ struct TargetLoads {
       if (lane == 0) raise_status(a.status, TW_EINVAL);
       label = -1;
     }
-    for (int k = lane; k < K; k += 32) {
-      int i = k == lane ? i_first : a.t_idx[row * K + k];
-      float t = k == lane ? t_first : teacher_logit(a, row * K + k);
+    auto entry = [&](int k, int i, float t) {
       if (i < 0 || i >= a.V) {
         if (i != -1) raise_status(a.status, TW_EINVAL);
         i = -1;
@@ -414,7 +418,11 @@ struct TargetLoads {
       }
       l.idx[k] = i;
       l.lp[k] = t > neg_inf_f() ? fmaxf(t / a.temperature, -FLT_MAX) : t;  // a finite logit stays one
-    }
+    };
+#pragma unroll
+    for (int n = 0; n < kFirst; ++n)
+      if (lane + 32 * n < K) entry(lane + 32 * n, i_first[n], t_first[n]);
+    for (int k = lane + 32 * kFirst; k < K; k += 32) entry(k, a.t_idx[row * K + k], teacher_logit(a, row * K + k));
     teacher_distribution(l, K, t_rest, target);
     if (lane == 0) {
       target->label = label;

@@ -280,9 +280,10 @@ static_assert(kMaxAlternatives * kMaxCluster <= kCandidates, "a cluster's lists 
 // top[0..K) = the K largest of cand[0..n), descending, 0 past n. Distinct keys have
 // distinct ranks: each thread counts the keys above its own. top is zeroed before; cand
 // has room for one more.
+template <int NT>
 TW_DEV void rank_select(Key* cand, int n, Key* top, int K) {
   const ulonglong2* two = reinterpret_cast<const ulonglong2*>(cand);
-  for (int i = threadIdx.x; i < n; i += kThreads) {
+  for (int i = threadIdx.x; i < n; i += NT) {
     const Key k = cand[i];
     int r = 0;
 #pragma unroll 4
@@ -313,24 +314,35 @@ TW_DEV uint32_t find_threshold(uint32_t v, int K) {
 
 // f(vector, index) for each of the thread's whole vectors, and for the edges, which the
 // CTA's first and last thread take.
-template <int DT, class F>
+template <int DT, int NT, class F>
 TW_DEV void each_vector(const Part<DT>& p, F f) {
 #pragma unroll 4
-  for (int j = p.lo + threadIdx.x; j < p.hi; j += kThreads) f(*reinterpret_cast<const uint4*>(p.at(j)), j);
-  if (p.template first_edge<kThreads>()) f(p.edge(0), 0);
-  if (p.template last_edge<kThreads>()) f(p.edge(p.n - 1), p.n - 1);
+  for (int j = p.lo + threadIdx.x; j < p.hi; j += NT) f(*reinterpret_cast<const uint4*>(p.at(j)), j);
+  if (p.template first_edge<NT>()) f(p.edge(0), 0);
+  if (p.template last_edge<NT>()) f(p.edge(p.n - 1), p.n - 1);
+}
+
+// A thread's batches of a part in chunks, whose largest elements are kept apart: the
+// alternatives are then looked for in a few chunks, not in all of a thread's vectors
+// (2048 rows of 131072 bf16 with 32 alternatives took 157 us, without any 82).
+constexpr int kChunks = 8;
+template <int DT, int NT>
+TW_DEV int chunk_batches(const Part<DT>& p) {
+  const int batches = (p.hi - p.lo + kBatch * NT - 1) / (kBatch * NT);
+  return max(1, (batches + kChunks - 1) / kChunks);
 }
 
 // The K largest keys of the CTA's part, descending, into top (0 past the finite ones).
-// A threshold that the largest elements of at least K threads reach leaves few
-// candidates, all in those threads' vectors. The whole CTA reads these once more (from
-// L2), a vector a thread: left to their owners, one lane of a warp would walk a row's
-// worth of latencies. A list that overflows (many ties, or the largest elements all with
-// few threads) falls back to K sweeps for the next largest key. high: the upper half of
-// the order of the thread's largest element, 0 when it has none; count (two zeros) and top
-// (zeros): set by the caller behind a barrier; above: room for a thread number each.
-template <int DT>
-TW_DEV void part_top(const Part<DT>& p, uint32_t high, int K, Key* cand, Key* top, uint32_t thr, int* count,
+// thr is reached by the largest elements of at least K threads, and so leaves few
+// candidates, all in the chunks of threads whose largest element reaches it. The whole CTA
+// reads these once more (from L2), a vector a thread: left to their owners, one lane of a
+// warp would walk a row's worth of latencies. A list that overflows (many ties, or the
+// largest elements all in few chunks) falls back to K sweeps for the next largest key.
+// highs: the thread's own column of its chunks' largest elements, NT apart, as upper halves
+// of their order (0: none); count (two zeros) and top (zeros): set by the caller behind a
+// barrier; above: room for a number of each chunk.
+template <int DT, int NT>
+TW_DEV void part_top(const Part<DT>& p, const uint16_t* highs, int K, Key* cand, Key* top, uint32_t thr, int* count,
                      uint16_t* above, Key* wkey) {
   using El = Elem<DT>;
   constexpr int E = El::E;
@@ -347,25 +359,31 @@ TW_DEV void part_top(const Part<DT>& p, uint32_t high, int K, Key* cand, Key* to
         if (at < kCandidates) cand[at] = key_of(v[e], p.col(j) + e);
       }
   };
-  if (high != 0 && high >= thr) above[atomicAdd(count + 1, 1)] = static_cast<uint16_t>(tid);
-  if (p.template first_edge<kThreads>()) collect(p.edge(0), 0);
-  if (p.template last_edge<kThreads>()) collect(p.edge(p.n - 1), p.n - 1);
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    const uint32_t high = highs[c * NT];
+    if (high != 0 && high >= thr) above[atomicAdd(count + 1, 1)] = static_cast<uint16_t>(c * NT + tid);
+  }
+  if (p.template first_edge<NT>()) collect(p.edge(0), 0);
+  if (p.template last_edge<NT>()) collect(p.edge(p.n - 1), p.n - 1);
   __syncthreads();
-  const int rounds = (p.hi - p.lo + kThreads - 1) / kThreads, work = count[1] * rounds;
-  for (int i = tid; i < work; i += kThreads) {
-    const int j = p.lo + above[i / rounds] + (i % rounds) * kThreads;
+  const int each = chunk_batches<DT, NT>(p) * kBatch, work = count[1] * each;
+#pragma unroll 4
+  for (int i = tid; i < work; i += NT) {
+    const int from = above[i / each];
+    const int j = p.lo + from % NT + (from / NT * each + i % each) * NT;
     if (j < p.hi) collect(*reinterpret_cast<const uint4*>(p.at(j)), j);
   }
   __syncthreads();
   const int n = *count;
   if (n <= kCandidates) {
-    rank_select(cand, n, top, K);
+    rank_select<NT>(cand, n, top, K);
     return;
   }
   Key last = ~0ull;
   for (int r = 0; r < K; ++r) {
     Key best = 0;
-    each_vector(p, [&](const uint4& w, int j) {
+    each_vector<DT, NT>(p, [&](const uint4& w, int j) {
       float v[E];
       El::unpack(w, v);
 #pragma unroll
@@ -379,7 +397,7 @@ TW_DEV void part_top(const Part<DT>& p, uint32_t high, int K, Key* cand, Key* to
     if ((tid & 31) == 0) wkey[tid >> 5] = best;
     __syncthreads();
     best = 0;
-    for (int w = 0; w < kWarps; ++w) best = max(best, wkey[w]);
+    for (int w = 0; w < NT / 32; ++w) best = max(best, wkey[w]);
     if (tid == 0) top[r] = best;
     last = best;
     __syncthreads();
@@ -401,16 +419,17 @@ TW_DEV void add_terms(const uint4& r, const Scale& a, float2& s, float2& w) {
   }
 }
 
-// Three batches a thread on their way: 48 KB, four CTAs an SM. (One batch ahead in
+// Three batches a thread on their way: 48 KB an SM's quarter. (One batch ahead in
 // registers: 8192 x 65536 bf16 took 194 us, now 178.)
-template <int DT>
-using ProbRing = RowRing<DT, kThreads, 3>;
+template <int DT, int NT>
+using ProbRing = RowRing<DT, NT, 3>;
 
 // The thread's share of the part in one sweep: its largest element and its sums relative
-// to that.
-template <int DT>
-TW_DEV ProbStat own_probs(const Part<DT>& p, float c, const ProbRing<DT>& ring) {
+// to that. highs (null: not wanted): see part_top.
+template <int DT, int NT>
+TW_DEV ProbStat own_probs(const Part<DT>& p, float c, const ProbRing<DT, NT>& ring, uint16_t* highs) {
   Running<DT> run;
+  float largest = neg_inf_f();  // of the chunks that are done
   const float slack = kSlack * fminf(1.f, kLog2e / c);
   float2 s = both(0.f), w = both(0.f);
   Scale a(neg_inf_f(), c);
@@ -432,17 +451,35 @@ TW_DEV ProbStat own_probs(const Part<DT>& p, float c, const ProbRing<DT>& ring) 
       for (int i = 0; i < kBatch; ++i) add_terms<DT, false>(r[i], a, s, w);
     }
   };
-  ring.sweep(p, [&](const uint4 (&r)[kBatch], int) { batch(r); });
+  auto high_of = [](float v) { return v > neg_inf_f() ? static_cast<uint16_t>(order_of(v) >> 16) : uint16_t{0}; };
+  int left = highs != nullptr ? chunk_batches<DT, NT>(p) : 0, chunk = 0;
+  const int per = left;
+  if (highs != nullptr) {
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) highs[c * NT] = 0;
+  }
+  ring.sweep(p, [&](const uint4 (&r)[kBatch], int) {
+    batch(r);
+    if (highs != nullptr) {  // kept as the chunk goes: the last one may be short
+      const float m = run.top.get();
+      highs[chunk * NT] = high_of(m);
+      if (--left == 0) {
+        largest = fmaxf(largest, m);
+        run.top = typename Elem<DT>::Max();
+        left = per, ++chunk;
+      }
+    }
+  });
   if (p.lo > 0 || p.hi < p.n) {  // the edges: one vector of the first thread, one of the last
     uint4 r[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) r[i] = no_vector<DT>();
-    if (p.template first_edge<kThreads>()) r[0] = p.edge(0);
-    if (p.template last_edge<kThreads>()) r[1] = p.edge(p.n - 1);
+    if (p.template first_edge<NT>()) r[0] = p.edge(0);
+    if (p.template last_edge<NT>()) r[1] = p.edge(p.n - 1);
     batch(r);
   }
   ProbStat st;
-  st.M = run.top.get();
+  st.M = fmaxf(largest, run.top.get());
   const float d = fmaf(a.m - base_of(st.M), c, a.shift()), f = exp2_fast(d);
   st.s = add_lanes(s);
   st.w = f * fmaf(st.s, d, add_lanes(w));
@@ -450,23 +487,26 @@ TW_DEV ProbStat own_probs(const Part<DT>& p, float c, const ProbRing<DT>& ring) 
   return st;
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs a, int cluster) {
+// NT threads (64, 128 or 256); 1024 / NT CTAs an SM.
+template <int DT, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const LogprobArgs a, int cluster) {
   using El = Elem<DT>;
   using S = typename El::S;
-  extern __shared__ uint4 smem[];  // the ring, then the candidates
+  constexpr int kWarps = NT / 32;
+  extern __shared__ uint4 smem[];  // the ring, then the candidates and the chunks above the threshold
   __shared__ Key top[kMaxAlternatives];
   __shared__ ProbStat wstat[kWarps], cstat;
   __shared__ Key wkey[kWarps];
-  __shared__ uint16_t above[kThreads];
+  __shared__ uint16_t highs[kChunks * NT];
   __shared__ int count[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = blockIdx.x % cluster;
   const size_t row = blockIdx.x / cluster;
   const int K = a.K;
   Key* cand = reinterpret_cast<Key*>(smem);
+  uint16_t* above = reinterpret_cast<uint16_t*>(cand + kCandidates);
   if (tid < 2) count[tid] = 0;
-  for (int k = tid; k < K; k += kThreads) top[k] = 0;
+  for (int k = tid; k < K; k += NT) top[k] = 0;
   pdl_enter();
 
   const S* z = static_cast<const S*>(a.z) + row * a.ldz;
@@ -480,9 +520,9 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
     t_first = a.tokens[row * a.n_tokens + lane];
     if (t_first >= 0 && t_first < a.V) z_first = El::get(z[t_first]);
   }
-  const ProbRing<DT> ring(smem);
+  const ProbRing<DT, NT> ring(smem);
   ring.start(part);
-  ProbStat st = own_probs(part, c, ring);
+  ProbStat st = own_probs<DT, NT>(part, c, ring, K > 0 ? highs + tid : nullptr);
   const float mine = st.M;
   st = join<32>(st, c);
   if (lane == 0) wstat[warp] = st;
@@ -495,9 +535,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
     st = join<kParts>(lane % kParts < kWarps ? wstat[lane % kParts] : none, c);
     if (lane == 0) cstat = st;
   }
-  if (K > 0) {
-    part_top<DT>(part, high, K, cand, top, thr, count, above, wkey);
-  }
+  if (K > 0) part_top<DT, NT>(part, highs + tid, K, cand, top, thr, count, above, wkey);
   if (cluster > 1) {
     cluster_barrier();
     if (rank == 0) {
@@ -516,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
         Key least = 0;
         for (int r = 0; r < cluster; ++r) least = max(least, ld_cluster_u64(peer_smem_addr(top + K - 1, r)));
         __syncthreads();
-        for (int i = tid; i < cluster * K; i += kThreads) {
+        for (int i = tid; i < cluster * K; i += NT) {
           const Key k = ld_cluster_u64(peer_smem_addr(top + i % K, i / K));
           if (k != 0 && k >= least) cand[atomicAdd(count, 1)] = k;
         }
@@ -525,9 +563,9 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
     cluster_barrier();  // every list has been read: the CTAs may leave, rank 0 may overwrite its own
     if (rank != 0) return;
     if (K > 0) {
-      for (int k = tid; k < K; k += kThreads) top[k] = 0;
+      for (int k = tid; k < K; k += NT) top[k] = 0;
       __syncthreads();
-      rank_select(cand, count[0], top, K);
+      rank_select<NT>(cand, count[0], top, K);
     }
   }
   if (K > 0) __syncthreads();
@@ -590,12 +628,12 @@ int distill_rows_threads(const DistillArgs& a) {
 }
 
 template <class... KArgs, class... Args>
-cudaError_t launch_rows(void (*kern)(KArgs...), int64_t N, const RowShape& r, size_t smem, const char* label,
-                        cudaStream_t s, Args... args) {
+cudaError_t launch_rows(void (*kern)(KArgs...), int64_t N, const RowShape& r, int threads, size_t smem,
+                        const char* label, cudaStream_t s, Args... args) {
   cudaError_t e = cudaSuccess;
   if (smem > 40 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(N * r.cluster)), block(kThreads);
+  const dim3 grid(static_cast<unsigned>(N * r.cluster)), block(threads);
   e = r.cluster == 1 ? launch(kern, grid, block, smem, s, args...)
                      : launch_clustered(kern, grid, block, smem, r.cluster, s, args...);
   trace_mark(s, label);
@@ -610,7 +648,7 @@ cudaError_t distill(const DistillArgs& a, cudaStream_t s) {
   const RowShape r = row_shape(a.N, a.V, DT, 72 * 1024, device_sm_count(), 8 * 1024);
   const size_t smem = r.part_bytes + kListBytes * static_cast<size_t>(a.K);
   const int ahead = 3 * device_sm_count() / r.cluster;
-  auto run = [&](auto kern) { return launch_rows(kern, a.N, r, smem, "distill", s, a, r.cluster, r.part_bytes, ahead); };
+  auto run = [&](auto kern) { return launch_rows(kern, a.N, r, kThreads, smem, "distill", s, a, r.cluster, r.part_bytes, ahead); };
   switch (hard_form(a)) {
     case kNoSum: return run(distill_kernel<DT, kNoSum>);
     case 2: return run(distill_kernel<DT, 2>);
@@ -619,14 +657,28 @@ cudaError_t distill(const DistillArgs& a, cudaStream_t s) {
   }
 }
 
-// A row needs no place on chip: one CTA takes it, more where there are few rows. Two
-// threads an alternative, so that a threshold which K threads reach is passed by few
-// elements.
+template <int DT, int NT>
+cudaError_t logprobs(const LogprobArgs& a, const RowShape& r, cudaStream_t s) {
+  const size_t lists = a.K > 0 ? sizeof(Key) * kCandidates + sizeof(uint16_t) * kChunks * NT : 0;
+  return launch_rows(logprobs_kernel<DT, NT>, a.N, r, NT, std::max<size_t>(ProbRing<DT, NT>::kBytes, lists),
+                     "token_logprobs", s, a, r.cluster);
+}
+
+// A row needs no place on chip: one CTA takes it, more where there are few rows. Many
+// short rows: smaller CTAs, as many more of them an SM, so that the steps after one row's
+// sweep run under the others' sweeps; but with few threads an alternative the threshold
+// lets many elements pass. Fraction of the copy rate with 5 alternatives (32), 64 / 128 /
+// 256 threads: bf16 rows of 16 KB 0.47 / 0.38 / 0.24 (0.23 / 0.29 / 0.21), 32 KB 0.66 /
+// 0.56 / 0.40 (0.37 / 0.46 / 0.36), 64 KB 0.82 / 0.78 / 0.61 (0.43 / 0.66 / 0.56), 128 KB
+// - / 0.90 / 0.82 (- / 0.69 / 0.77); without any, 64 threads reach it from 32 KB.
 template <int DT>
-cudaError_t logprobs(const LogprobArgs& a, cudaStream_t s) {
-  const RowShape r = row_shape(a.N, a.V, DT, 1 << 30, 4 * device_sm_count(), 8 * 1024);
-  const size_t smem = std::max<size_t>(ProbRing<DT>::kBytes, a.K > 0 ? sizeof(Key) * kCandidates : 0);
-  return launch_rows(logprobs_kernel<DT>, a.N, r, smem, "token_logprobs", s, a, r.cluster);
+cudaError_t logprobs_any(const LogprobArgs& a, cudaStream_t s) {
+  const int sms = device_sm_count();
+  const RowShape r = row_shape(a.N, a.V, DT, 1 << 30, 4 * sms, 8 * 1024);
+  const int kb = row_vectors(a.V, DT) / 64;
+  if (kb <= 48 && a.K <= 16 && a.N >= 16 * sms) return logprobs<DT, 64>(a, r, s);
+  if (((kb <= 72 && a.K <= 32) || (kb <= 140 && a.K <= 8)) && a.N >= 8 * sms) return logprobs<DT, 128>(a, r, s);
+  return logprobs<DT, 256>(a, r, s);
 }
 
 }  // namespace
@@ -642,7 +694,9 @@ cudaError_t launch_distill(const DistillArgs& a, cudaStream_t s) {
 
 cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t s) {
   if (a.N == 0) return cudaSuccess;
-  return a.dtype == TW_F32 ? logprobs<TW_F32>(a, s) : a.dtype == TW_BF16 ? logprobs<TW_BF16>(a, s) : logprobs<TW_F16>(a, s);
+  return a.dtype == TW_F32    ? logprobs_any<TW_F32>(a, s)
+         : a.dtype == TW_BF16 ? logprobs_any<TW_BF16>(a, s)
+                              : logprobs_any<TW_F16>(a, s);
 }
 
 }  // namespace tw

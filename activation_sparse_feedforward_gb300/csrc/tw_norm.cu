@@ -522,9 +522,9 @@ cudaError_t norm_bwd_direct(const NormBwdArgs& a, cudaStream_t s) {
 }
 
 // Up to so many rows: one launch (norm_bwd_few_kernel). 77 rows of 2048 bf16 take 2.7 us
-// against 8.7 in two; the two meet between 450 (512 columns) and 700 rows (8192), and at
-// 90 where single elements are loaded.
-constexpr int kFewRows = 512, kFewRowsSingly = 80;
+// against 6 in two; the two meet between 250 (512 columns) and 430 rows (8192), and at 80
+// where single elements are loaded.
+constexpr int kFewRows = 320, kFewRowsSingly = 80;
 template <int DT, bool VEC>
 cudaError_t norm_bwd_few(const NormBwdArgs& a, cudaStream_t s) {
   const int vpt = a.d <= 4096 ? 1 : 2;

@@ -328,7 +328,7 @@ def _check_logprobs(out, z, tokens, K, tau):
     np.testing.assert_array_equal(idx.cpu().numpy(), ri)
 
 
-@pytest.mark.parametrize("N,V", VS + [(40, 9001), (2, 262144), (200, 60000)])
+@pytest.mark.parametrize("N,V", VS + [(40, 9001), (2, 262144), (200, 60000), (1300, 3001), (2500, 3001)])
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
 @pytest.mark.parametrize("K,S,tau", [(0, 1, 1.0), (1, 1, 0.7), (20, 3, 1.0), (128, 2, 2.0)])
 def test_logprobs_match_oracle(N, V, dtype, K, S, tau):
@@ -345,8 +345,8 @@ def test_logprobs_match_oracle(N, V, dtype, K, S, tau):
 
 
 @pytest.mark.parametrize("kind", ["equal", "ascending", "descending", "two_values", "one_thread", "zeros_of_both_signs"])
-@pytest.mark.parametrize("V,K", [(5000, 7), (33000, 100), (200000, 20)])
-def test_alternatives_of_hard_rows(kind, V, K):
+@pytest.mark.parametrize("V,K,tiles", [(5000, 7, 1), (33000, 100, 1), (200000, 20, 1), (5000, 7, 900), (5000, 20, 420)])
+def test_alternatives_of_hard_rows(kind, V, K, tiles):
     """Rows whose ties or order defeat a threshold: every element equal, sorted both ways
     (each new one larger than all before), two values, the largest all close together,
     and -0 among 0."""
@@ -369,8 +369,10 @@ def test_alternatives_of_hard_rows(kind, V, K):
     for dtype in (F32, BF16):
         zt = z.to(dtype)
         tokens = torch.tensor([[0], [V - 1], [V // 2]], dtype=torch.int32, device="cuda")
-        op = tw.TokenLogprobs(3, V, top_k=K, dtype=dtype)
-        _check_logprobs(op(zt, tokens), zt, tokens, K, 1.0)
+        op = tw.TokenLogprobs(3 * tiles, V, top_k=K, dtype=dtype)
+        out = op(zt.repeat(tiles, 1), tokens.repeat(tiles, 1))
+        _check_logprobs([t[:3] for t in out], zt, tokens, K, 1.0)
+        assert all(torch.equal(t.view(tiles, 3, -1), t[:3].view(1, 3, -1).expand(tiles, -1, -1)) for t in out)
 
 
 def test_logprobs_masks_and_special_rows():

@@ -143,7 +143,7 @@ tw_status check_side(std::initializer_list<const void*> required, std::initializ
 // Logits [N, V] and what their kernels hold of a row on chip.
 tw_status check_logits(const void* z, int64_t ldz, int N, int V, int dtype, float temperature) {
   if (N < 0 || V < 1 || check_dtype(dtype) != TW_OK) return TW_EINVAL;
-  if (!(temperature > 0.f) || !std::isfinite(temperature)) return TW_EINVAL;
+  if (!(temperature >= 1e-6f && temperature <= 1e6f)) return TW_EINVAL;
   if (V > 393216 || N > (1 << 27)) return TW_EUNSUPPORTED;
   if (N == 0) return TW_OK;
   const RowMatrix m = {z, ldz, true, false};
@@ -153,7 +153,7 @@ tw_status check_logits(const void* z, int64_t ldz, int N, int V, int dtype, floa
 tw_status check_norm(int T, int d, int dtype, int wtype) {
   if (T < 0 || d < 1) return TW_EINVAL;
   if (check_dtype(dtype) != TW_OK || (wtype != dtype && wtype != TW_F32)) return TW_EINVAL;
-  return d <= 16384 ? TW_OK : TW_EUNSUPPORTED;
+  return d <= 16384 && T <= (1 << 30) ? TW_OK : TW_EUNSUPPORTED;
 }
 
 // ------------------------------------------------------------------ workspace layouts

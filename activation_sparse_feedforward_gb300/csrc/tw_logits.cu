@@ -9,8 +9,12 @@
 //
 // Bound: HBM, one read of the logits and, with a gradient, one write. Measured on one GB300
 // against the copy rate (6681 GB/s): log probabilities 8192 x 65536 bf16 with five
-// alternatives 178 us (0.90); distillation 4096 x 131072 bf16, K = 64, temperature 2, rest
-// and labels 447 us (0.72), fp32 1023 x 50011 93 us (0.66).
+// alternatives 168 us (0.96); distillation 4096 x 131072 bf16, K = 64, temperature 2, rest
+// and labels 433 us (0.74), fp32 1023 x 50011, K = 33, 93 us (0.66). What keeps the
+// distillation from the copy rate are the steps between a slice's sweeps: of the 11.4 us a
+// CTA takes for 64 KB (three on an SM) 2.9 pass until the copies are issued and the target
+// taken, 0.6 with the listed entries, 1.9 with the sums, 2.1 with joining the cluster's
+// statistics and 3 with the gradient.
 //
 // Both join partial statistics through distributed shared memory: one launch, no
 // workspace, no atomics on results.
@@ -420,7 +424,7 @@ TW_DEV void add_terms(const uint4& r, const Scale& a, float2& s, float2& w) {
 }
 
 // Three batches a thread on their way: 48 KB an SM's quarter. (One batch ahead in
-// registers: 8192 x 65536 bf16 took 194 us, now 178.)
+// registers: 8192 x 65536 bf16 with five alternatives took 194 us, this 178.)
 template <int DT, int NT>
 using ProbRing = RowRing<DT, NT, 3>;
 

@@ -74,7 +74,6 @@ struct Part {
   }
   // first column of the part's vector j
   TW_DEV int col(int j) const { return (first + j) * E - lead; }
-  TW_DEV bool whole(int j) const { return j >= lo && j < hi; }
   TW_DEV const S* at(int j) const { return row + col(j); }
   TW_DEV uint4 edge(int j) const {
     union {
@@ -116,13 +115,13 @@ struct Scale {
 constexpr int kBatch = 4;  // vectors a thread takes at a time
 
 // f(j, all) for the thread's vectors j, j + NT, ... of [lo, hi), NT the CTA's threads, in
-// batches of BATCH; all: a constant, whether the whole batch is below hi.
+// batches of kBatch; all: a constant, whether the whole batch is below hi.
 struct Yes { static constexpr bool value = true; };
 struct No { static constexpr bool value = false; };
-template <int NT, int BATCH = kBatch, class F>
+template <int NT, class F>
 TW_DEV void in_batches(int lo, int hi, F f) {
   int j = lo + threadIdx.x;
-  for (; j + (BATCH - 1) * NT < hi; j += BATCH * NT) f(j, Yes());
+  for (; j + (kBatch - 1) * NT < hi; j += kBatch * NT) f(j, Yes());
   if (j < hi) f(j, No());
 }
 

@@ -16,6 +16,11 @@
 // thread copies and reads back its own 16 bytes, so the ring needs no barrier), and
 // weights and column sums stay in registers. Rows that 16-byte accesses do not fit, or
 // that are too wide for a ring, are loaded straight into registers.
+//
+// Measured on one GB300 against the copy rate (6681 GB/s), bf16 with fp32 weights: forward
+// 16384 x 2048 with residual and saved statistics 46.0 us (0.87); backward 16384 x 2048
+// with the residual's gradient and both sums 47.4 us (0.85), fp32 8191 x 8192 without the
+// residual's 130 us (0.92). One read of each input: no second sweep from HBM.
 #include <algorithm>
 
 #include "tw_internal.h"
@@ -178,6 +183,8 @@ struct Ring {
   }
 };
 
+// Three CTAs of 256 threads an SM: while a team waits for the two sums over its row, the
+// other CTAs' rows go on.
 template <int DT, int VPT, bool VEC, int DEPTH, int TPR, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 3 : 1) norm_fwd_kernel(const NormFwdArgs a) {
   using M = RowMap<DT, VPT, VEC, TPR>;
@@ -248,6 +255,11 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 3 : 1) norm_fwd_kernel(con
   }
 }
 
+// One CTA of 512 threads an SM, 16 elements of a row a thread: the column sums of dw and
+// db, 32 registers a thread, are kept once for all of a team's rows and go to memory once
+// an SM. 16384 x 2048 bf16 with dres, in microseconds: 512 threads and a ring of three rows
+// 51.2, of four 57.6; 640 threads 79, 768 62, 1024 65.8; the saved statistics three rows
+// ahead in registers 53.7. (With the partial sums in the threads' order, as now: 47.4.)
 template <int DT, int VPT, bool VEC, int DEPTH, int TPR, int MAXT>
 __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwdArgs a) {
   using M = RowMap<DT, VPT, VEC, TPR>;
@@ -521,6 +533,13 @@ cudaError_t norm_bwd_direct(const NormBwdArgs& a, cudaStream_t s) {
   return norm_bwd<DT, VPT, VEC, 0, 0, MAXT>(a, team_of(a.d, VPT, MAXT, a.T), s);
 }
 
+// Whether dx and an input matrix share memory.
+bool overlap(const NormBwdArgs& a, const void* p, int64_t ld) {
+  const size_t es = elem_size(a.dtype), rows = static_cast<size_t>(a.T) - 1;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(a.dx);
+  return x < y + es * (rows * a.lddx + a.d) && y < x + es * (rows * ld + a.d);
+}
+
 // Up to so many rows: one launch (norm_bwd_few_kernel). 77 rows of 2048 bf16 take 2.7 us
 // against 6 in two; the two meet between 250 (512 columns) and 430 rows (8192), and at 80
 // where single elements are loaded.
@@ -556,7 +575,9 @@ cudaError_t norm_fwd_width(const NormFwdArgs& a, cudaStream_t s) {
 }
 template <int DT, bool VEC>
 cudaError_t norm_bwd_width(const NormBwdArgs& a, cudaStream_t s) {
-  if (a.T <= (VEC ? kFewRows : kFewRowsSingly) && a.d <= 8192) return norm_bwd_few<DT, VEC>(a, s);
+  // (its column sums read x and dy while rows of dx are written: not in place of them)
+  if (a.T <= (VEC ? kFewRows : kFewRowsSingly) && a.d <= 8192 && !overlap(a, a.x, a.ldx) && !overlap(a, a.dy, a.lddy))
+    return norm_bwd_few<DT, VEC>(a, s);
   if constexpr (VEC) {
     constexpr int kDepth = DT == TW_F32 ? 2 : 3;
     if (a.d <= 1024) return norm_bwd_ring<DT, 2, 64, 512, kDepth>(a, s);

@@ -40,9 +40,6 @@ struct Elem<TW_F32> {
   static TW_DEV uint4 pack_pairs(const float2 (&v)[2]) {
     return make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
   }
-  static TW_DEV uint4 pack(const float (&v)[4]) {
-    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-  }
   // running maximum of vectors (a NaN loses to a number)
   struct Max {
     float m = -__builtin_huge_valf();
@@ -80,10 +77,6 @@ struct Elem<TW_BF16> {
   static TW_DEV uint4 pack_pairs(const float2 (&v)[4]) {
     return make_uint4(pack_bf16x2_rn(v[0].x, v[0].y), pack_bf16x2_rn(v[1].x, v[1].y), pack_bf16x2_rn(v[2].x, v[2].y),
                       pack_bf16x2_rn(v[3].x, v[3].y));
-  }
-  static TW_DEV uint4 pack(const float (&v)[8]) {
-    return make_uint4(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]), pack_bf16x2_rn(v[4], v[5]),
-                      pack_bf16x2_rn(v[6], v[7]));
   }
   struct Max {
     uint32_t m = 0xFF80FF80u;
@@ -131,10 +124,6 @@ struct Elem<TW_F16> {
     return make_uint4(pack_f16x2_rn(v[0].x, v[0].y), pack_f16x2_rn(v[1].x, v[1].y), pack_f16x2_rn(v[2].x, v[2].y),
                       pack_f16x2_rn(v[3].x, v[3].y));
   }
-  static TW_DEV uint4 pack(const float (&v)[8]) {
-    return make_uint4(pack_f16x2_rn(v[0], v[1]), pack_f16x2_rn(v[2], v[3]), pack_f16x2_rn(v[4], v[5]),
-                      pack_f16x2_rn(v[6], v[7]));
-  }
   struct Max {
     uint32_t m = 0xFC00FC00u;
     TW_DEV void add(const uint4& w) {
@@ -164,7 +153,7 @@ TW_DEV float2 both(float v) { return make_float2(v, v); }
 
 // ------------------------------------------------------------------ asynchronous copies
 // One 16-byte copy, global to shared, past L1; the copying thread sees its own copies
-// after cp_wait_all() (no wait loop: the hardware counts them).
+// after cp_wait (no wait loop: the hardware counts them).
 TW_DEV void cp_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
 }
@@ -174,11 +163,7 @@ TW_DEV void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Asks for [src, src + bytes) (both multiples of 16) in L2, without waiting or a place.
-TW_DEV void prefetch_l2(const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
-}
-
+// Asks for the line of p in L2, without waiting or a place.
 TW_DEV void prefetch_line(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // ------------------------------------------------------------------ reductions

@@ -436,7 +436,7 @@ typedef enum { TW_F32 = 0, TW_BF16 = 1, TW_F16 = 2 } tw_dtype;
  * res itself (same pointer and stride). weight, bias [d]: NULL for 1 and 0; of type
  * wtype, which is dtype or TW_F32. mean, rstd [T] fp32: NULL when no backward
  * follows. Statistics are fp32 over the row in registers; y and s are rounded once.
- * 1 <= d <= 16384 (TW_EUNSUPPORTED above); T >= 0, T = 0 does nothing; eps >= 0 and
+ * 1 <= d <= 16384, 0 <= T <= 2^30 (TW_EUNSUPPORTED above), T = 0 does nothing; eps >= 0 and
  * finite. A row with a NaN or an infinity gives NaN in y. */
 tw_status tw_layer_norm_fwd(const void* x, int64_t ldx, const void* res, int64_t ldres, const void* weight,
                             const void* bias, int T, int d, float eps, int dtype, int wtype, void* sum,
@@ -450,7 +450,7 @@ size_t tw_layer_norm_bwd_workspace_size(int T, int d);
  *   dx = rstd (g - sum(g) / d - xh sum(g xh) / d) + dres
  *   dweight = sum over rows of dy xh,  dbias = sum over rows of dy
  * dres: NULL, or [T, d], the gradient that reaches s along the residual stream; dx
- * may be dres or dy itself (same pointer and stride). weight: NULL for 1. dx [T, d] of
+ * may be dres, dy or x itself (same pointer and stride). weight: NULL for 1. dx [T, d] of
  * type dtype; dweight, dbias [d] fp32, overwritten, each NULL when not wanted; T = 0
  * writes zeros into them. The sums over rows are taken in an order that depends on
  * T and d only: the same inputs give the same bits. Widths as the forward. */
@@ -485,7 +485,8 @@ tw_status tw_layer_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t
  *    itself (same pointer and stride). dloss [N] fp32, or NULL for 1.
  *  - Statistics are fp32 over a row held on chip; dz is rounded once. The same inputs
  *    give the same bits.
- * 0 <= K <= 1024; 1 <= V <= 393216; temperature > 0; weights finite. Device condition:
+ * 0 <= K <= 1024; 1 <= V <= 393216; 1e-6 <= temperature <= 1e6; weights finite. A NaN or
+ * +inf among a row's entries makes its loss NaN, and dz where P enters it. Device condition:
  * a token or label outside [-1, V) raises TW_EINVAL in *dev_status and is read as -1. */
 tw_status tw_distill(const void* z, int64_t ldz, int N, int V, int dtype, const int32_t* t_idx, const void* t_val,
                      int t_dtype, int K, const float* t_rest, const int32_t* labels, float temperature,
@@ -503,7 +504,7 @@ tw_status tw_distill(const void* z, int64_t ldz, int N, int V, int dtype, const 
  * log probability is -inf, and they are no alternatives: places past the unmasked ones
  * hold index -1 and -inf. A row with nothing but -inf has entropy 0. A NaN or +inf in a
  * row makes its log probabilities and entropy NaN and its top indices -1.
- * 1 <= V <= 393216; temperature > 0. Device condition: a token outside [-1, V) raises
+ * 1 <= V <= 393216; 1e-6 <= temperature <= 1e6. Device condition: a token outside [-1, V) raises
  * TW_EINVAL in *dev_status and is read as -1. */
 tw_status tw_token_logprobs(const void* z, int64_t ldz, int N, int V, int dtype, const int32_t* tokens, int n_tokens,
                             float temperature, int top_k, float* logprob, float* entropy, int32_t* top_idx,

@@ -63,7 +63,8 @@ def _check_fwd(y, s, w, b, mean, rstd, dtype):
 
 
 SHAPES = [(1, 1), (1, 7), (2, 31), (3, 256), (5, 1027), (77, 2048), (130, 2047), (17, 4096), (9, 8192), (6, 8200),
-          (3, 16384), (700, 512), (2000, 96)]
+          (3, 16384), (700, 512), (2000, 96), (330, 1000), (400, 2040), (350, 4096), (330, 5632), (330, 8192), (330, 9000),
+          (100, 1027), (90, 8199), (321, 16384)]
 
 
 @pytest.mark.parametrize("T,d", SHAPES)
@@ -187,6 +188,25 @@ def test_in_place_stream_and_gradient():
                                ln.ws.numel(), st)
     assert code == _lib.TW_OK
     assert torch.equal(g, dx) and torch.equal(dw2, dw)
+
+
+@pytest.mark.parametrize("T", [5, 77, 400, 1500])
+@pytest.mark.parametrize("d", [777, 2048])
+def test_gradient_in_place_of_its_input(T, d):
+    """dx over dy, and over x: the sums over rows still see the inputs."""
+    from activation_sparse_feedforward_gb300 import _lib
+    rng = np.random.default_rng(T + d)
+    x, dy, w = _rand(rng, (T, d), BF16), _rand(rng, (T, d), BF16), _rand(rng, d, F32, 1, 0.2)
+    ln = tw.LayerNorm(T, d, weight_dtype=F32)
+    ln.forward(x, w)
+    for over in ("dy", "x"):
+        t = dict(x=x.clone(), dy=dy.clone())
+        code = tw.load().tw_layer_norm_bwd(t["dy"].data_ptr(), d, t["x"].data_ptr(), d, ln.mean.data_ptr(),
+                                           ln.rstd.data_ptr(), w.data_ptr(), None, 0, T, d, 1, 0, t[over].data_ptr(), d,
+                                           ln.dweight.data_ptr(), ln.dbias.data_ptr(), ln.ws.data_ptr(), ln.ws.numel(),
+                                           torch.cuda.current_stream().cuda_stream)
+        assert code == _lib.TW_OK
+        _check_bwd(t[over], ln.dweight, ln.dbias, dy, x, w, None, ln.mean, ln.rstd, BF16)
 
 
 def test_rows_are_independent_and_nan_stays_in_its_row():

@@ -30,7 +30,8 @@ def _norm_fwd(lib, **kw):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(T=-1), "EINVAL"), (dict(d=0), "EINVAL"), (dict(d=16385), "EUNSUPPORTED"), (dict(dtype=3), "EINVAL"),
+    (dict(T=-1), "EINVAL"), (dict(d=0), "EINVAL"), (dict(d=16385), "EUNSUPPORTED"),
+    (dict(T=(1 << 30) + 1), "EUNSUPPORTED"), (dict(dtype=3), "EINVAL"),
     (dict(dtype=-1), "EINVAL"), (dict(wtype=2), "EINVAL"), (dict(eps=-1.0), "EINVAL"), (dict(eps=math.nan), "EINVAL"),
     (dict(eps=math.inf), "EINVAL"), (dict(x=None), "EINVAL"), (dict(y=None), "EINVAL"), (dict(x=P + 1), "EALIGN"),
     (dict(w=P + 2), "EALIGN"), (dict(ldy=63), "EINVAL"), (dict(ldx=-1), "EINVAL"), (dict(sum=P), "EINVAL"),
@@ -74,7 +75,8 @@ def _distill(lib, **kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(N=-1), "EINVAL"), (dict(V=0), "EINVAL"), (dict(V=393217, ldz=400000, lddz=400000), "EUNSUPPORTED"),
     (dict(N=(1 << 27) + 1), "EUNSUPPORTED"), (dict(dtype=9), "EINVAL"), (dict(vtype=-1), "EINVAL"), (dict(K=-1), "EINVAL"),
-    (dict(K=1025), "EUNSUPPORTED"), (dict(tau=0.0), "EINVAL"), (dict(tau=-1.0), "EINVAL"), (dict(tau=math.nan), "EINVAL"),
+    (dict(K=1025), "EUNSUPPORTED"), (dict(tau=0.0), "EINVAL"), (dict(tau=-1.0), "EINVAL"), (dict(tau=math.nan), "EINVAL"), (dict(tau=1e-7), "EINVAL"),
+    (dict(tau=2e6), "EINVAL"),
     (dict(tau=math.inf), "EINVAL"), (dict(kd=math.nan), "EINVAL"), (dict(scale=math.inf), "EINVAL"),
     (dict(loss=None, dz=None), "EINVAL"), (dict(z=None), "EINVAL"), (dict(z=P + 1), "EALIGN"), (dict(lddz=99), "EINVAL"),
     (dict(ldz=-5), "EINVAL"), (dict(idx=None), "EINVAL"), (dict(val=None), "EINVAL"), (dict(val=P + 2), "EALIGN"),

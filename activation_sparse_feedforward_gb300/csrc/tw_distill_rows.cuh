@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows_kernel(const Disti
               if (all.value || j + i * NT < p.hi) store_last(out + j + i * NT, f(r[i]));
           });
         } else {
-          for (int j = p.lo + tid; j < p.hi; j += NT) singly(load_last(src + j), j);
+          store_shifted<DT, NT>(p, dz, p.lo, p.hi, [&](int j) { return src[j]; }, f);
         }
         if (p.template first_edge<NT>()) singly(p.edge(0), 0);
         if (p.template last_edge<NT>()) singly(p.edge(p.n - 1), p.n - 1);

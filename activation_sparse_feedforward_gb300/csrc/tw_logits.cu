@@ -110,11 +110,16 @@ TW_DEV void owners(const Slice<DT>& sl, int K, int* l_idx, float* l_z, int label
   __syncthreads();
 }
 
-// f of each of the thread's vectors, stored at its columns of dz.
+// f of the slice's vectors, stored at their columns of dz; each thread takes its own where
+// dz's row lies against 16 bytes as z's does.
 template <int DT, class F>
 TW_DEV void store_slice(const Slice<DT>& sl, typename Elem<DT>::S* dz, F f) {
   using S = typename Elem<DT>::S;
   constexpr int E = Elem<DT>::E;
+  if (Part<DT>::lead_of(dz) != sl.lead) {
+    store_shifted<DT, kThreads>(sl, dz, 0, sl.n, [&](int j) { return sl.buf[j]; }, f);
+    return;
+  }
   auto singly = [&](int j) {
     const uint4 g = f(sl.buf[j]);
     const S* o = reinterpret_cast<const S*>(&g);
@@ -123,16 +128,12 @@ TW_DEV void store_slice(const Slice<DT>& sl, typename Elem<DT>::S* dz, F f) {
     for (int e = 0; e < E; ++e)
       if (c + e >= 0 && c + e < sl.V) dz[c + e] = o[e];
   };
-  if (Part<DT>::lead_of(dz) == sl.lead) {  // the same alignment as z's row
-    uint4* out = reinterpret_cast<uint4*>(dz + sl.col(0));
-    in_batches<kThreads>(sl.lo, sl.hi, [&](int j, auto all) {
+  uint4* out = reinterpret_cast<uint4*>(dz + sl.col(0));
+  in_batches<kThreads>(sl.lo, sl.hi, [&](int j, auto all) {
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        if (all.value || j + i * kThreads < sl.hi) out[j + i * kThreads] = f(sl.buf[j + i * kThreads]);
-    });
-  } else {
-    for (int j = sl.lo + threadIdx.x; j < sl.hi; j += kThreads) singly(j);
-  }
+    for (int i = 0; i < kBatch; ++i)
+      if (all.value || j + i * kThreads < sl.hi) out[j + i * kThreads] = f(sl.buf[j + i * kThreads]);
+  });
   if (sl.first_edge()) singly(0);
   if (sl.last_edge()) singly(sl.n - 1);
 }

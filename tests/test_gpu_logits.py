@@ -183,6 +183,34 @@ def test_distill_strided_rows_write_their_own_columns_only(dtype, pad, off, out_
     assert (buf[:, :off] == 9).all() and (buf[:, off + V:] == 9).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("N,V", [(9, 1), (9, 2), (9, 9), (9, 17), (9, 1237), (160, 1237), (310, 33), (310, 4099), (2500, 7), (2500, 515),
+                                 (9, 90001), (155, 40001)])
+def test_distill_gradient_of_rows_aligned_otherwise(dtype, N, V):
+    """The alignment of the gradient's rows changes none of its bits, and nothing beside them."""
+    rng = np.random.default_rng(V + N)
+    K = min(V, 6)
+    z = _logits(rng, N, V, dtype, pad=(8 - V) % 8)  # rows on 16 bytes
+    idx, val = _teacher(rng, z, K)
+    labels = torch.from_numpy(rng.integers(0, V, N).astype(np.int32)).cuda()
+    op = tw.DistillLoss(N, V, K, dtype=dtype, temperature=2.0, kd_weight=0.5, ce_weight=0.5)
+
+    def run(zz, pad, off):
+        buf = torch.full((N, off + V + pad), 9.0, dtype=dtype, device="cuda")
+        loss, dz = op.forward_backward(zz, idx, val, labels=labels, out=buf[:, off:off + V])
+        assert (buf[:, :off] == 9).all() and (buf[:, off + V:] == 9).all()
+        return loss.clone(), dz
+
+    for off_z in (0, 3):  # rows that begin on 16 bytes, and 3 elements past them
+        zz = torch.zeros((N, off_z + V + (16 - V - off_z) % 8), dtype=dtype, device="cuda")[:, off_z:off_z + V]
+        zz.copy_(z)
+        loss, dz = run(zz, (16 - V - off_z) % 8, off_z)  # as z's own rows
+        _check_distill(loss, dz, zz, idx, val, None, labels, 2.0, 0.5, 0.5)
+        for pad, off in [(p, o) for p in (0, 1, 5) for o in (0, 1, 2, 3, 6)] if V < 5000 else [(0, 1), (5, 0)]:
+            l2, d2 = run(zz, pad, off)
+            assert torch.equal(l2, loss) and torch.equal(d2, dz), (off_z, pad, off)
+
+
 @pytest.mark.parametrize("dtype,V,N", [(BF16, 777, 5), (F32, 90000, 3), (BF16, 777, 500), (F32, 9001, 310), (BF16, 777, 2600), (BF16, 90001, 155)])
 def test_distill_gradient_in_place(dtype, V, N):
     rng = np.random.default_rng(1)

@@ -1,5 +1,5 @@
-// The distillation loss and its gradient with one small CTA a row, for many short rows (see
-// tw_logits.cu for when). A row comes from HBM once, through a ring of asynchronous copies,
+// The distillation loss and its gradient with one small CTA a row, for many short rows, and
+// the loss alone for long ones (see tw_logits.cu for when). A row comes from HBM once, through a ring of asynchronous copies,
 // for its statistics; for the gradient it is read again, from L2: the rows under way on
 // the device, at most 52 KB times eight CTAs an SM, are still there (loads and stores of
 // that sweep are marked as the last use).

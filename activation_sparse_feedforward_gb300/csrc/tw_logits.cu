@@ -4,8 +4,9 @@
 //  log probabilities  One CTA a row (a cluster of up to eight where there are few rows), the
 //                     row through a ring of asynchronous copies, read once.
 //  distillation       A cluster of up to eight CTAs a row, each with a slice of it in shared
-//                     memory, so that HBM is read once. Many short rows: one small CTA a
-//                     row, which reads it a second time from L2 (tw_distill_rows.cuh).
+//                     memory, so that HBM is read once. Many short rows, and the loss
+//                     alone: one small CTA a row, which reads it a second time from L2 for
+//                     the gradient (tw_distill_rows.cuh).
 //
 // Bound: HBM, one read of the logits and, with a gradient, one write. Measured on one GB300
 // against the copy rate (6681 GB/s): log probabilities 8192 x 65536 bf16 with five
@@ -625,10 +626,13 @@ RowShape row_shape(int64_t N, int V, int dtype, int most, int64_t fill, int leas
 // rest and labels, 64 threads / 128 threads / one row per cluster: rows of 8 KB (bf16)
 // 0.41 / 0.31 / 0.16, 16 KB 0.55 / 0.47 / 0.30, 32 KB 0.67 / 0.63 / 0.48, 48 KB 0.69 / 0.72 /
 // 0.60; fp32 of 48 KB 0.72 / 0.91 / 0.85, 64 KB 0.67 / 0.81 / 0.85. At 32 KB a cluster is
-// faster up to two rows an SM, and 64 threads slower up to sixteen.
+// faster up to two rows an SM, and 64 threads slower up to sixteen. The loss alone needs no
+// second sweep, so it takes long rows too once they fill the device: 4096 x 128000 bf16 162
+// us (cluster 291), 320 x 64000 13.7 (15.5), 160 x 128000 16.8 (16.3), 640 x 32000 15.3 (14.1).
 int distill_rows_threads(const DistillArgs& a) {
   const int64_t kb = static_cast<int64_t>(row_vectors(a.V, a.dtype)) / 64, sms = device_sm_count();
   if (kb <= 24 && a.N >= 16 * sms) return 64;
+  if (a.dz == nullptr && kb > 52) return (kb >= 100 && a.N >= sms && kb * a.N >= 256 * sms) || a.N >= 8 * sms ? 128 : 0;
   return kb <= 52 && a.N >= 2 * sms ? 128 : 0;
 }
 

@@ -224,6 +224,28 @@ def test_distill_gradient_in_place(dtype, V, N):
     assert torch.equal(l2, loss) and torch.equal(z, dz)
 
 
+@pytest.mark.parametrize("dtype,N,V", [(BF16, 170, 130001), (F32, 160, 70003), (F16, 1300, 30011), (F16, 320, 393216)])
+@pytest.mark.parametrize("tau,ce", [(1.0, 0.0), (0.8, 0.5), (2.0, 0.5)])
+def test_loss_alone_is_the_loss(dtype, N, V, tau, ce):
+    """Without a gradient long rows take another path: the same loss, against the formula's on some rows."""
+    rng = np.random.default_rng(N)
+    K = 40
+    z = torch.randn((N, V), device="cuda", dtype=torch.float32, generator=torch.Generator("cuda").manual_seed(N)).mul_(2.5).to(dtype)
+    few = torch.tensor([0, 1, 7, N // 2, N - 2, N - 1], device="cuda")
+    idx = torch.from_numpy(np.stack([rng.choice(V, K, replace=False) for _ in range(N)]).astype(np.int32)).cuda()
+    idx[1, 5] = -1
+    idx[7, 3] = idx[7, 9]
+    idx[0, 0], idx[0, 1] = 0, V - 1
+    val = torch.from_numpy(rng.normal(0, 2, (N, K)).astype(np.float32)).cuda()
+    rest = torch.from_numpy(rng.normal(1, 1, N).astype(np.float32)).cuda()
+    labels = torch.from_numpy(rng.integers(0, V, N).astype(np.int32)).cuda()
+    labels[0], labels[1] = V - 1, -1
+    op = tw.DistillLoss(N, V, K, dtype=dtype, temperature=tau, kd_weight=0.7, ce_weight=ce, grad=False)
+    loss = op.forward(z, idx, val, rest, labels=labels)
+    _check_distill(loss[few], None, z[few], idx[few], val[few], rest[few], labels[few] if ce else None, tau, 0.7, ce)
+    tw.raise_if_device_error(op.status)
+
+
 def test_cross_entropy_alone():
     rng = np.random.default_rng(2)
     z = _logits(rng, 40, 3001, BF16)

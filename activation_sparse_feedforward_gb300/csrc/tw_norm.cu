@@ -139,15 +139,20 @@ TW_DEV float team_sum(float v, float* red, int team, int tpr, int tid) {
   for (int w = 1; w < warps; ++w) v += red[w];
   return v;
 }
-TW_DEV float2 team_sum2(float a, float b, float2* red, int team, int tpr, int tid) {
+// The same for two sums, in two halves: every warp gives its part, and after the team's
+// barrier each thread takes the total (tpr 32: the part is the total).
+TW_DEV float2 give_sum2(float a, float b, float2* red, int tpr, int tid) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
     b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
   }
-  if (tpr == 32) return make_float2(a, b);
-  const int lane = tid & 31, warp = tid >> 5, warps = tpr >> 5;
-  if (lane == 0) red[warp] = make_float2(a, b);
+  if (tpr > 32 && (tid & 31) == 0) red[tid >> 5] = make_float2(a, b);
+  return make_float2(a, b);
+}
+TW_DEV float2 take_sum2(float2 own, const float2* red, int team, int tpr, int tid) {
+  if (tpr == 32) return own;
+  const int lane = tid & 31, warps = tpr >> 5;
   team_barrier(team + 1, tpr);
   if (warps > 8) {
     const float2 p = lane < warps ? red[lane] : make_float2(0.f, 0.f);
@@ -183,10 +188,12 @@ struct Ring {
   }
 };
 
-// Three CTAs of 256 threads an SM: while a team waits for the two sums over its row, the
-// other CTAs' rows go on.
+// CTAs an SM of a forward kernel of so many threads: about 800 threads, so that while a
+// team waits for the two sums over its row, the other CTAs' rows go on.
+constexpr int fwd_ctas(int threads) { return threads > 448 ? 1 : threads > 320 ? 2 : 800 / threads; }
+
 template <int DT, int VPT, bool VEC, int DEPTH, int TPR, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 3 : 1) norm_fwd_kernel(const NormFwdArgs a) {
+__global__ void __launch_bounds__(MAXT, fwd_ctas(MAXT)) norm_fwd_kernel(const NormFwdArgs a) {
   using M = RowMap<DT, VPT, VEC, TPR>;
   using S = typename M::S;
   constexpr int NP = M::NP;
@@ -255,11 +262,13 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 3 : 1) norm_fwd_kernel(con
   }
 }
 
-// One CTA of 512 threads an SM, 16 elements of a row a thread: the column sums of dw and
-// db, 32 registers a thread, are kept once for all of a team's rows and go to memory once
-// an SM. 16384 x 2048 bf16 with dres, in microseconds: 512 threads and a ring of three rows
-// 51.2, of four 57.6; 640 threads 79, 768 62, 1024 65.8; the saved statistics three rows
-// ahead in registers 53.7. (With the partial sums in the threads' order, as now: 47.4.)
+// One CTA of about 512 threads an SM, 16 elements of a row a thread: the column sums of dw
+// and db, 32 registers a thread, are kept once for all of a team's rows and go to memory
+// once an SM. 16384 x 2048 bf16 with dres, in microseconds: 512 threads and a ring of three
+// rows 51.2, of four 57.6; 640 threads 79, 768 62, 1024 65.8; the saved statistics three
+// rows ahead in registers 53.7; with the partial sums in the threads' order 47.4; one row
+// ahead (below), a ring of four, 46.7, and 4096 x 8192, where one team has the SM to
+// itself, 49.7 in place of 55.8.
 template <int DT, int VPT, bool VEC, int DEPTH, int TPR, int MAXT>
 __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwdArgs a) {
   using M = RowMap<DT, VPT, VEC, TPR>;
@@ -292,18 +301,8 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwdArgs a) {
 #pragma unroll
   for (int i = 0; i < NP; ++i) dw[i] = db[i] = both(0.f);
   const float inv_d = 1.f / static_cast<float>(a.d);
-  float mean = row < a.T ? a.mean[row] : 0.f, rstd = row < a.T ? a.rstd[row] : 0.f;
-  for (int flip = 0, stage = 0; row < a.T; row += stride, flip ^= 1) {
-    float2 x[NP], g[NP], more[NP];
-    if constexpr (DEPTH > 0) {
-      cp_wait<DEPTH - 1>();
-      ring.read(mv, stage, 0, x);
-      ring.read(mv, stage, 1, g);
-      if (a.dres != nullptr) ring.read(mv, stage, 2, more);
-    } else {
-      m.load(at(a.x, a.ldx, row), x);
-      m.load(at(a.dy, a.lddy, row), g);
-    }
+  // x becomes xh, g dy w; the thread's parts of the row's two sums, and its column sums
+  auto sums = [&](float2 (&x)[NP], float2 (&g)[NP], float mean, float rstd, float2* to) {
     float2 c1 = both(0.f), c2 = both(0.f);
     m.each([&](int i) {
       x[i] = m.keep(i, mul2(add2(x[i], both(-mean)), both(rstd)));
@@ -313,23 +312,82 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwdArgs a) {
       c1 = add2(c1, g[i]);
       c2 = fma2(g[i], x[i], c2);
     });
-    const float2 c = team_sum2(c1.x + c1.y, c2.x + c2.y, red[flip][team], team, tpr, tid);
-    if constexpr (DEPTH > 0) {  // the row has left its places
-      fetch(stage, row + DEPTH * stride);
-      stage = stage + 1 == DEPTH ? 0 : stage + 1;
-    } else if (a.dres != nullptr) {
-      m.load(at(a.dres, a.lddres, row), more);
-    }
-    const int next = row + stride;
-    const float mean_next = next < a.T ? a.mean[next] : 0.f, rstd_next = next < a.T ? a.rstd[next] : 0.f;
+    return give_sum2(c1.x + c1.y, c2.x + c2.y, to, tpr, tid);
+  };
+  auto finish = [&](const float2 (&x)[NP], float2 (&g)[NP], const float2 (&more)[NP], float2 c, float rstd, int r) {
     const float2 k1 = both(-c.x * inv_d), k2 = both(-c.y * inv_d);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       g[i] = mul2(add2(g[i], fma2(x[i], k2, k1)), both(rstd));
       if (a.dres != nullptr) g[i] = add2(g[i], more[i]);
     }
-    m.store(static_cast<S*>(a.dx) + static_cast<size_t>(row) * a.lddx, g);
-    mean = mean_next, rstd = rstd_next;
+    m.store(static_cast<S*>(a.dx) + static_cast<size_t>(r) * a.lddx, g);
+  };
+  auto mean_of = [&](int r) { return r < a.T ? a.mean[r] : 0.f; };
+  auto rstd_of = [&](int r) { return r < a.T ? a.rstd[r] : 0.f; };
+  float mean = mean_of(row), rstd = rstd_of(row);
+  if constexpr (DEPTH >= 4) {
+    // One row ahead: the team's barrier finds the parts of this row's sums long given, and
+    // the next row's sums are taken before this row's dx, both from the ring.
+    float mean_next = mean_of(row + stride), rstd_next = rstd_of(row + stride);
+    float2 part = both(0.f);
+    if (row < a.T) {
+      float2 x[NP], g[NP];
+      cp_wait<DEPTH - 1>();
+      ring.read(mv, 0, 0, x);
+      ring.read(mv, 0, 1, g);
+      part = sums(x, g, mean, rstd, red[0][team]);
+    }
+    for (int flip = 0, stage = 0; row < a.T; row += stride, flip ^= 1) {
+      const int next = stage + 1 == DEPTH ? 0 : stage + 1;
+      const float mean_2 = mean_of(row + 2 * stride), rstd_2 = rstd_of(row + 2 * stride);
+      const float2 c = take_sum2(part, red[flip][team], team, tpr, tid);
+      if (row + stride < a.T) {
+        float2 x[NP], g[NP];
+        cp_wait<DEPTH - 2>();
+        ring.read(mv, next, 0, x);
+        ring.read(mv, next, 1, g);
+        part = sums(x, g, mean_next, rstd_next, red[flip ^ 1][team]);
+      }
+      float2 x[NP], g[NP], more[NP];
+      ring.read(mv, stage, 0, x);
+      ring.read(mv, stage, 1, g);
+      if (a.dres != nullptr) ring.read(mv, stage, 2, more);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        x[i] = mul2(add2(x[i], both(-mean)), both(rstd));
+        g[i] = mul2(g[i], w[i]);
+      }
+      finish(x, g, more, c, rstd, row);
+      fetch(stage, row + DEPTH * stride);
+      stage = next;
+      mean = mean_next, rstd = rstd_next;
+      mean_next = mean_2, rstd_next = rstd_2;
+    }
+  } else {
+    for (int flip = 0, stage = 0; row < a.T; row += stride, flip ^= 1) {
+      float2 x[NP], g[NP], more[NP];
+      if constexpr (DEPTH > 0) {
+        cp_wait<DEPTH - 1>();
+        ring.read(mv, stage, 0, x);
+        ring.read(mv, stage, 1, g);
+        if (a.dres != nullptr) ring.read(mv, stage, 2, more);
+      } else {
+        m.load(at(a.x, a.ldx, row), x);
+        m.load(at(a.dy, a.lddy, row), g);
+      }
+      const float2 part = sums(x, g, mean, rstd, red[flip][team]);
+      const float2 c = take_sum2(part, red[flip][team], team, tpr, tid);
+      if constexpr (DEPTH > 0) {  // the row has left its places
+        fetch(stage, row + DEPTH * stride);
+        stage = stage + 1 == DEPTH ? 0 : stage + 1;
+      } else if (a.dres != nullptr) {
+        m.load(at(a.dres, a.lddres, row), more);
+      }
+      const float mean_next = mean_of(row + stride), rstd_next = rstd_of(row + stride);
+      finish(x, g, more, c, rstd, row);
+      mean = mean_next, rstd = rstd_next;
+    }
   }
   if (a.part == nullptr) return;
   // The CTA's partial sums, [2][NE tpr] in the order of the threads' own elements: a
@@ -392,7 +450,7 @@ __global__ void __launch_bounds__(kFewThreads) norm_bwd_few_kernel(const NormBwd
       c2 = fma2(g[i], x[i], c2);
     });
     if (a.dres != nullptr) m.load(at(a.dres, a.lddres, row), w);
-    const float2 c = team_sum2(c1.x + c1.y, c2.x + c2.y, red[team], team, tpr, m.tid);
+    const float2 c = take_sum2(give_sum2(c1.x + c1.y, c2.x + c2.y, red[team], tpr, m.tid), red[team], team, tpr, m.tid);
     const float inv_d = 1.f / static_cast<float>(a.d);
     const float2 k1 = both(-c.x * inv_d), k2 = both(-c.y * inv_d);
 #pragma unroll
@@ -494,9 +552,9 @@ template <int DT, int TPR, int MAXT>
 cudaError_t norm_fwd_ring(const NormFwdArgs& a, cudaStream_t s) {
   constexpr int kTeams = MAXT / TPR;
   const size_t smem = ring_bytes(DT, 2, MAXT, 3, a.res != nullptr ? 2 : 1);
-  // as many CTAs as stay resident: three by registers (512 threads: one)
+  // as many CTAs as stay resident
   const int fit = static_cast<int>(kSmemMost / (smem + 6 * 1024));
-  const int per_sm = std::max(1, std::min(MAXT <= 256 ? 3 : 1, fit));
+  const int per_sm = std::max(1, std::min(fwd_ctas(MAXT), fit));
   return launch_norm(norm_fwd_kernel<DT, 2, true, 3, TPR, MAXT>,
                      std::min((a.T + kTeams - 1) / kTeams, device_sm_count() * per_sm), Team{TPR, kTeams}, smem,
                      "norm_fwd", a, s);
@@ -561,11 +619,17 @@ cudaError_t norm_bwd_few(const NormBwdArgs& a, cudaStream_t s) {
 template <int DT, bool VEC>
 cudaError_t norm_fwd_width(const NormFwdArgs& a, cudaStream_t s) {
   if constexpr (VEC) {
-    if (a.d <= 512) return norm_fwd_ring<DT, 32, 256>(a, s);
-    if (a.d <= 1024) return norm_fwd_ring<DT, 64, 256>(a, s);
-    if (a.d <= 2048) return norm_fwd_ring<DT, 128, 256>(a, s);
-    if (a.d <= 4096) return norm_fwd_ring<DT, 256, 256>(a, s);
-    if (a.d <= 8192) return norm_fwd_ring<DT, 512, 512>(a, s);
+    if (a.d <= 16 * 32) return norm_fwd_ring<DT, 32, 256>(a, s);
+    if (a.d <= 16 * 64) return norm_fwd_ring<DT, 64, 256>(a, s);
+    if (a.d <= 16 * 96) return norm_fwd_ring<DT, 96, 192>(a, s);
+    if (a.d <= 16 * 128) return norm_fwd_ring<DT, 128, 256>(a, s);
+    if (a.d <= 16 * 160) return norm_fwd_ring<DT, 160, 320>(a, s);
+    if (a.d <= 16 * 192) return norm_fwd_ring<DT, 192, 192>(a, s);
+    if (a.d <= 16 * 256) return norm_fwd_ring<DT, 256, 256>(a, s);
+    if (a.d <= 16 * 320) return norm_fwd_ring<DT, 320, 320>(a, s);
+    if (a.d <= 16 * 384) return norm_fwd_ring<DT, 384, 384>(a, s);
+    if (a.d <= 16 * 448) return norm_fwd_ring<DT, 448, 448>(a, s);
+    if (a.d <= 16 * 512) return norm_fwd_ring<DT, 512, 512>(a, s);
     return norm_fwd_direct<DT, 2, true, 1024>(a, s);
   } else {
     return a.d <= 2048   ? norm_fwd_direct<DT, 1, false, 256>(a, s)
@@ -579,11 +643,15 @@ cudaError_t norm_bwd_width(const NormBwdArgs& a, cudaStream_t s) {
   if (a.T <= (VEC ? kFewRows : kFewRowsSingly) && a.d <= 8192 && !overlap(a, a.x, a.ldx) && !overlap(a, a.dy, a.lddy))
     return norm_bwd_few<DT, VEC>(a, s);
   if constexpr (VEC) {
-    constexpr int kDepth = DT == TW_F32 ? 2 : 3;
-    if (a.d <= 1024) return norm_bwd_ring<DT, 2, 64, 512, kDepth>(a, s);
-    if (a.d <= 2048) return norm_bwd_ring<DT, 2, 128, 512, kDepth>(a, s);
-    if (a.d <= 4096) return norm_bwd_ring<DT, 2, 256, 512, kDepth>(a, s);
-    if (a.d <= 8192) return norm_bwd_ring<DT, 2, 512, 512, kDepth>(a, s);
+    constexpr int kDepth = DT == TW_F32 ? 2 : 4;
+    if (a.d <= 16 * 32) return norm_bwd_ring<DT, 2, 32, 480, kDepth>(a, s);
+    if (a.d <= 16 * 64) return norm_bwd_ring<DT, 2, 64, 512, kDepth>(a, s);
+    if (a.d <= 16 * 96) return norm_bwd_ring<DT, 2, 96, 480, kDepth>(a, s);
+    if (a.d <= 16 * 128) return norm_bwd_ring<DT, 2, 128, 512, kDepth>(a, s);
+    if (a.d <= 16 * 160) return norm_bwd_ring<DT, 2, 160, 480, kDepth>(a, s);
+    if (a.d <= 16 * 256) return norm_bwd_ring<DT, 2, 256, 512, kDepth>(a, s);
+    if (a.d <= 16 * 384) return norm_bwd_ring<DT, 2, 384, 384, kDepth>(a, s);
+    if (a.d <= 16 * 512) return norm_bwd_ring<DT, 2, 512, 512, kDepth>(a, s);
     return norm_bwd_direct<DT, 2, true, 1024>(a, s);
   } else {
     return a.d <= 4096   ? norm_bwd_direct<DT, 1, false, 512>(a, s)

@@ -31,6 +31,8 @@ def _matrix(name: str, t: torch.Tensor, dtype: torch.dtype, rows: int, cols: int
         raise ValueError(f"{name} must be a CUDA {dtype} tensor")
     if t.shape != (rows, cols):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
+    if t.is_contiguous():
+        return cols
     ld, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"{name} must have unit stride along its rows")
@@ -47,9 +49,14 @@ def _vector(name: str, t: torch.Tensor | None, dtype: torch.dtype, n: int) -> in
 
 
 def _rows(name: str, t: torch.Tensor, most: int) -> int:
-    if t.dim() != 2 or t.shape[0] > most:
+    if t.dim() != 2 or (n := t.shape[0]) > most:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected at most {most} rows")
-    return t.shape[0]
+    return n
+
+
+def _addresses(*buffers: torch.Tensor | None) -> tuple[int | None, ...]:
+    """An object's own buffers' addresses, asked for once."""
+    return tuple(None if t is None else t.data_ptr() for t in buffers)
 
 
 def _stream_of(t: torch.Tensor) -> int:
@@ -87,6 +94,8 @@ class LayerNorm:
             self.dbias = torch.empty(d, dtype=torch.float32, device=device)
             self.ws_bytes = int(self._lib.tw_layer_norm_bwd_workspace_size(T, d))
             self.ws = _workspace(self.ws_bytes, device)
+            self._to_bwd = _addresses(self.dx, self.dweight, self.dbias, self.ws)
+        self._to_fwd = _addresses(self.y, self.sum, self._mean, self._rstd)
 
     def forward(self, x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
                 residual: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
@@ -99,12 +108,13 @@ class LayerNorm:
             y, s = y[:n], s[:n]
         if n != self.mean.shape[0]:
             self.mean, self.rstd = self._mean[:n], self._rstd[:n]
+        to_y, to, to_mean, to_rstd = self._to_fwd
         if residual is None:
             r, ldr, to = None, 0, None
         else:
-            r, ldr, to = residual.data_ptr(), _matrix("residual", residual, dt, n, d), s.data_ptr()
+            r, ldr = residual.data_ptr(), _matrix("residual", residual, dt, n, d)
         code = self._lib.tw_layer_norm_fwd(x.data_ptr(), ldx, r, ldr, w, b, n, d, self.eps, self._dt, self._wdt, to, d,
-                                           y.data_ptr(), d, self.mean.data_ptr(), self.rstd.data_ptr(), _stream_of(x))
+                                           to_y, d, to_mean, to_rstd, _stream_of(x))
         if code:
             _lib.check(code, "tw_layer_norm_fwd")
         return y, (x if residual is None else s)
@@ -125,9 +135,9 @@ class LayerNorm:
         g, ldg = (None, 0) if dres is None else (dres.data_ptr(), _matrix("dres", dres, dt, n, d))
         if n != self.T:
             dx = dx[:n]
+        to, to_w, to_b, ws = self._to_bwd
         code = self._lib.tw_layer_norm_bwd(dy.data_ptr(), lddy, x.data_ptr(), ldx, m, r, w, g, ldg, n, d, self._dt,
-                                           self._wdt, dx.data_ptr(), d, self.dweight.data_ptr(), self.dbias.data_ptr(),
-                                           self.ws.data_ptr(), self.ws_bytes, _stream_of(x))
+                                           self._wdt, to, d, to_w, to_b, ws, self.ws_bytes, _stream_of(x))
         if code:
             _lib.check(code, "tw_layer_norm_bwd")
         return dx, self.dweight, self.dbias
@@ -167,22 +177,23 @@ class DistillLoss:
         self.loss = torch.empty(N, dtype=torch.float32, device=device)
         self.dz = torch.empty((N, V), dtype=dtype, device=device) if grad else None
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        self._to = _addresses(self.loss, self.dz, self.status)
 
     def _run(self, z, idx, val, rest, labels, dloss, scale, want_loss, want_grad, out):
         n, K, V = _rows("z", z, self.N), self.K, self.V
         ld = _matrix("z", z, self.dtype, n, V)
+        to_loss, to_dz, status = self._to
         dz, to, ldd = None, None, 0
         if want_grad:
             dz = self.dz if out is None else out
             if dz is None:
                 raise ValueError("this DistillLoss was made with grad=False: give `out`")
             if out is not None:
-                ldd = _matrix("out", out, self.dtype, n, V)
+                to, ldd = out.data_ptr(), _matrix("out", out, self.dtype, n, V)
             else:
-                ldd = V
+                to, ldd = to_dz, V
                 if n != self.N:
                     dz = dz[:n]
-            to = dz.data_ptr()
         i = v = None
         tdt = self._dt
         if K > 0:
@@ -193,8 +204,8 @@ class DistillLoss:
         code = self._lib.tw_distill(
             z.data_ptr(), ld, n, V, self._dt, i, v, tdt, K, _vector("rest", rest, torch.float32, n),
             _vector("labels", labels, torch.int32, n), self.temperature, self.kd_weight, self.ce_weight,
-            _vector("dloss", dloss, torch.float32, n), scale, self.loss.data_ptr() if want_loss else None, to, ldd,
-            self.status.data_ptr(), _stream_of(z))
+            _vector("dloss", dloss, torch.float32, n), scale, to_loss if want_loss else None, to, ldd, status,
+            _stream_of(z))
         if code:
             _lib.check(code, "tw_distill")
         return (self.loss if n == self.N else self.loss[:n]), dz
@@ -239,6 +250,7 @@ class TokenLogprobs:
         self.top_idx = torch.empty((N, top_k), dtype=torch.int32, device=device)
         self.top_logprob = torch.empty((N, top_k), dtype=torch.float32, device=device)
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        self._to = _addresses(self.logprob, self.entropy, self.top_idx, self.top_logprob, self.status)
 
     def __call__(self, z: torch.Tensor, tokens: torch.Tensor | None = None):
         """(logprob [n, n_tokens], entropy [n], top_idx [n, top_k], top_logprob [n, top_k])."""
@@ -250,9 +262,7 @@ class TokenLogprobs:
                 raise ValueError("tokens must be given for n_tokens > 0")
             t = _vector("tokens", tokens, torch.int32, n * s)
         code = self._lib.tw_token_logprobs(
-            z.data_ptr(), ld, n, self.V, self._dt, t, s, self.temperature, self.top_k, self.logprob.data_ptr(),
-            self.entropy.data_ptr(), self.top_idx.data_ptr(), self.top_logprob.data_ptr(), self.status.data_ptr(),
-            _stream_of(z))
+            z.data_ptr(), ld, n, self.V, self._dt, t, s, self.temperature, self.top_k, *self._to, _stream_of(z))
         if code:
             _lib.check(code, "tw_token_logprobs")
         if n == self.N:

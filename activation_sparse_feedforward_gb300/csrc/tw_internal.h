@@ -380,8 +380,7 @@ struct NormBwdArgs {
 };
 // The most CTAs whose partial sums over rows the backward keeps in its workspace.
 constexpr int kNormPartials = 512;
-// The most columns of one partial: the threads' elements for d columns, teams being powers
-// of two of threads up to 8192 columns and whole warps above.
+// At least the columns of one partial, the elements of a team's threads for d columns.
 constexpr int norm_partial_width(int d) {
   int w = 1024;
   while (w < d && w < 8192) w *= 2;

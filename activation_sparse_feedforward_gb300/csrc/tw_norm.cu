@@ -548,14 +548,14 @@ cudaError_t launch_norm(Kern kern, int grid, const Team& t, size_t smem, const c
 size_t ring_bytes(int dtype, int vpt, int threads, int depth, int tensors) {
   return static_cast<size_t>(threads) * depth * tensors * 8 * vpt * elem_size(dtype);
 }
-template <int DT, int TPR, int MAXT>
+template <int DT, int TPR, int MAXT, int VPT = 2>
 cudaError_t norm_fwd_ring(const NormFwdArgs& a, cudaStream_t s) {
   constexpr int kTeams = MAXT / TPR;
-  const size_t smem = ring_bytes(DT, 2, MAXT, 3, a.res != nullptr ? 2 : 1);
+  const size_t smem = ring_bytes(DT, VPT, MAXT, 3, a.res != nullptr ? 2 : 1);
   // as many CTAs as stay resident
   const int fit = static_cast<int>(kSmemMost / (smem + 6 * 1024));
   const int per_sm = std::max(1, std::min(fwd_ctas(MAXT), fit));
-  return launch_norm(norm_fwd_kernel<DT, 2, true, 3, TPR, MAXT>,
+  return launch_norm(norm_fwd_kernel<DT, VPT, true, 3, TPR, MAXT>,
                      std::min((a.T + kTeams - 1) / kTeams, device_sm_count() * per_sm), Team{TPR, kTeams}, smem,
                      "norm_fwd", a, s);
 }
@@ -614,8 +614,12 @@ cudaError_t norm_bwd_few(const NormBwdArgs& a, cudaStream_t s) {
   return e;
 }
 
-// Teams of a power of two of threads, the least that holds the row at 16 elements a
-// thread, and three rows in the ring (the backward in fp32: two).
+// The least team that holds the row at 16 elements a thread, and three rows in the ring
+// (the backward: four, in fp32 two). Rows that take a CTA's whole team: 8 elements a thread
+// where that makes more warps without spills. Backward with dres, 33.5 M elements bf16: 5120
+// columns 54.5 us (16 a thread 64.1), 5632 54.9 (61.9), but 6656 57.2 (52.3), 8192 79 (49.7);
+// fp32, 16.8 M: 5632 49.8 (64.2), 8192 59.6 (48.2). Forward without residual: bf16 5632 37.4
+// (27.5), 8192 33.2 (27.8); fp32 7168 23.2 (25.0).
 template <int DT, bool VEC>
 cudaError_t norm_fwd_width(const NormFwdArgs& a, cudaStream_t s) {
   if constexpr (VEC) {
@@ -628,8 +632,13 @@ cudaError_t norm_fwd_width(const NormFwdArgs& a, cudaStream_t s) {
     if (a.d <= 16 * 256) return norm_fwd_ring<DT, 256, 256>(a, s);
     if (a.d <= 16 * 320) return norm_fwd_ring<DT, 320, 320>(a, s);
     if (a.d <= 16 * 384) return norm_fwd_ring<DT, 384, 384>(a, s);
-    if (a.d <= 16 * 448) return norm_fwd_ring<DT, 448, 448>(a, s);
-    if (a.d <= 16 * 512) return norm_fwd_ring<DT, 512, 512>(a, s);
+    if constexpr (DT == TW_F32) {
+      if (a.d <= 8 * 896) return norm_fwd_ring<DT, 896, 896, 1>(a, s);
+      if (a.d <= 8 * 1024) return norm_fwd_ring<DT, 1024, 1024, 1>(a, s);
+    } else {
+      if (a.d <= 16 * 448) return norm_fwd_ring<DT, 448, 448>(a, s);
+      if (a.d <= 16 * 512) return norm_fwd_ring<DT, 512, 512>(a, s);
+    }
     return norm_fwd_direct<DT, 2, true, 1024>(a, s);
   } else {
     return a.d <= 2048   ? norm_fwd_direct<DT, 1, false, 256>(a, s)
@@ -650,7 +659,11 @@ cudaError_t norm_bwd_width(const NormBwdArgs& a, cudaStream_t s) {
     if (a.d <= 16 * 128) return norm_bwd_ring<DT, 2, 128, 512, kDepth>(a, s);
     if (a.d <= 16 * 160) return norm_bwd_ring<DT, 2, 160, 480, kDepth>(a, s);
     if (a.d <= 16 * 256) return norm_bwd_ring<DT, 2, 256, 512, kDepth>(a, s);
-    if (a.d <= 16 * 384) return norm_bwd_ring<DT, 2, 384, 384, kDepth>(a, s);
+    if (a.d <= 8 * 640) return norm_bwd_ring<DT, 1, 640, 640, kDepth>(a, s);
+    if (a.d <= 8 * 704) return norm_bwd_ring<DT, 1, 704, 704, kDepth>(a, s);
+    if constexpr (DT == TW_F32) {
+      if (a.d <= 8 * 896) return norm_bwd_ring<DT, 1, 896, 896, kDepth>(a, s);
+    }
     if (a.d <= 16 * 512) return norm_bwd_ring<DT, 2, 512, 512, kDepth>(a, s);
     return norm_bwd_direct<DT, 2, true, 1024>(a, s);
   } else {

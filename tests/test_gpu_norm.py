@@ -64,7 +64,8 @@ def _check_fwd(y, s, w, b, mean, rstd, dtype):
 
 SHAPES = [(1, 1), (1, 7), (2, 31), (3, 256), (5, 1027), (77, 2048), (130, 2047), (17, 4096), (9, 8192), (6, 8200),
           (3, 16384), (700, 512), (2000, 96), (330, 1000), (400, 2040), (350, 4096), (330, 5632), (330, 8192), (330, 9000),
-          (100, 1027), (90, 8199), (321, 16384)]
+          (100, 1027), (90, 8199), (321, 16384), (2500, 500), (1100, 1288), (700, 2400), (330, 2600), (330, 5120), (340, 6400),
+          (330, 7168)]
 
 
 @pytest.mark.parametrize("T,d", SHAPES)

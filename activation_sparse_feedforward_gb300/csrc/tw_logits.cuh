@@ -457,23 +457,6 @@ TW_DEV uint4 gradient(const uint4& r, const Scale& a, const Scale& b, float u, f
   }
   return El::pack_pairs(v);
 }
-// The 16 bytes that begin `shift` elements (1 to E - 1) into a and b.
-template <int DT>
-TW_DEV uint4 shifted(const uint4& a, const uint4& b, int shift) {
-  constexpr int kHalf = Elem<DT>::E / 4 - 1;  // elements of 16 bits: a last step of half a word
-  const bool two = (shift >> kHalf) & 2, one = (shift >> kHalf) & 1;
-  const uint32_t w[6] = {two ? a.z : a.x, two ? a.w : a.y, two ? b.x : a.z, two ? b.y : a.w, two ? b.z : b.x, two ? b.w : b.y};
-  uint32_t v[5];
-#pragma unroll
-  for (int i = 0; i < 5; ++i) v[i] = one ? w[i + 1] : w[i];
-  if constexpr (kHalf > 0) {
-    const uint32_t half = shift & 1 ? 0x5432u : 0x3210u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = __byte_perm(v[i], v[i + 1], half);
-  }
-  return make_uint4(v[0], v[1], v[2], v[3]);
-}
-
 // Stores f of the vectors [lo, hi) of a part, which get(j) reads, at their columns of a row
 // that lies otherwise against 16 bytes: each vector stored is put together from two. (One
 // element at a time, 3358 x 120602 bf16 took 965 us, most of it partial writes in L2.)

@@ -30,21 +30,22 @@ namespace tw {
 
 namespace {
 
-// Elements of a row owned by a thread, 8 VPT of them as packed pairs: vectors of 16 bytes
-// (VEC) or single elements (any d, alignment and row stride), both in strides of the
-// team so that a warp's accesses are adjacent. What lies past the row reads 0. TPR: the
+// Elements of a row owned by a thread, 8 VPT of them as packed pairs: vectors of 16 bytes in
+// strides of the team, so that a warp's accesses are adjacent. VEC: rows begin on 16 bytes
+// and hold whole vectors; else rows lie anywhere and d is any, and a vector is put together
+// from two (tw_rows.cuh). What lies past the row reads 0. TPR: the
 // team's threads where they are a constant of the kernel (offsets are then immediates),
 // else 0.
 template <int DT, int VPT, bool VEC, int TPR>
 struct RowMap {
   using S = typename Elem<DT>::S;
   static constexpr int NE = 8 * VPT, NP = NE / 2;
-  static constexpr int E = VEC ? Elem<DT>::E : 1, NV = NE / E;  // elements of a vector, vectors
+  static constexpr int E = Elem<DT>::E, NV = NE / E;  // elements of a vector, vectors
   int d, tid, tpr_;
   TW_DEV RowMap(int d_, int tid_, int tpr) : d(d_), tid(tid_), tpr_(tpr) {}
   TW_DEV int tpr() const { return TPR > 0 ? TPR : tpr_; }
   TW_DEV int col(int i) const { return (i / E * tpr() + tid) * E + i % E; }
-  TW_DEV bool has(int i) const { return col(i / E * E) < d; }  // a vector is in the row whole or not at all
+  TW_DEV bool has(int i) const { return col(i / E * E) < d; }  // the element's vector is in the row, at least in part
 
   static TW_DEV void widen16(const uint4& w, float2* v) {
     float2 u[Elem<DT>::E / 2];
@@ -52,33 +53,34 @@ struct RowMap {
 #pragma unroll
     for (int e = 0; e < Elem<DT>::E / 2; ++e) v[e] = u[e];
   }
-  TW_DEV void load(const S* p, float2 (&v)[NP]) const {
-    if constexpr (VEC) {
+  // careful: see load_any
+  TW_DEV void load(const S* p, float2 (&v)[NP], bool careful = true) const {
+    uint4 r[NV];
 #pragma unroll
-      for (int k = 0; k < NV; ++k)
-        widen16(has(k * E) ? *reinterpret_cast<const uint4*>(p + col(k * E)) : make_uint4(0, 0, 0, 0), v + k * E / 2);
-    } else {
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        v[i].x = has(2 * i) ? Elem<DT>::get(p[col(2 * i)]) : 0.f;
-        v[i].y = has(2 * i + 1) ? Elem<DT>::get(p[col(2 * i + 1)]) : 0.f;
+    for (int k = 0; k < NV; ++k) {
+      const int c = col(k * E);
+      r[k] = make_uint4(0, 0, 0, 0);
+      if (VEC) {
+        if (c < d) r[k] = *reinterpret_cast<const uint4*>(p + c);
+      } else {
+        if (c < d) r[k] = load_any<DT>(p + c, d - c, careful);
       }
     }
+#pragma unroll
+    for (int k = 0; k < NV; ++k) widen16(r[k], v + k * E / 2);
   }
+  // by whole warps
   TW_DEV void store(S* p, const float2 (&v)[NP]) const {
-    if constexpr (VEC) {
 #pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        float2 u[E / 2];
+    for (int k = 0; k < NV; ++k) {
+      float2 u[E / 2];
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) u[e] = v[k * E / 2 + e];
-        if (has(k * E)) *reinterpret_cast<uint4*>(p + col(k * E)) = Elem<DT>::pack_pairs(u);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        if (has(2 * i)) p[col(2 * i)] = Elem<DT>::put(v[i].x);
-        if (has(2 * i + 1)) p[col(2 * i + 1)] = Elem<DT>::put(v[i].y);
+      for (int e = 0; e < E / 2; ++e) u[e] = v[k * E / 2 + e];
+      const int c = col(k * E);
+      if (VEC) {
+        if (c < d) *reinterpret_cast<uint4*>(p + c) = Elem<DT>::pack_pairs(u);
+      } else {
+        store_any<DT>(p + c, Elem<DT>::pack_pairs(u), d - c, tid & 31);
       }
     }
   }
@@ -96,33 +98,33 @@ struct RowMap {
         if constexpr (VEC) {
           v[i] = has(2 * i) ? *reinterpret_cast<const float2*>(p + col(2 * i)) : both(0.f);
         } else {
-          v[i].x = has(2 * i) ? p[col(2 * i)] : 0.f;
-          v[i].y = has(2 * i + 1) ? p[col(2 * i + 1)] : 0.f;
+          v[i].x = in(2 * i) ? p[col(2 * i)] : 0.f;
+          v[i].y = in(2 * i + 1) ? p[col(2 * i + 1)] : 0.f;
         }
       }
     }
   }
-  // f(pair) for the pairs inside the row; where a pair may be half in it (single
-  // elements) f's result is masked by keep()
+  // f(pair) for the pairs of vectors in the row; where a vector may be in it in part, what f
+  // adds to elements that read 0 is masked by keep()
   template <class F>
   TW_DEV void each(F f) const {
-    if constexpr (VEC) {
 #pragma unroll
-      for (int k = 0; k < NV; ++k)
-        if (has(k * E)) {
+    for (int k = 0; k < NV; ++k)
+      if (has(k * E)) {
 #pragma unroll
-          for (int e = 0; e < E / 2; ++e) f(k * E / 2 + e);
-        }
-    } else {
-#pragma unroll
-      for (int i = 0; i < NP; ++i) f(i);
-    }
+        for (int e = 0; e < E / 2; ++e) f(k * E / 2 + e);
+      }
   }
+  TW_DEV bool in(int i) const { return col(i) < d; }
   TW_DEV float2 keep(int i, float2 v) const {
-    if constexpr (!VEC) v = make_float2(has(2 * i) ? v.x : 0.f, has(2 * i + 1) ? v.y : 0.f);
+    if constexpr (!VEC) v = make_float2(in(2 * i) ? v.x : 0.f, in(2 * i + 1) ? v.y : 0.f);
     return v;
   }
 };
+
+// The rows around whose ends 16 bytes (E elements) may lie outside the matrix: the first and
+// the last, and all where they lie closer together than that (a stride of 0 repeats a row).
+TW_DEV bool end_row(int row, int T, int64_t ld, int E) { return row == 0 || row == T - 1 || ld < E; }
 
 constexpr int kMaxTeams = 15;  // named barriers 1..15
 
@@ -164,29 +166,70 @@ TW_DEV float2 take_sum2(float2 own, const float2* red, int team, int tpr, int ti
 }
 
 
-// A thread's places in its team's ring: DEPTH rows of up to three tensors, NV vectors of
-// 16 bytes each (the thread's chunks of 8 elements). DEPTH 0: no ring.
-template <int DT, int VPT, int DEPTH, int TPR>
+// A team's ring: DEPTH rows of up to three tensors (0: no ring). VEC: each thread copies and
+// reads back its own NV vectors, so that the ring needs no barrier. Else the row's aligned 16
+// bytes as they lie in memory, copied by the whole team and read, two for a vector, after
+// its barrier.
+template <int DT, int VPT, bool VEC, int DEPTH, int TPR>
 struct Ring {
-  using M = RowMap<DT, VPT, true, TPR>;
-  static constexpr int E = M::E, NV = M::NV;
+  using M = RowMap<DT, VPT, VEC, TPR>;
+  using S = typename M::S;
+  static constexpr int E = M::E, NV = M::NV, kExtra = VEC ? 0 : 1;
   uint4* mine;
   int tensors;
   TW_DEV Ring(uint4* smem, int team, int tensors_, const M& m)
-      : mine(smem + team * (DEPTH * tensors_ * NV * m.tpr()) + m.tid), tensors(tensors_) {}
-  TW_DEV uint4* place(const M& m, int stage, int t) const { return mine + (stage * tensors + t) * NV * m.tpr(); }
-  TW_DEV void copy(const M& m, int stage, int t, const typename M::S* row) const {
+      : mine(smem + team * (DEPTH * tensors_ * (NV * m.tpr() + kExtra)) + (VEC ? m.tid : 0)), tensors(tensors_) {}
+  TW_DEV uint4* place(const M& m, int stage, int t) const { return mine + (stage * tensors + t) * (NV * m.tpr() + kExtra); }
+  static TW_DEV int lead_of(const S* row) { return static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(S)); }
+  // careful: see end_row
+  TW_DEV void copy(const M& m, int stage, int t, const S* row, bool careful) const {
     uint4* to = place(m, stage, t);
+    if constexpr (VEC) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-      if (m.has(k * E)) cp_async16(to + k * m.tpr(), row + m.col(k * E));
+      for (int k = 0; k < NV; ++k)
+        if (m.has(k * E)) cp_async16(to + k * m.tpr(), row + m.col(k * E));
+    } else {
+      const int lead = lead_of(row), end = lead + m.d;
+      auto one = [&](int g) {
+        if (g * E >= end) return;
+        const S* p = row - lead + g * E;
+        if (careful && ((g == 0 && lead > 0) || g * E + E > end)) {
+          S* q = reinterpret_cast<S*>(to + g);
+          for (int e = 0; e < E; ++e)
+            if (g * E + e >= lead && g * E + e < end) q[e] = p[e];
+        } else {
+          cp_async16(to + g, p);
+        }
+      };
+#pragma unroll
+      for (int k = 0; k < NV; ++k) one(k * m.tpr() + m.tid);
+      if (m.tid == 0) one(NV * m.tpr());
+    }
   }
-  TW_DEV void read(const M& m, int stage, int t, float2 (&v)[M::NP]) const {
+  TW_DEV void read(const M& m, int stage, int t, const S* row, float2 (&v)[M::NP]) const {
     const uint4* from = place(m, stage, t);
+    if constexpr (VEC) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) M::widen16(m.has(k * E) ? from[k * m.tpr()] : make_uint4(0, 0, 0, 0), v + k * E / 2);
+      for (int k = 0; k < NV; ++k) M::widen16(m.has(k * E) ? from[k * m.tpr()] : make_uint4(0, 0, 0, 0), v + k * E / 2);
+    } else {
+      const int lead = lead_of(row);
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int g = k * m.tpr() + m.tid, left = m.d - g * E;
+        uint4 r = make_uint4(0, 0, 0, 0);
+        if (left > 0) r = first_of<DT>(shifted<DT>(from[g], from[g + 1], lead), left);
+        M::widen16(r, v + k * E / 2);
+      }
+    }
   }
 };
+template <int TPR>
+TW_DEV void team_sync(int team) {
+  if constexpr (TPR == 32)
+    __syncwarp();
+  else
+    team_barrier(team + 1, TPR);
+}
 
 // CTAs an SM of a forward kernel of so many threads: about 800 threads, so that while a
 // team waits for the two sums over its row, the other CTAs' rows go on.
@@ -205,12 +248,11 @@ __global__ void __launch_bounds__(MAXT, fwd_ctas(MAXT)) norm_fwd_kernel(const No
   int row = blockIdx.x * teams + team;
   const M m(a.d, tid, tpr);
   auto at = [](const void* p, int64_t ld, int r) { return static_cast<const S*>(p) + static_cast<size_t>(r) * ld; };
-  const RowMap<DT, VPT, true, TPR> mv(a.d, tid, tpr);
-  const Ring<DT, VPT, DEPTH, TPR> ring(smem, team, a.res != nullptr ? 2 : 1, mv);
+  const Ring<DT, VPT, VEC, DEPTH, TPR> ring(smem, team, a.res != nullptr ? 2 : 1, m);
   auto fetch = [&](int stage, int r) {
     if (r < a.T) {
-      ring.copy(mv, stage, 0, at(a.x, a.ldx, r));
-      if (a.res != nullptr) ring.copy(mv, stage, 1, at(a.res, a.ldres, r));
+      ring.copy(m, stage, 0, at(a.x, a.ldx, r), end_row(r, a.T, a.ldx, M::E));
+      if (a.res != nullptr) ring.copy(m, stage, 1, at(a.res, a.ldres, r), end_row(r, a.T, a.ldres, M::E));
     }
     cp_commit();
   };
@@ -222,15 +264,19 @@ __global__ void __launch_bounds__(MAXT, fwd_ctas(MAXT)) norm_fwd_kernel(const No
   m.weight(a.w, a.wtype, 1.f, w);
   m.weight(a.b, a.wtype, 0.f, b);
   const float inv_d = 1.f / static_cast<float>(a.d);
+  if constexpr (DEPTH > 0 && !VEC) {
+    cp_wait<DEPTH - 1>();
+    team_sync<TPR>(team);
+  }
   for (int stage = 0; row < a.T; row += stride) {
     float2 v[NP], u[NP];
     if constexpr (DEPTH > 0) {
-      cp_wait<DEPTH - 1>();
-      ring.read(mv, stage, 0, v);
-      if (a.res != nullptr) ring.read(mv, stage, 1, u);
+      if constexpr (VEC) cp_wait<DEPTH - 1>();  // else before the last row's second sum
+      ring.read(m, stage, 0, at(a.x, a.ldx, row), v);
+      if (a.res != nullptr) ring.read(m, stage, 1, at(a.res, a.ldres, row), u);
     } else {
-      m.load(at(a.x, a.ldx, row), v);
-      if (a.res != nullptr) m.load(at(a.res, a.ldres, row), u);
+      m.load(at(a.x, a.ldx, row), v, end_row(row, a.T, a.ldx, M::E));
+      if (a.res != nullptr) m.load(at(a.res, a.ldres, row), u, end_row(row, a.T, a.ldres, M::E));
     }
     const size_t r = static_cast<size_t>(row);
     if (a.res != nullptr) {
@@ -245,6 +291,10 @@ __global__ void __launch_bounds__(MAXT, fwd_ctas(MAXT)) norm_fwd_kernel(const No
     if constexpr (DEPTH > 0) {  // the row has left its places
       fetch(stage, row + DEPTH * stride);
       stage = stage + 1 == DEPTH ? 0 : stage + 1;
+      if constexpr (!VEC) {  // the next row is here, and after the second sum's barrier for all
+        cp_wait<DEPTH - 1>();
+        if constexpr (TPR == 32) __syncwarp();
+      }
     }
     float2 q = both(0.f);
     m.each([&](int i) {
@@ -279,16 +329,16 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwdArgs a) {
   pdl_enter();
   const int tid = threadIdx.x, tpr = TPR > 0 ? TPR : blockDim.x, team = threadIdx.y, teams = TPR > 0 ? MAXT / TPR : blockDim.y;
   const int stride = gridDim.x * teams;
-  int row = blockIdx.x * teams + team;
+  const int first = blockIdx.x * teams + team;
+  int row = first;
   const M m(a.d, tid, tpr);
   auto at = [](const void* p, int64_t ld, int r) { return static_cast<const S*>(p) + static_cast<size_t>(r) * ld; };
-  const RowMap<DT, VPT, true, TPR> mv(a.d, tid, tpr);
-  const Ring<DT, VPT, DEPTH, TPR> ring(smem, team, a.dres != nullptr ? 3 : 2, mv);
+  const Ring<DT, VPT, VEC, DEPTH, TPR> ring(smem, team, a.dres != nullptr ? 3 : 2, m);
   auto fetch = [&](int stage, int r) {
     if (r < a.T) {
-      ring.copy(mv, stage, 0, at(a.x, a.ldx, r));
-      ring.copy(mv, stage, 1, at(a.dy, a.lddy, r));
-      if (a.dres != nullptr) ring.copy(mv, stage, 2, at(a.dres, a.lddres, r));
+      ring.copy(m, stage, 0, at(a.x, a.ldx, r), end_row(r, a.T, a.ldx, M::E));
+      ring.copy(m, stage, 1, at(a.dy, a.lddy, r), end_row(r, a.T, a.lddy, M::E));
+      if (a.dres != nullptr) ring.copy(m, stage, 2, at(a.dres, a.lddres, r), end_row(r, a.T, a.lddres, M::E));
     }
     cp_commit();
   };
@@ -328,38 +378,48 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwdArgs a) {
   float mean = mean_of(row), rstd = rstd_of(row);
   if constexpr (DEPTH >= 4) {
     // One row ahead: the team's barrier finds the parts of this row's sums long given, and
-    // the next row's sums are taken before this row's dx, both from the ring.
+    // the next row's sums are taken before this row's dx, both from the ring. Without VEC the
+    // barrier also says that the next row is there for all, and that the last one is read:
+    // only then are its places filled again.
     float mean_next = mean_of(row + stride), rstd_next = rstd_of(row + stride);
     float2 part = both(0.f);
     if (row < a.T) {
       float2 x[NP], g[NP];
       cp_wait<DEPTH - 1>();
-      ring.read(mv, 0, 0, x);
-      ring.read(mv, 0, 1, g);
+      if constexpr (!VEC) team_sync<TPR>(team);
+      ring.read(m, 0, 0, at(a.x, a.ldx, row), x);
+      ring.read(m, 0, 1, at(a.dy, a.lddy, row), g);
       part = sums(x, g, mean, rstd, red[0][team]);
     }
     for (int flip = 0, stage = 0; row < a.T; row += stride, flip ^= 1) {
       const int next = stage + 1 == DEPTH ? 0 : stage + 1;
       const float mean_2 = mean_of(row + 2 * stride), rstd_2 = rstd_of(row + 2 * stride);
+      if constexpr (!VEC) {
+        cp_wait<DEPTH - 3>();
+        if constexpr (TPR == 32) __syncwarp();
+      }
       const float2 c = take_sum2(part, red[flip][team], team, tpr, tid);
+      if constexpr (!VEC) {
+        if (row >= first + stride) fetch(stage == 0 ? DEPTH - 1 : stage - 1, row + (DEPTH - 1) * stride);
+      }
       if (row + stride < a.T) {
         float2 x[NP], g[NP];
-        cp_wait<DEPTH - 2>();
-        ring.read(mv, next, 0, x);
-        ring.read(mv, next, 1, g);
+        if constexpr (VEC) cp_wait<DEPTH - 2>();
+        ring.read(m, next, 0, at(a.x, a.ldx, row + stride), x);
+        ring.read(m, next, 1, at(a.dy, a.lddy, row + stride), g);
         part = sums(x, g, mean_next, rstd_next, red[flip ^ 1][team]);
       }
       float2 x[NP], g[NP], more[NP];
-      ring.read(mv, stage, 0, x);
-      ring.read(mv, stage, 1, g);
-      if (a.dres != nullptr) ring.read(mv, stage, 2, more);
+      ring.read(m, stage, 0, at(a.x, a.ldx, row), x);
+      ring.read(m, stage, 1, at(a.dy, a.lddy, row), g);
+      if (a.dres != nullptr) ring.read(m, stage, 2, at(a.dres, a.lddres, row), more);
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         x[i] = mul2(add2(x[i], both(-mean)), both(rstd));
         g[i] = mul2(g[i], w[i]);
       }
       finish(x, g, more, c, rstd, row);
-      fetch(stage, row + DEPTH * stride);
+      if constexpr (VEC) fetch(stage, row + DEPTH * stride);
       stage = next;
       mean = mean_next, rstd = rstd_next;
       mean_next = mean_2, rstd_next = rstd_2;
@@ -369,12 +429,13 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwdArgs a) {
       float2 x[NP], g[NP], more[NP];
       if constexpr (DEPTH > 0) {
         cp_wait<DEPTH - 1>();
-        ring.read(mv, stage, 0, x);
-        ring.read(mv, stage, 1, g);
-        if (a.dres != nullptr) ring.read(mv, stage, 2, more);
+        static_assert(DEPTH == 0 || VEC, "rows read by others need the form above");
+        ring.read(m, stage, 0, nullptr, x);
+        ring.read(m, stage, 1, nullptr, g);
+        if (a.dres != nullptr) ring.read(m, stage, 2, nullptr, more);
       } else {
-        m.load(at(a.x, a.ldx, row), x);
-        m.load(at(a.dy, a.lddy, row), g);
+        m.load(at(a.x, a.ldx, row), x, end_row(row, a.T, a.ldx, M::E));
+        m.load(at(a.dy, a.lddy, row), g, end_row(row, a.T, a.lddy, M::E));
       }
       const float2 part = sums(x, g, mean, rstd, red[flip][team]);
       const float2 c = take_sum2(part, red[flip][team], team, tpr, tid);
@@ -382,7 +443,7 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwdArgs a) {
         fetch(stage, row + DEPTH * stride);
         stage = stage + 1 == DEPTH ? 0 : stage + 1;
       } else if (a.dres != nullptr) {
-        m.load(at(a.dres, a.lddres, row), more);
+        m.load(at(a.dres, a.lddres, row), more, end_row(row, a.T, a.lddres, M::E));
       }
       const float mean_next = mean_of(row + stride), rstd_next = rstd_of(row + stride);
       finish(x, g, more, c, rstd, row);
@@ -438,8 +499,8 @@ __global__ void __launch_bounds__(kFewThreads) norm_bwd_few_kernel(const NormBwd
     if (team >= teams || row >= a.T) return;
     const M m(a.d, threadIdx.x - team * tpr, tpr);
     float2 x[M::NP], g[M::NP], w[M::NP];
-    m.load(at(a.x, a.ldx, row), x);
-    m.load(at(a.dy, a.lddy, row), g);
+    m.load(at(a.x, a.ldx, row), x, end_row(row, a.T, a.ldx, M::E));
+    m.load(at(a.dy, a.lddy, row), g, end_row(row, a.T, a.lddy, M::E));
     const float mean = a.mean[row], rstd = a.rstd[row];
     m.weight(a.w, a.wtype, 1.f, w);
     float2 c1 = both(0.f), c2 = both(0.f);
@@ -449,7 +510,7 @@ __global__ void __launch_bounds__(kFewThreads) norm_bwd_few_kernel(const NormBwd
       c1 = add2(c1, g[i]);
       c2 = fma2(g[i], x[i], c2);
     });
-    if (a.dres != nullptr) m.load(at(a.dres, a.lddres, row), w);
+    if (a.dres != nullptr) m.load(at(a.dres, a.lddres, row), w, end_row(row, a.T, a.lddres, M::E));
     const float2 c = take_sum2(give_sum2(c1.x + c1.y, c2.x + c2.y, red[team], tpr, m.tid), red[team], team, tpr, m.tid);
     const float inv_d = 1.f / static_cast<float>(a.d);
     const float2 k1 = both(-c.x * inv_d), k2 = both(-c.y * inv_d);
@@ -470,8 +531,8 @@ __global__ void __launch_bounds__(kFewThreads) norm_bwd_few_kernel(const NormBwd
 #pragma unroll 4
   for (int row = warp; row < a.T; row += kFewWarps) {
     float2 x[M::NP], g[M::NP];
-    m.load(at(a.x, a.ldx, row) + first, x);
-    m.load(at(a.dy, a.lddy, row) + first, g);
+    m.load(at(a.x, a.ldx, row) + first, x, end_row(row, a.T, a.ldx, M::E));
+    m.load(at(a.dy, a.lddy, row) + first, g, end_row(row, a.T, a.lddy, M::E));
     const float mean = a.mean[row], rstd = a.rstd[row];
 #pragma unroll
     for (int i = 0; i < M::NP; ++i) {
@@ -545,17 +606,17 @@ cudaError_t launch_norm(Kern kern, int grid, const Team& t, size_t smem, const c
 }
 
 // Rows through a ring of DEPTH: MAXT / TPR teams of TPR threads, 16 elements a thread.
-size_t ring_bytes(int dtype, int vpt, int threads, int depth, int tensors) {
-  return static_cast<size_t>(threads) * depth * tensors * 8 * vpt * elem_size(dtype);
+size_t ring_bytes(int dtype, int vpt, const Team& t, int depth, int tensors, bool vec) {
+  return t.teams * depth * tensors * (t.tpr * 8 * vpt * elem_size(dtype) + (vec ? 0 : 16));
 }
-template <int DT, int TPR, int MAXT, int VPT = 2>
+template <int DT, int TPR, int MAXT, int VPT = 2, bool VEC = true>
 cudaError_t norm_fwd_ring(const NormFwdArgs& a, cudaStream_t s) {
   constexpr int kTeams = MAXT / TPR;
-  const size_t smem = ring_bytes(DT, VPT, MAXT, 3, a.res != nullptr ? 2 : 1);
+  const size_t smem = ring_bytes(DT, VPT, Team{TPR, kTeams}, 3, a.res != nullptr ? 2 : 1, VEC);
   // as many CTAs as stay resident
   const int fit = static_cast<int>(kSmemMost / (smem + 6 * 1024));
   const int per_sm = std::max(1, std::min(fwd_ctas(MAXT), fit));
-  return launch_norm(norm_fwd_kernel<DT, VPT, true, 3, TPR, MAXT>,
+  return launch_norm(norm_fwd_kernel<DT, VPT, VEC, 3, TPR, MAXT>,
                      std::min((a.T + kTeams - 1) / kTeams, device_sm_count() * per_sm), Team{TPR, kTeams}, smem,
                      "norm_fwd", a, s);
 }
@@ -577,14 +638,14 @@ template <int DT, int VPT, bool VEC, int DEPTH, int TPR, int MAXT>
 cudaError_t norm_bwd(const NormBwdArgs& a, const Team& t, cudaStream_t s) {
   using M = RowMap<DT, VPT, VEC, TPR>;
   const int grid = std::min({(a.T + t.teams - 1) / t.teams, device_sm_count(), kNormPartials}), width = M::NE * t.tpr;
-  const size_t smem = std::max(ring_bytes(DT, VPT, t.teams * t.tpr, DEPTH, a.dres != nullptr ? 3 : 2),
+  const size_t smem = std::max(ring_bytes(DT, VPT, t, DEPTH, a.dres != nullptr ? 3 : 2, VEC),
                                t.teams > 1 ? 2 * sizeof(float) * t.teams * width : size_t{0});
   const cudaError_t e = launch_norm(norm_bwd_kernel<DT, VPT, VEC, DEPTH, TPR, MAXT>, grid, t, smem, "norm_bwd", a, s);
   return e != cudaSuccess || a.part == nullptr ? e : norm_bwd_finish(a, grid, width, t.tpr, M::E, s);
 }
-template <int DT, int VPT, int TPR, int MAXT, int DEPTH>
+template <int DT, int VPT, int TPR, int MAXT, int DEPTH, bool VEC = true>
 cudaError_t norm_bwd_ring(const NormBwdArgs& a, cudaStream_t s) {
-  return norm_bwd<DT, VPT, true, DEPTH, TPR, MAXT>(a, Team{TPR, MAXT / TPR}, s);
+  return norm_bwd<DT, VPT, VEC, DEPTH, TPR, MAXT>(a, Team{TPR, MAXT / TPR}, s);
 }
 template <int DT, int VPT, bool VEC, int MAXT>
 cudaError_t norm_bwd_direct(const NormBwdArgs& a, cudaStream_t s) {
@@ -641,9 +702,15 @@ cudaError_t norm_fwd_width(const NormFwdArgs& a, cudaStream_t s) {
     }
     return norm_fwd_direct<DT, 2, true, 1024>(a, s);
   } else {
-    return a.d <= 2048   ? norm_fwd_direct<DT, 1, false, 256>(a, s)
-           : a.d <= 8192 ? norm_fwd_direct<DT, 1, false, 1024>(a, s)
-                         : norm_fwd_direct<DT, 2, false, 1024>(a, s);
+    if (a.d <= 16 * 32) return norm_fwd_ring<DT, 32, 256, 2, false>(a, s);
+    if (a.d <= 16 * 64) return norm_fwd_ring<DT, 64, 256, 2, false>(a, s);
+    if (a.d <= 16 * 96) return norm_fwd_ring<DT, 96, 192, 2, false>(a, s);
+    if (a.d <= 16 * 128) return norm_fwd_ring<DT, 128, 256, 2, false>(a, s);
+    if (a.d <= 16 * 192) return norm_fwd_ring<DT, 192, 192, 2, false>(a, s);
+    if (a.d <= 16 * 256) return norm_fwd_ring<DT, 256, 256, 2, false>(a, s);
+    if (a.d <= 16 * 384) return norm_fwd_ring<DT, 384, 384, 2, false>(a, s);
+    if (a.d <= 16 * 512) return norm_fwd_ring<DT, 512, 512, 2, false>(a, s);
+    return norm_fwd_direct<DT, 2, false, 1024>(a, s);
   }
 }
 template <int DT, bool VEC>
@@ -667,9 +734,15 @@ cudaError_t norm_bwd_width(const NormBwdArgs& a, cudaStream_t s) {
     if (a.d <= 16 * 512) return norm_bwd_ring<DT, 2, 512, 512, kDepth>(a, s);
     return norm_bwd_direct<DT, 2, true, 1024>(a, s);
   } else {
-    return a.d <= 4096   ? norm_bwd_direct<DT, 1, false, 512>(a, s)
-           : a.d <= 8192 ? norm_bwd_direct<DT, 1, false, 1024>(a, s)
-                         : norm_bwd_direct<DT, 2, false, 1024>(a, s);
+    constexpr int kVpt = DT == TW_F32 ? 1 : 2, kE = 8 * kVpt;
+    if (a.d <= kE * 32) return norm_bwd_ring<DT, kVpt, 32, 480, 4, false>(a, s);
+    if (a.d <= kE * 64) return norm_bwd_ring<DT, kVpt, 64, 512, 4, false>(a, s);
+    if (a.d <= kE * 96) return norm_bwd_ring<DT, kVpt, 96, 480, 4, false>(a, s);
+    if (a.d <= kE * 128) return norm_bwd_ring<DT, kVpt, 128, 512, 4, false>(a, s);
+    if (a.d <= kE * 160) return norm_bwd_ring<DT, kVpt, 160, 480, 4, false>(a, s);
+    if (a.d <= kE * 256) return norm_bwd_ring<DT, kVpt, 256, 512, 4, false>(a, s);
+    if (a.d <= kE * 512) return norm_bwd_ring<DT, kVpt, 512, 512, 4, false>(a, s);
+    return a.d <= 8192 ? norm_bwd_direct<DT, 1, false, 1024>(a, s) : norm_bwd_direct<DT, 2, false, 1024>(a, s);
   }
 }
 

@@ -166,6 +166,89 @@ TW_DEV void cp_wait() {
 // Asks for the line of p in L2, without waiting or a place.
 TW_DEV void prefetch_line(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
+// ------------------------------------------------------------------ rows off 16 bytes
+// The 16 bytes that begin `shift` elements (0 to E - 1) into a and b.
+template <int DT>
+TW_DEV uint4 shifted(const uint4& a, const uint4& b, int shift) {
+  constexpr int kHalf = Elem<DT>::E / 4 - 1;  // elements of 16 bits: a last step of half a word
+  const bool two = (shift >> kHalf) & 2, one = (shift >> kHalf) & 1;
+  const uint32_t w[6] = {two ? a.z : a.x, two ? a.w : a.y, two ? b.x : a.z, two ? b.y : a.w, two ? b.z : b.x, two ? b.w : b.y};
+  uint32_t v[5];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) v[i] = one ? w[i + 1] : w[i];
+  if constexpr (kHalf > 0) {
+    const uint32_t half = shift & 1 ? 0x5432u : 0x3210u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __byte_perm(v[i], v[i + 1], half);
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// The first n (1 or more) elements of v, then 0.
+template <int DT>
+TW_DEV uint4 first_of(const uint4& v, int n) {
+  constexpr int E = Elem<DT>::E;
+  if (n >= E) return v;
+  union {
+    uint4 w;
+    typename Elem<DT>::S e[E];
+  } u;
+  u.w = v;
+#pragma unroll
+  for (int i = 0; i < E; ++i)
+    if (i >= n) u.e[i] = Elem<DT>::put(0.f);
+  return u.w;
+}
+
+// The vector of the E elements from p on, of which n (1 or more) are the row's: the others
+// read 0. p may lie anywhere; read are whole 16 bytes that hold an element of the row, or,
+// where careful, the row's elements alone.
+template <int DT>
+TW_DEV uint4 load_any(const typename Elem<DT>::S* p, int n, bool careful) {
+  using S = typename Elem<DT>::S;
+  constexpr int E = Elem<DT>::E;
+  const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(S)), left = min(n, E);
+  union {
+    S e[E];
+    uint4 w;
+  } u;
+  if (careful) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) u.e[i] = i < left ? p[i] : Elem<DT>::put(0.f);
+    return u.w;
+  }
+  const uint4* at = reinterpret_cast<const uint4*>(p - shift);
+  const uint4 a = at[0], b = shift + left > E ? at[1] : make_uint4(0, 0, 0, 0);
+  return first_of<DT>(shifted<DT>(a, b, shift), left);
+}
+
+// Stores v at p, of which n elements are the row's (0 or fewer: none). All lanes of a warp,
+// whose vectors follow each other in one row: an aligned 16 bytes are written by the lane
+// that holds their end, with the lane before's elements; what is left at the warp's and the
+// row's ends goes out by the element.
+template <int DT>
+TW_DEV void store_any(typename Elem<DT>::S* p, const uint4& v, int n, int lane) {
+  using S = typename Elem<DT>::S;
+  constexpr int E = Elem<DT>::E;
+  const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(S)), head = E - shift;
+  const uint4 before = make_uint4(__shfl_up_sync(0xFFFFFFFFu, v.x, 1), __shfl_up_sync(0xFFFFFFFFu, v.y, 1),
+                                  __shfl_up_sync(0xFFFFFFFFu, v.z, 1), __shfl_up_sync(0xFFFFFFFFu, v.w, 1));
+  const bool whole = (lane > 0 || shift == 0) && n >= head;
+  const bool next = shift > 0 && lane < 31 && n - E >= head;  // the next lane takes this one's end
+  if (whole) *reinterpret_cast<uint4*>(p - shift) = shift == 0 ? v : shifted<DT>(before, v, head);
+  const int from = whole ? head : 0, to = next ? head : min(n, E);
+  if (from < to) {
+    union {
+      uint4 w;
+      S e[E];
+    } u;
+    u.w = v;
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if (i >= from && i < to) p[i] = u.e[i];
+  }
+}
+
 // ------------------------------------------------------------------ reductions
 TW_DEV float warp_sum(float v) {
 #pragma unroll

@@ -152,6 +152,56 @@ def test_strided_and_unaligned_rows(pad, off):
         assert torch.equal(ln2.forward(x.contiguous(), w)[0], y)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("T,d", [(3, 1), (90, 3), (700, 7), (90, 8), (90, 9), (700, 15), (90, 33), (700, 250), (90, 257), (90, 1027), (700, 2050),
+                                 (330, 4101), (5, 8190), (330, 9001)])
+def test_rows_at_any_offset_touch_their_own_columns_only(dtype, T, d):
+    """Inputs between NaN, outputs between nines, each at an offset and a stride of its own."""
+    from activation_sparse_feedforward_gb300 import _lib
+    rng = np.random.default_rng(T + d)
+    w, b = _rand(rng, d, F32, 1, 0.3), _rand(rng, d, F32, 0, 0.2)
+    ln = tw.LayerNorm(T, d, dtype=dtype, weight_dtype=F32, eps=EPS)
+    dt = {F32: 0, BF16: 1, F16: 2}[dtype]
+
+    def inside(off, pad, fill, values):
+        buf = torch.full((T, off + d + pad), fill, dtype=dtype, device="cuda")
+        if values is not None:
+            buf[:, off:off + d] = values
+        return buf, buf[:, off:off + d]
+
+    vals = [_rand(rng, (T, d), dtype, 0.3, 1.5) for _ in range(2)]
+    stream = torch.cuda.current_stream().cuda_stream
+    for offs in ((0, 1, 2, 3), (1, 6, 0, 5), (7, 3, 4, 1), (2, 2, 2, 2), (3, 0, 6, 4)):
+        (_, x), (_, r) = inside(offs[0], offs[1] % 3, float("nan"), vals[0]), inside(offs[1], offs[2] % 5, float("nan"), vals[1])
+        (sb, s), (yb, y) = inside(offs[2], offs[3] % 4, 9.0, None), inside(offs[3], offs[0] % 6, 9.0, None)
+        code = tw.load().tw_layer_norm_fwd(x.data_ptr(), x.stride(0), r.data_ptr(), r.stride(0), w.data_ptr(), b.data_ptr(), T, d, EPS,
+                                           dt, 0, s.data_ptr(), s.stride(0), y.data_ptr(), y.stride(0), ln.mean.data_ptr(),
+                                           ln.rstd.data_ptr(), stream)
+        assert code == _lib.TW_OK
+        assert torch.equal(s, (vals[0].float() + vals[1].float()).to(dtype))
+        _check_fwd(y, s, w, b, ln.mean, ln.rstd, dtype)
+        (db_, dx), (_, dres) = inside(offs[1], offs[0] % 4, 9.0, None), inside(offs[3], offs[1] % 7, float("nan"), vals[0])
+        code = tw.load().tw_layer_norm_bwd(r.data_ptr(), r.stride(0), s.data_ptr(), s.stride(0), ln.mean.data_ptr(), ln.rstd.data_ptr(),
+                                           w.data_ptr(), dres.data_ptr(), dres.stride(0), T, d, dt, 0, dx.data_ptr(), dx.stride(0),
+                                           ln.dweight.data_ptr(), ln.dbias.data_ptr(), ln.ws.data_ptr(), ln.ws.numel(), stream)
+        assert code == _lib.TW_OK
+        _check_bwd(dx, ln.dweight, ln.dbias, r, s, w, dres, ln.mean, ln.rstd, dtype)
+        for buf, off in ((sb, offs[2]), (yb, offs[3]), (db_, offs[1])):
+            assert (buf[:, :off] == 9).all() and (buf[:, off + d:] == 9).all()
+
+
+@pytest.mark.parametrize("T,d", [(40, 3), (40, 777), (400, 777)])
+def test_one_odd_row_for_all(T, d):
+    rng = np.random.default_rng(d)
+    x, r = _rand(rng, (1, d), BF16).expand(T, d), _rand(rng, (T, d), BF16)
+    ln = tw.LayerNorm(T, d)
+    y, s = ln.forward(x, residual=r)
+    assert torch.equal(s, (x.float() + r.float()).bfloat16())
+    _check_fwd(y, s, None, None, ln.mean, ln.rstd, BF16)
+    dx, dw, db = ln.backward(x, s, dres=x)
+    _check_bwd(dx, dw, db, x, s, None, x, ln.mean, ln.rstd, BF16)
+
+
 def test_one_row_for_all_and_fewer_rows_than_the_object():
     rng = np.random.default_rng(5)
     x, r = _rand(rng, (1, 768), BF16).expand(40, 768), _rand(rng, (40, 768), BF16)

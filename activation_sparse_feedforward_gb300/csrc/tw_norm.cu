@@ -104,8 +104,7 @@ struct RowMap {
       }
     }
   }
-  // f(pair) for the pairs of vectors in the row; where a vector may be in it in part, what f
-  // adds to elements that read 0 is masked by keep()
+  // f(pair) for the pairs of vectors in the row, at least in part
   template <class F>
   TW_DEV void each(F f) const {
 #pragma unroll
@@ -116,9 +115,16 @@ struct RowMap {
       }
   }
   TW_DEV bool in(int i) const { return col(i) < d; }
-  TW_DEV float2 keep(int i, float2 v) const {
-    if constexpr (!VEC) v = make_float2(in(2 * i) ? v.x : 0.f, in(2 * i + 1) ? v.y : 0.f);
-    return v;
+  // 0 in the places past the row of a vector that is in it in part
+  TW_DEV void trim(float2 (&v)[NP]) const {
+    if constexpr (VEC) return;
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+      if (has(k * E) && !in(k * E + E - 1)) {
+#pragma unroll
+        for (int i = k * E / 2; i < (k + 1) * E / 2; ++i)
+          v[i] = make_float2(in(2 * i) ? v[i].x : 0.f, in(2 * i + 1) ? v[i].y : 0.f);
+      }
   }
 };
 
@@ -217,7 +223,7 @@ struct Ring {
       for (int k = 0; k < NV; ++k) {
         const int g = k * m.tpr() + m.tid, left = m.d - g * E;
         uint4 r = make_uint4(0, 0, 0, 0);
-        if (left > 0) r = first_of<DT>(shifted<DT>(from[g], from[g + 1], lead), left);
+        if (left > 0) r = first_of<DT>(shifted_from<DT>(from + g, lead), left);
         M::widen16(r, v + k * E / 2);
       }
     }
@@ -297,10 +303,10 @@ __global__ void __launch_bounds__(MAXT, fwd_ctas(MAXT)) norm_fwd_kernel(const No
       }
     }
     float2 q = both(0.f);
-    m.each([&](int i) {
-      v[i] = m.keep(i, add2(v[i], both(-mean)));
-      q = fma2(v[i], v[i], q);
-    });
+#pragma unroll
+    for (int i = 0; i < NP; ++i) v[i] = add2(v[i], both(-mean));
+    m.trim(v);
+    m.each([&](int i) { q = fma2(v[i], v[i], q); });
     const float rstd = rsqrtf(team_sum(q.x + q.y, red[1][team], team, tpr, tid) * inv_d + a.eps);
 #pragma unroll
     for (int i = 0; i < NP; ++i) v[i] = fma2(mul2(v[i], both(rstd)), w[i], b[i]);
@@ -351,11 +357,12 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwdArgs a) {
 #pragma unroll
   for (int i = 0; i < NP; ++i) dw[i] = db[i] = both(0.f);
   const float inv_d = 1.f / static_cast<float>(a.d);
-  // x becomes xh, g dy w; the thread's parts of the row's two sums, and its column sums
+  // x becomes xh, g dy w; the thread's parts of the row's two sums, and its column sums.
+  // Past the row g is 0, so what xh is there adds nothing.
   auto sums = [&](float2 (&x)[NP], float2 (&g)[NP], float mean, float rstd, float2* to) {
     float2 c1 = both(0.f), c2 = both(0.f);
     m.each([&](int i) {
-      x[i] = m.keep(i, mul2(add2(x[i], both(-mean)), both(rstd)));
+      x[i] = mul2(add2(x[i], both(-mean)), both(rstd));
       dw[i] = fma2(g[i], x[i], dw[i]);
       db[i] = add2(db[i], g[i]);
       g[i] = mul2(g[i], w[i]);
@@ -505,7 +512,7 @@ __global__ void __launch_bounds__(kFewThreads) norm_bwd_few_kernel(const NormBwd
     m.weight(a.w, a.wtype, 1.f, w);
     float2 c1 = both(0.f), c2 = both(0.f);
     m.each([&](int i) {
-      x[i] = m.keep(i, mul2(add2(x[i], both(-mean)), both(rstd)));
+      x[i] = mul2(add2(x[i], both(-mean)), both(rstd));
       g[i] = mul2(g[i], w[i]);
       c1 = add2(c1, g[i]);
       c2 = fma2(g[i], x[i], c2);

@@ -184,6 +184,25 @@ TW_DEV uint4 shifted(const uint4& a, const uint4& b, int shift) {
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
+// The same from two adjacent vectors in shared memory, from the 8 bytes on that hold the
+// first element: fewer words to choose from.
+template <int DT>
+TW_DEV uint4 shifted_from(const uint4* from, int shift) {
+  const uint32_t bytes = shift * sizeof(typename Elem<DT>::S);
+  const uint2* at = reinterpret_cast<const uint2*>(from) + (bytes >> 3);
+  const uint2 a = at[0], b = at[1], c = at[2];
+  const uint32_t w[6] = {a.x, a.y, b.x, b.y, c.x, c.y};
+  uint32_t v[5];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) v[i] = bytes & 4 ? w[i + 1] : w[i];
+  if constexpr (Elem<DT>::E == 8) {
+    const uint32_t half = bytes & 2 ? 0x5432u : 0x3210u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __byte_perm(v[i], v[i + 1], half);
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
 // The first n (1 or more) elements of v, then 0.
 template <int DT>
 TW_DEV uint4 first_of(const uint4& v, int n) {
@@ -224,8 +243,8 @@ TW_DEV uint4 load_any(const typename Elem<DT>::S* p, int n, bool careful) {
 
 // Stores v at p, of which n elements are the row's (0 or fewer: none). All lanes of a warp,
 // whose vectors follow each other in one row: an aligned 16 bytes are written by the lane
-// that holds their end, with the lane before's elements; what is left at the warp's and the
-// row's ends goes out by the element.
+// that holds their end, with the lane before's elements. What is left at a full warp's two
+// ends makes one vector's elements: a lane each. Where the row ends, by the element.
 template <int DT>
 TW_DEV void store_any(typename Elem<DT>::S* p, const uint4& v, int n, int lane) {
   using S = typename Elem<DT>::S;
@@ -234,8 +253,24 @@ TW_DEV void store_any(typename Elem<DT>::S* p, const uint4& v, int n, int lane) 
   const uint4 before = make_uint4(__shfl_up_sync(0xFFFFFFFFu, v.x, 1), __shfl_up_sync(0xFFFFFFFFu, v.y, 1),
                                   __shfl_up_sync(0xFFFFFFFFu, v.z, 1), __shfl_up_sync(0xFFFFFFFFu, v.w, 1));
   const bool whole = (lane > 0 || shift == 0) && n >= head;
-  const bool next = shift > 0 && lane < 31 && n - E >= head;  // the next lane takes this one's end
   if (whole) *reinterpret_cast<uint4*>(p - shift) = shift == 0 ? v : shifted<DT>(before, v, head);
+  if (n - (31 - lane) * E >= E) {  // every lane's vector is whole
+    if (shift == 0) return;
+    const int from = lane < head ? 0 : 31;
+    const uint32_t w[4] = {__shfl_sync(0xFFFFFFFFu, v.x, from), __shfl_sync(0xFFFFFFFFu, v.y, from),
+                           __shfl_sync(0xFFFFFFFFu, v.z, from), __shfl_sync(0xFFFFFFFFu, v.w, from)};
+    if (lane < E) {
+      const int word = lane / (E / 4);
+      const uint32_t a = word & 2 ? w[2] : w[0], b = word & 2 ? w[3] : w[1], c = word & 1 ? b : a;
+      S* q = p + (from - lane) * E + lane;
+      if constexpr (E == 8)
+        *reinterpret_cast<uint16_t*>(q) = static_cast<uint16_t>(lane & 1 ? c >> 16 : c);
+      else
+        *reinterpret_cast<uint32_t*>(q) = c;
+    }
+    return;
+  }
+  const bool next = shift > 0 && lane < 31 && n - E >= head;  // the next lane takes this one's end
   const int from = whole ? head : 0, to = next ? head : min(n, E);
   if (from < to) {
     union {

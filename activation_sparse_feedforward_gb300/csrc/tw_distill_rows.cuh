@@ -118,14 +118,14 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows_kernel(const Disti
       }
       sums.add(r);
     };
+    const bool first = p.template first_edge<NT>(), last = p.template last_edge<NT>();
+    const uint4 e0 = first ? p.edge(0) : no_vector<DT>(), e1 = last ? p.edge(p.n - 1) : no_vector<DT>();
     ring.sweep(p, [&](uint4 (&r)[kBatch], int j) {
       const int at[kBatch] = {j, j + NT, j + 2 * NT, j + 3 * NT};
       add(r, at);
     });
-    if (p.template first_edge<NT>() || p.template last_edge<NT>()) {
-      const bool first = p.template first_edge<NT>(), last = p.template last_edge<NT>();
-      uint4 r[kBatch] = {first ? p.edge(0) : no_vector<DT>(), last ? p.edge(p.n - 1) : no_vector<DT>(), no_vector<DT>(),
-                         no_vector<DT>()};
+    if (first || last) {
+      uint4 r[kBatch] = {e0, e1, no_vector<DT>(), no_vector<DT>()};
       const int at[kBatch] = {first ? 0 : p.n, last ? p.n - 1 : p.n, p.n, p.n};
       add(r, at);
     }
@@ -163,7 +163,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows_kernel(const Disti
               if (all.value || j + i * NT < p.hi) store_last(out + j + i * NT, f(r[i]));
           });
         } else {
-          store_shifted<DT, NT>(p, dz, p.lo, p.hi, [&](int j) { return src[j]; }, f);
+          store_shifted<DT, NT>(p, dz, p.lo, p.hi, [&](int j) { return src[j]; },
+                                [&](int j, int shift) { return shifted<DT>(src[j], src[j + 1], shift); }, f);
         }
         if (p.template first_edge<NT>()) singly(p.edge(0), 0);
         if (p.template last_edge<NT>()) singly(p.edge(p.n - 1), p.n - 1);

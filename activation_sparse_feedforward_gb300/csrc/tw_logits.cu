@@ -118,7 +118,8 @@ TW_DEV void store_slice(const Slice<DT>& sl, typename Elem<DT>::S* dz, F f) {
   using S = typename Elem<DT>::S;
   constexpr int E = Elem<DT>::E;
   if (Part<DT>::lead_of(dz) != sl.lead) {
-    store_shifted<DT, kThreads>(sl, dz, 0, sl.n, [&](int j) { return sl.buf[j]; }, f);
+    store_shifted<DT, kThreads>(sl, dz, 0, sl.n, [&](int j) { return sl.buf[j]; },
+                                [&](int j, int shift) { return shifted_from<DT>(sl.buf + j, shift); }, f);
     return;
   }
   auto singly = [&](int j) {
@@ -464,6 +465,9 @@ TW_DEV ProbStat own_probs(const Part<DT>& p, float c, const ProbRing<DT, NT>& ri
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) highs[c * NT] = 0;
   }
+  // the edges, one vector of the first thread and one of the last, come while the row does
+  const bool first = p.template first_edge<NT>(), last = p.template last_edge<NT>();
+  const uint4 e0 = first ? p.edge(0) : no_vector<DT>(), e1 = last ? p.edge(p.n - 1) : no_vector<DT>();
   ring.sweep(p, [&](const uint4 (&r)[kBatch], int) {
     batch(r);
     if (highs != nullptr) {  // kept as the chunk goes: the last one may be short
@@ -476,12 +480,8 @@ TW_DEV ProbStat own_probs(const Part<DT>& p, float c, const ProbRing<DT, NT>& ri
       }
     }
   });
-  if (p.lo > 0 || p.hi < p.n) {  // the edges: one vector of the first thread, one of the last
-    uint4 r[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) r[i] = no_vector<DT>();
-    if (p.template first_edge<NT>()) r[0] = p.edge(0);
-    if (p.template last_edge<NT>()) r[1] = p.edge(p.n - 1);
+  if (first || last) {
+    const uint4 r[kBatch] = {e0, e1, no_vector<DT>(), no_vector<DT>()};
     batch(r);
   }
   ProbStat st;

@@ -458,10 +458,11 @@ TW_DEV uint4 gradient(const uint4& r, const Scale& a, const Scale& b, float u, f
   return El::pack_pairs(v);
 }
 // Stores f of the vectors [lo, hi) of a part, which get(j) reads, at their columns of a row
-// that lies otherwise against 16 bytes: each vector stored is put together from two. (One
+// that lies otherwise against 16 bytes: each vector stored is put together from two, by
+// both(j, shift). (One
 // element at a time, 3358 x 120602 bf16 took 965 us, most of it partial writes in L2.)
-template <int DT, int NT, class G, class F>
-TW_DEV void store_shifted(const Part<DT>& p, typename Elem<DT>::S* dz, int lo, int hi, G get, F f) {
+template <int DT, int NT, class G, class B, class F>
+TW_DEV void store_shifted(const Part<DT>& p, typename Elem<DT>::S* dz, int lo, int hi, G get, B both, F f) {
   using S = typename Elem<DT>::S;
   constexpr int E = Elem<DT>::E;
   const int shift = (p.lead - Part<DT>::lead_of(dz)) & (E - 1), first = p.col(lo) + shift;
@@ -474,7 +475,7 @@ TW_DEV void store_shifted(const Part<DT>& p, typename Elem<DT>::S* dz, int lo, i
   };
 #pragma unroll 2
   for (int i = threadIdx.x; i < hi - lo - 1; i += NT) {
-    const uint4 r = shifted<DT>(get(lo + i), get(lo + i + 1), shift);
+    const uint4 r = both(lo + i, shift);
     const int c = first + i * E;
     if (c >= 0 && c + E <= p.V)
       *reinterpret_cast<uint4*>(dz + c) = f(r);

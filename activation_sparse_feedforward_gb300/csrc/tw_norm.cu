@@ -667,9 +667,9 @@ bool overlap(const NormBwdArgs& a, const void* p, int64_t ld) {
 }
 
 // Up to so many rows: one launch (norm_bwd_few_kernel). 77 rows of 2048 bf16 take 2.7 us
-// against 6 in two; the two meet between 250 (512 columns) and 430 rows (8192), and at 80
-// where single elements are loaded.
-constexpr int kFewRows = 320, kFewRowsSingly = 80;
+// against 6 in two; the two meet between 250 (512 columns) and 430 rows (8192), and at 200
+// rows off 16 bytes.
+constexpr int kFewRows = 320, kFewRowsOff16 = 160;
 template <int DT, bool VEC>
 cudaError_t norm_bwd_few(const NormBwdArgs& a, cudaStream_t s) {
   const int vpt = a.d <= 4096 ? 1 : 2;
@@ -715,6 +715,7 @@ cudaError_t norm_fwd_width(const NormFwdArgs& a, cudaStream_t s) {
     if (a.d <= 16 * 128) return norm_fwd_ring<DT, 128, 256, 2, false>(a, s);
     if (a.d <= 16 * 192) return norm_fwd_ring<DT, 192, 192, 2, false>(a, s);
     if (a.d <= 16 * 256) return norm_fwd_ring<DT, 256, 256, 2, false>(a, s);
+    if (a.d <= 16 * 320) return norm_fwd_ring<DT, 320, 320, 2, false>(a, s);
     if (a.d <= 16 * 384) return norm_fwd_ring<DT, 384, 384, 2, false>(a, s);
     if (a.d <= 16 * 512) return norm_fwd_ring<DT, 512, 512, 2, false>(a, s);
     return norm_fwd_direct<DT, 2, false, 1024>(a, s);
@@ -723,7 +724,7 @@ cudaError_t norm_fwd_width(const NormFwdArgs& a, cudaStream_t s) {
 template <int DT, bool VEC>
 cudaError_t norm_bwd_width(const NormBwdArgs& a, cudaStream_t s) {
   // (its column sums read x and dy while rows of dx are written: not in place of them)
-  if (a.T <= (VEC ? kFewRows : kFewRowsSingly) && a.d <= 8192 && !overlap(a, a.x, a.ldx) && !overlap(a, a.dy, a.lddy))
+  if (a.T <= (VEC ? kFewRows : kFewRowsOff16) && a.d <= 8192 && !overlap(a, a.x, a.ldx) && !overlap(a, a.dy, a.lddy))
     return norm_bwd_few<DT, VEC>(a, s);
   if constexpr (VEC) {
     constexpr int kDepth = DT == TW_F32 ? 2 : 4;

@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows_kernel(const Disti
   }
   if (a.loss == nullptr) return;
   const float share = warp_sum(
-      loss_share<HARD>(a, st, c0, l, target, NT, tid == 0, tid == 0 && label >= 0, z_label, [](int) { return true; }));
+      loss_share<HARD>(a, st, l, target, NT, tid == 0, tid == 0 && label >= 0, z_label, [](int) { return true; }));
   if (lane == 0) shares[warp] = share;
   __syncthreads();
   if (warp != 0) return;

@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillArgs 
   const bool holds_label = label >= 0 && sl.element(label) != nullptr;
   const float z_label = !holds_label ? 0.f : label_entry >= 0 ? l.z[label_entry] : El::get(*sl.element(label));
   if (a.loss != nullptr) {
-    float share = loss_share<HARD>(a, st, c0, l, target, kThreads, rank == 0 && tid == 0, holds_label && tid == 0, z_label,
+    float share = loss_share<HARD>(a, st, l, target, kThreads, rank == 0 && tid == 0, holds_label && tid == 0, z_label,
                                    [&](int i) { return sl.element(i) != nullptr; });
     share = warp_sum(share);
     if (lane == 0) {

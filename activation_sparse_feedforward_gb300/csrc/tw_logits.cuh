@@ -338,15 +338,15 @@ TW_DEV float teacher_logit(const DistillArgs& a, size_t e) {
 
 // What a row is to learn, beside its list.
 struct Target {
-  bool some;              // the teacher has mass
-  float p_rest, lp_rest;  // P and log2 P of the rest
+  bool some;          // the teacher has mass
+  float sum, p_rest;  // sum over its classes of e^(logit - the largest), and P of the rest
   int label;
-  float up;               // the upstream gradient
-  float z_label;          // z at the label (kept by the kernels that need it)
+  float up;           // the upstream gradient
+  float z_label;      // z at the label (kept by the kernels that need it)
 };
 // A row's list in shared memory: the token (after the marking -2 - token where the entry
-// does not own its place), log2 P (at first the teacher's logit over the temperature), P,
-// and z at the token.
+// does not own its place), the teacher's logit over the temperature (after
+// teacher_distribution less the largest), P, and z at the token.
 struct List {
   int* idx;
   float *lp, *p, *z;
@@ -359,7 +359,7 @@ struct List {
 constexpr int kListBytes = 16;  // an entry
 
 // By one warp: the teacher's distribution over the list, whose logits are in l.lp, and the
-// rest, into l.p, l.lp and the target.
+// rest, into l.p and the target.
 TW_DEV void teacher_distribution(const List& l, int K, float t_rest, Target* target) {
   const int lane = threadIdx.x & 31;
   float tm = t_rest;
@@ -373,15 +373,15 @@ TW_DEV void teacher_distribution(const List& l, int K, float t_rest, Target* tar
   }
   const float e_rest = exp_of(t_rest, tm, kLog2e);
   ts = warp_sum(ts) + e_rest;
-  const float inv = 1.f / ts, l2 = log2f(ts);
+  const float inv = 1.f / ts;
   for (int k = lane; k < K; k += 32) {
     l.p[k] *= inv;
-    l.lp[k] = (l.lp[k] - tm) * kLog2e - l2;
+    l.lp[k] -= tm;
   }
   if (lane == 0) {
     target->some = ts != 0.f;  // NaN counts as some
     target->p_rest = ts != 0.f ? e_rest * inv : 0.f;
-    target->lp_rest = (t_rest - tm) * kLog2e - l2;
+    target->sum = ts;
   }
 }
 
@@ -459,8 +459,8 @@ TW_DEV uint4 gradient(const uint4& r, const Scale& a, const Scale& b, float u, f
 }
 // Stores f of the vectors [lo, hi) of a part, which get(j) reads, at their columns of a row
 // that lies otherwise against 16 bytes: each vector stored is put together from two, by
-// both(j, shift). (One
-// element at a time, 3358 x 120602 bf16 took 965 us, most of it partial writes in L2.)
+// both(j, shift). (One element at a time, 3358 x 120602 bf16 took 965 us, most of it partial
+// writes in L2; this 396.)
 template <int DT, int NT, class G, class B, class F>
 TW_DEV void store_shifted(const Part<DT>& p, typename Elem<DT>::S* dz, int lo, int hi, G get, B both, F f) {
   using S = typename Elem<DT>::S;
@@ -489,22 +489,25 @@ TW_DEV void store_shifted(const Part<DT>& p, typename Elem<DT>::S* dz, int lo, i
 
 // A row's loss from its statistics, in units of log2: the terms of the entries for which
 // here(k, token) holds, by the threads that fill them; the rest's and the label's by
-// the threads told so.
+// the threads told so. log P - log q is taken from the logits' distances to their largest
+// and from quotients of the sums: all are small where teacher and student agree, while
+// each logarithm by itself rounds at its own size.
 template <int HARD, class F>
-TW_DEV float loss_share(const DistillArgs& a, const DistillStat& st, float c0, const List& l, const Target& t, int threads,
+TW_DEV float loss_share(const DistillArgs& a, const DistillStat& st, const List& l, const Target& t, int threads,
                         bool takes_rest, bool takes_label, float z_label, F here) {
-  const float b = base_of(st.M), total = st.rest + st.list, l2 = log2f(total);
+  const float b = base_of(st.M), total = st.rest + st.list;
   float share = 0.f;
   if (t.some) {
+    const float ratio = log2f(total / t.sum);
     for (int k = threadIdx.x; k < a.K; k += threads) {
       const int i = l.idx[k] >= 0 ? l.idx[k] : -2 - l.idx[k];
       const float p = l.p[k];
-      if (i >= 0 && p != 0.f && here(i)) share += p * (l.lp[k] - ((l.z[k] - b) * c0 - l2));
+      if (i >= 0 && p != 0.f && here(i)) share += p * fmaf(l.lp[k] - (l.z[k] - b) / a.temperature, kLog2e, ratio);
     }
-    if (takes_rest && t.p_rest != 0.f) share += t.p_rest * (t.lp_rest - (log2f(st.rest) - l2));
+    if (takes_rest && t.p_rest != 0.f) share += t.p_rest * log2f(t.p_rest * total / st.rest);
     share *= a.kd_weight * a.temperature * a.temperature;
   }
-  if (takes_label) share += a.ce_weight * (log2f(HARD != kNoSum ? st.s1 : total) - (z_label - b) * kLog2e);
+  if (takes_label) share += a.ce_weight * fmaf(b - z_label, kLog2e, log2f(HARD != kNoSum ? st.s1 : total));
   return share;
 }
 

@@ -10,8 +10,8 @@
 //
 // Bound: HBM, one read of the logits and, with a gradient, one write. Measured on one GB300
 // against the copy rate (6681 GB/s): log probabilities 8192 x 65536 bf16 with five
-// alternatives 168 us (0.96); distillation 4096 x 131072 bf16, K = 64, temperature 2, rest
-// and labels 433 us (0.74), fp32 1023 x 50011, K = 33, 93 us (0.66). What keeps the
+// alternatives 167 us (0.96); distillation 4096 x 131072 bf16, K = 64, temperature 2, rest
+// and labels 430 us (0.75), fp32 1023 x 50011, K = 33, 92 us (0.66). What keeps the
 // distillation from the copy rate are the steps between a slice's sweeps: of the 11.4 us a
 // CTA takes for 64 KB (three on an SM) 2.9 pass until the copies are issued and the target
 // taken, 0.6 with the listed entries, 1.9 with the sums, 2.1 with joining the cluster's

@@ -288,8 +288,9 @@ struct Sums {
     const bool some = run.limit > neg_inf_f();
     if (run.grow(r, slack())) {
       const Scale to = scale_at(run.top.get());
-      s0 = some ? mul2(s0, both(exp2_fast(a.move(to)))) : both(0.f);
-      if (HARD != kNoSum) s1 = some ? mul2(s1, both(exp2_fast(hard(a).move(hard(to))))) : both(0.f);
+      // a factor of 0, not a sum set to 0, where only -inf came before: a NaN among them stays
+      s0 = mul2(s0, both(some ? exp2_fast(a.move(to)) : 0.f));
+      if (HARD != kNoSum) s1 = mul2(s1, both(some ? exp2_fast(hard(a).move(hard(to))) : 0.f));
       a = to;
     }
     if (a.fused)

@@ -95,8 +95,8 @@ TW_DEV void owners(const Slice<DT>& sl, int K, int* l_idx, float* l_z, int label
   for (int k = threadIdx.x; k < K; k += kThreads, ++n) {
     const int i = -2 - l_idx[k];
     bool own = i >= 0 && sl.element(i) != nullptr;
-    for (int q = 0; own && q < K; ++q) {
-      if (l_idx[q] == i) l_z[k] = l_z[q], own = false;
+    for (int q = 0; i >= 0 && q < K; ++q) {
+      if (l_idx[q] == i) l_z[k] = l_z[q], own = false;  // wherever the owner stands in the list
       if (q < k && l_idx[q] == -2 - i) own = false;
     }
     owns |= own ? 1u << n : 0u;

@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows_kernel(const Disti
   }
 
   // Listed tokens leave the sums of the rest: an entry marks its token, and the first to do
-  // so owns it.
+  // so owns it; where tokens are listed twice, the lowest entry.
   bool dup = false;
   for (int k = tid; k < K; k += NT) {
     int i = k == tid ? i_first : a.t_idx[row * K + k];
@@ -97,6 +97,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows_kernel(const Disti
     if (owner && i == label) label_entry = k;
   }
   if (K > 0) dup = __syncthreads_or(dup);
+  if (dup) lowest_own<NT>(l, K, label, &label_entry, [](int) { return true; });
   if (warp == kWarps - 1) {  // the teacher's distribution, read by the others after the sums
     teacher_distribution(l, K, a.t_rest != nullptr ? a.t_rest[row] : neg_inf_f(), &target);
     if (lane == 0) target.up = a.scale * (a.dloss != nullptr ? a.dloss[row] : 1.f), target.label = label;

@@ -84,33 +84,6 @@ TW_DEV DistillStat own_sums(const Slice<DT>& sl, float c0) {
   return sums.get();
 }
 
-// The rare part of the marking, by the whole CTA: entries that found -inf at their token.
-// The lowest of those whose token no other entry took owns it (its logit is masked);
-// the others learn the logit from the owner.
-template <int DT>
-TW_DEV void owners(const Slice<DT>& sl, int K, int* l_idx, float* l_z, int label, int* label_entry) {
-  __syncthreads();
-  uint32_t owns = 0;  // a bit for each of the thread's entries: at most 1024 / 64
-  int n = 0;
-  for (int k = threadIdx.x; k < K; k += kThreads, ++n) {
-    const int i = -2 - l_idx[k];
-    bool own = i >= 0 && sl.element(i) != nullptr;
-    for (int q = 0; i >= 0 && q < K; ++q) {
-      if (l_idx[q] == i) l_z[k] = l_z[q], own = false;  // wherever the owner stands in the list
-      if (q < k && l_idx[q] == -2 - i) own = false;
-    }
-    owns |= own ? 1u << n : 0u;
-  }
-  __syncthreads();
-  n = 0;
-  for (int k = threadIdx.x; k < K; k += kThreads, ++n)
-    if (owns >> n & 1u) {
-      l_idx[k] = -2 - l_idx[k];
-      if (l_idx[k] == label) *label_entry = k;
-    }
-  __syncthreads();
-}
-
 // f of the slice's vectors, stored at their columns of dz; each thread takes its own where
 // dz's row lies against 16 bytes as z's does.
 template <int DT, class F>
@@ -175,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillArgs 
 
   // Listed tokens leave the row: an entry takes the token's logit and puts -inf in its
   // place. Whoever finds -inf there comes second (a token listed twice), or the logit was
-  // masked: owners() sorts that out.
+  // masked: lowest_own() sorts that out.
   cp_wait<0>();
   __syncthreads();
   const int label = target.label;
@@ -193,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillArgs 
       if (owner && i == label) label_entry = k;
     }
     dup = __syncthreads_or(dup);
-    if (dup) owners(sl, K, l.idx, l.z, label, &label_entry);
+    if (dup) lowest_own<kThreads>(l, K, label, &label_entry, [&](int i) { return sl.element(i) != nullptr; });
   }
 
   // the row's statistics

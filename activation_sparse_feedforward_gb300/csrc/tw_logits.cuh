@@ -359,6 +359,38 @@ struct List {
 };
 constexpr int kListBytes = 16;  // an entry
 
+// The rare part of the marking, by the whole CTA of NT threads: of the entries that name one
+// token (here(token): in this CTA's part of the row) the lowest owns it, whichever thread
+// came to the token first, so that sums are taken in one order; the others learn the token's
+// logit from whom had it. Entries that found a masked token have no owner among them yet.
+template <int NT, class H>
+TW_DEV void lowest_own(const List& l, int K, int label, int* label_entry, H here) {
+  static_assert(1024 / NT <= 32, "a bit for each of a thread's entries");
+  auto token = [&](int k) { return l.idx[k] >= 0 ? l.idx[k] : -2 - l.idx[k]; };
+  __syncthreads();
+  uint32_t owns = 0;
+  int n = 0;
+  for (int k = threadIdx.x; k < K; k += NT, ++n) {
+    const int i = token(k);
+    bool own = i >= 0 && here(i);
+    for (int q = 0; i >= 0 && q < K; ++q) {
+      const int at = l.idx[q];
+      if (at == i && q != k) l.z[k] = l.z[q];
+      if (q < k && (at == i || at == -2 - i)) own = false;
+    }
+    owns |= own ? 1u << n : 0u;
+  }
+  __syncthreads();
+  n = 0;
+  for (int k = threadIdx.x; k < K; k += NT, ++n) {
+    const int i = token(k);
+    const bool own = owns >> n & 1u;
+    l.idx[k] = own ? i : -2 - i;
+    if (own && i == label) *label_entry = k;
+  }
+  __syncthreads();
+}
+
 // By one warp: the teacher's distribution over the list, whose logits are in l.lp, and the
 // rest, into l.p and the target.
 TW_DEV void teacher_distribution(const List& l, int K, float t_rest, Target* target) {

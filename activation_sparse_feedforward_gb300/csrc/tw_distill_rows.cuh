@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows_kernel(const Disti
   using Ring = RowRing<DT, NT, kRowDepth>;
   constexpr int E = El::E, kWarps = NT / 32;
   extern __shared__ uint4 smem[];
-  __shared__ float4 stats[kWarps];
+  __shared__ SoftSum stats[kWarps], list;
   __shared__ float shares[kWarps];
   __shared__ Target target;
   __shared__ DistillStat row_stat;
@@ -130,15 +130,17 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows_kernel(const Disti
       const int at[kBatch] = {first ? 0 : p.n, last ? p.n - 1 : p.n, p.n, p.n};
       add(r, at);
     }
-    DistillStat st = sums.get();
-    if (K > 0) add_listed<HARD>(st, c0, K, NT, l.idx, l.z);
-    st = join<HARD>(st, c0);
-    if (lane == 0) stats[warp] = make_float4(st.M, st.rest, st.list, st.s1);
+    const SoftSum own = join<HARD>(sums.get(), c0);
+    if (lane == 0) stats[warp] = own;
+    if (warp == 0) {
+      const SoftSum of_list = list_sums<HARD, 0>(l, K, c0);
+      if (lane == 0) list = of_list;
+    }
   }
   __syncthreads();
   {
-    const float4 part = lane < kWarps ? stats[lane] : make_float4(neg_inf_f(), 0.f, 0.f, 0.f);
-    const DistillStat st = join<HARD>(DistillStat{part.x, part.y, part.z, part.w}, c0);
+    const SoftSum rest = join<HARD>(lane < kWarps ? stats[lane] : SoftSum::none(), c0);
+    const DistillStat st = row_stat_of<HARD>(rest, list, c0);
     if (tid == 0) row_stat = st;  // for after the sweep, which wants the registers
     if (a.dz != nullptr) {
       S* dz = static_cast<S*>(a.dz) + row * a.lddz;
@@ -181,18 +183,18 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_rows_kernel(const Disti
     const Gradient<HARD> g(a, st, c0, target);
     if (some && !g.zero) {
       for (int k = tid; k < K; k += NT)
-        if (l.idx[k] >= 0) dz[l.idx[k]] = El::put(g.listed(l, K, k, label, dup));
+        if (l.idx[k] >= 0) dz[l.idx[k]] = El::put(g.listed(st, l, K, k, label, dup));
     }
     if (tid == 0 && label >= 0 && (label_entry < 0 || !some) && !g.zero) dz[label] = El::put(g.at_label(z_label));
   }
   if (a.loss == nullptr) return;
   const float share = warp_sum(
-      loss_share<HARD>(a, st, l, target, NT, tid == 0, tid == 0 && label >= 0, z_label, [](int) { return true; }));
+      loss_share(a, st, l, target, NT, tid == 0, tid == 0 && label >= 0, z_label, [](int) { return true; }));
   if (lane == 0) shares[warp] = share;
   __syncthreads();
   if (warp != 0) return;
-  const float loss = kLn2 * warp_sum(lane < kWarps ? shares[lane] : 0.f), total = st.rest + st.list;
-  if (lane == 0) a.loss[row] = !some && label < 0 ? 0.f : total == 0.f ? __int_as_float(0x7F800000) : loss;
+  const float loss = warp_sum(lane < kWarps ? shares[lane] : 0.f);
+  if (lane == 0) a.loss[row] = !some && label < 0 ? 0.f : st.total == 0.f ? __int_as_float(0x7F800000) : loss;
 }
 
 template <int DT, int NT>

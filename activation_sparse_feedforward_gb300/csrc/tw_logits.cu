@@ -68,7 +68,7 @@ struct Slice : Part<DT> {
 
 // The thread's own vectors of the slice in one sweep.
 template <int DT, int HARD>
-TW_DEV DistillStat own_sums(const Slice<DT>& sl, float c0) {
+TW_DEV SoftSum own_sums(const Slice<DT>& sl, float c0) {
   Sums<DT, HARD> sums(c0);
   in_batches<kThreads>(sl.lo, sl.hi, [&](int j, auto all) {
     uint4 r[kBatch];
@@ -122,6 +122,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillArgs 
   using S = typename El::S;
   extern __shared__ uint4 smem[];
   __shared__ float4 stats[kMaxCluster * kWarps];
+  __shared__ float4 lists[kMaxCluster];
   __shared__ float shares[kMaxCluster * kWarps];
   __shared__ Target target;
   __shared__ int label_entry;
@@ -169,33 +170,44 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillArgs 
     if (dup) lowest_own<kThreads>(l, K, label, &label_entry, [&](int i) { return sl.element(i) != nullptr; });
   }
 
-  // the row's statistics
-  DistillStat st = own_sums<DT, HARD>(sl, c0);
-  if (some) add_listed<HARD>(st, c0, K, kThreads, l.idx, l.z);
-  st = join<HARD>(st, c0);
-  const float4 mine = make_float4(st.M, st.rest, st.list, st.s1);
+  // the row's statistics: every warp's sums of its own tokens, and first the last warp's of the list
+  const SoftSum none = SoftSum::none();
+  auto packed = [](const SoftSum& v) { return make_float4(v.M, v.s, v.s1, 0.f); };
+  auto unpacked = [](const float4& v) { return SoftSum{v.x, v.y, v.z}; };
+  const bool takes_list = warp == kWarps - 1;
+  const SoftSum own_list = takes_list && some ? list_sums<HARD, 4>(l, K, c0) : none;
+  const SoftSum own = join<HARD>(own_sums<DT, HARD>(sl, c0), c0);
   if (cluster > 1) {
     cluster_wait();
-    if (lane < cluster) st_cluster_v4(peer_smem_addr(&stats[rank * kWarps + warp], lane), mine);
+    if (lane < cluster) {
+      st_cluster_v4(peer_smem_addr(&stats[rank * kWarps + warp], lane), packed(own));
+      if (takes_list) st_cluster_v4(peer_smem_addr(&lists[rank], lane), packed(own_list));
+    }
     cluster_barrier();
   } else {
-    if (lane == 0) stats[warp] = mine;
+    if (lane == 0) {
+      stats[warp] = packed(own);
+      if (takes_list) lists[0] = packed(own_list);
+    }
     __syncthreads();
   }
   const int parts = cluster * kWarps;
-  auto part = [&](int i) {
-    const float4 s = i < parts ? stats[i] : make_float4(neg_inf_f(), 0.f, 0.f, 0.f);
-    return DistillStat{s.x, s.y, s.z, s.w};
-  };
-  st = part(lane);
-  if (parts > 32) st = join_two<HARD>(st, part(lane + 32), c0);
-  st = join<HARD>(st, c0);
+  auto part = [&](int i) { return i < parts ? unpacked(stats[i]) : none; };
+  SoftSum rest = part(lane);
+  if (parts > 32) rest = join_two<HARD>(rest, part(lane + 32), c0);
+  rest = join<HARD>(rest, c0);
+  SoftSum list = none;
+  if (some) {
+    const int r = lane % kMaxCluster;
+    list = cluster == 1 ? unpacked(lists[0]) : join<HARD, kMaxCluster>(r < cluster ? unpacked(lists[r]) : none, c0);
+  }
+  const DistillStat st = row_stat_of<HARD>(rest, list, c0);
 
   const bool holds_label = label >= 0 && sl.element(label) != nullptr;
   const float z_label = !holds_label ? 0.f : label_entry >= 0 ? l.z[label_entry] : El::get(*sl.element(label));
   if (a.loss != nullptr) {
-    float share = loss_share<HARD>(a, st, l, target, kThreads, rank == 0 && tid == 0, holds_label && tid == 0, z_label,
-                                   [&](int i) { return sl.element(i) != nullptr; });
+    float share = loss_share(a, st, l, target, kThreads, rank == 0 && tid == 0, holds_label && tid == 0, z_label,
+                             [&](int i) { return sl.element(i) != nullptr; });
     share = warp_sum(share);
     if (lane == 0) {
       if (cluster > 1)
@@ -213,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillArgs 
     __syncthreads();  // the listed tokens and the label overwrite what the sweep stored
     if (some && !g.zero) {
       for (int k = tid; k < K; k += kThreads)
-        if (l.idx[k] >= 0) dz[l.idx[k]] = El::put(g.listed(l, K, k, label, dup));
+        if (l.idx[k] >= 0) dz[l.idx[k]] = El::put(g.listed(st, l, K, k, label, dup));
     }
     if (tid == 0 && holds_label && label_entry < 0 && !g.zero) dz[label] = El::put(g.at_label(z_label));
   }
@@ -224,9 +236,8 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillArgs 
     __syncthreads();
   if (rank == 0 && warp == 0 && a.loss != nullptr) {
     float loss = (lane < parts ? shares[lane] : 0.f) + (lane + 32 < parts ? shares[lane + 32] : 0.f);
-    loss = kLn2 * warp_sum(loss);
-    const float total = st.rest + st.list;
-    if (lane == 0) a.loss[row] = !some && label < 0 ? 0.f : total == 0.f ? __int_as_float(0x7F800000) : loss;
+    loss = warp_sum(loss);
+    if (lane == 0) a.loss[row] = !some && label < 0 ? 0.f : st.total == 0.f ? __int_as_float(0x7F800000) : loss;
   }
 }
 

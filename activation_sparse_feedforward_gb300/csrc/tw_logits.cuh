@@ -29,9 +29,15 @@ TW_DEV float exp_of(float z, float base, float c) { return exp2_fast((z - base) 
 // over groups of W lanes
 template <int W = 32>
 TW_DEV float warp_max(float v) {
+  if constexpr (W == 32) {  // one instruction; a NaN loses to a number, as with fmaxf
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+  } else {
 #pragma unroll
-  for (int o = W / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-  return v;
+    for (int o = W / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
+  }
 }
 template <int W>
 TW_DEV float group_sum(float v) {
@@ -207,9 +213,13 @@ struct RowRing {
 // kOwnSum at any other temperature.
 constexpr int kNoSum = 0, kOwnSum = 1;
 
-struct DistillStat {
-  float M, rest, list;  // sums at the temperature over the unlisted and the listed tokens
-  float s1;             // at temperature 1 over all (not with kNoSum)
+// The listed and the unlisted tokens' sums each have a reference of their own: against the
+// row's largest logit the unlisted ones' would be 0 where the list lies far above them, and
+// log q_rest and q / q_rest with it.
+struct SoftSum {
+  float M, s;  // the largest logit, and the sum at the temperature against it
+  float s1;    // the sum at temperature 1 (not with kNoSum)
+  static TW_DEV SoftSum none() { return {neg_inf_f(), 0.f, 0.f}; }
 };
 
 // The scale at temperature 1 beside `a` at the temperature. (c is log2(e) / HARD, an
@@ -221,25 +231,40 @@ TW_DEV Scale hard_scale(const Scale& a) {
   return b;
 }
 
-// Joins one DistillStat per lane (M = -inf, sums 0 in unused lanes); all lanes get it.
-template <int HARD>
-TW_DEV DistillStat join(DistillStat a, float c0) {
-  DistillStat r;
-  r.M = warp_max(a.M);
-  const float base = base_of(r.M), f0 = exp_of(a.M, base, c0);
-  r.rest = warp_sum(a.rest * f0);
-  r.list = warp_sum(a.list * f0);
-  r.s1 = HARD != kNoSum ? warp_sum(a.s1 * exp_of(a.M, base, kLog2e)) : 0.f;
+// Joins one SoftSum per lane of groups of W lanes; all of them get it.
+template <int HARD, int W = 32>
+TW_DEV SoftSum join(SoftSum a, float c0) {
+  SoftSum r;
+  r.M = warp_max<W>(a.M);
+  const float base = base_of(r.M);
+  r.s = group_sum<W>(a.s * exp_of(a.M, base, c0));
+  r.s1 = HARD != kNoSum ? group_sum<W>(a.s1 * exp_of(a.M, base, kLog2e)) : 0.f;
   return r;
 }
 template <int HARD>
-TW_DEV DistillStat join_two(DistillStat a, DistillStat b, float c0) {
-  DistillStat r;
+TW_DEV SoftSum join_two(SoftSum a, SoftSum b, float c0) {
+  SoftSum r;
   r.M = fmaxf(a.M, b.M);
-  const float base = base_of(r.M), fa = exp_of(a.M, base, c0), fb = exp_of(b.M, base, c0);
-  r.rest = a.rest * fa + b.rest * fb;
-  r.list = a.list * fa + b.list * fb;
+  const float base = base_of(r.M);
+  r.s = a.s * exp_of(a.M, base, c0) + b.s * exp_of(b.M, base, c0);
   r.s1 = HARD != kNoSum ? a.s1 * exp_of(a.M, base, kLog2e) + b.s1 * exp_of(b.M, base, kLog2e) : 0.f;
+  return r;
+}
+// A row's statistics.
+struct DistillStat {
+  float M, total;        // the largest logit of all, and the sum over all against it
+  float rest_top, rest;  // the unlisted tokens' largest logit and sum
+  float rest_near;       // that sum against M
+  float s1;              // at temperature 1 over all, against M (total with kNoSum, where that is wanted)
+};
+template <int HARD>
+TW_DEV DistillStat row_stat_of(const SoftSum& rest, const SoftSum& list, float c0) {
+  DistillStat r;
+  const SoftSum all = join_two<HARD>(rest, list, c0);
+  r.M = all.M, r.total = all.s;
+  r.rest_top = rest.M, r.rest = rest.s;
+  r.rest_near = rest.s * exp_of(rest.M, base_of(all.M), c0);
+  r.s1 = HARD != kNoSum ? all.s1 : all.s;
   return r;
 }
 
@@ -298,35 +323,16 @@ struct Sums {
     else
       add_exps<DT, HARD, false>(r, a, hard(a), s0, s1);
   }
-  TW_DEV DistillStat get() const {
-    DistillStat st;
-    st.M = run.top.get();
-    const float base = base_of(st.M);
+  TW_DEV SoftSum get() const {
+    SoftSum r;
+    r.M = run.top.get();
+    const float base = base_of(r.M);
     const Scale b = hard(a);
-    st.rest = add_lanes(s0) * exp2_fast(fmaf(a.m - base, c0, a.shift()));
-    st.list = 0.f;
-    st.s1 = HARD != kNoSum ? add_lanes(s1) * exp2_fast(fmaf(b.m - base, kLog2e, b.shift())) : 0.f;
-    return st;
+    r.s = add_lanes(s0) * exp2_fast(fmaf(a.m - base, c0, a.shift()));
+    r.s1 = HARD != kNoSum ? add_lanes(s1) * exp2_fast(fmaf(b.m - base, kLog2e, b.shift())) : 0.f;
+    return r;
   }
 };
-
-// The list's tokens that the thread owns (l_idx >= 0), added to its sums.
-template <int HARD>
-TW_DEV void add_listed(DistillStat& st, float c0, int K, int threads, const int* l_idx, const float* l_z) {
-  const float was = st.M;
-  for (int k = threadIdx.x; k < K; k += threads)
-    if (l_idx[k] >= 0) st.M = fmaxf(st.M, l_z[k]);
-  const float base = base_of(st.M);
-  if (st.M != was) {
-    st.rest *= exp_of(was, base, c0);
-    if (HARD != kNoSum) st.s1 *= exp_of(was, base, kLog2e);
-  }
-  for (int k = threadIdx.x; k < K; k += threads)
-    if (l_idx[k] >= 0) {
-      st.list += exp_of(l_z[k], base, c0);
-      if (HARD != kNoSum) st.s1 += exp_of(l_z[k], base, kLog2e);
-    }
-}
 
 template <int DT>
 TW_DEV float value_at(const void* p, size_t i) {
@@ -389,6 +395,35 @@ TW_DEV void lowest_own(const List& l, int K, int label, int* label_entry, H here
     if (own && i == label) *label_entry = k;
   }
   __syncthreads();
+}
+
+// By one warp: the sums of the tokens that the list owns (l.idx >= 0); all lanes get them.
+// A lane holds its first FIRST entries' logits between the sweep for the largest and the
+// sums (0: where registers are short).
+template <int HARD, int FIRST>
+TW_DEV SoftSum list_sums(const List& l, int K, float c0) {
+  constexpr int kUnroll = FIRST > 0 ? 4 : 2;
+  const int lane = threadIdx.x & 31;
+  auto owned = [&](int k) { return k < K && l.idx[k] >= 0 ? l.z[k] : neg_inf_f(); };
+  SoftSum r = SoftSum::none();
+  float z[FIRST + 1];  // (+ 1: not empty)
+#pragma unroll
+  for (int n = 0; n < FIRST; ++n) r.M = fmaxf(r.M, z[n] = owned(lane + 32 * n));
+#pragma unroll kUnroll
+  for (int k = lane + 32 * FIRST; k < K; k += 32) r.M = fmaxf(r.M, owned(k));
+  r.M = warp_max(r.M);
+  const float base = base_of(r.M);
+  auto add = [&](float v) {
+    r.s += exp_of(v, base, c0);
+    if (HARD != kNoSum) r.s1 += exp_of(v, base, kLog2e);
+  };
+#pragma unroll
+  for (int n = 0; n < FIRST; ++n) add(z[n]);
+#pragma unroll kUnroll
+  for (int k = lane + 32 * FIRST; k < K; k += 32) add(owned(k));
+  r.s = warp_sum(r.s);
+  if (HARD != kNoSum) r.s1 = warp_sum(r.s1);
+  return r;
 }
 
 // By one warp: the teacher's distribution over the list, whose logits are in l.lp, and the
@@ -520,53 +555,66 @@ TW_DEV void store_shifted(const Part<DT>& p, typename Elem<DT>::S* dz, int lo, i
   if (threadIdx.x == NT - 1) singly(get(hi - 1), p.col(hi - 1), shift, E);
 }
 
-// A row's loss from its statistics, in units of log2: the terms of the entries for which
-// here(k, token) holds, by the threads that fill them; the rest's and the label's by
-// the threads told so. log P - log q is taken from the logits' distances to their largest
-// and from quotients of the sums: all are small where teacher and student agree, while
-// each logarithm by itself rounds at its own size.
-template <int HARD, class F>
+// A row's loss from its statistics: the terms of the entries for which here(k, token)
+// holds, by the threads that fill them; the rest's and the label's by the threads told so.
+// tau (log P - log q), in the logits' own units so that a mask of the type's lowest value
+// stays finite, is taken from the logits' distances to their largest and from quotients of
+// the sums: all are small where teacher and student agree, while each logarithm by itself
+// rounds at its own size.
+template <class F>
 TW_DEV float loss_share(const DistillArgs& a, const DistillStat& st, const List& l, const Target& t, int threads,
                         bool takes_rest, bool takes_label, float z_label, F here) {
-  const float b = base_of(st.M), total = st.rest + st.list;
+  const float tau = a.temperature, b = base_of(st.M);
   float share = 0.f;
   if (t.some) {
-    const float ratio = log2f(total / t.sum);
+    const float ratio = tau * logf(st.total / t.sum);
     for (int k = threadIdx.x; k < a.K; k += threads) {
       const int i = l.idx[k] >= 0 ? l.idx[k] : -2 - l.idx[k];
       const float p = l.p[k];
-      if (i >= 0 && p != 0.f && here(i)) share += p * fmaf(l.lp[k] - (l.z[k] - b) / a.temperature, kLog2e, ratio);
+      if (i >= 0 && p != 0.f && here(i)) share += p * (fmaf(tau, l.lp[k], b - l.z[k]) + ratio);
     }
-    if (takes_rest && t.p_rest != 0.f) share += t.p_rest * log2f(t.p_rest * total / st.rest);
-    share *= a.kd_weight * a.temperature * a.temperature;
+    if (takes_rest && t.p_rest != 0.f) {
+      // the quotient against M while it has all its digits, else the distance beside it
+      const bool near = st.rest_near >= 0x1p-60f;
+      const float d = tau * logf(t.p_rest * st.total / (near ? st.rest_near : st.rest));
+      share += t.p_rest * (near ? d : d + (st.M - st.rest_top));
+    }
+    share *= a.kd_weight * tau;
   }
-  if (takes_label) share += a.ce_weight * fmaf(b - z_label, kLog2e, log2f(HARD != kNoSum ? st.s1 : total));
+  if (takes_label) share += a.ce_weight * (b - z_label + logf(st.s1));
   return share;
 }
 
-// The gradient's factors of a row (see the header): u 2^(c0 (z - M)) + w e^(z - M) on
-// unlisted tokens, and the values that overwrite it at the list and the label.
+// The gradient's factors of a row (see the header): u 2^(c0 (z - m)) + w e^(z - m) on
+// unlisted tokens, and the values that overwrite it at the list and the label. m is the
+// unlisted tokens' largest logit where the teacher has a rest, so that P_rest q / q_rest is
+// a sum of factors of at most 1 whatever the list's logits are; else the row's largest.
 template <int HARD>
 struct Gradient {
+  bool rest;  // the teacher has a rest, and the student tokens for it
   float b, c0, total, gk, gc, u, w;
   Scale sa, sb;
   float uf, wf;  // u and w against the scales' own references
   bool fused, zero;
   TW_DEV Gradient(const DistillArgs& a, const DistillStat& st, float c0_, const Target& t)
-      : b(base_of(st.M)), c0(c0_), total(st.rest + st.list), sa(st.M, c0_), sb(hard_scale<HARD>(sa)) {
+      : rest(t.p_rest != 0.f && st.rest != 0.f), b(base_of(st.M)), c0(c0_), total(st.total),
+        sa(rest ? st.rest_top : st.M, c0_), sb(hard_scale<HARD>(sa)) {
     zero = (!t.some && t.label < 0) || total == 0.f;
     gk = t.up * a.kd_weight * a.temperature;
     gc = t.label >= 0 ? t.up * a.ce_weight : 0.f;
     u = t.some ? gk / total : 0.f;
-    if (t.p_rest != 0.f && st.rest != 0.f) u -= gk * t.p_rest / st.rest;
-    w = t.label >= 0 ? gc / (HARD != kNoSum ? st.s1 : total) : 0.f;
+    w = t.label >= 0 ? gc / st.s1 : 0.f;
+    if (rest) {
+      u = u * exp_of(sa.m, b, c0) - gk * t.p_rest / st.rest;
+      w *= exp_of(sa.m, b, kLog2e);
+    }
     if (HARD == kNoSum) u += w;
     fused = sa.fused && sb.fused;
     uf = fused ? u * exp2_fast(sa.shift()) : u;
     wf = fused ? w * exp2_fast(sb.shift()) : w;
   }
   // at entry k, which owns token l.idx[k]; dup: entries may name a token twice
-  TW_DEV float listed(const List& l, int K, int k, int label, bool dup) const {
+  TW_DEV float listed(const DistillStat& st, const List& l, int K, int k, int label, bool dup) const {
     const int i = l.idx[k];
     float p = l.p[k];
     if (dup) {  // add up, in list order, every entry that names the same token
@@ -575,12 +623,13 @@ struct Gradient {
         if (l.idx[q] == i || l.idx[q] == -2 - i) p += l.p[q];
     }
     float d = gk * (exp_of(l.z[k], b, c0) / total - p);
-    if (label >= 0) d += w * exp_of(l.z[k], b, kLog2e);
+    if (label >= 0) d += gc / st.s1 * exp_of(l.z[k], b, kLog2e);
     return i == label ? d - gc : d;
   }
+  // at the label, which is not listed
   TW_DEV float at_label(float z) const {
-    float d = u * exp_of(z, b, c0) - gc;
-    return HARD != kNoSum ? fmaf(w, exp_of(z, b, kLog2e), d) : d;
+    const float d = u * exp_of(z, sa.m, c0) - gc;
+    return HARD != kNoSum ? fmaf(w, exp_of(z, sa.m, kLog2e), d) : d;
   }
   // f(vector -> gradient) chosen by the row's case
   template <int DT, class F>

@@ -68,7 +68,9 @@ def _distill_row(z, idx, val, rest, label, tau, kd_w, ce_w):
         for k, (i, _) in enumerate(entries):
             pt[i] += P[k]
         if P[-1] > 0 and log_rest > -np.inf:
-            pt[~listed] += P[-1] * np.exp(logq[~listed] - log_rest)
+            zr = z[~listed] / tau  # q / q_rest: log q - log q_rest would lose the count of tokens at -3e38
+            e = np.exp(zr - zr.max())
+            pt[~listed] += P[-1] * e / e.sum()
         loss += kd_w * tau * tau * kd
         dz += kd_w * tau * (np.exp(logq) - pt)
     if has:

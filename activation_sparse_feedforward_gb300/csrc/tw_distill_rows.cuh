@@ -203,7 +203,7 @@ cudaError_t distill_rows(const DistillArgs& a, cudaStream_t s) {
   const size_t smem = RowRing<DT, NT, kRowDepth>::kBytes + bit_bytes + kListBytes * static_cast<size_t>(a.K);
   const int ahead = device_sm_count() * (1024 / NT);
   auto run = [&](auto kern) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    cudaError_t e = allow_smem(kern, smem);
     if (e != cudaSuccess) return e;
     e = launch(kern, dim3(a.N), dim3(NT), smem, s, a, bit_bytes, ahead);
     trace_mark(s, "distill_rows");

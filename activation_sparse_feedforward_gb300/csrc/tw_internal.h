@@ -62,6 +62,18 @@ cudaError_t launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, c
   return cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
 }
 
+// The most dynamic shared memory of a launch whose size depends on its operands (227 KB are
+// there for it and a kernel's static share).
+constexpr size_t kSmemMost = 216 * 1024;
+// Leave for a launch of `kern` with so much: the same for every size, so that of two host
+// threads neither lowers the other's between its asking and its launch.
+template <typename... KArgs>
+cudaError_t allow_smem(void (*kern)(KArgs...), size_t smem) {
+  if (smem > kSmemMost) return cudaErrorInvalidValue;
+  return smem <= 40 * 1024 ? cudaSuccess
+                           : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemMost));
+}
+
 // The same launch as clusters of `cluster` CTAs along x (gridDim.x a multiple of it).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_clustered(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t s,

@@ -623,8 +623,7 @@ int distill_rows_threads(const DistillArgs& a) {
 template <class... KArgs, class... Args>
 cudaError_t launch_rows(void (*kern)(KArgs...), int64_t N, const RowShape& r, int threads, size_t smem,
                         const char* label, cudaStream_t s, Args... args) {
-  cudaError_t e = cudaSuccess;
-  if (smem > 40 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  cudaError_t e = allow_smem(kern, smem);
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(N * r.cluster)), block(threads);
   e = r.cluster == 1 ? launch(kern, grid, block, smem, s, args...)

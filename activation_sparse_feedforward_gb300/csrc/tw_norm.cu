@@ -600,14 +600,10 @@ Team team_of(int d, int vpt, int threads, int T) {
   return t;
 }
 
-constexpr size_t kSmemMost = 216 * 1024;  // beside the kernels' static shared memory
-
 template <class Kern, class Args>
 cudaError_t launch_norm(Kern kern, int grid, const Team& t, size_t smem, const char* label, const Args& a,
                         cudaStream_t s) {
-  cudaError_t e = cudaSuccess;
-  if (smem > 40 * 1024)
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  cudaError_t e = allow_smem(kern, smem);
   if (e != cudaSuccess) return e;
   e = launch(kern, dim3(grid), dim3(t.tpr, t.teams), smem, s, a);
   trace_mark(s, label);

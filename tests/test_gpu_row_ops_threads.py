@@ -1,4 +1,5 @@
-"""Calls of other sizes from two host threads at once: each launch's shared memory is its own."""
+"""Calls of other sizes from several host threads at once, through the C entry points: each
+launch's shared memory is its own, whatever another thread asks of the same kernel."""
 import threading
 
 import pytest
@@ -6,6 +7,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import activation_sparse_feedforward_gb300 as tw  # noqa: E402
+from activation_sparse_feedforward_gb300 import _lib  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -18,53 +20,59 @@ def _need_gpu():
 
 
 def _at_once(calls, times):
-    """Runs each call `times` times on a thread and a stream of its own; what they raised."""
-    raised, start = [], threading.Barrier(len(calls))
+    """Each call (function, arguments without the stream) `times` times on a thread and a
+    stream of its own; the status codes that came back."""
+    codes, start = set(), threading.Barrier(len(calls))
+    streams = [torch.cuda.Stream() for _ in calls]
     torch.cuda.synchronize()
 
-    def work(call):
-        try:
-            with torch.cuda.stream(torch.cuda.Stream()):
-                start.wait()
-                for n in range(times):
-                    call()
-                    if n % 64 == 63:
-                        torch.cuda.current_stream().synchronize()
-                torch.cuda.current_stream().synchronize()
-        except Exception as e:  # noqa: BLE001 (reported by the test)
-            raised.append(repr(e))
+    def work(call, stream):
+        function, args = call
+        args = (*args, stream.cuda_stream)
+        start.wait()
+        for _ in range(times):
+            codes.add(function(*args))
 
-    threads = [threading.Thread(target=work, args=(c,)) for c in calls]
+    threads = [threading.Thread(target=work, args=a) for a in zip(calls, streams)]
     for t in threads:
         t.start()
     for t in threads:
         t.join()
     torch.cuda.synchronize()
-    return raised
+    return codes
 
 
-def _distill(N, V, K):
-    z = torch.randn(N, V, device="cuda")
-    labels = torch.zeros(N, dtype=torch.int32, device="cuda")
-    op = tw.DistillLoss(N, V, 0, dtype=torch.float32, kd_weight=0.0, ce_weight=1.0)
-    return lambda: op.forward_backward(z, labels=labels)
+def _distill(N, V, keep):
+    z, dz = torch.randn(N, V, device="cuda"), torch.empty(N, V, device="cuda")
+    labels, loss = torch.zeros(N, dtype=torch.int32, device="cuda"), torch.empty(N, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    keep += [z, dz, labels, loss, status]
+    return tw.load().tw_distill, (z.data_ptr(), V, N, V, _lib.TW_F32, None, None, 0, 0, None, labels.data_ptr(), 1.0, 0.0,
+                                  1.0, None, 1.0, loss.data_ptr(), dz.data_ptr(), V, status.data_ptr())
 
 
-def _norm(T, d, residual, backward):
-    x = torch.randn(T, d, device="cuda")
-    r = torch.randn(T, d, device="cuda") if residual else None
-    op = tw.LayerNorm(T, d, dtype=torch.float32)
-    if not backward:
-        return lambda: op.forward(x, residual=r)
-    op.forward(x)
-    return lambda: op.backward(x, x, dres=r)
+def _norm_fwd(T, d, residual, keep):
+    x, r, y = (torch.randn(T, d, device="cuda") for _ in range(3))
+    keep += [x, r, y]
+    return tw.load().tw_layer_norm_fwd, (x.data_ptr(), d, r.data_ptr() if residual else None, d, None, None, T, d, 1e-5,
+                                         _lib.TW_F32, _lib.TW_F32, None, 0, y.data_ptr(), d, None, None)
 
 
-# pairs of one kernel with other sizes of shared memory, both above what needs no leave
-@pytest.mark.parametrize("pair", ["distill_cluster", "distill_rows", "norm_fwd", "norm_bwd"])
-def test_two_threads_with_other_sizes(pair):
-    calls = dict(distill_cluster=lambda: (_distill(8, 140000, 0), _distill(8, 100000, 0)),
-                 distill_rows=lambda: (_distill(320, 1000, 0), _distill(320, 12000, 0)),
-                 norm_fwd=lambda: (_norm(64, 2048, True, False), _norm(64, 2048, False, False)),
-                 norm_bwd=lambda: (_norm(400, 2048, True, True), _norm(400, 2048, False, True)))[pair]()
-    assert _at_once(calls, 3000) == []
+def _norm_bwd(T, d, residual, keep):
+    x, dy, r, dx = (torch.randn(T, d, device="cuda") for _ in range(4))
+    mean, rstd = torch.zeros(T, device="cuda"), torch.ones(T, device="cuda")
+    keep += [x, dy, r, dx, mean, rstd]
+    return tw.load().tw_layer_norm_bwd, (dy.data_ptr(), d, x.data_ptr(), d, mean.data_ptr(), rstd.data_ptr(), None,
+                                         r.data_ptr() if residual else None, d, T, d, _lib.TW_F32, _lib.TW_F32,
+                                         dx.data_ptr(), d, None, None, None, 0)
+
+
+# pairs that share a kernel and want other amounts of shared memory of it, both above what
+# any kernel may have without asking
+@pytest.mark.parametrize("pair", ["distill", "norm_fwd", "norm_bwd"])
+def test_threads_with_other_sizes(pair):
+    keep = []
+    calls = dict(distill=lambda: [_distill(4, 140000, keep), _distill(4, 100000, keep)],
+                 norm_fwd=lambda: [_norm_fwd(16, 2048, True, keep), _norm_fwd(16, 2048, False, keep)],
+                 norm_bwd=lambda: [_norm_bwd(400, 2048, True, keep), _norm_bwd(400, 2048, False, keep)])[pair]()
+    assert _at_once(calls * 3, 4000) == {_lib.TW_OK}

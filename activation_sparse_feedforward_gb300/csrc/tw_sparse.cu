@@ -62,10 +62,6 @@ TW_DEV void out_f32x8(float* p, const F8& y, bool add) {
     stcs_f32x8(p, y);
 }
 constexpr int kCountHistMaxBins = 48 * 1024;  // 192 KB of shared memory
-template <class K>
-cudaError_t set_smem_bytes(K kern, size_t bytes) {
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-}
 int grid_for(long items, int per_block, int blocks_per_sm) {
   const long blocks = (items + per_block - 1) / per_block;
   return static_cast<int>(
@@ -326,7 +322,7 @@ static cudaError_t token_side(const SparseBwdArgs& a, cudaStream_t s) {
   // one CTA per SM; a shared-memory histogram of the columns when it fits
   const int bins = a.I <= kCountHistMaxBins ? a.I : 0;
   const size_t smem = sizeof(int) * static_cast<size_t>(bins);
-  e = set_smem_bytes(csc_count_scan_kernel, smem);
+  e = allow_smem(csc_count_scan_kernel, smem);
   if (e != cudaSuccess) return e;
   e = launch(csc_count_scan_kernel, dim3(grid_for(a.T, 32, 1)), dim3(1024), smem, s, a, ticket, bins);
   trace_mark(s, "csc_count_scan");

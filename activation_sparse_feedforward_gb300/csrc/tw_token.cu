@@ -636,10 +636,6 @@ __global__ void __launch_bounds__(NCH * 32, ctas_per_sm(NCH)) token_bwd_kernel(c
 
 // ====================================================================== launchers
 namespace {
-template <class K>
-cudaError_t set_smem(K kern, size_t bytes) {
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-}
 int token_grid(int T, int nch) {
   const int per_sm = ctas_per_sm(nch);
   return std::max(1, std::min(T, device_sm_count() * per_sm));
@@ -675,11 +671,11 @@ static cudaError_t token_fwd(const SparseFwdArgs& a, cudaStream_t s) {
 #define TW_TF(n)                                                                                        \
   if constexpr (kSpecialised) {                                                                         \
     const int grid = std::max(1, std::min(a.T, device_sm_count() * ws_ctas_per_sm(n)));                \
-    e = set_smem(token_fwd_ws_kernel<n, GATED, HYBRID>, smem);                                          \
+    e = allow_smem(token_fwd_ws_kernel<n, GATED, HYBRID>, smem);                                        \
     if (e != cudaSuccess) return e;                                                                     \
     e = launch(token_fwd_ws_kernel<n, GATED, HYBRID>, dim3(grid), dim3((n + 1) * 32), smem, s, a);     \
   } else {                                                                                              \
-    e = set_smem(token_fwd_kernel<n, GATED, HYBRID>, smem);                                             \
+    e = allow_smem(token_fwd_kernel<n, GATED, HYBRID>, smem);                                           \
     if (e != cudaSuccess) return e;                                                                     \
     e = launch(token_fwd_kernel<n, GATED, HYBRID>, dim3(token_grid(a.T, n)), dim3(n * 32), smem, s, a); \
   }
@@ -706,7 +702,7 @@ static cudaError_t token_bwd(const SparseBwdArgs& a, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
 #define TW_TB(n)                                                                    \
   {                                                                                 \
-    e = set_smem(token_bwd_kernel<n, GATED>, smem);                                 \
+    e = allow_smem(token_bwd_kernel<n, GATED>, smem);                               \
     if (e != cudaSuccess) return e;                                                 \
     e = launch(token_bwd_kernel<n, GATED>, dim3(grid), dim3(n * 32), smem, s, a); \
   }

@@ -6,8 +6,11 @@ As in ``ops``: objects preallocate every buffer, calls enqueue on torch's curren
 stream and neither allocate nor synchronise; one-shot functions build such an object.
 Matrices are [rows, columns] views with unit column stride and any row stride; a call
 may pass fewer rows than the object was made for and gets views of that many rows back.
+Every operand is on the object's device, and that is the current one; else ValueError.
 """
 from __future__ import annotations
+
+import functools
 
 import torch
 
@@ -24,11 +27,11 @@ def _dtype_code(dtype: torch.dtype) -> int:
     return code
 
 
-def _matrix(name: str, t: torch.Tensor, dtype: torch.dtype, rows: int, cols: int) -> int:
+def _matrix(name: str, t: torch.Tensor, dtype: torch.dtype, device: int, rows: int, cols: int) -> int:
     """Checks a [rows, cols] matrix; its row stride in elements (a single row's is its
-    length, whatever torch says)."""
-    if t.dtype is not dtype or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA {dtype} tensor")
+    length, whatever torch says). device: see _device_of."""
+    if t.dtype is not dtype or t.get_device() != device:
+        raise ValueError(f"{name} must be a CUDA {dtype} tensor on the object's device")
     if t.shape != (rows, cols):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
     if t.is_contiguous():
@@ -39,12 +42,12 @@ def _matrix(name: str, t: torch.Tensor, dtype: torch.dtype, rows: int, cols: int
     return ld if rows > 1 else cols
 
 
-def _vector(name: str, t: torch.Tensor | None, dtype: torch.dtype, n: int) -> int | None:
+def _vector(name: str, t: torch.Tensor | None, dtype: torch.dtype, device: int, n: int) -> int | None:
     """Checks a contiguous side array of n elements, or None; its address."""
     if t is None:
         return None
-    if t.dtype is not dtype or not t.is_cuda or t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of {n} elements")
+    if t.dtype is not dtype or t.get_device() != device or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of {n} elements on the object's device")
     return t.data_ptr()
 
 
@@ -59,10 +62,25 @@ def _addresses(*buffers: torch.Tensor | None) -> tuple[int | None, ...]:
     return tuple(None if t is None else t.data_ptr() for t in buffers)
 
 
-def _stream_of(t: torch.Tensor) -> int:
-    """The raw current stream of the tensor's device: torch.cuda.current_stream() builds a
-    Stream object for it, 2.9 us of a small call's host time against 0.1."""
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+def _device_of(buffer: torch.Tensor) -> int:
+    """The index of an object's GPU; where its buffers are on the host, one that no tensor has."""
+    index = buffer.get_device()
+    return index if index >= 0 else -2
+
+
+def _stream_of(device: int):
+    """What gives the device's raw current stream: torch.cuda.current_stream() builds a Stream
+    object for it, 2.9 us of a small call's host time against 0.1. A launch goes to the current
+    device, so with several GPUs that has to be this one."""
+    if torch.cuda.device_count() == 1:
+        return functools.partial(torch._C._cuda_getCurrentRawStream, device)
+
+    def checked() -> int:
+        if torch._C._cuda_getDevice() != device:
+            raise ValueError(f"the operands are on cuda:{device}, which is not the current device")
+        return torch._C._cuda_getCurrentRawStream(device)
+
+    return checked
 
 
 class LayerNorm:
@@ -96,13 +114,15 @@ class LayerNorm:
             self.ws = _workspace(self.ws_bytes, device)
             self._to_bwd = _addresses(self.dx, self.dweight, self.dbias, self.ws)
         self._to_fwd = _addresses(self.y, self.sum, self._mean, self._rstd)
+        self._device = _device_of(self.y)
+        self._stream = _stream_of(self._device)
 
     def forward(self, x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
                 residual: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
         """(y, s): s = x + residual (x itself without one), y = norm(s) weight + bias."""
-        n, d, dt = _rows("x", x, self.T), self.d, self.dtype
-        ldx = _matrix("x", x, dt, n, d)
-        w, b = _vector("weight", weight, self.weight_dtype, d), _vector("bias", bias, self.weight_dtype, d)
+        n, d, dt, dev = _rows("x", x, self.T), self.d, self.dtype, self._device
+        ldx = _matrix("x", x, dt, dev, n, d)
+        w, b = _vector("weight", weight, self.weight_dtype, dev, d), _vector("bias", bias, self.weight_dtype, dev, d)
         y, s = self.y, self.sum
         if n != self.T:
             y, s = y[:n], s[:n]
@@ -112,9 +132,9 @@ class LayerNorm:
         if residual is None:
             r, ldr, to = None, 0, None
         else:
-            r, ldr = residual.data_ptr(), _matrix("residual", residual, dt, n, d)
+            r, ldr = residual.data_ptr(), _matrix("residual", residual, dt, dev, n, d)
         code = self._lib.tw_layer_norm_fwd(x.data_ptr(), ldx, r, ldr, w, b, n, d, self.eps, self._dt, self._wdt, to, d,
-                                           to_y, d, to_mean, to_rstd, _stream_of(x))
+                                           to_y, d, to_mean, to_rstd, self._stream())
         if code:
             _lib.check(code, "tw_layer_norm_fwd")
         return y, (x if residual is None else s)
@@ -127,17 +147,17 @@ class LayerNorm:
         dx = self.dx
         if dx is None:
             raise ValueError("this LayerNorm was made with backward=False")
-        n, d, dt = _rows("x", x, self.T), self.d, self.dtype
-        ldx, lddy = _matrix("x", x, dt, n, d), _matrix("dy", dy, dt, n, d)
-        w = _vector("weight", weight, self.weight_dtype, d)
-        m = _vector("mean", self.mean if mean is None else mean, torch.float32, n)
-        r = _vector("rstd", self.rstd if rstd is None else rstd, torch.float32, n)
-        g, ldg = (None, 0) if dres is None else (dres.data_ptr(), _matrix("dres", dres, dt, n, d))
+        n, d, dt, dev = _rows("x", x, self.T), self.d, self.dtype, self._device
+        ldx, lddy = _matrix("x", x, dt, dev, n, d), _matrix("dy", dy, dt, dev, n, d)
+        w = _vector("weight", weight, self.weight_dtype, dev, d)
+        m = _vector("mean", self.mean if mean is None else mean, torch.float32, dev, n)
+        r = _vector("rstd", self.rstd if rstd is None else rstd, torch.float32, dev, n)
+        g, ldg = (None, 0) if dres is None else (dres.data_ptr(), _matrix("dres", dres, dt, dev, n, d))
         if n != self.T:
             dx = dx[:n]
         to, to_w, to_b, ws = self._to_bwd
         code = self._lib.tw_layer_norm_bwd(dy.data_ptr(), lddy, x.data_ptr(), ldx, m, r, w, g, ldg, n, d, self._dt,
-                                           self._wdt, to, d, to_w, to_b, ws, self.ws_bytes, _stream_of(x))
+                                           self._wdt, to, d, to_w, to_b, ws, self.ws_bytes, self._stream())
         if code:
             _lib.check(code, "tw_layer_norm_bwd")
         return dx, self.dweight, self.dbias
@@ -178,10 +198,12 @@ class DistillLoss:
         self.dz = torch.empty((N, V), dtype=dtype, device=device) if grad else None
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
         self._to = _addresses(self.loss, self.dz, self.status)
+        self._device = _device_of(self.loss)
+        self._stream = _stream_of(self._device)
 
     def _run(self, z, idx, val, rest, labels, dloss, scale, want_loss, want_grad, out):
-        n, K, V = _rows("z", z, self.N), self.K, self.V
-        ld = _matrix("z", z, self.dtype, n, V)
+        n, K, V, dev = _rows("z", z, self.N), self.K, self.V, self._device
+        ld = _matrix("z", z, self.dtype, dev, n, V)
         to_loss, to_dz, status = self._to
         dz, to, ldd = None, None, 0
         if want_grad:
@@ -189,7 +211,7 @@ class DistillLoss:
             if dz is None:
                 raise ValueError("this DistillLoss was made with grad=False: give `out`")
             if out is not None:
-                to, ldd = out.data_ptr(), _matrix("out", out, self.dtype, n, V)
+                to, ldd = out.data_ptr(), _matrix("out", out, self.dtype, dev, n, V)
             else:
                 to, ldd = to_dz, V
                 if n != self.N:
@@ -200,12 +222,12 @@ class DistillLoss:
             if idx is None or val is None:
                 raise ValueError("idx and val must be given for K > 0")
             tdt = _dtype_code(val.dtype)
-            i, v = _vector("idx", idx, torch.int32, n * K), _vector("val", val, val.dtype, n * K)
+            i, v = _vector("idx", idx, torch.int32, dev, n * K), _vector("val", val, val.dtype, dev, n * K)
         code = self._lib.tw_distill(
-            z.data_ptr(), ld, n, V, self._dt, i, v, tdt, K, _vector("rest", rest, torch.float32, n),
-            _vector("labels", labels, torch.int32, n), self.temperature, self.kd_weight, self.ce_weight,
-            _vector("dloss", dloss, torch.float32, n), scale, to_loss if want_loss else None, to, ldd, status,
-            _stream_of(z))
+            z.data_ptr(), ld, n, V, self._dt, i, v, tdt, K, _vector("rest", rest, torch.float32, dev, n),
+            _vector("labels", labels, torch.int32, dev, n), self.temperature, self.kd_weight, self.ce_weight,
+            _vector("dloss", dloss, torch.float32, dev, n), scale, to_loss if want_loss else None, to, ldd, status,
+            self._stream())
         if code:
             _lib.check(code, "tw_distill")
         return (self.loss if n == self.N else self.loss[:n]), dz
@@ -251,18 +273,20 @@ class TokenLogprobs:
         self.top_logprob = torch.empty((N, top_k), dtype=torch.float32, device=device)
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
         self._to = _addresses(self.logprob, self.entropy, self.top_idx, self.top_logprob, self.status)
+        self._device = _device_of(self.entropy)
+        self._stream = _stream_of(self._device)
 
     def __call__(self, z: torch.Tensor, tokens: torch.Tensor | None = None):
         """(logprob [n, n_tokens], entropy [n], top_idx [n, top_k], top_logprob [n, top_k])."""
-        n, s = _rows("z", z, self.N), self.n_tokens
-        ld = _matrix("z", z, self.dtype, n, self.V)
+        n, s, dev = _rows("z", z, self.N), self.n_tokens, self._device
+        ld = _matrix("z", z, self.dtype, dev, n, self.V)
         t = None
         if s > 0:
             if tokens is None:
                 raise ValueError("tokens must be given for n_tokens > 0")
-            t = _vector("tokens", tokens, torch.int32, n * s)
+            t = _vector("tokens", tokens, torch.int32, dev, n * s)
         code = self._lib.tw_token_logprobs(
-            z.data_ptr(), ld, n, self.V, self._dt, t, s, self.temperature, self.top_k, *self._to, _stream_of(z))
+            z.data_ptr(), ld, n, self.V, self._dt, t, s, self.temperature, self.top_k, *self._to, self._stream())
         if code:
             _lib.check(code, "tw_token_logprobs")
         if n == self.N:

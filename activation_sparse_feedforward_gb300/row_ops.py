@@ -51,6 +51,16 @@ def _vector(name: str, t: torch.Tensor | None, dtype: torch.dtype, device: int, 
     return t.data_ptr()
 
 
+def _list(name: str, t: torch.Tensor, dtype: torch.dtype, device: int, n: int, k: int) -> int:
+    """Checks a contiguous array of n rows of k entries (the entries last, or all in one
+    dimension); its address."""
+    if t.dtype is not dtype or t.get_device() != device or t.numel() != n * k or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of {(n, k)} on the object's device")
+    if k != 1 and t.size(-1) != k and t.dim() != 1:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(n, k)}")
+    return t.data_ptr()
+
+
 def _rows(name: str, t: torch.Tensor, most: int) -> int:
     if t.dim() != 2 or (n := t.shape[0]) > most:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected at most {most} rows")
@@ -222,7 +232,7 @@ class DistillLoss:
             if idx is None or val is None:
                 raise ValueError("idx and val must be given for K > 0")
             tdt = _dtype_code(val.dtype)
-            i, v = _vector("idx", idx, torch.int32, dev, n * K), _vector("val", val, val.dtype, dev, n * K)
+            i, v = _list("idx", idx, torch.int32, dev, n, K), _list("val", val, val.dtype, dev, n, K)
         code = self._lib.tw_distill(
             z.data_ptr(), ld, n, V, self._dt, i, v, tdt, K, _vector("rest", rest, torch.float32, dev, n),
             _vector("labels", labels, torch.int32, dev, n), self.temperature, self.kd_weight, self.ce_weight,
@@ -284,7 +294,7 @@ class TokenLogprobs:
         if s > 0:
             if tokens is None:
                 raise ValueError("tokens must be given for n_tokens > 0")
-            t = _vector("tokens", tokens, torch.int32, dev, n * s)
+            t = _list("tokens", tokens, torch.int32, dev, n, s)
         code = self._lib.tw_token_logprobs(
             z.data_ptr(), ld, n, self.V, self._dt, t, s, self.temperature, self.top_k, *self._to, self._stream())
         if code:

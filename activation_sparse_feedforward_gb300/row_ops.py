@@ -306,6 +306,12 @@ class TokenLogprobs:
 
 def token_logprobs(z, tokens=None, top_k: int = 0, temperature: float = 1.0):
     """One-shot form; tokens [n] or [n, s]. Returns (logprob, entropy, top_idx, top_logprob, status)."""
-    s = 0 if tokens is None else tokens.numel() // max(z.shape[0], 1)
-    op = TokenLogprobs(z.shape[0], z.shape[1], s, top_k, temperature, z.dtype, z.device)
+    n = z.shape[0]
+    if tokens is None:
+        s = 0
+    elif tokens.dim() == 2 and tokens.shape[0] == n:
+        s = tokens.shape[1]
+    else:  # at least one, so that tokens for fewer rows are refused
+        s = max(1, tokens.numel() // max(n, 1))
+    op = TokenLogprobs(n, z.shape[1], s, top_k, temperature, z.dtype, z.device)
     return (*op(z, tokens), op.status)

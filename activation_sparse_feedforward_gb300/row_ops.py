@@ -191,7 +191,8 @@ class DistillLoss:
     """Preallocated distillation loss of up to N rows of V logits from a teacher's top K
     (see tw_distill): kd_weight * KD at `temperature` + ce_weight * cross entropy of the
     labels. K = 0 is plain cross entropy. grad: whether a gradient buffer dz is kept
-    (calls may also name theirs with `out`, the logits themselves among them).
+    (calls may also name theirs with `out`, the logits themselves among them). A part whose
+    weight is 0 is not looked at.
 
     idx [n, K] int32 (-1: no entry), val [n, K] float32, bfloat16 or float16, rest [n]
     float32 or None, labels [n] int32 (-1: none) or None. An index outside [-1, V)
@@ -228,7 +229,7 @@ class DistillLoss:
                     dz = dz[:n]
         i = v = None
         tdt = self._dt
-        if K > 0:
+        if K > 0 and self.kd_weight != 0.0:
             if idx is None or val is None:
                 raise ValueError("idx and val must be given for K > 0")
             tdt = _dtype_code(val.dtype)

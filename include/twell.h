@@ -452,8 +452,11 @@ size_t tw_layer_norm_bwd_workspace_size(int T, int d);
  * dres: NULL, or [T, d], the gradient that reaches s along the residual stream; dx
  * may be dres, dy or x itself (same pointer and stride). weight: NULL for 1. dx [T, d] of
  * type dtype; dweight, dbias [d] fp32, overwritten, each NULL when not wanted; T = 0
- * writes zeros into them. The sums over rows are taken in an order that depends on
- * T and d only: the same inputs give the same bits. Widths as the forward. */
+ * writes zeros into them. The sums over rows are taken in a fixed order: the same call
+ * gives the same bits. The order depends on T, d and the types, on whether every matrix
+ * and the weight lie on 16 bytes, on whether dx shares memory with x or dy, and on the
+ * device's number of SMs: calls that differ there may differ in the sums' last bits.
+ * Widths as the forward. */
 tw_status tw_layer_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const float* mean,
                             const float* rstd, const void* weight, const void* dres, int64_t lddres, int T, int d,
                             int dtype, int wtype, void* dx, int64_t lddx, float* dweight, float* dbias, void* ws,

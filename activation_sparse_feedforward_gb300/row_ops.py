@@ -54,9 +54,9 @@ def _vector(name: str, t: torch.Tensor | None, dtype: torch.dtype, device: int, 
 def _list(name: str, t: torch.Tensor, dtype: torch.dtype, device: int, n: int, k: int) -> int:
     """Checks a contiguous array of n rows of k entries (the entries last, or all in one
     dimension); its address."""
-    if t.dtype is not dtype or t.get_device() != device or t.numel() != n * k or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of {(n, k)} on the object's device")
-    if k != 1 and t.size(-1) != k and t.dim() != 1:
+    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor on the object's device")
+    if t.shape != (n, k) and (t.numel() != n * k or not (k == 1 or t.dim() == 1 or t.shape[-1] == k)):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(n, k)}")
     return t.data_ptr()
 
@@ -234,11 +234,12 @@ class DistillLoss:
                 raise ValueError("idx and val must be given for K > 0")
             tdt = _dtype_code(val.dtype)
             i, v = _list("idx", idx, torch.int32, dev, n, K), _list("val", val, val.dtype, dev, n, K)
+        r = None if rest is None else _vector("rest", rest, torch.float32, dev, n)
+        lab = None if labels is None else _vector("labels", labels, torch.int32, dev, n)
+        up = None if dloss is None else _vector("dloss", dloss, torch.float32, dev, n)
         code = self._lib.tw_distill(
-            z.data_ptr(), ld, n, V, self._dt, i, v, tdt, K, _vector("rest", rest, torch.float32, dev, n),
-            _vector("labels", labels, torch.int32, dev, n), self.temperature, self.kd_weight, self.ce_weight,
-            _vector("dloss", dloss, torch.float32, dev, n), scale, to_loss if want_loss else None, to, ldd, status,
-            self._stream())
+            z.data_ptr(), ld, n, V, self._dt, i, v, tdt, K, r, lab, self.temperature, self.kd_weight, self.ce_weight, up,
+            scale, to_loss if want_loss else None, to, ldd, status, self._stream())
         if code:
             _lib.check(code, "tw_distill")
         return (self.loss if n == self.N else self.loss[:n]), dz

@@ -11,11 +11,11 @@
 // Bound: HBM, one read of the logits and, with a gradient, one write. Measured on one GB300
 // against the copy rate (6681 GB/s): log probabilities 8192 x 65536 bf16 with five
 // alternatives 167 us (0.96); distillation 4096 x 131072 bf16, K = 64, temperature 2, rest
-// and labels 430 us (0.75), fp32 1023 x 50011, K = 33, 92 us (0.66). What keeps the
-// distillation from the copy rate are the steps between a slice's sweeps: of the 11.4 us a
-// CTA takes for 64 KB (three on an SM) 2.9 pass until the copies are issued and the target
-// taken, 0.6 with the listed entries, 1.9 with the sums, 2.1 with joining the cluster's
-// statistics and 3 with the gradient.
+// and labels 428 us (0.75), fp32 1023 x 50011, K = 33, 92 us (0.67). What keeps the
+// distillation from the copy rate are the steps between a slice's sweeps: of the 11.9 us a
+// CTA takes for 64 KB (three on an SM, with time stamps) 3.7 pass until the copies are issued
+// and the target taken, 0.6 with the listed entries, 2.1 with the sums, 1.8 with joining the
+// cluster's statistics and 3.1 with the gradient.
 //
 // Both join partial statistics through distributed shared memory: one launch, no
 // workspace, no atomics on results.
@@ -410,8 +410,9 @@ TW_DEV void add_terms(const uint4& r, const Scale& a, float2& s, float2& w) {
   }
 }
 
-// Three batches a thread on their way: 48 KB an SM's quarter. (One batch ahead in
-// registers: 8192 x 65536 bf16 with five alternatives took 194 us, this 178.)
+// Three batches a thread on their way: 48 KB an SM's quarter. (8192 x 65536 bf16 with five
+// alternatives 167 us. When the ring took the place of one batch ahead in registers, before
+// the chunks and the smaller CTAs, that went from 194 us to 178.)
 template <int DT, int NT>
 using ProbRing = RowRing<DT, NT, 3>;
 
@@ -607,9 +608,10 @@ RowShape row_shape(int64_t N, int V, int dtype, int most, int64_t fill, int leas
 // second time from L2 for the gradient (tw_distill_rows.cuh). Short rows are bound by the
 // steps between their sweeps, so many small CTAs an SM beat a few that hold rows on chip;
 // long ones would not stay in L2. Fraction of the copy rate at K = 64, temperature 2, with
-// rest and labels, 64 threads / 128 threads / one row per cluster: rows of 8 KB (bf16)
-// 0.41 / 0.31 / 0.16, 16 KB 0.55 / 0.47 / 0.30, 32 KB 0.67 / 0.63 / 0.48, 48 KB 0.69 / 0.72 /
-// 0.60; fp32 of 48 KB 0.72 / 0.91 / 0.85, 64 KB 0.67 / 0.81 / 0.85. At 32 KB a cluster is
+// rest and labels, 64 threads / 128 threads / one row per cluster, 134 to 402 MB of logits:
+// rows of 8 KB (bf16) 0.43 / 0.34 / 0.16, 16 KB 0.57 / 0.49 / 0.30, 32 KB 0.69 / 0.64 / 0.49,
+// 48 KB 0.69 / 0.74 / 0.61; fp32 of 32 KB 0.76 / 0.76 / 0.57, 48 KB 0.66 / 0.84 / 0.73, 64 KB
+// 0.60 / 0.77 / 0.81. At 32 KB a cluster is
 // faster up to two rows an SM, and 64 threads slower up to sixteen. The loss alone needs no
 // second sweep, so it takes long rows too once they fill the device: 4096 x 128000 bf16 162
 // us (cluster 291), 320 x 64000 13.7 (15.5), 160 x 128000 16.8 (16.3), 640 x 32000 15.3 (14.1).
@@ -640,7 +642,9 @@ cudaError_t distill(const DistillArgs& a, cudaStream_t s) {
   const RowShape r = row_shape(a.N, a.V, DT, 72 * 1024, device_sm_count(), 8 * 1024);
   const size_t smem = r.part_bytes + kListBytes * static_cast<size_t>(a.K);
   const int ahead = 3 * device_sm_count() / r.cluster;
-  auto run = [&](auto kern) { return launch_rows(kern, a.N, r, kThreads, smem, "distill", s, a, r.cluster, r.part_bytes, ahead); };
+  auto run = [&](auto kern) {
+    return launch_rows(kern, a.N, r, kThreads, smem, "distill", s, a, r.cluster, r.part_bytes, ahead);
+  };
   switch (hard_form(a)) {
     case kNoSum: return run(distill_kernel<DT, kNoSum>);
     case 2: return run(distill_kernel<DT, 2>);

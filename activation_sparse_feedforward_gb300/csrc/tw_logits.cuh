@@ -6,7 +6,8 @@
 // temperature; two such pairs join as M = max(M1, M2), S = S1 2^(c (M1-M)) + S2 2^(c (M2-M)).
 // M is taken off before the scaling: c z alone would overflow, or lose the whole
 // exponent to rounding, where a mask is the type's lowest value. A row, part or thread
-// with nothing but -inf has M = -inf and S = 0.
+// with nothing but -inf has M = -inf and S = 0. The distillation keeps a pair for the listed
+// tokens and one for the others, whose mass and gradient are needed by themselves.
 #pragma once
 
 #include <cfloat>

@@ -15,9 +15,11 @@
 // will take next on their way through its own places of a ring in shared memory (each
 // thread copies and reads back its own 16 bytes, so the ring needs no barrier), and
 // weights and column sums stay in registers. Rows off 16 bytes go through the ring as the
-// aligned vectors that they lie in, and are put together from two of them (those instructions
-// bound them: 32672 x 1027 bf16 forward 55 us, 0.36 of the copy rate). Rows too wide for a ring
-// are loaded straight into registers.
+// aligned vectors that they lie in, and are put together from two of them (those instructions,
+// and in the forward's 80 registers spills of 8 to 144 bytes a thread, bound them: 32672 x 1027
+// fp16 forward 55 us, 0.36 of the copy rate). Rows too wide for a ring are loaded straight
+// into registers, of which 1024 threads have too few (spills of 8 to 392 bytes a thread in
+// the forward, 536 to 656 in the backward).
 //
 // Measured on one GB300 against the copy rate (6681 GB/s), bf16 with fp32 weights: forward
 // 16384 x 2048 with residual and saved statistics 45.4 us (0.89); backward 16384 x 2048
@@ -767,7 +769,10 @@ cudaError_t launch_norm_fwd(const NormFwdArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_norm_bwd(const NormBwdArgs& a, cudaStream_t s) {
-  if (a.T == 0) return a.dw != nullptr || a.db != nullptr ? norm_bwd_finish(a, 0, (a.d + 31) / 32 * 32, (a.d + 31) / 32 * 32, 1, s) : cudaSuccess;  // sums over no rows
+  if (a.T == 0) {  // sums over no rows
+    const int width = (a.d + 31) / 32 * 32;
+    return a.dw != nullptr || a.db != nullptr ? norm_bwd_finish(a, 0, width, width, 1, s) : cudaSuccess;
+  }
   const int dt = a.dtype;
   const bool vec = a.d % 8 == 0 && on16(a.x) && on16(a.dy) && on16(a.dres) && on16(a.dx) && on16(a.w) &&
                    stride16(a.ldx, dt) && stride16(a.lddy, dt) && stride16(a.lddres, dt) && stride16(a.lddx, dt);

@@ -35,3 +35,7 @@ from .row_ops import (  # noqa: F401
     layer_norm_fwd,
     token_logprobs,
 )
+from .weight_ops import (  # noqa: F401
+    Orthogonalize,
+    orthogonalize,
+)

@@ -39,6 +39,8 @@ class TwHybrid(ctypes.Structure):
 
 TW_F32, TW_BF16, TW_F16 = 0, 1, 2
 
+TW_ORTHO_MOST = 8
+
 TW_ROUTE_SPARSE, TW_ROUTE_DENSE, TW_ROUTE_AUTO = 0, 1, 2
 ROUTES = {"sparse": TW_ROUTE_SPARSE, "dense": TW_ROUTE_DENSE, "auto": TW_ROUTE_AUTO}
 
@@ -93,6 +95,10 @@ SIGNATURES = {
                            c_void_p]),
     "tw_token_logprobs": (c_int, [c_void_p, c_int64, c_int, c_int, c_int, c_void_p, c_int, c_float, c_int, c_void_p,
                                   c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "tw_orthogonalize_workspace_size": (c_size_t, [c_int, c_int, c_int]),
+    "tw_orthogonalize": (c_int, [c_void_p, c_int64, c_int, c_void_p, c_int64, c_float, c_int, c_int, c_int, c_int, c_int,
+                                 c_void_p, c_float, c_float, c_void_p, c_int64, c_int, c_void_p, c_size_t, c_void_p,
+                                 c_void_p]),
     "tw_trace_begin": (c_int, [ctypes.POINTER(c_void_p), c_int]),
     "tw_trace_end": (c_int, []),
     "tw_trace_label": (ctypes.c_char_p, [c_int]),

@@ -1,6 +1,7 @@
 // extern "C" entry points declared in include/twell.h: host-side validation,
 // workspace layout and the launch sequence of each operation. Everything is
 // enqueued on the caller's stream; nothing is allocated, freed or synchronised.
+#include <algorithm>
 #include <cmath>
 #include <stdint.h>
 #include <string.h>
@@ -154,6 +155,11 @@ tw_status check_norm(int T, int d, int dtype, int wtype) {
   if (T < 0 || d < 1) return TW_EINVAL;
   if (check_dtype(dtype) != TW_OK || (wtype != dtype && wtype != TW_F32)) return TW_EINVAL;
   return d <= 16384 && T <= (1 << 30) ? TW_OK : TW_EUNSUPPORTED;
+}
+
+tw_status check_ortho(int m, int n, int count) {
+  if (m < 1 || n < 1 || count < 1) return TW_EINVAL;
+  return std::max(m, n) <= (1 << 20) && std::min(m, n) <= 16384 && count <= TW_ORTHO_MOST ? TW_OK : TW_EUNSUPPORTED;
 }
 
 // ------------------------------------------------------------------ workspace layouts
@@ -899,6 +905,44 @@ tw_status tw_token_logprobs(const void* z, int64_t ldz, int N, int V, int dtype,
   a.tokens = tokens, a.n_tokens = n_tokens, a.K = top_k, a.temperature = temperature;
   a.logprob = logprob, a.entropy = entropy, a.top_idx = top_idx, a.top_logprob = top_logprob, a.status = dev_status;
   return from_cuda(tw::launch_logprobs(a, as_stream(stream)));
+}
+
+// ------------------------------------------------------------------ orthogonalised updates
+size_t tw_orthogonalize_workspace_size(int m, int n, int count) {
+  if (check_ortho(m, n, count) != TW_OK) return 0;
+  return tw::ortho_workspace(m, n, count);
+}
+
+tw_status tw_orthogonalize(const void* const* grads, int64_t ldg, int gtype, float* const* buffers, int64_t ldbuf,
+                           float momentum, int nesterov, int count, int m, int n, int steps, const float* coefficients,
+                           float scale, float beta, void* const* out, int64_t ldo, int otype, void* ws, size_t ws_bytes,
+                           int32_t* dev_status, void* stream) {
+  tw_status st = check_ortho(m, n, count);
+  if (st != TW_OK) return st;
+  if (check_dtype(gtype) != TW_OK || check_dtype(otype) != TW_OK) return TW_EINVAL;
+  if (grads == nullptr || out == nullptr || coefficients == nullptr || steps < 1 || steps > 32) return TW_EINVAL;
+  if (!std::isfinite(momentum) || !std::isfinite(scale) || !std::isfinite(beta)) return TW_EINVAL;
+  for (int i = 0; i < 3 * steps; ++i)
+    if (!std::isfinite(coefficients[i])) return TW_EINVAL;
+  for (int i = 0; i < count; ++i) {
+    const RowMatrix g = {grads[i], ldg, true, true}, o = {out[i], ldo, true, true};
+    st = check_rows(&g, 1, n, gtype);
+    if (st == TW_OK) st = check_rows(&o, 1, n, otype);
+    if (st == TW_OK && buffers != nullptr) {
+      const RowMatrix b = {buffers[i], ldbuf, true, true};
+      st = check_rows(&b, 1, n, TW_F32);
+    }
+    if (st != TW_OK) return st;
+  }
+  st = check_ptrs({ws});
+  if (st == TW_OK) st = check_side({dev_status}, {});
+  if (st != TW_OK) return st;
+  if (ws_bytes < tw::ortho_workspace(m, n, count)) return TW_EWORKSPACE;
+  tw::OrthoArgs a = {};
+  a.g = grads, a.buf = buffers, a.out = out, a.ldg = ldg, a.ldbuf = ldbuf, a.ldo = ldo;
+  a.gtype = gtype, a.otype = otype, a.count = count, a.m = m, a.n = n, a.steps = steps, a.nesterov = nesterov != 0;
+  a.mu = momentum, a.scale = scale, a.beta = beta, a.coef = coefficients, a.ws = ws, a.status = dev_status;
+  return from_cuda(tw::launch_ortho(a, as_stream(stream)));
 }
 
 }  // extern "C"

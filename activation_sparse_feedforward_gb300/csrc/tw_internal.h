@@ -436,4 +436,19 @@ struct LogprobArgs {
 };
 cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t s);
 
+
+// ---------------------------------------------------------------- tw_ortho.cu
+struct OrthoArgs {
+  const void* const* g;     // [count], host arrays of device pointers
+  float* const* buf;        // [count] momentum buffers, or null
+  void* const* out;         // [count]
+  int64_t ldg, ldbuf, ldo;
+  int gtype, otype, count, m, n, steps, nesterov;
+  float mu, scale, beta;
+  const float* coef;        // [steps][3], host
+  void* ws;
+  int32_t* status;
+};
+size_t ortho_workspace(int m, int n, int count);
+cudaError_t launch_ortho(const OrthoArgs& a, cudaStream_t s);
 }  // namespace tw

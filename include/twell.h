@@ -513,6 +513,39 @@ tw_status tw_token_logprobs(const void* z, int64_t ldz, int N, int V, int dtype,
                             float temperature, int top_k, float* logprob, float* entropy, int32_t* top_idx,
                             float* top_logprob, int32_t* dev_status, void* stream);
 
+/* The most matrices of one tw_orthogonalize call. */
+enum { TW_ORTHO_MOST = 8 };
+
+/* Workspace bytes tw_orthogonalize needs for `count` matrices [m, n]; 0 for sizes it does
+ * not take. */
+size_t tw_orthogonalize_workspace_size(int m, int n, int count);
+
+/* Orthogonalised updates of `count` weight matrices of one shape [m, n], as optimisers of
+ * hidden weights take them: momentum, then Newton-Schulz steps that bring the update's
+ * singular values near 1. For each matrix, with G its gradient and M its buffer:
+ *   M = momentum M + G (in place);  U = G + momentum M when nesterov, else M
+ *   (buffers NULL: U = G)
+ *   X = U / |U|_F (0 where U is 0)
+ *   `steps` times, with (a, b, c) the step's three coefficients:
+ *     X = a X + (b A + c A^2) X,  A = X X^T   (equally X (b A + c A^2), A = X^T X)
+ *   out = beta out + scale X
+ * so that out = the update itself (beta 0: what out held is not read, and out may be G), or
+ * the weights, updated in place (beta = 1 - decay, scale = -rate).
+ * grads, buffers, out, coefficients [3 steps]: host arrays; the matrices they name are on
+ * the device, with row strides of at least n elements: grads of type gtype, buffers fp32,
+ * out of type otype. 1 <= steps <= 32; 1 <= count <= TW_ORTHO_MOST; min(m, n) <= 16384,
+ * max(m, n) <= 2^20.
+ * Precision: products of fp16 operands (11 bits) with fp32 sums, X kept to 22 bits between
+ * them. With the usual coefficients (3.4445, -4.7750, 2.0315), 5 steps, out is within about
+ * 1e-3 of the definition in the 2-norm. Coefficients have to keep the singular values below
+ * 2, or fp16 may overflow. U's norm neither overflows nor underflows. An infinity or a NaN
+ * in U makes out NaN. The same call gives the same bits on the same device.
+ * Device condition: TW_ETIMEOUT as the FFN's products. */
+tw_status tw_orthogonalize(const void* const* grads, int64_t ldg, int gtype, float* const* buffers, int64_t ldbuf,
+                           float momentum, int nesterov, int count, int m, int n, int steps, const float* coefficients,
+                           float scale, float beta, void* const* out, int64_t ldo, int otype, void* ws, size_t ws_bytes,
+                           int32_t* dev_status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -28,11 +28,18 @@ from .ops import (  # noqa: F401
 )
 from .row_ops import (  # noqa: F401
     DistillLoss,
+    Embedding,
     LayerNorm,
+    RMSNorm,
     TokenLogprobs,
     distill_loss,
+    embedding_bwd,
+    embedding_fwd,
     layer_norm_bwd,
     layer_norm_fwd,
+    rms_norm_bwd,
+    rms_norm_fwd,
+    rms_norm_fwd_fp8,
     token_logprobs,
 )
 from .weight_ops import (  # noqa: F401

@@ -90,11 +90,23 @@ SIGNATURES = {
     "tw_layer_norm_bwd": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_void_p,
                                   c_int64, c_int, c_int, c_int, c_int, c_void_p, c_int64, c_void_p, c_void_p,
                                   c_void_p, c_size_t, c_void_p]),
+    "tw_rms_norm_fwd": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int, c_int, c_float, c_int, c_int,
+                                c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p]),
+    "tw_rms_norm_fwd_fp8": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int, c_int, c_float, c_int, c_int,
+                                    c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int, c_void_p, c_void_p]),
+    "tw_rms_norm_bwd_workspace_size": (c_size_t, [c_int, c_int]),
+    "tw_rms_norm_bwd": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_int64, c_int,
+                                c_int, c_int, c_int, c_void_p, c_int64, c_void_p, c_void_p, c_size_t, c_void_p]),
     "tw_distill": (c_int, [c_void_p, c_int64, c_int, c_int, c_int, c_void_p, c_void_p, c_int, c_int, c_void_p, c_void_p,
                            c_float, c_float, c_float, c_void_p, c_float, c_void_p, c_void_p, c_int64, c_void_p,
                            c_void_p]),
     "tw_token_logprobs": (c_int, [c_void_p, c_int64, c_int, c_int, c_int, c_void_p, c_int, c_float, c_int, c_void_p,
                                   c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "tw_embedding_fwd": (c_int, [c_void_p, c_void_p, c_int64, c_int, c_int, c_int, c_float, c_int, c_int, c_void_p,
+                                 c_int64, c_void_p, c_void_p]),
+    "tw_embedding_bwd_workspace_size": (c_size_t, [c_int, c_int, c_int]),
+    "tw_embedding_bwd": (c_int, [c_void_p, c_int64, c_void_p, c_int, c_int, c_int, c_float, c_int, c_int, c_void_p,
+                                 c_int64, c_void_p, c_size_t, c_void_p, c_void_p]),
     "tw_orthogonalize_workspace_size": (c_size_t, [c_int, c_int, c_int]),
     "tw_orthogonalize": (c_int, [c_void_p, c_int64, c_int, c_void_p, c_int64, c_float, c_int, c_int, c_int, c_int, c_int,
                                  c_void_p, c_float, c_float, c_void_p, c_int64, c_int, c_void_p, c_size_t, c_void_p,

@@ -157,6 +157,11 @@ tw_status check_norm(int T, int d, int dtype, int wtype) {
   return d <= 16384 && T <= (1 << 30) ? TW_OK : TW_EUNSUPPORTED;
 }
 
+tw_status check_embed(int T, int V, int d, float scale, int dtype) {
+  if (T < 0 || V < 1 || d < 1 || check_dtype(dtype) != TW_OK || !std::isfinite(scale)) return TW_EINVAL;
+  return d <= 16384 && T <= (1 << 22) && V <= (1 << 22) ? TW_OK : TW_EUNSUPPORTED;
+}
+
 tw_status check_ortho(int m, int n, int count) {
   if (m < 1 || n < 1 || count < 1) return TW_EINVAL;
   return std::max(m, n) <= (1 << 20) && std::min(m, n) <= 16384 && count <= TW_ORTHO_MOST ? TW_OK : TW_EUNSUPPORTED;
@@ -853,6 +858,80 @@ tw_status tw_layer_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t
   return from_cuda(tw::launch_norm_bwd(a, as_stream(stream)));
 }
 
+// ------------------------------------------------------------------ root-mean-square norm
+namespace {
+// The forward's checks; y: rows of ytype bytes or elements
+tw_status check_rms_fwd(const void* x, int64_t ldx, const void* res, int64_t ldres, const void* weight, int T, int d,
+                        float eps, int dtype, int wtype, void* sum, int64_t ldsum, float* rstd, tw::NormFwdArgs& a) {
+  tw_status st = check_norm(T, d, dtype, wtype);
+  if (st != TW_OK) return st;
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return TW_EINVAL;
+  if (T == 0) return TW_OK;
+  if (sum != nullptr && res == nullptr) return TW_EINVAL;
+  const RowMatrix rows[] = {{x, ldx, true, false}, {res, ldres, false, false}, {sum, ldsum, false, true}};
+  st = check_rows(rows, 3, d, dtype);
+  if (st == TW_OK) st = check_elems(weight, wtype);
+  if (st == TW_OK) st = check_side({}, {rstd});
+  a.x = x, a.res = res, a.w = weight, a.sum = sum, a.rstd = rstd;
+  a.ldx = ldx, a.ldres = res ? ldres : 0, a.ldsum = sum ? ldsum : 0;
+  a.T = T, a.d = d, a.eps = eps, a.dtype = dtype, a.wtype = wtype;
+  return st;
+}
+}  // namespace
+
+tw_status tw_rms_norm_fwd(const void* x, int64_t ldx, const void* res, int64_t ldres, const void* weight, int T, int d,
+                          float eps, int dtype, int wtype, void* sum, int64_t ldsum, void* y, int64_t ldy, float* rstd,
+                          void* stream) {
+  tw::NormFwdArgs a = {};
+  tw_status st = check_rms_fwd(x, ldx, res, ldres, weight, T, d, eps, dtype, wtype, sum, ldsum, rstd, a);
+  if (st != TW_OK || T == 0) return st;
+  const RowMatrix out = {y, ldy, true, true};
+  st = check_rows(&out, 1, d, dtype);
+  if (st != TW_OK) return st;
+  a.y = y, a.ldy = ldy;
+  return from_cuda(tw::launch_rms_fwd(a, as_stream(stream)));
+}
+
+tw_status tw_rms_norm_fwd_fp8(const void* x, int64_t ldx, const void* res, int64_t ldres, const void* weight, int T,
+                              int d, float eps, int dtype, int wtype, void* sum, int64_t ldsum, uint8_t* q, int64_t ldq,
+                              float* scales, int group, float* rstd, void* stream) {
+  if (group != 0 && group != 128) return group < 0 ? TW_EINVAL : TW_EUNSUPPORTED;
+  tw::NormFwdArgs a = {};
+  tw_status st = check_rms_fwd(x, ldx, res, ldres, weight, T, d, eps, dtype, wtype, sum, ldsum, rstd, a);
+  if (st != TW_OK || T == 0) return st;
+  if (q == nullptr || ldq < d) return TW_EINVAL;
+  st = check_side({scales}, {});
+  if (st != TW_OK) return st;
+  a.y = q, a.ldy = ldq, a.scales = scales;
+  return from_cuda(tw::launch_rms_fp8(a, group, as_stream(stream)));
+}
+
+size_t tw_rms_norm_bwd_workspace_size(int T, int d) { return tw_layer_norm_bwd_workspace_size(T, d) / 2; }
+
+tw_status tw_rms_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const float* rstd,
+                          const void* weight, const void* dres, int64_t lddres, int T, int d, int dtype, int wtype,
+                          void* dx, int64_t lddx, float* dweight, void* ws, size_t ws_bytes, void* stream) {
+  tw_status st = check_norm(T, d, dtype, wtype);
+  if (st != TW_OK) return st;
+  st = check_side({}, {dweight});
+  if (st != TW_OK) return st;
+  if (T > 0) {
+    const RowMatrix rows[] = {{dy, lddy, true, false}, {x, ldx, true, false}, {dres, lddres, false, false}, {dx, lddx, true, true}};
+    st = check_rows(rows, 4, d, dtype);
+    if (st == TW_OK) st = check_side({rstd}, {});
+    if (st == TW_OK) st = check_elems(weight, wtype);
+    if (st == TW_OK && dweight != nullptr) st = check_ptrs({ws});
+    if (st != TW_OK) return st;
+    if (dweight != nullptr && ws_bytes < tw_rms_norm_bwd_workspace_size(T, d)) return TW_EWORKSPACE;
+  }
+  tw::NormBwdArgs a = {};
+  a.dy = dy, a.x = x, a.w = weight, a.dres = dres, a.rstd = rstd, a.dx = dx, a.dw = dweight;
+  a.part = dweight != nullptr ? static_cast<float*>(ws) : nullptr;
+  a.lddy = lddy, a.ldx = ldx, a.lddres = dres ? lddres : 0, a.lddx = lddx;
+  a.T = T, a.d = d, a.dtype = dtype, a.wtype = wtype;
+  return from_cuda(tw::launch_rms_bwd(a, as_stream(stream)));
+}
+
 // ------------------------------------------------------------------ rows of logits
 tw_status tw_distill(const void* z, int64_t ldz, int N, int V, int dtype, const int32_t* t_idx, const void* t_val,
                      int t_dtype, int K, const float* t_rest, const int32_t* labels, float temperature,
@@ -905,6 +984,51 @@ tw_status tw_token_logprobs(const void* z, int64_t ldz, int N, int V, int dtype,
   a.tokens = tokens, a.n_tokens = n_tokens, a.K = top_k, a.temperature = temperature;
   a.logprob = logprob, a.entropy = entropy, a.top_idx = top_idx, a.top_logprob = top_logprob, a.status = dev_status;
   return from_cuda(tw::launch_logprobs(a, as_stream(stream)));
+}
+
+// ------------------------------------------------------------------ token embedding
+tw_status tw_embedding_fwd(const int32_t* tokens, const void* weight, int64_t ldw, int T, int V, int d, float scale,
+                           int dtype, int wtype, void* y, int64_t ldy, int32_t* dev_status, void* stream) {
+  tw_status st = check_embed(T, V, d, scale, dtype);
+  if (st == TW_OK && wtype != dtype && wtype != TW_F32) st = TW_EINVAL;
+  if (st != TW_OK || T == 0) return st;
+  const RowMatrix w = {weight, ldw, true, false}, o = {y, ldy, true, true};
+  st = check_rows(&w, 1, d, wtype);
+  if (st == TW_OK) st = check_rows(&o, 1, d, dtype);
+  if (st == TW_OK) st = check_side({tokens, dev_status}, {});
+  if (st != TW_OK) return st;
+  tw::EmbedFwdArgs a = {};
+  a.tokens = tokens, a.w = weight, a.y = y, a.status = dev_status, a.ldw = ldw, a.ldy = ldy;
+  a.T = T, a.V = V, a.d = d, a.dtype = dtype, a.wtype = wtype, a.scale = scale;
+  return from_cuda(tw::launch_embed_fwd(a, as_stream(stream)));
+}
+
+size_t tw_embedding_bwd_workspace_size(int T, int V, int d) {
+  return check_embed(T, V, d, 1.f, TW_F32) == TW_OK ? tw::embed_bwd_plan(T, V, d).bytes : 0;
+}
+
+tw_status tw_embedding_bwd(const void* dy, int64_t lddy, const int32_t* tokens, int T, int V, int d, float scale,
+                           int dtype, int add, float* dweight, int64_t lddw, void* ws, size_t ws_bytes,
+                           int32_t* dev_status, void* stream) {
+  tw_status st = check_embed(T, V, d, scale, dtype);
+  if (st != TW_OK) return st;
+  if (T == 0 && add) return TW_OK;
+  const RowMatrix g = {dy, lddy, T > 0, false}, o = {dweight, lddw, true, true};
+  st = check_rows(&g, 1, d, dtype);
+  if (st == TW_OK) st = check_rows(&o, 1, d, TW_F32);
+  if (st == TW_OK && T > 0) st = check_side({tokens}, {});
+  if (st == TW_OK) st = check_side({dev_status}, {});
+  if (st != TW_OK) return st;
+  const size_t need = tw::embed_bwd_plan(T, V, d).bytes;
+  if (need > 0) {
+    st = check_ptrs({ws});
+    if (st != TW_OK) return st;
+    if (ws_bytes < need) return TW_EWORKSPACE;
+  }
+  tw::EmbedBwdArgs a = {};
+  a.dy = dy, a.tokens = tokens, a.dw = dweight, a.status = dev_status, a.lddy = lddy, a.lddw = lddw;
+  a.T = T, a.V = V, a.d = d, a.dtype = dtype, a.add = add != 0, a.scale = scale;
+  return from_cuda(tw::launch_embed_bwd(a, ws, as_stream(stream)));
 }
 
 // ------------------------------------------------------------------ orthogonalised updates

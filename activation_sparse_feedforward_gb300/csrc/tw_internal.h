@@ -377,8 +377,12 @@ struct NormFwdArgs {
   int T, d;
   float eps;
   int dtype, wtype;
+  float* scales;                // RMS norm into 8 bits: [T], or [T, ceil(d / 128)]
 };
 cudaError_t launch_norm_fwd(const NormFwdArgs& a, cudaStream_t s);
+// RMS norm: no b and mean; fp8: y holds e4m3 bytes, group 0 (a scale a row) or 128
+cudaError_t launch_rms_fwd(const NormFwdArgs& a, cudaStream_t s);
+cudaError_t launch_rms_fp8(const NormFwdArgs& a, int group, cudaStream_t s);
 
 struct NormBwdArgs {
   const void *dy, *x, *w, *dres;  // w, dres may be null
@@ -399,6 +403,7 @@ constexpr int norm_partial_width(int d) {
   return d <= w ? w : (d + 511) / 512 * 512;
 }
 cudaError_t launch_norm_bwd(const NormBwdArgs& a, cudaStream_t s);
+cudaError_t launch_rms_bwd(const NormBwdArgs& a, cudaStream_t s);  // no mean and db; part [..][1][..]
 
 // ---------------------------------------------------------------- tw_logits.cu
 struct DistillArgs {
@@ -436,6 +441,43 @@ struct LogprobArgs {
 };
 cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t s);
 
+
+// ---------------------------------------------------------------- tw_embed.cu
+struct EmbedFwdArgs {
+  const int32_t* tokens;
+  const void* w;
+  void* y;
+  int32_t* status;
+  int64_t ldw, ldy;
+  int T, V, d, dtype, wtype;
+  float scale;
+};
+cudaError_t launch_embed_fwd(const EmbedFwdArgs& a, cudaStream_t s);
+
+constexpr int kEmbedMostChunk = 1024;
+// Sizes and workspace offsets of the backward's sort; bytes 0 where it needs none.
+struct EmbedBwdPlan {
+  int range, chunk, part_ld;
+  size_t key, pos, n_valid, present, part, bytes;
+};
+EmbedBwdPlan embed_bwd_plan(int T, int V, int d);
+
+struct EmbedBwdArgs {
+  const void* dy;
+  const int32_t* tokens;
+  float* dw;
+  int32_t* status;
+  int64_t lddy, lddw;
+  int T, V, d, dtype, add;
+  float scale;
+  // set by launch_embed_bwd
+  int *key, *pos, *n_valid;  // tokens and positions in sorted order, how many
+  unsigned* present;         // a bit for each token that occurs (null: not wanted)
+  float* part;               // [chunks][2][part_ld]: heads and tails of runs
+  int range, chunk, part_ld;
+  bool vec_out;
+};
+cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, void* ws, cudaStream_t s);
 
 // ---------------------------------------------------------------- tw_ortho.cu
 struct OrthoArgs {

@@ -1,0 +1,14 @@
+// Root-mean-square norm over the rows of [T, d], after an optional residual add
+// (tw_rms_norm_fwd).
+//
+//   s = x + r rounded to the type;  rstd = (sum s^2 / d + eps)^-1/2;  y = s rstd w
+//
+// The form of layer norm's forward (tw_norm.cu) with one sum, so one barrier, a row. Bound
+// by HBM.
+#include "tw_norm_rows.cuh"
+
+namespace tw {
+
+cudaError_t launch_rms_fwd(const NormFwdArgs& a, cudaStream_t s) { return norm_fwd<RMS_NORM>(a, s); }
+
+}  // namespace tw

@@ -1,6 +1,6 @@
-"""Torch-facing binding of the operators at the ends of a model around the feedforward
-layer: layer norm, the distillation loss and token log probabilities (see the last
-part of include/twell.h).
+"""Torch-facing binding of the operators on rows around the feedforward layer: token
+embedding, layer norm, root-mean-square norm, the distillation loss and token log
+probabilities (see the last part of include/twell.h).
 
 As in ``ops``: objects preallocate every buffer, calls enqueue on torch's current
 stream and neither allocate nor synchronise; one-shot functions build such an object.
@@ -185,6 +185,212 @@ def layer_norm_bwd(dy, x, mean, rstd, weight=None, dres=None):
     """One-shot backward. Returns (dx, dweight, dbias)."""
     ln = LayerNorm(x.shape[0], x.shape[1], x.dtype, None if weight is None else weight.dtype, device=x.device)
     return ln.backward(dy, x, weight, dres, mean, rstd)
+
+
+class RMSNorm:
+    """Preallocated root-mean-square norm of up to T rows of width d, forward (into the type,
+    or into 8 bits with scales) and backward (see tw_rms_norm_fwd, tw_rms_norm_fwd_fp8,
+    tw_rms_norm_bwd).
+
+    weight_dtype: the type of the weight, `dtype` (default) or float32. backward: whether the
+    buffers of the backward (dx, fp32 dweight, workspace) are kept. fp8: whether those of
+    forward_fp8 are kept in place of the forward's y. group: the columns of one scale, 128,
+    or 0 for the whole row.
+    """
+
+    def __init__(self, T: int, d: int, dtype: torch.dtype = torch.bfloat16, weight_dtype: torch.dtype | None = None,
+                 eps: float = 1e-6, backward: bool = True, fp8: bool = False, group: int = 0, device="cuda"):
+        self.T, self.d, self.dtype, self.eps, self.group = T, d, dtype, float(eps), group
+        self.weight_dtype = weight_dtype or dtype
+        self._dt, self._wdt = _dtype_code(dtype), _dtype_code(self.weight_dtype)
+        if self._wdt not in (self._dt, _lib.TW_F32):
+            raise ValueError(f"weight_dtype must be {dtype} or float32, got {self.weight_dtype}")
+        if group not in (0, 128):
+            raise ValueError(f"group must be 0 (the row) or 128, got {group}")
+        self._lib = _lib.load()
+        self.y = self.q = self.scales = None
+        if fp8:
+            self.q = torch.empty((T, d), dtype=torch.float8_e4m3fn, device=device)
+            self.scales = torch.empty((T, (d + 127) // 128 if group else 1), dtype=torch.float32, device=device)
+        else:
+            self.y = torch.empty((T, d), dtype=dtype, device=device)
+        self.sum = torch.empty((T, d), dtype=dtype, device=device)
+        self._rstd = torch.empty(T, dtype=torch.float32, device=device)
+        #: fp32 1 / sqrt(mean square + eps) of the last forward's rows
+        self.rstd = self._rstd
+        self.dx = self.dweight = None
+        if backward:
+            self.dx = torch.empty((T, d), dtype=dtype, device=device)
+            self.dweight = torch.empty(d, dtype=torch.float32, device=device)
+            self.ws_bytes = int(self._lib.tw_rms_norm_bwd_workspace_size(T, d))
+            self.ws = _workspace(self.ws_bytes, device)
+            self._to_bwd = _addresses(self.dx, self.dweight, self.ws)
+        self._to_fwd = _addresses(self.y, self.sum, self._rstd, self.q, self.scales)
+        self._device = _device_of(self.sum)
+        self._stream = _stream_of(self._device)
+
+    def _forward(self, x, weight, residual, fp8):
+        n, d, dt, dev = _rows("x", x, self.T), self.d, self.dtype, self._device
+        ldx = _matrix("x", x, dt, dev, n, d)
+        w = _vector("weight", weight, self.weight_dtype, dev, d)
+        if n != self.rstd.shape[0]:
+            self.rstd = self._rstd[:n]
+        to_y, to, to_rstd, to_q, to_scales = self._to_fwd
+        if residual is None:
+            r, ldr, to = None, 0, None
+        else:
+            r, ldr = residual.data_ptr(), _matrix("residual", residual, dt, dev, n, d)
+        if fp8:
+            code = self._lib.tw_rms_norm_fwd_fp8(x.data_ptr(), ldx, r, ldr, w, n, d, self.eps, self._dt, self._wdt, to, d,
+                                                 to_q, d, to_scales, self.group, to_rstd, self._stream())
+        else:
+            code = self._lib.tw_rms_norm_fwd(x.data_ptr(), ldx, r, ldr, w, n, d, self.eps, self._dt, self._wdt, to, d,
+                                             to_y, d, to_rstd, self._stream())
+        if code:
+            _lib.check(code, "tw_rms_norm_fwd_fp8" if fp8 else "tw_rms_norm_fwd")
+        return n, x if residual is None else self.sum if n == self.T else self.sum[:n]
+
+    def forward(self, x: torch.Tensor, weight: torch.Tensor | None = None,
+                residual: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+        """(y, s): s = x + residual (x itself without one), y = norm(s) weight."""
+        if self.y is None:
+            raise ValueError("this RMSNorm was made with fp8=True: call forward_fp8")
+        n, s = self._forward(x, weight, residual, False)
+        return (self.y if n == self.T else self.y[:n]), s
+
+    def forward_fp8(self, x: torch.Tensor, weight: torch.Tensor | None = None,
+                    residual: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+        """(q, scales, s): q [n, d] float8_e4m3fn and scales [n, 1] (or [n, ceil(d / 128)])
+        float32 with norm(s) weight = q scales."""
+        if self.q is None:
+            raise ValueError("this RMSNorm was made with fp8=False")
+        n, s = self._forward(x, weight, residual, True)
+        return (self.q, self.scales, s) if n == self.T else (self.q[:n], self.scales[:n], s)
+
+    def backward(self, dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor | None = None,
+                 dres: torch.Tensor | None = None, rstd: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+        """(dx, dweight) for x the tensor that was normalised (the forward's s); dres is added
+        to dx. rstd: the statistic, of the last forward by default."""
+        dx = self.dx
+        if dx is None:
+            raise ValueError("this RMSNorm was made with backward=False")
+        n, d, dt, dev = _rows("x", x, self.T), self.d, self.dtype, self._device
+        ldx, lddy = _matrix("x", x, dt, dev, n, d), _matrix("dy", dy, dt, dev, n, d)
+        w = _vector("weight", weight, self.weight_dtype, dev, d)
+        r = _vector("rstd", self.rstd if rstd is None else rstd, torch.float32, dev, n)
+        g, ldg = (None, 0) if dres is None else (dres.data_ptr(), _matrix("dres", dres, dt, dev, n, d))
+        if n != self.T:
+            dx = dx[:n]
+        to, to_w, ws = self._to_bwd
+        code = self._lib.tw_rms_norm_bwd(dy.data_ptr(), lddy, x.data_ptr(), ldx, r, w, g, ldg, n, d, self._dt, self._wdt,
+                                         to, d, to_w, ws, self.ws_bytes, self._stream())
+        if code:
+            _lib.check(code, "tw_rms_norm_bwd")
+        return dx, self.dweight
+
+
+def rms_norm_fwd(x, weight=None, eps: float = 1e-6, residual=None):
+    """One-shot forward. Returns (y, s, rstd)."""
+    op = RMSNorm(x.shape[0], x.shape[1], x.dtype, None if weight is None else weight.dtype, eps, backward=False,
+                 device=x.device)
+    y, s = op.forward(x, weight, residual)
+    return y, s, op.rstd
+
+
+def rms_norm_fwd_fp8(x, weight=None, eps: float = 1e-6, residual=None, group: int = 0):
+    """One-shot forward into 8 bits. Returns (q, scales, s, rstd)."""
+    op = RMSNorm(x.shape[0], x.shape[1], x.dtype, None if weight is None else weight.dtype, eps, backward=False, fp8=True,
+                 group=group, device=x.device)
+    return (*op.forward_fp8(x, weight, residual), op.rstd)
+
+
+def rms_norm_bwd(dy, x, rstd, weight=None, dres=None):
+    """One-shot backward. Returns (dx, dweight)."""
+    op = RMSNorm(x.shape[0], x.shape[1], x.dtype, None if weight is None else weight.dtype, device=x.device)
+    return op.backward(dy, x, weight, dres, rstd)
+
+
+class Embedding:
+    """Preallocated token embedding of up to T tokens from a table [V, d], forward and backward
+    (see tw_embedding_fwd, tw_embedding_bwd).
+
+    weight_dtype: the table's type, `dtype` (default) or float32. scale: what the rows are
+    multiplied with. backward: whether the workspace of the backward is kept; dweight: whether
+    a float32 gradient buffer [V, d] is (calls may also name theirs with `out`). Tokens are
+    int32, -1: none (a row of zeros); others outside [0, V) raise TW_EINVAL in `status`.
+    """
+
+    def __init__(self, T: int, V: int, d: int, dtype: torch.dtype = torch.bfloat16,
+                 weight_dtype: torch.dtype | None = None, scale: float = 1.0, backward: bool = True, dweight: bool = True,
+                 device="cuda"):
+        self.T, self.V, self.d, self.dtype, self.scale = T, V, d, dtype, float(scale)
+        self.weight_dtype = weight_dtype or dtype
+        self._dt, self._wdt = _dtype_code(dtype), _dtype_code(self.weight_dtype)
+        if self._wdt not in (self._dt, _lib.TW_F32):
+            raise ValueError(f"weight_dtype must be {dtype} or float32, got {self.weight_dtype}")
+        self._lib = _lib.load()
+        self.y = torch.empty((T, d), dtype=dtype, device=device)
+        self.dweight, self._backward = None, backward
+        if backward:
+            if dweight:
+                self.dweight = torch.empty((V, d), dtype=torch.float32, device=device)
+            self.ws_bytes = int(self._lib.tw_embedding_bwd_workspace_size(T, V, d))
+            self.ws = _workspace(self.ws_bytes, device)
+            self._to_bwd = _addresses(self.dweight, self.ws)
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        self._to_fwd = _addresses(self.y, self.status)
+        self._device = _device_of(self.y)
+        self._stream = _stream_of(self._device)
+
+    def _tokens(self, tokens: torch.Tensor) -> tuple[int, int]:
+        n = tokens.numel()
+        if n > self.T:
+            raise ValueError(f"tokens has {n} elements, expected at most {self.T}")
+        return n, _vector("tokens", tokens, torch.int32, self._device, n)
+
+    def forward(self, tokens: torch.Tensor, weight: torch.Tensor) -> torch.Tensor:
+        """y [n, d] for the n tokens, in their order whatever their shape."""
+        n, t = self._tokens(tokens)
+        ldw = _matrix("weight", weight, self.weight_dtype, self._device, self.V, self.d)
+        to, status = self._to_fwd
+        code = self._lib.tw_embedding_fwd(t, weight.data_ptr(), ldw, n, self.V, self.d, self.scale, self._dt, self._wdt, to,
+                                          self.d, status, self._stream())
+        if code:
+            _lib.check(code, "tw_embedding_fwd")
+        return self.y if n == self.T else self.y[:n]
+
+    def backward(self, dy: torch.Tensor, tokens: torch.Tensor, out: torch.Tensor | None = None,
+                 add: bool = False) -> torch.Tensor:
+        """The table's gradient [V, d] float32, written whole, or added to what `out` (or the
+        object's dweight) holds."""
+        if not self._backward:
+            raise ValueError("this Embedding was made with backward=False")
+        n, t = self._tokens(tokens)
+        lddy = _matrix("dy", dy, self.dtype, self._device, n, self.d)
+        to, ws = self._to_bwd
+        ld = self.d
+        if out is not None:
+            to, ld = out.data_ptr(), _matrix("out", out, torch.float32, self._device, self.V, self.d)
+        elif to is None:
+            raise ValueError("this Embedding was made with dweight=False: give `out`")
+        code = self._lib.tw_embedding_bwd(dy.data_ptr(), lddy, t, n, self.V, self.d, self.scale, self._dt, add, to, ld, ws,
+                                          self.ws_bytes, self._to_fwd[1], self._stream())
+        if code:
+            _lib.check(code, "tw_embedding_bwd")
+        return self.dweight if out is None else out
+
+
+def embedding_fwd(tokens, weight, scale: float = 1.0, dtype: torch.dtype | None = None):
+    """One-shot forward. Returns (y [tokens.numel(), d], status)."""
+    op = Embedding(tokens.numel(), weight.shape[0], weight.shape[1], dtype or weight.dtype, weight.dtype, scale,
+                   backward=False, device=weight.device)
+    return op.forward(tokens, weight), op.status
+
+
+def embedding_bwd(dy, tokens, V: int, scale: float = 1.0, out=None, add: bool = False):
+    """One-shot backward. Returns (dweight [V, d] float32, status)."""
+    op = Embedding(tokens.numel(), V, dy.shape[1], dy.dtype, scale=scale, dweight=out is None, device=dy.device)
+    return op.backward(dy, tokens, out, add), op.status
 
 
 class DistillLoss:

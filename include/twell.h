@@ -462,6 +462,35 @@ tw_status tw_layer_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t
                             int dtype, int wtype, void* dx, int64_t lddx, float* dweight, float* dbias, void* ws,
                             size_t ws_bytes, void* stream);
 
+/* Root-mean-square norm forward over the rows of x [T, d], after an optional residual add:
+ *   s = x + res (rounded to the type; s = x when res is NULL)
+ *   rstd = (sum(s^2) / d + eps)^-1/2,  y = s rstd * weight
+ * Arguments, types, strides and limits as tw_layer_norm_fwd. */
+tw_status tw_rms_norm_fwd(const void* x, int64_t ldx, const void* res, int64_t ldres, const void* weight, int T, int d,
+                          float eps, int dtype, int wtype, void* sum, int64_t ldsum, void* y, int64_t ldy, float* rstd,
+                          void* stream);
+
+/* The same with y in 8 bits, as the operand of an 8-bit product: e4m3 with an fp32 scale
+ * for each row (group 0) or for each 128 columns of it (group 128; the last may be shorter):
+ *   scale = max(max |y| / 448, 2^-126) over the row or group, of y in fp32
+ *   q = y / scale to e4m3, round to nearest even
+ * q [T, d] bytes, row stride ldq >= d; scales [T] or [T, ceil(d / 128)], dense. A row or
+ * group of zeros has scale 2^-126 and q 0. A NaN in y makes its scale and q NaN (0x7F). */
+tw_status tw_rms_norm_fwd_fp8(const void* x, int64_t ldx, const void* res, int64_t ldres, const void* weight, int T,
+                              int d, float eps, int dtype, int wtype, void* sum, int64_t ldsum, uint8_t* q, int64_t ldq,
+                              float* scales, int group, float* rstd, void* stream);
+
+/* Workspace bytes tw_rms_norm_bwd needs (partial sums of the weight's gradient). */
+size_t tw_rms_norm_bwd_workspace_size(int T, int d);
+
+/* Root-mean-square norm backward. x is what the forward normalised (its `sum` when it added
+ * a residual). With xh = x rstd, g = dy weight:
+ *   dx = rstd (g - xh sum(g xh) / d) + dres,  dweight = sum over rows of dy xh
+ * Arguments, in-place forms, order of the sums and limits as tw_layer_norm_bwd. */
+tw_status tw_rms_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const float* rstd,
+                          const void* weight, const void* dres, int64_t lddres, int T, int d, int dtype, int wtype,
+                          void* dx, int64_t lddx, float* dweight, void* ws, size_t ws_bytes, void* stream);
+
 /* Distillation of a student's logits z [N, V] from a teacher's top logits, with hard
  * labels mixed in; loss and gradient in one pass over z. Row n has a list of up to K
  * teacher entries: tokens t_idx[n, k] (-1: no entry) and logits t_val[n, k] (type
@@ -512,6 +541,28 @@ tw_status tw_distill(const void* z, int64_t ldz, int N, int V, int dtype, const 
 tw_status tw_token_logprobs(const void* z, int64_t ldz, int N, int V, int dtype, const int32_t* tokens, int n_tokens,
                             float temperature, int top_k, float* logprob, float* entropy, int32_t* top_idx,
                             float* top_logprob, int32_t* dev_status, void* stream);
+
+/* Token embedding forward: y[t] = scale * weight[tokens[t]] (one rounding), a row of zeros
+ * where the token is -1. weight [V, d] of type wtype, which is dtype or TW_F32; y [T, d] of
+ * type dtype. 0 <= T <= 2^22, 1 <= V <= 2^22, 1 <= d <= 16384; scale finite. Device condition:
+ * a token outside [-1, V) raises TW_EINVAL in *dev_status and is read as -1. */
+tw_status tw_embedding_fwd(const int32_t* tokens, const void* weight, int64_t ldw, int T, int V, int d, float scale,
+                           int dtype, int wtype, void* y, int64_t ldy, int32_t* dev_status, void* stream);
+
+/* Workspace bytes tw_embedding_bwd needs (the sorted positions, parts of long runs); 0 up to
+ * 512 tokens (ws may then be NULL). */
+size_t tw_embedding_bwd_workspace_size(int T, int V, int d);
+
+/* Token embedding backward, by sorted tokens:
+ *   dweight[v] = scale * sum of dy[t] over the t with tokens[t] = v   (+ dweight[v] when add)
+ * dy [T, d] of type dtype; dweight [V, d] fp32, row stride lddw: written whole (add 0: zeros
+ * for tokens that do not occur), or added to, which touches the rows of tokens that occur
+ * alone. Sums are fp32 in the order of t, long runs of one token in parts of fixed size: the
+ * same call gives the same bits. Limits, tokens of -1 and the device condition as the
+ * forward. */
+tw_status tw_embedding_bwd(const void* dy, int64_t lddy, const int32_t* tokens, int T, int V, int d, float scale,
+                           int dtype, int add, float* dweight, int64_t lddw, void* ws, size_t ws_bytes,
+                           int32_t* dev_status, void* stream);
 
 /* The most matrices of one tw_orthogonalize call. */
 enum { TW_ORTHO_MOST = 8 };

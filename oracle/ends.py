@@ -1,6 +1,6 @@
 """Definitions in float64 of the operators at the ends of a model around the
-feedforward layer: layer norm, distillation from a teacher's top logits, and token log
-probabilities. Plain numpy; infinities follow the conventions of include/twell.h."""
+feedforward layer: token embedding, layer norm, root-mean-square norm (into 8 bits too),
+distillation from a teacher's top logits, and token log probabilities. Plain numpy; infinities follow the conventions of include/twell.h."""
 from __future__ import annotations
 
 import numpy as np
@@ -30,6 +30,69 @@ def layer_norm_grad(dy, s, weight=None, eps=1e-5, dres=None):
     if dres is not None:
         dx = dx + dres
     return dx, (dy * xh).sum(axis=0), dy.sum(axis=0)
+
+
+# ---------------------------------------------------------------------- root-mean-square norm
+
+def rms_norm(s, weight=None, eps=1e-6):
+    """y and rstd of the rows of s (the residual stream, already added)."""
+    s = np.asarray(s, dtype=np.float64)
+    rstd = 1.0 / np.sqrt((s * s).mean(axis=1) + eps)
+    y = s * rstd[:, None]
+    return (y if weight is None else y * weight), rstd
+
+
+def rms_norm_grad(dy, s, weight=None, eps=1e-6, dres=None):
+    """dx, dweight of sum(dy * y) (+ sum(dres * s))."""
+    dy = np.asarray(dy, dtype=np.float64)
+    xh, rstd = rms_norm(s, eps=eps)
+    g = dy if weight is None else dy * weight
+    dx = rstd[:, None] * (g - xh * (g * xh).mean(axis=1, keepdims=True))
+    if dres is not None:
+        dx = dx + dres
+    return dx, (dy * xh).sum(axis=0)
+
+
+def e4m3_values():
+    """The non-negative finite e4m3 numbers, ascending: code c stands for the c-th."""
+    codes = np.arange(0x7F)
+    exp, man = codes >> 3, codes & 7
+    return np.where(exp == 0, man * 2.0 ** -9, (1 + man / 8.0) * 2.0 ** (exp - 7.0))
+
+
+def to_e4m3(v):
+    """v rounded to the nearest e4m3 number, ties to the even code, at most 448."""
+    grid = e4m3_values()
+    a = np.minimum(np.abs(v), grid[-1])
+    hi = np.searchsorted(grid, a)
+    lo = np.maximum(hi - 1, 0)
+    up, down = grid[hi] - a, a - grid[lo]
+    take = np.where((up < down) | ((up == down) & (hi % 2 == 0)), hi, lo)
+    return np.copysign(grid[take], v)
+
+
+def fp8_scales(y, group=0):
+    """Scales [T, parts] of y's rows, or of each `group` of their columns."""
+    parts = [y] if group == 0 else [y[:, c:c + group] for c in range(0, y.shape[1], group)]
+    return np.stack([np.maximum(np.abs(p).max(axis=1) / 448.0, 2.0 ** -126) for p in parts], axis=1)
+
+
+# ---------------------------------------------------------------------- token embedding
+
+def embedding(tokens, weight, scale=1.0):
+    y = np.zeros((len(tokens), weight.shape[1]))
+    for t, v in enumerate(tokens):
+        if v >= 0:
+            y[t] = scale * weight[v]
+    return y
+
+
+def embedding_grad(dy, tokens, V, scale=1.0):
+    dw = np.zeros((V, dy.shape[1]))
+    for t, v in enumerate(tokens):
+        if v >= 0:
+            dw[v] += scale * dy[t]
+    return dw
 
 
 # ---------------------------------------------------------------------- distillation

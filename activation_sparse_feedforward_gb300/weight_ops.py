@@ -41,11 +41,12 @@ class Orthogonalize:
         if not 1 <= self.steps <= 32:
             raise ValueError(f"steps must be 1 to 32, got {steps}")
         rows = list(coefficients)
-        rows = [tuple(rows)] * self.steps if len(rows) == 3 and not hasattr(rows[0], "__len__") else [tuple(r) for r in rows]
-        if len(rows) != self.steps or any(len(r) != 3 for r in rows):
+        if not any(hasattr(r, "__len__") for r in rows):
+            rows = [rows] * self.steps
+        if len(rows) != self.steps or any(not hasattr(r, "__len__") or len(r) != 3 for r in rows):
             raise ValueError("coefficients must be three numbers, or three for each step")
-        self.coefficients = rows
-        self._coef = (ctypes.c_float * (3 * self.steps))(*[float(v) for r in rows for v in r])
+        self.coefficients = [tuple(float(v) for v in r) for r in rows]
+        self._coef = (ctypes.c_float * (3 * self.steps))(*[v for r in self.coefficients for v in r])
         self._lib = _lib.load()
         self.ws_bytes = int(self._lib.tw_orthogonalize_workspace_size(m, n, count))
         if self.ws_bytes == 0:

@@ -30,6 +30,9 @@
 #include <algorithm>
 #include <cmath>
 
+#include <type_traits>
+
+#include "tw_gemm.cuh"
 #include "tw_internal.h"
 #include "tw_rows.cuh"
 
@@ -39,12 +42,15 @@ namespace {
 
 constexpr int kTile = 256;         // rows and columns of a unit; workspace matrices are whole tiles
 constexpr int kBK = 64;            // K of a stage
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kEpiWarps = 8;       // two per TMEM lane quarter, 128 columns each
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kOperandBytes = 128 * kBK * 2;  // a CTA's 128 rows of A, or its half of B's
 constexpr int kStageBytes = 2 * kOperandBytes;
-constexpr int kSmem = kStages * kStageBytes + 1024 + 256;
+constexpr int kChunkBytes = 32 * 32 * 2;       // an epilogue warp's 32 rows x 32 columns of fp16
+constexpr int kStagingBytes = kEpiWarps * 4 * kChunkBytes;  // two buffers of two blocks a warp
+constexpr int kSmem = kStages * kStageBytes + kStagingBytes + 1024 + 512;
+static_assert(kSmem <= 232448, "shared memory per CTA");
 constexpr int kGramLog2 = 12;      // E is stored times 2^12: |E| <= 4
 constexpr int kPolyLog2 = 10;      // B times 2^10: |B| <= 32
 
@@ -54,21 +60,21 @@ enum Kind { GRAM, SQUARE, APPLY };
 TW_DEV float2 half2_of(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
 
 struct NsArgs {
-  CUtensorMap a, b;
+  CUtensorMap a, b;          // operands
+  CUtensorMap in0, in1;      // epilogue blocks: SQUARE: E; APPLY: hi and lo
+  CUtensorMap out0, out1;    // GRAM: E; SQUARE: B; APPLY: the next hi, and lo
   int tiles_m, tiles_n;      // of one matrix of the result, in 256 x 256 tiles
   int count;                 // matrices
   int rows_a, rows_b;        // rows from one matrix to the next in the operands' maps
-  int kb_total, ksplit;      // K blocks; slices of a tile's K loop
+  int kb_total;              // K blocks of a tile
+  int tiles, whole, ksplit;  // tiles; how many of the first run as one unit, the others in ksplit slices
   int np, mp;                // padded sizes
-  float* part;               // [tiles][ksplit][2][kEpiWarps][128][32] fp32 (ksplit > 1)
-  int* arrived;              // [tiles][2][kEpiWarps], 0 between launches
+  float* part;               // [tiles - whole][ksplit][2][kEpiWarps][128][32] fp32
+  int* arrived;              // [tiles - whole][2][kEpiWarps], 0 between launches
   int32_t* status;
-  // epilogues
-  uint16_t* d;               // GRAM: E; SQUARE: B; APPLY: the next hi (null in the last step)
-  const uint16_t* e;         // SQUARE: E; APPLY: hi
-  uint16_t* lo;              // APPLY: lo, read and written in place
   float f0, f1;              // GRAM: acc * f0 - f1 on the diagonal; SQUARE: e * f0 + acc * f1;
                              // APPLY: x * f0 + acc * f1
+  int last;                  // APPLY: the last step, into out
   // the last step's APPLY: out [rows, cols] of type otype, row stride ldo, transposed or not
   void* out[TW_ORTHO_MOST];
   int64_t ldo;
@@ -77,16 +83,25 @@ struct NsArgs {
 };
 
 struct Unit {
-  int tile;   // over all matrices
-  int mat, i, j, slice, kb_lo, kb_hi;
+  int mat, i, j;             // matrix and tile
+  int split, slice;          // the tile's number among those in slices, or -1
+  int kb_lo, kb_hi;
 };
 template <int KIND>
 TW_DEV Unit unit_of(const NsArgs& p, int u, int per_mat) {
   Unit r;
-  r.tile = u / p.ksplit;
-  r.slice = u - r.tile * p.ksplit;
-  r.mat = r.tile / per_mat;
-  const int t = r.tile - r.mat * per_mat;
+  int tile = u;
+  r.split = -1, r.slice = 0, r.kb_lo = 0, r.kb_hi = p.kb_total;
+  if (u >= p.whole) {
+    r.split = (u - p.whole) / p.ksplit;
+    r.slice = (u - p.whole) - r.split * p.ksplit;
+    tile = p.whole + r.split;
+    const int chunk = (p.kb_total + p.ksplit - 1) / p.ksplit;
+    r.kb_lo = r.slice * chunk;
+    r.kb_hi = min(p.kb_total, r.kb_lo + chunk);
+  }
+  r.mat = tile / per_mat;
+  const int t = tile - r.mat * per_mat;
   if (KIND == APPLY) {
     r.i = t / p.tiles_n;
     r.j = t - r.i * p.tiles_n;
@@ -97,89 +112,174 @@ TW_DEV Unit unit_of(const NsArgs& p, int u, int per_mat) {
     r.i = i;
     r.j = t - i * (i + 1) / 2;
   }
-  const int chunk = (p.kb_total + p.ksplit - 1) / p.ksplit;
-  r.kb_lo = r.slice * chunk;
-  r.kb_hi = min(p.kb_total, r.kb_lo + chunk);
   return r;
 }
 
-// One output value of the last step.
+// The last step's result: 32 x 32 of it, a row a lane, into out's own type and strides.
 template <int OT>
-TW_DEV void put_out(const NsArgs& p, void* out, size_t at, float x) {
+TW_DEV void put_out(const NsArgs& p, void* base, int row, int col, const float (&v)[32], uint8_t* staging) {
   using S = typename Elem<OT>::S;
-  S* o = static_cast<S*>(out) + at;
-  float v = p.scale * x;
-  if (p.beta != 0.f) v = fmaf(p.beta, Elem<OT>::get(*o), v);
-  *o = Elem<OT>::put(v);
+  S* out = static_cast<S*>(base);
+  const int lane = threadIdx.x & 31;
+  auto one = [&](size_t at, float x) {
+    x *= p.scale;
+    if (p.beta != 0.f) x = fmaf(p.beta, Elem<OT>::get(out[at]), x);
+    out[at] = Elem<OT>::put(x);
+  };
+  if (p.transposed) {  // the lanes' rows are neighbours
+    if (row < p.rows) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (col + i < p.cols) one(static_cast<size_t>(col + i) * p.ldo + row, v[i]);
+    }
+    return;
+  }
+  // through shared memory, so that eight lanes write a row's 32 columns: rows of 128 bytes,
+  // 16-byte pieces at piece ^ (row % 8)
+  float4* st = reinterpret_cast<float4*>(staging);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) st[lane * 8 + (q ^ (lane & 7))] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+  __syncwarp();
+  const int sub = lane >> 3, q = lane & 7, c = col + 4 * q, row0 = row - lane;
+  const bool vec = p.ldo % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & (4 * sizeof(S) - 1)) == 0 && c + 4 <= p.cols;
+#pragma unroll
+  for (int r = sub; r < 32; r += 4) {
+    if (row0 + r >= p.rows) break;
+    float4 x = st[r * 8 + (q ^ (r & 7))];
+    const size_t at = static_cast<size_t>(row0 + r) * p.ldo + c;
+    if (vec) {
+      x.x *= p.scale, x.y *= p.scale, x.z *= p.scale, x.w *= p.scale;
+      using V = std::conditional_t<OT == TW_F32, uint4, uint2>;
+      union {
+        V w;
+        S e[4];
+      } u;
+      if (p.beta != 0.f) {
+        u.w = *reinterpret_cast<const V*>(out + at);
+        x.x = fmaf(p.beta, Elem<OT>::get(u.e[0]), x.x), x.y = fmaf(p.beta, Elem<OT>::get(u.e[1]), x.y);
+        x.z = fmaf(p.beta, Elem<OT>::get(u.e[2]), x.z), x.w = fmaf(p.beta, Elem<OT>::get(u.e[3]), x.w);
+      }
+      u.e[0] = Elem<OT>::put(x.x), u.e[1] = Elem<OT>::put(x.y), u.e[2] = Elem<OT>::put(x.z), u.e[3] = Elem<OT>::put(x.w);
+      *reinterpret_cast<V*>(out + at) = u.w;
+    } else {
+      const float y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c + i < p.cols) one(at + i, y[i]);
+    }
+  }
+  fence_proxy_async_smem();  // these accesses before the next block's arrival
+  __syncwarp();
 }
 
-// 32 columns from `col` on of the result's row `row` (both within the matrix).
+// A warp's way out: 32 x 32 blocks of the result by TMA, in two buffers of two blocks in
+// turn, each block's 64-byte rows in 16-byte pieces at piece ^ ((row / 2) % 4) (the maps'
+// 64-byte swizzle). Where the epilogue reads matrices (SQUARE: E, APPLY: hi and lo), their
+// blocks arrive in the same places, asked for as soon as the buffer's last stores have been
+// read. (Row by row from registers, 32 rows to an instruction, the stores alone outlasted
+// the products.)
 template <int KIND>
-TW_DEV void emit(const NsArgs& p, const Unit& u, int row, int col, float (&v)[32]) {
-  const int ld = p.np;
-  if constexpr (KIND == GRAM) {
+struct Blocks {
+  const NsArgs& p;
+  uint8_t* staging;     // this warp's 8 KB
+  uint64_t* bar;        // [2]
+  volatile int* abort_flag;
+  int lane, n = 0;      // chunks so far
+  int asked = 0;        // lane 0: chunks asked for
+  TW_DEV uint8_t* buffer(int k) const { return staging + (k & 1) * 2 * kChunkBytes; }
+  // lane 0: the next chunk's blocks at (row, col) of the stacked matrices
+  TW_DEV void ask(int row, int col) {
+    // one group a chunk: with the latest one excepted, this buffer's stores have been read
+    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    if constexpr (KIND != GRAM) {
+      uint8_t* b = buffer(n);
+      ++asked;
+      mbar_arrive_expect_tx(bar + (n & 1), (KIND == APPLY ? 2 : 1) * kChunkBytes);
+      tma_load_2d(b, &p.in0, bar + (n & 1), col, row);
+      if (KIND == APPLY) tma_load_2d(b + kChunkBytes, &p.in1, bar + (n & 1), col, row);
+    }
+  }
+  // the buffer is free, and what was asked for is there, for every lane
+  TW_DEV bool here() {
+    __syncwarp();
+    if constexpr (KIND == GRAM) return true;
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar + (n & 1), (n >> 1) & 1u, abort_flag, p.status)) != 0;
+  }
+  // lane 0, before the CTA leaves: no copy of this warp is under way
+  TW_DEV void finish() {
+    if (asked > n) mbar_wait_drain(bar + (n & 1), (n >> 1) & 1u);
+    bulk_wait_all();
+  }
+  TW_DEV uint4* piece(uint8_t* block, int row, int q) const {
+    return reinterpret_cast<uint4*>(block + row * 64) + (q ^ ((row >> 1) & 3));
+  }
+  // v: the products' sums of row `row` of the matrix (this lane's), columns [col, col + 32);
+  // base: the matrix's first row in the maps
+  TW_DEV void put(const Unit& u, int base, int row, int col, float (&v)[32]) {
+    uint8_t* b0 = buffer(n);
+    uint8_t* b1 = b0 + kChunkBytes;
+    if constexpr (KIND == GRAM) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = v[i] * p.f0 - (row == col + i ? p.f1 : 0.f);
-  } else {
-    const size_t at = (static_cast<size_t>(u.mat) * (KIND == APPLY ? p.mp : p.np) + row) * ld + col;
-    const uint4* e = reinterpret_cast<const uint4*>(p.e + at);
-    const uint4* lo = reinterpret_cast<const uint4*>(p.lo + at);
+      for (int i = 0; i < 32; ++i) v[i] = v[i] * p.f0 - (row == col + i ? p.f1 : 0.f);
+    } else {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint4 w = e[q];
-      uint4 l = make_uint4(0, 0, 0, 0);
-      if (KIND == APPLY) l = lo[q];
-      const uint32_t h[4] = {w.x, w.y, w.z, w.w}, m[4] = {l.x, l.y, l.z, l.w};
+      for (int q = 0; q < 4; ++q) {
+        const uint4 w = *piece(b0, lane, q);
+        uint4 l = make_uint4(0, 0, 0, 0);
+        if (KIND == APPLY) l = *piece(b1, lane, q);
+        const uint32_t h[4] = {w.x, w.y, w.z, w.w}, m[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float2 x = half2_of(h[k]);
-        if (KIND == APPLY) x = add2(x, half2_of(m[k]));
-        const int i = 8 * q + 2 * k;
-        v[i] = fmaf(v[i], p.f1, x.x * p.f0);
-        v[i + 1] = fmaf(v[i + 1], p.f1, x.y * p.f0);
+        for (int k = 0; k < 4; ++k) {
+          float2 x = half2_of(h[k]);
+          if (KIND == APPLY) x = add2(x, half2_of(m[k]));
+          const int i = 8 * q + 2 * k;
+          v[i] = fmaf(v[i], p.f1, x.x * p.f0);
+          v[i + 1] = fmaf(v[i + 1], p.f1, x.y * p.f0);
+        }
       }
     }
-  }
-  if constexpr (KIND == APPLY) {
-    if (p.d == nullptr) {
-      void* out = p.out[u.mat];
-      if (row >= p.rows) return;
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        if (col + i >= p.cols) break;
-        const size_t at = p.transposed ? static_cast<size_t>(col + i) * p.ldo + row
-                                       : static_cast<size_t>(row) * p.ldo + col + i;
-        if (p.otype == TW_F32) put_out<TW_F32>(p, out, at, v[i]);
-        else if (p.otype == TW_BF16) put_out<TW_BF16>(p, out, at, v[i]);
-        else put_out<TW_F16>(p, out, at, v[i]);
+    if constexpr (KIND == APPLY) {
+      if (p.last) {
+        __syncwarp();  // every lane has read its rows: the buffer is free
+        void* out = p.out[u.mat];
+        if (p.otype == TW_F32) put_out<TW_F32>(p, out, row, col, v, b0);
+        else if (p.otype == TW_BF16) put_out<TW_BF16>(p, out, row, col, v, b0);
+        else put_out<TW_F16>(p, out, row, col, v, b0);
+        if (lane == 0) bulk_commit();  // an empty group: a group a chunk
+        ++n;
+        return;
       }
-      return;
     }
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = pack_f16x2_rn(v[2 * i], v[2 * i + 1]);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) *piece(b0, lane, q) = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+    const bool mirror = KIND != APPLY && u.i != u.j;
+    if constexpr (KIND == APPLY) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float2 h = half2_of(w[i]);
+        w[i] = pack_f16x2_rn(v[2 * i] - h.x, v[2 * i + 1] - h.y);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) *piece(b1, lane, q) = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+    } else if (mirror) {  // the other side of the diagonal: columns as rows, 64 bytes a warp's store
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        reinterpret_cast<uint16_t*>(piece(b1, i, lane >> 3))[lane & 7] = static_cast<uint16_t>(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(&p.out0, b0, col, base + row);
+      if (KIND == APPLY) tma_store_2d(&p.out1, b1, col, base + row);
+      if (mirror) tma_store_2d(&p.out1, b1, row, base + col);
+      bulk_commit();
+    }
+    ++n;
   }
-  uint32_t w[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) w[i] = pack_f16x2_rn(v[2 * i], v[2 * i + 1]);
-  const size_t base = static_cast<size_t>(u.mat) * (KIND == APPLY ? p.mp : p.np);
-  uint4* d = reinterpret_cast<uint4*>(p.d + (base + row) * ld + col);
-#pragma unroll
-  for (int q = 0; q < 4; ++q) d[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-  if constexpr (KIND == APPLY) {
-    uint4* lo = reinterpret_cast<uint4*>(p.lo + (base + row) * ld + col);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float2 h = half2_of(w[i]);
-      w[i] = pack_f16x2_rn(v[2 * i] - h.x, v[2 * i + 1] - h.y);
-    }
-#pragma unroll
-    for (int q = 0; q < 4; ++q) lo[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-  } else if (u.i != u.j) {  // the other side of the diagonal: 32 rows' worth of a column at once
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      p.d[(base + col + 2 * i) * ld + row] = static_cast<uint16_t>(w[i]);
-      p.d[(base + col + 2 * i + 1) * ld + row] = static_cast<uint16_t>(w[i] >> 16);
-    }
-  }
-}
+};
 
 template <int KIND>
 __global__ void __launch_bounds__(kThreads, 1) ns_gemm_kernel(const __grid_constant__ NsArgs p) {
@@ -188,11 +288,13 @@ __global__ void __launch_bounds__(kThreads, 1) ns_gemm_kernel(const __grid_const
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
   uint8_t* tiles = smem_raw + pad;
-  uint64_t* full = reinterpret_cast<uint64_t*>(tiles + kStages * kStageBytes);
+  uint8_t* staging = tiles + kStages * kStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + kStagingBytes);
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;
   uint64_t* tempty = tfull + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+  uint64_t* block_bars = tempty + 2;  // [kEpiWarps][2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(block_bars + 2 * kEpiWarps);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -206,6 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_gemm_kernel(const __grid_const
       mbar_init(tfull + b, 1);
       mbar_init(tempty + b, 2 * kEpiWarps);
     }
+    for (int b = 0; b < 2 * kEpiWarps; ++b) mbar_init(block_bars + b, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -225,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_gemm_kernel(const __grid_const
   pdl_enter();
 
   const int per_mat = KIND == APPLY ? p.tiles_m * p.tiles_n : p.tiles_n * (p.tiles_n + 1) / 2;
-  const int units = per_mat * p.count * p.ksplit;
+  const int units = p.whole + (p.tiles - p.whole) * p.ksplit;
   const int pairs = gridDim.x >> 1, first = blockIdx.x >> 1;
 
   if (warp == 0) {
@@ -309,24 +412,29 @@ __global__ void __launch_bounds__(kThreads, 1) ns_gemm_kernel(const __grid_const
     }
   } else {
     const int ew = warp - 2, quarter = warp & 3, half = ew >> 2;
+    Blocks<KIND> blocks{p, staging + ew * 4 * kChunkBytes, block_bars + 2 * ew, abort_flag, lane};
     int local = 0;
-    for (int n = first; n < units; n += pairs, ++local) {
+    bool ok = true;
+    for (int n = first; ok && n < units; n += pairs, ++local) {
       const Unit u = unit_of<KIND>(p, n, per_mat);
       const int buf = local & 1;
-      int ok = 0;
-      if (lane == 0) ok = mbar_wait(tfull + buf, (local >> 1) & 1u, abort_flag, p.status) ? 1 : 0;
-      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-      if (!ok) break;
+      const int base = u.mat * (KIND == APPLY ? p.mp : p.np);
+      const int row = u.i * kTile + static_cast<int>(rank) * 128 + quarter * 32 + lane, col = u.j * kTile + half * 128;
+      const bool split = u.split >= 0;
+      // while the products run (a slice may have nothing to finish: its blocks come later)
+      if (!split && lane == 0) blocks.ask(base + row, col);
+      int done = 0;
+      if (lane == 0) done = mbar_wait(tfull + buf, (local >> 1) & 1u, abort_flag, p.status) ? 1 : 0;
+      if (!__shfl_sync(0xFFFFFFFFu, done, 0)) break;
       tc_fence_after_sync();
       const uint32_t t0 = tmem_base + static_cast<uint32_t>(buf * kTile + half * 128) + (static_cast<uint32_t>(quarter * 32) << 16);
-      const int row = u.i * kTile + static_cast<int>(rank) * 128 + quarter * 32 + lane, col = u.j * kTile + half * 128;
       bool finish = true;
       // this warp's block of a slice's sums, a column's 32 rows side by side
       auto slot = [&](int slice) {
-        return p.part + ((static_cast<size_t>(u.tile) * p.ksplit + slice) * 2 * kEpiWarps + rank * kEpiWarps + ew) * (128 * 32) + lane;
+        return p.part + ((static_cast<size_t>(u.split) * p.ksplit + slice) * 2 * kEpiWarps + rank * kEpiWarps + ew) * (128 * 32) + lane;
       };
-      int* arrived = p.arrived + (static_cast<size_t>(u.tile) * 2 + rank) * kEpiWarps + ew;
-      if (p.ksplit > 1) {
+      int* arrived = p.arrived + (static_cast<size_t>(u.split) * 2 + rank) * kEpiWarps + ew;
+      if (split) {
         // the warp that finds all other slices' sums here adds them, in the slices' order
         int seen = 0;
         if (lane == 0) seen = *static_cast<volatile int*>(arrived);
@@ -348,17 +456,18 @@ __global__ void __launch_bounds__(kThreads, 1) ns_gemm_kernel(const __grid_const
         }
         finish = seen == p.ksplit - 1;
         __threadfence();
+        if (finish && lane == 0) blocks.ask(base + row, col);
       }
       if (finish) {
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; ok && c < 4; ++c) {
           uint32_t w[32];
           float v[32];
           tmem_ld32(t0 + c * 32, w);
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(w[i]);
-          if (p.ksplit > 1) {
+          if (split) {
             float s[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) s[i] = 0.f;
@@ -375,14 +484,18 @@ __global__ void __launch_bounds__(kThreads, 1) ns_gemm_kernel(const __grid_const
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = s[i];
           }
-          emit<KIND>(p, u, row, col + c * 32, v);
+          ok = blocks.here();
+          if (!ok) break;
+          blocks.put(u, base, row, col + c * 32, v);
+          if (c + 1 < 4 && lane == 0) blocks.ask(base + row, col + (c + 1) * 32);
         }
-        if (p.ksplit > 1 && lane == 0) *arrived = 0;
+        if (split && lane == 0) *arrived = 0;
       }
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(peer_smem_addr(tempty + buf, 0));
     }
+    if (lane == 0) blocks.finish();
   }
   __syncthreads();
   cluster_sync();
@@ -419,15 +532,17 @@ struct NsInArgs {
   float mu;
   int nesterov;
   float* norms;                // [count][kNormBlocks][3]
-  float2* factor;              // [count]: two factors whose product is 2^k / |U|_F
   int* arrived;                // counters to clear
   int n_arrived;
   uint16_t *hi, *lo;           // [count][mp][np]
-  int mp, np, transposed, klog2;
+  int mp, np, klog2;
+  int first;                   // the launch's first matrix
+  bool vec;                    // g's and m's rows are whole vectors of 8 elements on 16 bytes
 };
 
 constexpr int kNormBlocks = 304, kNormThreads = 512;
 
+// U at element (r, c); store: writes the new momentum
 template <int GT>
 TW_DEV float update_of(const NsInArgs& a, int mat, int r, int c, bool store) {
   using S = typename Elem<GT>::S;
@@ -438,16 +553,62 @@ TW_DEV float update_of(const NsInArgs& a, int mat, int r, int c, bool store) {
   if (store) *m = v = fmaf(a.mu, v, g);
   return a.nesterov ? fmaf(a.mu, v, g) : v;
 }
+// The same for the 8 elements from c on; vec: rows of whole vectors on 16 bytes. Elements
+// past the row are 0.
+template <int GT>
+TW_DEV void update8(const NsInArgs& a, int mat, int r, int c, bool store, float (&u)[8]) {
+  if (!a.vec) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = c + i < a.cols ? update_of<GT>(a, mat, r, c + i, store) : 0.f;
+    return;
+  }
+  constexpr int E = Elem<GT>::E;
+  const uint4* g = reinterpret_cast<const uint4*>(static_cast<const typename Elem<GT>::S*>(a.g[mat]) + static_cast<size_t>(r) * a.ldg + c);
+#pragma unroll
+  for (int k = 0; k < 8 / E; ++k) {
+    float w[E];
+    Elem<GT>::unpack(g[k], w);
+#pragma unroll
+    for (int i = 0; i < E; ++i) u[k * E + i] = w[i];
+  }
+  if (a.m[mat] == nullptr) return;
+  float4* m = reinterpret_cast<float4*>(a.m[mat] + static_cast<size_t>(r) * a.ldm + c);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    float4 v = m[k];
+    float* x = u + 4 * k;
+    if (store) {
+      v = make_float4(fmaf(a.mu, v.x, x[0]), fmaf(a.mu, v.y, x[1]), fmaf(a.mu, v.z, x[2]), fmaf(a.mu, v.w, x[3]));
+      m[k] = v;
+    }
+    if (a.nesterov)
+      x[0] = fmaf(a.mu, v.x, x[0]), x[1] = fmaf(a.mu, v.y, x[1]), x[2] = fmaf(a.mu, v.z, x[2]), x[3] = fmaf(a.mu, v.w, x[3]);
+    else
+      x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+  }
+}
 
 // The momentum, and the squares' sums of U.
 template <int GT>
 __global__ void __launch_bounds__(kNormThreads) ns_norm_kernel(const NsInArgs a) {
   __shared__ NormSums red[kNormThreads / 32];
   pdl_enter();
-  const int mat = blockIdx.y;
+  const int mat = a.first + blockIdx.y;
   NormSums s = {0.f, 0.f, 0.f};
-  for (int r = blockIdx.x; r < a.rows; r += gridDim.x)
-    for (int c = threadIdx.x; c < a.cols; c += kNormThreads) add_square(s, update_of<GT>(a, mat, r, c, true));
+  const unsigned per_row = (a.cols + 7) / 8;
+  const long total = static_cast<long>(a.rows) * per_row, step = static_cast<long>(gridDim.x) * kNormThreads;
+  long i = static_cast<long>(blockIdx.x) * kNormThreads + threadIdx.x;
+  int r = static_cast<int>(i / per_row), c = static_cast<int>(i - static_cast<long>(r) * per_row);
+  const int dr = static_cast<int>(step / per_row), dc = static_cast<int>(step - static_cast<long>(dr) * per_row);
+#pragma unroll 2
+  for (; i < total; i += step) {
+    float u[8];
+    update8<GT>(a, mat, r, c * 8, true, u);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) add_square(s, u[k]);
+    r += dr, c += dc;
+    if (c >= static_cast<int>(per_row)) c -= per_row, ++r;
+  }
   s.small = warp_sum(s.small), s.mid = warp_sum(s.mid), s.big = warp_sum(s.big);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
   __syncthreads();
@@ -458,86 +619,109 @@ __global__ void __launch_bounds__(kNormThreads) ns_norm_kernel(const NsInArgs a)
     to[0] = s.small, to[1] = s.mid, to[2] = s.big;
   }
   if (mat == 0)
-    for (int i = blockIdx.x * kNormThreads + threadIdx.x; i < a.n_arrived; i += gridDim.x * kNormThreads) a.arrived[i] = 0;
+    for (int k = blockIdx.x * kNormThreads + threadIdx.x; k < a.n_arrived; k += gridDim.x * kNormThreads) a.arrived[k] = 0;
 }
 
-// X0 = U / |U|_F as hi + lo, times 2^klog2, on 64 x 64 tiles of the padded matrix.
-template <int GT>
-__global__ void __launch_bounds__(256) ns_start_kernel(const NsInArgs a, int norm_blocks) {
-  __shared__ float t[64][65];
+// 2^k / |U|_F from the sums, by every CTA (256 threads) in the same order; as two factors, so
+// that neither they nor a product by one of them overflows.
+TW_DEV float2 start_factor(const NsInArgs& a, int mat, int norm_blocks) {
   __shared__ double sum[256];
   __shared__ float2 factor;
-  pdl_enter();
-  const int mat = blockIdx.z, tid = threadIdx.x;
-  {  // the norm, by every CTA in the same order
-    double s = 0.0;
-    for (int i = tid; i < norm_blocks; i += 256) {
-      const float* n = a.norms + (static_cast<size_t>(mat) * kNormBlocks + i) * 3;
-      s += static_cast<double>(n[0]) * 0x1p-180 + static_cast<double>(n[1]) + static_cast<double>(n[2]) * 0x1p160;
-    }
-    sum[tid] = s;
-    __syncthreads();
-    if (tid < 32) {
-      for (int i = tid + 32; i < 256; i += 32) s += sum[i];
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-      if (tid == 0) {
-        // 2^k / |U| as two factors, so that neither they nor a product by one overflows
-        const double f = s > 0.0 ? ldexp(1.0 / sqrt(s), a.klog2) : (s == 0.0 ? 0.0 : s);
-        int e = 0;
-        if (f > 0.0 && f < 1e300) e = ilogb(f) / 2;
-        factor = make_float2(static_cast<float>(ldexp(1.0, e)), static_cast<float>(ldexp(f, -e)));
-      }
-    }
-    __syncthreads();
+  const int tid = threadIdx.x;
+  double s = 0.0;
+  for (int i = tid; i < norm_blocks; i += 256) {
+    const float* n = a.norms + (static_cast<size_t>(mat) * kNormBlocks + i) * 3;
+    s += static_cast<double>(n[0]) * 0x1p-180 + static_cast<double>(n[1]) + static_cast<double>(n[2]) * 0x1p160;
   }
+  sum[tid] = s;
+  __syncthreads();
+  if (tid < 32) {
+    for (int i = tid + 32; i < 256; i += 32) s += sum[i];
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    if (tid == 0) {
+      const double f = s > 0.0 ? ldexp(1.0 / sqrt(s), a.klog2) : (s == 0.0 ? 0.0 : s);
+      int e = 0;
+      if (f > 0.0 && f < 1e300) e = ilogb(f) / 2;
+      factor = make_float2(static_cast<float>(ldexp(1.0, e)), static_cast<float>(ldexp(f, -e)));
+    }
+  }
+  __syncthreads();
+  return factor;
+}
+
+// v as hi + lo, packed pairs
+TW_DEV void split_pair(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = pack_f16x2_rn(x, y);
+  const float2 h = half2_of(hi);
+  lo = pack_f16x2_rn(x - h.x, y - h.y);
+}
+
+// X0 = U / |U|_F as hi + lo, times 2^klog2, into the padded matrix.
+template <int GT>
+__global__ void __launch_bounds__(256) ns_start_kernel(const NsInArgs a, int norm_blocks) {
+  pdl_enter();
+  const int mat = a.first + blockIdx.y;
+  const float2 f = start_factor(a, mat, norm_blocks);
+  const unsigned per_row = a.np / 8;
+  const long total = static_cast<long>(a.mp) * per_row, step = static_cast<long>(gridDim.x) * 256;
+  long i = static_cast<long>(blockIdx.x) * 256 + threadIdx.x;
+  int r = static_cast<int>(i / per_row), c = static_cast<int>(i - static_cast<long>(r) * per_row);
+  const int dr = static_cast<int>(step / per_row), dc = static_cast<int>(step - static_cast<long>(dr) * per_row);
+#pragma unroll 2
+  for (; i < total; i += step) {
+    float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (r < a.rows && c * 8 < a.cols) update8<GT>(a, mat, r, c * 8, false, u);
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) split_pair(u[2 * k] * f.x * f.y, u[2 * k + 1] * f.x * f.y, h[k], l[k]);
+    const size_t at = (static_cast<size_t>(mat) * a.mp + r) * a.np + c * 8;
+    *reinterpret_cast<uint4*>(a.hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(a.lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+    r += dr, c += dc;
+    if (c >= static_cast<int>(per_row)) c -= per_row, ++r;
+  }
+}
+
+// The same for a wide matrix, whose transpose is kept, on 64 x 64 tiles.
+template <int GT>
+__global__ void __launch_bounds__(256) ns_start_wide_kernel(const NsInArgs a, int norm_blocks) {
+  __shared__ float t[64][65];
+  pdl_enter();
+  const int mat = a.first + blockIdx.z, tid = threadIdx.x;
+  const float2 f = start_factor(a, mat, norm_blocks);
   const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;  // in the padded matrix
   const int lane = tid & 63, first = tid >> 6;
+#pragma unroll 4
   for (int i = first; i < 64; i += 4) {
-    const int r = a.transposed ? c0 + i : r0 + i, c = a.transposed ? r0 + lane : c0 + lane;  // in g
-    float v = 0.f;
-    if (r < a.rows && c < a.cols) v = update_of<GT>(a, mat, r, c, false) * factor.x * factor.y;
-    if (a.transposed)
-      t[lane][i] = v;
-    else
-      t[i][lane] = v;
+    const int r = c0 + i, c = r0 + lane;  // in g
+    t[lane][i] = r < a.rows && c < a.cols ? update_of<GT>(a, mat, r, c, false) * f.x * f.y : 0.f;
   }
   __syncthreads();
   for (int i = tid; i < 64 * 32; i += 256) {
     const int r = i >> 5, c = (i & 31) * 2;
-    const float x = t[r][c], y = t[r][c + 1];
-    const uint32_t h = pack_f16x2_rn(x, y);
-    const float2 hv = half2_of(h);
+    uint32_t h, l;
+    split_pair(t[r][c], t[r][c + 1], h, l);
     const size_t at = (static_cast<size_t>(mat) * a.mp + r0 + r) * a.np + c0 + c;
     *reinterpret_cast<uint32_t*>(a.hi + at) = h;
-    *reinterpret_cast<uint32_t*>(a.lo + at) = pack_f16x2_rn(x - hv.x, y - hv.y);
+    *reinterpret_cast<uint32_t*>(a.lo + at) = l;
   }
 }
 
 // ------------------------------------------------------------------ host
 int up(int n) { return (n + kTile - 1) / kTile * kTile; }
 
+// The most units that run slices of tiles: two for each pair of SMs, or 8 for each tile.
+constexpr int kMostSlices = 152;
+
 struct Layout {
-  int mp, np, tri, ksplit_most;
+  int mp, np, tri, full, slices;
   size_t hi0, hi1, lo, e, b, part, arrived, norms, bytes;
 };
-// K slices of a symmetric product's tiles, so that its units about fill the pairs once.
-int slices(int tiles, int kb, int pairs, int most) {
-  int best = 1;
-  long best_cost = -1;
-  for (int s = 1; s <= std::min(kb, most); ++s) {
-    const int chunk = (kb + s - 1) / s;
-    if ((kb + chunk - 1) / chunk != s) continue;  // no empty slice
-    const long rounds = (static_cast<long>(tiles) * s + pairs - 1) / pairs;
-    const long cost = rounds * (chunk + 6) + (s > 1 ? 4 : 0);  // in K blocks; 6: a unit's fill and drain
-    if (best_cost < 0 || cost < best_cost) best = s, best_cost = cost;
-  }
-  return best;
-}
 Layout layout(int m, int n, int count) {
   Layout l{};
   l.mp = up(std::max(m, n)), l.np = up(std::min(m, n));
   const int t = l.np / kTile;
-  l.tri = t * (t + 1) / 2 * count;
+  l.tri = t * (t + 1) / 2 * count, l.full = l.mp / kTile * t * count;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t was = at;
@@ -546,29 +730,71 @@ Layout layout(int m, int n, int count) {
   };
   const size_t x = static_cast<size_t>(count) * l.mp * l.np * 2, s = static_cast<size_t>(count) * l.np * l.np * 2;
   l.hi0 = take(x), l.hi1 = take(x), l.lo = take(x), l.e = take(s), l.b = take(s);
-  // at most 16 slices of a tile, and no more units than two rounds of 76 pairs unless the tiles are more
-  l.ksplit_most = std::max(1, std::min(16, 160 / l.tri));
-  l.part = take(l.ksplit_most > 1 ? static_cast<size_t>(l.tri) * l.ksplit_most * kTile * kTile * 4 : 0);
-  l.arrived = take(static_cast<size_t>(l.tri) * 2 * kEpiWarps * 4);
+  l.slices = std::min(kMostSlices, 8 * std::max(l.tri, l.full));
+  l.part = take(static_cast<size_t>(l.slices) * kTile * kTile * 4);
+  l.arrived = take(static_cast<size_t>(l.slices) * 2 * kEpiWarps * 4);
   l.norms = take(static_cast<size_t>(count) * kNormBlocks * 3 * 4);
   l.bytes = at;
   return l;
 }
 
+// Which of a product's tiles run whole, in full rounds over the pairs, and in how many
+// slices of K the others do. Costs in K blocks (0.33 us): a unit's fill and drain that the
+// next one does not hide, and what the last slice of a tile reads of the others.
+void split_tiles(NsArgs& p, int pairs, int most) {
+  p.whole = p.tiles, p.ksplit = 1;
+  const int rounds = p.tiles / pairs;
+  long best = static_cast<long>((p.tiles + pairs - 1) / pairs) * (p.kb_total + 1);
+  for (int w = rounds; w >= std::max(0, rounds - 1); --w)
+    for (int s = 2; s <= std::min(p.kb_total, 8); ++s) {
+      const int rest = p.tiles - w * pairs, chunk = (p.kb_total + s - 1) / s;
+      if (rest == 0 || rest * s > most || (p.kb_total + chunk - 1) / chunk != s) continue;  // no empty slice
+      const long cost = static_cast<long>(w) * (p.kb_total + 1) + static_cast<long>((rest * s + pairs - 1) / pairs) * (chunk + 4) + 4 + 2 * s;
+      if (cost < best) best = cost, p.whole = w * pairs, p.ksplit = s;
+    }
+}
+
 template <int KIND>
-cudaError_t run_gemm(NsArgs& p, cudaStream_t s, const char* label) {
+cudaError_t run_gemm(NsArgs& p, int most_slices, cudaStream_t s, const char* label) {
   auto kern = ns_gemm_kernel<KIND>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  const int per_mat = KIND == APPLY ? p.tiles_m * p.tiles_n : p.tiles_n * (p.tiles_n + 1) / 2;
-  const long units = static_cast<long>(per_mat) * p.count * p.ksplit;
   static int resident = -1;  // the query depends only on the kernel
   if (resident < 0) resident = max_active_clusters(kern, kThreads, kSmem, 2);
-  const int pairs = static_cast<int>(std::min<long>(units, std::min(resident, device_sm_count() / 2)));
-  if (pairs < 1) return cudaErrorInvalidConfiguration;
-  e = launch_clustered(kern, dim3(2 * pairs), dim3(kThreads), kSmem, 2, s, p);
+  const int most = std::min(resident, device_sm_count() / 2);
+  if (most < 1) return cudaErrorInvalidConfiguration;
+  p.tiles = (KIND == APPLY ? p.tiles_m * p.tiles_n : p.tiles_n * (p.tiles_n + 1) / 2) * p.count;
+  split_tiles(p, most, most_slices);
+  const int units = p.whole + (p.tiles - p.whole) * p.ksplit;
+  e = launch_clustered(kern, dim3(2 * std::min(units, most)), dim3(kThreads), kSmem, 2, s, p);
   trace_mark(s, label);
   return e;
+}
+
+template <int GT>
+cudaError_t way_in(NsInArgs& in, bool wide, cudaStream_t s) {
+  // 8 rows or columns a thread and more; at most two CTAs an SM
+  const long vecs = static_cast<long>(in.rows) * ((in.cols + 7) / 8);
+  const int norm_blocks = static_cast<int>(std::min<long>(kNormBlocks, (vecs + kNormThreads - 1) / kNormThreads));
+  // matrices that fit L2 together go together; larger ones one after the other, so that the
+  // second kernel finds what the first has read and written
+  const size_t bytes = static_cast<size_t>(in.rows) * in.cols * ((GT == TW_F32 ? 4 : 2) + (in.m[0] != nullptr ? 4 : 0));
+  const int together = bytes * in.count <= (80u << 20) ? in.count : 1;
+  for (in.first = 0; in.first < in.count; in.first += together) {
+    cudaError_t e = launch(ns_norm_kernel<GT>, dim3(norm_blocks, together), dim3(kNormThreads), 0, s, in);
+    trace_mark(s, "ortho_norm");
+    if (e != cudaSuccess) return e;
+    if (wide) {
+      e = launch(ns_start_wide_kernel<GT>, dim3(in.np / 64, in.mp / 64, together), dim3(256), 0, s, in, norm_blocks);
+    } else {
+      const long n = static_cast<long>(in.mp) * (in.np / 8);
+      e = launch(ns_start_kernel<GT>, dim3(static_cast<unsigned>(std::min<long>(152 * 6, (n + 255) / 256)), together), dim3(256), 0, s, in,
+                 norm_blocks);
+    }
+    trace_mark(s, "ortho_start");
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
@@ -583,81 +809,65 @@ cudaError_t launch_ortho(const OrthoArgs& o, cudaStream_t s) {
   const int k = std::min(14, std::max(0, static_cast<int>(std::lround(0.5 * std::log2(static_cast<double>(o.m) * o.n)))));
 
   NsInArgs in = {};
-  for (int i = 0; i < o.count; ++i) in.g[i] = o.g[i], in.m[i] = o.buf != nullptr ? o.buf[i] : nullptr;
+  bool vec = o.n % 8 == 0 && o.ldg * static_cast<int64_t>(o.gtype == TW_F32 ? 4 : 2) % 16 == 0 && o.ldbuf % 4 == 0;
+  for (int i = 0; i < o.count; ++i) {
+    in.g[i] = o.g[i], in.m[i] = o.buf != nullptr ? o.buf[i] : nullptr;
+    vec = vec && ((reinterpret_cast<uintptr_t>(in.g[i]) | reinterpret_cast<uintptr_t>(in.m[i])) & 15u) == 0;
+  }
   in.ldg = o.ldg, in.ldm = o.ldbuf, in.gtype = o.gtype, in.count = o.count, in.rows = o.m, in.cols = o.n;
-  in.mu = o.mu, in.nesterov = o.nesterov;
+  in.mu = o.mu, in.nesterov = o.nesterov, in.vec = vec;
   in.norms = reinterpret_cast<float*>(ws + l.norms);
-  in.arrived = reinterpret_cast<int*>(ws + l.arrived), in.n_arrived = l.tri * 2 * kEpiWarps;
-  in.hi = at16(l.hi0), in.lo = at16(l.lo), in.mp = l.mp, in.np = l.np, in.transposed = wide, in.klog2 = k;
-  const int norm_blocks = std::min(o.m, kNormBlocks);
-  const dim3 start(l.np / 64, l.mp / 64, o.count);
-  cudaError_t e;
-  auto both_kernels = [&](auto norm, auto begin) {
-    e = launch(norm, dim3(norm_blocks, o.count), dim3(kNormThreads), 0, s, in);
-    trace_mark(s, "ortho_norm");
-    if (e != cudaSuccess) return;
-    e = launch(begin, start, dim3(256), 0, s, in, norm_blocks);
-    trace_mark(s, "ortho_start");
-  };
-  if (o.gtype == TW_F32) both_kernels(ns_norm_kernel<TW_F32>, ns_start_kernel<TW_F32>);
-  else if (o.gtype == TW_BF16) both_kernels(ns_norm_kernel<TW_BF16>, ns_start_kernel<TW_BF16>);
-  else both_kernels(ns_norm_kernel<TW_F16>, ns_start_kernel<TW_F16>);
+  in.arrived = reinterpret_cast<int*>(ws + l.arrived), in.n_arrived = l.slices * 2 * kEpiWarps;
+  in.hi = at16(l.hi0), in.lo = at16(l.lo), in.mp = l.mp, in.np = l.np, in.klog2 = k;
+  cudaError_t e = o.gtype == TW_F32    ? way_in<TW_F32>(in, wide, s)
+                  : o.gtype == TW_BF16 ? way_in<TW_BF16>(in, wide, s)
+                                       : way_in<TW_F16>(in, wide, s);
   if (e != cudaSuccess) return e;
 
+  // maps: operands in boxes of 64 x 128 (K-major) and 64 x 64 (MN-major), the epilogues' 32 x 32
   const uint64_t np2 = static_cast<uint64_t>(l.np) * 2;
   const uint64_t xrows = static_cast<uint64_t>(l.mp) * o.count, srows = static_cast<uint64_t>(l.np) * o.count;
-  CUtensorMap x_k[2], x_mn[2], em, bm;
+  CUtensorMap x_k[2], x_mn[2], x_block[2], lo_block, e_k, b_k, e_block, b_block;
+  bool ok = true;
+  auto map = [&](CUtensorMap& m, size_t at, uint64_t rows, uint32_t box_cols, uint32_t box_rows) {
+    ok = ok && make_tmap_bf16(&m, ws + at, l.np, rows, np2, box_cols, box_rows, box_cols == 32);
+  };
   for (int i = 0; i < 2; ++i) {
-    const uint16_t* x = at16(i ? l.hi1 : l.hi0);
-    if (!make_tmap_bf16(&x_k[i], x, l.np, xrows, np2, 64, 128, false) ||
-        !make_tmap_bf16(&x_mn[i], x, l.np, xrows, np2, 64, 64, false))
-      return cudaErrorInvalidValue;
+    const size_t x = i ? l.hi1 : l.hi0;
+    map(x_k[i], x, xrows, 64, 128), map(x_mn[i], x, xrows, 64, 64), map(x_block[i], x, xrows, 32, 32);
   }
-  if (!make_tmap_bf16(&em, at16(l.e), l.np, srows, np2, 64, 128, false) ||
-      !make_tmap_bf16(&bm, at16(l.b), l.np, srows, np2, 64, 128, false))
-    return cudaErrorInvalidValue;
+  map(lo_block, l.lo, xrows, 32, 32);
+  map(e_k, l.e, srows, 64, 128), map(b_k, l.b, srows, 64, 128), map(e_block, l.e, srows, 32, 32), map(b_block, l.b, srows, 32, 32);
+  if (!ok) return cudaErrorInvalidValue;
 
-  const int pairs = device_sm_count() / 2;
-  NsArgs base = {};
-  base.tiles_m = l.mp / kTile, base.tiles_n = l.np / kTile, base.count = o.count;
-  base.np = l.np, base.mp = l.mp;
-  base.part = reinterpret_cast<float*>(ws + l.part), base.arrived = in.arrived;
-  base.status = o.status, base.ksplit = 1;
+  NsArgs p = {};
+  p.tiles_m = l.mp / kTile, p.tiles_n = l.np / kTile, p.count = o.count, p.np = l.np, p.mp = l.mp;
+  p.part = reinterpret_cast<float*>(ws + l.part), p.arrived = in.arrived, p.status = o.status;
+  for (int i = 0; i < o.count; ++i) p.out[i] = o.out[i];
+  p.ldo = o.ldo, p.rows = std::max(o.m, o.n), p.cols = std::min(o.m, o.n), p.otype = o.otype, p.transposed = wide;
+  p.scale = static_cast<float>(std::ldexp(static_cast<double>(o.scale), -k)), p.beta = o.beta;
   for (int step = 0; step < o.steps; ++step) {
     const double a = o.coef[3 * step], b = o.coef[3 * step + 1], c = o.coef[3 * step + 2];
     const double t = step >= 3 ? 1.0 : 0.0, q0 = a + b * t + c * t * t, q1 = b + 2.0 * c * t;
     const int at = step & 1;
-    NsArgs p = base;
-    p.a = p.b = x_mn[at];
+    p.a = p.b = x_mn[at], p.in0 = p.in1 = p.out0 = p.out1 = e_block;
     p.rows_a = p.rows_b = l.mp, p.kb_total = l.mp / kBK;
-    p.ksplit = slices(l.tri, p.kb_total, pairs, l.ksplit_most);
-    p.d = at16(l.e);
     p.f0 = std::ldexp(1.f, kGramLog2 - 2 * k), p.f1 = static_cast<float>(std::ldexp(t, kGramLog2));
-    e = run_gemm<GRAM>(p, s, "ortho_gram");
+    e = run_gemm<GRAM>(p, l.slices, s, "ortho_gram");
     if (e != cudaSuccess) return e;
 
-    p.a = p.b = em;
+    p.a = p.b = e_k, p.out0 = p.out1 = b_block;
     p.rows_a = p.rows_b = l.np, p.kb_total = l.np / kBK;
-    p.ksplit = slices(l.tri, p.kb_total, pairs, l.ksplit_most);
-    p.d = at16(l.b), p.e = at16(l.e);
     p.f0 = static_cast<float>(std::ldexp(q1, kPolyLog2 - kGramLog2));
     p.f1 = static_cast<float>(std::ldexp(c, kPolyLog2 - 2 * kGramLog2));
-    e = run_gemm<SQUARE>(p, s, "ortho_square");
+    e = run_gemm<SQUARE>(p, l.slices, s, "ortho_square");
     if (e != cudaSuccess) return e;
 
-    p = base;
-    p.a = x_k[at], p.b = bm;
-    p.rows_a = l.mp, p.rows_b = l.np, p.kb_total = l.np / kBK;
-    const bool last = step + 1 == o.steps;
-    p.d = last ? nullptr : at16(at ? l.hi0 : l.hi1);
-    p.e = at16(at ? l.hi1 : l.hi0), p.lo = at16(l.lo);
+    p.a = x_k[at], p.b = b_k, p.in0 = x_block[at], p.in1 = p.out1 = lo_block, p.out0 = x_block[at ^ 1];
+    p.rows_a = l.mp;
+    p.last = step + 1 == o.steps;
     p.f0 = static_cast<float>(q0), p.f1 = std::ldexp(1.f, -kPolyLog2);
-    if (last) {
-      for (int i = 0; i < o.count; ++i) p.out[i] = o.out[i];
-      p.ldo = o.ldo, p.rows = std::max(o.m, o.n), p.cols = std::min(o.m, o.n), p.otype = o.otype, p.transposed = wide;
-      p.scale = static_cast<float>(std::ldexp(static_cast<double>(o.scale), -k)), p.beta = o.beta;
-    }
-    e = run_gemm<APPLY>(p, s, "ortho_apply");
+    e = run_gemm<APPLY>(p, l.slices, s, "ortho_apply");
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -42,13 +42,13 @@ namespace {
 
 constexpr int kTile = 256;         // rows and columns of a unit; workspace matrices are whole tiles
 constexpr int kBK = 64;            // K of a stage
-constexpr int kStages = 5;
+constexpr int kStages = 6;
 constexpr int kEpiWarps = 8;       // two per TMEM lane quarter, 128 columns each
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kOperandBytes = 128 * kBK * 2;  // a CTA's 128 rows of A, or its half of B's
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kChunkBytes = 32 * 32 * 2;       // an epilogue warp's 32 rows x 32 columns of fp16
-constexpr int kStagingBytes = kEpiWarps * 4 * kChunkBytes;  // two buffers of two blocks a warp
+constexpr int kStagingBytes = kEpiWarps * 2 * kChunkBytes;  // two blocks a warp
 constexpr int kSmem = kStages * kStageBytes + kStagingBytes + 1024 + 512;
 static_assert(kSmem <= 232448, "shared memory per CTA");
 constexpr int kGramLog2 = 12;      // E is stored times 2^12: |E| <= 4
@@ -61,7 +61,7 @@ TW_DEV float2 half2_of(uint32_t w) { return __half22float2(*reinterpret_cast<con
 
 struct NsArgs {
   CUtensorMap a, b;          // operands
-  CUtensorMap in0, in1;      // epilogue blocks: SQUARE: E; APPLY: hi and lo
+  const uint16_t *in0, *in1; // what the epilogue reads: SQUARE: E; APPLY: hi and lo
   CUtensorMap out0, out1;    // GRAM: E; SQUARE: B; APPLY: the next hi, and lo
   int tiles_m, tiles_n;      // of one matrix of the result, in 256 x 256 tiles
   int count;                 // matrices
@@ -168,47 +168,43 @@ TW_DEV void put_out(const NsArgs& p, void* base, int row, int col, const float (
         if (c + i < p.cols) one(at + i, y[i]);
     }
   }
-  fence_proxy_async_smem();  // these accesses before the next block's arrival
   __syncwarp();
 }
 
-// A warp's way out: 32 x 32 blocks of the result by TMA, in two buffers of two blocks in
-// turn, each block's 64-byte rows in 16-byte pieces at piece ^ ((row / 2) % 4) (the maps'
-// 64-byte swizzle). Where the epilogue reads matrices (SQUARE: E, APPLY: hi and lo), their
-// blocks arrive in the same places, asked for as soon as the buffer's last stores have been
-// read. (Row by row from registers, 32 rows to an instruction, the stores alone outlasted
-// the products.)
+// A warp's way out: 32 x 32 blocks of the result by TMA from shared memory, each
+// block's 64-byte rows in 16-byte pieces at piece ^ ((row / 2) % 4) (the maps'
+// 64-byte swizzle). Where the epilogue reads matrices (SQUARE: E, APPLY: hi and lo), a
+// block's 16 bytes a lane, four lanes to a row, are asked for a chunk ahead into registers
+// and handed to the lanes of their rows through the same buffer. (Row by row from
+// registers, 32 rows to an instruction, the accesses alone outlasted the products; with the
+// blocks read by TMA a chunk waited 1 us for its own.)
 template <int KIND>
 struct Blocks {
+  static constexpr int kIn = KIND == GRAM ? 0 : KIND == SQUARE ? 1 : 2;
   const NsArgs& p;
-  uint8_t* staging;     // this warp's 8 KB
-  uint64_t* bar;        // [2]
-  volatile int* abort_flag;
-  int lane, n = 0;      // chunks so far
-  int asked = 0;        // lane 0: chunks asked for
-  TW_DEV uint8_t* buffer(int k) const { return staging + (k & 1) * 2 * kChunkBytes; }
-  // lane 0: the next chunk's blocks at (row, col) of the stacked matrices
-  TW_DEV void ask(int row, int col) {
-    // one group a chunk: with the latest one excepted, this buffer's stores have been read
-    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-    if constexpr (KIND != GRAM) {
-      uint8_t* b = buffer(n);
-      ++asked;
-      mbar_arrive_expect_tx(bar + (n & 1), (KIND == APPLY ? 2 : 1) * kChunkBytes);
-      tma_load_2d(b, &p.in0, bar + (n & 1), col, row);
-      if (KIND == APPLY) tma_load_2d(b + kChunkBytes, &p.in1, bar + (n & 1), col, row);
-    }
+  uint8_t* staging;     // this warp's two blocks
+  int lane;
+  uint4 ahead[kIn > 0 ? kIn * 4 : 1];
+  // the chunk at (row0, col) of the stacked matrices
+  TW_DEV void ask(int row0, int col) {
+    const uint16_t* in[2] = {p.in0, p.in1};
+#pragma unroll
+    for (int m = 0; m < kIn; ++m)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        ahead[4 * m + q] = __ldcg(reinterpret_cast<const uint4*>(in[m] + static_cast<size_t>(row0 + 8 * q + (lane >> 2)) * p.np + col) + (lane & 3));
   }
-  // the buffer is free, and what was asked for is there, for every lane
-  TW_DEV bool here() {
+  // the buffer is free for every lane, and holds what was asked for
+  TW_DEV void take() {
+    if (lane == 0) bulk_wait_read_all();
     __syncwarp();
-    if constexpr (KIND == GRAM) return true;
-    return __all_sync(0xFFFFFFFFu, mbar_wait(bar + (n & 1), (n >> 1) & 1u, abort_flag, p.status)) != 0;
-  }
-  // lane 0, before the CTA leaves: no copy of this warp is under way
-  TW_DEV void finish() {
-    if (asked > n) mbar_wait_drain(bar + (n & 1), (n >> 1) & 1u);
-    bulk_wait_all();
+    if constexpr (kIn > 0) {
+#pragma unroll
+      for (int m = 0; m < kIn; ++m)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) *piece(staging + m * kChunkBytes, 8 * q + (lane >> 2), lane & 3) = ahead[4 * m + q];
+      __syncwarp();
+    }
   }
   TW_DEV uint4* piece(uint8_t* block, int row, int q) const {
     return reinterpret_cast<uint4*>(block + row * 64) + (q ^ ((row >> 1) & 3));
@@ -216,7 +212,7 @@ struct Blocks {
   // v: the products' sums of row `row` of the matrix (this lane's), columns [col, col + 32);
   // base: the matrix's first row in the maps
   TW_DEV void put(const Unit& u, int base, int row, int col, float (&v)[32]) {
-    uint8_t* b0 = buffer(n);
+    uint8_t* b0 = staging;
     uint8_t* b1 = b0 + kChunkBytes;
     if constexpr (KIND == GRAM) {
 #pragma unroll
@@ -240,13 +236,11 @@ struct Blocks {
     }
     if constexpr (KIND == APPLY) {
       if (p.last) {
-        __syncwarp();  // every lane has read its rows: the buffer is free
+        __syncwarp();  // every lane has read its rows
         void* out = p.out[u.mat];
         if (p.otype == TW_F32) put_out<TW_F32>(p, out, row, col, v, b0);
         else if (p.otype == TW_BF16) put_out<TW_BF16>(p, out, row, col, v, b0);
         else put_out<TW_F16>(p, out, row, col, v, b0);
-        if (lane == 0) bulk_commit();  // an empty group: a group a chunk
-        ++n;
         return;
       }
     }
@@ -277,7 +271,6 @@ struct Blocks {
       if (mirror) tma_store_2d(&p.out1, b1, row, base + col);
       bulk_commit();
     }
-    ++n;
   }
 };
 
@@ -293,8 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_gemm_kernel(const __grid_const
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;
   uint64_t* tempty = tfull + 2;
-  uint64_t* block_bars = tempty + 2;  // [kEpiWarps][2]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(block_bars + 2 * kEpiWarps);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -308,7 +300,6 @@ __global__ void __launch_bounds__(kThreads, 1) ns_gemm_kernel(const __grid_const
       mbar_init(tfull + b, 1);
       mbar_init(tempty + b, 2 * kEpiWarps);
     }
-    for (int b = 0; b < 2 * kEpiWarps; ++b) mbar_init(block_bars + b, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -412,17 +403,16 @@ __global__ void __launch_bounds__(kThreads, 1) ns_gemm_kernel(const __grid_const
     }
   } else {
     const int ew = warp - 2, quarter = warp & 3, half = ew >> 2;
-    Blocks<KIND> blocks{p, staging + ew * 4 * kChunkBytes, block_bars + 2 * ew, abort_flag, lane};
+    Blocks<KIND> blocks{p, staging + ew * 2 * kChunkBytes, lane};
     int local = 0;
-    bool ok = true;
-    for (int n = first; ok && n < units; n += pairs, ++local) {
+    for (int n = first; n < units; n += pairs, ++local) {
       const Unit u = unit_of<KIND>(p, n, per_mat);
       const int buf = local & 1;
       const int base = u.mat * (KIND == APPLY ? p.mp : p.np);
       const int row = u.i * kTile + static_cast<int>(rank) * 128 + quarter * 32 + lane, col = u.j * kTile + half * 128;
       const bool split = u.split >= 0;
       // while the products run (a slice may have nothing to finish: its blocks come later)
-      if (!split && lane == 0) blocks.ask(base + row, col);
+      if (!split) blocks.ask(base + row - lane, col);
       int done = 0;
       if (lane == 0) done = mbar_wait(tfull + buf, (local >> 1) & 1u, abort_flag, p.status) ? 1 : 0;
       if (!__shfl_sync(0xFFFFFFFFu, done, 0)) break;
@@ -456,11 +446,11 @@ __global__ void __launch_bounds__(kThreads, 1) ns_gemm_kernel(const __grid_const
         }
         finish = seen == p.ksplit - 1;
         __threadfence();
-        if (finish && lane == 0) blocks.ask(base + row, col);
+        if (finish) blocks.ask(base + row - lane, col);
       }
       if (finish) {
 #pragma unroll 1
-        for (int c = 0; ok && c < 4; ++c) {
+        for (int c = 0; c < 4; ++c) {
           uint32_t w[32];
           float v[32];
           tmem_ld32(t0 + c * 32, w);
@@ -484,10 +474,9 @@ __global__ void __launch_bounds__(kThreads, 1) ns_gemm_kernel(const __grid_const
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = s[i];
           }
-          ok = blocks.here();
-          if (!ok) break;
+          blocks.take();
+          if (c + 1 < 4) blocks.ask(base + row - lane, col + (c + 1) * 32);
           blocks.put(u, base, row, col + c * 32, v);
-          if (c + 1 < 4 && lane == 0) blocks.ask(base + row, col + (c + 1) * 32);
         }
         if (split && lane == 0) *arrived = 0;
       }
@@ -495,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_gemm_kernel(const __grid_const
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(peer_smem_addr(tempty + buf, 0));
     }
-    if (lane == 0) blocks.finish();
+    if (lane == 0) bulk_wait_all();
   }
   __syncthreads();
   cluster_sync();
@@ -850,20 +839,20 @@ cudaError_t launch_ortho(const OrthoArgs& o, cudaStream_t s) {
     const double a = o.coef[3 * step], b = o.coef[3 * step + 1], c = o.coef[3 * step + 2];
     const double t = step >= 3 ? 1.0 : 0.0, q0 = a + b * t + c * t * t, q1 = b + 2.0 * c * t;
     const int at = step & 1;
-    p.a = p.b = x_mn[at], p.in0 = p.in1 = p.out0 = p.out1 = e_block;
+    p.a = p.b = x_mn[at], p.out0 = p.out1 = e_block;
     p.rows_a = p.rows_b = l.mp, p.kb_total = l.mp / kBK;
     p.f0 = std::ldexp(1.f, kGramLog2 - 2 * k), p.f1 = static_cast<float>(std::ldexp(t, kGramLog2));
     e = run_gemm<GRAM>(p, l.slices, s, "ortho_gram");
     if (e != cudaSuccess) return e;
 
-    p.a = p.b = e_k, p.out0 = p.out1 = b_block;
+    p.a = p.b = e_k, p.in0 = at16(l.e), p.out0 = p.out1 = b_block;
     p.rows_a = p.rows_b = l.np, p.kb_total = l.np / kBK;
     p.f0 = static_cast<float>(std::ldexp(q1, kPolyLog2 - kGramLog2));
     p.f1 = static_cast<float>(std::ldexp(c, kPolyLog2 - 2 * kGramLog2));
     e = run_gemm<SQUARE>(p, l.slices, s, "ortho_square");
     if (e != cudaSuccess) return e;
 
-    p.a = x_k[at], p.b = b_k, p.in0 = x_block[at], p.in1 = p.out1 = lo_block, p.out0 = x_block[at ^ 1];
+    p.a = x_k[at], p.b = b_k, p.in0 = at16(at ? l.hi1 : l.hi0), p.in1 = at16(l.lo), p.out0 = x_block[at ^ 1], p.out1 = lo_block;
     p.rows_a = l.mp;
     p.last = step + 1 == o.steps;
     p.f0 = static_cast<float>(q0), p.f1 = std::ldexp(1.f, -kPolyLog2);

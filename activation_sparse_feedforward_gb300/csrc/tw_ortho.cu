@@ -8,7 +8,10 @@
 // X is kept with its longer side as rows ([m, n], m >= n; a wide matrix is transposed on
 // the way in and out), padded with zeros to 256 x 256 tiles, which the products keep zero.
 // Three products a step on the tensor cores, each on CTA pairs (tcgen05.mma.cta_group::2,
-// 256 x 256 units, TMEM double-buffered, TMA ring):
+// 256 x 256 units, TMEM double-buffered, TMA ring), all steps' in one launch: pairs draw
+// units (a tile of a product of a matrix) from one list, and a unit's loads wait until the
+// counter of what it reads says that it is there (15 launches had cost a tail each, in
+// which most SMs had nothing to do):
 //
 //   gram    E = X^T X - t I     the lower triangle's tiles, stored on both sides
 //   square  B = q1 E + c E^2    the same
@@ -42,13 +45,13 @@ namespace {
 
 constexpr int kTile = 256;         // rows and columns of a unit; workspace matrices are whole tiles
 constexpr int kBK = 64;            // K of a stage
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kEpiWarps = 8;       // two per TMEM lane quarter, 128 columns each
-constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kThreads = 96 + 32 * kEpiWarps;
 constexpr int kOperandBytes = 128 * kBK * 2;  // a CTA's 128 rows of A, or its half of B's
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kChunkBytes = 32 * 32 * 2;       // an epilogue warp's 32 rows x 32 columns of fp16
-constexpr int kStagingBytes = kEpiWarps * 2 * kChunkBytes;  // two blocks a warp
+constexpr int kStagingBytes = kEpiWarps * 4 * kChunkBytes;  // two buffers of two blocks a warp
 constexpr int kSmem = kStages * kStageBytes + kStagingBytes + 1024 + 512;
 static_assert(kSmem <= 232448, "shared memory per CTA");
 constexpr int kGramLog2 = 12;      // E is stored times 2^12: |E| <= 4
@@ -59,22 +62,25 @@ enum Kind { GRAM, SQUARE, APPLY };
 // a word's worth of fp16
 TW_DEV float2 half2_of(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
 
+constexpr int kMostSteps = 32;
+
 struct NsArgs {
-  CUtensorMap a, b;          // operands
-  const uint16_t *in0, *in1; // what the epilogue reads: SQUARE: E; APPLY: hi and lo
-  CUtensorMap out0, out1;    // GRAM: E; SQUARE: B; APPLY: the next hi, and lo
-  int tiles_m, tiles_n;      // of one matrix of the result, in 256 x 256 tiles
-  int count;                 // matrices
-  int rows_a, rows_b;        // rows from one matrix to the next in the operands' maps
-  int kb_total;              // K blocks of a tile
-  int tiles, whole, ksplit;  // tiles; how many of the first run as one unit, the others in ksplit slices
+  // operands: X as K-major and MN-major boxes (X alternates between two buffers), E and B
+  CUtensorMap x_k[2], x_mn[2], e_k, b_k;
+  // 32 x 32 blocks that the epilogues read and write: hi, lo, E, B
+  CUtensorMap x_block[2], lo_block, e_block, b_block;
+  int tiles_m, tiles_n;      // 256 x 256 tiles of X; tiles_n along a side of E and B
+  int count, steps;          // matrices, steps
   int np, mp;                // padded sizes
-  float* part;               // [tiles - whole][ksplit][2][kEpiWarps][128][32] fp32
-  int* arrived;              // [tiles - whole][2][kEpiWarps], 0 between launches
+  int slices[3];             // slices of a tile's K loop, by Kind
+  int slots;                 // part's and arrived's tiles x slices of one matrix
+  float* part;               // [count][slots][2][kEpiWarps][128][32] fp32
+  int* arrived;              // [count][slots][2][kEpiWarps], 0 between calls
+  int* done;                 // [count][3]: blocks of warps finished, by Kind, over all steps; 0 at first
+  int* next;                 // the next unit, 0 at first
   int32_t* status;
-  float f0, f1;              // GRAM: acc * f0 - f1 on the diagonal; SQUARE: e * f0 + acc * f1;
-                             // APPLY: x * f0 + acc * f1
-  int last;                  // APPLY: the last step, into out
+  // GRAM: acc * f0 - f1 on the diagonal; SQUARE: e * f0 + acc * f1; APPLY: x * f0 + acc * f1
+  float f0[kMostSteps][3], f1[kMostSteps][3];
   // the last step's APPLY: out [rows, cols] of type otype, row stride ldo, transposed or not
   void* out[TW_ORTHO_MOST];
   int64_t ldo;
@@ -82,38 +88,154 @@ struct NsArgs {
   float scale, beta;
 };
 
+// A unit: a tile of one product of one matrix in one step, or a slice of its K loop.
 struct Unit {
-  int mat, i, j;             // matrix and tile
-  int split, slice;          // the tile's number among those in slices, or -1
-  int kb_lo, kb_hi;
+  int step, kind, mat, tile, slice;
 };
-template <int KIND>
-TW_DEV Unit unit_of(const NsArgs& p, int u, int per_mat) {
-  Unit r;
-  int tile = u;
-  r.split = -1, r.slice = 0, r.kb_lo = 0, r.kb_hi = p.kb_total;
-  if (u >= p.whole) {
-    r.split = (u - p.whole) / p.ksplit;
-    r.slice = (u - p.whole) - r.split * p.ksplit;
-    tile = p.whole + r.split;
-    const int chunk = (p.kb_total + p.ksplit - 1) / p.ksplit;
-    r.kb_lo = r.slice * chunk;
-    r.kb_hi = min(p.kb_total, r.kb_lo + chunk);
+// The units in the order in which they are handed out. In a step: every matrix's gram, then
+// a matrix's square always one matrix ahead of its apply, so that what a unit waits for was
+// handed out well before it. A unit waits only for units before it in this order; whoever
+// was given those is running, so the wait ends, however few of the CTAs are resident.
+TW_DEV bool unit_at(const NsArgs& p, int n, Unit& u) {
+  const int tri = p.tiles_n * (p.tiles_n + 1) / 2, all = p.tiles_m * p.tiles_n;
+  const int g = tri * p.slices[GRAM], q = tri * p.slices[SQUARE], a = all * p.slices[APPLY];
+  const int per_step = p.count * (g + q + a);
+  u.step = n / per_step;
+  if (u.step >= p.steps) return false;
+  int r = n - u.step * per_step;
+  auto is = [&](int kind, int mat) {
+    u.kind = kind, u.mat = mat, u.tile = r / p.slices[kind], u.slice = r - u.tile * p.slices[kind];
+  };
+  if (r < p.count * g) {
+    const int mat = r / g;
+    r -= mat * g;
+    is(GRAM, mat);
+    return true;
   }
-  r.mat = tile / per_mat;
-  const int t = tile - r.mat * per_mat;
-  if (KIND == APPLY) {
-    r.i = t / p.tiles_n;
-    r.j = t - r.i * p.tiles_n;
-  } else {  // the lower triangle, row by row
-    int i = static_cast<int>((sqrtf(8.f * t + 1.f) - 1.f) * 0.5f);
-    while ((i + 1) * (i + 2) / 2 <= t) ++i;
-    while (i * (i + 1) / 2 > t) --i;
-    r.i = i;
-    r.j = t - i * (i + 1) / 2;
+  r -= p.count * g;
+  for (int i = -1; i < p.count; ++i) {
+    if (i + 1 < p.count) {
+      if (r < q) {
+        is(SQUARE, i + 1);
+        return true;
+      }
+      r -= q;
+    }
+    if (i >= 0) {
+      if (r < a) {
+        is(APPLY, i);
+        return true;
+      }
+      r -= a;
+    }
   }
-  return r;
+  return false;
 }
+// tile row and column
+TW_DEV void tile_at(const NsArgs& p, const Unit& u, int& i, int& j) {
+  if (u.kind == APPLY) {
+    i = u.tile / p.tiles_n;
+    j = u.tile - i * p.tiles_n;
+  } else {  // the lower triangle, row by row
+    i = static_cast<int>((sqrtf(8.f * u.tile + 1.f) - 1.f) * 0.5f);
+    while ((i + 1) * (i + 2) / 2 <= u.tile) ++i;
+    while (i * (i + 1) / 2 > u.tile) --i;
+    j = u.tile - i * (i + 1) / 2;
+  }
+}
+TW_DEV void k_blocks(const NsArgs& p, const Unit& u, int& lo, int& hi) {
+  const int total = (u.kind == GRAM ? p.mp : p.np) / kBK, chunk = (total + p.slices[u.kind] - 1) / p.slices[u.kind];
+  lo = u.slice * chunk;
+  hi = min(total, lo + chunk);
+}
+
+TW_DEV int ld_acquire(const int* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+// Waits (one thread, bounded) until all that unit u reads has been written: the apply of the
+// step before for a gram, the gram for a square, the square for an apply, of its matrix.
+TW_DEV bool wait_inputs(const NsArgs& p, const Unit& u, volatile int* abort_flag) {
+  const int tri = p.tiles_n * (p.tiles_n + 1) / 2, all = p.tiles_m * p.tiles_n;
+  const int of = u.kind == GRAM ? APPLY : u.kind == SQUARE ? GRAM : SQUARE;
+  const int need = (u.kind == GRAM ? u.step * all : (u.step + 1) * tri) * 2 * kEpiWarps;
+  const int* done = p.done + u.mat * 3 + of;
+  if (ld_acquire(done) < need) {
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t n = 1; ld_acquire(done) < need; ++n) {
+      __nanosleep(40);
+      if (*abort_flag) return false;
+      if ((n & 31u) == 0 && global_timer_ns() - t0 > TW_WAIT_LIMIT_NS) {
+        *abort_flag = 1;
+        raise_status(p.status, TW_ETIMEOUT);
+        return false;
+      }
+    }
+  }
+  return true;
+}
+// Orders what was written through the generic or async proxy and acquired here before this
+// thread's later accesses through either.
+TW_DEV void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+// A wait whose phase the other CTA of the pair completes, with data it wrote before.
+TW_DEV bool mbar_try_wait_cluster(uint32_t addr, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(addr), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+TW_DEV bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
+  const uint32_t addr = smem_addr(bar);
+  if (mbar_try_wait_cluster(addr, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t n = 1;; ++n) {
+    if (mbar_try_wait_cluster(addr, parity)) return true;
+    if ((n & 31u) == 0) {
+      if (*abort_flag) return false;
+      if (global_timer_ns() - t0 > TW_WAIT_LIMIT_NS) {
+        *abort_flag = 1;
+        raise_status(status, TW_ETIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+
+// The units of a pair: one thread of rank 0 draws them and puts each into a ring in both
+// CTAs' shared memory; every role of both CTAs takes them from there in turn.
+constexpr int kRing = 4;
+constexpr int kTakers = (2 + kEpiWarps) + (1 + kEpiWarps);  // rank 0's producer, issuer and warps; rank 1's
+struct UnitRing {
+  uint64_t full[kRing];    // one arrival
+  uint64_t empty[kRing];   // rank 0's: kTakers arrivals
+  uint2 unit[kRing];       // step | kind | mat | slice (8 bits each), tile; ~0: no more
+};
+struct Taker {
+  UnitRing* ring;
+  volatile int* abort_flag;
+  int32_t* status;
+  int n = 0;
+  // whole warps (or one thread that stands for its warp): the next unit; false: no more, or given up
+  TW_DEV bool take(Unit& u, bool one_thread) {
+    const int slot = n & (kRing - 1);
+    const bool ok = mbar_wait_cluster(ring->full + slot, (n / kRing) & 1u, abort_flag, status);
+    if (!(one_thread ? ok : __all_sync(0xFFFFFFFFu, ok))) return false;
+    const uint2 w = ring->unit[slot];
+    if (!one_thread) __syncwarp();
+    if (one_thread || (threadIdx.x & 31) == 0) mbar_arrive_cluster(peer_smem_addr(ring->empty + slot, 0));
+    ++n;
+    if (w.x == ~0u) return false;
+    u.step = w.x >> 24, u.kind = (w.x >> 16) & 255, u.mat = (w.x >> 8) & 255, u.slice = w.x & 255, u.tile = static_cast<int>(w.y);
+    return true;
+  }
+};
 
 // The last step's result: 32 x 32 of it, a row a lane, into out's own type and strides.
 template <int OT>
@@ -168,55 +290,54 @@ TW_DEV void put_out(const NsArgs& p, void* base, int row, int col, const float (
         if (c + i < p.cols) one(at + i, y[i]);
     }
   }
+  fence_proxy_async_smem();  // these accesses before the next block's arrival
   __syncwarp();
 }
 
-// A warp's way out: 32 x 32 blocks of the result by TMA from shared memory, each
-// block's 64-byte rows in 16-byte pieces at piece ^ ((row / 2) % 4) (the maps'
-// 64-byte swizzle). Where the epilogue reads matrices (SQUARE: E, APPLY: hi and lo), a
-// block's 16 bytes a lane, four lanes to a row, are asked for a chunk ahead into registers
-// and handed to the lanes of their rows through the same buffer. (Row by row from
-// registers, 32 rows to an instruction, the accesses alone outlasted the products; with the
-// blocks read by TMA a chunk waited 1 us for its own.)
+// A warp's way out: 32 x 32 blocks of the result by TMA, in two buffers of two blocks in
+// turn, each block's 64-byte rows in 16-byte pieces at piece ^ ((row / 2) % 4) (the maps'
+// 64-byte swizzle). Where the epilogue reads matrices (SQUARE: E, APPLY: hi and lo), their
+// blocks arrive in the same places by TMA, the first two before the products are done.
+// (Row by row from registers, 32 rows to an instruction, the accesses outlasted the
+// products; loads into registers a chunk ahead are waited for by the fence before the
+// stores: 2 us a chunk against 0.6.)
 template <int KIND>
 struct Blocks {
   static constexpr int kIn = KIND == GRAM ? 0 : KIND == SQUARE ? 1 : 2;
   const NsArgs& p;
-  uint8_t* staging;     // this warp's two blocks
-  int lane;
-  uint4 ahead[kIn > 0 ? kIn * 4 : 1];
-  // the chunk at (row0, col) of the stacked matrices
-  TW_DEV void ask(int row0, int col) {
-    const uint16_t* in[2] = {p.in0, p.in1};
-#pragma unroll
-    for (int m = 0; m < kIn; ++m)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        ahead[4 * m + q] = __ldcg(reinterpret_cast<const uint4*>(in[m] + static_cast<size_t>(row0 + 8 * q + (lane >> 2)) * p.np + col) + (lane & 3));
-  }
-  // the buffer is free for every lane, and holds what was asked for
-  TW_DEV void take() {
-    if (lane == 0) bulk_wait_read_all();
-    __syncwarp();
+  const Unit& u;
+  uint8_t* staging;     // this warp's 8 KB
+  uint64_t* bar;        // [2], each completed twice a tile: chunk c is phase c / 2 of its buffer's
+  int lane, base, i, j; // base: the matrix's first row in the maps; i, j: the tile
+  TW_DEV uint8_t* buffer(int c) const { return staging + (c & 1) * 2 * kChunkBytes; }
+  // lane 0: chunk c's blocks, from row and column of the matrix
+  TW_DEV void ask(int c, int row, int col) {
     if constexpr (kIn > 0) {
-#pragma unroll
-      for (int m = 0; m < kIn; ++m)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) *piece(staging + m * kChunkBytes, 8 * q + (lane >> 2), lane & 3) = ahead[4 * m + q];
-      __syncwarp();
+      uint8_t* b = buffer(c);
+      mbar_arrive_expect_tx(bar + (c & 1), kIn * kChunkBytes);
+      tma_load_2d(b, KIND == SQUARE ? &p.e_block : &p.x_block[u.step & 1], bar + (c & 1), col, base + row);
+      if (KIND == APPLY) tma_load_2d(b + kChunkBytes, &p.lo_block, bar + (c & 1), col, base + row);
     }
+  }
+  // chunk c's buffer, for every lane: free, or filled with what was asked for
+  TW_DEV bool here(int c, volatile int* abort_flag) {
+    if constexpr (kIn > 0) return __all_sync(0xFFFFFFFFu, mbar_wait(bar + (c & 1), (c >> 1) & 1u, abort_flag, p.status)) != 0;
+    // one group a chunk: with the latest one excepted, this buffer's stores have been read
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    __syncwarp();
+    return true;
   }
   TW_DEV uint4* piece(uint8_t* block, int row, int q) const {
     return reinterpret_cast<uint4*>(block + row * 64) + (q ^ ((row >> 1) & 3));
   }
-  // v: the products' sums of row `row` of the matrix (this lane's), columns [col, col + 32);
-  // base: the matrix's first row in the maps
-  TW_DEV void put(const Unit& u, int base, int row, int col, float (&v)[32]) {
-    uint8_t* b0 = staging;
+  // v: the products' sums of row `row` of the matrix (this lane's), columns [col, col + 32)
+  TW_DEV void put(int c, int row, int col, float (&v)[32]) {
+    uint8_t* b0 = buffer(c);
     uint8_t* b1 = b0 + kChunkBytes;
+    const float f0 = p.f0[u.step][KIND], f1 = p.f1[u.step][KIND];
     if constexpr (KIND == GRAM) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = v[i] * p.f0 - (row == col + i ? p.f1 : 0.f);
+      for (int k = 0; k < 32; ++k) v[k] = v[k] * f0 - (row == col + k ? f1 : 0.f);
     } else {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -228,14 +349,14 @@ struct Blocks {
         for (int k = 0; k < 4; ++k) {
           float2 x = half2_of(h[k]);
           if (KIND == APPLY) x = add2(x, half2_of(m[k]));
-          const int i = 8 * q + 2 * k;
-          v[i] = fmaf(v[i], p.f1, x.x * p.f0);
-          v[i + 1] = fmaf(v[i + 1], p.f1, x.y * p.f0);
+          const int at = 8 * q + 2 * k;
+          v[at] = fmaf(v[at], f1, x.x * f0);
+          v[at + 1] = fmaf(v[at + 1], f1, x.y * f0);
         }
       }
     }
     if constexpr (KIND == APPLY) {
-      if (p.last) {
+      if (u.step + 1 == p.steps) {
         __syncwarp();  // every lane has read its rows
         void* out = p.out[u.mat];
         if (p.otype == TW_F32) put_out<TW_F32>(p, out, row, col, v, b0);
@@ -246,38 +367,143 @@ struct Blocks {
     }
     uint32_t w[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = pack_f16x2_rn(v[2 * i], v[2 * i + 1]);
+    for (int k = 0; k < 16; ++k) w[k] = pack_f16x2_rn(v[2 * k], v[2 * k + 1]);
 #pragma unroll
     for (int q = 0; q < 4; ++q) *piece(b0, lane, q) = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-    const bool mirror = KIND != APPLY && u.i != u.j;
+    const bool mirror = KIND != APPLY && i != j;
     if constexpr (KIND == APPLY) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float2 h = half2_of(w[i]);
-        w[i] = pack_f16x2_rn(v[2 * i] - h.x, v[2 * i + 1] - h.y);
+      for (int k = 0; k < 16; ++k) {
+        const float2 h = half2_of(w[k]);
+        w[k] = pack_f16x2_rn(v[2 * k] - h.x, v[2 * k + 1] - h.y);
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) *piece(b1, lane, q) = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
     } else if (mirror) {  // the other side of the diagonal: columns as rows, 64 bytes a warp's store
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        reinterpret_cast<uint16_t*>(piece(b1, i, lane >> 3))[lane & 7] = static_cast<uint16_t>(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
+      for (int k = 0; k < 32; ++k)
+        reinterpret_cast<uint16_t*>(piece(b1, k, lane >> 3))[lane & 7] = static_cast<uint16_t>(k & 1 ? w[k / 2] >> 16 : w[k / 2]);
     }
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      tma_store_2d(&p.out0, b0, col, base + row);
-      if (KIND == APPLY) tma_store_2d(&p.out1, b1, col, base + row);
-      if (mirror) tma_store_2d(&p.out1, b1, row, base + col);
+      const CUtensorMap* to = KIND == GRAM ? &p.e_block : KIND == SQUARE ? &p.b_block : &p.x_block[(u.step & 1) ^ 1];
+      tma_store_2d(to, b0, col, base + row);
+      if (KIND == APPLY) tma_store_2d(&p.lo_block, b1, col, base + row);
+      if (mirror) tma_store_2d(to, b1, row, base + col);
       bulk_commit();
     }
   }
 };
 
+// One warp's 32 rows x 128 columns of a unit; false where a bounded wait ran out.
 template <int KIND>
-__global__ void __launch_bounds__(kThreads, 1) ns_gemm_kernel(const __grid_constant__ NsArgs p) {
-  constexpr bool kMN = KIND == GRAM;  // both operands stored [K, MN]
-  constexpr uint32_t kIdesc = idesc_bf16_f32(kTile, kTile, kMN, kMN, true);
+TW_DEV bool epilogue(const NsArgs& p, const Unit& u, uint8_t* staging, uint64_t* bar, uint64_t* tfull, uint32_t parity,
+                     uint32_t tmem, int rank, int ew, volatile int* abort_flag) {
+  const int lane = threadIdx.x & 31, quarter = (ew + 2) & 3, half = ew >> 2;
+  int ti, tj;
+  tile_at(p, u, ti, tj);
+  Blocks<KIND> blocks{p, u, staging, bar, lane, u.mat * (KIND == APPLY ? p.mp : p.np), ti, tj};
+  const int row = ti * kTile + rank * 128 + quarter * 32 + lane, col = tj * kTile + half * 128;
+  const int slices = p.slices[KIND];
+  int asked = 0, taken = 0;  // chunks
+  auto ask = [&] {
+    if (lane == 0) blocks.ask(asked, row, col + asked * 32);
+    ++asked;
+  };
+  auto drained = [&] {  // given up: no copy of this warp's may be under way when its CTA leaves
+    if (KIND != GRAM && lane == 0)
+      for (; taken < asked; ++taken) mbar_wait_drain(bar + (taken & 1), (taken >> 1) & 1u);
+    __syncwarp();
+    return false;
+  };
+  int ok = 1;
+  if (KIND != GRAM) {
+    if (lane == 0) ok = wait_inputs(p, u, abort_flag) ? 1 : 0;
+    if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) return false;
+    if (lane == 0) fence_proxy_async_all();
+    if (slices == 1) ask(), ask();  // while the products run (a slice may have nothing to finish)
+  }
+  if (lane == 0) ok = mbar_wait(tfull, parity, abort_flag, p.status) ? 1 : 0;
+  if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) return drained();
+  tc_fence_after_sync();
+  // this warp's block of a slice's sums, a column's 32 rows side by side
+  const size_t place = static_cast<size_t>(u.mat) * p.slots + static_cast<size_t>(u.tile) * slices;
+  auto slot = [&](int slice) { return p.part + ((place + slice) * 2 * kEpiWarps + rank * kEpiWarps + ew) * (128 * 32) + lane; };
+  int* arrived = p.arrived + (place * 2 + rank) * kEpiWarps + ew;
+  if (slices > 1) {
+    // the warp that finds all other slices' sums here adds them, in the slices' order
+    int seen = 0;
+    if (lane == 0) seen = ld_acquire(arrived);
+    seen = __shfl_sync(0xFFFFFFFFu, seen, 0);
+    if (seen != slices - 1) {
+      float* to = slot(u.slice);
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t v[32];
+        tmem_ld32(tmem + c * 32, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 32; ++k) __stcg(to + (c * 32 + k) * 32, __uint_as_float(v[k]));
+      }
+      __threadfence();
+      __syncwarp();
+      if (lane == 0) seen = atomicAdd(arrived, 1);
+      seen = __shfl_sync(0xFFFFFFFFu, seen, 0);
+    }
+    __threadfence();
+    if (seen != slices - 1) return true;
+    if (KIND != GRAM) ask(), ask();
+  }
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t w[32];
+    float v[32];
+    tmem_ld32(tmem + c * 32, w);
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(w[k]);
+    if (slices > 1) {
+      float s[32];
+#pragma unroll
+      for (int k = 0; k < 32; ++k) s[k] = 0.f;
+      for (int q = 0; q < slices; ++q) {
+        const float* from = slot(q) + c * 32 * 32;
+        if (q == u.slice) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) s[k] += v[k];
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) s[k] += __ldcg(from + k * 32);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 32; ++k) v[k] = s[k];
+    }
+    if (!blocks.here(c, abort_flag)) return drained();
+    taken = c + 1;
+    blocks.put(c, row, col + c * 32, v);
+    if (KIND != GRAM && c < 2) {
+      if (lane == 0) bulk_wait_read_all();
+      ask();
+    }
+  }
+  // the tile's writes are there for whoever is told so; the next step reads them
+  if (lane == 0) {
+    if (slices > 1) *arrived = 0;
+    bulk_wait_all();
+    fence_proxy_async_all();
+    __threadfence();
+    asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(p.done + u.mat * 3 + KIND) : "memory");
+  }
+  __syncwarp();
+  return true;
+}
+
+// All steps' products in one launch. Warp 0: TMA producer; warp 1: MMA issuer (rank 0 of the
+// pair, for both CTAs); warps 2 to 9: epilogues, while the next unit's MMAs fill the other
+// TMEM buffer; warp 10: draws the pair's units (rank 0).
+__global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__ NsArgs p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
   uint8_t* tiles = smem_raw + pad;
@@ -286,10 +512,12 @@ __global__ void __launch_bounds__(kThreads, 1) ns_gemm_kernel(const __grid_const
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;
   uint64_t* tempty = tfull + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+  uint64_t* block_bars = tempty + 2;  // [kEpiWarps][2]
+  UnitRing* ring = reinterpret_cast<UnitRing*>(block_bars + 2 * kEpiWarps);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ring + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
+  const int rank = static_cast<int>(cluster_rank());
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -300,12 +528,13 @@ __global__ void __launch_bounds__(kThreads, 1) ns_gemm_kernel(const __grid_const
       mbar_init(tfull + b, 1);
       mbar_init(tempty + b, 2 * kEpiWarps);
     }
+    for (int b = 0; b < 2 * kEpiWarps; ++b) mbar_init(block_bars + b, 1);
+    for (int b = 0; b < kRing; ++b) {
+      mbar_init(ring->full + b, 1);
+      mbar_init(ring->empty + b, kTakers);
+    }
     *abort_flag = 0;
     fence_barrier_init();
-  }
-  if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&p.a);
-    tma_prefetch_desc(&p.b);
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, 512);
@@ -318,20 +547,26 @@ __global__ void __launch_bounds__(kThreads, 1) ns_gemm_kernel(const __grid_const
   const uint32_t tmem_base = *tmem_slot;
   pdl_enter();
 
-  const int per_mat = KIND == APPLY ? p.tiles_m * p.tiles_n : p.tiles_n * (p.tiles_n + 1) / 2;
-  const int units = p.whole + (p.tiles - p.whole) * p.ksplit;
-  const int pairs = gridDim.x >> 1, first = blockIdx.x >> 1;
-
+  Taker units{ring, abort_flag, p.status};
+  Unit u;
   if (warp == 0) {
     if (lane == 0) {  // TMA producer
       int stage = 0;
       uint32_t phase = 0;
       long issued = 0;
       bool ok = true;
-      for (int n = first; ok && n < units; n += pairs) {
-        const Unit u = unit_of<KIND>(p, n, per_mat);
-        const int m0 = u.i * kTile + static_cast<int>(rank) * 128, n0 = u.j * kTile + static_cast<int>(rank) * 128;
-        for (int kb = u.kb_lo; kb < u.kb_hi; ++kb) {
+      while (ok && units.take(u, true)) {
+        int i, j, lo, hi;
+        tile_at(p, u, i, j);
+        k_blocks(p, u, lo, hi);
+        if (!wait_inputs(p, u, abort_flag)) {
+          ok = false;
+          break;
+        }
+        fence_proxy_async_all();
+        const int m0 = i * kTile + rank * 128, n0 = j * kTile + rank * 128, x = u.step & 1;
+        const int xrow = u.mat * p.mp, srow = u.mat * p.np;
+        for (int kb = lo; kb < hi; ++kb) {
           if (!mbar_wait(empty + stage, phase ^ 1u, abort_flag, p.status)) {
             ok = false;
             break;
@@ -341,23 +576,26 @@ __global__ void __launch_bounds__(kThreads, 1) ns_gemm_kernel(const __grid_const
           if (rank == 0) mbar_arrive_expect_tx(full + stage, 2 * kStageBytes);
           const uint32_t bar = peer_smem_addr(full + stage, 0);
           const int k0 = kb * kBK;
-          if (kMN) {
-            const int row = u.mat * p.rows_a + k0;
-            tma_load_2d_pair(sa, &p.a, bar, m0, row);
-            tma_load_2d_pair(sa + 8192, &p.a, bar, m0 + 64, row);
-            tma_load_2d_pair(sb, &p.b, bar, n0, row);
-            tma_load_2d_pair(sb + 8192, &p.b, bar, n0 + 64, row);
+          if (u.kind == GRAM) {  // both operands stored [K, MN]
+            tma_load_2d_pair(sa, &p.x_mn[x], bar, m0, xrow + k0);
+            tma_load_2d_pair(sa + 8192, &p.x_mn[x], bar, m0 + 64, xrow + k0);
+            tma_load_2d_pair(sb, &p.x_mn[x], bar, n0, xrow + k0);
+            tma_load_2d_pair(sb + 8192, &p.x_mn[x], bar, n0 + 64, xrow + k0);
+          } else if (u.kind == SQUARE) {
+            tma_load_2d_pair(sa, &p.e_k, bar, k0, srow + m0);
+            tma_load_2d_pair(sb, &p.e_k, bar, k0, srow + n0);
           } else {
-            tma_load_2d_pair(sa, &p.a, bar, k0, u.mat * p.rows_a + m0);
-            tma_load_2d_pair(sb, &p.b, bar, k0, u.mat * p.rows_b + n0);
+            tma_load_2d_pair(sa, &p.x_k[x], bar, k0, xrow + m0);
+            tma_load_2d_pair(sb, &p.b_k, bar, k0, srow + n0);
           }
           ++issued;
           if (++stage == kStages) stage = 0, phase ^= 1u;
         }
       }
-      if (!ok && rank == 0) {
-        for (long i = 0; i < kStages && i < issued; ++i) {
-          const long q = issued - 1 - i;
+      if (*abort_flag && rank == 0) {
+        // let the loads already issued land (rank 1's complete on rank 0's barriers)
+        for (long n = 0; n < kStages && n < issued; ++n) {
+          const long q = issued - 1 - n;
           mbar_wait_drain(full + (q % kStages), static_cast<uint32_t>((q / kStages) & 1));
         }
       }
@@ -367,8 +605,9 @@ __global__ void __launch_bounds__(kThreads, 1) ns_gemm_kernel(const __grid_const
       int stage = 0, local = 0;
       uint32_t phase = 0;
       bool ok = true, issued_any = false;
-      for (int n = first; ok && n < units; n += pairs, ++local) {
-        const Unit u = unit_of<KIND>(p, n, per_mat);
+      for (; ok && units.take(u, true); ++local) {
+        int lo, hi;
+        k_blocks(p, u, lo, hi);
         const int buf = local & 1;
         if (!mbar_wait(tempty + buf, ((local >> 1) & 1u) ^ 1u, abort_flag, p.status)) {
           ok = false;
@@ -376,19 +615,20 @@ __global__ void __launch_bounds__(kThreads, 1) ns_gemm_kernel(const __grid_const
         }
         tc_fence_after_sync();
         const uint32_t d0 = tmem_base + static_cast<uint32_t>(buf * kTile);
-        for (int kb = u.kb_lo; kb < u.kb_hi; ++kb) {
+        const bool mn = u.kind == GRAM;
+        const uint32_t idesc = mn ? idesc_bf16_f32(kTile, kTile, true, true, true) : idesc_bf16_f32(kTile, kTile, false, false, true);
+        for (int kb = lo; kb < hi; ++kb) {
           if (!mbar_wait(full + stage, phase, abort_flag, p.status)) {
             ok = false;
             break;
           }
           tc_fence_after_sync();
           const uint32_t sa = smem_addr(tiles + stage * kStageBytes), sb = sa + kOperandBytes;
+          const uint32_t step = mn ? 2048 : 32, lbo = mn ? 8192 : 16;
 #pragma unroll
-          for (int k16 = 0; k16 < kBK / 16; ++k16) {
-            const uint64_t ad = kMN ? smem_desc_sw128(sa + k16 * 2048, 8192, 1024) : smem_desc_sw128(sa + k16 * 32, 16, 1024);
-            const uint64_t bd = kMN ? smem_desc_sw128(sb + k16 * 2048, 8192, 1024) : smem_desc_sw128(sb + k16 * 32, 16, 1024);
-            tc_mma_bf16_pair(d0, ad, bd, kIdesc, kb > u.kb_lo || k16 > 0 ? 1u : 0u);
-          }
+          for (int k16 = 0; k16 < kBK / 16; ++k16)
+            tc_mma_bf16_pair(d0, smem_desc_sw128(sa + k16 * step, lbo, 1024), smem_desc_sw128(sb + k16 * step, lbo, 1024), idesc,
+                             kb > lo || k16 > 0 ? 1u : 0u);
           issued_any = true;
           tc_commit_pair(empty + stage);
           if (++stage == kStages) stage = 0, phase ^= 1u;
@@ -396,95 +636,44 @@ __global__ void __launch_bounds__(kThreads, 1) ns_gemm_kernel(const __grid_const
         if (!ok) break;
         tc_commit_pair(tfull + buf);
       }
-      if (!ok && issued_any) {
+      if (*abort_flag && issued_any) {
         tc_commit_pair(empty + stage);
         mbar_wait_drain(empty + stage, phase);
       }
     }
-  } else {
+  } else if (warp < 2 + kEpiWarps) {
     const int ew = warp - 2, quarter = warp & 3, half = ew >> 2;
-    Blocks<KIND> blocks{p, staging + ew * 2 * kChunkBytes, lane};
-    int local = 0;
-    for (int n = first; n < units; n += pairs, ++local) {
-      const Unit u = unit_of<KIND>(p, n, per_mat);
+    bool ok = true;
+    for (int local = 0; ok && units.take(u, false); ++local) {
       const int buf = local & 1;
-      const int base = u.mat * (KIND == APPLY ? p.mp : p.np);
-      const int row = u.i * kTile + static_cast<int>(rank) * 128 + quarter * 32 + lane, col = u.j * kTile + half * 128;
-      const bool split = u.split >= 0;
-      // while the products run (a slice may have nothing to finish: its blocks come later)
-      if (!split) blocks.ask(base + row - lane, col);
-      int done = 0;
-      if (lane == 0) done = mbar_wait(tfull + buf, (local >> 1) & 1u, abort_flag, p.status) ? 1 : 0;
-      if (!__shfl_sync(0xFFFFFFFFu, done, 0)) break;
-      tc_fence_after_sync();
       const uint32_t t0 = tmem_base + static_cast<uint32_t>(buf * kTile + half * 128) + (static_cast<uint32_t>(quarter * 32) << 16);
-      bool finish = true;
-      // this warp's block of a slice's sums, a column's 32 rows side by side
-      auto slot = [&](int slice) {
-        return p.part + ((static_cast<size_t>(u.split) * p.ksplit + slice) * 2 * kEpiWarps + rank * kEpiWarps + ew) * (128 * 32) + lane;
-      };
-      int* arrived = p.arrived + (static_cast<size_t>(u.split) * 2 + rank) * kEpiWarps + ew;
-      if (split) {
-        // the warp that finds all other slices' sums here adds them, in the slices' order
-        int seen = 0;
-        if (lane == 0) seen = *static_cast<volatile int*>(arrived);
-        seen = __shfl_sync(0xFFFFFFFFu, seen, 0);
-        if (seen != p.ksplit - 1) {
-          float* to = slot(u.slice);
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[32];
-            tmem_ld32(t0 + c * 32, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) __stcg(to + (c * 32 + i) * 32, __uint_as_float(v[i]));
-          }
-          __threadfence();
-          __syncwarp();
-          if (lane == 0) seen = atomicAdd(arrived, 1);
-          seen = __shfl_sync(0xFFFFFFFFu, seen, 0);
-        }
-        finish = seen == p.ksplit - 1;
-        __threadfence();
-        if (finish) blocks.ask(base + row - lane, col);
-      }
-      if (finish) {
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t w[32];
-          float v[32];
-          tmem_ld32(t0 + c * 32, w);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(w[i]);
-          if (split) {
-            float s[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) s[i] = 0.f;
-            for (int q = 0; q < p.ksplit; ++q) {
-              const float* from = slot(q) + c * 32 * 32;
-              if (q == u.slice) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) s[i] += v[i];
-              } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) s[i] += __ldcg(from + i * 32);
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = s[i];
-          }
-          blocks.take();
-          if (c + 1 < 4) blocks.ask(base + row - lane, col + (c + 1) * 32);
-          blocks.put(u, base, row, col + c * 32, v);
-        }
-        if (split && lane == 0) *arrived = 0;
-      }
+      uint8_t* st = staging + ew * 4 * kChunkBytes;
+      uint64_t* bar = block_bars + 2 * ew;
+      const uint32_t parity = (local >> 1) & 1u;
+      if (u.kind == GRAM) ok = epilogue<GRAM>(p, u, st, bar, tfull + buf, parity, t0, rank, ew, abort_flag);
+      else if (u.kind == SQUARE) ok = epilogue<SQUARE>(p, u, st, bar, tfull + buf, parity, t0, rank, ew, abort_flag);
+      else ok = epilogue<APPLY>(p, u, st, bar, tfull + buf, parity, t0, rank, ew, abort_flag);
+      if (!ok) break;
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(peer_smem_addr(tempty + buf, 0));
     }
     if (lane == 0) bulk_wait_all();
+  } else if (rank == 0 && lane == 0) {
+    // every unit drawn is given to both CTAs, the end too
+    for (int n = 0;; ++n) {
+      const int slot = n & (kRing - 1);
+      if (!mbar_wait_cluster(ring->empty + slot, ((n / kRing) & 1u) ^ 1u, abort_flag, p.status)) break;
+      uint2 w = make_uint2(~0u, 0u);
+      const bool more = unit_at(p, atomicAdd(p.next, 1), u);
+      if (more) w = make_uint2(static_cast<uint32_t>(u.step << 24 | u.kind << 16 | u.mat << 8 | u.slice), static_cast<uint32_t>(u.tile));
+#pragma unroll
+      for (uint32_t r = 0; r < 2; ++r) {
+        asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(peer_smem_addr(ring->unit + slot, r)), "r"(w.x), "r"(w.y) : "memory");
+        mbar_arrive_cluster(peer_smem_addr(ring->full + slot, r));
+      }
+      if (!more) break;
+    }
   }
   __syncthreads();
   cluster_sync();
@@ -699,18 +888,35 @@ __global__ void __launch_bounds__(256) ns_start_wide_kernel(const NsInArgs a, in
 // ------------------------------------------------------------------ host
 int up(int n) { return (n + kTile - 1) / kTile * kTile; }
 
-// The most units that run slices of tiles: two for each pair of SMs, or 8 for each tile.
-constexpr int kMostSlices = 152;
+// Slices of a tile's K loop, where a matrix's tiles are fewer than the pairs of SMs (76 on
+// this GPU; a constant, so that the workspace does not depend on the device). In K blocks of
+// 0.33 us: handing a slice's sums on and adding them takes about 15.
+constexpr int kPairs = 76, kMostSlices = 8;
+int slices_of(int tiles, int kb) {
+  int best = 1, cost = kb;
+  for (int s = 2; s <= kMostSlices && s * tiles <= kPairs; ++s) {
+    const int chunk = (kb + s - 1) / s;
+    if ((kb + chunk - 1) / chunk != s) continue;  // no empty slice
+    if (chunk + 15 + 2 * s < cost) best = s, cost = chunk + 15 + 2 * s;
+  }
+  return best;
+}
 
 struct Layout {
-  int mp, np, tri, full, slices;
-  size_t hi0, hi1, lo, e, b, part, arrived, norms, bytes;
+  int mp, np, slices[3], slots;
+  size_t hi0, hi1, lo, e, b, part, arrived, counters, norms, bytes;
+  int words() const { return static_cast<int>((norms - arrived) / 4); }  // arrived and the counters after it
 };
 Layout layout(int m, int n, int count) {
   Layout l{};
   l.mp = up(std::max(m, n)), l.np = up(std::min(m, n));
-  const int t = l.np / kTile;
-  l.tri = t * (t + 1) / 2 * count, l.full = l.mp / kTile * t * count;
+  const int t = l.np / kTile, tri = t * (t + 1) / 2, all = l.mp / kTile * t;
+  l.slices[GRAM] = slices_of(tri * count, l.mp / kBK);
+  l.slices[SQUARE] = slices_of(tri * count, l.np / kBK);
+  l.slices[APPLY] = slices_of(all * count, l.np / kBK);
+  const int tiles[3] = {tri, tri, all};
+  for (int k = 0; k < 3; ++k)
+    if (l.slices[k] > 1) l.slots = std::max(l.slots, tiles[k] * l.slices[k]);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t was = at;
@@ -719,45 +925,12 @@ Layout layout(int m, int n, int count) {
   };
   const size_t x = static_cast<size_t>(count) * l.mp * l.np * 2, s = static_cast<size_t>(count) * l.np * l.np * 2;
   l.hi0 = take(x), l.hi1 = take(x), l.lo = take(x), l.e = take(s), l.b = take(s);
-  l.slices = std::min(kMostSlices, 8 * std::max(l.tri, l.full));
-  l.part = take(static_cast<size_t>(l.slices) * kTile * kTile * 4);
-  l.arrived = take(static_cast<size_t>(l.slices) * 2 * kEpiWarps * 4);
+  l.part = take(static_cast<size_t>(count) * l.slots * kTile * kTile * 4);
+  l.arrived = take(static_cast<size_t>(count) * l.slots * 2 * kEpiWarps * 4);
+  l.counters = take(static_cast<size_t>(3 * count + 1) * 4);
   l.norms = take(static_cast<size_t>(count) * kNormBlocks * 3 * 4);
   l.bytes = at;
   return l;
-}
-
-// Which of a product's tiles run whole, in full rounds over the pairs, and in how many
-// slices of K the others do. Costs in K blocks (0.33 us): a unit's fill and drain that the
-// next one does not hide, and what the last slice of a tile reads of the others.
-void split_tiles(NsArgs& p, int pairs, int most) {
-  p.whole = p.tiles, p.ksplit = 1;
-  const int rounds = p.tiles / pairs;
-  long best = static_cast<long>((p.tiles + pairs - 1) / pairs) * (p.kb_total + 1);
-  for (int w = rounds; w >= std::max(0, rounds - 1); --w)
-    for (int s = 2; s <= std::min(p.kb_total, 8); ++s) {
-      const int rest = p.tiles - w * pairs, chunk = (p.kb_total + s - 1) / s;
-      if (rest == 0 || rest * s > most || (p.kb_total + chunk - 1) / chunk != s) continue;  // no empty slice
-      const long cost = static_cast<long>(w) * (p.kb_total + 1) + static_cast<long>((rest * s + pairs - 1) / pairs) * (chunk + 4) + 4 + 2 * s;
-      if (cost < best) best = cost, p.whole = w * pairs, p.ksplit = s;
-    }
-}
-
-template <int KIND>
-cudaError_t run_gemm(NsArgs& p, int most_slices, cudaStream_t s, const char* label) {
-  auto kern = ns_gemm_kernel<KIND>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess) return e;
-  static int resident = -1;  // the query depends only on the kernel
-  if (resident < 0) resident = max_active_clusters(kern, kThreads, kSmem, 2);
-  const int most = std::min(resident, device_sm_count() / 2);
-  if (most < 1) return cudaErrorInvalidConfiguration;
-  p.tiles = (KIND == APPLY ? p.tiles_m * p.tiles_n : p.tiles_n * (p.tiles_n + 1) / 2) * p.count;
-  split_tiles(p, most, most_slices);
-  const int units = p.whole + (p.tiles - p.whole) * p.ksplit;
-  e = launch_clustered(kern, dim3(2 * std::min(units, most)), dim3(kThreads), kSmem, 2, s, p);
-  trace_mark(s, label);
-  return e;
 }
 
 template <int GT>
@@ -806,7 +979,7 @@ cudaError_t launch_ortho(const OrthoArgs& o, cudaStream_t s) {
   in.ldg = o.ldg, in.ldm = o.ldbuf, in.gtype = o.gtype, in.count = o.count, in.rows = o.m, in.cols = o.n;
   in.mu = o.mu, in.nesterov = o.nesterov, in.vec = vec;
   in.norms = reinterpret_cast<float*>(ws + l.norms);
-  in.arrived = reinterpret_cast<int*>(ws + l.arrived), in.n_arrived = l.slices * 2 * kEpiWarps;
+  in.arrived = reinterpret_cast<int*>(ws + l.arrived), in.n_arrived = l.words();
   in.hi = at16(l.hi0), in.lo = at16(l.lo), in.mp = l.mp, in.np = l.np, in.klog2 = k;
   cudaError_t e = o.gtype == TW_F32    ? way_in<TW_F32>(in, wide, s)
                   : o.gtype == TW_BF16 ? way_in<TW_BF16>(in, wide, s)
@@ -814,52 +987,48 @@ cudaError_t launch_ortho(const OrthoArgs& o, cudaStream_t s) {
   if (e != cudaSuccess) return e;
 
   // maps: operands in boxes of 64 x 128 (K-major) and 64 x 64 (MN-major), the epilogues' 32 x 32
+  NsArgs p = {};
   const uint64_t np2 = static_cast<uint64_t>(l.np) * 2;
   const uint64_t xrows = static_cast<uint64_t>(l.mp) * o.count, srows = static_cast<uint64_t>(l.np) * o.count;
-  CUtensorMap x_k[2], x_mn[2], x_block[2], lo_block, e_k, b_k, e_block, b_block;
   bool ok = true;
   auto map = [&](CUtensorMap& m, size_t at, uint64_t rows, uint32_t box_cols, uint32_t box_rows) {
     ok = ok && make_tmap_bf16(&m, ws + at, l.np, rows, np2, box_cols, box_rows, box_cols == 32);
   };
   for (int i = 0; i < 2; ++i) {
     const size_t x = i ? l.hi1 : l.hi0;
-    map(x_k[i], x, xrows, 64, 128), map(x_mn[i], x, xrows, 64, 64), map(x_block[i], x, xrows, 32, 32);
+    map(p.x_k[i], x, xrows, 64, 128), map(p.x_mn[i], x, xrows, 64, 64), map(p.x_block[i], x, xrows, 32, 32);
   }
-  map(lo_block, l.lo, xrows, 32, 32);
-  map(e_k, l.e, srows, 64, 128), map(b_k, l.b, srows, 64, 128), map(e_block, l.e, srows, 32, 32), map(b_block, l.b, srows, 32, 32);
+  map(p.lo_block, l.lo, xrows, 32, 32), map(p.e_block, l.e, srows, 32, 32), map(p.b_block, l.b, srows, 32, 32);
+  map(p.e_k, l.e, srows, 64, 128), map(p.b_k, l.b, srows, 64, 128);
   if (!ok) return cudaErrorInvalidValue;
 
-  NsArgs p = {};
-  p.tiles_m = l.mp / kTile, p.tiles_n = l.np / kTile, p.count = o.count, p.np = l.np, p.mp = l.mp;
-  p.part = reinterpret_cast<float*>(ws + l.part), p.arrived = in.arrived, p.status = o.status;
+  p.tiles_m = l.mp / kTile, p.tiles_n = l.np / kTile, p.count = o.count, p.steps = o.steps, p.np = l.np, p.mp = l.mp;
+  for (int i = 0; i < 3; ++i) p.slices[i] = l.slices[i];
+  p.slots = l.slots, p.part = reinterpret_cast<float*>(ws + l.part), p.arrived = in.arrived;
+  p.done = reinterpret_cast<int*>(ws + l.counters), p.next = p.done + 3 * o.count, p.status = o.status;
   for (int i = 0; i < o.count; ++i) p.out[i] = o.out[i];
   p.ldo = o.ldo, p.rows = std::max(o.m, o.n), p.cols = std::min(o.m, o.n), p.otype = o.otype, p.transposed = wide;
   p.scale = static_cast<float>(std::ldexp(static_cast<double>(o.scale), -k)), p.beta = o.beta;
   for (int step = 0; step < o.steps; ++step) {
     const double a = o.coef[3 * step], b = o.coef[3 * step + 1], c = o.coef[3 * step + 2];
     const double t = step >= 3 ? 1.0 : 0.0, q0 = a + b * t + c * t * t, q1 = b + 2.0 * c * t;
-    const int at = step & 1;
-    p.a = p.b = x_mn[at], p.out0 = p.out1 = e_block;
-    p.rows_a = p.rows_b = l.mp, p.kb_total = l.mp / kBK;
-    p.f0 = std::ldexp(1.f, kGramLog2 - 2 * k), p.f1 = static_cast<float>(std::ldexp(t, kGramLog2));
-    e = run_gemm<GRAM>(p, l.slices, s, "ortho_gram");
-    if (e != cudaSuccess) return e;
-
-    p.a = p.b = e_k, p.in0 = at16(l.e), p.out0 = p.out1 = b_block;
-    p.rows_a = p.rows_b = l.np, p.kb_total = l.np / kBK;
-    p.f0 = static_cast<float>(std::ldexp(q1, kPolyLog2 - kGramLog2));
-    p.f1 = static_cast<float>(std::ldexp(c, kPolyLog2 - 2 * kGramLog2));
-    e = run_gemm<SQUARE>(p, l.slices, s, "ortho_square");
-    if (e != cudaSuccess) return e;
-
-    p.a = x_k[at], p.b = b_k, p.in0 = at16(at ? l.hi1 : l.hi0), p.in1 = at16(l.lo), p.out0 = x_block[at ^ 1], p.out1 = lo_block;
-    p.rows_a = l.mp;
-    p.last = step + 1 == o.steps;
-    p.f0 = static_cast<float>(q0), p.f1 = std::ldexp(1.f, -kPolyLog2);
-    e = run_gemm<APPLY>(p, l.slices, s, "ortho_apply");
-    if (e != cudaSuccess) return e;
+    p.f0[step][GRAM] = std::ldexp(1.f, kGramLog2 - 2 * k), p.f1[step][GRAM] = static_cast<float>(std::ldexp(t, kGramLog2));
+    p.f0[step][SQUARE] = static_cast<float>(std::ldexp(q1, kPolyLog2 - kGramLog2));
+    p.f1[step][SQUARE] = static_cast<float>(std::ldexp(c, kPolyLog2 - 2 * kGramLog2));
+    p.f0[step][APPLY] = static_cast<float>(q0), p.f1[step][APPLY] = std::ldexp(1.f, -kPolyLog2);
   }
-  return cudaSuccess;
+  e = cudaFuncSetAttribute(ns_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  static int resident = -1;  // the query depends only on the kernel
+  if (resident < 0) resident = max_active_clusters(ns_kernel, kThreads, kSmem, 2);
+  // no more pairs than a product of all matrices has units
+  const long tri = static_cast<long>(p.tiles_n) * (p.tiles_n + 1) / 2, all = static_cast<long>(p.tiles_m) * p.tiles_n;
+  const long most = o.count * std::max({tri * l.slices[GRAM], tri * l.slices[SQUARE], all * l.slices[APPLY]});
+  const int pairs = static_cast<int>(std::min<long>(most, std::min(resident, device_sm_count() / 2)));
+  if (pairs < 1) return cudaErrorInvalidConfiguration;
+  e = launch_clustered(ns_kernel, dim3(2 * pairs), dim3(kThreads), kSmem, 2, s, p);
+  trace_mark(s, "ortho_products");
+  return e;
 }
 
 }  // namespace tw

@@ -154,9 +154,21 @@ TW_DEV int ld_acquire(const int* p) {
   asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
+// Orders what was written through the generic or async proxy and acquired here before this
+// thread's later accesses through either.
+TW_DEV void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+// What a thread knows to be written: for each kind, 8 bits a matrix, the last step + 1 whose
+// inputs it has waited for.
+struct Known {
+  uint64_t steps[3] = {0, 0, 0};
+};
 // Waits (one thread, bounded) until all that unit u reads has been written: the apply of the
 // step before for a gram, the gram for a square, the square for an apply, of its matrix.
-TW_DEV bool wait_inputs(const NsArgs& p, const Unit& u, volatile int* abort_flag) {
+TW_DEV bool wait_inputs(const NsArgs& p, const Unit& u, Known& known, volatile int* abort_flag) {
+  const uint64_t steps = u.kind == GRAM ? known.steps[GRAM] : u.kind == SQUARE ? known.steps[SQUARE] : known.steps[APPLY];
+  const int at = 8 * u.mat;
+  if (static_cast<int>(steps >> at & 255) == u.step + 1) return true;
   const int tri = p.tiles_n * (p.tiles_n + 1) / 2, all = p.tiles_m * p.tiles_n;
   const int of = u.kind == GRAM ? APPLY : u.kind == SQUARE ? GRAM : SQUARE;
   const int need = (u.kind == GRAM ? u.step * all : (u.step + 1) * tri) * 2 * kEpiWarps;
@@ -173,11 +185,13 @@ TW_DEV bool wait_inputs(const NsArgs& p, const Unit& u, volatile int* abort_flag
       }
     }
   }
+  fence_proxy_async_all();
+  const uint64_t now = (steps & ~(255ull << at)) | static_cast<uint64_t>(u.step + 1) << at;
+  if (u.kind == GRAM) known.steps[GRAM] = now;
+  else if (u.kind == SQUARE) known.steps[SQUARE] = now;
+  else known.steps[APPLY] = now;
   return true;
 }
-// Orders what was written through the generic or async proxy and acquired here before this
-// thread's later accesses through either.
-TW_DEV void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 // A wait whose phase the other CTA of the pair completes, with data it wrote before.
 TW_DEV bool mbar_try_wait_cluster(uint32_t addr, uint32_t parity) {
@@ -211,10 +225,12 @@ TW_DEV bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abor
 // The units of a pair: one thread of rank 0 draws them and puts each into a ring in both
 // CTAs' shared memory; every role of both CTAs takes them from there in turn.
 constexpr int kRing = 4;
+constexpr int kDrawAhead = 8;  // K blocks before the end of a unit's loads
 constexpr int kTakers = (2 + kEpiWarps) + (1 + kEpiWarps);  // rank 0's producer, issuer and warps; rank 1's
 struct UnitRing {
   uint64_t full[kRing];    // one arrival
   uint64_t empty[kRing];   // rank 0's: kTakers arrivals
+  uint64_t draw;           // rank 0's: its producer is near the end of a unit's loads
   uint2 unit[kRing];       // step | kind | mat | slice (8 bits each), tile; ~0: no more
 };
 struct Taker {
@@ -362,6 +378,7 @@ struct Blocks {
         if (p.otype == TW_F32) put_out<TW_F32>(p, out, row, col, v, b0);
         else if (p.otype == TW_BF16) put_out<TW_BF16>(p, out, row, col, v, b0);
         else put_out<TW_F16>(p, out, row, col, v, b0);
+        if (lane == 0) bulk_commit();  // a group a chunk
         return;
       }
     }
@@ -399,7 +416,7 @@ struct Blocks {
 // One warp's 32 rows x 128 columns of a unit; false where a bounded wait ran out.
 template <int KIND>
 TW_DEV bool epilogue(const NsArgs& p, const Unit& u, uint8_t* staging, uint64_t* bar, uint64_t* tfull, uint32_t parity,
-                     uint32_t tmem, int rank, int ew, volatile int* abort_flag) {
+                     uint32_t tmem, int rank, int ew, Known& known, volatile int* abort_flag) {
   const int lane = threadIdx.x & 31, quarter = (ew + 2) & 3, half = ew >> 2;
   int ti, tj;
   tile_at(p, u, ti, tj);
@@ -419,9 +436,8 @@ TW_DEV bool epilogue(const NsArgs& p, const Unit& u, uint8_t* staging, uint64_t*
   };
   int ok = 1;
   if (KIND != GRAM) {
-    if (lane == 0) ok = wait_inputs(p, u, abort_flag) ? 1 : 0;
+    if (lane == 0) ok = wait_inputs(p, u, known, abort_flag) ? 1 : 0;
     if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) return false;
-    if (lane == 0) fence_proxy_async_all();
     if (slices == 1) ask(), ask();  // while the products run (a slice may have nothing to finish)
   }
   if (lane == 0) ok = mbar_wait(tfull, parity, abort_flag, p.status) ? 1 : 0;
@@ -483,8 +499,8 @@ TW_DEV bool epilogue(const NsArgs& p, const Unit& u, uint8_t* staging, uint64_t*
     if (!blocks.here(c, abort_flag)) return drained();
     taken = c + 1;
     blocks.put(c, row, col + c * 32, v);
-    if (KIND != GRAM && c < 2) {
-      if (lane == 0) bulk_wait_read_all();
+    if (KIND != GRAM && (c == 1 || c == 2)) {  // the buffer of the chunk before: its stores have been read by now
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
       ask();
     }
   }
@@ -492,8 +508,6 @@ TW_DEV bool epilogue(const NsArgs& p, const Unit& u, uint8_t* staging, uint64_t*
   if (lane == 0) {
     if (slices > 1) *arrived = 0;
     bulk_wait_all();
-    fence_proxy_async_all();
-    __threadfence();
     asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(p.done + u.mat * 3 + KIND) : "memory");
   }
   __syncwarp();
@@ -533,6 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
       mbar_init(ring->full + b, 1);
       mbar_init(ring->empty + b, kTakers);
     }
+    mbar_init(&ring->draw, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -548,6 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
   pdl_enter();
 
   Taker units{ring, abort_flag, p.status};
+  Known known;
   Unit u;
   if (warp == 0) {
     if (lane == 0) {  // TMA producer
@@ -559,14 +575,15 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
         int i, j, lo, hi;
         tile_at(p, u, i, j);
         k_blocks(p, u, lo, hi);
-        if (!wait_inputs(p, u, abort_flag)) {
+        if (!wait_inputs(p, u, known, abort_flag)) {
           ok = false;
           break;
         }
-        fence_proxy_async_all();
         const int m0 = i * kTile + rank * 128, n0 = j * kTile + rank * 128, x = u.step & 1;
         const int xrow = u.mat * p.mp, srow = u.mat * p.np;
+        const int draw_at = max(lo, hi - kDrawAhead);
         for (int kb = lo; kb < hi; ++kb) {
+          if (rank == 0 && kb == draw_at) mbar_arrive(&ring->draw);
           if (!mbar_wait(empty + stage, phase ^ 1u, abort_flag, p.status)) {
             ok = false;
             break;
@@ -650,9 +667,9 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
       uint8_t* st = staging + ew * 4 * kChunkBytes;
       uint64_t* bar = block_bars + 2 * ew;
       const uint32_t parity = (local >> 1) & 1u;
-      if (u.kind == GRAM) ok = epilogue<GRAM>(p, u, st, bar, tfull + buf, parity, t0, rank, ew, abort_flag);
-      else if (u.kind == SQUARE) ok = epilogue<SQUARE>(p, u, st, bar, tfull + buf, parity, t0, rank, ew, abort_flag);
-      else ok = epilogue<APPLY>(p, u, st, bar, tfull + buf, parity, t0, rank, ew, abort_flag);
+      if (u.kind == GRAM) ok = epilogue<GRAM>(p, u, st, bar, tfull + buf, parity, t0, rank, ew, known, abort_flag);
+      else if (u.kind == SQUARE) ok = epilogue<SQUARE>(p, u, st, bar, tfull + buf, parity, t0, rank, ew, known, abort_flag);
+      else ok = epilogue<APPLY>(p, u, st, bar, tfull + buf, parity, t0, rank, ew, known, abort_flag);
       if (!ok) break;
       tc_fence_before_sync();
       __syncwarp();
@@ -660,8 +677,10 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
     }
     if (lane == 0) bulk_wait_all();
   } else if (rank == 0 && lane == 0) {
-    // every unit drawn is given to both CTAs, the end too
+    // every unit drawn is given to both CTAs, the end too; one ahead of the loads, no more: a
+    // unit held by a pair that is busy keeps those that wait for it waiting
     for (int n = 0;; ++n) {
+      if (n > 0 && !mbar_wait(&ring->draw, (n - 1) & 1u, abort_flag, p.status)) break;
       const int slot = n & (kRing - 1);
       if (!mbar_wait_cluster(ring->empty + slot, ((n / kRing) & 1u) ^ 1u, abort_flag, p.status)) break;
       uint2 w = make_uint2(~0u, 0u);

@@ -222,10 +222,19 @@ TW_DEV bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abor
   }
 }
 
+// An arrival on the barrier of a CTA of the pair that orders nothing but itself; `after`: a
+// value that it waits for.
+TW_DEV void mbar_arrive_cluster_relaxed(uint32_t cluster_addr, bool after) {
+  asm volatile("{\n\t.reg .u32 t;\n\tand.b32 t, %1, 0;\n\tadd.u32 t, t, %0;\n\t"
+               "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [t];\n\t}" ::"r"(cluster_addr),
+               "r"(static_cast<uint32_t>(after))
+               : "memory");
+}
+
 // The units of a pair: one thread of rank 0 draws them and puts each into a ring in both
 // CTAs' shared memory; every role of both CTAs takes them from there in turn.
 constexpr int kRing = 4;
-constexpr int kDrawAhead = 8;  // K blocks before the end of a unit's loads
+constexpr int kDrawAhead = 18;  // K blocks before the end of a unit's loads
 constexpr int kTakers = (2 + kEpiWarps) + (1 + kEpiWarps);  // rank 0's producer, issuer and warps; rank 1's
 struct UnitRing {
   uint64_t full[kRing];    // one arrival
@@ -244,12 +253,14 @@ struct Taker {
     const bool ok = mbar_wait_cluster(ring->full + slot, (n / kRing) & 1u, abort_flag, status);
     if (!(one_thread ? ok : __all_sync(0xFFFFFFFFu, ok))) return false;
     const uint2 w = ring->unit[slot];
-    if (!one_thread) __syncwarp();
-    if (one_thread || (threadIdx.x & 31) == 0) mbar_arrive_cluster(peer_smem_addr(ring->empty + slot, 0));
     ++n;
-    if (w.x == ~0u) return false;
     u.step = w.x >> 24, u.kind = (w.x >> 16) & 255, u.mat = (w.x >> 8) & 255, u.slice = w.x & 255, u.tile = static_cast<int>(w.y);
-    return true;
+    const bool more = w.x != ~0u;
+    if (!one_thread) __syncwarp();
+    // (relaxed: nothing was written that the place's next owner would have to see; a release
+    // at the cluster's scope cost the producer 0.7 us a unit)
+    if (one_thread || (threadIdx.x & 31) == 0) mbar_arrive_cluster_relaxed(peer_smem_addr(ring->empty + slot, 0), more);
+    return more;
   }
 };
 

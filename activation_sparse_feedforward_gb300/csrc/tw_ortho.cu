@@ -66,10 +66,12 @@ constexpr int kMostSteps = 32;
 
 struct NsArgs {
   // operands: X as K-major and MN-major boxes (X alternates between two buffers), E and B
-  CUtensorMap x_k[2], x_mn[2], e_k, b_k;
+  CUtensorMap x_k[2], x_mn[2], e_k;
+  CUtensorMap e_n, b_n;      // as the right-hand operand: boxes of half a unit's columns (SQUARE, APPLY)
   // 32 x 32 blocks that the epilogues read and write: hi, lo, E, B
   CUtensorMap x_block[2], lo_block, e_block, b_block;
   int tiles_m, tiles_n;      // 256 x 256 tiles of X; tiles_n along a side of E and B
+  int width[3];              // columns of a unit, by Kind: 256 or 128
   int count, steps;          // matrices, steps
   int np, mp;                // padded sizes
   int slices[3];             // slices of a tile's K loop, by Kind
@@ -92,13 +94,16 @@ struct NsArgs {
 struct Unit {
   int step, kind, mat, tile, slice;
 };
+// tiles of one matrix's product: 256 rows by width columns
+TW_DEV int tiles_of(const NsArgs& p, int kind) {
+  return (kind == APPLY ? p.tiles_m * p.tiles_n : p.tiles_n * (p.tiles_n + 1) / 2) << (p.width[kind] == 128);
+}
 // The units in the order in which they are handed out. In a step: every matrix's gram, then
 // a matrix's square always one matrix ahead of its apply, so that what a unit waits for was
 // handed out well before it. A unit waits only for units before it in this order; whoever
 // was given those is running, so the wait ends, however few of the CTAs are resident.
 TW_DEV bool unit_at(const NsArgs& p, int n, Unit& u) {
-  const int tri = p.tiles_n * (p.tiles_n + 1) / 2, all = p.tiles_m * p.tiles_n;
-  const int g = tri * p.slices[GRAM], q = tri * p.slices[SQUARE], a = all * p.slices[APPLY];
+  const int g = tiles_of(p, GRAM) * p.slices[GRAM], q = tiles_of(p, SQUARE) * p.slices[SQUARE], a = tiles_of(p, APPLY) * p.slices[APPLY];
   const int per_step = p.count * (g + q + a);
   u.step = n / per_step;
   if (u.step >= p.steps) return false;
@@ -131,16 +136,19 @@ TW_DEV bool unit_at(const NsArgs& p, int n, Unit& u) {
   }
   return false;
 }
-// tile row and column
+// tile row (of 256) and column (of width)
 TW_DEV void tile_at(const NsArgs& p, const Unit& u, int& i, int& j) {
+  const int narrow = p.width[u.kind] == 128;
   if (u.kind == APPLY) {
-    i = u.tile / p.tiles_n;
-    j = u.tile - i * p.tiles_n;
-  } else {  // the lower triangle, row by row
-    i = static_cast<int>((sqrtf(8.f * u.tile + 1.f) - 1.f) * 0.5f);
-    while ((i + 1) * (i + 2) / 2 <= u.tile) ++i;
-    while (i * (i + 1) / 2 > u.tile) --i;
-    j = u.tile - i * (i + 1) / 2;
+    const int per_row = p.tiles_n << narrow;
+    i = u.tile / per_row;
+    j = u.tile - i * per_row;
+  } else {  // the lower triangle with the whole 256 x 256 blocks of the diagonal, row by row
+    const int t = u.tile >> narrow;
+    i = static_cast<int>((sqrtf(8.f * t + 1.f) - 1.f) * 0.5f);
+    while ((i + 1) * (i + 2) / 2 <= t) ++i;
+    while (i * (i + 1) / 2 > t) --i;
+    j = u.tile - (i * (i + 1) / 2 << narrow);
   }
 }
 TW_DEV void k_blocks(const NsArgs& p, const Unit& u, int& lo, int& hi) {
@@ -169,9 +177,8 @@ TW_DEV bool wait_inputs(const NsArgs& p, const Unit& u, Known& known, volatile i
   const uint64_t steps = u.kind == GRAM ? known.steps[GRAM] : u.kind == SQUARE ? known.steps[SQUARE] : known.steps[APPLY];
   const int at = 8 * u.mat;
   if (static_cast<int>(steps >> at & 255) == u.step + 1) return true;
-  const int tri = p.tiles_n * (p.tiles_n + 1) / 2, all = p.tiles_m * p.tiles_n;
   const int of = u.kind == GRAM ? APPLY : u.kind == SQUARE ? GRAM : SQUARE;
-  const int need = (u.kind == GRAM ? u.step * all : (u.step + 1) * tri) * 2 * kEpiWarps;
+  const int need = (u.kind == GRAM ? u.step : u.step + 1) * tiles_of(p, of) * 2 * kEpiWarps;
   const int* done = p.done + u.mat * 3 + of;
   if (ld_acquire(done) < need) {
     const uint64_t t0 = global_timer_ns();
@@ -334,8 +341,10 @@ struct Blocks {
   const NsArgs& p;
   const Unit& u;
   uint8_t* staging;     // this warp's 8 KB
-  uint64_t* bar;        // [2], each completed twice a tile: chunk c is phase c / 2 of its buffer's
-  int lane, base, i, j; // base: the matrix's first row in the maps; i, j: the tile
+  uint64_t* bar;        // [2]
+  int turn;             // phases of each that are over: chunk c completes phase turn + c / 2 of its buffer's
+  int lane, base;       // base: the matrix's first row in the maps
+  bool mirror;          // off the diagonal's blocks: written on its other side too
   TW_DEV uint8_t* buffer(int c) const { return staging + (c & 1) * 2 * kChunkBytes; }
   // lane 0: chunk c's blocks, from row and column of the matrix
   TW_DEV void ask(int c, int row, int col) {
@@ -348,7 +357,7 @@ struct Blocks {
   }
   // chunk c's buffer, for every lane: free, or filled with what was asked for
   TW_DEV bool here(int c, volatile int* abort_flag) {
-    if constexpr (kIn > 0) return __all_sync(0xFFFFFFFFu, mbar_wait(bar + (c & 1), (c >> 1) & 1u, abort_flag, p.status)) != 0;
+    if constexpr (kIn > 0) return __all_sync(0xFFFFFFFFu, mbar_wait(bar + (c & 1), (turn + (c >> 1)) & 1u, abort_flag, p.status)) != 0;
     // one group a chunk: with the latest one excepted, this buffer's stores have been read
     if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
     __syncwarp();
@@ -398,7 +407,6 @@ struct Blocks {
     for (int k = 0; k < 16; ++k) w[k] = pack_f16x2_rn(v[2 * k], v[2 * k + 1]);
 #pragma unroll
     for (int q = 0; q < 4; ++q) *piece(b0, lane, q) = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-    const bool mirror = KIND != APPLY && i != j;
     if constexpr (KIND == APPLY) {
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
@@ -424,16 +432,17 @@ struct Blocks {
   }
 };
 
-// One warp's 32 rows x 128 columns of a unit; false where a bounded wait ran out.
+// One warp's 32 rows of half a unit's columns; false where a bounded wait ran out.
 template <int KIND>
-TW_DEV bool epilogue(const NsArgs& p, const Unit& u, uint8_t* staging, uint64_t* bar, uint64_t* tfull, uint32_t parity,
-                     uint32_t tmem, int rank, int ew, Known& known, volatile int* abort_flag) {
+TW_DEV bool epilogue(const NsArgs& p, const Unit& u, uint8_t* staging, uint64_t* bar, int& turn, uint64_t* tfull,
+                     uint32_t parity, uint32_t tmem, int rank, int ew, Known& known, volatile int* abort_flag) {
   const int lane = threadIdx.x & 31, quarter = (ew + 2) & 3, half = ew >> 2;
+  const int width = p.width[KIND], chunks = width / 64, slices = p.slices[KIND];
   int ti, tj;
   tile_at(p, u, ti, tj);
-  Blocks<KIND> blocks{p, u, staging, bar, lane, u.mat * (KIND == APPLY ? p.mp : p.np), ti, tj};
-  const int row = ti * kTile + rank * 128 + quarter * 32 + lane, col = tj * kTile + half * 128;
-  const int slices = p.slices[KIND];
+  Blocks<KIND> blocks{p, u, staging, bar, turn, lane, u.mat * (KIND == APPLY ? p.mp : p.np), KIND != APPLY && tj * width / kTile != ti};
+  const int row = ti * kTile + rank * 128 + quarter * 32 + lane, col = tj * width + half * (width / 2);
+  tmem += half * (width / 2) + (static_cast<uint32_t>(quarter * 32) << 16);
   int asked = 0, taken = 0;  // chunks
   auto ask = [&] {
     if (lane == 0) blocks.ask(asked, row, col + asked * 32);
@@ -441,7 +450,7 @@ TW_DEV bool epilogue(const NsArgs& p, const Unit& u, uint8_t* staging, uint64_t*
   };
   auto drained = [&] {  // given up: no copy of this warp's may be under way when its CTA leaves
     if (KIND != GRAM && lane == 0)
-      for (; taken < asked; ++taken) mbar_wait_drain(bar + (taken & 1), (taken >> 1) & 1u);
+      for (; taken < asked; ++taken) mbar_wait_drain(bar + (taken & 1), (turn + (taken >> 1)) & 1u);
     __syncwarp();
     return false;
   };
@@ -466,7 +475,7 @@ TW_DEV bool epilogue(const NsArgs& p, const Unit& u, uint8_t* staging, uint64_t*
     if (seen != slices - 1) {
       float* to = slot(u.slice);
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < chunks; ++c) {
         uint32_t v[32];
         tmem_ld32(tmem + c * 32, v);
         tmem_wait_ld();
@@ -483,7 +492,7 @@ TW_DEV bool epilogue(const NsArgs& p, const Unit& u, uint8_t* staging, uint64_t*
     if (KIND != GRAM) ask(), ask();
   }
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < chunks; ++c) {
     uint32_t w[32];
     float v[32];
     tmem_ld32(tmem + c * 32, w);
@@ -510,11 +519,12 @@ TW_DEV bool epilogue(const NsArgs& p, const Unit& u, uint8_t* staging, uint64_t*
     if (!blocks.here(c, abort_flag)) return drained();
     taken = c + 1;
     blocks.put(c, row, col + c * 32, v);
-    if (KIND != GRAM && (c == 1 || c == 2)) {  // the buffer of the chunk before: its stores have been read by now
+    if (KIND != GRAM && c > 0 && asked < chunks) {  // the buffer of the chunk before: its stores have been read by now
       if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
       ask();
     }
   }
+  if (KIND != GRAM) turn += chunks / 2;
   // the tile's writes are there for whoever is told so; the next step reads them
   if (lane == 0) {
     if (slices > 1) *arrived = 0;
@@ -590,7 +600,8 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
           ok = false;
           break;
         }
-        const int m0 = i * kTile + rank * 128, n0 = j * kTile + rank * 128, x = u.step & 1;
+        const int half = p.width[u.kind] / 2;  // columns of the unit in each CTA
+        const int m0 = i * kTile + rank * 128, n0 = j * 2 * half + rank * half, x = u.step & 1;
         const int xrow = u.mat * p.mp, srow = u.mat * p.np;
         const int draw_at = max(lo, hi - kDrawAhead);
         for (int kb = lo; kb < hi; ++kb) {
@@ -601,20 +612,20 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
           }
           uint8_t* sa = tiles + stage * kStageBytes;
           uint8_t* sb = sa + kOperandBytes;
-          if (rank == 0) mbar_arrive_expect_tx(full + stage, 2 * kStageBytes);
+          if (rank == 0) mbar_arrive_expect_tx(full + stage, 2 * (kOperandBytes + half * kBK * 2));
           const uint32_t bar = peer_smem_addr(full + stage, 0);
           const int k0 = kb * kBK;
           if (u.kind == GRAM) {  // both operands stored [K, MN]
             tma_load_2d_pair(sa, &p.x_mn[x], bar, m0, xrow + k0);
             tma_load_2d_pair(sa + 8192, &p.x_mn[x], bar, m0 + 64, xrow + k0);
             tma_load_2d_pair(sb, &p.x_mn[x], bar, n0, xrow + k0);
-            tma_load_2d_pair(sb + 8192, &p.x_mn[x], bar, n0 + 64, xrow + k0);
+            if (half == 128) tma_load_2d_pair(sb + 8192, &p.x_mn[x], bar, n0 + 64, xrow + k0);
           } else if (u.kind == SQUARE) {
             tma_load_2d_pair(sa, &p.e_k, bar, k0, srow + m0);
-            tma_load_2d_pair(sb, &p.e_k, bar, k0, srow + n0);
+            tma_load_2d_pair(sb, &p.e_n, bar, k0, srow + n0);
           } else {
             tma_load_2d_pair(sa, &p.x_k[x], bar, k0, xrow + m0);
-            tma_load_2d_pair(sb, &p.b_k, bar, k0, srow + n0);
+            tma_load_2d_pair(sb, &p.b_n, bar, k0, srow + n0);
           }
           ++issued;
           if (++stage == kStages) stage = 0, phase ^= 1u;
@@ -644,7 +655,9 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
         tc_fence_after_sync();
         const uint32_t d0 = tmem_base + static_cast<uint32_t>(buf * kTile);
         const bool mn = u.kind == GRAM;
-        const uint32_t idesc = mn ? idesc_bf16_f32(kTile, kTile, true, true, true) : idesc_bf16_f32(kTile, kTile, false, false, true);
+        const uint32_t idesc = p.width[u.kind] == 256
+                                   ? (mn ? idesc_bf16_f32(kTile, 256, true, true, true) : idesc_bf16_f32(kTile, 256, false, false, true))
+                                   : (mn ? idesc_bf16_f32(kTile, 128, true, true, true) : idesc_bf16_f32(kTile, 128, false, false, true));
         for (int kb = lo; kb < hi; ++kb) {
           if (!mbar_wait(full + stage, phase, abort_flag, p.status)) {
             ok = false;
@@ -670,17 +683,18 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
       }
     }
   } else if (warp < 2 + kEpiWarps) {
-    const int ew = warp - 2, quarter = warp & 3, half = ew >> 2;
+    const int ew = warp - 2;
+    int turn = 0;
     bool ok = true;
     for (int local = 0; ok && units.take(u, false); ++local) {
       const int buf = local & 1;
-      const uint32_t t0 = tmem_base + static_cast<uint32_t>(buf * kTile + half * 128) + (static_cast<uint32_t>(quarter * 32) << 16);
+      const uint32_t t0 = tmem_base + static_cast<uint32_t>(buf * kTile);
       uint8_t* st = staging + ew * 4 * kChunkBytes;
       uint64_t* bar = block_bars + 2 * ew;
       const uint32_t parity = (local >> 1) & 1u;
-      if (u.kind == GRAM) ok = epilogue<GRAM>(p, u, st, bar, tfull + buf, parity, t0, rank, ew, known, abort_flag);
-      else if (u.kind == SQUARE) ok = epilogue<SQUARE>(p, u, st, bar, tfull + buf, parity, t0, rank, ew, known, abort_flag);
-      else ok = epilogue<APPLY>(p, u, st, bar, tfull + buf, parity, t0, rank, ew, known, abort_flag);
+      if (u.kind == GRAM) ok = epilogue<GRAM>(p, u, st, bar, turn, tfull + buf, parity, t0, rank, ew, known, abort_flag);
+      else if (u.kind == SQUARE) ok = epilogue<SQUARE>(p, u, st, bar, turn, tfull + buf, parity, t0, rank, ew, known, abort_flag);
+      else ok = epilogue<APPLY>(p, u, st, bar, turn, tfull + buf, parity, t0, rank, ew, known, abort_flag);
       if (!ok) break;
       tc_fence_before_sync();
       __syncwarp();
@@ -803,19 +817,26 @@ __global__ void __launch_bounds__(kNormThreads) ns_norm_kernel(const NsInArgs a)
   pdl_enter();
   const int mat = a.first + blockIdx.y;
   NormSums s = {0.f, 0.f, 0.f};
-  const unsigned per_row = (a.cols + 7) / 8;
+  const unsigned per_row = a.vec ? a.cols / 8 : a.cols;
   const long total = static_cast<long>(a.rows) * per_row, step = static_cast<long>(gridDim.x) * kNormThreads;
   long i = static_cast<long>(blockIdx.x) * kNormThreads + threadIdx.x;
   int r = static_cast<int>(i / per_row), c = static_cast<int>(i - static_cast<long>(r) * per_row);
   const int dr = static_cast<int>(step / per_row), dc = static_cast<int>(step - static_cast<long>(dr) * per_row);
-#pragma unroll 2
-  for (; i < total; i += step) {
-    float u[8];
-    update8<GT>(a, mat, r, c * 8, true, u);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) add_square(s, u[k]);
-    r += dr, c += dc;
+  auto next = [&] {
+    i += step, r += dr, c += dc;
     if (c >= static_cast<int>(per_row)) c -= per_row, ++r;
+  };
+  if (a.vec) {
+#pragma unroll 2
+    for (; i < total; next()) {
+      float u[8];
+      update8<GT>(a, mat, r, c * 8, true, u);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) add_square(s, u[k]);
+    }
+  } else {
+#pragma unroll 4
+    for (; i < total; next()) add_square(s, update_of<GT>(a, mat, r, c, true));
   }
   s.small = warp_sum(s.small), s.mid = warp_sum(s.mid), s.big = warp_sum(s.big);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
@@ -918,22 +939,30 @@ __global__ void __launch_bounds__(256) ns_start_wide_kernel(const NsInArgs a, in
 // ------------------------------------------------------------------ host
 int up(int n) { return (n + kTile - 1) / kTile * kTile; }
 
-// Slices of a tile's K loop, where a matrix's tiles are fewer than the pairs of SMs (76 on
-// this GPU; a constant, so that the workspace does not depend on the device). In K blocks of
-// 0.33 us: handing a slice's sums on and adding them takes about 15.
+// How a product of `tiles` 256 x 256 tiles (of all matrices) with kb K blocks runs: whole
+// tiles where there is one for every pair of SMs (a matrix's products overlap the others');
+// with fewer, units of 256 or 128 columns, and slices of their K loop. 76 pairs of SMs (a constant, so that the
+// workspace does not depend on the device). Costs in K blocks of a 256-wide unit, 0.33 us: a
+// narrow unit's takes 0.7 (its operands are three quarters of the bytes for half the work);
+// after the last K block a unit's epilogue takes 23 (7.6 us), a narrow one's 14; slices hand
+// on their sums and add them.
 constexpr int kPairs = 76, kMostSlices = 8;
-int slices_of(int tiles, int kb) {
-  int best = 1, cost = kb;
-  for (int s = 2; s <= kMostSlices && s * tiles <= kPairs; ++s) {
-    const int chunk = (kb + s - 1) / s;
-    if ((kb + chunk - 1) / chunk != s) continue;  // no empty slice
-    if (chunk + 15 + 2 * s < cost) best = s, cost = chunk + 15 + 2 * s;
-  }
-  return best;
+void form_of(int tiles, int kb, int& width, int& slices) {
+  width = 256, slices = 1;
+  if (tiles >= kPairs) return;
+  float best = 0.f;
+  for (int w = 256; w >= 128; w /= 2)
+    for (int s = 1; s <= std::min(kMostSlices, kb); ++s) {
+      const int units = tiles * (256 / w) * s, chunk = (kb + s - 1) / s;
+      if ((kb + chunk - 1) / chunk != s || (s > 1 && units > kPairs)) continue;  // no empty slice
+      const float cost = static_cast<float>((units + kPairs - 1) / kPairs) * chunk * (w == 256 ? 1.f : 0.7f) + (w == 256 ? 23.f : 14.f) +
+                         (s > 1 ? (w == 256 ? 30.f : 18.f) + 3.f * s : 0.f);
+      if (best == 0.f || cost < best) best = cost, width = w, slices = s;
+    }
 }
 
 struct Layout {
-  int mp, np, slices[3], slots;
+  int mp, np, width[3], slices[3], slots;
   size_t hi0, hi1, lo, e, b, part, arrived, counters, norms, bytes;
   int words() const { return static_cast<int>((norms - arrived) / 4); }  // arrived and the counters after it
 };
@@ -941,12 +970,11 @@ Layout layout(int m, int n, int count) {
   Layout l{};
   l.mp = up(std::max(m, n)), l.np = up(std::min(m, n));
   const int t = l.np / kTile, tri = t * (t + 1) / 2, all = l.mp / kTile * t;
-  l.slices[GRAM] = slices_of(tri * count, l.mp / kBK);
-  l.slices[SQUARE] = slices_of(tri * count, l.np / kBK);
-  l.slices[APPLY] = slices_of(all * count, l.np / kBK);
   const int tiles[3] = {tri, tri, all};
-  for (int k = 0; k < 3; ++k)
-    if (l.slices[k] > 1) l.slots = std::max(l.slots, tiles[k] * l.slices[k]);
+  for (int k = 0; k < 3; ++k) {
+    form_of(tiles[k] * count, (k == GRAM ? l.mp : l.np) / kBK, l.width[k], l.slices[k]);
+    if (l.slices[k] > 1) l.slots = std::max(l.slots, tiles[k] * (256 / l.width[k]) * l.slices[k]);
+  }
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t was = at;
@@ -1029,11 +1057,11 @@ cudaError_t launch_ortho(const OrthoArgs& o, cudaStream_t s) {
     map(p.x_k[i], x, xrows, 64, 128), map(p.x_mn[i], x, xrows, 64, 64), map(p.x_block[i], x, xrows, 32, 32);
   }
   map(p.lo_block, l.lo, xrows, 32, 32), map(p.e_block, l.e, srows, 32, 32), map(p.b_block, l.b, srows, 32, 32);
-  map(p.e_k, l.e, srows, 64, 128), map(p.b_k, l.b, srows, 64, 128);
+  map(p.e_k, l.e, srows, 64, 128), map(p.e_n, l.e, srows, 64, l.width[SQUARE] / 2), map(p.b_n, l.b, srows, 64, l.width[APPLY] / 2);
   if (!ok) return cudaErrorInvalidValue;
 
   p.tiles_m = l.mp / kTile, p.tiles_n = l.np / kTile, p.count = o.count, p.steps = o.steps, p.np = l.np, p.mp = l.mp;
-  for (int i = 0; i < 3; ++i) p.slices[i] = l.slices[i];
+  for (int i = 0; i < 3; ++i) p.width[i] = l.width[i], p.slices[i] = l.slices[i];
   p.slots = l.slots, p.part = reinterpret_cast<float*>(ws + l.part), p.arrived = in.arrived;
   p.done = reinterpret_cast<int*>(ws + l.counters), p.next = p.done + 3 * o.count, p.status = o.status;
   for (int i = 0; i < o.count; ++i) p.out[i] = o.out[i];
@@ -1052,8 +1080,11 @@ cudaError_t launch_ortho(const OrthoArgs& o, cudaStream_t s) {
   static int resident = -1;  // the query depends only on the kernel
   if (resident < 0) resident = max_active_clusters(ns_kernel, kThreads, kSmem, 2);
   // no more pairs than a product of all matrices has units
-  const long tri = static_cast<long>(p.tiles_n) * (p.tiles_n + 1) / 2, all = static_cast<long>(p.tiles_m) * p.tiles_n;
-  const long most = o.count * std::max({tri * l.slices[GRAM], tri * l.slices[SQUARE], all * l.slices[APPLY]});
+  long most = 0;
+  for (int i = 0; i < 3; ++i) {
+    const long tiles = i == APPLY ? static_cast<long>(p.tiles_m) * p.tiles_n : static_cast<long>(p.tiles_n) * (p.tiles_n + 1) / 2;
+    most = std::max(most, o.count * tiles * (256 / l.width[i]) * l.slices[i]);
+  }
   const int pairs = static_cast<int>(std::min<long>(most, std::min(resident, device_sm_count() / 2)));
   if (pairs < 1) return cudaErrorInvalidConfiguration;
   e = launch_clustered(ns_kernel, dim3(2 * pairs), dim3(kThreads), kSmem, 2, s, p);

@@ -8,6 +8,7 @@
 // order, so the same call gives the same bits. Both are bound by HBM; the gradient written
 // whole is mostly the zeros of the tokens that do not occur.
 #include <algorithm>
+#include <type_traits>
 
 #include "tw_internal.h"
 #include "tw_rows.cuh"
@@ -74,58 +75,88 @@ __global__ void __launch_bounds__(kFwdThreads) embed_fwd_kernel(const EmbedFwdAr
 }
 
 // ------------------------------------------------------------------ backward: rows into registers
-// Columns [c, c + 8) of dy's rows, summed into acc in order; `n` rows at pos[0], pos[1], ...
-constexpr int kCols = 8, kBatch = 8;
+// A lane's 8 of a warp's 256 columns of dy's rows, summed into acc in order. VEC: 8 adjacent
+// ones, 16 bytes at a time. Else 32 columns apart, so that a warp's accesses are adjacent by
+// the element: rows off 16 bytes put together from aligned vectors (tw_rows.cuh) took twice
+// the instructions.
+constexpr int kCols = 8, kWarpCols = 32 * kCols;
 
 template <int DT, bool VEC>
 struct RowSum {
   using S = typename Elem<DT>::S;
-  static constexpr int E = Elem<DT>::E, NV = kCols / E;
+  static constexpr int E = VEC ? Elem<DT>::E : 1, NV = kCols / E;
+  static constexpr int kStride = VEC ? 1 : 32;  // from a lane's column to its next
+  using W = std::conditional_t<VEC, uint4, S>;  // what one load brings
   const EmbedBwdArgs& a;
-  int c;
+  int c;        // the lane's first column
   float acc[kCols];
-  TW_DEV RowSum(const EmbedBwdArgs& a_, int c_) : a(a_), c(c_) { clear(); }
+  TW_DEV RowSum(const EmbedBwdArgs& a_, int first) : a(a_), c(first + static_cast<int>(threadIdx.x & 31) * (VEC ? kCols : 1)) {
+    clear();
+  }
   TW_DEV void clear() {
 #pragma unroll
     for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
   }
-  TW_DEV void load(int pos, uint4 (&w)[NV]) const {
+  TW_DEV int col(int i) const { return c + i * kStride; }
+  TW_DEV void load(int pos, W (&w)[NV]) const {
     const S* row = static_cast<const S*>(a.dy) + static_cast<size_t>(pos) * a.lddy;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int at = c + k * E;
-      w[k] = make_uint4(0, 0, 0, 0);
-      if (at < a.d)
-        w[k] = VEC ? __ldg(reinterpret_cast<const uint4*>(row + at))
-                   : load_any<DT>(row + at, a.d - at, pos == 0 || pos == a.T - 1 || a.lddy < E);
+      if constexpr (VEC)
+        w[k] = col(k * E) < a.d ? __ldg(reinterpret_cast<const uint4*>(row + col(k * E))) : make_uint4(0, 0, 0, 0);
+      else
+        w[k] = col(k) < a.d ? __ldg(row + col(k)) : Elem<DT>::put(0.f);
     }
   }
-  TW_DEV void add(const uint4 (&w)[NV]) {
+  TW_DEV void add(const W (&w)[NV]) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      float u[E];
-      Elem<DT>::unpack(w[k], u);
+      if constexpr (VEC) {
+        float u[E];
+        Elem<DT>::unpack(w[k], u);
 #pragma unroll
-      for (int i = 0; i < E; ++i) acc[k * E + i] += u[i];
+        for (int i = 0; i < E; ++i) acc[k * E + i] += u[i];
+      } else {
+        acc[k] += Elem<DT>::get(w[k]);
+      }
     }
   }
-  // the finished sum of token v
-  TW_DEV void put(int v) {
-    float* out = a.dw + static_cast<size_t>(v) * a.lddw + c;
-    if (a.vec_out) {
+  // the sum so far to, and another added from, a part of a run: 256 columns a warp, in the
+  // lanes' order
+  TW_DEV void keep(float* part) const {
+    float4* to = reinterpret_cast<float4*>(part) + 2 * (threadIdx.x & 31);
+    to[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    to[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+  }
+  TW_DEV void join(const float4& p, const float4& q) {
+    acc[0] += p.x, acc[1] += p.y, acc[2] += p.z, acc[3] += p.w;
+    acc[4] += q.x, acc[5] += q.y, acc[6] += q.z, acc[7] += q.w;
+  }
+  TW_DEV void join(const float* part) {
+    const float4* from = reinterpret_cast<const float4*>(part) + 2 * (threadIdx.x & 31);
+    join(from[0], from[1]);
+  }
+  // the finished sum of token v, into its row
+  TW_DEV void put(int v) const {
+    float* out = a.dw + static_cast<size_t>(v) * a.lddw;
+    if (VEC && a.vec_out) {
+      float4 o[kCols / 4];
 #pragma unroll
-      for (int k = 0; k < kCols / 4; ++k) {
-        if (c + 4 * k >= a.d) break;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (a.add) o = reinterpret_cast<const float4*>(out)[k];
-        o.x = fmaf(a.scale, acc[4 * k], o.x), o.y = fmaf(a.scale, acc[4 * k + 1], o.y);
-        o.z = fmaf(a.scale, acc[4 * k + 2], o.z), o.w = fmaf(a.scale, acc[4 * k + 3], o.w);
-        reinterpret_cast<float4*>(out)[k] = o;
-      }
+      for (int k = 0; k < kCols / 4; ++k)
+        o[k] = a.add && c + 4 * k < a.d ? reinterpret_cast<const float4*>(out + c)[k] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kCols / 4; ++k)
+        if (c + 4 * k < a.d)
+          reinterpret_cast<float4*>(out + c)[k] =
+              make_float4(fmaf(a.scale, acc[4 * k], o[k].x), fmaf(a.scale, acc[4 * k + 1], o[k].y),
+                          fmaf(a.scale, acc[4 * k + 2], o[k].z), fmaf(a.scale, acc[4 * k + 3], o[k].w));
     } else {
+      float o[kCols];
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) o[i] = a.add && col(i) < a.d ? out[col(i)] : 0.f;
 #pragma unroll
       for (int i = 0; i < kCols; ++i)
-        if (c + i < a.d) out[i] = fmaf(a.scale, acc[i], a.add ? out[i] : 0.f);
+        if (col(i) < a.d) out[col(i)] = fmaf(a.scale, acc[i], o[i]);
     }
   }
 };
@@ -140,8 +171,7 @@ TW_DEV void zero_row(const EmbedBwdArgs& a, int v, int tid, int threads) {
   }
 }
 
-constexpr int kThreads = 256;                 // of the kernels below: 2048 columns
-constexpr int kBlockCols = kThreads * kCols;
+constexpr int kThreads = 128, kBlockCols = kThreads * kCols;  // of the kernels below
 
 // ------------------------------------------------------------------ backward of few tokens
 // One launch and no sort: the CTA of position i looks through the tokens; where its own
@@ -156,7 +186,7 @@ __global__ void __launch_bounds__(kThreads) embed_bwd_few_kernel(const EmbedBwdA
   pdl_enter();
   const int tid = threadIdx.x;
   for (int i = tid; i < a.T; i += kThreads) tok[i] = a.tokens[i];
-  if (tid < kFewTokens / 32) same[tid] = 0u;
+  for (int i = tid; i < kFewTokens / 32; i += kThreads) same[i] = 0u;
   __syncthreads();
   const int words = (a.T + 31) / 32;
   if (static_cast<int>(blockIdx.x) >= a.T) {  // zeros
@@ -184,9 +214,10 @@ __global__ void __launch_bounds__(kThreads) embed_bwd_few_kernel(const EmbedBwdA
   for (int w = 0; w < me >> 5; ++w)
     if (same[w] != 0u) return;
   if (same[me >> 5] & ((1u << (me & 31)) - 1u)) return;
-  RowSum<DT, VEC> sum(a, (blockIdx.y * kThreads + tid) * kCols);
+  constexpr int kBatch = 8;  // rows on their way at once
+  RowSum<DT, VEC> sum(a, blockIdx.y * kBlockCols + (tid >> 5) * kWarpCols);
   if (sum.c >= a.d) return;
-  uint4 w[kBatch][RowSum<DT, VEC>::NV];
+  typename RowSum<DT, VEC>::W w[kBatch][RowSum<DT, VEC>::NV];
   int n = 0;
   for (int word = me >> 5; word < words; ++word)
     for (unsigned m = same[word]; m != 0u;) {  // up to kBatch rows on their way at once
@@ -206,189 +237,249 @@ __global__ void __launch_bounds__(kThreads) embed_bwd_few_kernel(const EmbedBwdA
 }
 
 // ------------------------------------------------------------------ backward: sort
-// Positions in the order of (token, position). Each CTA owns `range` tokens (at most
-// kMostRange) and needs nothing from the others: it reads all tokens, counts those below
+// Positions in the order of (token, position). Each CTA owns `range` tokens (about V / 152, at
+// most kMostRange) and needs nothing from the others: it reads all tokens, counts those below
 // its own (where its part of the result begins) and its own for each warp's stretch of the
 // positions, and after a prefix sum over (token, warp) goes through them once more, each
-// warp its stretch in order, and puts them down.
-constexpr int kSortWarps = 16, kSortThreads = 32 * kSortWarps, kMostRange = 1024, kAhead = 8;
+// warp its stretch in order, and puts them down. Bound by the instructions of that: about 40
+// a warp for 128 tokens that are others'.
+constexpr int kSortWarps = 32, kSortThreads = 32 * kSortWarps, kMostRange = 1024, kAhead = 4;
+
+TW_DEV int warp_sum_int(int v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
 
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedBwdArgs a) {
-  extern __shared__ int count[];  // [kSortWarps][range]
+  extern __shared__ int count[];  // [kSortWarps][range], then [range + 1]: where a token's positions begin
   __shared__ int scan[kSortWarps], below[kSortWarps];
   pdl_enter();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, range = a.range;
   const int lo = blockIdx.x * range;
+  const unsigned own_range = min(range, a.V - lo);
+  // a warp's stretch: groups of 128 positions, four adjacent ones a lane
+  const int stretch = (a.T + 4 * kSortThreads - 1) / (4 * kSortThreads) * 128;
+  const int begin = min(a.T, warp * stretch), end = min(a.T, begin + stretch);
+  const bool whole = (reinterpret_cast<uintptr_t>(a.tokens) & 15u) == 0;
+  int4 t[kAhead];  // (up to 16384 tokens in all: read once)
+  auto read = [&](int base) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = base + 128 * k + 4 * lane;
+      const int* p = a.tokens + i;
+      if (whole && i + 4 <= end)
+        t[k] = __ldg(reinterpret_cast<const int4*>(p));
+      else
+        t[k] = make_int4(i < end ? p[0] : -1, i + 1 < end ? p[1] : -1, i + 2 < end ? p[2] : -1, i + 3 < end ? p[3] : -1);
+    }
+  };
+  auto own = [&](int v) { return static_cast<unsigned>(v - lo) < own_range; };
+  auto owns = [&](const int4& v) { return own(v.x) || own(v.y) || own(v.z) || own(v.w); };
+  read(begin);
   for (int i = tid; i < kSortWarps * range; i += kSortThreads) count[i] = 0;
   __syncthreads();
-  const int stretch = (a.T + kSortThreads - 1) / kSortThreads * 32;
-  const int begin = min(a.T, warp * stretch), end = min(a.T, begin + stretch);
   int* mine = count + warp * range;
+  int* start = count + kSortWarps * range;
   int less = 0;
   bool bad = false;
-  for (int i = begin + lane; i < end; i += 32 * kAhead) {
-    int t[kAhead];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) t[k] = i + 32 * k < end ? a.tokens[i + 32 * k] : -1;
+  for (int base = begin; base < end; base += 128 * kAhead) {
+    if (base > begin) read(base);
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      bad |= t[k] < -1 || t[k] >= a.V;
-      less += t[k] >= 0 && t[k] < lo;
-      if (static_cast<unsigned>(t[k] - lo) < static_cast<unsigned>(range) && t[k] < a.V) atomicAdd(mine + (t[k] - lo), 1);
+      const unsigned l = lo;
+      less += (static_cast<unsigned>(t[k].x) < l) + (static_cast<unsigned>(t[k].y) < l) + (static_cast<unsigned>(t[k].z) < l) +
+              (static_cast<unsigned>(t[k].w) < l);
+      if (owns(t[k])) {
+        if (own(t[k].x)) atomicAdd(mine + (t[k].x - lo), 1);
+        if (own(t[k].y)) atomicAdd(mine + (t[k].y - lo), 1);
+        if (own(t[k].z)) atomicAdd(mine + (t[k].z - lo), 1);
+        if (own(t[k].w)) atomicAdd(mine + (t[k].w - lo), 1);
+      }
+    }
+    if (blockIdx.x == 0) {
+      auto out = [&](int v) { return v < -1 || v >= a.V; };
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) bad |= out(t[k].x) || out(t[k].y) || out(t[k].z) || out(t[k].w);
     }
   }
-  if (bad && blockIdx.x == 0) raise_status(a.status, TW_EINVAL);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) less += __shfl_xor_sync(0xFFFFFFFFu, less, o);
+  if (bad) raise_status(a.status, TW_EINVAL);
+  less = warp_sum_int(less);
   if (lane == 0) below[warp] = less;
   __syncthreads();
-  // tokens 2 tid and 2 tid + 1: totals, prefixes over the warps, then over the tokens
-  int total[2] = {0, 0};
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int r = 2 * tid + k;
-    if (r < range)
-      for (int w = 0; w < kSortWarps; ++w) {
-        const int n = count[w * range + r];
-        count[w * range + r] = total[k];
-        total[k] += n;
-      }
-  }
-  const int both_ = total[0] + total[1], inc = warp_inclusive_scan(both_);
-  if (lane == 31) scan[warp] = inc;
-  // which tokens occur: a bit each
-  if (a.present != nullptr) {
-    const unsigned e = __ballot_sync(0xFFFFFFFFu, total[0] > 0), o = __ballot_sync(0xFFFFFFFFu, total[1] > 0);
-    if (lane < 2) {  // lane 0: tokens 64 warp .. + 31, lane 1: the next 32
-      const unsigned eh = lane ? e >> 16 : e & 0xFFFFu, oh = lane ? o >> 16 : o & 0xFFFFu;
-      unsigned m = 0u;
-#pragma unroll
-      for (int b = 0; b < 16; ++b) m |= ((eh >> b) & 1u) << (2 * b) | ((oh >> b) & 1u) << (2 * b + 1);
-      const int r = 64 * warp + 32 * lane;
-      if (r < range) a.present[(lo + r) >> 5] = m;
+  // token tid: its total, the prefix over the warps, then over the tokens
+  int total = 0;
+  if (tid < range) {
+#pragma unroll 16
+    for (int w = 0; w < kSortWarps; ++w) {
+      const int n = count[w * range + tid];
+      count[w * range + tid] = total;
+      total += n;
     }
   }
+  const int inc = warp_inclusive_scan(total);
+  if (lane == 31) scan[warp] = inc;
+  // which tokens occur: a bit each
+  const unsigned occur = __ballot_sync(0xFFFFFFFFu, total > 0);
+  if (a.present != nullptr && lane == 0 && 32 * warp < range) a.present[(lo >> 5) + warp] = occur;
   __syncthreads();
-  int at = inc - both_;
-  for (int w = 0; w < kSortWarps; ++w) at += (w < warp ? scan[w] : 0) + below[w];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int r = 2 * tid + k;
-    if (r < range)
-      for (int w = 0; w < kSortWarps; ++w) count[w * range + r] += at;
-    at += total[k];
-  }
-  if (blockIdx.x == gridDim.x - 1 && tid == kSortThreads - 1) *a.n_valid = at;
+  const int at = warp_sum_int(below[lane] + (lane < warp ? scan[lane] : 0)) + inc - total;
+  if (tid < range) start[tid] = at;
+  if (tid == range - 1) start[range] = at + total;
+  if (blockIdx.x == gridDim.x - 1 && tid == kSortThreads - 1) *a.n_valid = at + total;
   __syncthreads();
-  for (int base = begin; base < end; base += 32 * kAhead) {
-    int t[kAhead];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) t[k] = base + 32 * k + lane < end ? a.tokens[base + 32 * k + lane] : -1;
+  for (int base = begin; base < end; base += 128 * kAhead) {
+    if (end - begin > 128 * kAhead) read(base);
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      const bool own = static_cast<unsigned>(t[k] - lo) < static_cast<unsigned>(range) && t[k] < a.V;
-      const unsigned act = __ballot_sync(0xFFFFFFFFu, own);
-      if (act == 0u) continue;
-      if (own) {
-        const unsigned peers = __match_any_sync(act, t[k]);
-        int* n = mine + (t[k] - lo);
-        const int slot = *n + __popc(peers & ((1u << lane) - 1u));
-        __syncwarp(act);
-        if (lane == __ffs(peers) - 1) *n += __popc(peers);
-        a.pos[slot] = base + 32 * k + lane;
-        a.key[slot] = t[k];
+      if (!__any_sync(0xFFFFFFFFu, owns(t[k]))) continue;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {  // 32 positions in order, a lane each
+        const int from = 8 * q + (lane >> 2), j = lane & 3;
+        const int x = __shfl_sync(0xFFFFFFFFu, t[k].x, from), y = __shfl_sync(0xFFFFFFFFu, t[k].y, from);
+        const int z = __shfl_sync(0xFFFFFFFFu, t[k].z, from), w = __shfl_sync(0xFFFFFFFFu, t[k].w, from);
+        const int v = j == 0 ? x : j == 1 ? y : j == 2 ? z : w;
+        const unsigned act = __ballot_sync(0xFFFFFFFFu, own(v));
+        if (act == 0u) continue;
+        if (own(v)) {
+          const unsigned peers = __match_any_sync(act, v);
+          int* n = mine + (v - lo);
+          const int was = *n, slot = start[v - lo] + was + __popc(peers & ((1u << lane) - 1u));
+          __syncwarp(act);
+          if (lane == __ffs(peers) - 1) *n = was + __popc(peers);
+          a.pos[slot] = base + 128 * k + 32 * q + lane;
+          a.key[slot] = v;
+          a.end[slot] = start[v - lo + 1];
+        }
+        __syncwarp();
       }
-      __syncwarp();
     }
   }
 }
 
 // ------------------------------------------------------------------ backward: sums
-// A CTA takes `chunk` sorted positions, whatever tokens they are, so that frequent tokens
-// cost no more than rare ones. Runs that begin and end in the chunk are finished; of the
-// others the part here is kept: at the chunk's head (a run that began before) or its tail
-// (one that begins here and goes on). The CTAs behind those zero the rows of absent tokens.
+// Each warp takes `chunk` sorted positions, whatever tokens they are, and 256 columns: frequent
+// tokens cost no more than rare ones, and warps that wait for nothing but their own loads
+// keep an SM's memory pipe full (one CTA of 256 threads a chunk of 32 with 70 to 140 registers
+// left 10 to 24 warps an SM: 40009 rows of 1027 fp16 96 us). Runs that begin and end in the
+// chunk are finished; of the others the part here is kept: at the chunk's head (a run that
+// began before) or its tail (one that begins here and goes on). CTAs between those zero the
+// rows of absent tokens: their stores and the sums' waits share every SM.
 template <int DT, bool VEC>
-__global__ void __launch_bounds__(kThreads) embed_sum_kernel(const EmbedBwdArgs a, int sum_ctas) {
-  __shared__ int key[kEmbedMostChunk], pos[kEmbedMostChunk];
+__global__ void __launch_bounds__(kThreads, 8) embed_sum_kernel(const EmbedBwdArgs a, int fills, int blocks) {
   pdl_enter();
-  const int tid = threadIdx.x;
-  if (static_cast<int>(blockIdx.x) >= sum_ctas) {
-    if (blockIdx.y > 0) return;
-    const int lo = (blockIdx.x - sum_ctas) * kFillRows, hi = min(lo + kFillRows, a.V);
+  const int tid = threadIdx.x, lane = tid & 31;
+  // fills of the CTAs, at even distances, zero rows
+  const unsigned before = static_cast<uint64_t>(blockIdx.x) * fills / gridDim.x;
+  if (before != static_cast<unsigned>((blockIdx.x + 1ull) * fills / gridDim.x)) {
+    const int lo = before * kFillRows, hi = min(lo + kFillRows, a.V);
     for (int v = lo; v < hi; ++v)
       if (!((a.present[v >> 5] >> (v & 31)) & 1u)) zero_row(a, v, tid, kThreads);
     return;
   }
-  const int n_valid = *a.n_valid, lo = blockIdx.x * a.chunk, n = min(a.chunk, n_valid - lo);
-  if (n <= 0) return;
-  const bool from_before = lo > 0 && a.key[lo - 1] == a.key[lo];
-  const bool goes_on = lo + n < n_valid && a.key[lo + n] == a.key[lo + n - 1];
-  for (int i = tid; i < n; i += kThreads) key[i] = a.key[lo + i], pos[i] = a.pos[lo + i];
-  __syncthreads();
-  RowSum<DT, VEC> sum(a, (blockIdx.y * kThreads + tid) * kCols);
-  if (sum.c >= a.d) return;
-  bool head = from_before;
-  for (int i = 0; i < n; i += kBatch) {
-    uint4 w[kBatch][RowSum<DT, VEC>::NV];
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k)
-      if (i + k < n) sum.load(pos[i + k], w[k]);
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int j = i + k;
-      if (j >= n) break;
-      sum.add(w[k]);
-      const bool last = j + 1 == n;
-      if (!last && key[j + 1] == key[j]) continue;
-      if (head || (last && goes_on)) {
-        float4* to = reinterpret_cast<float4*>(a.part + (static_cast<size_t>(blockIdx.x) * 2 + (head ? 0 : 1)) * a.part_ld + sum.c);
-        to[0] = make_float4(sum.acc[0], sum.acc[1], sum.acc[2], sum.acc[3]);
-        to[1] = make_float4(sum.acc[4], sum.acc[5], sum.acc[6], sum.acc[7]);
-      } else {
-        sum.put(key[j]);
+  const int chunk = (blockIdx.x - before) / blocks;
+  const int n_valid = *a.n_valid, lo = chunk * a.chunk, n = min(a.chunk, n_valid - lo);
+  const int block = (blockIdx.x - before - chunk * blocks) * kBlockCols + (tid >> 5) * kWarpCols, width = min(kWarpCols, a.d - block);
+  if (n <= 0 || width <= 0) return;  // the whole warp
+  RowSum<DT, VEC> sum(a, block);
+  const bool goes_on = a.end[lo + n - 1] > lo + n;
+  bool head = lo > 0 && a.end[lo - 1] > lo;
+  float* part = a.part + static_cast<size_t>(chunk) * 2 * a.part_ld + block;
+  for (int first = 0; first < n; first += 32) {  // 32 keys and positions, a lane each
+    const int m = min(32, n - first), at = lo + first + lane;
+    const int key = lane < m ? a.key[at] : -1, pos = lane < m ? a.pos[at] : 0;
+    // where a run ends, or the chunk
+    const unsigned ends = __ballot_sync(0xFFFFFFFFu, lane < m && (first + lane + 1 == n || a.end[at] == at + 1));
+    // every row of dy, and every row that a run's sum will be added to, asked for in L2 now: the
+    // accesses below wait for one after the other
+    if (lane < m) {
+      const char* row = reinterpret_cast<const char*>(static_cast<const typename RowSum<DT, VEC>::S*>(a.dy) + static_cast<size_t>(pos) * a.lddy + block);
+      const int bytes = width * static_cast<int>(sizeof(typename RowSum<DT, VEC>::S));
+      for (int b = 0; b < bytes; b += 128) prefetch_line(row + b);
+      prefetch_line(row + bytes - 1);
+      if (a.add && (ends >> lane & 1u)) {
+        const char* out = reinterpret_cast<const char*>(a.dw + static_cast<size_t>(key) * a.lddw + block);
+        for (int b = 0; b < 4 * width; b += 128) prefetch_line(out + b);
+        prefetch_line(out + 4 * width - 1);
       }
-      sum.clear();
-      head = false;
+    }
+    constexpr int kBatch = 4;
+    for (int i = 0; i < m; i += kBatch) {
+      typename RowSum<DT, VEC>::W w[kBatch][RowSum<DT, VEC>::NV];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (i + k < m) sum.load(__shfl_sync(0xFFFFFFFFu, pos, i + k), w[k]);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (i + k >= m) break;
+        sum.add(w[k]);
+        if (!((ends >> (i + k)) & 1u)) continue;
+        const bool tail = first + i + k + 1 == n && goes_on;
+        if (head || tail)
+          sum.keep(part + (head ? 0 : a.part_ld));
+        else
+          sum.put(__shfl_sync(0xFFFFFFFFu, key, i + k));
+        sum.clear();
+        head = false;
+      }
     }
   }
 }
 
 // The runs over several chunks: the tail where the run begins, then the heads of the chunks
-// after it, in order.
+// after it, in order. A CTA takes 256 columns of the runs that begin in four chunks, a warp
+// each; a run of many heads is left to all four warps, a quarter of the heads each, whose
+// sums are joined in order. (The split goes by the heads' number alone.)
+constexpr int kJoinWarps = kThreads / 32, kAlone = 16;
+
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(kThreads) embed_join_kernel(const EmbedBwdArgs a) {
+  __shared__ float4 sums[kJoinWarps - 1][2][32];
+  __shared__ int many[kJoinWarps];  // heads of a run left to all
   pdl_enter();
-  const int n_valid = *a.n_valid, tid = threadIdx.x, lane = tid & 31;
-  const int lo = blockIdx.x * a.chunk, next = lo + a.chunk;
-  if (next >= n_valid) return;
-  const int v = a.key[next];
-  // the run begins in this chunk and goes on in the next
-  if (a.key[next - 1] != v || (lo > 0 && a.key[lo - 1] == v)) return;
-  int heads = 0;  // chunks after this one that begin inside the run
-  for (;; heads += 32) {
-    const long i = next + static_cast<long>(heads + lane) * a.chunk;
-    const unsigned m = __ballot_sync(0xFFFFFFFFu, i < n_valid && a.key[i] == v);
-    if (m != 0xFFFFFFFFu) {
-      heads += __ffs(~m) - 1;
-      break;
+  const int n_valid = *a.n_valid, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, block = blockIdx.y * kWarpCols;
+  auto next_of = [&](long chunk) { return (chunk + 1) * a.chunk; };
+  auto part_of = [&](long chunk) { return a.part + static_cast<size_t>(chunk) * 2 * a.part_ld + block; };
+  RowSum<DT, VEC> sum(a, block);
+  {
+    const long chunk = static_cast<long>(blockIdx.x) * kJoinWarps + warp, lo = chunk * a.chunk, next = next_of(chunk);
+    int heads = 0;  // chunks after this one that begin inside its run
+    if (next < n_valid) {
+      const int end = a.end[next - 1], before = lo > 0 ? a.end[lo - 1] : 0;  // (a run is known by its end)
+      if (end > next && before != end) heads = static_cast<int>((end - next + a.chunk - 1) / a.chunk);
+    }
+    if (lane == 0) many[warp] = heads > kAlone ? heads : 0;
+    if (heads > 0 && heads <= kAlone) {
+      const float* part = part_of(chunk);
+      sum.join(part + a.part_ld);
+#pragma unroll 4
+      for (int h = 1; h <= heads; ++h) sum.join(part + static_cast<size_t>(h) * 2 * a.part_ld);
+      if (sum.c < a.d) sum.put(a.key[next]);
     }
   }
-  RowSum<DT, VEC> sum(a, (blockIdx.y * kThreads + tid) * kCols);
-  if (sum.c >= a.d) return;
-  auto add = [&](const float4& p, const float4& q) {
-    sum.acc[0] += p.x, sum.acc[1] += p.y, sum.acc[2] += p.z, sum.acc[3] += p.w;
-    sum.acc[4] += q.x, sum.acc[5] += q.y, sum.acc[6] += q.z, sum.acc[7] += q.w;
-  };
-  const float4* tail = reinterpret_cast<const float4*>(a.part + (static_cast<size_t>(blockIdx.x) * 2 + 1) * a.part_ld + sum.c);
-  add(tail[0], tail[1]);
-  const float* head = a.part + (static_cast<size_t>(blockIdx.x) + 1) * 2 * a.part_ld + sum.c;
+  __syncthreads();
+  for (int q = 0; q < kJoinWarps; ++q) {
+    const int heads = many[q];
+    if (heads == 0) continue;
+    const long chunk = static_cast<long>(blockIdx.x) * kJoinWarps + q;
+    const int each = (heads + kJoinWarps - 1) / kJoinWarps, from = min(heads, warp * each), to = min(heads, from + each);
+    const float* part = part_of(chunk);
+    sum.clear();
+    if (warp == 0) sum.join(part + a.part_ld);
 #pragma unroll 8
-  for (int h = 0; h < heads; ++h) {
-    const float4* p = reinterpret_cast<const float4*>(head + static_cast<size_t>(h) * 2 * a.part_ld);
-    add(p[0], p[1]);
+    for (int h = from + 1; h <= to; ++h) sum.join(part + static_cast<size_t>(h) * 2 * a.part_ld);
+    if (warp > 0) {
+      sums[warp - 1][0][lane] = make_float4(sum.acc[0], sum.acc[1], sum.acc[2], sum.acc[3]);
+      sums[warp - 1][1][lane] = make_float4(sum.acc[4], sum.acc[5], sum.acc[6], sum.acc[7]);
+    }
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll
+      for (int w = 0; w < kJoinWarps - 1; ++w) sum.join(sums[w][0][lane], sums[w][1][lane]);
+      if (sum.c < a.d) sum.put(a.key[next_of(chunk)]);
+    }
+    __syncthreads();
   }
-  sum.put(v);
 }
 
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -404,20 +495,18 @@ cudaError_t embed_fwd(const EmbedFwdArgs& a, bool vec, cudaStream_t s) {
   return e;
 }
 
-template <int DT>
-cudaError_t embed_bwd(EmbedBwdArgs a, cudaStream_t s) {
-  const bool vec = rows16(a.dy, a.lddy, DT) && a.d % Elem<DT>::E == 0;
+template <int DT, bool VEC>
+cudaError_t embed_bwd_as(EmbedBwdArgs a, cudaStream_t s) {
   const unsigned blocks = (a.d + kBlockCols - 1) / kBlockCols;
-  const int fill = a.add ? 0 : (a.V + kFillRows - 1) / kFillRows;
+  const int fill = a.add ? 0 : (a.V + kFillRows - 1) / kFillRows;  // CTAs that zero rows
   cudaError_t e;
   if (a.T <= kFewTokens) {
-    // (the fill's CTAs past the first column block have nothing to do)
-    e = launch(vec ? embed_bwd_few_kernel<DT, true> : embed_bwd_few_kernel<DT, false>, dim3(a.T + fill, blocks), dim3(kThreads), 0, s, a);
+    e = launch(embed_bwd_few_kernel<DT, VEC>, dim3(a.T + fill, blocks), dim3(kThreads), 0, s, a);
     trace_mark(s, "embed_bwd_few");
     return e;
   }
   const int ctas = (a.V + a.range - 1) / a.range;
-  const size_t smem = static_cast<size_t>(kSortWarps) * a.range * sizeof(int);
+  const size_t smem = (static_cast<size_t>(kSortWarps + 1) * a.range + 1) * sizeof(int);
   e = allow_smem(embed_sort_kernel, smem);
   if (e != cudaSuccess) return e;
   if (a.add) a.present = nullptr;
@@ -425,12 +514,16 @@ cudaError_t embed_bwd(EmbedBwdArgs a, cudaStream_t s) {
   trace_mark(s, "embed_sort");
   if (e != cudaSuccess) return e;
   const int chunks = (a.T + a.chunk - 1) / a.chunk;
-  e = launch(vec ? embed_sum_kernel<DT, true> : embed_sum_kernel<DT, false>, dim3(chunks + fill, blocks), dim3(kThreads), 0, s, a, chunks);
+  e = launch(embed_sum_kernel<DT, VEC>, dim3(chunks * blocks + fill), dim3(kThreads), 0, s, a, fill, static_cast<int>(blocks));
   trace_mark(s, "embed_sum");
   if (e != cudaSuccess || chunks < 2) return e;
-  e = launch(vec ? embed_join_kernel<DT, true> : embed_join_kernel<DT, false>, dim3(chunks - 1, blocks), dim3(kThreads), 0, s, a);
+  e = launch(embed_join_kernel<DT, VEC>, dim3((chunks + kJoinWarps - 1) / kJoinWarps, (a.d + kWarpCols - 1) / kWarpCols), dim3(kThreads), 0, s, a);
   trace_mark(s, "embed_join");
   return e;
+}
+template <int DT>
+cudaError_t embed_bwd(const EmbedBwdArgs& a, cudaStream_t s) {
+  return rows16(a.dy, a.lddy, DT) && a.d % Elem<DT>::E == 0 ? embed_bwd_as<DT, true>(a, s) : embed_bwd_as<DT, false>(a, s);
 }
 
 }  // namespace
@@ -440,9 +533,9 @@ EmbedBwdPlan embed_bwd_plan(int T, int V, int d) {
   if (T <= kFewTokens) return p;
   // tokens of a sorting CTA: whole words of the bits that say which occur
   p.range = std::min(kMostRange, ((V + 151) / 152 + 31) / 32 * 32);
-  p.chunk = 32;
-  while (p.chunk < kEmbedMostChunk && T / p.chunk > 4096) p.chunk *= 2;
-  p.part_ld = (d + kCols - 1) / kCols * kCols;
+  p.chunk = 16;
+  while (T / p.chunk > 4096) p.chunk *= 2;
+  p.part_ld = (d + kWarpCols - 1) / kWarpCols * kWarpCols;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t was = at;
@@ -450,6 +543,7 @@ EmbedBwdPlan embed_bwd_plan(int T, int V, int d) {
     return was;
   };
   p.key = take(sizeof(int) * static_cast<size_t>(T)), p.pos = take(sizeof(int) * static_cast<size_t>(T));
+  p.end = take(sizeof(int) * static_cast<size_t>(T));
   p.n_valid = take(sizeof(int));
   p.present = take((static_cast<size_t>(V) + kMostRange) / 8);
   p.part = take(sizeof(float) * 2 * static_cast<size_t>(p.part_ld) * ((T + p.chunk - 1) / p.chunk));
@@ -471,7 +565,7 @@ cudaError_t launch_embed_bwd(const EmbedBwdArgs& given, void* ws, cudaStream_t s
   const EmbedBwdPlan p = embed_bwd_plan(a.T, a.V, a.d);
   uint8_t* w = static_cast<uint8_t*>(ws);
   if (p.bytes > 0) {
-    a.key = reinterpret_cast<int*>(w + p.key), a.pos = reinterpret_cast<int*>(w + p.pos);
+    a.key = reinterpret_cast<int*>(w + p.key), a.pos = reinterpret_cast<int*>(w + p.pos), a.end = reinterpret_cast<int*>(w + p.end);
     a.n_valid = reinterpret_cast<int*>(w + p.n_valid), a.present = reinterpret_cast<unsigned*>(w + p.present);
     a.part = reinterpret_cast<float*>(w + p.part);
     a.range = p.range, a.chunk = p.chunk, a.part_ld = p.part_ld;

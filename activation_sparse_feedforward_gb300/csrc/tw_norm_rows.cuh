@@ -37,6 +37,12 @@ TW_DEV float fp8_scale(float most) {
   const float s = most * (1.f / kFp8Max);
   return s < kFp8LeastScale ? kFp8LeastScale : s;
 }
+// 1 / scale (hardware approximation to about 1 ulp; e4m3 has 20 bits fewer)
+TW_DEV float reciprocal(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
 // two values as e4m3, round to nearest even, NaN kept
 TW_DEV uint32_t fp8x2(float2 v) { return __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3); }
 
@@ -295,10 +301,17 @@ TW_DEV void team_sync(int team) {
 
 // CTAs an SM of a forward kernel of so many threads: about 800 threads, so that while a
 // team waits for the two sums over its row, the other CTAs' rows go on.
-constexpr int fwd_ctas(int threads) { return threads > 448 ? 1 : threads > 320 ? 2 : 800 / threads; }
+// RMS norm's rows of whole vectors of 16 bits: 1024 threads, one sum a row leaves less to
+// wait for (8191 x 8192 into e4m3 with a scale a row 36 us, at 800 threads 41; 16384 x 2048
+// 22 against 23; but off 16 bytes 54 against 42, and fp32 gains nothing).
+constexpr int fwd_ctas(int threads, bool more) {
+  if (more) return threads > 512 ? 1 : 1024 / threads;
+  return threads > 448 ? 1 : threads > 320 ? 2 : 800 / threads;
+}
+constexpr bool fwd_more(int kind, int dtype, bool vec, int depth) { return kind != LAYER_NORM && dtype != TW_F32 && vec && depth > 0; }
 
 template <int DT, int VPT, bool VEC, int DEPTH, int TPR, int MAXT, int KIND>
-__global__ void __launch_bounds__(MAXT, fwd_ctas(MAXT)) norm_fwd_kernel(const NormFwdArgs a) {
+__global__ void __launch_bounds__(MAXT, fwd_ctas(MAXT, fwd_more(KIND, DT, VEC, DEPTH))) norm_fwd_kernel(const NormFwdArgs a) {
   constexpr bool RMS = KIND != LAYER_NORM;
   using M = RowMap<DT, VPT, VEC, TPR>;
   using S = typename M::S;
@@ -385,7 +398,7 @@ __global__ void __launch_bounds__(MAXT, fwd_ctas(MAXT)) norm_fwd_kernel(const No
         if constexpr (KIND == RMS_FP8_ROW) {
           const float scale = fp8_scale(most * rstd);
           if (tid == 0) a.scales[row] = scale;
-          const float inv = 1.f / scale;
+          const float inv = reciprocal(scale);
 #pragma unroll
           for (int i = 0; i < NP; ++i) v[i] = mul2(v[i], both(inv));
         } else {
@@ -399,7 +412,7 @@ __global__ void __launch_bounds__(MAXT, fwd_ctas(MAXT)) norm_fwd_kernel(const No
             const float scale = fp8_scale(warp_max_nan(g, kLanes));
             const int c = m.col(k * E);
             if (c < a.d && c % kFp8Group == 0) a.scales[r * groups + c / kFp8Group] = scale;
-            const float inv = 1.f / scale;
+            const float inv = reciprocal(scale);
 #pragma unroll
             for (int e = k * E / 2; e < (k + 1) * E / 2; ++e) v[e] = mul2(v[e], both(inv));
           }
@@ -750,7 +763,7 @@ cudaError_t norm_fwd_ring(const NormFwdArgs& a, cudaStream_t s) {
   const size_t smem = ring_bytes(DT, VPT, Team{TPR, kTeams}, 3, a.res != nullptr ? 2 : 1, VEC);
   // as many CTAs as stay resident
   const int fit = static_cast<int>(kSmemMost / (smem + 6 * 1024));
-  const int per_sm = std::max(1, std::min(fwd_ctas(MAXT), fit));
+  const int per_sm = std::max(1, std::min(fwd_ctas(MAXT, fwd_more(KIND, DT, VEC, 3)), fit));
   return launch_norm(norm_fwd_kernel<DT, VPT, VEC, 3, TPR, MAXT, KIND>,
                      std::min((a.T + kTeams - 1) / kTeams, device_sm_count() * per_sm), Team{TPR, kTeams}, smem,
                      "norm_fwd", a, s);

@@ -132,9 +132,19 @@ struct RowSum {
     acc[0] += p.x, acc[1] += p.y, acc[2] += p.z, acc[3] += p.w;
     acc[4] += q.x, acc[5] += q.y, acc[6] += q.z, acc[7] += q.w;
   }
-  TW_DEV void join(const float* part) {
+  // n parts, `step` floats apart, in order; N on their way at once
+  template <int N>
+  TW_DEV void join(const float* part, int n, size_t step) {
     const float4* from = reinterpret_cast<const float4*>(part) + 2 * (threadIdx.x & 31);
-    join(from[0], from[1]);
+    for (int i = 0; i < n; i += N) {
+      float4 p[N], q[N];
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (i + k < n) p[k] = from[(i + k) * step / 4], q[k] = from[(i + k) * step / 4 + 1];
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (i + k < n) join(p[k], q[k]);
+    }
   }
   // the finished sum of token v, into its row
   TW_DEV void put(int v) const {
@@ -171,13 +181,13 @@ TW_DEV void zero_row(const EmbedBwdArgs& a, int v, int tid, int threads) {
   }
 }
 
-constexpr int kThreads = 128, kBlockCols = kThreads * kCols;  // of the kernels below
+constexpr int kThreads = 256, kBlockCols = kThreads * kCols;  // of the kernels below
 
 // ------------------------------------------------------------------ backward of few tokens
 // One launch and no sort: the CTA of position i looks through the tokens; where its own
 // occurs before i it has nothing to do, else it sums all rows of the token. The CTAs behind
 // those zero the rows of the tokens that do not occur, kFillRows each.
-constexpr int kFewTokens = 512, kFillRows = 64;
+constexpr int kFewTokens = 512, kFillRows = 8;
 
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(kThreads) embed_bwd_few_kernel(const EmbedBwdArgs a) {
@@ -363,23 +373,23 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedBwd
 // keep an SM's memory pipe full (one CTA of 256 threads a chunk of 32 with 70 to 140 registers
 // left 10 to 24 warps an SM: 40009 rows of 1027 fp16 96 us). Runs that begin and end in the
 // chunk are finished; of the others the part here is kept: at the chunk's head (a run that
-// began before) or its tail (one that begins here and goes on). CTAs between those zero the
-// rows of absent tokens: their stores and the sums' waits share every SM.
+// began before) or its tail (one that begins here and goes on). The CTAs behind those zero
+// the rows of absent tokens, eight each (16384 tokens of 131072 x 2048, all of it: 176 us; with
+// CTAs of both kinds in turn 190, of 128 threads 182, 64 rows each 187).
 template <int DT, bool VEC>
-__global__ void __launch_bounds__(kThreads, 8) embed_sum_kernel(const EmbedBwdArgs a, int fills, int blocks) {
+__global__ void __launch_bounds__(kThreads, 4) embed_sum_kernel(const EmbedBwdArgs a, int fills, int blocks) {
   pdl_enter();
   const int tid = threadIdx.x, lane = tid & 31;
-  // fills of the CTAs, at even distances, zero rows
-  const unsigned before = static_cast<uint64_t>(blockIdx.x) * fills / gridDim.x;
-  if (before != static_cast<unsigned>((blockIdx.x + 1ull) * fills / gridDim.x)) {
-    const int lo = before * kFillRows, hi = min(lo + kFillRows, a.V);
+  const int sums = gridDim.x - fills;
+  if (static_cast<int>(blockIdx.x) >= sums) {
+    const int lo = (blockIdx.x - sums) * kFillRows, hi = min(lo + kFillRows, a.V);
     for (int v = lo; v < hi; ++v)
       if (!((a.present[v >> 5] >> (v & 31)) & 1u)) zero_row(a, v, tid, kThreads);
     return;
   }
-  const int chunk = (blockIdx.x - before) / blocks;
+  const int chunk = blockIdx.x / blocks;
   const int n_valid = *a.n_valid, lo = chunk * a.chunk, n = min(a.chunk, n_valid - lo);
-  const int block = (blockIdx.x - before - chunk * blocks) * kBlockCols + (tid >> 5) * kWarpCols, width = min(kWarpCols, a.d - block);
+  const int block = (blockIdx.x - chunk * blocks) * kBlockCols + (tid >> 5) * kWarpCols, width = min(kWarpCols, a.d - block);
   if (n <= 0 || width <= 0) return;  // the whole warp
   RowSum<DT, VEC> sum(a, block);
   const bool goes_on = a.end[lo + n - 1] > lo + n;
@@ -427,8 +437,8 @@ __global__ void __launch_bounds__(kThreads, 8) embed_sum_kernel(const EmbedBwdAr
 }
 
 // The runs over several chunks: the tail where the run begins, then the heads of the chunks
-// after it, in order. A CTA takes 256 columns of the runs that begin in four chunks, a warp
-// each; a run of many heads is left to all four warps, a quarter of the heads each, whose
+// after it, in order. A CTA takes 256 columns of the runs that begin in eight chunks, a warp
+// each; a run of many heads is left to all eight warps, an eighth of the heads each, whose
 // sums are joined in order. (The split goes by the heads' number alone.)
 constexpr int kJoinWarps = kThreads / 32, kAlone = 16;
 
@@ -451,9 +461,8 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const EmbedBwdArgs
     if (lane == 0) many[warp] = heads > kAlone ? heads : 0;
     if (heads > 0 && heads <= kAlone) {
       const float* part = part_of(chunk);
-      sum.join(part + a.part_ld);
-#pragma unroll 4
-      for (int h = 1; h <= heads; ++h) sum.join(part + static_cast<size_t>(h) * 2 * a.part_ld);
+      sum.template join<1>(part + a.part_ld, 1, 0);
+      sum.template join<4>(part + 2 * a.part_ld, heads, 2 * static_cast<size_t>(a.part_ld));
       if (sum.c < a.d) sum.put(a.key[next]);
     }
   }
@@ -465,9 +474,8 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const EmbedBwdArgs
     const int each = (heads + kJoinWarps - 1) / kJoinWarps, from = min(heads, warp * each), to = min(heads, from + each);
     const float* part = part_of(chunk);
     sum.clear();
-    if (warp == 0) sum.join(part + a.part_ld);
-#pragma unroll 8
-    for (int h = from + 1; h <= to; ++h) sum.join(part + static_cast<size_t>(h) * 2 * a.part_ld);
+    if (warp == 0) sum.template join<1>(part + a.part_ld, 1, 0);
+    sum.template join<8>(part + static_cast<size_t>(from + 1) * 2 * a.part_ld, to - from, 2 * static_cast<size_t>(a.part_ld));
     if (warp > 0) {
       sums[warp - 1][0][lane] = make_float4(sum.acc[0], sum.acc[1], sum.acc[2], sum.acc[3]);
       sums[warp - 1][1][lane] = make_float4(sum.acc[4], sum.acc[5], sum.acc[6], sum.acc[7]);

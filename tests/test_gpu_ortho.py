@@ -240,3 +240,67 @@ def test_one_shot():
     out, status = tw.orthogonalize(g, scale=2.0)
     assert status.item() == 0
     _check(out, 2.0 * updates.newton_schulz(_f64(g)), BF16)
+
+
+def _exact(g, steps=5, coefficients=updates.COEFFICIENTS):
+    """updates.newton_schulz on the GPU, for sizes that numpy would take long over."""
+    x = g.double()
+    x = x / x.norm()
+    a, b, c = coefficients
+    for _ in range(steps):
+        gram = x.T @ x if x.shape[0] >= x.shape[1] else x @ x.T
+        p = b * gram + c * gram @ gram
+        x = a * x + (x @ p if x.shape[0] >= x.shape[1] else p @ x)
+    return x.cpu().numpy()
+
+
+# tall and thin (many slices of a tile), more tiles than pairs of SMs, the layer's own shapes
+@pytest.mark.parametrize("m,n,count", [(70000, 40, 1), (40, 70000, 2), (9000, 300, 1), (3000, 2900, 1), (5632, 2048, 1), (2048, 8192, 2)])
+def test_large(m, n, count):
+    gen = torch.Generator(device="cuda").manual_seed(m + n)
+    gs = [torch.randn(m, n, generator=gen, device="cuda") * torch.exp(torch.randn(m, 1, generator=gen, device="cuda")) for _ in range(count)]
+    op = tw.Orthogonalize(m, n, count=count, momentum=0.0)
+    outs = op(gs)
+    torch.cuda.synchronize()
+    tw.raise_if_device_error(op.status)
+    for g, o in zip(gs, outs):
+        _check(o, _exact(g), BF16)
+
+
+def test_two_at_once_on_two_streams():
+    """Neither waits for the other's units, and neither is disturbed."""
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    sizes = [(2000, 1500), (1300, 2100)]
+    gs = [torch.randn(*s, generator=gen, device="cuda") for s in sizes]
+    ops = [tw.Orthogonalize(*s, momentum=0.0) for s in sizes]
+    want = [op(g).clone() for op, g in zip(ops, gs)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[], []]
+    for _ in range(12):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                outs[i].append(ops[i](gs[i]).clone())
+    torch.cuda.synchronize()
+    for i in range(2):
+        tw.raise_if_device_error(ops[i].status)
+        assert all(torch.equal(o, want[i]) for o in outs[i])
+
+
+def test_next_to_other_work_on_the_gpu():
+    """Long kernels on another stream hold SMs back from the products."""
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    g = torch.randn(2048, 1024, generator=gen, device="cuda")
+    op = tw.Orthogonalize(2048, 1024, momentum=0.0)
+    want = op(g).clone()
+    a = torch.randn(8192, 8192, device="cuda", dtype=BF16)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for _ in range(30):
+            b = a @ a
+    for _ in range(10):
+        assert torch.equal(op(g), want)
+    torch.cuda.synchronize()
+    tw.raise_if_device_error(op.status)
+    assert b.shape == a.shape

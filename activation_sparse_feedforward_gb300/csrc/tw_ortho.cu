@@ -753,20 +753,21 @@ struct NsInArgs {
   int gtype, count, rows, cols;  // of g as given
   float mu;
   int nesterov;
-  float* norms;                // [count][kNormBlocks][3]
+  double* norms;               // [count][kNormBlocks]
   int* arrived;                // counters to clear
   int n_arrived;
   uint16_t *hi, *lo;           // [count][mp][np]
   int mp, np, klog2;
   int first;                   // the launch's first matrix
   bool vec;                    // g's and m's rows are whole vectors of 8 elements on 16 bytes
+  bool flat;                   // g's and m's rows follow each other: the sums take them as one, on 16 bytes
 };
 
 constexpr int kNormBlocks = 304, kNormThreads = 512;
 
 // U at element (r, c); store: writes the new momentum
 template <int GT>
-TW_DEV float update_of(const NsInArgs& a, int mat, int r, int c, bool store) {
+TW_DEV float update_of(const NsInArgs& a, int mat, int r, long c, bool store) {
   using S = typename Elem<GT>::S;
   const float g = Elem<GT>::get(static_cast<const S*>(a.g[mat])[static_cast<size_t>(r) * a.ldg + c]);
   if (a.m[mat] == nullptr) return g;
@@ -775,11 +776,11 @@ TW_DEV float update_of(const NsInArgs& a, int mat, int r, int c, bool store) {
   if (store) *m = v = fmaf(a.mu, v, g);
   return a.nesterov ? fmaf(a.mu, v, g) : v;
 }
-// The same for the 8 elements from c on; vec: rows of whole vectors on 16 bytes. Elements
-// past the row are 0.
+// The same for the 8 elements from c on, on 16 bytes (or, where rows are not of whole vectors
+// there and nothing is stored, anywhere; elements past the row are then 0).
 template <int GT>
-TW_DEV void update8(const NsInArgs& a, int mat, int r, int c, bool store, float (&u)[8]) {
-  if (!a.vec) {
+TW_DEV void update8(const NsInArgs& a, int mat, int r, long c, bool store, float (&u)[8]) {
+  if (!a.vec && !store) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) u[i] = c + i < a.cols ? update_of<GT>(a, mat, r, c + i, store) : 0.f;
     return;
@@ -817,26 +818,40 @@ __global__ void __launch_bounds__(kNormThreads) ns_norm_kernel(const NsInArgs a)
   pdl_enter();
   const int mat = a.first + blockIdx.y;
   NormSums s = {0.f, 0.f, 0.f};
-  const unsigned per_row = a.vec ? a.cols / 8 : a.cols;
-  const long total = static_cast<long>(a.rows) * per_row, step = static_cast<long>(gridDim.x) * kNormThreads;
-  long i = static_cast<long>(blockIdx.x) * kNormThreads + threadIdx.x;
-  int r = static_cast<int>(i / per_row), c = static_cast<int>(i - static_cast<long>(r) * per_row);
-  const int dr = static_cast<int>(step / per_row), dc = static_cast<int>(step - static_cast<long>(dr) * per_row);
-  auto next = [&] {
-    i += step, r += dr, c += dc;
-    if (c >= static_cast<int>(per_row)) c -= per_row, ++r;
-  };
-  if (a.vec) {
+  const long step = static_cast<long>(gridDim.x) * kNormThreads, first = static_cast<long>(blockIdx.x) * kNormThreads + threadIdx.x;
+  if (a.flat) {
+    const long all = static_cast<long>(a.rows) * a.cols;
 #pragma unroll 2
-    for (; i < total; next()) {
+    for (long i = first; i < all / 8; i += step) {
       float u[8];
-      update8<GT>(a, mat, r, c * 8, true, u);
+      update8<GT>(a, mat, 0, i * 8, true, u);
 #pragma unroll
       for (int k = 0; k < 8; ++k) add_square(s, u[k]);
     }
+    if (first < all % 8) add_square(s, update_of<GT>(a, mat, 0, all / 8 * 8 + first, true));
   } else {
-#pragma unroll 4
-    for (; i < total; next()) add_square(s, update_of<GT>(a, mat, r, c, true));
+    const int one = a.vec ? 8 : 1;  // elements of a row at once
+    const unsigned per_row = a.cols / one;
+    const long total = static_cast<long>(a.rows) * per_row;
+    long i = first;
+    int r = static_cast<int>(i / per_row), c = static_cast<int>(i - static_cast<long>(r) * per_row);
+    const int dr = static_cast<int>(step / per_row), dc = static_cast<int>(step - static_cast<long>(dr) * per_row);
+    auto next = [&] {
+      i += step, r += dr, c += dc;
+      if (c >= static_cast<int>(per_row)) c -= per_row, ++r;
+    };
+    if (a.vec) {
+#pragma unroll 2
+      for (; i < total; next()) {
+        float u[8];
+        update8<GT>(a, mat, r, c * 8, true, u);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) add_square(s, u[k]);
+      }
+    } else {
+#pragma unroll 8
+      for (; i < total; next()) add_square(s, update_of<GT>(a, mat, r, c, true));
+    }
   }
   s.small = warp_sum(s.small), s.mid = warp_sum(s.mid), s.big = warp_sum(s.big);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
@@ -844,35 +859,34 @@ __global__ void __launch_bounds__(kNormThreads) ns_norm_kernel(const NsInArgs a)
   if (threadIdx.x == 0) {
     for (int w = 1; w < kNormThreads / 32; ++w)
       s.small += red[w].small, s.mid += red[w].mid, s.big += red[w].big;
-    float* to = a.norms + (static_cast<size_t>(mat) * kNormBlocks + blockIdx.x) * 3;
-    to[0] = s.small, to[1] = s.mid, to[2] = s.big;
+    a.norms[static_cast<size_t>(mat) * kNormBlocks + blockIdx.x] =
+        static_cast<double>(s.small) * 0x1p-180 + static_cast<double>(s.mid) + static_cast<double>(s.big) * 0x1p160;
   }
   if (mat == 0)
-    for (int k = blockIdx.x * kNormThreads + threadIdx.x; k < a.n_arrived; k += gridDim.x * kNormThreads) a.arrived[k] = 0;
+    for (long k = first; k < a.n_arrived; k += step) a.arrived[k] = 0;
 }
 
-// 2^k / |U|_F from the sums, by every CTA (256 threads) in the same order; as two factors, so
-// that neither they nor a product by one of them overflows.
+// 2^k / |U|_F from the sums, by one warp of every CTA in the same order (the SM adds two
+// doubles a clock: all eight warps together took 7 us); as two factors, so that neither they
+// nor a product by one of them overflows. The root of the sum's mantissa is fp32's: 2^-22 of
+// a matrix's every value.
 TW_DEV float2 start_factor(const NsInArgs& a, int mat, int norm_blocks) {
-  __shared__ double sum[256];
   __shared__ float2 factor;
-  const int tid = threadIdx.x;
-  double s = 0.0;
-  for (int i = tid; i < norm_blocks; i += 256) {
-    const float* n = a.norms + (static_cast<size_t>(mat) * kNormBlocks + i) * 3;
-    s += static_cast<double>(n[0]) * 0x1p-180 + static_cast<double>(n[1]) + static_cast<double>(n[2]) * 0x1p160;
-  }
-  sum[tid] = s;
-  __syncthreads();
-  if (tid < 32) {
-    for (int i = tid + 32; i < 256; i += 32) s += sum[i];
+  if (threadIdx.x < 32) {
+    double s = 0.0;
+    for (int i = threadIdx.x; i < norm_blocks; i += 32) s += a.norms[static_cast<size_t>(mat) * kNormBlocks + i];
+#pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    if (tid == 0) {
-      const double f = s > 0.0 ? ldexp(1.0 / sqrt(s), a.klog2) : (s == 0.0 ? 0.0 : s);
-      int e = 0;
-      if (f > 0.0 && f < 1e300) e = ilogb(f) / 2;
-      factor = make_float2(static_cast<float>(ldexp(1.0, e)), static_cast<float>(ldexp(f, -e)));
+    float2 f = make_float2(1.f, s == 0.0 || s > 0.0 ? 0.f : __int_as_float(0x7FC00000));
+    if (s > 0.0 && s < 0x1p1000) {
+      // s = m 4^e, 1 <= m < 4
+      const int bits = __double2hiint(s), e = ((bits >> 20) - 1023) >> 1;
+      const float m = static_cast<float>(__hiloint2double(bits - (e << 21), __double2loint(s)));
+      const int power = a.klog2 - e, half = power >> 1;
+      auto pow2 = [](int n) { return __int_as_float((n + 127) << 23); };
+      f = make_float2(pow2(half), rsqrtf(m) * pow2(power - half));
     }
+    if (threadIdx.x == 0) factor = f;
   }
   __syncthreads();
   return factor;
@@ -920,8 +934,9 @@ __global__ void __launch_bounds__(256) ns_start_wide_kernel(const NsInArgs a, in
   const float2 f = start_factor(a, mat, norm_blocks);
   const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;  // in the padded matrix
   const int lane = tid & 63, first = tid >> 6;
-#pragma unroll 4
-  for (int i = first; i < 64; i += 4) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const int i = first + 4 * k;
     const int r = c0 + i, c = r0 + lane;  // in g
     t[lane][i] = r < a.rows && c < a.cols ? update_of<GT>(a, mat, r, c, false) * f.x * f.y : 0.f;
   }
@@ -986,7 +1001,7 @@ Layout layout(int m, int n, int count) {
   l.part = take(static_cast<size_t>(count) * l.slots * kTile * kTile * 4);
   l.arrived = take(static_cast<size_t>(count) * l.slots * 2 * kEpiWarps * 4);
   l.counters = take(static_cast<size_t>(3 * count + 1) * 4);
-  l.norms = take(static_cast<size_t>(count) * kNormBlocks * 3 * 4);
+  l.norms = take(static_cast<size_t>(count) * kNormBlocks * sizeof(double));
   l.bytes = at;
   return l;
 }
@@ -1029,14 +1044,16 @@ cudaError_t launch_ortho(const OrthoArgs& o, cudaStream_t s) {
   const int k = std::min(14, std::max(0, static_cast<int>(std::lround(0.5 * std::log2(static_cast<double>(o.m) * o.n)))));
 
   NsInArgs in = {};
-  bool vec = o.n % 8 == 0 && o.ldg * static_cast<int64_t>(o.gtype == TW_F32 ? 4 : 2) % 16 == 0 && o.ldbuf % 4 == 0;
+  bool on16 = true;
   for (int i = 0; i < o.count; ++i) {
     in.g[i] = o.g[i], in.m[i] = o.buf != nullptr ? o.buf[i] : nullptr;
-    vec = vec && ((reinterpret_cast<uintptr_t>(in.g[i]) | reinterpret_cast<uintptr_t>(in.m[i])) & 15u) == 0;
+    on16 = on16 && ((reinterpret_cast<uintptr_t>(in.g[i]) | reinterpret_cast<uintptr_t>(in.m[i])) & 15u) == 0;
   }
   in.ldg = o.ldg, in.ldm = o.ldbuf, in.gtype = o.gtype, in.count = o.count, in.rows = o.m, in.cols = o.n;
-  in.mu = o.mu, in.nesterov = o.nesterov, in.vec = vec;
-  in.norms = reinterpret_cast<float*>(ws + l.norms);
+  in.mu = o.mu, in.nesterov = o.nesterov;
+  in.vec = on16 && o.n % 8 == 0 && o.ldg * static_cast<int64_t>(o.gtype == TW_F32 ? 4 : 2) % 16 == 0 && o.ldbuf % 4 == 0;
+  in.flat = on16 && (o.m == 1 || (o.ldg == o.n && (o.buf == nullptr || o.ldbuf == o.n)));
+  in.norms = reinterpret_cast<double*>(ws + l.norms);
   in.arrived = reinterpret_cast<int*>(ws + l.arrived), in.n_arrived = l.words();
   in.hi = at16(l.hi0), in.lo = at16(l.lo), in.mp = l.mp, in.np = l.np, in.klog2 = k;
   cudaError_t e = o.gtype == TW_F32    ? way_in<TW_F32>(in, wide, s)

@@ -167,6 +167,23 @@ tw_status check_ortho(int m, int n, int count) {
   return std::max(m, n) <= (1 << 20) && std::min(m, n) <= 16384 && count <= TW_ORTHO_MOST ? TW_OK : TW_EUNSUPPORTED;
 }
 
+// Whether two [m, n] matrices share an element: of one type's size and row stride their
+// columns may lie between each other's; else any memory between their ends counts.
+struct Placed {
+  const void* p;
+  int64_t ld;
+  uint64_t size;  // of an element
+};
+bool overlap(const Placed& a, const Placed& b, int64_t m, int64_t n) {
+  const uint64_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  const uint64_t end_x = x + a.size * ((m - 1) * a.ld + n), end_y = y + b.size * ((m - 1) * b.ld + n);
+  if (x >= end_y || y >= end_x) return false;
+  const uint64_t apart = x < y ? y - x : x - y;
+  if (a.ld != b.ld || a.size != b.size || apart % a.size != 0) return true;
+  const int64_t elements = static_cast<int64_t>(apart / a.size), rows = elements / a.ld, column = elements % a.ld;
+  return column < n || (a.ld - column < n && rows + 1 < m);
+}
+
 // ------------------------------------------------------------------ workspace layouts
 struct FwdWs {
   uint16_t* X;
@@ -1058,6 +1075,14 @@ tw_status tw_orthogonalize(const void* const* grads, int64_t ldg, int gtype, flo
     }
     if (st != TW_OK) return st;
   }
+  const uint64_t gsize = gtype == TW_F32 ? 4 : 2, osize = otype == TW_F32 ? 4 : 2;
+  for (int i = 0; i < count; ++i)
+    for (int j = 0; j < count; ++j) {
+      if (j < i && overlap({out[i], ldo, osize}, {out[j], ldo, osize}, m, n)) return TW_EINVAL;
+      if (buffers == nullptr) continue;
+      if (j < i && overlap({buffers[i], ldbuf, 4}, {buffers[j], ldbuf, 4}, m, n)) return TW_EINVAL;
+      if (overlap({buffers[i], ldbuf, 4}, {grads[j], ldg, gsize}, m, n)) return TW_EINVAL;
+    }
   st = check_ptrs({ws});
   if (st == TW_OK) st = check_side({dev_status}, {});
   if (st != TW_OK) return st;

@@ -16,6 +16,8 @@ Modules
              formats (the method is exact: it only skips multiplications by zero).
 ``neurons``  per-neuron activity counts and the dead-neuron re-initialisation of
              the gate projection (a counter-based SplitMix64 / Irwin-Hall draw).
+``ends``     the operators around the layer: token embedding, norms, losses, read-out.
+``updates``  momentum and Newton-Schulz steps of a weight's update.
 
 Every function here is pinned by ``-m "not gpu"`` tests against something other
 than itself (brute force, closed forms, finite differences, a hand-worked fixture,

@@ -118,20 +118,24 @@ def test_embedding_bwd_refusals(lib, kw, code):
 def test_embedding_workspace(lib):
     size = lib.tw_embedding_bwd_workspace_size
     assert size(512, 1000, 64) == 0 and size(513, 1000, 64) >= 513 * 8 and size(-1, 10, 10) == 0
-    # bounded per token for long batches: the parts of runs are few
-    assert size(1 << 22, 1000, 64) < (1 << 22) * 8 + 2 * 4 * 64 * 5000 + 10000
+    # three words a token, and for long batches no more parts of runs than 4096 chunks have
+    assert size(1 << 22, 1000, 64) < (1 << 22) * 12 + 2 * 4 * 256 * 4100 + 10000
 
 
 def _pointers(*values):
     return (ctypes.c_void_p * len(values))(*values)
 
 
+BIG = 1 << 40  # far between the fake matrices
+
+
 def _ortho(lib, **kw):
     coef = kw.pop("coef_values", [3.4445, -4.775, 2.0315] * 5)
     m, n, count = kw.get("m", 64), kw.get("n", 64), kw.get("count", 1)
-    a = dict(grads=_pointers(*[P] * max(count, 1)), ldg=64, gtype=0, buffers=_pointers(*[P] * max(count, 1)), ldb=64, mu=0.9, nesterov=1,
+    at = lambda k: _pointers(*[(k + 3 * i) * BIG for i in range(max(count, 1))])  # noqa: E731
+    a = dict(grads=at(1), ldg=64, gtype=0, buffers=at(2), ldb=64, mu=0.9, nesterov=1,
              count=count, m=m, n=n, steps=5, coef=(ctypes.c_float * len(coef))(*coef), scale=1.0, beta=0.0,
-             out=_pointers(*[P] * max(count, 1)), ldo=64, otype=1, ws=P,
+             out=at(3), ldo=64, otype=1, ws=P,
              ws_bytes=lib.tw_orthogonalize_workspace_size(m, n, count), status=P)
     assert set(kw) <= set(a)
     return lib.tw_orthogonalize(*{**a, **kw}.values(), None)
@@ -150,6 +154,30 @@ def _ortho(lib, **kw):
 ], ids=str)
 def test_orthogonalize_refusals(lib, kw, code):
     assert _ortho(lib, **kw) == getattr(_lib, "TW_" + code)
+
+
+def test_orthogonalize_shared_memory(lib):
+    """Matrices that are written and share an element are refused; the library goes on to the
+    workspace's size (here too small) where they do not."""
+    ok, bad = _lib.TW_EWORKSPACE, _lib.TW_EINVAL
+    m, n, row = 64, 64, 200  # rows of 200 elements: room for three matrices side by side
+
+    def out(*offsets, size=2, **kw):
+        return _ortho(lib, count=2, ldo=row, ws_bytes=1, out=_pointers(*[7 * BIG + size * o for o in offsets]), **kw)
+
+    assert out(0, m * row) == ok and out(0, 64) == ok and out(136, 64) == ok      # below, beside, beside
+    assert out(0, 0) == bad and out(0, 63) == bad and out(0, 64 * row - 137) == bad
+    assert out(0, row - 63) == bad                                                # its columns wrap into the next row's first
+    assert out(0, (m - 1) * row + 64) == ok and out(0, (m - 1) * row + 63) == bad  # behind the last row
+    assert out(0, 64, size=4, otype=0) == ok and out(0, 63, size=4, otype=0) == bad
+    same = _pointers(BIG, BIG)
+    assert _ortho(lib, count=2, buffers=same) == bad
+    assert _ortho(lib, count=2, buffers=_pointers(5 * BIG, 5 * BIG + 4 * 64 * 64), ws_bytes=1) == ok
+    assert _ortho(lib, count=2, grads=same, buffers=None, ws_bytes=1) == ok        # read alone
+    assert _ortho(lib, buffers=_pointers(BIG)) == bad                              # a buffer in its gradient
+    assert _ortho(lib, buffers=_pointers(BIG + 4 * 64 * 64), ws_bytes=1) == ok
+    assert _ortho(lib, gtype=1, buffers=_pointers(BIG + 64 * 64)) == bad           # two bytes an element and four
+    assert _ortho(lib, out=_pointers(BIG), otype=0, ws_bytes=1) == ok              # the result in the gradient's place
 
 
 def test_orthogonalize_workspace(lib):
@@ -310,5 +338,5 @@ def test_orthogonalize_lists(lib, current_device):
     with pytest.raises(ValueError, match="shape"):
         op([g.T], [g])
     assert not notes.calls
-    assert len(op([g], [g])) == 1 and isinstance(op(g, g), torch.Tensor)
+    assert len(op([g], [g])) == 1 and isinstance(op(g, g), torch.Tensor)  # (the library here only takes notes)
     assert [c[0] for c in notes.calls] == ["tw_orthogonalize"] * 2

@@ -1051,7 +1051,11 @@ tw_status tw_embedding_bwd(const void* dy, int64_t lddy, const int32_t* tokens, 
 // ------------------------------------------------------------------ orthogonalised updates
 size_t tw_orthogonalize_workspace_size(int m, int n, int count) {
   if (check_ortho(m, n, count) != TW_OK) return 0;
-  return tw::ortho_workspace(m, n, count);
+  // fewer matrices may be split into more slices, which take more: whoever has room for
+  // `count` has it for any number below
+  size_t most = 0;
+  for (int k = 1; k <= count; ++k) most = std::max(most, tw::ortho_workspace(m, n, k));
+  return most;
 }
 
 tw_status tw_orthogonalize(const void* const* grads, int64_t ldg, int gtype, float* const* buffers, int64_t ldbuf,

@@ -7,6 +7,12 @@
 // atomics: it sorts the positions by token, stably, and sums each token's rows in that
 // order, so the same call gives the same bits. Both are bound by HBM; the gradient written
 // whole is mostly the zeros of the tokens that do not occur.
+//
+// Measured on one GB300 against the copy rate (6777 GB/s): forward of 16384 tokens, 2048
+// columns, fp32 table of 131072 rows, bf16 out 22.2 us for 123 MB (0.82); the gradient of the
+// same, written whole, 179 us for 1.14 GB (0.94; a memset of the table alone takes 140); added
+// to a table of 5003 x 1027, 40009 positions of fp16, 84 us for 117 MB (0.21: 22 the sort, 48
+// the sums, whose rows of odd widths are read by the element, the rest the join).
 #include <algorithm>
 #include <type_traits>
 
@@ -371,7 +377,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedBwd
 // Each warp takes `chunk` sorted positions, whatever tokens they are, and 256 columns: frequent
 // tokens cost no more than rare ones, and warps that wait for nothing but their own loads
 // keep an SM's memory pipe full (one CTA of 256 threads a chunk of 32 with 70 to 140 registers
-// left 10 to 24 warps an SM: 40009 rows of 1027 fp16 96 us). Runs that begin and end in the
+// left 10 to 24 warps an SM: 40009 rows of 1027 fp16 96 us against 48). Runs that begin and end in the
 // chunk are finished; of the others the part here is kept: at the chunk's head (a run that
 // began before) or its tail (one that begins here and goes on). The CTAs behind those zero
 // the rows of absent tokens, eight each (16384 tokens of 131072 x 2048, all of it: 176 us; with
@@ -536,13 +542,15 @@ cudaError_t embed_bwd(const EmbedBwdArgs& a, cudaStream_t s) {
 
 }  // namespace
 
+constexpr int kMostChunks = 4096;  // whole ones
+
 EmbedBwdPlan embed_bwd_plan(int T, int V, int d) {
   EmbedBwdPlan p{};
   if (T <= kFewTokens) return p;
   // tokens of a sorting CTA: whole words of the bits that say which occur
   p.range = std::min(kMostRange, ((V + 151) / 152 + 31) / 32 * 32);
   p.chunk = 16;
-  while (T / p.chunk > 4096) p.chunk *= 2;
+  while (T / p.chunk > kMostChunks) p.chunk *= 2;
   p.part_ld = (d + kWarpCols - 1) / kWarpCols * kWarpCols;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -554,7 +562,9 @@ EmbedBwdPlan embed_bwd_plan(int T, int V, int d) {
   p.end = take(sizeof(int) * static_cast<size_t>(T));
   p.n_valid = take(sizeof(int));
   p.present = take((static_cast<size_t>(V) + kMostRange) / 8);
-  p.part = take(sizeof(float) * 2 * static_cast<size_t>(p.part_ld) * ((T + p.chunk - 1) / p.chunk));
+  // never less than for fewer tokens, whose smaller chunks may be more: whoever has room for T
+  // has it for any number below
+  p.part = take(sizeof(float) * 2 * static_cast<size_t>(p.part_ld) * std::min((T + 15) / 16, kMostChunks + 1));
   p.bytes = at;
   return p;
 }

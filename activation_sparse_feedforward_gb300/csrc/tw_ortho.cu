@@ -28,6 +28,13 @@
 // otherwise be amplified as the small singular values are (up to 3.44 a step), while in
 // X B they meet B's small rows. Against the definition in 64 bits, in the 2-norm: 4e-4 to
 // 1.3e-3 for spectra over up to four decades (hi alone: up to 2.4e-2).
+//
+// Large matrices are bound by the tensor cores under the board's power: on one GB300 three of
+// 5632 x 2048, fp32 gradients and momentum, five steps take 1.05 ms for 1.19e12 operations,
+// 1130 TFLOP/s over all (0.65 of the sustained 1736): some 110 us are the way in (bytes), and of
+// the products' the pairs spend 0.89 in MMAs, at 1340 W and 1.85 GHz. Small ones are bound by
+// the latency of 15 products that wait for one another: 704 x 256 takes 107 us, two of
+// 1027 x 2500 265.
 #include <cuda.h>
 
 #include <algorithm>

@@ -3,7 +3,9 @@
 //
 //   xh = x rstd;  g = dy w;  dx = rstd (g - xh sum(g xh) / d) + dres;  dw = sum_t dy xh
 //
-// The form of layer norm's backward (tw_norm.cu) without the mean's terms. Bound by HBM.
+// The form of layer norm's backward (tw_norm.cu) without the mean's terms. Bound by HBM: one
+// GB300, 16384 x 2048 bf16 with the residual's gradient and fp32 weights 45.3 us for 268 MB
+// (0.87 of the copy rate, 6777 GB/s).
 #include "tw_norm_rows.cuh"
 
 namespace tw {

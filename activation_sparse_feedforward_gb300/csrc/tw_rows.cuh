@@ -1,4 +1,4 @@
-// Device helpers of the row operators (tw_norm.cu, tw_logits.cu): the three element
+// Device helpers of the row operators (tw_norm_rows.cuh, tw_logits.cuh, tw_embed.cu): the three element
 // types, 16-byte vectors of them, asynchronous 16-byte copies into shared memory,
 // sums over teams of warps, and reads of another CTA's shared memory in a cluster.
 #pragma once

@@ -465,7 +465,8 @@ tw_status tw_layer_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t
 /* Root-mean-square norm forward over the rows of x [T, d], after an optional residual add:
  *   s = x + res (rounded to the type; s = x when res is NULL)
  *   rstd = (sum(s^2) / d + eps)^-1/2,  y = s rstd * weight
- * Arguments, types, strides and limits as tw_layer_norm_fwd. */
+ * Arguments, types, strides and limits as tw_layer_norm_fwd. The squares are fp32: a row of
+ * values beyond 1e19 has an infinite sum and rstd 0. */
 tw_status tw_rms_norm_fwd(const void* x, int64_t ldx, const void* res, int64_t ldres, const void* weight, int T, int d,
                           float eps, int dtype, int wtype, void* sum, int64_t ldsum, void* y, int64_t ldy, float* rstd,
                           void* stream);
@@ -475,7 +476,8 @@ tw_status tw_rms_norm_fwd(const void* x, int64_t ldx, const void* res, int64_t l
  *   scale = max(max |y| / 448, 2^-126) over the row or group, of y in fp32
  *   q = y / scale to e4m3, round to nearest even
  * q [T, d] bytes, row stride ldq >= d; scales [T] or [T, ceil(d / 128)], dense. A row or
- * group of zeros has scale 2^-126 and q 0. A NaN in y makes its scale and q NaN (0x7F). */
+ * group of zeros has scale 2^-126 and q 0. A NaN in y makes its scale and q NaN (0x7F). The
+ * largest is taken of |s weight| in fp32: where that product passes 3.4e38 the scale is inf. */
 tw_status tw_rms_norm_fwd_fp8(const void* x, int64_t ldx, const void* res, int64_t ldres, const void* weight, int T,
                               int d, float eps, int dtype, int wtype, void* sum, int64_t ldsum, uint8_t* q, int64_t ldq,
                               float* scales, int group, float* rstd, void* stream);
@@ -549,8 +551,8 @@ tw_status tw_token_logprobs(const void* z, int64_t ldz, int N, int V, int dtype,
 tw_status tw_embedding_fwd(const int32_t* tokens, const void* weight, int64_t ldw, int T, int V, int d, float scale,
                            int dtype, int wtype, void* y, int64_t ldy, int32_t* dev_status, void* stream);
 
-/* Workspace bytes tw_embedding_bwd needs (the sorted positions, parts of long runs); 0 up to
- * 512 tokens (ws may then be NULL). */
+/* Workspace bytes tw_embedding_bwd needs (the sorted positions, parts of long runs) for T
+ * tokens or fewer; 0 up to 512 (ws may then be NULL). */
 size_t tw_embedding_bwd_workspace_size(int T, int V, int d);
 
 /* Token embedding backward, by sorted tokens:
@@ -567,8 +569,8 @@ tw_status tw_embedding_bwd(const void* dy, int64_t lddy, const int32_t* tokens, 
 /* The most matrices of one tw_orthogonalize call. */
 enum { TW_ORTHO_MOST = 8 };
 
-/* Workspace bytes tw_orthogonalize needs for `count` matrices [m, n]; 0 for sizes it does
- * not take. */
+/* Workspace bytes tw_orthogonalize needs for `count` matrices [m, n] or fewer; 0 for sizes it
+ * does not take. */
 size_t tw_orthogonalize_workspace_size(int m, int n, int count);
 
 /* Orthogonalised updates of `count` weight matrices of one shape [m, n], as optimisers of

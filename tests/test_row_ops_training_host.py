@@ -186,6 +186,19 @@ def test_orthogonalize_workspace(lib):
     assert size(5632, 2048, 3) >= 3 * 3 * 5632 * 2048 * 2 and size(2048, 5632, 3) == size(5632, 2048, 3)
 
 
+def test_workspace_serves_smaller_calls(lib):
+    """A workspace made for so many tokens or matrices has room for fewer: fewer tokens may go
+    in smaller chunks, fewer matrices in more slices."""
+    size = lib.tw_embedding_bwd_workspace_size
+    tokens = [512, 513, 4096, 65535, 65536, 65551, 65552, 70000, 131000, 131103, 131104, 262207, 262208, 1 << 22]
+    sizes = [size(t, 5003, 1027) for t in tokens]
+    assert sizes == sorted(sizes)
+    for m in list(range(64, 4200, 448)) + [1, 3712, 3904]:
+        for n in list(range(64, 4200, 448)) + [1, 448]:
+            sizes = [lib.tw_orthogonalize_workspace_size(m, n, k) for k in range(1, 9)]
+            assert sizes == sorted(sizes), (m, n)
+
+
 # ------------------------------------------------------------------------------ the binding
 
 BF16, F32, I32 = torch.bfloat16, torch.float32, torch.int32

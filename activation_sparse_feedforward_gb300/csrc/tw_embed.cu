@@ -177,6 +177,14 @@ struct RowSum {
   }
 };
 
+// Asks for a warp's columns of row v, which a sum will be added to, in L2.
+TW_DEV void prefetch_out(const EmbedBwdArgs& a, int v, int block) {
+  const char* out = reinterpret_cast<const char*>(a.dw + static_cast<size_t>(v) * a.lddw + block);
+  const int bytes = 4 * min(kWarpCols, a.d - block);
+  for (int b = 0; b < bytes; b += 128) prefetch_line(out + b);
+  prefetch_line(out + bytes - 1);
+}
+
 // Zeros into row v's columns, by `threads` threads.
 TW_DEV void zero_row(const EmbedBwdArgs& a, int v, int tid, int threads) {
   float* out = a.dw + static_cast<size_t>(v) * a.lddw;
@@ -187,7 +195,7 @@ TW_DEV void zero_row(const EmbedBwdArgs& a, int v, int tid, int threads) {
   }
 }
 
-constexpr int kThreads = 256, kBlockCols = kThreads * kCols;  // of the kernels below
+constexpr int kThreads = 256, kWarps = kThreads / 32;  // of the kernels below
 
 // ------------------------------------------------------------------ backward of few tokens
 // One launch and no sort: the CTA of position i looks through the tokens; where its own
@@ -231,7 +239,7 @@ __global__ void __launch_bounds__(kThreads) embed_bwd_few_kernel(const EmbedBwdA
     if (same[w] != 0u) return;
   if (same[me >> 5] & ((1u << (me & 31)) - 1u)) return;
   constexpr int kBatch = 8;  // rows on their way at once
-  RowSum<DT, VEC> sum(a, blockIdx.y * kBlockCols + (tid >> 5) * kWarpCols);
+  RowSum<DT, VEC> sum(a, (blockIdx.y * kWarps + (tid >> 5)) * kWarpCols);
   if (sum.c >= a.d) return;
   typename RowSum<DT, VEC>::W w[kBatch][RowSum<DT, VEC>::NV];
   int n = 0;
@@ -365,7 +373,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedBwd
           if (lane == __ffs(peers) - 1) *n = was + __popc(peers);
           a.pos[slot] = base + 128 * k + 32 * q + lane;
           a.key[slot] = v;
-          a.end[slot] = start[v - lo + 1];
+          a.run[slot] = make_int2(start[v - lo], start[v - lo + 1]);
         }
         __syncwarp();
       }
@@ -375,15 +383,86 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedBwd
 
 // ------------------------------------------------------------------ backward: sums
 // Each warp takes `chunk` sorted positions, whatever tokens they are, and 256 columns: frequent
-// tokens cost no more than rare ones, and warps that wait for nothing but their own loads
-// keep an SM's memory pipe full (one CTA of 256 threads a chunk of 32 with 70 to 140 registers
-// left 10 to 24 warps an SM: 40009 rows of 1027 fp16 96 us against 48). Runs that begin and end in the
-// chunk are finished; of the others the part here is kept: at the chunk's head (a run that
-// began before) or its tail (one that begins here and goes on). The CTAs behind those zero
-// the rows of absent tokens, eight each (16384 tokens of 131072 x 2048, all of it: 176 us; with
-// CTAs of both kinds in turn 190, of 128 threads 182, 64 rows each 187).
+// tokens cost no more than rare ones. A run of up to kWhole positions is the warp's that has its
+// first, to its end; of a longer one over several chunks the part here is kept: at the chunk's
+// head (a run that began before) or its tail (one that begins here and goes on).
+//
+// Bound by how fast rows in no order come (40009 of 1027 fp16, with the event's 4 us: 37 us for
+// 82 MB and the 34 MB added to): two rows a group of copies, four groups a warp, 32 warps an SM.
+// 24 warps 41, 40 or more 41 to 43, four rows a group 39, four groups of them 43; loads into
+// registers behind an L2 prefetch 53, without it 80. The CTAs behind those zero the rows of
+// absent tokens, eight each (16384 tokens of 131072 x 2048, all of it: 172 us; with CTAs of both
+// kinds in turn, of 64 rows or of 128 threads 2 to 8 % more).
+constexpr int kWhole = 16;  // (1: the join takes twice as long where runs are of 8; 32: sums of short batches 6 us longer)
+TW_DEV bool in_parts(const int2& run, int chunk) { return run.y - run.x > kWhole && run.x / chunk != (run.y - 1) / chunk; }
+
+// A warp's 256 columns of rows of dy on their way through shared memory, kBatch rows a group
+// of asynchronous copies, kGroups groups. VEC: each lane copies the vectors that it will read.
+// Else the aligned vectors that the columns lie in, and a column is read by the element.
 template <int DT, bool VEC>
-__global__ void __launch_bounds__(kThreads, 4) embed_sum_kernel(const EmbedBwdArgs a, int fills, int blocks) {
+struct RowRing {
+  using S = typename Elem<DT>::S;
+  static constexpr int E = Elem<DT>::E, NV = kCols / E;         // a lane's vectors of a row
+  static constexpr int kBatch = 2, kGroups = NV == 1 ? 4 : 2;
+  static constexpr int kRowVecs = 32 * NV + 1;                    // places of a row
+  static constexpr int kVecs = kBatch * kGroups * kRowVecs;       // of a warp
+  const EmbedBwdArgs& a;
+  const S* columns;  // of dy's first row
+  uint4* mine;       // the warp's places
+  int width, lane;
+  TW_DEV uint4* place(int i) const { return mine + i % (kBatch * kGroups) * kRowVecs; }
+  // elements from an aligned 16 bytes to row pos's columns
+  TW_DEV int lead(int pos) const {
+    return static_cast<int>(reinterpret_cast<uintptr_t>(columns) / sizeof(S) + static_cast<unsigned>(pos) * static_cast<unsigned>(a.lddy)) & (E - 1);
+  }
+  // row `pos` into the place of the block's i-th position
+  TW_DEV void copy(int i, int pos) const {
+    uint4* to = place(i) + lane;
+    const S* from = columns + static_cast<size_t>(pos) * a.lddy;
+    if constexpr (VEC) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+        if (lane * kCols + k * E < width) cp_async16(to + k * 32, from + lane * kCols + k * E);
+    } else {
+      const int before = lead(pos), end = before + width;
+      from += lane * E - before;
+      const bool careful = pos == 0 || pos == a.T - 1 || a.lddy < 8;  // nothing of the row's neighbours may be read
+      if (!careful) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+          if ((k * 32 + lane) * E < end) cp_async16(to + k * 32, from + k * 32 * E);
+        if (lane == 0 && NV * 32 * E < end) cp_async16(to + NV * 32, from + NV * 32 * E);
+        return;
+      }
+      for (int k = 0; (k * 32 + lane) * E < end; ++k)
+        for (int q = 0; q < E; ++q) {
+          const int c = (k * 32 + lane) * E + q;
+          if (c >= before && c < end) reinterpret_cast<S*>(to + k * 32)[q] = from[k * 32 * E + q];
+        }
+    }
+  }
+  // (the sums of columns past the last are of whatever is there, and go nowhere)
+  TW_DEV void add(int i, int pos, float (&acc)[kCols]) const {
+    const uint4* from = place(i);
+    if constexpr (VEC) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        float u[E];
+        Elem<DT>::unpack(from[k * 32 + lane], u);
+#pragma unroll
+        for (int q = 0; q < E; ++q) acc[k * E + q] += u[q];
+      }
+    } else {
+      const S* e = reinterpret_cast<const S*>(from) + lead(pos) + lane;
+#pragma unroll
+      for (int k = 0; k < kCols; ++k) acc[k] += Elem<DT>::get(e[k * 32]);
+    }
+  }
+};
+
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(kThreads, 4) embed_sum_kernel(const EmbedBwdArgs a, int fills, int parts) {
+  extern __shared__ uint4 places[];
   pdl_enter();
   const int tid = threadIdx.x, lane = tid & 31;
   const int sums = gridDim.x - fills;
@@ -393,42 +472,45 @@ __global__ void __launch_bounds__(kThreads, 4) embed_sum_kernel(const EmbedBwdAr
       if (!((a.present[v >> 5] >> (v & 31)) & 1u)) zero_row(a, v, tid, kThreads);
     return;
   }
-  const int chunk = blockIdx.x / blocks;
-  const int n_valid = *a.n_valid, lo = chunk * a.chunk, n = min(a.chunk, n_valid - lo);
-  const int block = (blockIdx.x - chunk * blocks) * kBlockCols + (tid >> 5) * kWarpCols, width = min(kWarpCols, a.d - block);
-  if (n <= 0 || width <= 0) return;  // the whole warp
+  const int id = blockIdx.x * kWarps + (tid >> 5), chunk = id / parts;  // of all warps
+  const int n_valid = *a.n_valid, begin = chunk * a.chunk, past = min(begin + a.chunk, n_valid);
+  if (begin >= past) return;  // the whole warp
+  const int block = (id - chunk * parts) * kWarpCols, width = min(kWarpCols, a.d - block);
+  using Ring = RowRing<DT, VEC>;
+  constexpr int kBatch = Ring::kBatch;
+  const Ring ring{a, static_cast<const typename Ring::S*>(a.dy) + block, places + (tid >> 5) * Ring::kVecs, width, lane};
   RowSum<DT, VEC> sum(a, block);
-  const bool goes_on = a.end[lo + n - 1] > lo + n;
-  bool head = lo > 0 && a.end[lo - 1] > lo;
+  const int2 first_run = a.run[begin], last_run = a.run[past - 1];
+  const bool skip = first_run.x < begin && !in_parts(first_run, a.chunk);  // (another warp's)
+  const int lo = skip ? min(first_run.y, past) : begin;
+  const bool goes_on = last_run.y > past && in_parts(last_run, a.chunk);
+  const int n = (goes_on || (skip && first_run.y >= past) ? past : last_run.y) - lo;
+  bool head = first_run.x < begin && !skip;
   float* part = a.part + static_cast<size_t>(chunk) * 2 * a.part_ld + block;
   for (int first = 0; first < n; first += 32) {  // 32 keys and positions, a lane each
     const int m = min(32, n - first), at = lo + first + lane;
     const int key = lane < m ? a.key[at] : -1, pos = lane < m ? a.pos[at] : 0;
-    // where a run ends, or the chunk
-    const unsigned ends = __ballot_sync(0xFFFFFFFFu, lane < m && (first + lane + 1 == n || a.end[at] == at + 1));
-    // every row of dy, and every row that a run's sum will be added to, asked for in L2 now: the
-    // accesses below wait for one after the other
-    if (lane < m) {
-      const char* row = reinterpret_cast<const char*>(static_cast<const typename RowSum<DT, VEC>::S*>(a.dy) + static_cast<size_t>(pos) * a.lddy + block);
-      const int bytes = width * static_cast<int>(sizeof(typename RowSum<DT, VEC>::S));
-      for (int b = 0; b < bytes; b += 128) prefetch_line(row + b);
-      prefetch_line(row + bytes - 1);
-      if (a.add && (ends >> lane & 1u)) {
-        const char* out = reinterpret_cast<const char*>(a.dw + static_cast<size_t>(key) * a.lddw + block);
-        for (int b = 0; b < 4 * width; b += 128) prefetch_line(out + b);
-        prefetch_line(out + 4 * width - 1);
-      }
-    }
-    constexpr int kBatch = 4;
-    for (int i = 0; i < m; i += kBatch) {
-      typename RowSum<DT, VEC>::W w[kBatch][RowSum<DT, VEC>::NV];
+    auto fetch = [&](int i) {
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k)
-        if (i + k < m) sum.load(__shfl_sync(0xFFFFFFFFu, pos, i + k), w[k]);
+      for (int k = 0; k < kBatch; ++k) {
+        const int p = __shfl_sync(0xFFFFFFFFu, pos, (i + k) & 31);
+        if (i + k < m) ring.copy(i + k, p);
+      }
+      cp_commit();
+    };
+#pragma unroll
+    for (int g = 0; g < Ring::kGroups; ++g) fetch(g * kBatch);
+    // where a run ends, or the chunk
+    const unsigned ends = __ballot_sync(0xFFFFFFFFu, lane < m && (first + lane + 1 == n || a.run[at].y == at + 1));
+    // the rows that a run's sum will be added to, asked for in L2 now
+    if (a.add && (ends >> lane & 1u)) prefetch_out(a, key, block);
+    for (int i = 0; i < m; i += kBatch) {
+      cp_wait<Ring::kGroups - 1>();
+      __syncwarp();
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         if (i + k >= m) break;
-        sum.add(w[k]);
+        ring.add(i + k, __shfl_sync(0xFFFFFFFFu, pos, i + k), sum.acc);
         if (!((ends >> (i + k)) & 1u)) continue;
         const bool tail = first + i + k + 1 == n && goes_on;
         if (head || tail)
@@ -438,47 +520,46 @@ __global__ void __launch_bounds__(kThreads, 4) embed_sum_kernel(const EmbedBwdAr
         sum.clear();
         head = false;
       }
+      __syncwarp();
+      fetch(i + kBatch * Ring::kGroups);
     }
   }
 }
 
-// The runs over several chunks: the tail where the run begins, then the heads of the chunks
-// after it, in order. A CTA takes 256 columns of the runs that begin in eight chunks, a warp
-// each; a run of many heads is left to all eight warps, an eighth of the heads each, whose
-// sums are joined in order. (The split goes by the heads' number alone.)
-constexpr int kJoinWarps = kThreads / 32, kAlone = 16;
+// The runs in parts: the tail where the run begins, then the heads of the chunks after it, in
+// order. A CTA takes 256 columns of the runs that begin in 32 chunks (a lane each looks for
+// one), a warp each; a run of many heads is left to all warps, a stretch of the heads each,
+// whose sums are joined in order. (The split goes by the heads' number alone.)
+constexpr int kAlone = 16, kJoinWarps = 8, kJoinThreads = 32 * kJoinWarps;
 
 template <int DT, bool VEC>
-__global__ void __launch_bounds__(kThreads) embed_join_kernel(const EmbedBwdArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(const EmbedBwdArgs a) {
   __shared__ float4 sums[kJoinWarps - 1][2][32];
-  __shared__ int many[kJoinWarps];  // heads of a run left to all
   pdl_enter();
   const int n_valid = *a.n_valid, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, block = blockIdx.y * kWarpCols;
-  auto next_of = [&](long chunk) { return (chunk + 1) * a.chunk; };
   auto part_of = [&](long chunk) { return a.part + static_cast<size_t>(chunk) * 2 * a.part_ld + block; };
   RowSum<DT, VEC> sum(a, block);
-  {
-    const long chunk = static_cast<long>(blockIdx.x) * kJoinWarps + warp, lo = chunk * a.chunk, next = next_of(chunk);
-    int heads = 0;  // chunks after this one that begin inside its run
-    if (next < n_valid) {
-      const int end = a.end[next - 1], before = lo > 0 ? a.end[lo - 1] : 0;  // (a run is known by its end)
-      if (end > next && before != end) heads = static_cast<int>((end - next + a.chunk - 1) / a.chunk);
-    }
-    if (lane == 0) many[warp] = heads > kAlone ? heads : 0;
-    if (heads > 0 && heads <= kAlone) {
-      const float* part = part_of(chunk);
-      sum.template join<1>(part + a.part_ld, 1, 0);
-      sum.template join<4>(part + 2 * a.part_ld, heads, 2 * static_cast<size_t>(a.part_ld));
-      if (sum.c < a.d) sum.put(a.key[next]);
-    }
+  const long first = static_cast<long>(blockIdx.x) * 32, next = (first + lane + 1) * a.chunk;
+  int heads = 0, key = 0;  // chunks after the lane's that begin inside its run
+  if (next < n_valid) {
+    const int2 run = a.run[next - 1];
+    if (run.x >= next - a.chunk && run.y > next && in_parts(run, a.chunk)) heads = static_cast<int>((run.y - next + a.chunk - 1) / a.chunk), key = a.key[next];
   }
-  __syncthreads();
-  for (int q = 0; q < kJoinWarps; ++q) {
-    const int heads = many[q];
-    if (heads == 0) continue;
-    const long chunk = static_cast<long>(blockIdx.x) * kJoinWarps + q;
-    const int each = (heads + kJoinWarps - 1) / kJoinWarps, from = min(heads, warp * each), to = min(heads, from + each);
-    const float* part = part_of(chunk);
+  unsigned few = __ballot_sync(0xFFFFFFFFu, heads > 0 && heads <= kAlone), many = __ballot_sync(0xFFFFFFFFu, heads > kAlone);
+  if (a.add && heads > 0 && warp == 0) prefetch_out(a, key, block);
+  for (int i = 0; few != 0u; few &= few - 1u, ++i) {
+    if (i % kJoinWarps != warp) continue;
+    const int q = __ffs(few) - 1, n = __shfl_sync(0xFFFFFFFFu, heads, q), v = __shfl_sync(0xFFFFFFFFu, key, q);
+    const float* part = part_of(first + q);
+    sum.clear();
+    sum.template join<1>(part + a.part_ld, 1, 0);
+    sum.template join<4>(part + 2 * a.part_ld, n, 2 * static_cast<size_t>(a.part_ld));
+    if (sum.c < a.d) sum.put(v);
+  }
+  for (; many != 0u; many &= many - 1u) {
+    const int q = __ffs(many) - 1, n = __shfl_sync(0xFFFFFFFFu, heads, q), v = __shfl_sync(0xFFFFFFFFu, key, q);
+    const int each = (n + kJoinWarps - 1) / kJoinWarps, from = min(n, warp * each), to = min(n, from + each);
+    const float* part = part_of(first + q);
     sum.clear();
     if (warp == 0) sum.template join<1>(part + a.part_ld, 1, 0);
     sum.template join<8>(part + static_cast<size_t>(from + 1) * 2 * a.part_ld, to - from, 2 * static_cast<size_t>(a.part_ld));
@@ -490,7 +571,7 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const EmbedBwdArgs
     if (warp == 0) {
 #pragma unroll
       for (int w = 0; w < kJoinWarps - 1; ++w) sum.join(sums[w][0][lane], sums[w][1][lane]);
-      if (sum.c < a.d) sum.put(a.key[next_of(chunk)]);
+      if (sum.c < a.d) sum.put(v);
     }
     __syncthreads();
   }
@@ -511,11 +592,11 @@ cudaError_t embed_fwd(const EmbedFwdArgs& a, bool vec, cudaStream_t s) {
 
 template <int DT, bool VEC>
 cudaError_t embed_bwd_as(EmbedBwdArgs a, cudaStream_t s) {
-  const unsigned blocks = (a.d + kBlockCols - 1) / kBlockCols;
+  const unsigned parts = (a.d + kWarpCols - 1) / kWarpCols;  // of a row, a warp each
   const int fill = a.add ? 0 : (a.V + kFillRows - 1) / kFillRows;  // CTAs that zero rows
   cudaError_t e;
   if (a.T <= kFewTokens) {
-    e = launch(embed_bwd_few_kernel<DT, VEC>, dim3(a.T + fill, blocks), dim3(kThreads), 0, s, a);
+    e = launch(embed_bwd_few_kernel<DT, VEC>, dim3(a.T + fill, (parts + kWarps - 1) / kWarps), dim3(kThreads), 0, s, a);
     trace_mark(s, "embed_bwd_few");
     return e;
   }
@@ -528,10 +609,13 @@ cudaError_t embed_bwd_as(EmbedBwdArgs a, cudaStream_t s) {
   trace_mark(s, "embed_sort");
   if (e != cudaSuccess) return e;
   const int chunks = (a.T + a.chunk - 1) / a.chunk;
-  e = launch(embed_sum_kernel<DT, VEC>, dim3(chunks * blocks + fill), dim3(kThreads), 0, s, a, fill, static_cast<int>(blocks));
+  const size_t places = sizeof(uint4) * kWarps * RowRing<DT, VEC>::kVecs;
+  e = allow_smem(embed_sum_kernel<DT, VEC>, places);
+  if (e != cudaSuccess) return e;
+  e = launch(embed_sum_kernel<DT, VEC>, dim3((chunks * parts + kWarps - 1) / kWarps + fill), dim3(kThreads), places, s, a, fill, static_cast<int>(parts));
   trace_mark(s, "embed_sum");
   if (e != cudaSuccess || chunks < 2) return e;
-  e = launch(embed_join_kernel<DT, VEC>, dim3((chunks + kJoinWarps - 1) / kJoinWarps, (a.d + kWarpCols - 1) / kWarpCols), dim3(kThreads), 0, s, a);
+  e = launch(embed_join_kernel<DT, VEC>, dim3((chunks + 31) / 32, parts), dim3(kJoinThreads), 0, s, a);
   trace_mark(s, "embed_join");
   return e;
 }
@@ -559,7 +643,7 @@ EmbedBwdPlan embed_bwd_plan(int T, int V, int d) {
     return was;
   };
   p.key = take(sizeof(int) * static_cast<size_t>(T)), p.pos = take(sizeof(int) * static_cast<size_t>(T));
-  p.end = take(sizeof(int) * static_cast<size_t>(T));
+  p.run = take(sizeof(int2) * static_cast<size_t>(T));
   p.n_valid = take(sizeof(int));
   p.present = take((static_cast<size_t>(V) + kMostRange) / 8);
   // never less than for fewer tokens, whose smaller chunks may be more: whoever has room for T
@@ -583,7 +667,7 @@ cudaError_t launch_embed_bwd(const EmbedBwdArgs& given, void* ws, cudaStream_t s
   const EmbedBwdPlan p = embed_bwd_plan(a.T, a.V, a.d);
   uint8_t* w = static_cast<uint8_t*>(ws);
   if (p.bytes > 0) {
-    a.key = reinterpret_cast<int*>(w + p.key), a.pos = reinterpret_cast<int*>(w + p.pos), a.end = reinterpret_cast<int*>(w + p.end);
+    a.key = reinterpret_cast<int*>(w + p.key), a.pos = reinterpret_cast<int*>(w + p.pos), a.run = reinterpret_cast<int2*>(w + p.run);
     a.n_valid = reinterpret_cast<int*>(w + p.n_valid), a.present = reinterpret_cast<unsigned*>(w + p.present);
     a.part = reinterpret_cast<float*>(w + p.part);
     a.range = p.range, a.chunk = p.chunk, a.part_ld = p.part_ld;

@@ -457,7 +457,7 @@ cudaError_t launch_embed_fwd(const EmbedFwdArgs& a, cudaStream_t s);
 // Sizes and workspace offsets of the backward's sort; bytes 0 where it needs none.
 struct EmbedBwdPlan {
   int range, chunk, part_ld;
-  size_t key, pos, end, n_valid, present, part, bytes;
+  size_t key, pos, run, n_valid, present, part, bytes;
 };
 EmbedBwdPlan embed_bwd_plan(int T, int V, int d);
 
@@ -470,7 +470,8 @@ struct EmbedBwdArgs {
   int T, V, d, dtype, add;
   float scale;
   // set by launch_embed_bwd
-  int *key, *pos, *end;      // tokens and positions in sorted order, and where a token's end
+  int *key, *pos;            // tokens and positions in sorted order
+  int2* run;                 // where a position's token's begin and end there
   int* n_valid;              // how many
   unsigned* present;         // a bit for each token that occurs (null: not wanted)
   float* part;               // [chunks][2][part_ld]: heads and tails of runs

@@ -118,8 +118,8 @@ def test_embedding_bwd_refusals(lib, kw, code):
 def test_embedding_workspace(lib):
     size = lib.tw_embedding_bwd_workspace_size
     assert size(512, 1000, 64) == 0 and size(513, 1000, 64) >= 513 * 8 and size(-1, 10, 10) == 0
-    # three words a token, and for long batches no more parts of runs than 4096 chunks have
-    assert size(1 << 22, 1000, 64) < (1 << 22) * 12 + 2 * 4 * 256 * 4100 + 10000
+    # four words a token, and for long batches no more parts of runs than 4096 chunks have
+    assert size(1 << 22, 1000, 64) < (1 << 22) * 16 + 2 * 4 * 256 * 4100 + 10000
 
 
 def _pointers(*values):

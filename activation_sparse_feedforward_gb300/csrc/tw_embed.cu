@@ -10,9 +10,9 @@
 //
 // Measured on one GB300 against the copy rate (6777 GB/s): forward of 16384 tokens, 2048
 // columns, fp32 table of 131072 rows, bf16 out 22.2 us for 123 MB (0.82); the gradient of the
-// same, written whole, 179 us for 1.14 GB (0.94; a memset of the table alone takes 140); added
-// to a table of 5003 x 1027, 40009 positions of fp16, 84 us for 117 MB (0.21: 22 the sort, 48
-// the sums, whose rows of odd widths are read by the element, the rest the join).
+// same, written whole, 166 us for 1.14 GB (a memset of the table alone takes 140); added to a
+// table of 5003 x 1027, 40009 positions of fp16, 51 us for 117 MB (0.34: the sort takes 10, the
+// sums of rows in no order 33, the join 8).
 #include <algorithm>
 #include <type_traits>
 
@@ -262,12 +262,14 @@ __global__ void __launch_bounds__(kThreads) embed_bwd_few_kernel(const EmbedBwdA
 
 // ------------------------------------------------------------------ backward: sort
 // Positions in the order of (token, position). Each CTA owns `range` tokens (about V / 152, at
-// most kMostRange) and needs nothing from the others: it reads all tokens, counts those below
-// its own (where its part of the result begins) and its own for each warp's stretch of the
-// positions, and after a prefix sum over (token, warp) goes through them once more, each
-// warp its stretch in order, and puts them down. Bound by the instructions of that: about 40
-// a warp for 128 tokens that are others'.
-constexpr int kSortWarps = 32, kSortThreads = 32 * kSortWarps, kMostRange = 1024, kAhead = 4;
+// most kMostRange) and needs nothing from the others: it reads all tokens, each warp a stretch,
+// counts those below its own (where its part of the result begins) and lists its own in order.
+// After a prefix sum over (token, warp) each warp goes through its list and puts it down. A
+// warp whose list is full (a stretch of the CTA's tokens alone) reads its stretch again in its
+// place. Bound by the instructions of looking at all tokens, some 65 a warp for 128 of them:
+// 40009 tokens of 5003 10 us (20 where every group of 128 with one of the CTA's was gone through
+// twice, by shuffles), 16384 of 131072 6 us.
+constexpr int kSortWarps = 32, kSortThreads = 32 * kSortWarps, kMostRange = 1024, kAhead = 4, kList = 256;
 
 TW_DEV int warp_sum_int(int v) {
 #pragma unroll
@@ -276,17 +278,18 @@ TW_DEV int warp_sum_int(int v) {
 }
 
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedBwdArgs a) {
-  extern __shared__ int count[];  // [kSortWarps][range], then [range + 1]: where a token's positions begin
+  // [kSortWarps][range] counts, [range + 1]: where a token's positions begin, [kSortWarps][kList]
+  extern __shared__ int count[];
   __shared__ int scan[kSortWarps], below[kSortWarps];
   pdl_enter();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, range = a.range;
   const int lo = blockIdx.x * range;
-  const unsigned own_range = min(range, a.V - lo);
+  const unsigned own_range = min(range, a.V - lo), before = (1u << lane) - 1u;
   // a warp's stretch: groups of 128 positions, four adjacent ones a lane
   const int stretch = (a.T + 4 * kSortThreads - 1) / (4 * kSortThreads) * 128;
   const int begin = min(a.T, warp * stretch), end = min(a.T, begin + stretch);
   const bool whole = (reinterpret_cast<uintptr_t>(a.tokens) & 15u) == 0;
-  int4 t[kAhead];  // (up to 16384 tokens in all: read once)
+  int4 t[kAhead];
   auto read = [&](int base) {
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
@@ -299,13 +302,14 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedBwd
     }
   };
   auto own = [&](int v) { return static_cast<unsigned>(v - lo) < own_range; };
-  auto owns = [&](const int4& v) { return own(v.x) || own(v.y) || own(v.z) || own(v.w); };
   read(begin);
   for (int i = tid; i < kSortWarps * range; i += kSortThreads) count[i] = 0;
   __syncthreads();
   int* mine = count + warp * range;
   int* start = count + kSortWarps * range;
-  int less = 0;
+  unsigned* list = reinterpret_cast<unsigned*>(start + range + 1) + warp * kList;  // token - lo | position - begin << 10
+  static_assert(kMostRange <= 1 << 10 && (1 << 22) / kSortWarps <= 1 << 22, "an entry's fields");
+  int less = 0, listed = 0;  // (listed > kList: not all are)
   bool bad = false;
   for (int base = begin; base < end; base += 128 * kAhead) {
     if (base > begin) read(base);
@@ -314,12 +318,23 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedBwd
       const unsigned l = lo;
       less += (static_cast<unsigned>(t[k].x) < l) + (static_cast<unsigned>(t[k].y) < l) + (static_cast<unsigned>(t[k].z) < l) +
               (static_cast<unsigned>(t[k].w) < l);
-      if (owns(t[k])) {
-        if (own(t[k].x)) atomicAdd(mine + (t[k].x - lo), 1);
-        if (own(t[k].y)) atomicAdd(mine + (t[k].y - lo), 1);
-        if (own(t[k].z)) atomicAdd(mine + (t[k].z - lo), 1);
-        if (own(t[k].w)) atomicAdd(mine + (t[k].w - lo), 1);
+      const bool o[4] = {own(t[k].x), own(t[k].y), own(t[k].z), own(t[k].w)};
+      if (!__any_sync(0xFFFFFFFFu, o[0] || o[1] || o[2] || o[3])) continue;
+      int at = listed;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const unsigned owned = __ballot_sync(0xFFFFFFFFu, o[q]);
+        at += __popc(owned & before);
+        listed += __popc(owned);
       }
+      if (listed > kList) {
+        listed = kList + 1;
+        continue;
+      }
+      const int v[4] = {t[k].x, t[k].y, t[k].z, t[k].w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (o[q]) list[at++] = static_cast<unsigned>(v[q] - lo) | static_cast<unsigned>(base - begin + 128 * k + 4 * lane + q) << 10;
     }
     if (blockIdx.x == 0) {
       auto out = [&](int v) { return v < -1 || v >= a.V; };
@@ -328,6 +343,33 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedBwd
     }
   }
   if (bad) raise_status(a.status, TW_EINVAL);
+  // what the warp owns, 32 in order at a time, to act(token - lo, position, how many of the token
+  // lie before it among them, all of them)
+  auto each_owned = [&](auto&& act) {
+    __syncwarp();
+    auto some = [&](bool here, int v, int i) {
+      const unsigned all = __ballot_sync(0xFFFFFFFFu, here);
+      if (here) {
+        const unsigned peers = __match_any_sync(all, v);
+        act(v, i, __popc(peers & before), peers, all);
+      }
+      __syncwarp();
+    };
+    if (listed <= kList) {
+      for (int i = 0; i < listed; i += 32) {
+        const unsigned e = i + lane < listed ? list[i + lane] : 0u;
+        some(i + lane < listed, e & 1023u, begin + static_cast<int>(e >> 10));
+      }
+    } else {
+      for (int base = begin; base < end; base += 32) {
+        const int v = base + lane < end ? a.tokens[base + lane] : -1;
+        if (__any_sync(0xFFFFFFFFu, own(v))) some(own(v), v - lo, base + lane);
+      }
+    }
+  };
+  each_owned([&](int v, int, int rank, unsigned peers, unsigned) {
+    if (rank == 0) mine[v] += __popc(peers);
+  });
   less = warp_sum_int(less);
   if (lane == 0) below[warp] = less;
   __syncthreads();
@@ -352,33 +394,14 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedBwd
   if (tid == range - 1) start[range] = at + total;
   if (blockIdx.x == gridDim.x - 1 && tid == kSortThreads - 1) *a.n_valid = at + total;
   __syncthreads();
-  for (int base = begin; base < end; base += 128 * kAhead) {
-    if (end - begin > 128 * kAhead) read(base);
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      if (!__any_sync(0xFFFFFFFFu, owns(t[k]))) continue;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {  // 32 positions in order, a lane each
-        const int from = 8 * q + (lane >> 2), j = lane & 3;
-        const int x = __shfl_sync(0xFFFFFFFFu, t[k].x, from), y = __shfl_sync(0xFFFFFFFFu, t[k].y, from);
-        const int z = __shfl_sync(0xFFFFFFFFu, t[k].z, from), w = __shfl_sync(0xFFFFFFFFu, t[k].w, from);
-        const int v = j == 0 ? x : j == 1 ? y : j == 2 ? z : w;
-        const unsigned act = __ballot_sync(0xFFFFFFFFu, own(v));
-        if (act == 0u) continue;
-        if (own(v)) {
-          const unsigned peers = __match_any_sync(act, v);
-          int* n = mine + (v - lo);
-          const int was = *n, slot = start[v - lo] + was + __popc(peers & ((1u << lane) - 1u));
-          __syncwarp(act);
-          if (lane == __ffs(peers) - 1) *n = was + __popc(peers);
-          a.pos[slot] = base + 128 * k + 32 * q + lane;
-          a.key[slot] = v;
-          a.run[slot] = make_int2(start[v - lo], start[v - lo + 1]);
-        }
-        __syncwarp();
-      }
-    }
-  }
+  each_owned([&](int v, int position, int rank, unsigned peers, unsigned all) {
+    const int was = mine[v], slot = start[v] + was + rank;
+    __syncwarp(all);
+    if (rank == 0) mine[v] = was + __popc(peers);
+    a.pos[slot] = position;
+    a.key[slot] = lo + v;
+    a.run[slot] = make_int2(start[v], start[v + 1]);
+  });
 }
 
 // ------------------------------------------------------------------ backward: sums
@@ -601,7 +624,7 @@ cudaError_t embed_bwd_as(EmbedBwdArgs a, cudaStream_t s) {
     return e;
   }
   const int ctas = (a.V + a.range - 1) / a.range;
-  const size_t smem = (static_cast<size_t>(kSortWarps + 1) * a.range + 1) * sizeof(int);
+  const size_t smem = (static_cast<size_t>(kSortWarps + 1) * a.range + 1 + kSortWarps * kList) * sizeof(int);
   e = allow_smem(embed_sort_kernel, smem);
   if (e != cudaSuccess) return e;
   if (a.add) a.present = nullptr;

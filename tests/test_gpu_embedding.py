@@ -123,6 +123,26 @@ def test_long_batches(T):
     assert status.item() == 0 and (np.abs(_f64(dw) - ref) <= (n + 2) * 2.0 ** -24 * mag).all()
 
 
+@pytest.mark.parametrize("V", [7, 2000, 60000])
+@pytest.mark.parametrize("offset", [0, 1])
+def test_batches_whose_stretches_differ(V, offset):
+    """One token's positions together, others' anywhere, and a stretch of padding: the parts that
+    the sort reads differ in how many of them belong to one range of tokens. Sums of small
+    integers are exact in every order."""
+    rng = np.random.default_rng(V + offset)
+    T, d = 30001, 9
+    tok = rng.integers(0, V, T)
+    tok[4000:14000], tok[20000:23000] = 5, -1
+    dy = rng.integers(-8, 9, (T, d))
+    both = torch.from_numpy(np.concatenate([np.zeros(offset, np.int32), tok.astype(np.int32)])).cuda()
+    dw, status = tw.embedding_bwd(torch.from_numpy(dy).to("cuda", F32), both[offset:], V)
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    ref = np.zeros((V, d), np.int64)
+    np.add.at(ref, tok[tok >= 0], dy[tok >= 0])
+    assert np.array_equal(dw.cpu().numpy().astype(np.int64), ref)
+
+
 @pytest.mark.parametrize("T", [6, 600])
 def test_tokens_outside_raise_and_are_read_as_none(T):
     rng = np.random.default_rng(4)

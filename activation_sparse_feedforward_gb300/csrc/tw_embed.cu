@@ -9,7 +9,7 @@
 // whole is mostly the zeros of the tokens that do not occur.
 //
 // Measured on one GB300 against the copy rate (6777 GB/s): forward of 16384 tokens, 2048
-// columns, fp32 table of 131072 rows, bf16 out 22.2 us for 123 MB (0.82); the gradient of the
+// columns, fp32 table of 131072 rows, bf16 out 21.0 us for 123 MB (0.87); the gradient of the
 // same, written whole, 166 us for 1.14 GB (a memset of the table alone takes 140); added to a
 // table of 5003 x 1027, 40009 positions of fp16, 51 us for 117 MB (0.34: the sort takes 10, the
 // sums of rows in no order 33, the join 8).
@@ -24,58 +24,60 @@ namespace tw {
 namespace {
 
 // ------------------------------------------------------------------ forward
-constexpr int kFwdThreads = 128, kFwdVecs = 4;  // a CTA's vectors of 16 bytes of y: 512, of one row
+// A CTA takes 512 vectors of 16 bytes of y, four a thread, all on their way at once: of several
+// rows where they are short (32768 rows of 64 bf16 4.9 us, a CTA each 34; 16384 of 2048 19.9
+// against 22.3; of 1027 fp16 20 against 28). Two vectors a thread are as fast where rows are
+// whole vectors, one a thread takes 1.2 to 1.9 times as long.
+constexpr int kFwdThreads = 128, kFwdVecs = 4;
 
-// E elements of a table row from column c on, widened
-template <int WT, int E, bool VEC>
-TW_DEV void load_row(const typename Elem<WT>::S* row, int c, int d, bool careful, float (&v)[E]) {
-  constexpr int EW = Elem<WT>::E;
-#pragma unroll
-  for (int k = 0; k < E / EW; ++k) {
-    float u[EW];
-    uint4 w = make_uint4(0, 0, 0, 0);
-    const int at = c + k * EW;
-    if (at < d) w = VEC ? __ldg(reinterpret_cast<const uint4*>(row + at)) : load_any<WT>(row + at, d - at, careful);
-    Elem<WT>::unpack(w, u);
-#pragma unroll
-    for (int i = 0; i < EW; ++i) v[k * EW + i] = u[i];
-  }
-}
-
+// per_row: threads' vectors of a row (off 16 bytes whole warps of them, since store_any wants a
+// warp's in one row); rows: of a CTA
 template <int DT, int WT, bool VEC>
-__global__ void __launch_bounds__(kFwdThreads) embed_fwd_kernel(const EmbedFwdArgs a) {
+__global__ void __launch_bounds__(kFwdThreads) embed_fwd_kernel(const EmbedFwdArgs a, int per_row, int rows) {
   using S = typename Elem<DT>::S;
   constexpr int E = Elem<DT>::E;
   pdl_enter();
-  const int t = blockIdx.x, first = blockIdx.y * kFwdThreads * kFwdVecs + threadIdx.x;
-  const int tok = a.tokens[t];
-  const bool valid = tok >= 0 && tok < a.V;
-  if (threadIdx.x == 0 && blockIdx.y == 0 && !valid && tok != -1) raise_status(a.status, TW_EINVAL);
-  const auto* row = static_cast<const typename Elem<WT>::S*>(a.w) + static_cast<size_t>(valid ? tok : 0) * a.ldw;
-  const bool careful = tok == 0 || tok == a.V - 1 || a.ldw < 8;
-  S* y = static_cast<S*>(a.y) + static_cast<size_t>(t) * a.ldy;
-  float v[kFwdVecs][E];
+  const int t0 = blockIdx.x * rows, first = blockIdx.y * kFwdThreads * kFwdVecs;
+  int at[kFwdVecs], col[kFwdVecs], tok[kFwdVecs];  // row (-1: none), column, token
 #pragma unroll
   for (int k = 0; k < kFwdVecs; ++k) {
-    const int c = (first + k * kFwdThreads) * E;
-    if (valid && c < a.d) {
-      load_row<WT, E, VEC>(row, c, a.d, careful, v[k]);
-    } else {
+    const int i = threadIdx.x + k * kFwdThreads, r = rows == 1 ? 0 : i / per_row;
+    at[k] = r < rows && t0 + r < a.T ? t0 + r : -1;
+    col[k] = (first + i - r * per_row) * E;
+    tok[k] = at[k] >= 0 ? a.tokens[at[k]] : -1;
+  }
+  constexpr int EW = Elem<WT>::E, NW = E / EW;  // the table's vectors of one of y
+  uint4 v[kFwdVecs][NW];
 #pragma unroll
-      for (int i = 0; i < E; ++i) v[k][i] = 0.f;
+  for (int k = 0; k < kFwdVecs; ++k) {
+    const bool valid = tok[k] >= 0 && tok[k] < a.V;
+    if (!valid && tok[k] != -1) raise_status(a.status, TW_EINVAL);
+    const bool careful = tok[k] == 0 || tok[k] == a.V - 1 || a.ldw < 8;
+    const auto* row = static_cast<const typename Elem<WT>::S*>(a.w) + static_cast<size_t>(valid ? tok[k] : 0) * a.ldw;
+#pragma unroll
+    for (int q = 0; q < NW; ++q) {
+      const int c = col[k] + q * EW;
+      v[k][q] = make_uint4(0, 0, 0, 0);
+      if (valid && c < a.d) v[k][q] = VEC ? __ldg(reinterpret_cast<const uint4*>(row + c)) : load_any<WT>(row + c, a.d - c, careful);
     }
   }
 #pragma unroll
   for (int k = 0; k < kFwdVecs; ++k) {
-    const int c = (first + k * kFwdThreads) * E;
+    if (at[k] < 0) continue;  // (off 16 bytes the whole warp)
     float2 u[E / 2];
 #pragma unroll
-    for (int i = 0; i < E / 2; ++i) u[i] = make_float2(v[k][2 * i] * a.scale, v[k][2 * i + 1] * a.scale);
+    for (int q = 0; q < NW; ++q) {
+      float x[EW];
+      Elem<WT>::unpack(v[k][q], x);
+#pragma unroll
+      for (int i = 0; i < EW / 2; ++i) u[q * EW / 2 + i] = make_float2(x[2 * i] * a.scale, x[2 * i + 1] * a.scale);
+    }
     const uint4 w = Elem<DT>::pack_pairs(u);
+    S* y = static_cast<S*>(a.y) + static_cast<size_t>(at[k]) * a.ldy + col[k];
     if (VEC) {
-      if (c < a.d) *reinterpret_cast<uint4*>(y + c) = w;
+      if (col[k] < a.d) *reinterpret_cast<uint4*>(y) = w;
     } else {
-      store_any<DT>(y + c, w, a.d - c, threadIdx.x & 31);
+      store_any<DT>(y, w, a.d - col[k], threadIdx.x & 31);
     }
   }
 }
@@ -606,9 +608,11 @@ bool rows16(const void* p, int64_t ld, int dtype) { return on16(p) && ld * stati
 
 template <int DT, int WT>
 cudaError_t embed_fwd(const EmbedFwdArgs& a, bool vec, cudaStream_t s) {
-  constexpr int per_cta = kFwdThreads * kFwdVecs * Elem<DT>::E;
-  const dim3 grid(a.T, (a.d + per_cta - 1) / per_cta);
-  const cudaError_t e = launch(vec ? embed_fwd_kernel<DT, WT, true> : embed_fwd_kernel<DT, WT, false>, grid, dim3(kFwdThreads), 0, s, a);
+  constexpr int per_cta = kFwdThreads * kFwdVecs;
+  const int vecs = (a.d + Elem<DT>::E - 1) / Elem<DT>::E, per_row = vec ? vecs : (vecs + 31) / 32 * 32, rows = std::max(1, per_cta / per_row);
+  const dim3 grid((a.T + rows - 1) / rows, (per_row + per_cta - 1) / per_cta);
+  const cudaError_t e =
+      launch(vec ? embed_fwd_kernel<DT, WT, true> : embed_fwd_kernel<DT, WT, false>, grid, dim3(kFwdThreads), 0, s, a, per_row, rows);
   trace_mark(s, "embed_fwd");
   return e;
 }

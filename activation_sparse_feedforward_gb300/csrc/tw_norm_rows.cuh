@@ -46,22 +46,38 @@ TW_DEV float reciprocal(float v) {
 // two values as e4m3, round to nearest even, NaN kept
 TW_DEV uint32_t fp8x2(float2 v) { return __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3); }
 
+// How rows lie (VEC below). WHOLE: they begin on 16 bytes and hold whole vectors. ANYWHERE:
+// anywhere, d is any, and a vector is put together from two (tw_rows.cuh). ALIKE: d is any,
+// and a row lies alike in all matrices, `lead` elements behind 16 bytes. Vectors are then the
+// aligned ones, whose elements before and behind the row read 0 and are not written; a team's
+// rows are 8 (fp32: 4) apart, or a multiple, so that they have one lead, and weights and column
+// sums keep their places in the threads. (RMS norm's alone: 65344 rows of 1027 bf16 forward 60
+// us, ANYWHERE 79; backward 145 and 186, in fp32 161 and 265.)
+enum Rows { ANYWHERE = 0, WHOLE = 1, ALIKE = 2 };
+
 // Elements of a row owned by a thread, 8 VPT of them as packed pairs: vectors of 16 bytes in
-// strides of the team, so that a warp's accesses are adjacent. VEC: rows begin on 16 bytes
-// and hold whole vectors; else rows lie anywhere and d is any, and a vector is put together
-// from two (tw_rows.cuh). What lies past the row reads 0. TPR: the
-// team's threads where they are a constant of the kernel (offsets are then immediates),
-// else 0.
-template <int DT, int VPT, bool VEC, int TPR>
+// strides of the team, so that a warp's accesses are adjacent. What lies past the row reads 0.
+// TPR: the team's threads where they are a constant of the kernel (offsets are then
+// immediates), else 0.
+template <int DT, int VPT, int VEC, int TPR>
 struct RowMap {
   using S = typename Elem<DT>::S;
   static constexpr int NE = 8 * VPT, NP = NE / 2;
   static constexpr int E = Elem<DT>::E, NV = NE / E;  // elements of a vector, vectors
-  int d, tid, tpr_;
-  TW_DEV RowMap(int d_, int tid_, int tpr) : d(d_), tid(tid_), tpr_(tpr) {}
+  int d, tid, tpr_, lead;
+  bool edge;  // (ALIKE) the warp has a vector that is not whole: the others skip what those need
+  TW_DEV RowMap(int d_, int tid_, int tpr, int lead_ = 0) : d(d_), tid(tid_), tpr_(tpr), lead(VEC == ALIKE ? lead_ : 0), edge(false) {
+    if constexpr (VEC == ALIKE) {
+      bool parts = false;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) parts = parts || (has(k * E) && !whole(k));
+      edge = __any_sync(0xFFFFFFFFu, parts);
+    }
+  }
   TW_DEV int tpr() const { return TPR > 0 ? TPR : tpr_; }
-  TW_DEV int col(int i) const { return (i / E * tpr() + tid) * E + i % E; }
+  TW_DEV int col(int i) const { return (i / E * tpr() + tid) * E + i % E - lead; }
   TW_DEV bool has(int i) const { return col(i / E * E) < d; }  // the element's vector is in the row, at least in part
+  TW_DEV bool whole(int k) const { return VEC == WHOLE || (col(k * E) >= 0 && col(k * E) + E <= d); }  // vector k in all
 
   static TW_DEV void widen16(const uint4& w, float2* v) {
     float2 u[Elem<DT>::E / 2];
@@ -76,7 +92,7 @@ struct RowMap {
     for (int k = 0; k < NV; ++k) {
       const int c = col(k * E);
       r[k] = make_uint4(0, 0, 0, 0);
-      if (VEC) {
+      if constexpr (VEC != ANYWHERE) {
         if (c < d) r[k] = *reinterpret_cast<const uint4*>(p + c);
       } else {
         if (c < d) r[k] = load_any<DT>(p + c, d - c, careful);
@@ -93,7 +109,20 @@ struct RowMap {
 #pragma unroll
       for (int e = 0; e < E / 2; ++e) u[e] = v[k * E / 2 + e];
       const int c = col(k * E);
-      if (VEC) {
+      if constexpr (VEC == ALIKE) {
+        union {
+          uint4 w;
+          S e[E];
+        } q;
+        q.w = Elem<DT>::pack_pairs(u);
+        if (!edge || whole(k)) {
+          if (c < d) *reinterpret_cast<uint4*>(p + c) = q.w;
+        } else if (c < d) {
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if (in(k * E + e)) p[c + e] = q.e[e];
+        }
+      } else if constexpr (VEC != ANYWHERE) {
         if (c < d) *reinterpret_cast<uint4*>(p + c) = Elem<DT>::pack_pairs(u);
       } else {
         store_any<DT>(p + c, Elem<DT>::pack_pairs(u), d - c, tid & 31);
@@ -108,7 +137,7 @@ struct RowMap {
       uint32_t w[E / 4];
 #pragma unroll
       for (int e = 0; e < E / 4; ++e) w[e] = fp8x2(v[k * E / 2 + 2 * e]) | fp8x2(v[k * E / 2 + 2 * e + 1]) << 16;
-      if (VEC) {
+      if (VEC == WHOLE || (VEC == ALIKE && (!edge || whole(k)) && (reinterpret_cast<uintptr_t>(p + c) & (E - 1)) == 0)) {
         if (c >= d) continue;
         if constexpr (E == 8)
           *reinterpret_cast<uint2*>(p + c) = make_uint2(w[0], w[1]);
@@ -117,7 +146,7 @@ struct RowMap {
       } else {
 #pragma unroll
         for (int e = 0; e < E; ++e)
-          if (c + e < d) p[c + e] = static_cast<uint8_t>(w[e / 4] >> (8 * (e % 4)));
+          if (in(k * E + e)) p[c + e] = static_cast<uint8_t>(w[e / 4] >> (8 * (e % 4)));
       }
     }
   }
@@ -126,13 +155,20 @@ struct RowMap {
     if (w == nullptr) {
 #pragma unroll
       for (int i = 0; i < NP; ++i) v[i] = both(fill);
-    } else if (wtype == DT) {
+    } else if (VEC != ALIKE && wtype == DT) {
       load(static_cast<const S*>(w), v);
+    } else if (wtype == DT) {
+      const S* p = static_cast<const S*>(w);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        v[i].x = in(2 * i) ? Elem<DT>::get(p[col(2 * i)]) : 0.f;
+        v[i].y = in(2 * i + 1) ? Elem<DT>::get(p[col(2 * i + 1)]) : 0.f;
+      }
     } else {
       const float* p = static_cast<const float*>(w);
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        if constexpr (VEC) {
+        if constexpr (VEC == WHOLE) {
           v[i] = has(2 * i) ? *reinterpret_cast<const float2*>(p + col(2 * i)) : both(0.f);
         } else {
           v[i].x = in(2 * i) ? p[col(2 * i)] : 0.f;
@@ -151,13 +187,14 @@ struct RowMap {
         for (int e = 0; e < E / 2; ++e) f(k * E / 2 + e);
       }
   }
-  TW_DEV bool in(int i) const { return col(i) < d; }
+  TW_DEV bool in(int i) const { return col(i) < d && (VEC != ALIKE || col(i) >= 0); }
   // 0 in the places past the row of a vector that is in it in part
   TW_DEV void trim(float2 (&v)[NP]) const {
-    if constexpr (VEC) return;
+    if constexpr (VEC == WHOLE) return;
+    if (VEC == ALIKE && !edge) return;
 #pragma unroll
     for (int k = 0; k < NV; ++k)
-      if (has(k * E) && !in(k * E + E - 1)) {
+      if (has(k * E) && (VEC == ALIKE ? !whole(k) : !in(k * E + E - 1))) {
 #pragma unroll
         for (int i = k * E / 2; i < (k + 1) * E / 2; ++i)
           v[i] = make_float2(in(2 * i) ? v[i].x : 0.f, in(2 * i + 1) ? v[i].y : 0.f);
@@ -238,7 +275,7 @@ TW_DEV float2 team_sum_max(float s, float m, float2* red, int team, int tpr, int
 // reads back its own NV vectors, so that the ring needs no barrier. Else the row's aligned 16
 // bytes as they lie in memory, copied by the whole team and read, two for a vector, after
 // its barrier.
-template <int DT, int VPT, bool VEC, int DEPTH, int TPR>
+template <int DT, int VPT, int VEC, int DEPTH, int TPR>
 struct Ring {
   using M = RowMap<DT, VPT, VEC, TPR>;
   using S = typename M::S;
@@ -252,10 +289,19 @@ struct Ring {
   // careful: see end_row
   TW_DEV void copy(const M& m, int stage, int t, const S* row, bool careful) const {
     uint4* to = place(m, stage, t);
-    if constexpr (VEC) {
+    if constexpr (VEC != ANYWHERE) {
 #pragma unroll
-      for (int k = 0; k < NV; ++k)
-        if (m.has(k * E)) cp_async16(to + k * m.tpr(), row + m.col(k * E));
+      for (int k = 0; k < NV; ++k) {
+        if (!m.has(k * E)) continue;
+        const S* p = row + m.col(k * E);
+        if (VEC == ALIKE && careful && m.edge && !m.whole(k)) {
+          S* q = reinterpret_cast<S*>(to + k * m.tpr());
+          for (int e = 0; e < E; ++e)
+            if (m.in(k * E + e)) q[e] = p[e];
+        } else {
+          cp_async16(to + k * m.tpr(), p);
+        }
+      }
     } else {
       const int lead = lead_of(row), end = lead + m.d;
       auto one = [&](int g) {
@@ -276,9 +322,10 @@ struct Ring {
   }
   TW_DEV void read(const M& m, int stage, int t, const S* row, float2 (&v)[M::NP]) const {
     const uint4* from = place(m, stage, t);
-    if constexpr (VEC) {
+    if constexpr (VEC != ANYWHERE) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) M::widen16(m.has(k * E) ? from[k * m.tpr()] : make_uint4(0, 0, 0, 0), v + k * E / 2);
+      m.trim(v);
     } else {
       const int lead = lead_of(row);
 #pragma unroll
@@ -310,8 +357,8 @@ constexpr int fwd_ctas(int threads, bool more) {
 }
 constexpr bool fwd_more(int kind, int dtype, bool vec, int depth) { return kind != LAYER_NORM && dtype != TW_F32 && vec && depth > 0; }
 
-template <int DT, int VPT, bool VEC, int DEPTH, int TPR, int MAXT, int KIND>
-__global__ void __launch_bounds__(MAXT, fwd_ctas(MAXT, fwd_more(KIND, DT, VEC, DEPTH))) norm_fwd_kernel(const NormFwdArgs a) {
+template <int DT, int VPT, int VEC, int DEPTH, int TPR, int MAXT, int KIND>
+__global__ void __launch_bounds__(MAXT, fwd_ctas(MAXT, fwd_more(KIND, DT, VEC == WHOLE, DEPTH))) norm_fwd_kernel(const NormFwdArgs a) {
   constexpr bool RMS = KIND != LAYER_NORM;
   using M = RowMap<DT, VPT, VEC, TPR>;
   using S = typename M::S;
@@ -322,8 +369,8 @@ __global__ void __launch_bounds__(MAXT, fwd_ctas(MAXT, fwd_more(KIND, DT, VEC, D
   const int tid = threadIdx.x, tpr = TPR > 0 ? TPR : blockDim.x, team = threadIdx.y, teams = TPR > 0 ? MAXT / TPR : blockDim.y;
   const int stride = gridDim.x * teams;
   int row = blockIdx.x * teams + team;
-  const M m(a.d, tid, tpr);
   auto at = [](const void* p, int64_t ld, int r) { return static_cast<const S*>(p) + static_cast<size_t>(r) * ld; };
+  const M m(a.d, tid, tpr, static_cast<int>((reinterpret_cast<uintptr_t>(at(a.x, a.ldx, row)) & 15u) / sizeof(S)));
   const Ring<DT, VPT, VEC, DEPTH, TPR> ring(smem, team, a.res != nullptr ? 2 : 1, m);
   auto fetch = [&](int stage, int r) {
     if (r < a.T) {
@@ -348,7 +395,7 @@ __global__ void __launch_bounds__(MAXT, fwd_ctas(MAXT, fwd_more(KIND, DT, VEC, D
   for (int stage = 0; row < a.T; row += stride) {
     float2 v[NP], u[NP];
     if constexpr (DEPTH > 0) {
-      if constexpr (VEC) cp_wait<DEPTH - 1>();  // else before the last row's second sum
+      if constexpr (VEC != ANYWHERE) cp_wait<DEPTH - 1>();  // else before the last row's second sum
       ring.read(m, stage, 0, at(a.x, a.ldx, row), v);
       if (a.res != nullptr) ring.read(m, stage, 1, at(a.res, a.ldres, row), u);
     } else {
@@ -457,7 +504,7 @@ __global__ void __launch_bounds__(MAXT, fwd_ctas(MAXT, fwd_more(KIND, DT, VEC, D
 // rows ahead in registers 53.7; with the partial sums in the threads' order 47.4; one row
 // ahead (below), a ring of four, 46.7, and 4096 x 8192, where one team has the SM to
 // itself, 49.7 in place of 55.8.
-template <int DT, int VPT, bool VEC, int DEPTH, int TPR, int MAXT, bool RMS>
+template <int DT, int VPT, int VEC, int DEPTH, int TPR, int MAXT, bool RMS>
 __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwdArgs a) {
   using M = RowMap<DT, VPT, VEC, TPR>;
   using S = typename M::S;
@@ -469,8 +516,8 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwdArgs a) {
   const int stride = gridDim.x * teams;
   const int first = blockIdx.x * teams + team;
   int row = first;
-  const M m(a.d, tid, tpr);
   auto at = [](const void* p, int64_t ld, int r) { return static_cast<const S*>(p) + static_cast<size_t>(r) * ld; };
+  const M m(a.d, tid, tpr, static_cast<int>((reinterpret_cast<uintptr_t>(at(a.x, a.ldx, row)) & 15u) / sizeof(S)));
   const Ring<DT, VPT, VEC, DEPTH, TPR> ring(smem, team, a.dres != nullptr ? 3 : 2, m);
   auto fetch = [&](int stage, int r) {
     if (r < a.T) {
@@ -547,7 +594,7 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwdArgs a) {
       }
       if (row + stride < a.T) {
         float2 x[NP], g[NP];
-        if constexpr (VEC) cp_wait<DEPTH - 2>();
+        if constexpr (VEC != ANYWHERE) cp_wait<DEPTH - 2>();
         ring.read(m, next, 0, at(a.x, a.ldx, row + stride), x);
         ring.read(m, next, 1, at(a.dy, a.lddy, row + stride), g);
         part = sums(x, g, mean_next, rstd_next, red[flip ^ 1][team]);
@@ -562,7 +609,7 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwdArgs a) {
         g[i] = mul2(g[i], w[i]);
       }
       finish(x, g, more, c, rstd, row);
-      if constexpr (VEC) fetch(stage, row + DEPTH * stride);
+      if constexpr (VEC != ANYWHERE) fetch(stage, row + DEPTH * stride);
       stage = next;
       mean = mean_next, rstd = rstd_next;
       mean_next = mean_2, rstd_next = rstd_2;
@@ -606,8 +653,17 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwdArgs a) {
     cp_wait<0>();
     __syncthreads();
   }
+  if constexpr (VEC == ALIKE) {  // the places of the columns without a lead; lanes' are neighbours here too
+#pragma unroll
+    for (int i = 0; i < 2 * NP; ++i) {
+      constexpr int E = M::E;
+      const int back = m.lead > i % E ? 1 : 0, g = i / E * tpr + tid - back, e = i % E - m.lead + back * E;
+      if (m.in(i)) acc[(g / tpr * E + e) * tpr + g % tpr] = i % 2 ? dw[i / 2].y : dw[i / 2].x;
+    }
+  }
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
+    if constexpr (VEC == ALIKE) break;
     acc[2 * i * tpr + tid] = dw[i].x;
     acc[(2 * i + 1) * tpr + tid] = dw[i].y;
     if constexpr (!RMS) {
@@ -631,7 +687,7 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwdArgs a) {
 // more (from L2) over 16 warps, joined in order.
 constexpr int kFewThreads = 512, kFewWarps = kFewThreads / 32, kFewColumns = 256;
 
-template <int DT, int VPT, bool VEC, bool RMS>
+template <int DT, int VPT, int VEC, bool RMS>
 __global__ void __launch_bounds__(kFewThreads) norm_bwd_few_kernel(const NormBwdArgs a, int tpr, int row_ctas) {
   using S = typename Elem<DT>::S;
   __shared__ float2 red[kMaxTeams + 1][32];
@@ -757,18 +813,26 @@ cudaError_t launch_norm(Kern kern, int grid, const Team& t, size_t smem, const c
 size_t ring_bytes(int dtype, int vpt, const Team& t, int depth, int tensors, bool vec) {
   return t.teams * depth * tensors * (t.tpr * 8 * vpt * elem_size(dtype) + (vec ? 0 : 16));
 }
-template <int KIND, int DT, int TPR, int MAXT, int VPT = 2, bool VEC = true>
+// Of `want` CTAs (at most `most`) of so many teams: as many as make a team's rows a multiple of a
+// vector's elements apart where they have to be.
+int grid_of(int want, int most, int teams, int dtype, int vec) {
+  if (vec != ALIKE) return std::min(want, most);
+  int step = dtype == TW_F32 ? 4 : 8;
+  while (step > 1 && teams % 2 == 0) step /= 2, teams /= 2;
+  return std::max(step, std::min((want + step - 1) / step * step, most / step * step));
+}
+template <int KIND, int DT, int TPR, int MAXT, int VPT = 2, int VEC = WHOLE>
 cudaError_t norm_fwd_ring(const NormFwdArgs& a, cudaStream_t s) {
   constexpr int kTeams = MAXT / TPR;
   const size_t smem = ring_bytes(DT, VPT, Team{TPR, kTeams}, 3, a.res != nullptr ? 2 : 1, VEC);
   // as many CTAs as stay resident
   const int fit = static_cast<int>(kSmemMost / (smem + 6 * 1024));
-  const int per_sm = std::max(1, std::min(fwd_ctas(MAXT, fwd_more(KIND, DT, VEC, 3)), fit));
+  const int per_sm = std::max(1, std::min(fwd_ctas(MAXT, fwd_more(KIND, DT, VEC == WHOLE, 3)), fit));
   return launch_norm(norm_fwd_kernel<DT, VPT, VEC, 3, TPR, MAXT, KIND>,
-                     std::min((a.T + kTeams - 1) / kTeams, device_sm_count() * per_sm), Team{TPR, kTeams}, smem,
+                     grid_of((a.T + kTeams - 1) / kTeams, device_sm_count() * per_sm, kTeams, DT, VEC), Team{TPR, kTeams}, smem,
                      "norm_fwd", a, s);
 }
-template <int KIND, int DT, int VPT, bool VEC, int MAXT>
+template <int KIND, int DT, int VPT, int VEC, int MAXT>
 cudaError_t norm_fwd_direct(const NormFwdArgs& a, cudaStream_t s) {
   const Team t = team_of(a.d, VPT, MAXT <= 256 ? 256 : 32, a.T);
   return launch_norm(norm_fwd_kernel<DT, VPT, VEC, 0, 0, MAXT, KIND>,
@@ -782,21 +846,22 @@ cudaError_t norm_bwd_finish(const NormBwdArgs& a, int sums, int partials, int wi
   return e;
 }
 
-template <bool RMS, int DT, int VPT, bool VEC, int DEPTH, int TPR, int MAXT>
+template <bool RMS, int DT, int VPT, int VEC, int DEPTH, int TPR, int MAXT>
 cudaError_t norm_bwd(const NormBwdArgs& a, const Team& t, cudaStream_t s) {
   using M = RowMap<DT, VPT, VEC, TPR>;
   constexpr int kSums = RMS ? 1 : 2;
-  const int grid = std::min({(a.T + t.teams - 1) / t.teams, device_sm_count(), kNormPartials}), width = M::NE * t.tpr;
+  const int grid = grid_of((a.T + t.teams - 1) / t.teams, std::min(device_sm_count(), kNormPartials), t.teams, DT, VEC);
+  const int width = M::NE * t.tpr;
   const size_t smem = std::max(ring_bytes(DT, VPT, t, DEPTH, a.dres != nullptr ? 3 : 2, VEC),
                                t.teams > 1 ? kSums * sizeof(float) * t.teams * width : size_t{0});
   const cudaError_t e = launch_norm(norm_bwd_kernel<DT, VPT, VEC, DEPTH, TPR, MAXT, RMS>, grid, t, smem, "norm_bwd", a, s);
   return e != cudaSuccess || a.part == nullptr ? e : norm_bwd_finish(a, kSums, grid, width, t.tpr, M::E, s);
 }
-template <bool RMS, int DT, int VPT, int TPR, int MAXT, int DEPTH, bool VEC = true>
+template <bool RMS, int DT, int VPT, int TPR, int MAXT, int DEPTH, int VEC = WHOLE>
 cudaError_t norm_bwd_ring(const NormBwdArgs& a, cudaStream_t s) {
   return norm_bwd<RMS, DT, VPT, VEC, DEPTH, TPR, MAXT>(a, Team{TPR, MAXT / TPR}, s);
 }
-template <bool RMS, int DT, int VPT, bool VEC, int MAXT>
+template <bool RMS, int DT, int VPT, int VEC, int MAXT>
 cudaError_t norm_bwd_direct(const NormBwdArgs& a, cudaStream_t s) {
   return norm_bwd<RMS, DT, VPT, VEC, 0, 0, MAXT>(a, team_of(a.d, VPT, MAXT, a.T), s);
 }
@@ -812,7 +877,7 @@ bool overlap(const NormBwdArgs& a, const void* p, int64_t ld) {
 // against 6 in two; the two meet between 250 (512 columns) and 430 rows (8192), and at 200
 // rows off 16 bytes.
 constexpr int kFewRows = 320, kFewRowsOff16 = 160;
-template <bool RMS, int DT, bool VEC>
+template <bool RMS, int DT, int VEC>
 cudaError_t norm_bwd_few(const NormBwdArgs& a, cudaStream_t s) {
   const int vpt = a.d <= 4096 ? 1 : 2;
   const int tpr = ((a.d + 8 * vpt - 1) / (8 * vpt) + 31) / 32 * 32, teams = std::min(kFewThreads / tpr, kMaxTeams);
@@ -830,26 +895,27 @@ cudaError_t norm_bwd_few(const NormBwdArgs& a, cudaStream_t s) {
 // columns 54.5 us (16 a thread 64.1), 5632 54.9 (61.9), but 6656 57.2 (52.3), 8192 79 (49.7);
 // fp32, 16.8 M: 5632 49.8 (64.2), 8192 59.6 (48.2). Forward without residual: bf16 5632 37.4
 // (27.5), 8192 33.2 (27.8); fp32 7168 23.2 (25.0).
-template <int KIND, int DT, bool VEC>
+template <int KIND, int DT, int VEC>
 cudaError_t norm_fwd_width(const NormFwdArgs& a, cudaStream_t s) {
-  if constexpr (VEC) {
-    if (a.d <= 16 * 32) return norm_fwd_ring<KIND, DT, 32, 256>(a, s);
-    if (a.d <= 16 * 64) return norm_fwd_ring<KIND, DT, 64, 256>(a, s);
-    if (a.d <= 16 * 96) return norm_fwd_ring<KIND, DT, 96, 192>(a, s);
-    if (a.d <= 16 * 128) return norm_fwd_ring<KIND, DT, 128, 256>(a, s);
-    if (a.d <= 16 * 160) return norm_fwd_ring<KIND, DT, 160, 320>(a, s);
-    if (a.d <= 16 * 192) return norm_fwd_ring<KIND, DT, 192, 192>(a, s);
-    if (a.d <= 16 * 256) return norm_fwd_ring<KIND, DT, 256, 256>(a, s);
-    if (a.d <= 16 * 320) return norm_fwd_ring<KIND, DT, 320, 320>(a, s);
-    if (a.d <= 16 * 384) return norm_fwd_ring<KIND, DT, 384, 384>(a, s);
+  if constexpr (VEC != ANYWHERE) {
+    const int d = VEC == ALIKE ? a.d + Elem<DT>::E - 1 : a.d;
+    if (d <= 16 * 32) return norm_fwd_ring<KIND, DT, 32, 256, 2, VEC>(a, s);
+    if (d <= 16 * 64) return norm_fwd_ring<KIND, DT, 64, 256, 2, VEC>(a, s);
+    if (d <= 16 * 96) return norm_fwd_ring<KIND, DT, 96, 192, 2, VEC>(a, s);
+    if (d <= 16 * 128) return norm_fwd_ring<KIND, DT, 128, 256, 2, VEC>(a, s);
+    if (d <= 16 * 160) return norm_fwd_ring<KIND, DT, 160, 320, 2, VEC>(a, s);
+    if (d <= 16 * 192) return norm_fwd_ring<KIND, DT, 192, 192, 2, VEC>(a, s);
+    if (d <= 16 * 256) return norm_fwd_ring<KIND, DT, 256, 256, 2, VEC>(a, s);
+    if (d <= 16 * 320) return norm_fwd_ring<KIND, DT, 320, 320, 2, VEC>(a, s);
+    if (d <= 16 * 384) return norm_fwd_ring<KIND, DT, 384, 384, 2, VEC>(a, s);
     if constexpr (DT == TW_F32) {
-      if (a.d <= 8 * 896) return norm_fwd_ring<KIND, DT, 896, 896, 1>(a, s);
-      if (a.d <= 8 * 1024) return norm_fwd_ring<KIND, DT, 1024, 1024, 1>(a, s);
+      if (d <= 8 * 896) return norm_fwd_ring<KIND, DT, 896, 896, 1, VEC>(a, s);
+      if (d <= 8 * 1024) return norm_fwd_ring<KIND, DT, 1024, 1024, 1, VEC>(a, s);
     } else {
-      if (a.d <= 16 * 448) return norm_fwd_ring<KIND, DT, 448, 448>(a, s);
-      if (a.d <= 16 * 512) return norm_fwd_ring<KIND, DT, 512, 512>(a, s);
+      if (d <= 16 * 448) return norm_fwd_ring<KIND, DT, 448, 448, 2, VEC>(a, s);
+      if (d <= 16 * 512) return norm_fwd_ring<KIND, DT, 512, 512, 2, VEC>(a, s);
     }
-    return norm_fwd_direct<KIND, DT, 2, true, 1024>(a, s);
+    return norm_fwd_direct<KIND, DT, 2, VEC == WHOLE ? WHOLE : ANYWHERE, 1024>(a, s);
   } else {
     if (a.d <= 16 * 32) return norm_fwd_ring<KIND, DT, 32, 256, 2, false>(a, s);
     if (a.d <= 16 * 64) return norm_fwd_ring<KIND, DT, 64, 256, 2, false>(a, s);
@@ -863,26 +929,27 @@ cudaError_t norm_fwd_width(const NormFwdArgs& a, cudaStream_t s) {
     return norm_fwd_direct<KIND, DT, 2, false, 1024>(a, s);
   }
 }
-template <bool RMS, int DT, bool VEC>
+template <bool RMS, int DT, int VEC>
 cudaError_t norm_bwd_width(const NormBwdArgs& a, cudaStream_t s) {
   // (its column sums read x and dy while rows of dx are written: not in place of them)
-  if (a.T <= (VEC ? kFewRows : kFewRowsOff16) && a.d <= 8192 && !overlap(a, a.x, a.ldx) && !overlap(a, a.dy, a.lddy))
-    return norm_bwd_few<RMS, DT, VEC>(a, s);
-  if constexpr (VEC) {
+  if (a.T <= (VEC == WHOLE ? kFewRows : kFewRowsOff16) && a.d <= 8192 && !overlap(a, a.x, a.ldx) && !overlap(a, a.dy, a.lddy))
+    return norm_bwd_few<RMS, DT, VEC == WHOLE ? WHOLE : ANYWHERE>(a, s);
+  if constexpr (VEC != ANYWHERE) {
+    const int d = VEC == ALIKE ? a.d + Elem<DT>::E - 1 : a.d;
     constexpr int kDepth = DT == TW_F32 ? 2 : 4;
-    if (a.d <= 16 * 32) return norm_bwd_ring<RMS, DT, 2, 32, 480, kDepth>(a, s);
-    if (a.d <= 16 * 64) return norm_bwd_ring<RMS, DT, 2, 64, 512, kDepth>(a, s);
-    if (a.d <= 16 * 96) return norm_bwd_ring<RMS, DT, 2, 96, 480, kDepth>(a, s);
-    if (a.d <= 16 * 128) return norm_bwd_ring<RMS, DT, 2, 128, 512, kDepth>(a, s);
-    if (a.d <= 16 * 160) return norm_bwd_ring<RMS, DT, 2, 160, 480, kDepth>(a, s);
-    if (a.d <= 16 * 256) return norm_bwd_ring<RMS, DT, 2, 256, 512, kDepth>(a, s);
-    if (a.d <= 8 * 640) return norm_bwd_ring<RMS, DT, 1, 640, 640, kDepth>(a, s);
-    if (a.d <= 8 * 704) return norm_bwd_ring<RMS, DT, 1, 704, 704, kDepth>(a, s);
+    if (d <= 16 * 32) return norm_bwd_ring<RMS, DT, 2, 32, 480, kDepth, VEC>(a, s);
+    if (d <= 16 * 64) return norm_bwd_ring<RMS, DT, 2, 64, 512, kDepth, VEC>(a, s);
+    if (d <= 16 * 96) return norm_bwd_ring<RMS, DT, 2, 96, 480, kDepth, VEC>(a, s);
+    if (d <= 16 * 128) return norm_bwd_ring<RMS, DT, 2, 128, 512, kDepth, VEC>(a, s);
+    if (d <= 16 * 160) return norm_bwd_ring<RMS, DT, 2, 160, 480, kDepth, VEC>(a, s);
+    if (d <= 16 * 256) return norm_bwd_ring<RMS, DT, 2, 256, 512, kDepth, VEC>(a, s);
+    if (d <= 8 * 640) return norm_bwd_ring<RMS, DT, 1, 640, 640, kDepth, VEC>(a, s);
+    if (d <= 8 * 704) return norm_bwd_ring<RMS, DT, 1, 704, 704, kDepth, VEC>(a, s);
     if constexpr (DT == TW_F32) {
-      if (a.d <= 8 * 896) return norm_bwd_ring<RMS, DT, 1, 896, 896, kDepth>(a, s);
+      if (d <= 8 * 896) return norm_bwd_ring<RMS, DT, 1, 896, 896, kDepth, VEC>(a, s);
     }
-    if (a.d <= 16 * 512) return norm_bwd_ring<RMS, DT, 2, 512, 512, kDepth>(a, s);
-    return norm_bwd_direct<RMS, DT, 2, true, 1024>(a, s);
+    if (d <= 16 * 512) return norm_bwd_ring<RMS, DT, 2, 512, 512, kDepth, VEC>(a, s);
+    return norm_bwd_direct<RMS, DT, 2, VEC == WHOLE ? WHOLE : ANYWHERE, 1024>(a, s);
   } else {
     constexpr int kVpt = DT == TW_F32 ? 1 : 2, kE = 8 * kVpt;
     if (a.d <= kE * 32) return norm_bwd_ring<RMS, DT, kVpt, 32, 480, 4, false>(a, s);
@@ -896,38 +963,62 @@ cudaError_t norm_bwd_width(const NormBwdArgs& a, cudaStream_t s) {
   }
 }
 
-// By the type, and by whether every row begins on 16 bytes (an 8-bit one on 8) and holds
-// whole vectors.
+// Whether rows of stride ld from p on lie as x's do, each as many bytes behind 16 (p null: yes).
+bool alike(const void* p, int64_t ld, const void* x, int64_t ldx, int dtype) {
+  return p == nullptr || (((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(x)) & 15u) == 0 && stride16(ld - ldx, dtype));
+}
+
+// By the type, and by how the rows lie: every one on 16 bytes (an 8-bit one on 8) and of whole
+// vectors, or all alike, or not. (An 8-bit row's scales of 128 columns want whole vectors.)
+template <int KIND, int DT>
+cudaError_t norm_fwd_rows(const NormFwdArgs& a, cudaStream_t s) {
+  bool vec = a.d % 8 == 0 && on16(a.x) && on16(a.res) && on16(a.sum) && on16(a.w) && on16(a.b) && stride16(a.ldx, DT) &&
+             stride16(a.ldres, DT) && stride16(a.ldsum, DT);
+  if constexpr (KIND == LAYER_NORM || KIND == RMS_NORM)
+    vec = vec && on16(a.y) && stride16(a.ldy, DT);
+  else
+    vec = vec && (reinterpret_cast<uintptr_t>(a.y) & 7u) == 0 && a.ldy % 8 == 0;
+  if (vec) return norm_fwd_width<KIND, DT, WHOLE>(a, s);
+  if constexpr (KIND == RMS_NORM || KIND == RMS_FP8_ROW) {
+    if (a.d <= 8192 - 8 && alike(a.res, a.ldres, a.x, a.ldx, DT) && alike(a.sum, a.ldsum, a.x, a.ldx, DT) &&
+        (KIND == RMS_FP8_ROW || alike(a.y, a.ldy, a.x, a.ldx, DT)))
+      return norm_fwd_width<KIND, DT, ALIKE>(a, s);
+  }
+  return norm_fwd_width<KIND, DT, ANYWHERE>(a, s);
+}
 template <int KIND>
 cudaError_t norm_fwd(const NormFwdArgs& a, cudaStream_t s) {
   if (a.T == 0) return cudaSuccess;
-  const int dt = a.dtype;
-  bool vec = a.d % 8 == 0 && on16(a.x) && on16(a.res) && on16(a.sum) && on16(a.w) && on16(a.b) && stride16(a.ldx, dt) &&
-             stride16(a.ldres, dt) && stride16(a.ldsum, dt);
-  if constexpr (KIND == LAYER_NORM || KIND == RMS_NORM)
-    vec = vec && on16(a.y) && stride16(a.ldy, dt);
-  else
-    vec = vec && (reinterpret_cast<uintptr_t>(a.y) & 7u) == 0 && a.ldy % 8 == 0;
-  switch (dt) {
-    case TW_F32: return vec ? norm_fwd_width<KIND, TW_F32, true>(a, s) : norm_fwd_width<KIND, TW_F32, false>(a, s);
-    case TW_BF16: return vec ? norm_fwd_width<KIND, TW_BF16, true>(a, s) : norm_fwd_width<KIND, TW_BF16, false>(a, s);
-    default: return vec ? norm_fwd_width<KIND, TW_F16, true>(a, s) : norm_fwd_width<KIND, TW_F16, false>(a, s);
+  switch (a.dtype) {
+    case TW_F32: return norm_fwd_rows<KIND, TW_F32>(a, s);
+    case TW_BF16: return norm_fwd_rows<KIND, TW_BF16>(a, s);
+    default: return norm_fwd_rows<KIND, TW_F16>(a, s);
   }
 }
 
+template <bool RMS, int DT>
+cudaError_t norm_bwd_rows(const NormBwdArgs& a, cudaStream_t s) {
+  const bool vec = a.d % 8 == 0 && on16(a.x) && on16(a.dy) && on16(a.dres) && on16(a.dx) && on16(a.w) &&
+                   stride16(a.ldx, DT) && stride16(a.lddy, DT) && stride16(a.lddres, DT) && stride16(a.lddx, DT);
+  if (vec) return norm_bwd_width<RMS, DT, WHOLE>(a, s);
+  if constexpr (RMS) {
+    // (512: the CTAs, rounded up, are not more than the rows, which the workspace is made for)
+    if (a.T >= 512 && a.d <= 8192 - 8 && alike(a.dy, a.lddy, a.x, a.ldx, DT) && alike(a.dres, a.lddres, a.x, a.ldx, DT) &&
+        alike(a.dx, a.lddx, a.x, a.ldx, DT))
+      return norm_bwd_width<RMS, DT, ALIKE>(a, s);
+  }
+  return norm_bwd_width<RMS, DT, ANYWHERE>(a, s);
+}
 template <bool RMS>
 cudaError_t norm_bwd_any(const NormBwdArgs& a, cudaStream_t s) {
   if (a.T == 0) {  // sums over no rows
     const int width = (a.d + 31) / 32 * 32;
     return a.dw != nullptr || a.db != nullptr ? norm_bwd_finish(a, RMS ? 1 : 2, 0, width, width, 1, s) : cudaSuccess;
   }
-  const int dt = a.dtype;
-  const bool vec = a.d % 8 == 0 && on16(a.x) && on16(a.dy) && on16(a.dres) && on16(a.dx) && on16(a.w) &&
-                   stride16(a.ldx, dt) && stride16(a.lddy, dt) && stride16(a.lddres, dt) && stride16(a.lddx, dt);
-  switch (dt) {
-    case TW_F32: return vec ? norm_bwd_width<RMS, TW_F32, true>(a, s) : norm_bwd_width<RMS, TW_F32, false>(a, s);
-    case TW_BF16: return vec ? norm_bwd_width<RMS, TW_BF16, true>(a, s) : norm_bwd_width<RMS, TW_BF16, false>(a, s);
-    default: return vec ? norm_bwd_width<RMS, TW_F16, true>(a, s) : norm_bwd_width<RMS, TW_F16, false>(a, s);
+  switch (a.dtype) {
+    case TW_F32: return norm_bwd_rows<RMS, TW_F32>(a, s);
+    case TW_BF16: return norm_bwd_rows<RMS, TW_BF16>(a, s);
+    default: return norm_bwd_rows<RMS, TW_F16>(a, s);
   }
 }
 

@@ -5,8 +5,10 @@
 //
 // The form of layer norm's forward (tw_norm.cu) with one sum, so one barrier, a row. Bound
 // by HBM: one GB300, 16384 x 2048 bf16 with residual, its sum and fp32 weights 44.8 us for
-// 268 MB (0.88 of the copy rate, 6777 GB/s). Rows off 16 bytes are bound by the instructions
-// that put their vectors together, at 0.35 to 0.47 of that rate.
+// 268 MB (0.88 of the copy rate, 6777 GB/s). Rows off 16 bytes that lie
+// alike in all matrices (a dense x, y, r of any width) run at 0.45 (515 columns bf16, where half
+// of a team's lanes have nothing) to 0.9 of that rate, others at 0.35 to 0.5, bound by the
+// instructions that put their vectors together.
 #include "tw_norm_rows.cuh"
 
 namespace tw {

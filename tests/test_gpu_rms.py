@@ -277,6 +277,73 @@ def test_in_place():
         _check_bwd(to, op.dweight, r, want, w, x, rstd, BF16)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("T,d", [(512, 9), (513, 250), (900, 515), (1300, 1027), (700, 2047), (600, 4101), (520, 6401), (530, 7160),
+                                 (520, 8183), (520, 8184), (515, 8185)])
+@pytest.mark.parametrize("offset,pad,in_place", [(0, 0, False), (3, 0, True), (5, 2, False), (1, 6, True)])
+def test_rows_that_lie_alike(dtype, T, d, offset, pad, in_place):
+    """Rows off 16 bytes at one offset and stride in all matrices, whose first and last 16 bytes
+    they share with their neighbours: what stands between rows (NaN) and in a row of NaN stays
+    out of the others, and nothing else is written."""
+    rng = np.random.default_rng(T + d + offset)
+    lib, dt, ld = tw.load(), CODE[dtype], d + pad
+    stream = torch.cuda.current_stream().cuda_stream
+    w = _rand(rng, d, dtype, 1, 0.3)
+
+    def rows(values, fill):
+        buf = torch.full((offset + T * ld + 8,), fill, dtype=dtype, device="cuda")
+        view = torch.as_strided(buf, (T, d), (ld, 1), offset)
+        if values is not None:
+            view.copy_(values)
+        return buf, view
+
+    def untouched(buf, view):
+        view.fill_(9.0)
+        return bool((buf == 9).all())
+
+    nan = float("nan")
+    vx, vr, vd = (_rand(rng, (T, d), dtype, 0.3, 1.5) for _ in range(3))
+    vx[7] = nan
+    keep = torch.arange(T, device="cuda") != 7
+    (_, x), (_, r), (sb, sm), (yb, y) = rows(vx, nan), rows(vr, nan), rows(None, 9.0), rows(None, 9.0)
+    rstd = torch.empty(T, device="cuda")
+    fwd = x.data_ptr(), ld, r.data_ptr(), ld, w.data_ptr(), T, d, EPS, dt, dt, sm.data_ptr(), ld
+    assert lib.tw_rms_norm_fwd(*fwd, y.data_ptr(), ld, rstd.data_ptr(), stream) == _lib.TW_OK
+    want = (vx.float() + vr.float()).to(dtype)
+    assert torch.equal(sm[keep], want[keep]) and torch.isnan(y[7]).all()
+    _check_fwd(y[keep], want[keep], w, rstd[keep], dtype)
+    assert untouched(yb, y)
+    qb, scales = torch.full((T, d + 3), 9, dtype=torch.uint8, device="cuda"), torch.empty((T, 1), device="cuda")
+    q = qb[:, :d]
+    assert lib.tw_rms_norm_fwd_fp8(*fwd, q.data_ptr(), d + 3, scales.data_ptr(), 0, rstd.data_ptr(), stream) == _lib.TW_OK
+    _check_fp8(q.contiguous()[keep].view(torch.float8_e4m3fn), scales[keep], want[keep], w, rstd[keep], 0)
+    assert (qb[:, d:] == 9).all()
+
+    # backward, of the rows without NaN; dx in the place of dy or of its own
+    want[7], rstd[7] = 0.5, 2.0
+    sm.copy_(want)
+    dres = rows(vr, nan)[1]
+    db, dy = rows(vd, 9.0 if in_place else nan)
+    if in_place:
+        dx = dy
+    else:
+        db, dx = rows(None, 9.0)
+    op = tw.RMSNorm(T, d, dtype=dtype)
+    code = lib.tw_rms_norm_bwd(dy.data_ptr(), ld, sm.data_ptr(), ld, rstd.data_ptr(), w.data_ptr(), dres.data_ptr(), ld, T, d, dt, dt,
+                               dx.data_ptr(), ld, op.dweight.data_ptr(), op.ws.data_ptr(), op.ws_bytes, stream)
+    assert code == _lib.TW_OK
+    assert not torch.isnan(dx).any() and not torch.isnan(op.dweight).any()
+    k = keep.nonzero()[:, 0]
+    X, DY, R, W = _f64(want), _f64(vd), _f64(rstd)[:, None], _f64(w)
+    xh = X * R
+    _close(op.dweight, (DY * xh).sum(0), (F + T * 2.0 ** -24) * (np.abs(DY) * np.abs(xh)).sum(0), "dweight")
+    g = DY * W
+    ref = R * (g - xh * (g * xh).mean(1, keepdims=True)) + _f64(vr)
+    terms = R * (np.abs(g) + np.abs(xh) * (np.abs(g) * np.abs(xh)).mean(1, keepdims=True)) + np.abs(_f64(vr))
+    _close(dx[k], ref[_f64(k).astype(int)], (U[dtype] * np.abs(ref) + F * terms + TINY[dtype])[_f64(k).astype(int)], "dx")
+    assert untouched(db, dx) and untouched(sb, sm)
+
+
 def test_captured_and_replayed():
     rng = np.random.default_rng(9)
     x, w, r = _rand(rng, (64, 512), BF16), _rand(rng, 512, BF16), _rand(rng, (64, 512), BF16)

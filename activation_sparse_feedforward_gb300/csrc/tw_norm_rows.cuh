@@ -26,11 +26,23 @@ TW_DEV float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-TW_DEV float warp_max_nan(float v, int lanes) {
+// over groups of `lanes` lanes, of which those of `mask` are here
+TW_DEV float warp_max_nan(float v, int lanes, unsigned mask = 0xFFFFFFFFu) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
-    if (o < lanes) v = max_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    if (o < lanes) v = max_nan(v, __shfl_xor_sync(mask, v, o));
   return v;
+}
+TW_DEV float lanes_sum(float v, int lanes, unsigned mask) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < lanes) v += __shfl_xor_sync(mask, v, o);
+  return v;
+}
+// A team's lanes of its warp. Short rows' teams are less than a warp, whose teams may leave
+// their rows' loop one after the other.
+TW_DEV unsigned team_lanes(int tpr) {
+  return tpr >= 32 ? 0xFFFFFFFFu : ((1u << (tpr & 31)) - 1u) << (threadIdx.y * tpr & 31);
 }
 // the scale that the largest magnitude fits with
 TW_DEV float fp8_scale(float most) {
@@ -219,6 +231,7 @@ TW_DEV float2 centred(float2 x, float mean) {
 // Sum over a team's threads, the same bits in each of them. `red` holds 32 values; a
 // caller alternates between two of them, so that one barrier per sum is enough.
 TW_DEV float team_sum(float v, float* red, int team, int tpr, int tid) {
+  if (tpr < 32) return lanes_sum(v, tpr, team_lanes(tpr));
   v = warp_sum(v);
   if (tpr == 32) return v;
   const int lane = tid & 31, warp = tid >> 5, warps = tpr >> 5;
@@ -230,9 +243,10 @@ TW_DEV float team_sum(float v, float* red, int team, int tpr, int tid) {
   return v;
 }
 // The same for two sums, in two halves: every warp gives its part, and after the team's
-// barrier each thread takes the total (tpr 32: the part is the total).
+// barrier each thread takes the total (tpr 32 and less: the part is the total).
 template <bool ONE>  // ONE: a is 0
 TW_DEV float2 give_sum2(float a, float b, float2* red, int tpr, int tid) {
+  if (tpr < 32) return make_float2(ONE ? a : lanes_sum(a, tpr, team_lanes(tpr)), lanes_sum(b, tpr, team_lanes(tpr)));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     if constexpr (!ONE) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
@@ -242,7 +256,7 @@ TW_DEV float2 give_sum2(float a, float b, float2* red, int tpr, int tid) {
   return make_float2(a, b);
 }
 TW_DEV float2 take_sum2(float2 own, const float2* red, int team, int tpr, int tid) {
-  if (tpr == 32) return own;
+  if (tpr <= 32) return own;
   const int lane = tid & 31, warps = tpr >> 5;
   team_barrier(team + 1, tpr);
   if (warps > 8) {
@@ -256,6 +270,7 @@ TW_DEV float2 take_sum2(float2 own, const float2* red, int team, int tpr, int ti
 
 // A sum and a maximum over a team's threads (NaN where one is), one barrier.
 TW_DEV float2 team_sum_max(float s, float m, float2* red, int team, int tpr, int tid) {
+  if (tpr < 32) return make_float2(lanes_sum(s, tpr, team_lanes(tpr)), warp_max_nan(m, tpr, team_lanes(tpr)));
   s = warp_sum(s);
   m = warp_max_nan(m, 32);
   if (tpr == 32) return make_float2(s, m);
@@ -456,7 +471,7 @@ __global__ void __launch_bounds__(MAXT, fwd_ctas(MAXT, fwd_more(KIND, DT, VEC ==
             float g = 0.f;
 #pragma unroll
             for (int e = k * E / 2; e < (k + 1) * E / 2; ++e) g = max_nan(g, max_nan(fabsf(v[e].x), fabsf(v[e].y)));
-            const float scale = fp8_scale(warp_max_nan(g, kLanes));
+            const float scale = fp8_scale(warp_max_nan(g, kLanes, team_lanes(tpr)));
             const int c = m.col(k * E);
             if (c < a.d && c % kFp8Group == 0) a.scales[r * groups + c / kFp8Group] = scale;
             const float inv = reciprocal(scale);
@@ -899,6 +914,15 @@ template <int KIND, int DT, int VEC>
 cudaError_t norm_fwd_width(const NormFwdArgs& a, cudaStream_t s) {
   if constexpr (VEC != ANYWHERE) {
     const int d = VEC == ALIKE ? a.d + Elem<DT>::E - 1 : a.d;
+    if constexpr (VEC == WHOLE && KIND != LAYER_NORM) {  // several rows a warp
+      if constexpr (KIND != RMS_FP8_GROUP) {  // (of 128 columns and less: by row)
+        if (d <= 16 * 4) return norm_fwd_ring<KIND, DT, 4, 256>(a, s);
+        if (d <= 16 * 8) return norm_fwd_ring<KIND, DT, 8, 256>(a, s);
+      }
+      if constexpr (KIND != RMS_FP8_GROUP || DT != TW_F32) {  // (16 lanes hold a group in 16 bits)
+        if (d <= 16 * 16) return norm_fwd_ring<KIND, DT, 16, 256>(a, s);
+      }
+    }
     if (d <= 16 * 32) return norm_fwd_ring<KIND, DT, 32, 256, 2, VEC>(a, s);
     if (d <= 16 * 64) return norm_fwd_ring<KIND, DT, 64, 256, 2, VEC>(a, s);
     if (d <= 16 * 96) return norm_fwd_ring<KIND, DT, 96, 192, 2, VEC>(a, s);
@@ -937,6 +961,11 @@ cudaError_t norm_bwd_width(const NormBwdArgs& a, cudaStream_t s) {
   if constexpr (VEC != ANYWHERE) {
     const int d = VEC == ALIKE ? a.d + Elem<DT>::E - 1 : a.d;
     constexpr int kDepth = DT == TW_F32 ? 2 : 4;
+    if constexpr (VEC == WHOLE && RMS) {  // several rows a warp
+      if (d <= 16 * 4) return norm_bwd_ring<RMS, DT, 2, 4, 512, kDepth>(a, s);
+      if (d <= 16 * 8) return norm_bwd_ring<RMS, DT, 2, 8, 512, kDepth>(a, s);
+      if (d <= 16 * 16) return norm_bwd_ring<RMS, DT, 2, 16, 512, kDepth>(a, s);
+    }
     if (d <= 16 * 32) return norm_bwd_ring<RMS, DT, 2, 32, 480, kDepth, VEC>(a, s);
     if (d <= 16 * 64) return norm_bwd_ring<RMS, DT, 2, 64, 512, kDepth, VEC>(a, s);
     if (d <= 16 * 96) return norm_bwd_ring<RMS, DT, 2, 96, 480, kDepth, VEC>(a, s);
@@ -989,6 +1018,9 @@ cudaError_t norm_fwd_rows(const NormFwdArgs& a, cudaStream_t s) {
 template <int KIND>
 cudaError_t norm_fwd(const NormFwdArgs& a, cudaStream_t s) {
   if (a.T == 0) return cudaSuccess;
+  if constexpr (KIND == RMS_FP8_GROUP) {
+    if (a.d <= kFp8Group) return norm_fwd<RMS_FP8_ROW>(a, s);
+  }
   switch (a.dtype) {
     case TW_F32: return norm_fwd_rows<KIND, TW_F32>(a, s);
     case TW_BF16: return norm_fwd_rows<KIND, TW_BF16>(a, s);

@@ -8,7 +8,8 @@
 // 268 MB (0.88 of the copy rate, 6777 GB/s). Rows off 16 bytes that lie
 // alike in all matrices (a dense x, y, r of any width) run at 0.45 (515 columns bf16, where half
 // of a team's lanes have nothing) to 0.9 of that rate, others at 0.35 to 0.5, bound by the
-// instructions that put their vectors together.
+// instructions that put their vectors together. Rows of up to 256 columns go several to a warp:
+// 1048576 of 64 bf16 46 us (0.86; with a warp each 147).
 #include "tw_norm_rows.cuh"
 
 namespace tw {

@@ -77,7 +77,7 @@ def _check_fp8(q, scales, s, w, rstd, group):
 SHAPES = [(1, 1), (1, 7), (2, 31), (3, 256), (5, 1027), (77, 2048), (130, 2047), (17, 4096), (9, 8192), (6, 8200),
           (3, 16384), (700, 512), (2000, 96), (330, 1000), (400, 2040), (350, 4096), (330, 5632), (330, 8192), (330, 9000),
           (100, 1027), (90, 8199), (321, 16384), (2500, 500), (1100, 1288), (700, 2400), (330, 2600), (330, 5120), (340, 6400),
-          (330, 7168)]
+          (330, 7168), (1, 64), (13, 128), (4001, 64), (1203, 128), (3331, 120), (2505, 200), (1027, 256), (90001, 8)]
 TYPES = [(BF16, F32, True), (BF16, BF16, False), (F16, F16, True), (F32, F32, False), (F16, F32, False), (F32, F32, True)]
 
 
@@ -275,6 +275,29 @@ def test_in_place():
         assert lib.tw_rms_norm_bwd(dy.data_ptr(), d, xi.data_ptr(), d, rstd.data_ptr(), w.data_ptr(), dres.data_ptr(), d, T, d, 1, 1,
                                    to.data_ptr(), d, op.dweight.data_ptr(), op.ws.data_ptr(), op.ws_bytes, stream) == _lib.TW_OK
         _check_bwd(to, op.dweight, r, want, w, x, rstd, BF16)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [8, 64, 72, 128, 256])
+def test_short_rows_of_one_warp_know_nothing_of_each_other(dtype, d):
+    """Rows of NaN and of zeros next to others, at every number of rows that leaves a warp in part."""
+    rng = np.random.default_rng(d)
+    full, w = _rand(rng, (345, d), dtype, 0.3, 1.5), _rand(rng, d, dtype, 1, 0.3)
+    full[3], full[5] = float("nan"), 0.0
+    dy = _rand(rng, (345, d), dtype)
+    for T in (*range(321, 346), 1, 2, 6, 17):
+        x, op = full[:T], tw.RMSNorm(T, d, dtype=dtype, eps=EPS)
+        keep = torch.arange(T, device="cuda") != 3
+        y, _ = op.forward(x, w)
+        _check_fwd(y[keep], x[keep], w, op.rstd[keep], dtype)
+        assert T <= 3 or torch.isnan(y[3]).all()
+        op8 = tw.RMSNorm(T, d, dtype=dtype, eps=EPS, fp8=True, group=128, backward=False)
+        q, scales, _ = op8.forward_fp8(x, w)
+        _check_fp8(q.view(torch.uint8)[keep].view(torch.float8_e4m3fn), scales[keep], x[keep], w, op8.rstd[keep], 128)
+        clean = torch.where(torch.isnan(x), torch.full_like(x, 0.25), x)
+        op.forward(clean, w)
+        dx, dw = op.backward(dy[:T], clean, w)
+        _check_bwd(dx, dw, dy[:T], clean, w, None, op.rstd, dtype)
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])

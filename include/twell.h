@@ -488,7 +488,8 @@ size_t tw_rms_norm_bwd_workspace_size(int T, int d);
 /* Root-mean-square norm backward. x is what the forward normalised (its `sum` when it added
  * a residual). With xh = x rstd, g = dy weight:
  *   dx = rstd (g - xh sum(g xh) / d) + dres,  dweight = sum over rows of dy xh
- * Arguments, in-place forms, order of the sums and limits as tw_layer_norm_bwd. */
+ * Arguments, in-place forms, order of the sums and limits as tw_layer_norm_bwd; the order also
+ * depends on whether rows begin as many bytes behind 16 in every matrix. */
 tw_status tw_rms_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const float* rstd,
                           const void* weight, const void* dres, int64_t lddres, int T, int d, int dtype, int wtype,
                           void* dx, int64_t lddx, float* dweight, void* ws, size_t ws_bytes, void* stream);

@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedBwd
 }
 
 // ------------------------------------------------------------------ backward: sums
-// Each warp takes `chunk` sorted positions, whatever tokens they are, and 256 columns: frequent
+// Each warp takes `chunk` sorted positions (16; short batches 4 or 8), whatever tokens they are, and 256 columns: frequent
 // tokens cost no more than rare ones. A run of up to kWhole positions is the warp's that has its
 // first, to its end; of a longer one over several chunks the part here is kept: at the chunk's
 // head (a run that began before) or its tail (one that begins here and goes on).
@@ -654,15 +654,22 @@ cudaError_t embed_bwd(const EmbedBwdArgs& a, cudaStream_t s) {
 }  // namespace
 
 constexpr int kMostChunks = 4096;  // whole ones
+// Short batches go in chunks of 4 or 8 positions while those are no more warps than this, some
+// 40 an SM: a warp's sums are added to their rows one after the other (added, 4096 positions of
+// 1027 fp16 19.4 us, 28.5 in chunks of 16; 2000 of 2048 bf16 16.8, 28.3; at 3000 warps 21.8
+// and 20.4, at 12000 the same).
+constexpr int kFewWarps = 6000;
 
 EmbedBwdPlan embed_bwd_plan(int T, int V, int d) {
   EmbedBwdPlan p{};
   if (T <= kFewTokens) return p;
   // tokens of a sorting CTA: whole words of the bits that say which occur
   p.range = std::min(kMostRange, ((V + 151) / 152 + 31) / 32 * 32);
-  p.chunk = 16;
-  while (T / p.chunk > kMostChunks) p.chunk *= 2;
   p.part_ld = (d + kWarpCols - 1) / kWarpCols * kWarpCols;
+  const int parts = p.part_ld / kWarpCols;
+  p.chunk = 4;
+  while (p.chunk < 16 && T / p.chunk * parts > kFewWarps) p.chunk *= 2;
+  while (T / p.chunk > kMostChunks) p.chunk *= 2;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t was = at;
@@ -675,7 +682,8 @@ EmbedBwdPlan embed_bwd_plan(int T, int V, int d) {
   p.present = take((static_cast<size_t>(V) + kMostRange) / 8);
   // never less than for fewer tokens, whose smaller chunks may be more: whoever has room for T
   // has it for any number below
-  p.part = take(sizeof(float) * 2 * static_cast<size_t>(p.part_ld) * std::min((T + 15) / 16, kMostChunks + 1));
+  p.part = take(sizeof(float) * 2 * static_cast<size_t>(p.part_ld) *
+                std::min((T + 3) / 4, std::max(kFewWarps / parts + 2, std::min((T + 15) / 16, kMostChunks + 1))));
   p.bytes = at;
   return p;
 }

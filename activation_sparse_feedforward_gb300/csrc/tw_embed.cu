@@ -407,8 +407,8 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedBwd
 }
 
 // ------------------------------------------------------------------ backward: sums
-// Each warp takes `chunk` sorted positions (16; short batches 4 or 8), whatever tokens they are, and 256 columns: frequent
-// tokens cost no more than rare ones. A run of up to kWhole positions is the warp's that has its
+// Each warp takes `chunk` sorted positions (16; short batches 4 or 8), whatever tokens they
+// are, and 256 columns: frequent tokens cost no more than rare ones. A run of up to kWhole positions is the warp's that has its
 // first, to its end; of a longer one over several chunks the part here is kept: at the chunk's
 // head (a run that began before) or its tail (one that begins here and goes on).
 //

@@ -18,23 +18,29 @@
 //   apply   X' = q0 X + X B
 //
 // with q0 = a + b t + c t^2, q1 = b + 2 c t: the step's polynomial written around t. Any t
-// gives the same X'. With t = 1 once the singular values have come near 1 (from the fourth
-// step on) the terms are small instead of cancelling (3.44 - 4.78 + 2.03 at 1), and so are
-// their roundings.
+// gives the same X'. With t = 1 the terms are small where singular values are near 1, instead
+// of cancelling (3.44 - 4.78 + 2.03), and so are their roundings; but where they are near 0 B is
+// -b - c = 2.74, and the rounding of X's hi enters there, which each later step multiplies by
+// a = 3.44. So t is 1 in a call's last step alone (from the fourth on), and else 0.
 //
 // Operands of the products are fp16 (11 bits; bf16's 8 leave errors of 1e-2) scaled by
 // powers of two into its range, sums fp32 in TMEM. X itself is kept as hi + lo, two fp16
 // of 22 bits: the products read hi, the term q0 X reads both. Roundings of X would
 // otherwise be amplified as the small singular values are (up to 3.44 a step), while in
-// X B they meet B's small rows. Against the definition in 64 bits, in the 2-norm: 4e-4 to
-// 1.3e-3 for spectra over up to four decades (hi alone: up to 2.4e-2).
+// X B they meet B's small rows. What B's diagonal, its largest elements, loses to fp16 is kept
+// in fp32, and apply adds X's columns times that: else the most of the error where X is near
+// orthogonal. Relative to the definition in 64 bits, both norms Frobenius's, five steps, in a
+// numpy model of these roundings: 0.5e-3 to 1.5e-3 from 64 rows and columns on, whatever the rank
+// and for spectra over up to four decades (hi alone: up to 1e-2; t = 1 from the fourth step on:
+// 2.6e-3 at rank 1 to 77, and 0.1 at eight steps). The diagonal costs 1 us a step of a small
+// matrix (704 x 256, five steps: 105 us without, 110 with).
 //
 // Large matrices are bound by the tensor cores under the board's power: on one GB300 three of
 // 5632 x 2048, fp32 gradients and momentum, five steps take 1.05 ms for 1.19e12 operations,
 // 1130 TFLOP/s over all (0.65 of the sustained 1736): some 110 us are the way in (bytes), and of
 // the products' the pairs spend 0.89 in MMAs, at 1340 W and 1.85 GHz. Small ones are bound by
-// the latency of 15 products that wait for one another: 704 x 256 takes 107 us, two of
-// 1027 x 2500 265.
+// the latency of 15 products that wait for one another: 704 x 256 takes 110 us, two of
+// 1027 x 2500 273.
 #include <cuda.h>
 
 #include <algorithm>
@@ -59,7 +65,8 @@ constexpr int kOperandBytes = 128 * kBK * 2;  // a CTA's 128 rows of A, or its h
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kChunkBytes = 32 * 32 * 2;       // an epilogue warp's 32 rows x 32 columns of fp16
 constexpr int kStagingBytes = kEpiWarps * 4 * kChunkBytes;  // two buffers of two blocks a warp
-constexpr int kSmem = kStages * kStageBytes + kStagingBytes + 1024 + 512;
+constexpr int kFactorBytes = kEpiWarps * 32 * 4;
+constexpr int kSmem = kStages * kStageBytes + kStagingBytes + kFactorBytes + 1024 + 512;
 static_assert(kSmem <= 232448, "shared memory per CTA");
 constexpr int kGramLog2 = 12;      // E is stored times 2^12: |E| <= 4
 constexpr int kPolyLog2 = 10;      // B times 2^10: |B| <= 32
@@ -87,6 +94,7 @@ struct NsArgs {
   int* arrived;              // [count][slots][2][kEpiWarps], 0 between calls
   int* done;                 // [count][3]: blocks of warps finished, by Kind, over all steps; 0 at first
   int* next;                 // the next unit, 0 at first
+  float* diag;               // [count][np]: B's diagonal less its fp16, times 2^kPolyLog2
   int32_t* status;
   // GRAM: acc * f0 - f1 on the diagonal; SQUARE: e * f0 + acc * f1; APPLY: x * f0 + acc * f1
   float f0[kMostSteps][3], f1[kMostSteps][3];
@@ -162,6 +170,11 @@ TW_DEV void k_blocks(const NsArgs& p, const Unit& u, int& lo, int& hi) {
   const int total = (u.kind == GRAM ? p.mp : p.np) / kBK, chunk = (total + p.slices[u.kind] - 1) / p.slices[u.kind];
   lo = u.slice * chunk;
   hi = min(total, lo + chunk);
+}
+
+// `bytes` (a multiple of 16) of shared memory to p, both on 16 bytes, in the thread's bulk group.
+TW_DEV void bulk_store(void* p, const void* smem, int bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(p), "r"(smem_addr(smem)), "r"(bytes) : "memory");
 }
 
 TW_DEV int ld_acquire(const int* p) {
@@ -348,6 +361,7 @@ struct Blocks {
   const NsArgs& p;
   const Unit& u;
   uint8_t* staging;     // this warp's 8 KB
+  float* factors;       // and 32 numbers: (APPLY) of the chunk's columns of X
   uint64_t* bar;        // [2]
   int turn;             // phases of each that are over: chunk c completes phase turn + c / 2 of its buffer's
   int lane, base;       // base: the matrix's first row in the maps
@@ -388,13 +402,18 @@ struct Blocks {
         uint4 l = make_uint4(0, 0, 0, 0);
         if (KIND == APPLY) l = *piece(b1, lane, q);
         const uint32_t h[4] = {w.x, w.y, w.z, w.w}, m[4] = {l.x, l.y, l.z, l.w};
+        float f[8] = {f0, f0, f0, f0, f0, f0, f0, f0};
+        if (KIND == APPLY) {
+          const float4 a = reinterpret_cast<const float4*>(factors)[2 * q], b = reinterpret_cast<const float4*>(factors)[2 * q + 1];
+          f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+        }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           float2 x = half2_of(h[k]);
           if (KIND == APPLY) x = add2(x, half2_of(m[k]));
           const int at = 8 * q + 2 * k;
-          v[at] = fmaf(v[at], f1, x.x * f0);
-          v[at + 1] = fmaf(v[at + 1], f1, x.y * f0);
+          v[at] = fmaf(v[at], f1, x.x * f[2 * k]);
+          v[at + 1] = fmaf(v[at + 1], f1, x.y * f[2 * k + 1]);
         }
       }
     }
@@ -412,6 +431,17 @@ struct Blocks {
     uint32_t w[16];
 #pragma unroll
     for (int k = 0; k < 16; ++k) w[k] = pack_f16x2_rn(v[2 * k], v[2 * k + 1]);
+    if constexpr (KIND == SQUARE) {
+      if (row - lane == col) {  // a block on the diagonal, whose element here is column col + lane
+        float lost_here = 0.f;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const float2 h = half2_of(w[k / 2]);
+          if (k == lane) lost_here = v[k] - (k % 2 ? h.y : h.x);
+        }
+        factors[lane] = lost_here;
+      }
+    }
 #pragma unroll
     for (int q = 0; q < 4; ++q) *piece(b0, lane, q) = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
     if constexpr (KIND == APPLY) {
@@ -434,6 +464,7 @@ struct Blocks {
       tma_store_2d(to, b0, col, base + row);
       if (KIND == APPLY) tma_store_2d(&p.lo_block, b1, col, base + row);
       if (mirror) tma_store_2d(to, b1, row, base + col);
+      if (KIND == SQUARE && row == col) bulk_store(p.diag + static_cast<size_t>(u.mat) * p.np + row, factors, 32 * sizeof(float));
       bulk_commit();
     }
   }
@@ -441,13 +472,13 @@ struct Blocks {
 
 // One warp's 32 rows of half a unit's columns; false where a bounded wait ran out.
 template <int KIND>
-TW_DEV bool epilogue(const NsArgs& p, const Unit& u, uint8_t* staging, uint64_t* bar, int& turn, uint64_t* tfull,
+TW_DEV bool epilogue(const NsArgs& p, const Unit& u, uint8_t* staging, float* factors, uint64_t* bar, int& turn, uint64_t* tfull,
                      uint32_t parity, uint32_t tmem, int rank, int ew, Known& known, volatile int* abort_flag) {
   const int lane = threadIdx.x & 31, quarter = (ew + 2) & 3, half = ew >> 2;
   const int width = p.width[KIND], chunks = width / 64, slices = p.slices[KIND];
   int ti, tj;
   tile_at(p, u, ti, tj);
-  Blocks<KIND> blocks{p, u, staging, bar, turn, lane, u.mat * (KIND == APPLY ? p.mp : p.np), KIND != APPLY && tj * width / kTile != ti};
+  Blocks<KIND> blocks{p, u, staging, factors, bar, turn, lane, u.mat * (KIND == APPLY ? p.mp : p.np), KIND != APPLY && tj * width / kTile != ti};
   const int row = ti * kTile + rank * 128 + quarter * 32 + lane, col = tj * width + half * (width / 2);
   tmem += half * (width / 2) + (static_cast<uint32_t>(quarter * 32) << 16);
   int asked = 0, taken = 0;  // chunks
@@ -466,6 +497,15 @@ TW_DEV bool epilogue(const NsArgs& p, const Unit& u, uint8_t* staging, uint64_t*
     if (lane == 0) ok = wait_inputs(p, u, known, abort_flag) ? 1 : 0;
     if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) return false;
     if (slices == 1) ask(), ask();  // while the products run (a slice may have nothing to finish)
+  }
+  // of X's columns, a lane each (read past L1: another SM wrote it, before what lane 0 has waited for)
+  auto factor_at = [&](int c) {
+    return fmaf(__ldcg(p.diag + static_cast<size_t>(u.mat) * p.np + col + c * 32 + lane), p.f1[u.step][APPLY], p.f0[u.step][APPLY]);
+  };
+  [[maybe_unused]] float factor = 0.f;
+  if constexpr (KIND == APPLY) {
+    __syncwarp();
+    factor = factor_at(0);
   }
   if (lane == 0) ok = mbar_wait(tfull, parity, abort_flag, p.status) ? 1 : 0;
   if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) return drained();
@@ -523,6 +563,11 @@ TW_DEV bool epilogue(const NsArgs& p, const Unit& u, uint8_t* staging, uint64_t*
 #pragma unroll
       for (int k = 0; k < 32; ++k) v[k] = s[k];
     }
+    if constexpr (KIND == APPLY) {
+      factors[lane] = factor;
+      __syncwarp();
+      if (c + 1 < chunks) factor = factor_at(c + 1);
+    }
     if (!blocks.here(c, abort_flag)) return drained();
     taken = c + 1;
     blocks.put(c, row, col + c * 32, v);
@@ -550,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
   const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
   uint8_t* tiles = smem_raw + pad;
   uint8_t* staging = tiles + kStages * kStageBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(staging + kStagingBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + kStagingBytes + kFactorBytes);
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;
   uint64_t* tempty = tfull + 2;
@@ -697,11 +742,12 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
       const int buf = local & 1;
       const uint32_t t0 = tmem_base + static_cast<uint32_t>(buf * kTile);
       uint8_t* st = staging + ew * 4 * kChunkBytes;
+      float* factors = reinterpret_cast<float*>(staging + kStagingBytes) + ew * 32;
       uint64_t* bar = block_bars + 2 * ew;
       const uint32_t parity = (local >> 1) & 1u;
-      if (u.kind == GRAM) ok = epilogue<GRAM>(p, u, st, bar, turn, tfull + buf, parity, t0, rank, ew, known, abort_flag);
-      else if (u.kind == SQUARE) ok = epilogue<SQUARE>(p, u, st, bar, turn, tfull + buf, parity, t0, rank, ew, known, abort_flag);
-      else ok = epilogue<APPLY>(p, u, st, bar, turn, tfull + buf, parity, t0, rank, ew, known, abort_flag);
+      if (u.kind == GRAM) ok = epilogue<GRAM>(p, u, st, factors, bar, turn, tfull + buf, parity, t0, rank, ew, known, abort_flag);
+      else if (u.kind == SQUARE) ok = epilogue<SQUARE>(p, u, st, factors, bar, turn, tfull + buf, parity, t0, rank, ew, known, abort_flag);
+      else ok = epilogue<APPLY>(p, u, st, factors, bar, turn, tfull + buf, parity, t0, rank, ew, known, abort_flag);
       if (!ok) break;
       tc_fence_before_sync();
       __syncwarp();
@@ -985,7 +1031,7 @@ void form_of(int tiles, int kb, int& width, int& slices) {
 
 struct Layout {
   int mp, np, width[3], slices[3], slots;
-  size_t hi0, hi1, lo, e, b, part, arrived, counters, norms, bytes;
+  size_t hi0, hi1, lo, e, b, diag, part, arrived, counters, norms, bytes;
   int words() const { return static_cast<int>((norms - arrived) / 4); }  // arrived and the counters after it
 };
 Layout layout(int m, int n, int count) {
@@ -1005,6 +1051,7 @@ Layout layout(int m, int n, int count) {
   };
   const size_t x = static_cast<size_t>(count) * l.mp * l.np * 2, s = static_cast<size_t>(count) * l.np * l.np * 2;
   l.hi0 = take(x), l.hi1 = take(x), l.lo = take(x), l.e = take(s), l.b = take(s);
+  l.diag = take(static_cast<size_t>(count) * l.np * 4);
   l.part = take(static_cast<size_t>(count) * l.slots * kTile * kTile * 4);
   l.arrived = take(static_cast<size_t>(count) * l.slots * 2 * kEpiWarps * 4);
   l.counters = take(static_cast<size_t>(3 * count + 1) * 4);
@@ -1088,12 +1135,13 @@ cudaError_t launch_ortho(const OrthoArgs& o, cudaStream_t s) {
   for (int i = 0; i < 3; ++i) p.width[i] = l.width[i], p.slices[i] = l.slices[i];
   p.slots = l.slots, p.part = reinterpret_cast<float*>(ws + l.part), p.arrived = in.arrived;
   p.done = reinterpret_cast<int*>(ws + l.counters), p.next = p.done + 3 * o.count, p.status = o.status;
+  p.diag = reinterpret_cast<float*>(ws + l.diag);
   for (int i = 0; i < o.count; ++i) p.out[i] = o.out[i];
   p.ldo = o.ldo, p.rows = std::max(o.m, o.n), p.cols = std::min(o.m, o.n), p.otype = o.otype, p.transposed = wide;
   p.scale = static_cast<float>(std::ldexp(static_cast<double>(o.scale), -k)), p.beta = o.beta;
   for (int step = 0; step < o.steps; ++step) {
     const double a = o.coef[3 * step], b = o.coef[3 * step + 1], c = o.coef[3 * step + 2];
-    const double t = step >= 3 ? 1.0 : 0.0, q0 = a + b * t + c * t * t, q1 = b + 2.0 * c * t;
+    const double t = step >= 3 && step + 1 == o.steps ? 1.0 : 0.0, q0 = a + b * t + c * t * t, q1 = b + 2.0 * c * t;
     p.f0[step][GRAM] = std::ldexp(1.f, kGramLog2 - 2 * k), p.f1[step][GRAM] = static_cast<float>(std::ldexp(t, kGramLog2));
     p.f0[step][SQUARE] = static_cast<float>(std::ldexp(q1, kPolyLog2 - kGramLog2));
     p.f1[step][SQUARE] = static_cast<float>(std::ldexp(c, kPolyLog2 - 2 * kGramLog2));

@@ -591,10 +591,16 @@ size_t tw_orthogonalize_workspace_size(int m, int n, int count);
  * gradient (TW_EINVAL); columns of one larger matrix are apart. 1 <= steps <= 32; 1 <= count <= TW_ORTHO_MOST; min(m, n) <= 16384,
  * max(m, n) <= 2^20.
  * Precision: products of fp16 operands (11 bits) with fp32 sums, X kept to 22 bits between
- * them. With the usual coefficients (3.4445, -4.7750, 2.0315), 5 steps, out is within about
- * 1e-3 of the definition in the 2-norm. Coefficients have to keep the singular values below
- * 2, or fp16 may overflow. U's norm neither overflows nor underflows. An infinity or a NaN
- * in U makes out NaN. The same call gives the same bits on the same device.
+ * them. With the usual coefficients (3.4445, -4.7750, 2.0315), out before its rounding to otype
+ * is off from the definition, relative and in the Frobenius norm, by 0.5e-3 to 1.5e-3 after 5
+ * steps and 1e-3 to 2.5e-3 after 8, of any rank, where min(m, n) >= 64; in the 2-norm by two to
+ * three times that. Of few rows or columns one rounding is the whole error: 1e-3 to 2e-3 as a
+ * rule, to 2e-2 where a singular value comes out near 1.2. In directions where U's singular
+ * value is 0, roundings of 2^-23 are multiplied by the first coefficient each step, as they are
+ * in any arithmetic: at rank 1 to 8 4e-3 after 8 steps, 4e-2 after 10, 0.2 and more from 12 on.
+ * Coefficients have to keep the singular values below 2, or fp16 may overflow. U's norm neither
+ * overflows nor underflows. An infinity or a NaN in U makes out NaN. The same call gives the
+ * same bits on the same device.
  * Device condition: TW_ETIMEOUT as the FFN's products. */
 tw_status tw_orthogonalize(const void* const* grads, int64_t ldg, int gtype, float* const* buffers, int64_t ldbuf,
                            float momentum, int nesterov, int count, int m, int n, int steps, const float* coefficients,

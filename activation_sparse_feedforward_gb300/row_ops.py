@@ -333,7 +333,8 @@ class Embedding:
         self.dweight, self._backward = None, backward
         if backward:
             if dweight:
-                self.dweight = torch.empty((V, d), dtype=torch.float32, device=device)
+                # (zeros: the first call may be one that adds)
+                self.dweight = torch.zeros((V, d), dtype=torch.float32, device=device)
             self.ws_bytes = int(self._lib.tw_embedding_bwd_workspace_size(T, V, d))
             self.ws = _workspace(self.ws_bytes, device)
             self._to_bwd = _addresses(self.dweight, self.ws)
@@ -362,7 +363,7 @@ class Embedding:
     def backward(self, dy: torch.Tensor, tokens: torch.Tensor, out: torch.Tensor | None = None,
                  add: bool = False) -> torch.Tensor:
         """The table's gradient [V, d] float32, written whole, or added to what `out` (or the
-        object's dweight) holds."""
+        object's dweight, zeros at first) holds."""
         if not self._backward:
             raise ValueError("this Embedding was made with backward=False")
         n, t = self._tokens(tokens)
@@ -388,7 +389,9 @@ def embedding_fwd(tokens, weight, scale: float = 1.0, dtype: torch.dtype | None 
 
 
 def embedding_bwd(dy, tokens, V: int, scale: float = 1.0, out=None, add: bool = False):
-    """One-shot backward. Returns (dweight [V, d] float32, status)."""
+    """One-shot backward. Returns (dweight [V, d] float32, status). add needs `out`."""
+    if add and out is None:
+        raise ValueError("add needs `out`")
     op = Embedding(tokens.numel(), V, dy.shape[1], dy.dtype, scale=scale, dweight=out is None, device=dy.device)
     return op.backward(dy, tokens, out, add), op.status
 

@@ -1084,6 +1084,7 @@ tw_status tw_orthogonalize(const void* const* grads, int64_t ldg, int gtype, flo
     for (int j = 0; j < count; ++j) {
       if (j < i && overlap({out[i], ldo, osize}, {out[j], ldo, osize}, m, n)) return TW_EINVAL;
       if (buffers == nullptr) continue;
+      if (overlap({buffers[i], ldbuf, 4}, {out[j], ldo, osize}, m, n)) return TW_EINVAL;
       if (j < i && overlap({buffers[i], ldbuf, 4}, {buffers[j], ldbuf, 4}, m, n)) return TW_EINVAL;
       if (overlap({buffers[i], ldbuf, 4}, {grads[j], ldg, gsize}, m, n)) return TW_EINVAL;
     }

@@ -588,8 +588,8 @@ size_t tw_orthogonalize_workspace_size(int m, int n, int count);
  * grads, buffers, out, coefficients [3 steps]: host arrays; the matrices they name are on
  * the device, with row strides of at least n elements: grads of type gtype, buffers fp32,
  * out of type otype. No two buffers and no two results may share memory, nor a buffer and a
- * gradient (TW_EINVAL); columns of one larger matrix are apart. 1 <= steps <= 32; 1 <= count <= TW_ORTHO_MOST; min(m, n) <= 16384,
- * max(m, n) <= 2^20.
+ * gradient, nor a buffer and a result (TW_EINVAL); columns of one larger matrix are apart.
+ * 1 <= steps <= 32; 1 <= count <= TW_ORTHO_MOST; min(m, n) <= 16384, max(m, n) <= 2^20.
  * Precision: products of fp16 operands (11 bits) with fp32 sums, X kept to 22 bits between
  * them. With the usual coefficients (3.4445, -4.7750, 2.0315), out before its rounding to otype
  * is off from the definition, relative and in the Frobenius norm, by 0.5e-3 to 1.5e-3 after 5

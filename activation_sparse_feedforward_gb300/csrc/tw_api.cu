@@ -844,9 +844,7 @@ tw_status tw_layer_norm_fwd(const void* x, int64_t ldx, const void* res, int64_t
 }
 
 size_t tw_layer_norm_bwd_workspace_size(int T, int d) {
-  if (T <= 0 || d <= 0) return 0;
-  return sizeof(float) * 2 * static_cast<size_t>(tw::norm_partial_width(d)) *
-         static_cast<size_t>(T < tw::kNormPartials ? T : tw::kNormPartials);
+  return T <= 0 || d <= 0 ? 0 : sizeof(float) * tw::norm_partial_floats(T, d, false);
 }
 
 tw_status tw_layer_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const float* mean,
@@ -923,7 +921,9 @@ tw_status tw_rms_norm_fwd_fp8(const void* x, int64_t ldx, const void* res, int64
   return from_cuda(tw::launch_rms_fp8(a, group, as_stream(stream)));
 }
 
-size_t tw_rms_norm_bwd_workspace_size(int T, int d) { return tw_layer_norm_bwd_workspace_size(T, d) / 2; }
+size_t tw_rms_norm_bwd_workspace_size(int T, int d) {
+  return T <= 0 || d <= 0 ? 0 : sizeof(float) * tw::norm_partial_floats(T, d, true);
+}
 
 tw_status tw_rms_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const float* rstd,
                           const void* weight, const void* dres, int64_t lddres, int T, int d, int dtype, int wtype,

@@ -389,21 +389,27 @@ struct NormBwdArgs {
   const float *mean, *rstd;
   void* dx;
   float *dw, *db;                 // may be null
-  float* part;                    // [kNormPartials][2][norm_partial_width(d)] fp32, null when dw and db are
+  float* part;                    // norm_partial_floats(T, d, false) of them, null when dw and db are
   int64_t lddy, ldx, lddres, lddx;
   int T, d;
   int dtype, wtype;
 };
 // The most CTAs whose partial sums over rows the backward keeps in its workspace.
 constexpr int kNormPartials = 512;
-// At least the columns of one partial, the elements of a team's threads for d columns.
-constexpr int norm_partial_width(int d) {
+// At least the columns of one partial, the elements of a team's threads for d columns. RMS norm's
+// rows off 16 bytes take the threads of up to 7 columns more (those before a row in its first
+// aligned vector).
+constexpr int norm_partial_width(int d, bool rms) {
+  if (rms) d += 7;
   int w = 1024;
   while (w < d && w < 8192) w *= 2;
   return d <= w ? w : (d + 511) / 512 * 512;
 }
+constexpr size_t norm_partial_floats(int T, int d, bool rms) {
+  return (rms ? 1 : 2) * static_cast<size_t>(norm_partial_width(d, rms)) * static_cast<size_t>(T < kNormPartials ? T : kNormPartials);
+}
 cudaError_t launch_norm_bwd(const NormBwdArgs& a, cudaStream_t s);
-cudaError_t launch_rms_bwd(const NormBwdArgs& a, cudaStream_t s);  // no mean and db; part [..][1][..]
+cudaError_t launch_rms_bwd(const NormBwdArgs& a, cudaStream_t s);  // no mean and db; part: norm_partial_floats(T, d, true)
 
 // ---------------------------------------------------------------- tw_logits.cu
 struct DistillArgs {

@@ -867,6 +867,7 @@ cudaError_t norm_bwd(const NormBwdArgs& a, const Team& t, cudaStream_t s) {
   constexpr int kSums = RMS ? 1 : 2;
   const int grid = grid_of((a.T + t.teams - 1) / t.teams, std::min(device_sm_count(), kNormPartials), t.teams, DT, VEC);
   const int width = M::NE * t.tpr;
+  if (a.part != nullptr && static_cast<size_t>(kSums) * grid * width > norm_partial_floats(a.T, a.d, RMS)) return cudaErrorInvalidValue;
   const size_t smem = std::max(ring_bytes(DT, VPT, t, DEPTH, a.dres != nullptr ? 3 : 2, VEC),
                                t.teams > 1 ? kSums * sizeof(float) * t.teams * width : size_t{0});
   const cudaError_t e = launch_norm(norm_bwd_kernel<DT, VPT, VEC, DEPTH, TPR, MAXT, RMS>, grid, t, smem, "norm_bwd", a, s);
@@ -1034,7 +1035,7 @@ cudaError_t norm_bwd_rows(const NormBwdArgs& a, cudaStream_t s) {
                    stride16(a.ldx, DT) && stride16(a.lddy, DT) && stride16(a.lddres, DT) && stride16(a.lddx, DT);
   if (vec) return norm_bwd_width<RMS, DT, WHOLE>(a, s);
   if constexpr (RMS) {
-    // (512: the CTAs, rounded up, are not more than the rows, which the workspace is made for)
+    // (512: the CTAs, rounded up, are not more than the rows, which the workspace has partials for)
     if (a.T >= 512 && a.d <= 8192 - 8 && alike(a.dy, a.lddy, a.x, a.ldx, DT) && alike(a.dres, a.lddres, a.x, a.ldx, DT) &&
         alike(a.dx, a.lddx, a.x, a.ldx, DT))
       return norm_bwd_width<RMS, DT, ALIKE>(a, s);

@@ -219,8 +219,8 @@ __global__ void __launch_bounds__(kThreads) embed_bwd_few_kernel(const EmbedBwdA
     if (blockIdx.y > 0) return;
     const int lo = (blockIdx.x - a.T) * kFillRows, rows = min(kFillRows, a.V - lo);
     for (int i = tid; i < a.T; i += kThreads) {
-      const int r = tok[i] - lo;
-      if (r >= 0 && r < rows) atomicOr(&same[r >> 5], 1u << (r & 31));
+      const unsigned r = static_cast<unsigned>(tok[i]) - static_cast<unsigned>(lo);
+      if (r < static_cast<unsigned>(rows)) atomicOr(&same[r >> 5], 1u << (r & 31));
     }
     __syncthreads();
     for (int r = 0; r < rows; ++r)
@@ -303,7 +303,8 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedBwd
         t[k] = make_int4(i < end ? p[0] : -1, i + 1 < end ? p[1] : -1, i + 2 < end ? p[2] : -1, i + 3 < end ? p[3] : -1);
     }
   };
-  auto own = [&](int v) { return static_cast<unsigned>(v - lo) < own_range; };
+  // (unsigned: any int may stand among the tokens)
+  auto own = [&](int v) { return static_cast<unsigned>(v) - static_cast<unsigned>(lo) < own_range; };
   read(begin);
   for (int i = tid; i < kSortWarps * range; i += kSortThreads) count[i] = 0;
   __syncthreads();
@@ -365,7 +366,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedBwd
     } else {
       for (int base = begin; base < end; base += 32) {
         const int v = base + lane < end ? a.tokens[base + lane] : -1;
-        if (__any_sync(0xFFFFFFFFu, own(v))) some(own(v), v - lo, base + lane);
+        if (__any_sync(0xFFFFFFFFu, own(v))) some(own(v), own(v) ? v - lo : 0, base + lane);
       }
     }
   };

@@ -401,6 +401,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedBwd
     const int was = mine[v], slot = start[v] + was + rank;
     __syncwarp(all);
     if (rank == 0) mine[v] = was + __popc(peers);
+    if (!TW_CHECKED(slot >= 0 && slot < a.T && position < a.T, a.status)) return;
     a.pos[slot] = position;
     a.key[slot] = lo + v;
     a.run[slot] = make_int2(start[v], start[v + 1]);
@@ -501,12 +502,14 @@ __global__ void __launch_bounds__(kThreads, 4) embed_sum_kernel(const EmbedBwdAr
   const int id = blockIdx.x * kWarps + (tid >> 5), chunk = id / parts;  // of all warps
   const int n_valid = *a.n_valid, begin = chunk * a.chunk, past = min(begin + a.chunk, n_valid);
   if (begin >= past) return;  // the whole warp
+  if (!TW_CHECKED(n_valid <= a.T, a.status)) return;
   const int block = (id - chunk * parts) * kWarpCols, width = min(kWarpCols, a.d - block);
   using Ring = RowRing<DT, VEC>;
   constexpr int kBatch = Ring::kBatch;
   const Ring ring{a, static_cast<const typename Ring::S*>(a.dy) + block, places + (tid >> 5) * Ring::kVecs, width, lane};
   RowSum<DT, VEC> sum(a, block);
   const int2 first_run = a.run[begin], last_run = a.run[past - 1];
+  if (!TW_CHECKED(first_run.x <= begin && begin < first_run.y && last_run.x < past && past <= last_run.y && last_run.y <= n_valid, a.status)) return;
   const bool skip = first_run.x < begin && !in_parts(first_run, a.chunk);  // (another warp's)
   const int lo = skip ? min(first_run.y, past) : begin;
   const bool goes_on = last_run.y > past && in_parts(last_run, a.chunk);
@@ -515,7 +518,8 @@ __global__ void __launch_bounds__(kThreads, 4) embed_sum_kernel(const EmbedBwdAr
   float* part = a.part + static_cast<size_t>(chunk) * 2 * a.part_ld + block;
   for (int first = 0; first < n; first += 32) {  // 32 keys and positions, a lane each
     const int m = min(32, n - first), at = lo + first + lane;
-    const int key = lane < m ? a.key[at] : -1, pos = lane < m ? a.pos[at] : 0;
+    int key = lane < m ? a.key[at] : -1, pos = lane < m ? a.pos[at] : 0;
+    if (!TW_CHECKED(lane >= m || (key >= 0 && key < a.V && pos >= 0 && pos < a.T), a.status)) key = pos = 0;
     auto fetch = [&](int i) {
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
@@ -570,6 +574,7 @@ __global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(const EmbedBwd
   if (next < n_valid) {
     const int2 run = a.run[next - 1];
     if (run.x >= next - a.chunk && run.y > next && in_parts(run, a.chunk)) heads = static_cast<int>((run.y - next + a.chunk - 1) / a.chunk), key = a.key[next];
+    if (!TW_CHECKED(run.y <= n_valid && n_valid <= a.T && key >= 0 && key < a.V, a.status)) heads = 0;
   }
   unsigned few = __ballot_sync(0xFFFFFFFFu, heads > 0 && heads <= kAlone), many = __ballot_sync(0xFFFFFFFFu, heads > kAlone);
   if (a.add && heads > 0 && warp == 0) prefetch_out(a, key, block);

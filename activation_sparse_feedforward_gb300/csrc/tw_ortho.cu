@@ -762,7 +762,10 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
       const int slot = n & (kRing - 1);
       if (!mbar_wait_cluster(ring->empty + slot, ((n / kRing) & 1u) ^ 1u, abort_flag, p.status)) break;
       uint2 w = make_uint2(~0u, 0u);
-      const bool more = unit_at(p, atomicAdd(p.next, 1), u);
+      bool more = unit_at(p, atomicAdd(p.next, 1), u);
+      if (more && !TW_CHECKED(u.mat >= 0 && u.mat < p.count && u.tile >= 0 && u.tile < tiles_of(p, u.kind) && u.slice >= 0 &&
+                              u.slice < p.slices[u.kind], p.status))
+        more = false;
       if (more) w = make_uint2(static_cast<uint32_t>(u.step << 24 | u.kind << 16 | u.mat << 8 | u.slice), static_cast<uint32_t>(u.tile));
 #pragma unroll
       for (uint32_t r = 0; r < 2; ++r) {

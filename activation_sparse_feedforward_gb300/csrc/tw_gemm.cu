@@ -68,9 +68,9 @@ static cudaError_t run_gemm(const GemmMaps& maps, const GemmShape& sh, const typ
   if (tiles <= 0) return cudaSuccess;
   if constexpr (PAIR) {
     if (sh.ksplit > 1 || sh.ksplit < 0) return cudaErrorInvalidValue;  // CTA pairs run whole tiles
-    static int resident_pairs = -1;  // per instantiation: the query depends only on the kernel
-    if (resident_pairs < 0) resident_pairs = max_active_clusters(kern, gemm_threads<BN, Epi>(), smem, 2);
-    const int pairs = static_cast<int>(std::min<long>(tiles, std::min(resident_pairs, device_sm_count() / 2)));
+    static KnownClusters known;  // per instantiation
+    const int resident = resident_clusters(known, kern, gemm_threads<BN, Epi>(), smem, 2);
+    const int pairs = static_cast<int>(std::min<long>(tiles, std::min(resident, device_sm_count() / 2)));
     if (pairs < 1) return cudaErrorInvalidConfiguration;
     e = launch_clustered(kern, dim3(2 * pairs), dim3(gemm_threads<BN, Epi>()), smem, 2, s, maps, sh, ep);
   } else {

@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/twell.h"
 
 namespace tw {
@@ -112,6 +114,22 @@ int max_active_clusters(void (*kern)(KArgs...), int block, size_t smem, int clus
   cfg.numAttrs = 1;
   int n = 0;
   if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) return 0;
+  return n;
+}
+// The same, asked for once a kernel and device: `known` is a static of the caller's. An answer of 0
+// (a query that failed) is asked for again. Host threads may call at once.
+struct KnownClusters {
+  std::atomic<int> of[64];
+};
+template <typename... KArgs>
+int resident_clusters(KnownClusters& known, void (*kern)(KArgs...), int block, size_t smem, int cluster) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = known.of[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    n = max_active_clusters(kern, block, smem, cluster);
+    known.of[dev].store(n, std::memory_order_relaxed);
+  }
   return n;
 }
 

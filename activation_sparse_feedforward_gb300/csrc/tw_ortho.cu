@@ -806,7 +806,7 @@ struct NsInArgs {
   const void* g[TW_ORTHO_MOST];
   float* m[TW_ORTHO_MOST];     // momentum buffers, or null
   int64_t ldg, ldm;
-  int gtype, count, rows, cols;  // of g as given
+  int count, rows, cols;       // of g as given
   float mu;
   int nesterov;
   double* norms;               // [count][kNormBlocks]
@@ -1106,7 +1106,7 @@ cudaError_t launch_ortho(const OrthoArgs& o, cudaStream_t s) {
     in.g[i] = o.g[i], in.m[i] = o.buf != nullptr ? o.buf[i] : nullptr;
     on16 = on16 && ((reinterpret_cast<uintptr_t>(in.g[i]) | reinterpret_cast<uintptr_t>(in.m[i])) & 15u) == 0;
   }
-  in.ldg = o.ldg, in.ldm = o.ldbuf, in.gtype = o.gtype, in.count = o.count, in.rows = o.m, in.cols = o.n;
+  in.ldg = o.ldg, in.ldm = o.ldbuf, in.count = o.count, in.rows = o.m, in.cols = o.n;
   in.mu = o.mu, in.nesterov = o.nesterov;
   in.vec = on16 && o.n % 8 == 0 && o.ldg * static_cast<int64_t>(o.gtype == TW_F32 ? 4 : 2) % 16 == 0 && o.ldbuf % 4 == 0;
   in.flat = on16 && (o.m == 1 || (o.ldg == o.n && (o.buf == nullptr || o.ldbuf == o.n)));
@@ -1152,8 +1152,8 @@ cudaError_t launch_ortho(const OrthoArgs& o, cudaStream_t s) {
   }
   e = cudaFuncSetAttribute(ns_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  static int resident = -1;  // the query depends only on the kernel
-  if (resident < 0) resident = max_active_clusters(ns_kernel, kThreads, kSmem, 2);
+  static KnownClusters known;
+  const int resident = resident_clusters(known, ns_kernel, kThreads, kSmem, 2);
   // no more pairs than a product of all matrices has units
   long most = 0;
   for (int i = 0; i < 3; ++i) {

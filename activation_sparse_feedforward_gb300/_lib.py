@@ -111,6 +111,7 @@ SIGNATURES = {
     "tw_orthogonalize": (c_int, [c_void_p, c_int64, c_int, c_void_p, c_int64, c_float, c_int, c_int, c_int, c_int, c_int,
                                  c_void_p, c_float, c_float, c_void_p, c_int64, c_int, c_void_p, c_size_t, c_void_p,
                                  c_void_p]),
+    "tw_orthogonalize_timeout_probe": (c_int, [c_void_p, c_int, c_int, c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]),
     "tw_trace_begin": (c_int, [ctypes.POINTER(c_void_p), c_int]),
     "tw_trace_end": (c_int, []),
     "tw_trace_label": (ctypes.c_char_p, [c_int]),

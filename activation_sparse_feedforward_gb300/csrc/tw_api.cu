@@ -1099,4 +1099,23 @@ tw_status tw_orthogonalize(const void* const* grads, int64_t ldg, int gtype, flo
   return from_cuda(tw::launch_ortho(a, as_stream(stream)));
 }
 
+tw_status tw_orthogonalize_timeout_probe(const float* grad, int m, int n, float* out, void* ws, size_t ws_bytes,
+                                         int32_t* dev_status, void* stream) {
+  tw_status st = check_ortho(m, n, 1);
+  if (st != TW_OK) return st;
+  const RowMatrix rows[] = {{grad, n, true, true}, {out, n, true, true}};
+  st = check_rows(rows, 2, n, TW_F32);
+  if (st == TW_OK) st = check_ptrs({ws});
+  if (st == TW_OK) st = check_side({dev_status}, {});
+  if (st != TW_OK) return st;
+  if (ws_bytes < tw::ortho_workspace(m, n, 1)) return TW_EWORKSPACE;
+  const void* g = grad;
+  void* o = out;
+  const float coef[] = {1.5f, -0.5f, 0.f, 1.5f, -0.5f, 0.f};
+  tw::OrthoArgs a = {};
+  a.g = &g, a.out = &o, a.ldg = n, a.ldo = n, a.count = 1, a.m = m, a.n = n, a.steps = 2;
+  a.scale = 1.f, a.coef = coef, a.ws = ws, a.status = dev_status, a.withhold = 1;
+  return from_cuda(tw::launch_ortho(a, as_stream(stream)));
+}
+
 }  // extern "C"

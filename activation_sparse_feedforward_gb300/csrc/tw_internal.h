@@ -513,6 +513,7 @@ struct OrthoArgs {
   int gtype, otype, count, m, n, steps, nesterov;
   float mu, scale, beta;
   const float* coef;        // [steps][3], host
+  int withhold;             // 0; above: see tw_orthogonalize_timeout_probe
   void* ws;
   int32_t* status;
 };

@@ -95,6 +95,7 @@ struct NsArgs {
   int* done;                 // [count][3]: blocks of warps finished, by Kind, over all steps; 0 at first
   int* next;                 // the next unit, 0 at first
   float* diag;               // [count][np]: B's diagonal less its fp16, times 2^kPolyLog2
+  int withhold;              // (a test's) blocks that a square waits for and no one writes
   int32_t* status;
   // GRAM: acc * f0 - f1 on the diagonal; SQUARE: e * f0 + acc * f1; APPLY: x * f0 + acc * f1
   float f0[kMostSteps][3], f1[kMostSteps][3];
@@ -198,7 +199,7 @@ TW_DEV bool wait_inputs(const NsArgs& p, const Unit& u, Known& known, volatile i
   const int at = 8 * u.mat;
   if (static_cast<int>(steps >> at & 255) == u.step + 1) return true;
   const int of = u.kind == GRAM ? APPLY : u.kind == SQUARE ? GRAM : SQUARE;
-  const int need = (u.kind == GRAM ? u.step : u.step + 1) * tiles_of(p, of) * 2 * kEpiWarps;
+  const int need = (u.kind == GRAM ? u.step : u.step + 1) * tiles_of(p, of) * 2 * kEpiWarps + (u.kind == SQUARE ? p.withhold : 0);
   const int* done = p.done + u.mat * 3 + of;
   if (ld_acquire(done) < need) {
     const uint64_t t0 = global_timer_ns();
@@ -1137,7 +1138,7 @@ cudaError_t launch_ortho(const OrthoArgs& o, cudaStream_t s) {
   p.tiles_m = l.mp / kTile, p.tiles_n = l.np / kTile, p.count = o.count, p.steps = o.steps, p.np = l.np, p.mp = l.mp;
   for (int i = 0; i < 3; ++i) p.width[i] = l.width[i], p.slices[i] = l.slices[i];
   p.slots = l.slots, p.part = reinterpret_cast<float*>(ws + l.part), p.arrived = in.arrived;
-  p.done = reinterpret_cast<int*>(ws + l.counters), p.next = p.done + 3 * o.count, p.status = o.status;
+  p.done = reinterpret_cast<int*>(ws + l.counters), p.next = p.done + 3 * o.count, p.status = o.status, p.withhold = o.withhold;
   p.diag = reinterpret_cast<float*>(ws + l.diag);
   for (int i = 0; i < o.count; ++i) p.out[i] = o.out[i];
   p.ldo = o.ldo, p.rows = std::max(o.m, o.n), p.cols = std::min(o.m, o.n), p.otype = o.otype, p.transposed = wide;

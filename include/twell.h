@@ -607,6 +607,14 @@ tw_status tw_orthogonalize(const void* const* grads, int64_t ldg, int gtype, flo
                            float scale, float beta, void* const* out, int64_t ldo, int otype, void* ws, size_t ws_bytes,
                            int32_t* dev_status, void* stream);
 
+/* Test hook for its bounded waits, as tw_wait_timeout_probe: an update of one dense fp32 matrix,
+ * two steps, in which the first square waits for one block of the gram more than there is.
+ * Every wait of the pairs that have units left runs out after the library's limit (1 s) or sees
+ * that another of its CTA has: TW_ETIMEOUT in *dev_status, copies and MMAs drained, TMEM freed;
+ * out is left as it was, and the workspace serves the next call. */
+tw_status tw_orthogonalize_timeout_probe(const float* grad, int m, int n, float* out, void* ws, size_t ws_bytes,
+                                         int32_t* dev_status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

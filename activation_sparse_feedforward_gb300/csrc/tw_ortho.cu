@@ -40,7 +40,8 @@
 // 1130 TFLOP/s over all (0.65 of the sustained 1736): some 110 us are the way in (bytes), and of
 // the products' the pairs spend 0.89 in MMAs, at 1340 W and 1.85 GHz. Small ones are bound by
 // the latency of 15 products that wait for one another: 704 x 256 takes 110 us, two of
-// 1027 x 2500 273.
+// 1027 x 2500 273 (products of bf16 operands by the library, which keep fewer bits, in a graph with
+// the momentum and the norm: 1.40 ms, 72 and 1492 us).
 #include <cuda.h>
 
 #include <algorithm>

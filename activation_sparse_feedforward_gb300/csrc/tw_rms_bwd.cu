@@ -5,8 +5,8 @@
 //
 // The form of layer norm's backward (tw_norm.cu) without the mean's terms. Bound by HBM: one
 // GB300, 16384 x 2048 bf16 with the residual's gradient and fp32 weights 45.3 us for 268 MB
-// (0.87 of the copy rate, 6777 GB/s). Rows off 16 bytes that lie alike in all matrices: bf16 0.3
-// (515 columns) to 0.6 (4001), fp32 0.65 to 0.9; others 0.2 to 0.45. 1048576
+// (0.87 of the copy rate, 6777 GB/s). Rows off 16 bytes that lie alike in all matrices: bf16 0.27
+// (515 columns) to 0.58 (4001), fp32 0.65 to 0.81; others 0.2 to 0.45. 1048576
 // rows of 64 columns, several to a warp, 74 us without the residual's gradient (0.80; a warp
 // each 457).
 #include "tw_norm_rows.cuh"

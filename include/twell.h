@@ -466,7 +466,8 @@ tw_status tw_layer_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t
  *   s = x + res (rounded to the type; s = x when res is NULL)
  *   rstd = (sum(s^2) / d + eps)^-1/2,  y = s rstd * weight
  * Arguments, types, strides and limits as tw_layer_norm_fwd. The squares are fp32: a row of
- * values beyond 1e19 has an infinite sum and rstd 0. */
+ * values beyond 1e19 has an infinite sum and rstd 0, and squares of values below 1e-22 are 0
+ * (which only an eps of 0 shows). */
 tw_status tw_rms_norm_fwd(const void* x, int64_t ldx, const void* res, int64_t ldres, const void* weight, int T, int d,
                           float eps, int dtype, int wtype, void* sum, int64_t ldsum, void* y, int64_t ldy, float* rstd,
                           void* stream);
@@ -545,8 +546,8 @@ tw_status tw_token_logprobs(const void* z, int64_t ldz, int N, int V, int dtype,
                             float temperature, int top_k, float* logprob, float* entropy, int32_t* top_idx,
                             float* top_logprob, int32_t* dev_status, void* stream);
 
-/* Token embedding forward: y[t] = scale * weight[tokens[t]] (one rounding), a row of zeros
- * where the token is -1. weight [V, d] of type wtype, which is dtype or TW_F32; y [T, d] of
+/* Token embedding forward: y[t] = scale * weight[tokens[t]] (the product in fp32, then rounded to
+ * dtype), a row of zeros where the token is -1. weight [V, d] of type wtype, which is dtype or TW_F32; y [T, d] of
  * type dtype. 0 <= T <= 2^22, 1 <= V <= 2^22, 1 <= d <= 16384; scale finite. Device condition:
  * a token outside [-1, V) raises TW_EINVAL in *dev_status and is read as -1. */
 tw_status tw_embedding_fwd(const int32_t* tokens, const void* weight, int64_t ldw, int T, int V, int d, float scale,
@@ -560,9 +561,10 @@ size_t tw_embedding_bwd_workspace_size(int T, int V, int d);
  *   dweight[v] = scale * sum of dy[t] over the t with tokens[t] = v   (+ dweight[v] when add)
  * dy [T, d] of type dtype; dweight [V, d] fp32, row stride lddw: written whole (add 0: zeros
  * for tokens that do not occur), or added to, which touches the rows of tokens that occur
- * alone. Sums are fp32 in the order of t, long runs of one token in parts of fixed size: the
- * same call gives the same bits. Limits, tokens of -1 and the device condition as the
- * forward. */
+ * alone. Sums are fp32 in the order of t, a long run of one token in parts that are joined in
+ * order: the same call gives the same bits. The parts' size depends on T and d, so that batches
+ * of other lengths may differ in the last bits. Limits, tokens of -1 and the device condition as
+ * the forward. */
 tw_status tw_embedding_bwd(const void* dy, int64_t lddy, const int32_t* tokens, int T, int V, int d, float scale,
                            int dtype, int add, float* dweight, int64_t lddw, void* ws, size_t ws_bytes,
                            int32_t* dev_status, void* stream);

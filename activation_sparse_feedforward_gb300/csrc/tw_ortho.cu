@@ -29,11 +29,11 @@
 // otherwise be amplified as the small singular values are (up to 3.44 a step), while in
 // X B they meet B's small rows. What B's diagonal, its largest elements, loses to fp16 is kept
 // in fp32, and apply adds X's columns times that: else the most of the error where X is near
-// orthogonal. Relative to the definition in 64 bits, both norms Frobenius's, five steps, in a
-// numpy model of these roundings: 0.5e-3 to 1.5e-3 from 64 rows and columns on, whatever the rank
-// and for spectra over up to four decades (hi alone: up to 1e-2; t = 1 from the fourth step on:
-// 2.6e-3 at rank 1 to 77, and 0.1 at eight steps). The diagonal costs 1 us a step of a small
-// matrix (704 x 256, five steps: 105 us without, 110 with).
+// orthogonal. Relative to the definition in 64 bits, in the Frobenius norm, after five steps
+// (tests/test_ortho_roundings.py models these roundings): 0.5e-3 to 1.5e-3 from 64 rows and
+// columns on, whatever the rank and for spectra over up to four decades (hi alone: up to 1e-2;
+// t = 1 from the fourth step on: 2.6e-3 at rank 1 to 77, and 0.1 after eight). The diagonal costs
+// 1 us a step of a small matrix (704 x 256, five steps: 105 us without, 110 with).
 //
 // Large matrices are bound by the tensor cores under the board's power: on one GB300 three of
 // 5632 x 2048, fp32 gradients and momentum, five steps take 1.05 ms for 1.19e12 operations,
